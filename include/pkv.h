@@ -19,6 +19,15 @@
  *   paged_attention_step     slot mapping + K/V scatter + attention in one call
  *   paged_attention_step_cow the same, after the step's copy-on-write block copies
  *
+ * and the steps a request with several candidate continuations adds to it:
+ *
+ *   pkv_tree_mask          who is whose ancestor in a request's tree of drafted tokens
+ *   paged_attention_tree   attention of such trees over the paged cache
+ *   pkv_compact_path       the accepted path of a tree moved together in the cache
+ *   pkv_beam_select        the best continuations of a request's beams
+ *   pkv_fork_tables        block tables after the beams they continue: reference
+ *                          counts, freed and fresh blocks, copy-on-write
+ *
  * Conventions for every call
  *  - Pointers named as device pointers must point to device memory of the current
  *    CUDA device; `stream` is a cudaStream_t (NULL = legacy default stream).  All
@@ -33,6 +42,10 @@
  *    affected outputs are zeroed or skipped, and pkv_get_last_error() reports them.
  *  - No call allocates device memory except paged_attention(), which grows the
  *    workspace when a larger batch needs it (never during stream capture).
+ *  - A call that takes a `workspace` keeps its scratch there and nowhere else: the
+ *    matching *_workspace() call says how many bytes it needs, its contents need no
+ *    initialisation and mean nothing afterwards.  Calls that may overlap on the GPU
+ *    (two streams, two captured graphs) take one each.
  *
  * Cache layout (a reading where the pages are silent): k_cache and v_cache are
  * each [num_blocks][num_kv_heads][16][head_dim], row-major, so that one
@@ -276,12 +289,144 @@ PKV_API int paged_attention_noalloc(const void* q, const void* k_cache, const vo
                                     int64_t num_tokens, int32_t max_query_len, int32_t max_seq_len, float scale,
                                     void* out, uint32_t* error_bits, void* stream);
 
+/*
+ * pkv_tree_mask -- ancestor masks of drafted tokens.  Request i's new tokens
+ * query_start_loc[i] .. query_start_loc[i+1] - 1 are the nodes 0 .. q_i - 1 of a tree
+ * (a forest: several tokens may continue the context), and parents[t] names the node
+ * that token t continues, a smaller index than its own, or -1 for the context itself.
+ * Bit u of mask row t (bit u % 64 of word u / 64) is set iff node u is t's own node or
+ * one of its ancestors; depths[t] counts the ancestors, so that token t's position is
+ * seq_lens[i] - q_i + depths[t].
+ * parents         device int32 [num_tokens]
+ * mask            device uint64 [num_tokens][mask_words], written
+ * depths          optional device int32 [num_tokens], written (NULL: not stored)
+ * Device errors: a parent outside [-1, own index) or a node index that the row cannot
+ * hold (q_i > 64 * mask_words) flags PKV_ERR_INDEX and gives a zero row and depth 0.
+ */
+PKV_API int pkv_tree_mask(const int32_t* parents, const int32_t* query_start_loc, int32_t num_seqs,
+                          int64_t num_tokens, uint64_t* mask, int32_t mask_words, int32_t* depths, void* stream);
+
+/*
+ * paged_attention_tree -- attention of drafted tokens over the paged cache.  The new
+ * tokens of a request are candidates that a verification step checks in one pass: node j
+ * sees the whole context before the draft and, of the draft, what its mask row says.
+ * With c_i = seq_lens[i] - q_i, token t = query_start_loc[i] + j sees key u of its
+ * request iff u < c_i, or c_i <= u < seq_lens[i] and bit u - c_i of mask row t is set:
+ *     out[t][h][:] = sum_{u seen} softmax_u(scale * q[t][h] . K_u) V_u
+ * A row that sees no key is zero.  Keys and values that a row does not see have no part
+ * in it, whatever they hold (infinities and NaN among it).  K and V of the new tokens
+ * are already in the cache, node j at position c_i + j (pkv_slot_mapping and pkv_write
+ * put them there).  Chains, trees and any other mask are served alike, q_i from 1 on.
+ * tree_mask       device uint64 [num_tokens][mask_words]; bits past q_i are not read
+ * mask_words      64 * mask_words >= max_query_len
+ * max_query_len   host bound on q_i: a request with more is flagged (PKV_ERR_INDEX) and
+ *                 its rows zeroed
+ * max_seq_len     host bound on seq_lens, used only to plan the launch
+ * workspace       device memory of at least pkv_tree_workspace() bytes, 256-byte aligned
+ * Everything else, the types and the errors: as paged_attention().  Work is cut along the
+ * keys by the batch's sizes, so rounding (not the result) may depend on the batch.
+ */
+PKV_API int paged_attention_tree(const void* q, const void* k_cache, const void* v_cache,
+                                 const pkv_cache_desc* cache, const int32_t* block_tables,
+                                 int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                 const int32_t* query_start_loc, const uint64_t* tree_mask, int32_t mask_words,
+                                 int32_t num_seqs, int32_t num_q_heads, int64_t num_tokens, int32_t max_query_len,
+                                 int32_t max_seq_len, float scale, void* out, void* workspace,
+                                 int64_t workspace_bytes, void* stream);
+/* Bytes of workspace that paged_attention_tree needs for these sizes (*bytes). */
+PKV_API int pkv_tree_workspace(const pkv_cache_desc* cache, int32_t num_q_heads, int32_t max_query_len,
+                               int64_t* bytes);
+
+/*
+ * pkv_compact_path -- the accepted path of a tree of drafted tokens, moved together.
+ * Request i keeps the nodes path[i][0] < path[i][1] < ... (path_lens[i] of them) of the
+ * draft that its last q_i positions hold: with c_i = seq_lens[i] - q_i,
+ *     K and V at position c_i + a = what was at position c_i + path[i][a],  a < path_lens[i],
+ * in every layer, and new_seq_lens[i] = c_i + path_lens[i].  What lies behind that is no
+ * longer part of the request; its blocks and bytes stay as they are.
+ * k_cache, v_cache  [num_layers] pools of `cache`'s shape, one after the other
+ * path            device int32 [num_seqs][max_path], entries past path_lens[i] not read
+ * path_lens       device int32 [num_seqs]
+ * new_seq_lens    device int32 [num_seqs], written; not the same array as seq_lens
+ * Caller contract: the blocks that hold the draft belong to the request alone.
+ * Device errors: q_i or seq_lens[i] that do not fit (as in paged_attention), path_lens[i]
+ * outside [0, min(max_path, q_i)], a path that does not ascend within [0, q_i), or a bad
+ * block id flag PKV_ERR_INDEX; that request's rows stay as they are and its new length
+ * is seq_lens[i].
+ */
+PKV_API int pkv_compact_path(const int32_t* path, int32_t max_path, const int32_t* path_lens,
+                             const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                             const int32_t* query_start_loc, int32_t num_seqs, void* k_cache, void* v_cache,
+                             const pkv_cache_desc* cache, int32_t num_layers, int32_t* new_seq_lens,
+                             void* stream);
+
+/*
+ * pkv_beam_select -- beam search's step: the best continuations of each request's beams.
+ * Beam w of request n with token v scores
+ *     score(w, v) = cum_scores[n][w] + logits[n][w][v] - log sum_u exp(logits[n][w][u]),
+ * and a beam with finished[n][w] != 0 stands for itself: its one candidate is
+ * (w, eos_token) with score cum_scores[n][w].  The num_select best of all beams are
+ * returned, best first; equal scores are taken in order of w * vocab + v.  A score that
+ * is not finite (a NaN or infinite beam, a logit of -inf) is no candidate, and where the
+ * candidates run out, the score is -inf and beam and token are -1.  Scores are ranked in
+ * 64 bits; sums over the vocabulary run in 32 and are joined in 64.
+ * logits          device [num_seqs * num_beams] rows of vocab values of `dtype` (pkv_dtype),
+ *                 row_stride elements apart (>= vocab), aligned to their type
+ * cum_scores      device fp32 [num_seqs][num_beams]
+ * finished        optional device uint8 [num_seqs][num_beams] (NULL: none is)
+ * num_beams       1 to 64;  num_select  1 to 64;  num_beams * vocab < 2^31
+ * out_scores, out_parents, out_tokens  device fp32, int32, int32 [num_seqs][num_select]
+ * workspace       device memory of at least pkv_beam_workspace() bytes, 256-byte aligned
+ */
+PKV_API int pkv_beam_select(const void* logits, int32_t dtype, int64_t row_stride, const float* cum_scores,
+                            const uint8_t* finished, int32_t eos_token, int32_t num_seqs, int32_t num_beams,
+                            int32_t vocab, int32_t num_select, float* out_scores, int32_t* out_parents,
+                            int32_t* out_tokens, void* workspace, int64_t workspace_bytes, void* stream);
+PKV_API int pkv_beam_workspace(int32_t num_seqs, int32_t num_beams, int32_t vocab, int32_t num_select,
+                               int64_t* bytes);
+
+/*
+ * pkv_fork_tables -- block tables after the beams (or samples) they continue, with the
+ * pool's reference counts kept on the device ("The 1960s Operating System Trick ..."
+ * page, Technical Details: samples share blocks until they diverge, only the block that
+ * changes is duplicated, and a block without users is free again).
+ * Row b of the new tables continues row parents[b] of the old ones (-1: row b ends).  It
+ * holds the first ceil(n / 16) blocks of that row, n = seq_lens[parents[b]], and then
+ * whatever num_new more tokens need, all of it its own to write:
+ *  - a last block with room in it (n % 16 != 0, num_new > 0) that other rows or other
+ *    users hold too is replaced by a copy, in every layer of k_cache and v_cache; if no
+ *    one but rows of this call holds it, the lowest of them keeps the block itself;
+ *  - ceil((n + num_new) / 16) - ceil(n / 16) fresh blocks follow.
+ * Old rows give up all their blocks (every id >= 0 in the row); a block that nobody holds
+ * any more is free and may be handed out again by the same call.  Fresh blocks are the
+ * lowest free ids, given to rows in order, a row's copy before its other fresh blocks.
+ * Entries behind a row's last block are -1, and new_seq_lens[b] = n (0 for an ended row).
+ * ref_counts      device int32 [num_blocks], users of each block, 0 = free; updated.  Holds
+ *                 one for every row and entry that names the block, plus other holders
+ * block_tables, new_block_tables  device int32 [num_rows][max_blocks_per_seq], two arrays
+ * seq_lens, new_seq_lens          device int32 [num_rows], two arrays
+ * num_rows        1 to 4096;  num_new  0 to 65536
+ * k_cache, v_cache  [num_layers] pools of `cache`'s shape, one after the other; both NULL:
+ *                 no data is copied (the tables and counts alone)
+ * workspace       device memory of at least pkv_fork_workspace() bytes, 256-byte aligned
+ * Device errors leave everything as it was (the new tables and lengths equal the old):
+ * a parent outside [-1, num_rows), a length past the table's row or a bad block id within
+ * it flag PKV_ERR_INDEX, too few free blocks flag PKV_ERR_NO_MEMORY (bit 4).
+ */
+PKV_API int pkv_fork_tables(const int32_t* block_tables, const int32_t* seq_lens, int32_t num_rows,
+                            int32_t max_blocks_per_seq, const int32_t* parents, int32_t num_new,
+                            int32_t* ref_counts, int32_t* new_block_tables, int32_t* new_seq_lens, void* k_cache,
+                            void* v_cache, const pkv_cache_desc* cache, int32_t num_layers, void* workspace,
+                            int64_t workspace_bytes, void* stream);
+PKV_API int pkv_fork_workspace(int32_t num_rows, int64_t* bytes);
+
 /* Synchronises `stream`, returns the device error word of the current device as a
- * pkv_status (PKV_OK, PKV_ERR_INDEX or PKV_ERR_TIMEOUT) and clears it. */
+ * pkv_status (PKV_OK, PKV_ERR_INDEX, PKV_ERR_TIMEOUT, or PKV_ERR_NO_MEMORY where a fork
+ * that found too few free blocks is all there is) and clears it. */
 PKV_API int pkv_get_last_error(void* stream);
 
 /* Raw device error bits of the current device (bit 0 bad block id, bit 1 bad slot,
- * bit 2 bad length, bit 3 wait timeout); synchronises `stream`; does not clear. */
+ * bit 2 bad length, bit 3 wait timeout, bit 4 no free block left); synchronises `stream`; does not clear. */
 PKV_API int pkv_peek_error_bits(void* stream, uint32_t* bits);
 
 /* Human-readable name of a pkv_status value (static string). */
@@ -300,7 +445,8 @@ PKV_API void pkv_shutdown(void);
  * returns, per kernel kind, the launch count and the summed device time in ms,
  * then resets the counters.  Kinds: 0 slot mapping, 1 write, 2 copy, 3 plan,
  * 4 decode, 5 prefill, 6 generic attention, 7 split merge, 8 shared-prefix (cascade)
- * pass.  Arrays hold PKV_TRACE_KINDS entries.
+ * pass.  Arrays hold PKV_TRACE_KINDS entries.  (The calls for candidate continuations,
+ * pkv_tree_mask to pkv_fork_tables, are not traced.)
  */
 #define PKV_TRACE_KINDS 9
 PKV_API int pkv_trace_enable(int on);

@@ -10,6 +10,7 @@ If the library has not been built, importing a function raises immediately.
 Functions carry the C names:
   pkv_slot_mapping, pkv_write, pkv_copy_blocks, paged_attention, paged_attention_cascade,
   paged_attention_step,
+  pkv_tree_mask, paged_attention_tree, pkv_compact_path, pkv_beam_select, pkv_fork_tables,
   pkv_get_last_error, pkv_peek_error_bits, pkv_trace_enable, pkv_trace_read,
   pkv_num_workers, pkv_shutdown, pkv_umma_selftest, pkv_tma_selftest, pkv_wait_selftest.
 """
@@ -73,6 +74,14 @@ def lib():
                                          ctypes.POINTER(_PrefixGroups), P, P, P],
                 "paged_attention_step_cow": [P, P, P, P, P, D, P, i32, P, P, i32, i32, i64, i32, i32, f32,
                                              ctypes.POINTER(_PrefixGroups), P, P, i64, P, P, P],
+                "pkv_tree_mask": [P, P, i32, i64, P, i32, P, P],
+                "pkv_tree_workspace": [D, i32, i32, ctypes.POINTER(i64)],
+                "paged_attention_tree": [P, P, P, D, P, i32, P, P, P, i32, i32, i32, i64, i32, i32, f32, P, P, i64, P],
+                "pkv_compact_path": [P, i32, P, P, i32, P, P, i32, P, P, D, i32, P, P],
+                "pkv_beam_workspace": [i32, i32, i32, i32, ctypes.POINTER(i64)],
+                "pkv_beam_select": [P, i32, i64, P, P, i32, i32, i32, i32, i32, P, P, P, P, i64, P],
+                "pkv_fork_workspace": [i32, ctypes.POINTER(i64)],
+                "pkv_fork_tables": [P, P, i32, i32, P, i32, P, P, P, P, P, D, i32, P, i64, P],
                 "pkv_get_last_error": [P],
                 "pkv_peek_error_bits": [P, ctypes.POINTER(ctypes.c_uint32)],
                 "pkv_num_workers": [ctypes.POINTER(ctypes.c_int32)],
@@ -260,6 +269,227 @@ def paged_attention_step(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
                                               _dev(dst, "cow dst", torch.int32), src.shape[0], *tail),
                "paged_attention_step_cow")
     return out
+
+
+# ----------------------------------------------------------------------------- candidate continuations
+def _workspace(size_fn, args, like: torch.Tensor, stream) -> torch.Tensor:
+    """Scratch of one call, from torch's allocator: its own for every call and every captured
+    graph.  A tensor made here belongs to the current stream; one used on ``stream`` stays
+    alive until that stream is done with it."""
+    n = ctypes.c_int64(0)
+    _check(size_fn(*args, ctypes.byref(n)), "workspace size")
+    ws = torch.empty(max(256, n.value), dtype=torch.uint8, device=like.device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
+
+
+def _on_current_device(**tensors) -> None:
+    """The library launches on the current device and reads these tensors there."""
+    cur = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and (not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != cur):
+            raise ValueError(f"{name} must be a tensor on the current CUDA device (cuda:{cur})")
+
+
+def _new_out(shape, dtype, like, stream):
+    out = torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None:
+        out.record_stream(stream)
+    return out
+
+
+def _shaped(t: torch.Tensor, name: str, shape) -> None:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def pkv_tree_mask(parents: torch.Tensor, query_start_loc: torch.Tensor, max_query_len: int,
+                  out: torch.Tensor | None = None, depths: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Ancestor masks of drafted tokens: int64 [T, ceil(max_query_len / 64)], bit u of row t set
+    iff node u of t's request is t itself or one of its ancestors.  ``parents`` int32 [T]: the
+    node that each token continues (smaller than its own index), -1 for the context.
+    ``depths``, if given, receives the number of ancestors (int32 [T])."""
+    _on_current_device(parents=parents, query_start_loc=query_start_loc, out=out, depths=depths)
+    n, words = parents.shape[0], (int(max_query_len) + 63) // 64
+    if out is None:
+        out = _new_out((n, words), torch.int64, parents, stream)
+    elif out.dim() != 2 or out.shape[0] != n:
+        raise ValueError("out must be int64 [num_tokens, words]")
+    if depths is not None:
+        _shaped(depths, "depths", (n,))
+    _check(lib().pkv_tree_mask(_dev(parents, "parents", torch.int32),
+                               _dev(query_start_loc, "query_start_loc", torch.int32), query_start_loc.shape[0] - 1, n,
+                               _dev(out, "out", torch.int64), out.shape[1],
+                               _dev(depths, "depths", torch.int32) if depths is not None else None,
+                               _stream(stream)), "pkv_tree_mask")
+    return out
+
+
+def paged_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                         seq_lens: torch.Tensor, query_start_loc: torch.Tensor, tree_mask: torch.Tensor, scale: float,
+                         max_query_len: int, max_seq_len: int, out: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of drafted tokens over the paged cache: each of a request's q_i new tokens sees
+    the whole context before the draft and, of the draft, the nodes whose bits its row of
+    ``tree_mask`` (int64 [T, words], as pkv_tree_mask makes it) has.  A row that sees nothing
+    is zero.  ``workspace``: scratch of a caller that keeps its own (uint8; calls that may
+    overlap take one each)."""
+    desc = _cache_desc(k_cache, v_cache)
+    T, hq, d = q.shape
+    if d != desc.head_dim:
+        raise ValueError("q must be [num_tokens, num_q_heads, head_dim]")
+    if tree_mask.dim() != 2 or tree_mask.shape[0] != T:
+        raise ValueError("tree_mask must be int64 [num_tokens, words]")
+    n = seq_lens.shape[0]
+    if block_tables.dim() != 2 or block_tables.shape[0] != n or query_start_loc.shape[0] != n + 1:
+        raise ValueError("block_tables, seq_lens and query_start_loc disagree on the number of requests")
+    _on_current_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, seq_lens=seq_lens,
+                       query_start_loc=query_start_loc, tree_mask=tree_mask, out=out, workspace=workspace)
+    if out is None:
+        out = _new_out(q.shape, q.dtype, q, stream)
+    else:
+        _shaped(out, "out", q.shape)
+    L = lib()
+    if workspace is None and T:
+        workspace = _workspace(L.pkv_tree_workspace, (ctypes.byref(desc), hq, int(max_query_len)), q, stream)
+    _check(L.paged_attention_tree(_dev(q, "q", k_cache.dtype), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
+                                  ctypes.byref(desc), _dev(block_tables, "block_tables", torch.int32),
+                                  block_tables.shape[1], _dev(seq_lens, "seq_lens", torch.int32),
+                                  _dev(query_start_loc, "query_start_loc", torch.int32),
+                                  _dev(tree_mask, "tree_mask", torch.int64), tree_mask.shape[1], n, hq, T,
+                                  int(max_query_len), int(max_seq_len), float(scale), _dev(out, "out", k_cache.dtype),
+                                  _dev(workspace, "workspace", torch.uint8) if T else None,
+                                  workspace.numel() if T else 0, _stream(stream)), "paged_attention_tree")
+    return out
+
+
+def _layers(k_cache: torch.Tensor, v_cache: torch.Tensor):
+    """(descriptor, layers) of one cache [blocks, Hkv, 16, d] or of a model's, [layers, ...]."""
+    if k_cache.dim() == 5 and k_cache.shape == v_cache.shape and k_cache.shape[0] > 0:
+        return _cache_desc(k_cache[0], v_cache[0]), k_cache.shape[0]
+    return _cache_desc(k_cache, v_cache), 1
+
+
+def pkv_compact_path(path: torch.Tensor, path_lens: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                     query_start_loc: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     new_seq_lens: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Moves the accepted path of each request's drafted tree together, in place and in every
+    layer (caches [blocks, Hkv, 16, d] or [layers, blocks, Hkv, 16, d]): node path[i][a] goes
+    to position c_i + a, c_i = seq_lens[i] - q_i.  Returns the new lengths c_i + path_lens[i]."""
+    desc, layers = _layers(k_cache, v_cache)
+    n = seq_lens.shape[0]
+    if path.dim() != 2 or path.shape[0] != n or path_lens.shape[0] != n:
+        raise ValueError("path must be [num_seqs, max_path], path_lens [num_seqs]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != n or query_start_loc.shape[0] != n + 1:
+        raise ValueError("block_tables, seq_lens and query_start_loc disagree on the number of requests")
+    _on_current_device(path=path, path_lens=path_lens, block_tables=block_tables, seq_lens=seq_lens,
+                       query_start_loc=query_start_loc, k_cache=k_cache, v_cache=v_cache, new_seq_lens=new_seq_lens)
+    if new_seq_lens is None:
+        new_seq_lens = _new_out((n,), torch.int32, seq_lens, stream)
+    else:
+        _shaped(new_seq_lens, "new_seq_lens", (n,))
+    _check(lib().pkv_compact_path(_dev(path, "path", torch.int32), path.shape[1],
+                                  _dev(path_lens, "path_lens", torch.int32),
+                                  _dev(block_tables, "block_tables", torch.int32), block_tables.shape[1],
+                                  _dev(seq_lens, "seq_lens", torch.int32),
+                                  _dev(query_start_loc, "query_start_loc", torch.int32), n, _dev(k_cache, "k_cache"),
+                                  _dev(v_cache, "v_cache"), ctypes.byref(desc), layers,
+                                  _dev(new_seq_lens, "new_seq_lens", torch.int32), _stream(stream)),
+           "pkv_compact_path")
+    return new_seq_lens
+
+
+def pkv_beam_select(logits: torch.Tensor, cum_scores: torch.Tensor, num_select: int,
+                    finished: torch.Tensor | None = None, eos_token: int = 0,
+                    out: tuple[torch.Tensor, torch.Tensor, torch.Tensor] | None = None,
+                    workspace: torch.Tensor | None = None, stream=None):
+    """The ``num_select`` best continuations of each request's beams: (scores fp32, parents int32,
+    tokens int32), each [N, num_select], best first.  ``logits`` [N, W, V] fp32 or bf16, its
+    last dimension contiguous and its rows evenly spaced (a slice of a padded vocabulary
+    will do); ``cum_scores`` fp32 [N, W].  A beam with ``finished`` (bool or uint8 [N, W])
+    stands for itself, as token ``eos_token``.  Equal scores go by beam, then token; where
+    candidates run out, score is -inf and parent and token are -1."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 3:
+        raise ValueError("logits must be [num_seqs, num_beams, vocab]")
+    N, W, V = logits.shape
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    step = V
+    if N * W > 0 and V > 0:
+        step = logits.stride(1) if W > 1 else (logits.stride(0) if N > 1 else V)
+        if (V > 1 and logits.stride(2) != 1) or (N > 1 and logits.stride(0) != W * step) or step < V:
+            raise ValueError("logits must have contiguous rows, evenly spaced")
+    _shaped(cum_scores, "cum_scores", (N, W))
+    if finished is not None:
+        _shaped(finished, "finished", (N, W))
+        if finished.dtype == torch.bool:
+            finished = finished.view(torch.uint8)
+    K = int(num_select)
+    if out is None:
+        out = tuple(_new_out((N, max(K, 0)), t, logits, stream) for t in (torch.float32, torch.int32, torch.int32))
+    else:
+        for t, name in zip(out, ("scores", "parents", "tokens")):
+            _shaped(t, name, (N, K))
+    scores, parents, tokens = out
+    _on_current_device(logits=logits, cum_scores=cum_scores, finished=finished, scores=scores, parents=parents,
+                       tokens=tokens, workspace=workspace)
+    L = lib()
+    if workspace is None:
+        workspace = _workspace(L.pkv_beam_workspace, (N, W, V, K), logits, stream)
+    _check(L.pkv_beam_select(ctypes.c_void_p(logits.data_ptr()), PKV_F32 if logits.dtype == torch.float32 else PKV_BF16,
+                             step, _dev(cum_scores, "cum_scores", torch.float32),
+                             _dev(finished, "finished", torch.uint8) if finished is not None else None, int(eos_token),
+                             N, W, V, K, _dev(scores, "scores", torch.float32), _dev(parents, "parents", torch.int32),
+                             _dev(tokens, "tokens", torch.int32), _dev(workspace, "workspace", torch.uint8),
+                             workspace.numel(), _stream(stream)), "pkv_beam_select")
+    return scores, parents, tokens
+
+
+def pkv_fork_tables(block_tables: torch.Tensor, seq_lens: torch.Tensor, parents: torch.Tensor,
+                    ref_counts: torch.Tensor, k_cache: torch.Tensor | None, v_cache: torch.Tensor | None,
+                    new_tokens: int = 1, out: tuple[torch.Tensor, torch.Tensor] | None = None,
+                    workspace: torch.Tensor | None = None, stream=None):
+    """Block tables after the beams they continue: (new tables int32 [B, M], new lengths int32 [B]).
+    New row b holds the blocks of old row parents[b] (-1: the row ends) and whatever
+    ``new_tokens`` more tokens need, all of it its own to write: a last block that others
+    hold too is copied (in every layer; caches [blocks, Hkv, 16, d] or [layers, ...]), fresh
+    blocks are the lowest free ones.  ``ref_counts`` int32 [blocks] is kept up to date in
+    place; a block without users is free.  Too few free blocks change nothing and show as
+    PKV_ERR_NO_MEMORY in pkv_get_last_error.  Without caches (None, None) only the tables
+    and counts change."""
+    if k_cache is None or v_cache is None:
+        if k_cache is not None or v_cache is not None:
+            raise ValueError("k_cache and v_cache must be given together")
+        desc, layers = _CacheDesc(ref_counts.shape[0], BLOCK_SIZE, 1, 128, PKV_BF16), 1
+    else:
+        desc, layers = _layers(k_cache, v_cache)
+        if ref_counts.shape != (desc.num_blocks,):
+            raise ValueError("ref_counts must be [num_blocks] of the cache")
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [num_rows, max_blocks_per_seq]")
+    B, M = block_tables.shape
+    _shaped(seq_lens, "seq_lens", (B,))
+    _shaped(parents, "parents", (B,))
+    if out is None:
+        out = (_new_out((B, M), torch.int32, block_tables, stream), _new_out((B,), torch.int32, block_tables, stream))
+    tables, lens = out
+    _shaped(tables, "new tables", (B, M))
+    _shaped(lens, "new lengths", (B,))
+    _on_current_device(block_tables=block_tables, seq_lens=seq_lens, parents=parents, ref_counts=ref_counts,
+                       k_cache=k_cache, v_cache=v_cache, tables=tables, lens=lens, workspace=workspace)
+    L = lib()
+    if workspace is None:
+        workspace = _workspace(L.pkv_fork_workspace, (B,), block_tables, stream)
+    _check(L.pkv_fork_tables(_dev(block_tables, "block_tables", torch.int32), _dev(seq_lens, "seq_lens", torch.int32),
+                             B, M, _dev(parents, "parents", torch.int32), int(new_tokens),
+                             _dev(ref_counts, "ref_counts", torch.int32), _dev(tables, "new tables", torch.int32),
+                             _dev(lens, "new lengths", torch.int32),
+                             _dev(k_cache, "k_cache") if k_cache is not None else None,
+                             _dev(v_cache, "v_cache") if v_cache is not None else None, ctypes.byref(desc), layers,
+                             _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream)),
+           "pkv_fork_tables")
+    return tables, lens
 
 
 def pkv_get_last_error(stream=None) -> int:

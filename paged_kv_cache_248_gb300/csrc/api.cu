@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "pkv_internal.cuh"
+#include "api_checks.cuh"
 #include "k_generic.cuh"
 
 namespace pkv {
@@ -237,25 +238,6 @@ TraceScope::~TraceScope() {
 }  // namespace pkv
 
 using namespace pkv;
-
-// ------------------------------------------------------------------ argument checks
-namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int check_cache(const pkv_cache_desc* c) {
-  if (!c) return PKV_ERR_INVALID_ARG;
-  if (c->block_size != PKV_BLOCK_SIZE || c->num_blocks <= 0 || c->num_kv_heads <= 0 || c->head_dim <= 0)
-    return PKV_ERR_INVALID_ARG;
-  if (c->num_blocks > (int64_t(1) << 40)) return PKV_ERR_INVALID_ARG;
-  if (c->dtype == PKV_F32 && (c->head_dim == 64 || c->head_dim == 128)) return PKV_OK;
-  if (c->dtype == PKV_BF16 && c->head_dim == 128) return PKV_OK;
-  return PKV_ERR_UNSUPPORTED;
-}
-
-cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
-
-}  // namespace
 
 extern "C" {
 
@@ -536,6 +518,7 @@ int pkv_get_last_error(void* stream) {
   if (cudaMemset(ctx->err, 0, sizeof(uint32_t)) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess)
     return PKV_ERR_CUDA;
   if (bits & kErrTimeout) return PKV_ERR_TIMEOUT;
+  if (bits == kErrNoPages) return PKV_ERR_NO_MEMORY;
   if (bits) return PKV_ERR_INDEX;
   return PKV_OK;
 }

@@ -17,6 +17,7 @@ enum : uint32_t {
   kErrSlot = 1u << 1,      // slot past the pool
   kErrLength = 1u << 2,    // seq_len < q_len, or more blocks than a table row holds
   kErrTimeout = 1u << 3,   // a bounded wait gave up
+  kErrNoPages = 1u << 4,   // a fork found too few free blocks
 };
 
 constexpr int kTileKeys = 128;       // keys per tensor-core tile (8 blocks)
@@ -321,6 +322,39 @@ cudaError_t launch_k(void (*kernel)(Params...), dim3 grid, dim3 block, size_t sm
 int set_smem_once(const void* kernel, int bytes, uint64_t* done_mask);
 int encode_tensor_map_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                          uint32_t box_inner, uint32_t box_outer);
+
+// Candidate continuations: drafted trees (k_tree*.cu), pages (k_pages.cu), beams (k_beam.cu).
+struct TreeArgs {
+  AttnArgs a;
+  const uint64_t* mask;  // [num_tokens][mask_words]
+  int32_t mask_words;
+};
+int launch_tree_mask(const int32_t* parents, const int32_t* qsl, int32_t num_seqs, int64_t num_tokens, uint64_t* mask,
+                     int32_t words, int32_t* depths, uint32_t* err, cudaStream_t s);
+size_t tree_workspace(const pkv_cache_desc& c, int32_t num_q_heads, int32_t max_query_len, int num_sms);
+int launch_tree_attention(const TreeArgs& t, void* workspace, int num_sms, uint32_t* err, cudaStream_t s);
+int launch_compact_path(const int32_t* path, int32_t max_path, const int32_t* path_lens, const int32_t* bt,
+                        int32_t max_blocks, const int32_t* seq_lens, const int32_t* qsl, int32_t num_seqs, void* kc,
+                        void* vc, const pkv_cache_desc& c, int32_t num_layers, int32_t* new_lens, uint32_t* err,
+                        cudaStream_t s);
+size_t fork_workspace(int32_t num_rows);
+int launch_fork_tables(const int32_t* bt, const int32_t* lens, int32_t rows, int32_t max_blocks, const int32_t* parents,
+                       int32_t num_new, int32_t* refs, int32_t* new_bt, int32_t* new_lens, void* kc, void* vc,
+                       const pkv_cache_desc& c, int32_t num_layers, void* workspace, int num_sms, uint32_t* err,
+                       cudaStream_t s);
+struct BeamArgs {
+  const void* logits;
+  int32_t dtype;
+  int64_t row_stride;
+  const float* cum;
+  const uint8_t* finished;
+  int32_t eos, num_seqs, beams, vocab, select;
+  float* out_scores;
+  int32_t* out_parents;
+  int32_t* out_tokens;
+};
+size_t beam_workspace(int32_t num_seqs, int32_t beams, int32_t vocab, int32_t select, int num_sms);
+int launch_beam_select(const BeamArgs& a, void* workspace, int num_sms, cudaStream_t s);
 
 int run_umma_selftest(const int32_t* params, const void* a_img, const void* b_img, float* d_out, uint32_t* err,
                       cudaStream_t s);
