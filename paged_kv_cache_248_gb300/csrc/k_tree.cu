@@ -1,4 +1,4 @@
-// k_tree.cu -- attention of drafted tokens, which form a tree, over the paged cache, on
+// k_tree.cu -- attention of drafted tokens, which form a tree, over an fp32 paged cache, on
 // CUDA cores; and the ancestor masks of such trees.
 //
 // Mathematics.  Node j of request i sees the keys u < c_i = seq_len - q_len, and of the
@@ -197,10 +197,12 @@ int launch_tree_mask(const int32_t* parents, const int32_t* qsl, int32_t num_seq
                               num_seqs, num_tokens, mask, words, depths, err));
 }
 
-size_t tree_workspace(const pkv_cache_desc&, int32_t, int32_t, int) { return 256; }
+size_t tree_workspace(const pkv_cache_desc& c, int32_t num_q_heads, int32_t max_query_len, int num_sms) {
+  return c.dtype == PKV_BF16 ? tree_tc_workspace(num_q_heads / c.num_kv_heads, max_query_len, num_sms) : 256;
+}
 
-int launch_tree_attention(const TreeArgs& t, void*, int, uint32_t* err, cudaStream_t s) {
-  if (t.a.cache.dtype == PKV_BF16) return launch_typed<__nv_bfloat16, 128>(t, err, s);
+int launch_tree_attention(const TreeArgs& t, void* workspace, int num_sms, uint32_t* err, cudaStream_t s) {
+  if (t.a.cache.dtype == PKV_BF16) return launch_tree_tc(t, workspace, num_sms, err, s);
   return t.a.cache.head_dim == 64 ? launch_typed<float, 64>(t, err, s) : launch_typed<float, 128>(t, err, s);
 }
 

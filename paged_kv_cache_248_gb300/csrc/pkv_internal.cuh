@@ -333,6 +333,8 @@ int launch_tree_mask(const int32_t* parents, const int32_t* qsl, int32_t num_seq
                      int32_t words, int32_t* depths, uint32_t* err, cudaStream_t s);
 size_t tree_workspace(const pkv_cache_desc& c, int32_t num_q_heads, int32_t max_query_len, int num_sms);
 int launch_tree_attention(const TreeArgs& t, void* workspace, int num_sms, uint32_t* err, cudaStream_t s);
+size_t tree_tc_workspace(int32_t group, int32_t max_query_len, int num_sms);
+int launch_tree_tc(const TreeArgs& t, void* workspace, int num_sms, uint32_t* err, cudaStream_t s);
 int launch_compact_path(const int32_t* path, int32_t max_path, const int32_t* path_lens, const int32_t* bt,
                         int32_t max_blocks, const int32_t* seq_lens, const int32_t* qsl, int32_t num_seqs, void* kc,
                         void* vc, const pkv_cache_desc& c, int32_t num_layers, int32_t* new_lens, uint32_t* err,
