@@ -8,32 +8,33 @@
 // of it; the row sum takes the weights unrounded).
 //
 // Rows.  The G query heads of a kv head are folded into the 128 rows of an MMA tile: R = 128 / GP
-// nodes x GP heads (GP = G rounded up to a power of two).  A unit is (request, kv head, up to
-// two row tiles) and runs over all of the request's key tiles of 128 keys.
+// nodes x GP heads (GP = G rounded up to a power of two).  A unit is (request, kv head, one
+// row tile, or two) and goes over all of the request's key tiles of 128 keys.
 //
-// Cut.  All units' key tiles, one after the other, are cut into as many equal runs as there
-// are CTAs (at least kMinTiles long), so that one long request and a thousand short ones keep
-// every SM equally busy; a CTA derives its run from the lengths by itself, without a planning
-// launch.  A unit that lies within one run is finished there; of one that is cut, each run
-// leaves its rows' unnormalised accumulator, maximum and sum, and the merge kernel joins them
-// in order.  A CTA leaves at most two such partials.
+// Cut.  All units' key tiles, one after the other, are cut into equal runs, so that one long
+// request and a thousand short ones keep every SM equally busy; a CTA derives its runs from
+// the lengths by itself, without a planning launch.  A unit that lies within one run is
+// finished there; of one that is cut, each run leaves its rows' unnormalised accumulator,
+// maximum and sum, and the merge kernel joins them in order.  A run leaves at most two such
+// partials.
 //
-// Streams.  Two S/P/O accumulator sets live in TMEM, each with a warpgroup of its own, so that one
-// softmax runs while the tensor core works for the other.  With two row tiles a stream is a row
-// tile, and both read every key tile; with one, the streams take the key tiles by turns and are
-// joined at the end through TMEM, whose lanes both warpgroups can read.  A step n is one S
-// tile: stream n % 2, key tile n / 2 (two row tiles) or n (one).
+// Streams.  Two S/P/O accumulator sets live in TMEM, each with a softmax warpgroup of its own, so
+// that one softmax runs while the tensor core works for the other.
+//   tree_kernel<false>: a stream has a run of its own, of units of one row tile; the streams
+//     take turns at the tensor core and at the rings, a tile each, and one's last rows are
+//     stored while the other goes on.
+//   tree_kernel<true>: a CTA has one run, of units of two row tiles; a stream is a row tile,
+//     and every key tile is loaded once for both.
 //
-// Per CTA (320 threads): warp 0 loads (TMA boxes of the blocks' 16-token rows, 128-byte
-// swizzle, 2 K and 3 V tiles in flight), one thread of warp 1 issues the MMAs, warps 2-5 and
-// 6-9 are the streams' softmax.  The tiles that hold drafted keys (the last one or two of a
-// request) take their visibility from the mask row's bits, the others see every key.  Their V
-// rows are looked through for values that are not finite: a zero weight times those would
-// reach rows that do not see them, so they are taken out of the tile and given back, in the
-// epilogue, to the rows that do.
+// Per CTA (352 threads): warp 0 finds the runs' units and loads Q and K, warp 10 loads V (TMA
+// boxes of the blocks' 16-token rows, 128-byte swizzle; 2 K and 3 V tiles in flight), one
+// thread of warp 1 issues the MMAs, warps 2-5 and 6-9 are the streams' softmax.  The tiles
+// that hold drafted keys (the last one or two of a request) take their visibility from the
+// mask row's bits, the others see every key.  Their V rows are looked through for values that
+// are not finite: a zero weight times those would reach rows that do not see them, so they
+// are taken out of the tile and given back, at the end, to the rows that do.
 //
-// Bound: the K/V bytes, read once per two row tiles, up to about 256 rows a unit, where the
-// tensor core and the exponents take as long.  All waits are bounded (ptx.cuh).
+// All waits are bounded (ptx.cuh).
 #include "ptx.cuh"
 #include "pkv_internal.cuh"
 #include "softmax_row.cuh"
@@ -41,40 +42,42 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr int kKStages = 2;
 constexpr int kVStages = 3;
 constexpr int kHalfBytes = 16384;
 constexpr int kTileBytes = 2 * kHalfBytes;  // 128 x 128 bf16 in two 64-column halves
-constexpr int kRing = 4;
-constexpr uint32_t kTmemCols = 512;  // S_0, S_1 (P over their first 64 columns), O_0, O_1
+constexpr int kRing = 4;                    // items published ahead, per ring
+constexpr uint32_t kTmemCols = 512;         // S_0, S_1 (P over their first 64 columns), O_0, O_1
 constexpr uint32_t kOCol = 256;
 constexpr int kBlocksPerTile = kTileKeys / kBlock;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled when a row's maximum grows by > 2^8
-constexpr int kMinTiles = 2;               // a run's least length: one key tile per stream
 
+// A part of a unit: what one run does of it.
 struct alignas(16) Item {
   int32_t idx;  // -1: the run is over
-  int32_t seq, head, valid;
+  int32_t seq, head, slot;  // slot: where its partial goes, -1: the unit is finished here
   int32_t t0, q_len, ctx, len;
-  int32_t kt0, nt;        // key tiles kt0 .. kt0 + nt - 1
-  int32_t two;            // two row tiles (else the streams share one)
-  int32_t slot;           // partial slot, -1: the unit is finished here
-  int32_t j0[2], nq[2];   // row tile w: its first node and how many
+  int32_t kt0, nt, pad0, pad1;  // key tiles kt0 .. kt0 + nt - 1
+  int32_t j0[2], nq[2];         // row tile w: its first node and how many
+};
+
+struct Run {
+  int64_t begin, end, base;  // key tiles; the first tile of the request it begins in
+  int64_t seq;
 };
 
 struct Ctl {
   uint64_t kfull[kKStages], kempty[kKStages], vfull[kVStages], vempty[kVStages];
   uint64_t s_full[2], o_full[2], o_free[2], p_full[2][2], q_full[2], q_free[2];
-  uint64_t item_full[kRing], item_empty[kRing];
-  uint64_t joined, drain;
-  Item ring[kRing];
-  int bad[kRing];     // a block id outside of the pool
-  int spoilt[kRing];  // a drafted V row that is not finite
-  float ml[2][128][2];  // [stream][row]: maximum and sum
-  int64_t run_begin, run_end, run_len, start_base;
+  uint64_t item_full[2][kRing], item_empty[2][kRing];  // one ring per run
+  uint64_t drain;
+  Item ring[2][kRing];
+  int bad[2][kRing];     // a block id outside of the pool
+  int spoilt[2][kRing];  // a drafted V row that is not finite
+  Run run[2];
+  int64_t run_len;
   int64_t warp_sum[kThreads / 32];
-  int32_t start_seq;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -82,10 +85,10 @@ struct Ctl {
 constexpr int kSmemBytes = (2 + kKStages + kVStages) * kTileBytes + static_cast<int>(sizeof(Ctl));
 static_assert(kSmemBytes <= 232448, "tree attention shared memory");
 
-// What the merge kernel needs of a unit that a CTA begins and does not finish.
+// What the merge kernel needs of a unit that a run begins and does not finish.
 struct alignas(16) Cut {
   int32_t parts;  // runs that hold a part of it, 0: none
-  int32_t head, t0, two;
+  int32_t head, t0, pad;
   int32_t j0[2], nq[2];
 };
 
@@ -97,12 +100,12 @@ struct Params {
   const int32_t* qsl;
   const uint64_t* mask;
   uint32_t* err;
-  float* part_o;   // [2 * CTAs][rows_cap][128]
-  float* part_ml;  // [2 * CTAs][rows_cap][2]
-  Cut* cuts;       // [CTAs]
+  float* part_o;   // [2 * runs][rows_cap][128]
+  float* part_ml;  // [2 * runs][rows_cap][2]
+  Cut* cuts;       // [runs]
   int64_t num_blocks, num_tokens;
   int32_t num_seqs, max_blocks, max_q, mask_words;
-  int32_t hkv, hq, group, gp, gp_log2, rows_q, rows_cap, out_v8;
+  int32_t hkv, hq, group, gp, gp_log2, rows_q, unit_q, rows_cap, min_run, out_v8;
   float scale_log2;
 };
 
@@ -113,22 +116,24 @@ __device__ __forceinline__ void raise_abort(Ctl& c, uint32_t* err) {
 
 // ------------------------------------------------------------------ units
 struct Request {
-  int32_t t0, q_len, len, valid;
+  int32_t t0, q_len, len;
+  bool wrong;            // rows to zero: lengths that do not fit
   int32_t tiles, units;  // key tiles of a unit; units of one kv head
-  int64_t cost;          // key tiles of all its units (an invalid one: a unit that zeroes its rows)
+  int64_t cost;          // key tiles of all its units
 };
 
 __device__ __forceinline__ Request make_request(const Params& P, int32_t q0, int32_t q1, int32_t len) {
   Request r;
   const int64_t n = static_cast<int64_t>(q1) - q0;
   const bool rows = n > 0 && q0 >= 0 && q1 <= P.num_tokens;
+  const bool fits = rows && len >= n && n <= P.max_q && (static_cast<int64_t>(len) + kBlock - 1) / kBlock <= P.max_blocks;
   r.t0 = q0;
   r.q_len = rows ? static_cast<int32_t>(n) : 0;
   r.len = len;
-  r.valid = rows && len >= n && n <= P.max_q && (static_cast<int64_t>(len) + kBlock - 1) / kBlock <= P.max_blocks;
-  r.tiles = r.valid ? (len - 1) / kTileKeys + 1 : 1;
-  r.units = r.valid ? (r.q_len + 2 * P.rows_q - 1) / (2 * P.rows_q) : 1;
-  r.cost = rows ? (r.valid ? static_cast<int64_t>(P.hkv) * r.units * r.tiles : 1) : 0;
+  r.wrong = rows && !fits;
+  r.tiles = fits ? (len - 1) / kTileKeys + 1 : 1;
+  r.units = fits ? (r.q_len + P.unit_q - 1) / P.unit_q : 0;
+  r.cost = static_cast<int64_t>(P.hkv) * r.units * r.tiles;
   return r;
 }
 
@@ -136,12 +141,18 @@ __device__ __forceinline__ Request load_request(const Params& P, int i) {
   return make_request(P, __ldg(P.qsl + i), __ldg(P.qsl + i + 1), __ldg(P.seq_lens + i));
 }
 
-// This CTA's run of key tiles and the request it begins in (all threads).
-__device__ void find_run(const Params& P, Ctl& c) {
+// This CTA's kRuns runs (all threads).  Rows of requests whose lengths do not fit are zeroed here.
+template <int kRuns>
+__device__ void find_runs(const Params& P, Ctl& c) {
   const int per = (P.num_seqs + kThreads - 1) / kThreads;
   const int i0 = min(static_cast<int>(threadIdx.x) * per, P.num_seqs), i1 = min(i0 + per, P.num_seqs);
   int64_t mine = 0;
-  for (int i = i0; i < i1; ++i) mine += load_request(P, i).cost;
+  bool wrong = false;
+  for (int i = i0; i < i1; ++i) {
+    const Request r = load_request(P, i);
+    mine += r.cost;
+    wrong |= r.wrong;
+  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t incl = mine;
 #pragma unroll
@@ -150,289 +161,419 @@ __device__ void find_run(const Params& P, Ctl& c) {
     if (lane >= d) incl += y;
   }
   if (lane == 31) c.warp_sum[warp] = incl;
-  __syncthreads();
+  const bool any_wrong = __syncthreads_or(wrong);
   int64_t before = incl - mine, total = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += c.warp_sum[w];
     total += c.warp_sum[w];
   }
-  const int64_t even = (total + gridDim.x - 1) / gridDim.x;
-  const int64_t run = even > kMinTiles ? even : kMinTiles;
-  const int64_t begin = run * blockIdx.x, end = begin + run < total ? begin + run : total;
-  if (threadIdx.x == 0) {
-    c.run_begin = begin;
-    c.run_end = end;
-    c.run_len = run;
-  }
-  if (begin >= before && begin < before + mine) {
-    for (int i = i0; i < i1; ++i) {
-      const int64_t cost = load_request(P, i).cost;
-      if (begin < before + cost) {
-        c.start_seq = i;
-        c.start_base = before;
-        break;
+  const int64_t runs = static_cast<int64_t>(gridDim.x) * kRuns;
+  const int64_t even = (total + runs - 1) / runs;
+  const int64_t len = even > P.min_run ? even : P.min_run;
+  if (threadIdx.x == 0) c.run_len = len;
+#pragma unroll
+  for (int k = 0; k < kRuns; ++k) {
+    const int64_t begin = len * (static_cast<int64_t>(blockIdx.x) * kRuns + k);
+    if (threadIdx.x == 0) {
+      c.run[k].begin = begin;
+      c.run[k].end = begin + len < total ? begin + len : total;
+    }
+    if (begin >= before && begin < before + mine) {
+      int64_t at = before;
+      for (int i = i0; i < i1; ++i) {
+        const int64_t cost = load_request(P, i).cost;
+        if (begin < at + cost) {
+          c.run[k].seq = i;
+          c.run[k].base = at;
+          break;
+        }
+        at += cost;
       }
-      before += cost;
+    }
+  }
+  if (any_wrong) {
+    for (int i = blockIdx.x; i < P.num_seqs; i += gridDim.x) {
+      const Request r = load_request(P, i);
+      if (!r.wrong) continue;
+      if (threadIdx.x == 0) flag_error(P.err, kErrLength);
+      const int64_t vecs = static_cast<int64_t>(r.q_len) * P.hq * 16;
+      uint4* dst = reinterpret_cast<uint4*>(P.out) + static_cast<int64_t>(r.t0) * P.hq * 16;
+      for (int64_t v = threadIdx.x; v < vecs; v += kThreads) dst[v] = make_uint4(0, 0, 0, 0);
     }
   }
   __syncthreads();
 }
 
-// ------------------------------------------------------------------ producer warp
-__device__ void producer_warp(const Params& P, const CUtensorMap* qmap, const CUtensorMap* kmap, const CUtensorMap* vmap,
-                              Ctl& c, uint8_t* qbuf, uint8_t* kbuf, uint8_t* vbuf) {
-  const int lane = threadIdx.x & 31;
-  volatile int* abort_flag = &c.abort_flag;
-  int64_t pos = c.run_begin, base = c.start_base;
-  const int64_t end = c.run_end, run = c.run_len;
-  int i = c.start_seq, rb = 0;
-  uint32_t it = 0, tk = 0;
-  uint32_t qc[2] = {0, 0};
-  bool ok = true, loaded = false;
-  int32_t my_q0 = 0, my_q1 = 0, my_len = 0;  // lane l: request rb + l
-  Cut cut{};
-  while (ok) {
-    Item info{};
-    info.idx = -1;
-    if (pos < end) {
-      if (!loaded || i - rb >= 32) {
-        rb = i;
-        loaded = true;
-        const int r = min(rb + lane, P.num_seqs - 1);
-        my_q0 = __ldg(P.qsl + r);
-        my_q1 = __ldg(P.qsl + r + 1);
-        my_len = __ldg(P.seq_lens + r);
-      }
-      const int src = i - rb;
-      const Request rq = make_request(P, __shfl_sync(0xffffffffu, my_q0, src), __shfl_sync(0xffffffffu, my_q1, src),
-                                      __shfl_sync(0xffffffffu, my_len, src));
-      if (pos >= base + rq.cost) {  // (cost 0 among them)
-        base += rq.cost;
-        if (++i >= P.num_seqs) pos = end;  // (lengths that changed meanwhile)
-        continue;
-      }
-      const int64_t off = pos - base;
-      const int64_t unit = off / rq.tiles;
-      const int first = static_cast<int>(off - unit * rq.tiles);
-      const int64_t room = end - pos;
-      info.idx = 0;
-      info.seq = i;
-      info.valid = rq.valid;
-      info.t0 = rq.t0;
-      info.q_len = rq.q_len;
-      info.len = rq.len;
-      info.ctx = rq.len - rq.q_len;
-      info.kt0 = first;
-      info.nt = static_cast<int>(rq.tiles - first < room ? rq.tiles - first : room);
-      const int p = static_cast<int>(unit % rq.units);
-      info.head = static_cast<int>(unit / rq.units);
-      for (int w = 0; w < 2; ++w) {
-        info.j0[w] = (2 * p + w) * P.rows_q;
-        info.nq[w] = max(0, min(P.rows_q, rq.q_len - info.j0[w]));
-      }
-      info.two = info.nq[1] > 0 ? 1 : 0;
-      info.slot = -1;
-      if (rq.valid && info.nt < rq.tiles) {
-        info.slot = 2 * blockIdx.x + (first == 0 ? 1 : 0);
-        if (first == 0) {
-          const int64_t last = (base + (unit + 1) * rq.tiles - 1) / run;
-          cut.parts = static_cast<int32_t>(last - blockIdx.x) + 1;
-          cut.head = info.head;
-          cut.t0 = info.t0;
-          cut.two = info.two;
-          for (int w = 0; w < 2; ++w) {
-            cut.j0[w] = info.j0[w];
-            cut.nq[w] = info.nq[w];
-          }
-        }
-      }
-      pos += info.nt;
+// Walks the items of a run; the whole warp holds it, lane l the lengths of request rb + l.
+struct Walk {
+  int64_t pos, end, base;
+  int i, rb;
+  int32_t q0, q1, len;
+};
+
+__device__ __forceinline__ Walk start_walk(const Run& r) {
+  return Walk{r.begin, r.end, r.base, static_cast<int>(r.seq), -64, 0, 0, 0};
+}
+
+// The next item of run number `run` (idx -1: none is left).
+__device__ __noinline__ Item next_item(const Params& P, Walk& k, int run, int64_t run_len) {
+  Item info{};
+  info.idx = -1;
+  while (k.pos < k.end) {
+    if (k.i - k.rb >= 32) {
+      k.rb = k.i;
+      const int r = min(k.rb + static_cast<int>(threadIdx.x & 31), P.num_seqs - 1);
+      k.q0 = __ldg(P.qsl + r);
+      k.q1 = __ldg(P.qsl + r + 1);
+      k.len = __ldg(P.seq_lens + r);
     }
-    const int slot = it % kRing;
-    if (!mbar_wait(&c.item_empty[slot], ((it / kRing) & 1) ^ 1, abort_flag)) {
-      ok = false;
-      break;
+    const int src = k.i - k.rb;
+    const Request rq = make_request(P, __shfl_sync(0xffffffffu, k.q0, src), __shfl_sync(0xffffffffu, k.q1, src),
+                                    __shfl_sync(0xffffffffu, k.len, src));
+    if (k.pos >= k.base + rq.cost) {  // (cost 0 among them)
+      k.base += rq.cost;
+      if (++k.i >= P.num_seqs) k.pos = k.end;  // (lengths that changed meanwhile)
+      continue;
     }
-    if (lane == 0) {
-      c.ring[slot] = info;
-      c.bad[slot] = 0;
-      c.spoilt[slot] = 0;
-      mbar_arrive(&c.item_full[slot]);
-    }
-    __syncwarp();
-    ++it;
-    if (info.idx < 0) break;
-    if (!info.valid) continue;
+    const int64_t off = k.pos - k.base;
+    const int unit = static_cast<int>(off / rq.tiles);
+    const int first = static_cast<int>(off - static_cast<int64_t>(unit) * rq.tiles);
+    const int64_t room = k.end - k.pos;
+    info.idx = 0;
+    info.seq = k.i;
+    info.t0 = rq.t0;
+    info.q_len = rq.q_len;
+    info.len = rq.len;
+    info.ctx = rq.len - rq.q_len;
+    info.kt0 = first;
+    info.nt = static_cast<int>(rq.tiles - first < room ? rq.tiles - first : room);
+    info.head = unit / rq.units;
+    const int j = (unit - info.head * rq.units) * P.unit_q;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      if (w == 1 && !info.two) break;
-      if (!mbar_wait(&c.q_free[w], (qc[w] & 1) ^ 1, abort_flag)) {
-        ok = false;
-        break;
-      }
-      if (lane == 0) {
-        uint8_t* q = qbuf + w * kTileBytes;
-        mbar_arrive_expect_tx(&c.q_full[w], kTileBytes);
-        const int32_t y = info.head * P.group, z = info.t0 + info.j0[w];
-        tma_load_3d(q, qmap, &c.q_full[w], 0, y, z, l2_policy_evict_first());
-        tma_load_3d(q + kHalfBytes, qmap, &c.q_full[w], 64, y, z, l2_policy_evict_first());
-      }
-      __syncwarp();
-      ++qc[w];
+      info.j0[w] = j + w * P.rows_q;
+      info.nq[w] = max(0, min(P.rows_q, min(rq.q_len, j + P.unit_q) - info.j0[w]));
     }
-    if (!ok) break;
-    const int32_t* btrow = P.bt + static_cast<int64_t>(info.seq) * P.max_blocks;
-    const int blocks = (info.len - 1) / kBlock + 1;
-    int at = info.kt0 * kBlocksPerTile + lane;  // this lane's block of the next key tile
-    int id = lane < kBlocksPerTile && at < blocks ? __ldg(btrow + at) : 0;
-    for (int j = 0; j < info.nt; ++j) {
-      const int nblk = min(kBlocksPerTile, blocks - (info.kt0 + j) * kBlocksPerTile);
-      int cur = id;
-      at += kBlocksPerTile;  // the next tile's ids load while this one waits for its slots
-      if (j + 1 < info.nt) id = lane < kBlocksPerTile && at < blocks ? __ldg(btrow + at) : 0;
-      const bool wrong = lane < nblk && (cur < 0 || cur >= P.num_blocks);
+    info.slot = info.nt == rq.tiles ? -1 : 2 * run + (first == 0 ? 1 : 0);
+    if (info.slot >= 0 && first == 0 && (threadIdx.x & 31) == 0) {  // the unit goes on in the next runs
+      Cut cut;
+      const int64_t last = (k.base + (static_cast<int64_t>(unit) + 1) * rq.tiles - 1) / run_len;
+      cut.parts = static_cast<int32_t>(last - run) + 1;
+      cut.head = info.head;
+      cut.t0 = info.t0;
+      cut.pad = 0;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        cut.j0[w] = info.j0[w];
+        cut.nq[w] = info.nq[w];
+      }
+      P.cuts[run] = cut;
+    }
+    k.pos += info.nt;
+    break;
+  }
+  return info;
+}
+
+// ------------------------------------------------------------------ loads
+// Publishes an item in ring k (the whole warp).
+__device__ __forceinline__ bool publish(Ctl& c, int k, uint32_t it, const Item& info, volatile int* abort_flag) {
+  const int slot = it % kRing;
+  if (!mbar_wait(&c.item_empty[k][slot], ((it / kRing) & 1) ^ 1, abort_flag)) return false;
+  if ((threadIdx.x & 31) == 0) {
+    c.ring[k][slot] = info;
+    c.bad[k][slot] = 0;
+    c.spoilt[k][slot] = 0;
+    mbar_arrive(&c.item_full[k][slot]);
+  }
+  __syncwarp();
+  return true;
+}
+
+// Q tile w: the item's rows from node j0 on.  n counts its loads.
+__device__ __forceinline__ bool load_q(const Params& P, const CUtensorMap* qmap, Ctl& c, uint8_t* qbuf, int w, uint32_t& n,
+                                       const Item& info, int j0, volatile int* abort_flag) {
+  if (!mbar_wait(&c.q_free[w], (n & 1) ^ 1, abort_flag)) return false;
+  if ((threadIdx.x & 31) == 0) {
+    uint8_t* q = qbuf + w * kTileBytes;
+    mbar_arrive_expect_tx(&c.q_full[w], kTileBytes);
+    const int32_t y = info.head * P.group, z = info.t0 + j0;
+    tma_load_3d(q, qmap, &c.q_full[w], 0, y, z, l2_policy_evict_first());
+    tma_load_3d(q + kHalfBytes, qmap, &c.q_full[w], 64, y, z, l2_policy_evict_first());
+  }
+  __syncwarp();
+  ++n;
+  return true;
+}
+
+// This lane's block id of key tile `tile` of a request (lanes 0-7).
+__device__ __forceinline__ int tile_id(const Params& P, const Item& info, int tile) {
+  const int at = tile * kBlocksPerTile + static_cast<int>(threadIdx.x & 31);
+  return (threadIdx.x & 31) < kBlocksPerTile && at <= (info.len - 1) / kBlock
+             ? __ldg(P.bt + static_cast<int64_t>(info.seq) * P.max_blocks + at) : 0;
+}
+
+// A key tile's K or V rows into a ring slot: 2 boxes of 16 rows per block.
+__device__ __forceinline__ bool load_tile(const Params& P, const CUtensorMap* map, uint64_t* full, uint64_t* empty,
+                                          uint8_t* buf, int stages, uint32_t n, const Item& info, int tile, int id,
+                                          volatile int* abort_flag) {
+  const int lane = threadIdx.x & 31;
+  const int s = n % stages;
+  const int nblk = min(kBlocksPerTile, (info.len - 1) / kBlock + 1 - tile * kBlocksPerTile);
+  const int32_t row = (id * P.hkv + info.head) * kBlock;
+  if (!mbar_wait(&empty[s], ((n / stages) & 1) ^ 1, abort_flag)) return false;
+  if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nblk) * 4096u);
+  __syncwarp();
+  if (lane < nblk) {
+    uint8_t* d = buf + s * kTileBytes + lane * 2048;
+    tma_load_2d(d, map, &full[s], 0, row);
+    tma_load_2d(d + kHalfBytes, map, &full[s], 64, row);
+  }
+  return true;
+}
+
+// Copies already issued land before the CTA's shared memory goes away.
+__device__ __forceinline__ void drain_ring(uint64_t* full, int stages, uint32_t n) {
+  for (uint32_t i = n > static_cast<uint32_t>(stages) ? n - stages : 0; i < n; ++i)
+    mbar_wait(&full[i % stages], (i / stages) & 1, nullptr);
+}
+
+// The producers walk the runs' tiles in the order in which the MMA thread takes them: a tile
+// of each run by turns (one run: its tiles).  The K producer finds the items and publishes
+// them, the V producer reads them like the other warps.
+template <int kRuns>
+__device__ void k_producer_warp(const Params& P, const CUtensorMap* qmap, const CUtensorMap* kmap, Ctl& c, uint8_t* qbuf,
+                                uint8_t* kbuf) {
+  const int lane = threadIdx.x & 31;
+  volatile int* abort_flag = &c.abort_flag;
+  Walk walk[kRuns];
+  Item item[kRuns];
+  uint32_t it[kRuns], qn[2] = {0, 0}, tk = 0;
+  int j[kRuns], id[kRuns];
+  bool live[kRuns];
+#pragma unroll
+  for (int k = 0; k < kRuns; ++k) {
+    walk[k] = start_walk(c.run[k]);
+    item[k].nt = 0;
+    it[k] = 0;
+    j[k] = id[k] = 0;
+    live[k] = true;
+    if (lane == 0) P.cuts[static_cast<int64_t>(blockIdx.x) * kRuns + k].parts = 0;
+    __syncwarp();
+  }
+  bool ok = true, any = true;
+  while (ok && any) {
+    any = false;
+#pragma unroll
+    for (int k = 0; k < kRuns; ++k) {
+      if (!ok || !live[k]) continue;
+      if (j[k] == item[k].nt) {
+        item[k] = next_item(P, walk[k], blockIdx.x * kRuns + k, c.run_len);
+        j[k] = 0;
+        ok = publish(c, k, it[k]++, item[k], abort_flag);
+        live[k] = item[k].idx >= 0;
+        if (!ok || !live[k]) continue;
+        id[k] = tile_id(P, item[k], item[k].kt0);
+        if (kRuns == 2) {
+          ok = load_q(P, qmap, c, qbuf, k, qn[k], item[k], item[k].j0[0], abort_flag);
+        } else {
+          ok = load_q(P, qmap, c, qbuf, 0, qn[0], item[k], item[k].j0[0], abort_flag);
+          if (ok && item[k].nq[1] > 0)
+            ok = load_q(P, qmap, c, qbuf, 1, qn[1], item[k], item[k].j0[1], abort_flag);
+        }
+        if (!ok) continue;
+      }
+      any = true;
+      const int tile = item[k].kt0 + j[k];
+      int cur = id[k];
+      ++j[k];
+      if (j[k] < item[k].nt) id[k] = tile_id(P, item[k], tile + 1);  // loads while this tile waits for its slot
+      const bool wrong = cur < 0 || cur >= P.num_blocks;
       if (__any_sync(0xffffffffu, wrong)) {
         if (wrong) flag_error(P.err, kErrBlockId);
         if (wrong) cur = 0;
-        if (lane == 0) c.bad[slot] = 1;
+        if (lane == 0) c.bad[k][(it[k] - 1) % kRing] = 1;
         __syncwarp();
       }
-      const int32_t row = (cur * P.hkv + info.head) * kBlock;
-      const int sk = tk % kKStages, sv = tk % kVStages;
-      if (!mbar_wait(&c.kempty[sk], ((tk / kKStages) & 1) ^ 1, abort_flag)) {
-        ok = false;
-        break;
-      }
-      if (lane == 0) mbar_arrive_expect_tx(&c.kfull[sk], static_cast<uint32_t>(nblk) * 4096u);
-      __syncwarp();
-      if (lane < nblk) {
-        uint8_t* d = kbuf + sk * kTileBytes + lane * 2048;
-        tma_load_2d(d, kmap, &c.kfull[sk], 0, row);
-        tma_load_2d(d + kHalfBytes, kmap, &c.kfull[sk], 64, row);
-      }
-      // (an abort between the two leaves a K tile in flight without its V: counted below)
-      const bool v_ok = mbar_wait(&c.vempty[sv], ((tk / kVStages) & 1) ^ 1, abort_flag);
-      if (!v_ok) {
-        mbar_wait(&c.kfull[sk], (tk / kKStages) & 1, nullptr);
-        ok = false;
-        break;
-      }
-      if (lane == 0) mbar_arrive_expect_tx(&c.vfull[sv], static_cast<uint32_t>(nblk) * 4096u);
-      __syncwarp();
-      if (lane < nblk) {
-        uint8_t* d = vbuf + sv * kTileBytes + lane * 2048;
-        tma_load_2d(d, vmap, &c.vfull[sv], 0, row);
-        tma_load_2d(d + kHalfBytes, vmap, &c.vfull[sv], 64, row);
-      }
-      ++tk;
+      ok = load_tile(P, kmap, c.kfull, c.kempty, kbuf, kKStages, tk, item[k], tile, cur, abort_flag);
+      if (ok) ++tk;
     }
   }
-  if (lane == 0) P.cuts[blockIdx.x] = cut;
   if (!ok && !*abort_flag && lane == 0) raise_abort(c, P.err);
   if (*abort_flag) {
-    // copies already issued land before the CTA's shared memory goes away
-    for (uint32_t n = tk > static_cast<uint32_t>(kKStages) ? tk - kKStages : 0; n < tk; ++n)
-      mbar_wait(&c.kfull[n % kKStages], (n / kKStages) & 1, nullptr);
-    for (uint32_t n = tk > static_cast<uint32_t>(kVStages) ? tk - kVStages : 0; n < tk; ++n)
-      mbar_wait(&c.vfull[n % kVStages], (n / kVStages) & 1, nullptr);
+    drain_ring(c.kfull, kKStages, tk);
 #pragma unroll
     for (int w = 0; w < 2; ++w)
-      if (qc[w] > 0) mbar_wait(&c.q_full[w], (qc[w] - 1) & 1, nullptr);
+      if (qn[w] > 0) mbar_wait(&c.q_full[w], (qn[w] - 1) & 1, nullptr);
   }
 }
 
+template <int kRuns>
+__device__ void v_producer_warp(const Params& P, const CUtensorMap* vmap, Ctl& c, uint8_t* vbuf) {
+  const int lane = threadIdx.x & 31;
+  volatile int* abort_flag = &c.abort_flag;
+  Item item[kRuns];
+  uint32_t it[kRuns], tv = 0;
+  int j[kRuns], id[kRuns];
+  bool live[kRuns];
+#pragma unroll
+  for (int k = 0; k < kRuns; ++k) {
+    item[k].nt = 0;
+    it[k] = 0;
+    j[k] = id[k] = 0;
+    live[k] = true;
+  }
+  bool ok = true, any = true;
+  while (ok && any) {
+    any = false;
+#pragma unroll
+    for (int k = 0; k < kRuns; ++k) {
+      if (!ok || !live[k]) continue;
+      if (j[k] == item[k].nt) {
+        const int slot = it[k] % kRing;
+        ok = mbar_wait(&c.item_full[k][slot], (it[k] / kRing) & 1, abort_flag);
+        if (!ok) continue;
+        item[k] = c.ring[k][slot];
+        __syncwarp();
+        ++it[k];
+        j[k] = 0;
+        live[k] = item[k].idx >= 0;
+        if (!live[k]) continue;
+        if (lane == 0) mbar_arrive(&c.item_empty[k][slot]);
+        id[k] = tile_id(P, item[k], item[k].kt0);
+      }
+      any = true;
+      const int tile = item[k].kt0 + j[k];
+      const int cur = id[k] >= 0 && id[k] < P.num_blocks ? id[k] : 0;  // (the K producer flags it)
+      ++j[k];
+      if (j[k] < item[k].nt) id[k] = tile_id(P, item[k], tile + 1);
+      ok = load_tile(P, vmap, c.vfull, c.vempty, vbuf, kVStages, tv, item[k], tile, cur, abort_flag);
+      if (ok) ++tv;
+    }
+  }
+  if (!ok && !*abort_flag && lane == 0) raise_abort(c, P.err);
+  if (*abort_flag) drain_ring(c.vfull, kVStages, tv);
+}
+
 // ------------------------------------------------------------------ MMA warp
-__device__ void mma_warp(const Params& P, Ctl& c, uint8_t* qbuf, uint8_t* kbuf, uint8_t* vbuf, uint32_t tmem) {
-  if ((threadIdx.x & 31) == 0) {
-    const uint32_t idesc_s = umma_idesc_bf16(128, 128, false, false);
-    const uint32_t idesc_o = umma_idesc_bf16(128, 128, false, true);
-    const uint64_t qdesc[2] = {umma_smem_desc(smem_u32(qbuf), 16, 1024, kLayout128B),
-                               umma_smem_desc(smem_u32(qbuf + kTileBytes), 16, 1024, kLayout128B)};
-    volatile int* abort_flag = &c.abort_flag;
-    uint32_t it = 0, tiles = 0;
-    uint32_t qc[2] = {0, 0}, pc[2] = {0, 0}, ic[2] = {0, 0};
-    bool issued = false, ok = true;
-    auto issue_pv = [&](int w, int sv, bool acc, int hf) {
-      const uint64_t bd = umma_smem_desc(smem_u32(vbuf + sv * kTileBytes), kHalfBytes, 1024, kLayout128B);
+// One thread issues every MMA.  A stream's step is P V of its tile before, then S of its next
+// tile: MMAs of one thread complete in order, so S cannot overwrite the P that this P V reads,
+// and S being complete tells the softmax that O holds every tile before.
+struct Issuer {
+  Ctl& c;
+  uint32_t tmem, q, k, v;  // shared-memory addresses of the Q tiles and the rings
+  uint32_t idesc_s, idesc_o;
+  uint32_t pc[2], oc[2];   // P tiles taken and O accumulators begun, per stream
+  volatile int* abort_flag;
+  bool issued;
+
+  // O_w += P_w V of the tile numbered n; `first` begins O_w anew, `last` reports it.
+  __device__ __forceinline__ bool pv(int w, uint32_t n, bool first, bool last) {
+    const uint64_t bd = umma_smem_desc(v + (n % kVStages) * kTileBytes, kHalfBytes, 1024, kLayout128B);
+    if (!mbar_wait(&c.p_full[w][0], pc[w] & 1, abort_flag)) return false;
+    if (first && !mbar_wait(&c.o_free[w], (oc[w]++ & 1) ^ 1, abort_flag)) return false;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      if (hf && !mbar_wait(&c.p_full[w][1], pc[w] & 1, abort_flag)) return false;
+      tc_fence_after();
 #pragma unroll
       for (int k4 = 0; k4 < 4; ++k4) {
         const int kk = 4 * hf + k4;
         umma_f16_ts(tmem + kOCol + 128 * w, tmem + 128 * w + 8 * kk, umma_desc_advance(bd, kk * 2048), idesc_o,
-                    (acc || kk > 0) ? 1u : 0u);
+                    (!first || kk > 0) ? 1u : 0u);
       }
-    };
-    auto issue_s = [&](int w, int q, int sk) {
-      const uint64_t b = umma_smem_desc(smem_u32(kbuf + sk * kTileBytes), 16, 1024, kLayout128B);
+    }
+    ++pc[w];
+    if (last) umma_commit(&c.o_full[w]);
+    return true;
+  }
+
+  // S_w = Q_w K^T of the tile numbered n; `last`: Q_w has been read.
+  __device__ __forceinline__ bool s(int w, uint32_t n, bool last) {
+    const int slot = n % kKStages;
+    if (!mbar_wait(&c.kfull[slot], (n / kKStages) & 1, abort_flag)) return false;
+    tc_fence_after();
+    const uint64_t a = umma_smem_desc(q + w * kTileBytes, 16, 1024, kLayout128B);
+    const uint64_t b = umma_smem_desc(k + slot * kTileBytes, 16, 1024, kLayout128B);
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
-        umma_f16_ss(tmem + 128 * w, umma_desc_advance(qdesc[q], off), umma_desc_advance(b, off), idesc_s, kk > 0);
-      }
-    };
-    while (ok) {
-      const int slot = it % kRing;
-      if (!mbar_wait(&c.item_full[slot], (it / kRing) & 1, abort_flag)) {
-        ok = false;
-        break;
-      }
-      const Item info = c.ring[slot];
-      ++it;
-      if (info.idx < 0) break;
-      if (info.valid) {
-        const int two = info.two, steps = two ? 2 * info.nt : info.nt;
-        ok = mbar_wait(&c.q_full[0], qc[0] & 1, abort_flag) && (!two || mbar_wait(&c.q_full[1], qc[1] & 1, abort_flag));
-        // Step n: P V of step n - 2 (the stream's last one), then S of step n.  MMAs of one
-        // thread complete in order, so S of step n cannot overwrite the P that step n - 2's
-        // P V reads, and its completion tells the softmax that O holds every tile before.
-        for (int n = 0; n < steps + 2 && ok; ++n) {
-          const int w = n & 1;
-          if (n >= 2) {
-            const int m = n - 2;
-            const int sv = (tiles + (two ? m >> 1 : m)) % kVStages;
-            if (!mbar_wait(&c.p_full[w][0], pc[w] & 1, abort_flag) ||
-                (m < 2 && !mbar_wait(&c.o_free[w], (ic[w] & 1) ^ 1, abort_flag))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            issue_pv(w, sv, m >= 2, 0);
-            if (!mbar_wait(&c.p_full[w][1], pc[w] & 1, abort_flag)) {
-              ok = false;
-              break;
-            }
-            ++pc[w];
-            tc_fence_after();
-            issue_pv(w, sv, m >= 2, 1);
-            if (n >= steps) umma_commit(&c.o_full[w]);
+    for (int kk = 0; kk < 8; ++kk) {
+      const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
+      umma_f16_ss(tmem + 128 * w, umma_desc_advance(a, off), umma_desc_advance(b, off), idesc_s, kk > 0);
+    }
+    umma_commit(&c.s_full[w]);
+    if (last) umma_commit(&c.q_free[w]);
+    issued = true;
+    return true;
+  }
+};
+
+template <int kRuns>
+__device__ void mma_warp(const Params& P, Ctl& c, uint8_t* qbuf, uint8_t* kbuf, uint8_t* vbuf, uint32_t tmem) {
+  if ((threadIdx.x & 31) == 0) {
+    volatile int* abort_flag = &c.abort_flag;
+    Issuer x{c, tmem, smem_u32(qbuf), smem_u32(kbuf), smem_u32(vbuf), umma_idesc_bf16(128, 128, false, false),
+             umma_idesc_bf16(128, 128, false, true), {0, 0}, {0, 0}, abort_flag, false};
+    uint32_t qc[2] = {0, 0}, n = 0;  // Q tiles taken; tiles
+    bool ok = true;
+    if (kRuns == 2) {
+      uint32_t it[2] = {0, 0}, before[2] = {0, 0};
+      int nt[2] = {0, 0}, j[2] = {0, 0};
+      bool live[2] = {true, true}, pending[2] = {false, false};
+      while (ok && (live[0] || live[1])) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (!ok || !live[w]) continue;
+          if (pending[w]) {
+            ok = x.pv(w, before[w], j[w] == 1, j[w] == nt[w]);
+            pending[w] = false;
+            if (!ok) continue;
           }
-          if (n < steps) {
-            const int kt = two ? n >> 1 : n;
-            const uint32_t tk = tiles + kt;
-            if ((!two || w == 0) && !mbar_wait(&c.kfull[tk % kKStages], (tk / kKStages) & 1, abort_flag)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            issue_s(w, two ? w : 0, tk % kKStages);
-            umma_commit(&c.s_full[w]);
-            if (kt == info.nt - 1) umma_commit(&c.q_free[two ? w : 0]);
-            issued = true;
+          if (j[w] == nt[w]) {
+            const int slot = it[w] % kRing;
+            ok = mbar_wait(&c.item_full[w][slot], (it[w] / kRing) & 1, abort_flag);
+            if (!ok) continue;
+            nt[w] = c.ring[w][slot].nt;
+            live[w] = c.ring[w][slot].idx >= 0;
+            ++it[w];
+            j[w] = 0;
+            if (!live[w]) continue;
+            mbar_arrive(&c.item_empty[w][slot]);
+            ok = mbar_wait(&c.q_full[w], qc[w]++ & 1, abort_flag);
+            if (!ok) continue;
           }
-          if (n == 0 && steps == 1) ++n;  // a single step has no second stream
+          ++j[w];
+          ok = x.s(w, n, j[w] == nt[w]);
+          before[w] = n++;
+          pending[w] = true;
         }
-        tiles += info.nt;
-        ++qc[0];
-        ++ic[0];
-        if (two) ++qc[1];
-        if (steps > 1) ++ic[1];
       }
-      if (!ok) break;
-      mbar_arrive(&c.item_empty[slot]);
+    } else {
+      uint32_t it = 0;
+      while (ok) {
+        const int slot = it % kRing;
+        ok = mbar_wait(&c.item_full[0][slot], (it / kRing) & 1, abort_flag);
+        if (!ok) break;
+        const int nt = c.ring[0][slot].nt, rows = c.ring[0][slot].nq[1] > 0 ? 2 : 1;
+        const bool over = c.ring[0][slot].idx < 0;
+        ++it;
+        if (over) break;
+        mbar_arrive(&c.item_empty[0][slot]);
+        for (int w = 0; w < rows && ok; ++w) ok = mbar_wait(&c.q_full[w], qc[w]++ & 1, abort_flag);
+        for (int j = 0; j <= nt && ok; ++j) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (!ok || w >= rows) continue;
+            if (j > 0) ok = x.pv(w, n + j - 1, j == 1, j == nt);
+            if (ok && j < nt) ok = x.s(w, n + j, j == nt - 1);
+          }
+        }
+        n += nt;
+      }
     }
     if (!ok && !*abort_flag) raise_abort(c, P.err);
-    if (issued) {
-      // every MMA, and the arrivals that its commits trigger, is over before TMEM is freed
+    // every MMA, and the arrivals that its commits trigger, is over before TMEM is freed
+    if (x.issued) {
       umma_commit(&c.drain);
       mbar_wait(&c.drain, 0, nullptr);
     }
@@ -470,16 +611,75 @@ __device__ __forceinline__ uint32_t finite2(uint32_t x) {
   return x;
 }
 
+// Takes what is not finite out of row r of a V tile (whole rows past the context), so that a
+// weight of 0 can stand for a key that a row does not see.  Returns whether it took something
+// out that a row may see.
+__device__ __forceinline__ bool clean_v_row(uint8_t* vtile, int r, bool past) {
+  // starting each lane at chunk r mod 8 spreads eight lanes over all banks
+  uint8_t* row = vtile + r * 128;
+  bool wrote = past, spoilt = false;
+#pragma unroll 1  // (called with a score row in registers)
+  for (int ch = 0; ch < 8; ++ch) {
+    const int off = ((ch + r) & 7) * 16;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint4* at = reinterpret_cast<uint4*>(row + half * kHalfBytes + off);
+      if (past) {
+        *at = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      const uint4 x = *at;
+      if (not_finite2(x.x) | not_finite2(x.y) | not_finite2(x.z) | not_finite2(x.w)) {
+        *at = make_uint4(finite2(x.x), finite2(x.y), finite2(x.z), finite2(x.w));
+        wrote = spoilt = true;
+      }
+    }
+  }
+  if (wrote) fence_proxy_async_smem();
+  return spoilt;
+}
+
+// Gives the values that clean_v_row took out of an item's tiles back to a row that sees them, in
+// the row's stored result: sums with what is not finite are not finite (rare).
+__device__ __noinline__ void give_back(const Params& P, const Item& item, const uint64_t* mrow, int kt0, int nt,
+                                       uint8_t* dst) {
+  const int b1 = min((kt0 + nt) * kTileKeys, item.len);
+  for (int u = max(kt0 * kTileKeys, item.ctx); u < b1; ++u) {
+    if (!(seen_bits(mrow, P.mask_words, item.q_len, u - item.ctx) & 1)) continue;
+    const int id = __ldg(P.bt + static_cast<int64_t>(item.seq) * P.max_blocks + u / kBlock);
+    if (id < 0 || id >= P.num_blocks) continue;
+    const __nv_bfloat16* src = P.v_cache + ((static_cast<int64_t>(id) * P.hkv + item.head) * kBlock + u % kBlock) * 128;
+#pragma unroll 1
+    for (int e = 0; e < 128; ++e) {
+      const float x = __bfloat162float(src[e]);
+      if (isfinite(x)) continue;
+      if (item.slot >= 0) {
+        reinterpret_cast<float*>(dst)[e] += x;
+      } else {
+        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(dst) + e;
+        *o = __float2bfloat16_rn(__bfloat162float(*o) + x);
+      }
+    }
+  }
+}
+
+template <int kRuns>
 __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t tmem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wq = warp & 3;        // TMEM lane quarter of this warp
   const int w = (warp - 2) >> 2;  // its stream
-  const int r = wq * 32 + lane;   // its row
+  const int k = kRuns == 2 ? w : 0;     // its item ring
+  const int tile = kRuns == 2 ? 0 : w;  // its row tile of an item
+  const int r = wq * 32 + lane;         // its row
   const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-  const uint32_t srow = tmem + lane_off + 128u * w, orow_t = tmem + lane_off + kOCol + 128u * w;
+  const uint32_t srow = tmem + lane_off + 128u * w, orow = tmem + lane_off + kOCol + 128u * w;
   volatile int* abort_flag = &c.abort_flag;
-  uint32_t it = 0, tc = 0, tiles = 0, turns = 0;
-  uint32_t ic[2] = {0, 0};
+  // Tiles of this stream so far, and their numbers in the rings: with two runs the tiles
+  // alternate as long as both last.
+  const uint32_t other = kRuns == 2 ? static_cast<uint32_t>(max(int64_t(0), c.run[w ^ 1].end - c.run[w ^ 1].begin)) : 0;
+  uint32_t tiles = 0;
+  auto number = [&](uint32_t t) -> uint32_t { return kRuns == 2 ? t + min(t + w, other) : t; };
+  uint32_t it = 0, tc = 0, oc = 0;
   bool ok = true;
   const int rj = r >> P.gp_log2, rg = r & (P.gp - 1);
   const float scale = P.scale_log2;
@@ -487,40 +687,36 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
 
   while (ok) {
     const int slot = it % kRing;
-    if (!mbar_wait(&c.item_full[slot], (it / kRing) & 1, abort_flag)) {
+    if (!mbar_wait(&c.item_full[k][slot], (it / kRing) & 1, abort_flag)) {
       ok = false;
       break;
     }
-    const Item info = c.ring[slot];
+    const Item& item = c.ring[k][slot];  // stays until this warp gives the slot back
     ++it;
-    if (info.idx < 0) break;
-    if (!info.valid) {  // a request whose lengths do not fit: its rows are zero
-      if (r == 0 && w == 0) flag_error(P.err, kErrLength);
-      const int64_t vecs = static_cast<int64_t>(info.q_len) * P.hq * 16;
-      uint4* dst = reinterpret_cast<uint4*>(P.out) + static_cast<int64_t>(info.t0) * P.hq * 16;
-      for (int64_t v = threadIdx.x - 64; v < vecs; v += 256) dst[v] = make_uint4(0, 0, 0, 0);
+    if (item.idx < 0) break;
+    const int nt = item.nt, nq = item.nq[tile];
+    if (nq == 0) {  // the item has one row tile only
+      tiles += nt;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&c.item_empty[slot]);
+      if (lane == 0) mbar_arrive(&c.item_empty[k][slot]);
       continue;
     }
-    const int two = info.two, steps = two ? 2 * info.nt : info.nt;
-    const int tile = two ? w : 0;
-    const int nq = tile ? info.nq[1] : info.nq[0], j0 = tile ? info.j0[1] : info.j0[0];
-    const bool live = rj < nq && rg < P.group;      // a real (node, head) row
+    const int ctx = item.ctx, q_len = item.q_len, kt0 = item.kt0;
+    // this stream is the last one to read the item's tiles, and looks after their V rows
+    const bool releases = kRuns == 2 || w == 1 || item.nq[1] == 0, cleans = kRuns == 2 || w == 0;
+    const bool live = rj < nq && rg < P.group;  // a real (node, head) row
     const bool warp_live = __any_sync(0xffffffffu, live);
-    const uint64_t* mrow = P.mask + (static_cast<int64_t>(info.t0) + j0 + (rj < nq ? rj : 0)) * P.mask_words;
+    const uint64_t* mrow = P.mask + (static_cast<int64_t>(item.t0) + item.j0[tile] + (rj < nq ? rj : 0)) * P.mask_words;
     float m_ref = -INFINITY, l_sum = 0.f;
 
-    for (int n = w; n < steps && ok; n += 2) {
-      const int kt = two ? n >> 1 : n;
-      const uint32_t vt = tiles + kt;
-      const int sv = vt % kVStages;
-      const int k0 = (info.kt0 + kt) * kTileKeys;
-      const bool drafted = k0 + kTileKeys > info.ctx;  // the tile holds keys that not every row sees
+    for (int j = 0; j < nt; ++j) {
+      const uint32_t n = number(tiles + j);
+      const int k0 = (kt0 + j) * kTileKeys;
+      const bool drafted = k0 + kTileKeys > ctx;  // the tile holds keys that not every row sees
       uint32_t vis[4];
       if (drafted && warp_live) {
-        const uint64_t lo = seen_bits(mrow, P.mask_words, info.q_len, k0 - info.ctx);
-        const uint64_t hi = seen_bits(mrow, P.mask_words, info.q_len, k0 - info.ctx + 64);
+        const uint64_t lo = seen_bits(mrow, P.mask_words, q_len, k0 - ctx);
+        const uint64_t hi = seen_bits(mrow, P.mask_words, q_len, k0 - ctx + 64);
         vis[0] = static_cast<uint32_t>(lo);
         vis[1] = static_cast<uint32_t>(lo >> 32);
         vis[2] = static_cast<uint32_t>(hi);
@@ -532,46 +728,21 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
       }
       ++tc;
       tc_fence_after();
-      // S of this step is complete, and with it every MMA issued before: the K tile has been
-      // read by its last reader, and so has the V tile of this stream's previous step
-      if (r == 0 && (!two || w == 1)) {
-        mbar_arrive(&c.kempty[vt % kKStages]);
-        if (n >= 2) mbar_arrive(&c.vempty[(tiles + (two ? kt - 1 : kt - 2)) % kVStages]);
+      // S of this tile is complete, and with it every MMA issued before: K has been read, and
+      // V of the tile before
+      if (r == 0 && releases) {
+        mbar_arrive(&c.kempty[n % kKStages]);
+        if (j > 0) mbar_arrive(&c.vempty[number(tiles + j - 1) % kVStages]);
       }
       bool v_ok = true;
-      // Before the first half of P is handed over, V of this key tile has landed, its rows
-      // past the context are zero, and drafted rows that are not finite are taken out.
+      // Before the first half of P is handed over, V of this key tile has landed and is clean.
       auto first_half = [&]() {
         if (warp_live) tmem_st_wait();
-        v_ok = mbar_wait(&c.vfull[sv], (vt / kVStages) & 1, abort_flag);
+        v_ok = mbar_wait(&c.vfull[n % kVStages], (n / kVStages) & 1, abort_flag);
         if (!v_ok) return;
-        if (drafted && (!two || w == 0) && k0 + r >= info.ctx) {
-          // starting each lane at chunk r mod 8 spreads eight lanes over all banks
-          uint8_t* vrow = vbuf + sv * kTileBytes + r * 128;
-          const bool past = k0 + r >= info.len;
-          bool wrote = past;
-#pragma unroll
-          for (int ch = 0; ch < 8; ++ch) {
-            const int off = ((ch + r) & 7) * 16;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint4* at = reinterpret_cast<uint4*>(vrow + half * kHalfBytes + off);
-              if (past) {
-                *at = make_uint4(0, 0, 0, 0);
-                continue;
-              }
-              const uint4 x = *at;
-              if (not_finite2(x.x) | not_finite2(x.y) | not_finite2(x.z) | not_finite2(x.w)) {
-                *at = make_uint4(finite2(x.x), finite2(x.y), finite2(x.z), finite2(x.w));
-                *reinterpret_cast<volatile int*>(&c.spoilt[slot]) = 1;
-                wrote = true;
-              }
-            }
-          }
-          if (wrote) {
-            fence_proxy_async_smem();
-          }
-        }
+        if (drafted && cleans && k0 + r >= ctx &&
+            clean_v_row(vbuf + (n % kVStages) * kTileBytes, r, k0 + r >= ctx + q_len))
+          *reinterpret_cast<volatile int*>(&c.spoilt[k][slot]) = 1;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&c.p_full[w][0]);
@@ -582,7 +753,7 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
         if (drafted) raw = pos_scale ? row_extremum_bits<true>(srow, vis) : row_extremum_bits<false>(srow, vis);
         else raw = pos_scale ? row_extremum<true, false>(srow, kTileKeys) : row_extremum<false, true>(srow, kTileKeys);
         const float tmax = raw == hidden ? -INFINITY : raw * scale;
-        if (n < 2) {
+        if (j == 0) {
           m_ref = tmax;
         } else {
           const bool need = tmax > m_ref + kRescaleThreshold;
@@ -592,10 +763,10 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
 #pragma unroll
             for (int ch = 0; ch < 8; ++ch) {
               uint32_t v[16];
-              tmem_ld16_sync(orow_t + 16 * ch, v);
+              tmem_ld16_sync(orow + 16 * ch, v);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
-              tmem_st16(orow_t + 16 * ch, v);
+              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+              tmem_st16(orow + 16 * ch, v);
             }
             tmem_st_wait();
             l_sum *= alpha;
@@ -606,9 +777,9 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
         const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
         l_sum += drafted ? row_exp_to_p_bits(srow, vis, scale, m_use, first_half)
                          : row_exp_to_p<false>(srow, kTileKeys, scale, m_use, first_half);
-        if (v_ok) tmem_st_wait();
+        tmem_st_wait();
       } else {
-        first_half();
+        first_half();  // (no row of this warp is stored: its P may hold anything)
       }
       if (!v_ok) {
         ok = false;
@@ -619,163 +790,76 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
       if (lane == 0) mbar_arrive(&c.p_full[w][1]);
     }
     if (!ok) break;
-    const uint32_t last_v = two ? info.nt - 1 : (info.nt - 1 - ((info.nt - 1 - w) & 1));  // this stream's last key tile
-    const bool both = steps > 1;
-    float a0 = 1.f, a1 = 0.f;  // weights of O_0 and O_1 (one row tile), of O_w (two)
-    if (two) {
-      if (!mbar_wait(&c.o_full[w], ic[w] & 1, abort_flag)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      if (r == 0 && w == 1) mbar_arrive(&c.vempty[(tiles + last_v) % kVStages]);
-    } else {
-      // Both streams' maxima and sums, then their accumulators.  A stream's O being complete
-      // (the first stream's, for one without a step) means that all eight warps have read
-      // the unit before, so that ml may be written.
-      const int mine = w < steps ? w : 0;
-      if (!mbar_wait(&c.o_full[mine], ic[mine] & 1, abort_flag)) {
-        ok = false;
-        break;
-      }
-      c.ml[w][r][0] = m_ref;
-      c.ml[w][r][1] = l_sum;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c.joined);
-      if (!mbar_wait(&c.joined, turns & 1, abort_flag) || !mbar_wait(&c.o_full[0], ic[0] & 1, abort_flag) ||
-          (both && !mbar_wait(&c.o_full[1], ic[1] & 1, abort_flag))) {
-        ok = false;
-        break;
-      }
-      ++turns;
-      tc_fence_after();
-      if (r == 0 && w < steps) mbar_arrive(&c.vempty[(tiles + last_v) % kVStages]);
-      if (both) {
-        const float m0 = c.ml[0][r][0], m1 = c.ml[1][r][0];
-        m_ref = fmaxf(m0, m1);
-        if (isnan(m0) || isnan(m1)) m_ref = m0 + m1;
-        a0 = m0 == -INFINITY ? 0.f : exp2f(m0 - m_ref);
-        a1 = m1 == -INFINITY ? 0.f : exp2f(m1 - m_ref);
-        l_sum = c.ml[0][r][1] * a0 + c.ml[1][r][1] * a1;
-      } else {
-        m_ref = c.ml[0][r][0];
-        l_sum = c.ml[0][r][1];
-      }
+    if (!mbar_wait(&c.o_full[w], oc++ & 1, abort_flag)) {
+      ok = false;
+      break;
     }
-    ++ic[0];
-    if (both) ++ic[1];
-    tiles += info.nt;
-    const bool bad = c.bad[slot] != 0, spoilt = *reinterpret_cast<volatile int*>(&c.spoilt[slot]) != 0;
-    // columns: a whole row per thread with two row tiles, half of it per stream with one
-    const int c0 = two ? 0 : 64 * w;
-    uint32_t v[4][32];
-    if (two) {
+    tc_fence_after();
+    if (r == 0 && releases) mbar_arrive(&c.vempty[number(tiles + nt - 1) % kVStages]);
+    tiles += nt;
+    const bool bad = c.bad[k][slot] != 0;
+    const int part = item.slot;
+    // where the row goes: the output, or its partial
+    uint8_t* dst;
+    if (part < 0)
+      dst = reinterpret_cast<uint8_t*>(P.out + ((static_cast<int64_t>(item.t0) + item.j0[tile] + rj) * P.hq +
+                                                static_cast<int64_t>(item.head) * P.group + rg) * 128);
+    else
+      dst = reinterpret_cast<uint8_t*>(P.part_o + (static_cast<int64_t>(part) * P.rows_cap + 128 * tile + r) * 128);
+    uint32_t v[4][32];  // the whole O row from TMEM before any store
 #pragma unroll
-      for (int h = 0; h < 4; ++h) tmem_ld32_issue(orow_t + 32 * h, v[h]);
+    for (int h = 0; h < 4; ++h) tmem_ld32_issue(orow + 32 * h, v[h]);
 #pragma unroll
-      for (int h = 0; h < 4; ++h) tmem_ld32_wait(v[h]);
-    } else {
-      const uint32_t o0 = tmem + lane_off + kOCol + c0;
-      tmem_ld32_issue(o0, v[0]);
-      tmem_ld32_issue(o0 + 32, v[1]);
-      if (both) {
-        tmem_ld32_issue(o0 + 128, v[2]);
-        tmem_ld32_issue(o0 + 160, v[3]);
-      }
-      tmem_ld32_wait(v[0]);
-      tmem_ld32_wait(v[1]);
-      if (both) {
-        tmem_ld32_wait(v[2]);
-        tmem_ld32_wait(v[3]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            v[h][k] = __float_as_uint(fmaf(__uint_as_float(v[h][k]), a0, __uint_as_float(v[h + 2][k]) * a1));
-      }
-    }
-    // O is in registers: the next unit's first P V may overwrite it
+    for (int h = 0; h < 4; ++h) tmem_ld32_wait(v[h]);
+    // O is in registers: the next item's first P V may overwrite it
     tc_fence_before();
     __syncwarp();
-    if (lane < 2) {
-      if (two) mbar_arrive(&c.o_free[w]);  // (twice per warp: eight arrivals in all)
-      else if (lane == 0 || both) mbar_arrive(&c.o_free[lane]);
-    }
-    const int pieces = two ? 4 : 2;
-    if (spoilt && live) {
-      // give the values taken out back to the rows that see them (rare)
-      const int b0 = max(info.kt0 * kTileKeys, info.ctx), b1 = min((info.kt0 + info.nt) * kTileKeys, info.len);
-      for (int u = b0; u < b1; ++u) {
-        if (!(seen_bits(mrow, P.mask_words, info.q_len, u - info.ctx) & 1)) continue;
-        const int id = __ldg(P.bt + static_cast<int64_t>(info.seq) * P.max_blocks + u / kBlock);
-        if (id < 0 || id >= P.num_blocks) continue;
-        const __nv_bfloat16* src =
-            P.v_cache + ((static_cast<int64_t>(id) * P.hkv + info.head) * kBlock + u % kBlock) * 128 + c0;
+    if (lane == 0) mbar_arrive(&c.o_free[w]);
+    if (live && part >= 0) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          if (h >= pieces) break;
-          // (32 values at a time, so that v stays in registers)
+      for (int h = 0; h < 4; ++h)
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const float x = __bfloat162float(src[32 * h + k]);
-            if (!isfinite(x)) v[h][k] = __float_as_uint(__uint_as_float(v[h][k]) + x);
-          }
-        }
-      }
-    }
-    if (info.slot >= 0) {
-      // the rows' partial: accumulator, then maximum and sum (a sum of -1: a bad block id)
-      const int64_t prow = static_cast<int64_t>(info.slot) * P.rows_cap + (two ? 128 * w + r : r);
-      if (live) {
-        float* dst = P.part_o + prow * 128 + c0;
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          if (h >= pieces) break;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t(&w8)[8] = *reinterpret_cast<const uint32_t(*)[8]>(v[h] + 8 * q);
-            st_global_v8(dst + 32 * h + 8 * q, w8);
-          }
-        }
-        if (two || w == 0) {
-          P.part_ml[prow * 2] = m_ref;
-          P.part_ml[prow * 2 + 1] = bad ? -1.f : l_sum;
-        }
-      }
+        for (int q = 0; q < 4; ++q)
+          st_global_v8(dst + 128 * h + 32 * q, *reinterpret_cast<const uint32_t(*)[8]>(v[h] + 8 * q));
+      // maximum and sum (a sum of -1: a bad block id)
+      float* ml = P.part_ml + (static_cast<int64_t>(part) * P.rows_cap + 128 * tile + r) * 2;
+      ml[0] = m_ref;
+      ml[1] = bad ? -1.f : l_sum;
     } else if (live) {
-      const float inv = bad || l_sum == 0.f ? 0.f : 1.f / l_sum;
       const bool zero = bad || l_sum == 0.f;
-      __nv_bfloat16* dst = P.out + ((static_cast<int64_t>(info.t0) + j0 + rj) * P.hq +
-                                    static_cast<int64_t>(info.head) * P.group + rg) * 128 + c0;
+      const float inv = 1.f / l_sum;
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        if (h >= pieces) break;
-        uint32_t wv[16];
+      for (int h = 0; h < 4; ++h)
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          __nv_bfloat162 h2 =
-              __floats2bfloat162_rn(__uint_as_float(v[h][2 * q]) * inv, __uint_as_float(v[h][2 * q + 1]) * inv);
-          wv[q] = zero ? 0u : *reinterpret_cast<uint32_t*>(&h2);
+        for (int q = 0; q < 2; ++q) {
+          uint32_t wv[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(v[h][16 * q + 2 * e]) * inv,
+                                                            __uint_as_float(v[h][16 * q + 2 * e + 1]) * inv);
+            wv[e] = zero ? 0u : *reinterpret_cast<const uint32_t*>(&h2);
+          }
+          if (P.out_v8) {
+            st_global_v8(dst + 64 * h + 32 * q, wv);
+          } else {
+            reinterpret_cast<uint4*>(dst + 64 * h + 32 * q)[0] = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+            reinterpret_cast<uint4*>(dst + 64 * h + 32 * q)[1] = make_uint4(wv[4], wv[5], wv[6], wv[7]);
+          }
         }
-        if (P.out_v8) {
-#pragma unroll
-          for (int q = 0; q < 2; ++q) st_global_v8(dst + 32 * h + 16 * q, *reinterpret_cast<const uint32_t(*)[8]>(wv + 8 * q));
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            reinterpret_cast<uint4*>(dst + 32 * h)[q] = make_uint4(wv[4 * q], wv[4 * q + 1], wv[4 * q + 2], wv[4 * q + 3]);
-        }
-      }
     }
+    if (live && !bad && *reinterpret_cast<volatile int*>(&c.spoilt[k][slot]) != 0)
+      give_back(P, item, mrow, kt0, nt, dst);
     __syncwarp();
-    if (lane == 0) mbar_arrive(&c.item_empty[slot]);
+    if (lane == 0) mbar_arrive(&c.item_empty[k][slot]);
   }
   if (!ok && !*abort_flag && lane == 0) raise_abort(c, P.err);
 }
 
+template <bool kPairs>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ CUtensorMap qmap,
                                                            const __grid_constant__ CUtensorMap kmap,
                                                            const __grid_constant__ CUtensorMap vmap, const Params P) {
+  constexpr int kRuns = kPairs ? 1 : 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if (smem_u32(smem_raw) & 1023u) {  // the swizzled tiles need it, and no room is left to round up in
     flag_error(P.err, kErrTimeout);
@@ -800,19 +884,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       mbar_init(&c.p_full[w][0], 4);
       mbar_init(&c.p_full[w][1], 4);
       mbar_init(&c.o_full[w], 1);
-      mbar_init(&c.o_free[w], 8);
+      mbar_init(&c.o_free[w], 4);
       mbar_init(&c.q_full[w], 1);
       mbar_init(&c.q_free[w], 1);
+      for (int s = 0; s < kRing; ++s) {
+        mbar_init(&c.item_full[w][s], 1);
+        mbar_init(&c.item_empty[w][s], kPairs ? 10 : 6);  // the MMA thread, the V producer and the softmax warps
+      }
+      c.run[w].seq = 0;
+      c.run[w].base = 0;
     }
-    for (int s = 0; s < kRing; ++s) {
-      mbar_init(&c.item_full[s], 1);
-      mbar_init(&c.item_empty[s], 9);  // the MMA warp and the eight softmax warps
-    }
-    mbar_init(&c.joined, 8);
     mbar_init(&c.drain, 1);
     c.abort_flag = 0;
-    c.start_seq = 0;
-    c.start_base = 0;
     fence_mbar_init();
     tma_prefetch_map(&qmap);
     tma_prefetch_map(&kmap);
@@ -825,10 +908,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   const uint32_t tmem = c.tmem_base;
   grid_dep_wait();
   grid_dep_launch();
-  find_run(P, c);
-  if (warp == 0) producer_warp(P, &qmap, &kmap, &vmap, c, qbuf, kbuf, vbuf);
-  else if (warp == 1) mma_warp(P, c, qbuf, kbuf, vbuf, tmem);
-  else softmax_warps(P, c, vbuf, tmem);
+  find_runs<kRuns>(P, c);
+  if (warp == 0) k_producer_warp<kRuns>(P, &qmap, &kmap, c, qbuf, kbuf);
+  else if (warp == 1) mma_warp<kRuns>(P, c, qbuf, kbuf, vbuf, tmem);
+  else if (warp == 10) v_producer_warp<kRuns>(P, &vmap, c, vbuf);
+  else softmax_warps<kRuns>(P, c, vbuf, tmem);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -847,19 +931,18 @@ constexpr int kMergeRows = kMergeThreads / 32;
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const Params P) {
   grid_dep_wait();
   grid_dep_launch();
-  const int cta = blockIdx.x;
+  const int run = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int4* rec = reinterpret_cast<const int4*>(P.cuts + cta);
-  const int4 c0 = __ldcg(rec), c1 = __ldcg(rec + 1);  // parts, head, t0, two; j0[2], nq[2]
+  const int4* rec = reinterpret_cast<const int4*>(P.cuts + run);
+  const int4 c0 = __ldcg(rec), c1 = __ldcg(rec + 1);  // parts, head, t0; j0[2], nq[2]
   const int parts = c0.x;
   if (parts < 2) return;
   const int row = blockIdx.y * kMergeRows + warp;
   const int w = row >> 7, r = row & 127;
-  if (w > c0.w) return;
   const int rj = r >> P.gp_log2, rg = r & (P.gp - 1);
   if (rj >= (w ? c1.w : c1.z) || rg >= P.group) return;
   auto slot_row = [&](int p) -> int64_t {
-    return static_cast<int64_t>(p == 0 ? 2 * cta + 1 : 2 * (cta + p)) * P.rows_cap + row;
+    return static_cast<int64_t>(p == 0 ? 2 * run + 1 : 2 * (run + p)) * P.rows_cap + row;
   };
   float M = -INFINITY;
   bool bad = false, nan = false;
@@ -917,14 +1000,15 @@ struct Layout {
   int rows_cap;
   size_t o_bytes, ml_bytes, bytes;
 };
-Layout layout_of(int32_t group, int32_t max_query_len, int ctas) {
+Layout layout_of(int32_t group, int32_t max_query_len, int num_sms) {
   Layout l;
   const int64_t rows = static_cast<int64_t>(max_query_len) << gp_log2_of(group);
   l.rows_cap = static_cast<int>(rows < 256 ? rows : 256);
-  const size_t slots = 2 * static_cast<size_t>(ctas) * l.rows_cap;
+  const size_t runs = 2 * static_cast<size_t>(num_sms);  // at most two a CTA
+  const size_t slots = 2 * runs * l.rows_cap;
   l.o_bytes = slots * 128 * sizeof(float);
   l.ml_bytes = (slots * 2 * sizeof(float) + 255) & ~static_cast<size_t>(255);
-  l.bytes = l.o_bytes + l.ml_bytes + static_cast<size_t>(ctas) * sizeof(Cut);
+  l.bytes = l.o_bytes + l.ml_bytes + runs * sizeof(Cut);
   return l;
 }
 
@@ -953,11 +1037,15 @@ int launch_tree_tc(const TreeArgs& t, void* workspace, int num_sms, uint32_t* er
   const uint32_t qbox[3] = {64, static_cast<uint32_t>(p.gp), static_cast<uint32_t>(p.rows_q)};
   st = encode_tensor_map_3d(&qm, a.q, qdims, qstrides, qbox);
   if (st) return st;
+  const bool pairs = a.max_query_len > p.rows_q;
+  p.unit_q = pairs ? 2 * p.rows_q : p.rows_q;
+  p.min_run = pairs ? 2 : 1;
   // CTAs: one per SM, fewer where the caller's bounds leave less to do
-  const int64_t units = static_cast<int64_t>((a.max_query_len + 2 * p.rows_q - 1) / (2 * p.rows_q)) * hkv;
+  const int runs_per_cta = pairs ? 1 : 2;
+  const int64_t units = static_cast<int64_t>((a.max_query_len + p.unit_q - 1) / p.unit_q) * hkv;
   const int64_t tiles = units * ((static_cast<int64_t>(a.max_seq_len) + kTileKeys - 1) / kTileKeys);
-  const int64_t most = tiles >= num_sms ? num_sms : tiles * a.num_seqs;
-  const int ctas = static_cast<int>(most < num_sms ? (most + kMinTiles - 1) / kMinTiles : num_sms);
+  const int64_t most = tiles >= 2 * num_sms ? 2 * num_sms : tiles * a.num_seqs;
+  const int ctas = static_cast<int>(most < 2 * num_sms ? (most + 1) / 2 : num_sms);
   const Layout l = layout_of(group, a.max_query_len, num_sms);
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.v_cache = static_cast<const __nv_bfloat16*>(a.v_cache);
@@ -981,13 +1069,14 @@ int launch_tree_tc(const TreeArgs& t, void* workspace, int num_sms, uint32_t* er
   p.rows_cap = l.rows_cap;
   p.out_v8 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 ? 1 : 0;
   p.scale_log2 = a.scale * 1.4426950408889634f;
-  static uint64_t smem_set = 0;
-  st = set_smem_once(reinterpret_cast<const void*>(tree_kernel), kSmemBytes, &smem_set);
+  auto* kernel = pairs ? tree_kernel<true> : tree_kernel<false>;
+  static uint64_t smem_set[2] = {0, 0};
+  st = set_smem_once(reinterpret_cast<const void*>(kernel), kSmemBytes, &smem_set[pairs ? 1 : 0]);
   if (st) return st;
-  st = cuda_status(launch_k(tree_kernel, dim3(ctas), dim3(kThreads), kSmemBytes, s, qm, km, vm, p));
+  st = cuda_status(launch_k(kernel, dim3(ctas), dim3(kThreads), kSmemBytes, s, qm, km, vm, p));
   if (st) return st;
   const int row_blocks = (l.rows_cap + kMergeRows - 1) / kMergeRows;
-  return cuda_status(launch_k(tree_merge_kernel, dim3(ctas, row_blocks), dim3(kMergeThreads), 0, s, p));
+  return cuda_status(launch_k(tree_merge_kernel, dim3(ctas * runs_per_cta, row_blocks), dim3(kMergeThreads), 0, s, p));
 }
 
 }  // namespace pkv
