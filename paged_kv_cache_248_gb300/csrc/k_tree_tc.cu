@@ -106,6 +106,7 @@ struct Params {
   int64_t num_blocks, num_tokens;
   int32_t num_seqs, max_blocks, max_q, mask_words;
   int32_t hkv, hq, group, gp, gp_log2, rows_q, unit_q, rows_cap, min_run, out_v8;
+  int32_t row0[2];  // the MMA tile's row that holds a stream's first row (see launch_tree_tc)
   float scale_log2;
 };
 
@@ -376,7 +377,7 @@ __device__ void k_producer_warp(const Params& P, const CUtensorMap* qmap, const 
         if (!ok || !live[k]) continue;
         id[k] = tile_id(P, item[k], item[k].kt0);
         if (kRuns == 2) {
-          ok = load_q(P, qmap, c, qbuf, k, qn[k], item[k], item[k].j0[0], abort_flag);
+          ok = load_q(P, qmap, c, qbuf, k, qn[k], item[k], item[k].j0[0] - (P.row0[k] >> P.gp_log2), abort_flag);
         } else {
           ok = load_q(P, qmap, c, qbuf, 0, qn[0], item[k], item[k].j0[0], abort_flag);
           if (ok && item[k].nq[1] > 0)
@@ -681,9 +682,10 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
   auto number = [&](uint32_t t) -> uint32_t { return kRuns == 2 ? t + min(t + w, other) : t; };
   uint32_t it = 0, tc = 0, oc = 0;
   bool ok = true;
-  const int rj = r >> P.gp_log2, rg = r & (P.gp - 1);
+  const int row = r - P.row0[w];  // the row within the item's row tile (below 0: none)
+  const int rj = row >> P.gp_log2, rg = r & (P.gp - 1);
   const float scale = P.scale_log2;
-  const bool pos_scale = scale >= 0.f;
+  const float sign = scale >= 0.f ? 1.f : -1.f;
 
   while (ok) {
     const int slot = it % kRing;
@@ -704,17 +706,18 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
     const int ctx = item.ctx, q_len = item.q_len, kt0 = item.kt0;
     // this stream is the last one to read the item's tiles, and looks after their V rows
     const bool releases = kRuns == 2 || w == 1 || item.nq[1] == 0, cleans = kRuns == 2 || w == 0;
-    const bool live = rj < nq && rg < P.group;  // a real (node, head) row
+    const bool live = rj >= 0 && rj < nq && rg < P.group;  // a real (node, head) row
     const bool warp_live = __any_sync(0xffffffffu, live);
-    const uint64_t* mrow = P.mask + (static_cast<int64_t>(item.t0) + item.j0[tile] + (rj < nq ? rj : 0)) * P.mask_words;
+    const uint64_t* mrow = P.mask + (static_cast<int64_t>(item.t0) + item.j0[tile] + (live ? rj : 0)) * P.mask_words;
     float m_ref = -INFINITY, l_sum = 0.f;
 
     for (int j = 0; j < nt; ++j) {
       const uint32_t n = number(tiles + j);
       const int k0 = (kt0 + j) * kTileKeys;
       const bool drafted = k0 + kTileKeys > ctx;  // the tile holds keys that not every row sees
+      const bool masked = drafted || sign < 0.f;  // (a negative scale wants the minimum)
       uint32_t vis[4];
-      if (drafted && warp_live) {
+      if (masked && warp_live) {
         const uint64_t lo = seen_bits(mrow, P.mask_words, q_len, k0 - ctx);
         const uint64_t hi = seen_bits(mrow, P.mask_words, q_len, k0 - ctx + 64);
         vis[0] = static_cast<uint32_t>(lo);
@@ -748,11 +751,9 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
         if (lane == 0) mbar_arrive(&c.p_full[w][0]);
       };
       if (warp_live) {
-        const float hidden = pos_scale ? -INFINITY : INFINITY;
-        float raw;
-        if (drafted) raw = pos_scale ? row_extremum_bits<true>(srow, vis) : row_extremum_bits<false>(srow, vis);
-        else raw = pos_scale ? row_extremum<true, false>(srow, kTileKeys) : row_extremum<false, true>(srow, kTileKeys);
-        const float tmax = raw == hidden ? -INFINITY : raw * scale;
+        // (a row that sees nothing of the tile has no maximum)
+        const float raw = masked ? row_extremum_bits(srow, vis, sign) : row_extremum<true, false>(srow, kTileKeys);
+        const float tmax = raw == -INFINITY ? -INFINITY : raw * (scale * sign);
         if (j == 0) {
           m_ref = tmax;
         } else {
@@ -760,7 +761,7 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
           if (__any_sync(0xffffffffu, need)) {
             const float m_new = need ? tmax : m_ref;
             const float alpha = need ? exp2f(m_ref - m_new) : 1.f;
-#pragma unroll
+#pragma unroll 1  // rare, and small in the instruction cache
             for (int ch = 0; ch < 8; ++ch) {
               uint32_t v[16];
               tmem_ld16_sync(orow + 16 * ch, v);
@@ -775,7 +776,7 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
         }
         // a row that has seen nothing yet: all its weights are 0
         const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-        l_sum += drafted ? row_exp_to_p_bits(srow, vis, scale, m_use, first_half)
+        l_sum += masked ? row_exp_to_p_bits(srow, vis, scale, m_use, first_half)
                          : row_exp_to_p<false>(srow, kTileKeys, scale, m_use, first_half);
         tmem_st_wait();
       } else {
@@ -805,38 +806,26 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
       dst = reinterpret_cast<uint8_t*>(P.out + ((static_cast<int64_t>(item.t0) + item.j0[tile] + rj) * P.hq +
                                                 static_cast<int64_t>(item.head) * P.group + rg) * 128);
     else
-      dst = reinterpret_cast<uint8_t*>(P.part_o + (static_cast<int64_t>(part) * P.rows_cap + 128 * tile + r) * 128);
-    uint32_t v[4][32];  // the whole O row from TMEM before any store
-#pragma unroll
-    for (int h = 0; h < 4; ++h) tmem_ld32_issue(orow + 32 * h, v[h]);
-#pragma unroll
-    for (int h = 0; h < 4; ++h) tmem_ld32_wait(v[h]);
-    // O is in registers: the next item's first P V may overwrite it
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&c.o_free[w]);
-    if (live && part >= 0) {
-#pragma unroll
-      for (int h = 0; h < 4; ++h)
+      dst = reinterpret_cast<uint8_t*>(P.part_o + (static_cast<int64_t>(part) * P.rows_cap + 128 * tile + row) * 128);
+    const bool zero = bad || l_sum == 0.f;
+    const float inv = 1.f / l_sum;
+#pragma unroll 1  // a quarter of the row at a time keeps the code and the registers small
+    for (int h = 0; h < 4; ++h) {
+      uint32_t v[32];
+      tmem_ld32_issue(orow + 32 * h, v);
+      tmem_ld32_wait(v);
+      if (live && part >= 0) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          st_global_v8(dst + 128 * h + 32 * q, *reinterpret_cast<const uint32_t(*)[8]>(v[h] + 8 * q));
-      // maximum and sum (a sum of -1: a bad block id)
-      float* ml = P.part_ml + (static_cast<int64_t>(part) * P.rows_cap + 128 * tile + r) * 2;
-      ml[0] = m_ref;
-      ml[1] = bad ? -1.f : l_sum;
-    } else if (live) {
-      const bool zero = bad || l_sum == 0.f;
-      const float inv = 1.f / l_sum;
-#pragma unroll
-      for (int h = 0; h < 4; ++h)
+          st_global_v8(dst + 128 * h + 32 * q, *reinterpret_cast<const uint32_t(*)[8]>(v + 8 * q));
+      } else if (live) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t wv[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(v[h][16 * q + 2 * e]) * inv,
-                                                            __uint_as_float(v[h][16 * q + 2 * e + 1]) * inv);
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(v[16 * q + 2 * e]) * inv,
+                                                            __uint_as_float(v[16 * q + 2 * e + 1]) * inv);
             wv[e] = zero ? 0u : *reinterpret_cast<const uint32_t*>(&h2);
           }
           if (P.out_v8) {
@@ -846,7 +835,18 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
             reinterpret_cast<uint4*>(dst + 64 * h + 32 * q)[1] = make_uint4(wv[4], wv[5], wv[6], wv[7]);
           }
         }
+      }
+      __syncwarp();
     }
+    if (live && part >= 0) {  // maximum and sum (a sum of -1: a bad block id)
+      float* ml = P.part_ml + (static_cast<int64_t>(part) * P.rows_cap + 128 * tile + row) * 2;
+      ml[0] = m_ref;
+      ml[1] = bad ? -1.f : l_sum;
+    }
+    // O has been read: the next item's first P V may overwrite it
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&c.o_free[w]);
     if (live && !bad && *reinterpret_cast<volatile int*>(&c.spoilt[k][slot]) != 0)
       give_back(P, item, mrow, kt0, nt, dst);
     __syncwarp();
@@ -1068,6 +1068,15 @@ int launch_tree_tc(const TreeArgs& t, void* workspace, int num_sms, uint32_t* er
   p.group = group;
   p.rows_cap = l.rows_cap;
   p.out_v8 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 ? 1 : 0;
+  // Few rows: a warp takes as long for one live row as for 32, so the streams' live rows go to
+  // different SM sub-partitions (a warp's TMEM quarter is its sub-partition), away from the MMA
+  // thread's and the K producer's (1 and 0) where one warp is enough for each.
+  if (!pairs && l.rows_cap <= 32) {
+    p.row0[0] = 64;
+    p.row0[1] = 96;
+  } else if (!pairs && l.rows_cap <= 64) {
+    p.row0[1] = 64;
+  }
   p.scale_log2 = a.scale * 1.4426950408889634f;
   auto* kernel = pairs ? tree_kernel<true> : tree_kernel<false>;
   static uint64_t smem_set[2] = {0, 0};

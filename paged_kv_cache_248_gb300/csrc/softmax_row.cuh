@@ -116,38 +116,41 @@ __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
-// The same two passes over a row whose visible keys are a bit mask: bit c of vis[c / 32]
-// is key c of the tile.
-template <bool kPos>
-__device__ __forceinline__ float row_extremum_bits(uint32_t taddr, const uint32_t (&vis)[4]) {
-  const float hidden = kPos ? -INFINITY : INFINITY;
-  float mx[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) mx[k] = hidden;
-  uint32_t a[32];
-#pragma unroll
+// The same two passes over a row whose visible keys are a bit mask: bit c of vis[c / 32] is key
+// c of the tile.  These run on a request's last tiles only, and are kept small (one 32-column
+// piece of code) so that they do not push the loop over its other tiles out of the
+// instruction cache.  `sign` is 1, or -1 for the minimum, returned negated.
+__device__ __forceinline__ float row_extremum_bits(uint32_t taddr, const uint32_t (&vis)[4], float sign) {
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  uint32_t v0 = vis[0], v1 = vis[1], v2 = vis[2], v3 = vis[3];
+#pragma unroll 1
   for (int h = 0; h < 4; ++h) {
+    uint32_t a[32];
     tmem_ld32_issue(taddr + 32 * h, a);
     tmem_ld32_wait(a);
 #pragma unroll
     for (int k = 0; k < 32; k += 2) {
-      const float xa = (vis[h] >> k & 1u) ? __uint_as_float(a[k]) : hidden;
-      const float xb = (vis[h] >> (k + 1) & 1u) ? __uint_as_float(a[k + 1]) : hidden;
-      const int c = (k >> 1) & 7;
-      mx[c] = kPos ? fmax3(mx[c], xa, xb) : fmin3(mx[c], xa, xb);
+      const float xa = (v0 >> k & 1u) ? __uint_as_float(a[k]) * sign : -INFINITY;
+      const float xb = (v0 >> (k + 1) & 1u) ? __uint_as_float(a[k + 1]) * sign : -INFINITY;
+      const int c = (k >> 1) & 3;
+      mx[c] = fmax3(mx[c], xa, xb);
     }
+    v0 = v1;
+    v1 = v2;
+    v2 = v3;
   }
-  return kPos ? fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])))
-              : fminf(fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3])), fminf(fminf(mx[4], mx[5]), fminf(mx[6], mx[7])));
+  return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
 }
 
 template <typename Half>
 __device__ __forceinline__ float row_exp_to_p_bits(uint32_t taddr, const uint32_t (&vis)[4], float scale, float m_ref,
                                                    Half&& half) {
   float ls[4] = {0.f, 0.f, 0.f, 0.f};
-  uint32_t a[32];
-#pragma unroll
+  uint32_t v0 = vis[0], v1 = vis[1], v2 = vis[2], v3 = vis[3];
+#pragma unroll 1
   for (int h = 0; h < 4; ++h) {
+    if (h == 2) half();
+    uint32_t a[32];
     tmem_ld32_issue(taddr + 32 * h, a);
     tmem_ld32_wait(a);
     uint32_t pw[16];
@@ -155,15 +158,17 @@ __device__ __forceinline__ float row_exp_to_p_bits(uint32_t taddr, const uint32_
     for (int q = 0; q < 16; ++q) {
       float ya, yb;
       ffma2(ya, yb, __uint_as_float(a[2 * q]), __uint_as_float(a[2 * q + 1]), scale, -m_ref);
-      const float pa = ex2_approx((vis[h] >> (2 * q) & 1u) ? ya : -INFINITY);
-      const float pb = ex2_approx((vis[h] >> (2 * q + 1) & 1u) ? yb : -INFINITY);
+      const float pa = ex2_approx((v0 >> (2 * q) & 1u) ? ya : -INFINITY);
+      const float pb = ex2_approx((v0 >> (2 * q + 1) & 1u) ? yb : -INFINITY);
       if (q & 1) fadd2(ls[2], ls[3], pa, pb);
       else fadd2(ls[0], ls[1], pa, pb);
       __nv_bfloat162 h2 = __floats2bfloat162_rn(pa, pb);
       pw[q] = *reinterpret_cast<uint32_t*>(&h2);
     }
     tmem_st16(taddr + 16 * h, pw);
-    if (h == 1) half();
+    v0 = v1;
+    v1 = v2;
+    v2 = v3;
   }
   return (ls[0] + ls[1]) + (ls[2] + ls[3]);
 }
