@@ -79,6 +79,7 @@ struct Ctl {
   int64_t run_len;
   int64_t warp_sum[kThreads / 32];
   uint32_t tmem_base;
+  uint32_t q_loads[2];
   int abort_flag;
 };
 
@@ -109,6 +110,23 @@ struct Params {
   int32_t row0[2];  // the MMA tile's row that holds a stream's first row (see launch_tree_tc)
   float scale_log2;
 };
+
+// mbar_wait (ptx.cuh) in fewer instructions: this kernel has many waits, and the code that its
+// warps run by turns has to stay in the SM's instruction cache (see softmax_warps).  Gives up
+// after 2^31 SM cycles, about a second.
+__device__ __forceinline__ uint32_t sm_clock() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%clock;" : "=r"(t));
+  return t;
+}
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t t0 = sm_clock();
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity))
+    if ((abort_flag != nullptr && *abort_flag) || sm_clock() - t0 > 0x7fffffffu) return false;
+  return true;
+}
 
 __device__ __forceinline__ void raise_abort(Ctl& c, uint32_t* err) {
   *reinterpret_cast<volatile int*>(&c.abort_flag) = 1;
@@ -281,7 +299,7 @@ __device__ __noinline__ Item next_item(const Params& P, Walk& k, int run, int64_
 // Publishes an item in ring k (the whole warp).
 __device__ __forceinline__ bool publish(Ctl& c, int k, uint32_t it, const Item& info, volatile int* abort_flag) {
   const int slot = it % kRing;
-  if (!mbar_wait(&c.item_empty[k][slot], ((it / kRing) & 1) ^ 1, abort_flag)) return false;
+  if (!wait_for(&c.item_empty[k][slot], ((it / kRing) & 1) ^ 1, abort_flag)) return false;
   if ((threadIdx.x & 31) == 0) {
     c.ring[k][slot] = info;
     c.bad[k][slot] = 0;
@@ -295,7 +313,7 @@ __device__ __forceinline__ bool publish(Ctl& c, int k, uint32_t it, const Item& 
 // Q tile w: the item's rows from node j0 on.  n counts its loads.
 __device__ __forceinline__ bool load_q(const Params& P, const CUtensorMap* qmap, Ctl& c, uint8_t* qbuf, int w, uint32_t& n,
                                        const Item& info, int j0, volatile int* abort_flag) {
-  if (!mbar_wait(&c.q_free[w], (n & 1) ^ 1, abort_flag)) return false;
+  if (!wait_for(&c.q_free[w], (n & 1) ^ 1, abort_flag)) return false;
   if ((threadIdx.x & 31) == 0) {
     uint8_t* q = qbuf + w * kTileBytes;
     mbar_arrive_expect_tx(&c.q_full[w], kTileBytes);
@@ -303,8 +321,9 @@ __device__ __forceinline__ bool load_q(const Params& P, const CUtensorMap* qmap,
     tma_load_3d(q, qmap, &c.q_full[w], 0, y, z, l2_policy_evict_first());
     tma_load_3d(q + kHalfBytes, qmap, &c.q_full[w], 64, y, z, l2_policy_evict_first());
   }
-  __syncwarp();
   ++n;
+  if ((threadIdx.x & 31) == 0) c.q_loads[w] = n;
+  __syncwarp();
   return true;
 }
 
@@ -323,13 +342,13 @@ __device__ __forceinline__ bool load_tile(const Params& P, const CUtensorMap* ma
   const int s = n % stages;
   const int nblk = min(kBlocksPerTile, (info.len - 1) / kBlock + 1 - tile * kBlocksPerTile);
   const int32_t row = (id * P.hkv + info.head) * kBlock;
-  if (!mbar_wait(&empty[s], ((n / stages) & 1) ^ 1, abort_flag)) return false;
+  if (!wait_for(&empty[s], ((n / stages) & 1) ^ 1, abort_flag)) return false;
   if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nblk) * 4096u);
   __syncwarp();
   if (lane < nblk) {
     uint8_t* d = buf + s * kTileBytes + lane * 2048;
-    tma_load_2d(d, map, &full[s], 0, row);
-    tma_load_2d(d + kHalfBytes, map, &full[s], 64, row);
+    tma_load_2d(d, map, &full[s], 0, row, l2_policy_evict_first());
+    tma_load_2d(d + kHalfBytes, map, &full[s], 64, row, l2_policy_evict_first());
   }
   return true;
 }
@@ -337,121 +356,117 @@ __device__ __forceinline__ bool load_tile(const Params& P, const CUtensorMap* ma
 // Copies already issued land before the CTA's shared memory goes away.
 __device__ __forceinline__ void drain_ring(uint64_t* full, int stages, uint32_t n) {
   for (uint32_t i = n > static_cast<uint32_t>(stages) ? n - stages : 0; i < n; ++i)
-    mbar_wait(&full[i % stages], (i / stages) & 1, nullptr);
+    wait_for(&full[i % stages], (i / stages) & 1, nullptr);
 }
 
 // The producers walk the runs' tiles in the order in which the MMA thread takes them: a tile
 // of each run by turns (one run: its tiles).  The K producer finds the items and publishes
 // them, the V producer reads them like the other warps.
+// With two runs, a turn works on `a` and the two states change places after it, so that there
+// is one copy of the code.
+template <typename T>
+__device__ __forceinline__ void change_places(T& a, T& b) {
+  const T t = a;
+  a = b;
+  b = t;
+}
+
 template <int kRuns>
 __device__ void k_producer_warp(const Params& P, const CUtensorMap* qmap, const CUtensorMap* kmap, Ctl& c, uint8_t* qbuf,
                                 uint8_t* kbuf) {
+  struct State {
+    Walk walk;
+    Item item;
+    uint32_t it, qn;
+    int j, id, live;
+  };
   const int lane = threadIdx.x & 31;
   volatile int* abort_flag = &c.abort_flag;
-  Walk walk[kRuns];
-  Item item[kRuns];
-  uint32_t it[kRuns], qn[2] = {0, 0}, tk = 0;
-  int j[kRuns], id[kRuns];
-  bool live[kRuns];
-#pragma unroll
-  for (int k = 0; k < kRuns; ++k) {
-    walk[k] = start_walk(c.run[k]);
-    item[k].nt = 0;
-    it[k] = 0;
-    j[k] = id[k] = 0;
-    live[k] = true;
-    if (lane == 0) P.cuts[static_cast<int64_t>(blockIdx.x) * kRuns + k].parts = 0;
-    __syncwarp();
-  }
-  bool ok = true, any = true;
-  while (ok && any) {
-    any = false;
-#pragma unroll
-    for (int k = 0; k < kRuns; ++k) {
-      if (!ok || !live[k]) continue;
-      if (j[k] == item[k].nt) {
-        item[k] = next_item(P, walk[k], blockIdx.x * kRuns + k, c.run_len);
-        j[k] = 0;
-        ok = publish(c, k, it[k]++, item[k], abort_flag);
-        live[k] = item[k].idx >= 0;
-        if (!ok || !live[k]) continue;
-        id[k] = tile_id(P, item[k], item[k].kt0);
-        if (kRuns == 2) {
-          ok = load_q(P, qmap, c, qbuf, k, qn[k], item[k], item[k].j0[0] - (P.row0[k] >> P.gp_log2), abort_flag);
-        } else {
-          ok = load_q(P, qmap, c, qbuf, 0, qn[0], item[k], item[k].j0[0], abort_flag);
-          if (ok && item[k].nq[1] > 0)
-            ok = load_q(P, qmap, c, qbuf, 1, qn[1], item[k], item[k].j0[1], abort_flag);
-        }
-        if (!ok) continue;
+  uint32_t tk = 0, qn1 = 0;
+  State a{start_walk(c.run[0]), Item{}, 0, 0, 0, 0, 1};
+  State b{start_walk(c.run[kRuns - 1]), Item{}, 0, 0, 0, 0, kRuns == 2 ? 1 : 0};
+  if (lane < kRuns) P.cuts[static_cast<int64_t>(blockIdx.x) * kRuns + lane].parts = 0;
+  __syncwarp();
+  bool ok = true;
+#pragma unroll 1
+  for (int k = 0; ok && (a.live | b.live); k ^= kRuns - 1) {
+    if (a.live && a.j == a.item.nt) {
+      a.item = next_item(P, a.walk, blockIdx.x * kRuns + k, c.run_len);
+      a.j = 0;
+      ok = publish(c, k, a.it++, a.item, abort_flag);
+      a.live = a.item.idx >= 0;
+      if (ok && a.live) {
+        a.id = tile_id(P, a.item, a.item.kt0);
+        ok = load_q(P, qmap, c, qbuf, k, a.qn, a.item, a.item.j0[0] - (P.row0[k] >> P.gp_log2), abort_flag);
+        if (kRuns == 1 && ok && a.item.nq[1] > 0)
+          ok = load_q(P, qmap, c, qbuf, 1, qn1, a.item, a.item.j0[1], abort_flag);
       }
-      any = true;
-      const int tile = item[k].kt0 + j[k];
-      int cur = id[k];
-      ++j[k];
-      if (j[k] < item[k].nt) id[k] = tile_id(P, item[k], tile + 1);  // loads while this tile waits for its slot
+    }
+    if (ok && a.live) {
+      const int tile = a.item.kt0 + a.j;
+      int cur = a.id;
+      ++a.j;
+      if (a.j < a.item.nt) a.id = tile_id(P, a.item, tile + 1);  // loads while this tile waits for its slot
       const bool wrong = cur < 0 || cur >= P.num_blocks;
       if (__any_sync(0xffffffffu, wrong)) {
         if (wrong) flag_error(P.err, kErrBlockId);
         if (wrong) cur = 0;
-        if (lane == 0) c.bad[k][(it[k] - 1) % kRing] = 1;
+        if (lane == 0) c.bad[k][(a.it - 1) % kRing] = 1;
         __syncwarp();
       }
-      ok = load_tile(P, kmap, c.kfull, c.kempty, kbuf, kKStages, tk, item[k], tile, cur, abort_flag);
+      ok = load_tile(P, kmap, c.kfull, c.kempty, kbuf, kKStages, tk, a.item, tile, cur, abort_flag);
       if (ok) ++tk;
     }
+    if (kRuns == 2) change_places(a, b);
   }
   if (!ok && !*abort_flag && lane == 0) raise_abort(c, P.err);
   if (*abort_flag) {
     drain_ring(c.kfull, kKStages, tk);
-#pragma unroll
-    for (int w = 0; w < 2; ++w)
-      if (qn[w] > 0) mbar_wait(&c.q_full[w], (qn[w] - 1) & 1, nullptr);
+    const uint32_t q0 = c.q_loads[0], q1 = c.q_loads[1];
+    if (q0 > 0) wait_for(&c.q_full[0], (q0 - 1) & 1, nullptr);
+    if (q1 > 0) wait_for(&c.q_full[1], (q1 - 1) & 1, nullptr);
   }
 }
 
 template <int kRuns>
 __device__ void v_producer_warp(const Params& P, const CUtensorMap* vmap, Ctl& c, uint8_t* vbuf) {
+  struct State {
+    Item item;
+    uint32_t it;
+    int j, id, live;
+  };
   const int lane = threadIdx.x & 31;
   volatile int* abort_flag = &c.abort_flag;
-  Item item[kRuns];
-  uint32_t it[kRuns], tv = 0;
-  int j[kRuns], id[kRuns];
-  bool live[kRuns];
-#pragma unroll
-  for (int k = 0; k < kRuns; ++k) {
-    item[k].nt = 0;
-    it[k] = 0;
-    j[k] = id[k] = 0;
-    live[k] = true;
-  }
-  bool ok = true, any = true;
-  while (ok && any) {
-    any = false;
-#pragma unroll
-    for (int k = 0; k < kRuns; ++k) {
-      if (!ok || !live[k]) continue;
-      if (j[k] == item[k].nt) {
-        const int slot = it[k] % kRing;
-        ok = mbar_wait(&c.item_full[k][slot], (it[k] / kRing) & 1, abort_flag);
-        if (!ok) continue;
-        item[k] = c.ring[k][slot];
+  uint32_t tv = 0;
+  State a{Item{}, 0, 0, 0, 1};
+  State b{Item{}, 0, 0, 0, kRuns == 2 ? 1 : 0};
+  bool ok = true;
+#pragma unroll 1
+  for (int k = 0; ok && (a.live | b.live); k ^= kRuns - 1) {
+    if (a.live && a.j == a.item.nt) {
+      const int slot = a.it % kRing;
+      ok = wait_for(&c.item_full[k][slot], (a.it / kRing) & 1, abort_flag);
+      if (ok) {
+        a.item = c.ring[k][slot];
         __syncwarp();
-        ++it[k];
-        j[k] = 0;
-        live[k] = item[k].idx >= 0;
-        if (!live[k]) continue;
-        if (lane == 0) mbar_arrive(&c.item_empty[k][slot]);
-        id[k] = tile_id(P, item[k], item[k].kt0);
+        ++a.it;
+        a.j = 0;
+        a.live = a.item.idx >= 0;
+        if (a.live) {
+          if (lane == 0) mbar_arrive(&c.item_empty[k][slot]);
+          a.id = tile_id(P, a.item, a.item.kt0);
+        }
       }
-      any = true;
-      const int tile = item[k].kt0 + j[k];
-      const int cur = id[k] >= 0 && id[k] < P.num_blocks ? id[k] : 0;  // (the K producer flags it)
-      ++j[k];
-      if (j[k] < item[k].nt) id[k] = tile_id(P, item[k], tile + 1);
-      ok = load_tile(P, vmap, c.vfull, c.vempty, vbuf, kVStages, tv, item[k], tile, cur, abort_flag);
+    }
+    if (ok && a.live) {
+      const int tile = a.item.kt0 + a.j;
+      const int cur = a.id >= 0 && a.id < P.num_blocks ? a.id : 0;  // (the K producer flags it)
+      ++a.j;
+      if (a.j < a.item.nt) a.id = tile_id(P, a.item, tile + 1);
+      ok = load_tile(P, vmap, c.vfull, c.vempty, vbuf, kVStages, tv, a.item, tile, cur, abort_flag);
       if (ok) ++tv;
     }
+    if (kRuns == 2) change_places(a, b);
   }
   if (!ok && !*abort_flag && lane == 0) raise_abort(c, P.err);
   if (*abort_flag) drain_ring(c.vfull, kVStages, tv);
@@ -464,47 +479,59 @@ __device__ void v_producer_warp(const Params& P, const CUtensorMap* vmap, Ctl& c
 struct Issuer {
   Ctl& c;
   uint32_t tmem, q, k, v;  // shared-memory addresses of the Q tiles and the rings
-  uint32_t idesc_s, idesc_o;
-  uint32_t pc[2], oc[2];   // P tiles taken and O accumulators begun, per stream
   volatile int* abort_flag;
+  uint32_t p_phase, o_phase, q_phase;  // bit w: the phase to wait for next
   bool issued;
 
   // O_w += P_w V of the tile numbered n; `first` begins O_w anew, `last` reports it.
   __device__ __forceinline__ bool pv(int w, uint32_t n, bool first, bool last) {
-    const uint64_t bd = umma_smem_desc(v + (n % kVStages) * kTileBytes, kHalfBytes, 1024, kLayout128B);
-    if (!mbar_wait(&c.p_full[w][0], pc[w] & 1, abort_flag)) return false;
-    if (first && !mbar_wait(&c.o_free[w], (oc[w]++ & 1) ^ 1, abort_flag)) return false;
+    constexpr uint32_t idesc = umma_idesc_bf16(128, 128, false, true);
+    const uint64_t b = umma_smem_desc(v + (n % kVStages) * kTileBytes, kHalfBytes, 1024, kLayout128B);
+    const uint32_t s_col = tmem + 128 * w;
+    if (!wait_for(&c.p_full[w][0], p_phase >> w & 1, abort_flag)) return false;
+    if (first) {
+      if (!wait_for(&c.o_free[w], (o_phase >> w & 1) ^ 1, abort_flag)) return false;
+      o_phase ^= 1u << w;
+    }
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-      if (hf && !mbar_wait(&c.p_full[w][1], pc[w] & 1, abort_flag)) return false;
+      if (hf && !wait_for(&c.p_full[w][1], p_phase >> w & 1, abort_flag)) return false;
       tc_fence_after();
 #pragma unroll
-      for (int k4 = 0; k4 < 4; ++k4) {
-        const int kk = 4 * hf + k4;
-        umma_f16_ts(tmem + kOCol + 128 * w, tmem + 128 * w + 8 * kk, umma_desc_advance(bd, kk * 2048), idesc_o,
-                    (!first || kk > 0) ? 1u : 0u);
-      }
+      for (int k4 = 0; k4 < 4; ++k4)
+        umma_f16_ts(s_col + kOCol, s_col + 32 * hf + 8 * k4, umma_desc_advance(b, (4 * hf + k4) * 2048), idesc,
+                    (!first || hf + k4 > 0) ? 1u : 0u);
     }
-    ++pc[w];
+    p_phase ^= 1u << w;
     if (last) umma_commit(&c.o_full[w]);
     return true;
   }
 
   // S_w = Q_w K^T of the tile numbered n; `last`: Q_w has been read.
   __device__ __forceinline__ bool s(int w, uint32_t n, bool last) {
+    constexpr uint32_t idesc = umma_idesc_bf16(128, 128, false, false);
     const int slot = n % kKStages;
-    if (!mbar_wait(&c.kfull[slot], (n / kKStages) & 1, abort_flag)) return false;
+    if (!wait_for(&c.kfull[slot], (n / kKStages) & 1, abort_flag)) return false;
     tc_fence_after();
     const uint64_t a = umma_smem_desc(q + w * kTileBytes, 16, 1024, kLayout128B);
     const uint64_t b = umma_smem_desc(k + slot * kTileBytes, 16, 1024, kLayout128B);
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk) {
-      const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
-      umma_f16_ss(tmem + 128 * w, umma_desc_advance(a, off), umma_desc_advance(b, off), idesc_s, kk > 0);
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const uint32_t off = h * kHalfBytes + kk * 32;
+        umma_f16_ss(tmem + 128 * w, umma_desc_advance(a, off), umma_desc_advance(b, off), idesc, h + kk > 0);
+      }
     }
     umma_commit(&c.s_full[w]);
     if (last) umma_commit(&c.q_free[w]);
     issued = true;
+    return true;
+  }
+
+  __device__ __forceinline__ bool q_ready(int w) {
+    if (!wait_for(&c.q_full[w], q_phase >> w & 1, abort_flag)) return false;
+    q_phase ^= 1u << w;
     return true;
   }
 };
@@ -513,60 +540,62 @@ template <int kRuns>
 __device__ void mma_warp(const Params& P, Ctl& c, uint8_t* qbuf, uint8_t* kbuf, uint8_t* vbuf, uint32_t tmem) {
   if ((threadIdx.x & 31) == 0) {
     volatile int* abort_flag = &c.abort_flag;
-    Issuer x{c, tmem, smem_u32(qbuf), smem_u32(kbuf), smem_u32(vbuf), umma_idesc_bf16(128, 128, false, false),
-             umma_idesc_bf16(128, 128, false, true), {0, 0}, {0, 0}, abort_flag, false};
-    uint32_t qc[2] = {0, 0}, n = 0;  // Q tiles taken; tiles
+    Issuer x{c, tmem, smem_u32(qbuf), smem_u32(kbuf), smem_u32(vbuf), abort_flag, 0, 0, 0, false};
+    uint32_t n = 0;  // tiles
     bool ok = true;
     if (kRuns == 2) {
-      uint32_t it[2] = {0, 0}, before[2] = {0, 0};
-      int nt[2] = {0, 0}, j[2] = {0, 0};
-      bool live[2] = {true, true}, pending[2] = {false, false};
-      while (ok && (live[0] || live[1])) {
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (!ok || !live[w]) continue;
-          if (pending[w]) {
-            ok = x.pv(w, before[w], j[w] == 1, j[w] == nt[w]);
-            pending[w] = false;
-            if (!ok) continue;
+      struct State {
+        uint32_t it, before;
+        int nt, j, live, pending;
+      };
+      State a{0, 0, 0, 0, 1, 0}, b{0, 0, 0, 0, 1, 0};
+#pragma unroll 1
+      for (int w = 0; ok && (a.live | b.live); w ^= 1) {
+        if (a.pending) ok = x.pv(w, a.before, a.j == 1, a.j == a.nt);
+        a.pending = 0;
+        if (ok && a.live && a.j == a.nt) {
+          const int slot = a.it % kRing;
+          ok = wait_for(&c.item_full[w][slot], (a.it / kRing) & 1, abort_flag);
+          if (ok) {
+            a.nt = c.ring[w][slot].nt;
+            a.live = c.ring[w][slot].idx >= 0;
+            ++a.it;
+            a.j = 0;
+            if (a.live) {
+              mbar_arrive(&c.item_empty[w][slot]);
+              ok = x.q_ready(w);
+            }
           }
-          if (j[w] == nt[w]) {
-            const int slot = it[w] % kRing;
-            ok = mbar_wait(&c.item_full[w][slot], (it[w] / kRing) & 1, abort_flag);
-            if (!ok) continue;
-            nt[w] = c.ring[w][slot].nt;
-            live[w] = c.ring[w][slot].idx >= 0;
-            ++it[w];
-            j[w] = 0;
-            if (!live[w]) continue;
-            mbar_arrive(&c.item_empty[w][slot]);
-            ok = mbar_wait(&c.q_full[w], qc[w]++ & 1, abort_flag);
-            if (!ok) continue;
-          }
-          ++j[w];
-          ok = x.s(w, n, j[w] == nt[w]);
-          before[w] = n++;
-          pending[w] = true;
         }
+        if (ok && a.live) {
+          ++a.j;
+          ok = x.s(w, n, a.j == a.nt);
+          a.before = n++;
+          a.pending = 1;
+        }
+        change_places(a, b);
       }
     } else {
       uint32_t it = 0;
       while (ok) {
         const int slot = it % kRing;
-        ok = mbar_wait(&c.item_full[0][slot], (it / kRing) & 1, abort_flag);
+        ok = wait_for(&c.item_full[0][slot], (it / kRing) & 1, abort_flag);
         if (!ok) break;
         const int nt = c.ring[0][slot].nt, rows = c.ring[0][slot].nq[1] > 0 ? 2 : 1;
         const bool over = c.ring[0][slot].idx < 0;
         ++it;
         if (over) break;
         mbar_arrive(&c.item_empty[0][slot]);
-        for (int w = 0; w < rows && ok; ++w) ok = mbar_wait(&c.q_full[w], qc[w]++ & 1, abort_flag);
-        for (int j = 0; j <= nt && ok; ++j) {
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (!ok || w >= rows) continue;
-            if (j > 0) ok = x.pv(w, n + j - 1, j == 1, j == nt);
-            if (ok && j < nt) ok = x.s(w, n + j, j == nt - 1);
+        ok = x.q_ready(0) && (rows == 1 || x.q_ready(1));
+        // turns of the row tiles: 0, 1, 0, 1, ... (one row tile: 0, 0, ...)
+        int w = 0;
+#pragma unroll 1
+        for (int j = 0; j <= nt && ok;) {
+          if (j > 0) ok = x.pv(w, n + j - 1, j == 1, j == nt);
+          if (ok && j < nt) ok = x.s(w, n + j, j == nt - 1);
+          if (++w == rows) {
+            w = 0;
+            ++j;
           }
         }
         n += nt;
@@ -576,7 +605,7 @@ __device__ void mma_warp(const Params& P, Ctl& c, uint8_t* qbuf, uint8_t* kbuf, 
     // every MMA, and the arrivals that its commits trigger, is over before TMEM is freed
     if (x.issued) {
       umma_commit(&c.drain);
-      mbar_wait(&c.drain, 0, nullptr);
+      wait_for(&c.drain, 0, nullptr);
     }
   }
   __syncwarp();
@@ -664,6 +693,9 @@ __device__ __noinline__ void give_back(const Params& P, const Item& item, const 
   }
 }
 
+// (Code size: the streams, the MMA thread and the producers run different code by turns.  With every
+// loop below unrolled, two thirds of the instruction fetches missed the SM's cache and all of its
+// warps waited for instructions: 64 requests of 128..4096 keys took 169 us instead of MEASURED.)
 template <int kRuns>
 __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t tmem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -689,7 +721,7 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
 
   while (ok) {
     const int slot = it % kRing;
-    if (!mbar_wait(&c.item_full[k][slot], (it / kRing) & 1, abort_flag)) {
+    if (!wait_for(&c.item_full[k][slot], (it / kRing) & 1, abort_flag)) {
       ok = false;
       break;
     }
@@ -725,7 +757,7 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
         vis[2] = static_cast<uint32_t>(hi);
         vis[3] = static_cast<uint32_t>(hi >> 32);
       }
-      if (!mbar_wait(&c.s_full[w], tc & 1, abort_flag)) {
+      if (!wait_for(&c.s_full[w], tc & 1, abort_flag)) {
         ok = false;
         break;
       }
@@ -741,7 +773,7 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
       // Before the first half of P is handed over, V of this key tile has landed and is clean.
       auto first_half = [&]() {
         if (warp_live) tmem_st_wait();
-        v_ok = mbar_wait(&c.vfull[n % kVStages], (n / kVStages) & 1, abort_flag);
+        v_ok = wait_for(&c.vfull[n % kVStages], (n / kVStages) & 1, abort_flag);
         if (!v_ok) return;
         if (drafted && cleans && k0 + r >= ctx &&
             clean_v_row(vbuf + (n % kVStages) * kTileBytes, r, k0 + r >= ctx + q_len))
@@ -777,7 +809,8 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
         // a row that has seen nothing yet: all its weights are 0
         const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
         l_sum += masked ? row_exp_to_p_bits(srow, vis, scale, m_use, first_half)
-                         : row_exp_to_p<false>(srow, kTileKeys, scale, m_use, first_half);
+                        : kRuns == 1 ? row_exp_to_p<false>(srow, kTileKeys, scale, m_use, first_half)
+                                     : row_exp_to_p_loop(srow, scale, m_use, first_half);
         tmem_st_wait();
       } else {
         first_half();  // (no row of this warp is stored: its P may hold anything)
@@ -791,7 +824,7 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
       if (lane == 0) mbar_arrive(&c.p_full[w][1]);
     }
     if (!ok) break;
-    if (!mbar_wait(&c.o_full[w], oc++ & 1, abort_flag)) {
+    if (!wait_for(&c.o_full[w], oc++ & 1, abort_flag)) {
       ok = false;
       break;
     }
@@ -896,6 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     }
     mbar_init(&c.drain, 1);
     c.abort_flag = 0;
+    c.q_loads[0] = c.q_loads[1] = 0;
     fence_mbar_init();
     tma_prefetch_map(&qmap);
     tma_prefetch_map(&kmap);

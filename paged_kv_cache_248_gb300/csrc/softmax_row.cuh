@@ -116,6 +116,43 @@ __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
+// 32 scores to 16 columns of P; adds the weights to ls.
+__device__ __forceinline__ void exp_piece(uint32_t taddr, const uint32_t (&s)[32], float scale, float m_ref,
+                                          float (&ls)[4]) {
+  uint32_t pw[16];
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    float ya, yb;
+    ffma2(ya, yb, __uint_as_float(s[2 * q]), __uint_as_float(s[2 * q + 1]), scale, -m_ref);
+    const float pa = ex2_approx(ya), pb = ex2_approx(yb);
+    if (q & 1) fadd2(ls[2], ls[3], pa, pb);
+    else fadd2(ls[0], ls[1], pa, pb);
+    __nv_bfloat162 h2 = __floats2bfloat162_rn(pa, pb);
+    pw[q] = *reinterpret_cast<uint32_t*>(&h2);
+  }
+  tmem_st16(taddr, pw);
+}
+
+// row_exp_to_p without a mask in half the code: two 64-column pieces in a loop.
+template <typename Half>
+__device__ __forceinline__ float row_exp_to_p_loop(uint32_t taddr, float scale, float m_ref, Half&& half) {
+  float ls[4] = {0.f, 0.f, 0.f, 0.f};
+  uint32_t a[32], b[32];
+  tmem_ld32_issue(taddr, a);
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    tmem_ld32_wait(a);
+    tmem_ld32_issue(taddr + 64 * h + 32, b);
+    exp_piece(taddr + 32 * h, a, scale, m_ref, ls);
+    tmem_ld32_wait(b);
+    tmem_ld32_issue(taddr + 64, a);  // (the second time for nothing)
+    exp_piece(taddr + 32 * h + 16, b, scale, m_ref, ls);
+    if (h == 0) half();
+  }
+  tmem_ld32_wait(a);
+  return (ls[0] + ls[1]) + (ls[2] + ls[3]);
+}
+
 // The same two passes over a row whose visible keys are a bit mask: bit c of vis[c / 32] is key
 // c of the tile.  These run on a request's last tiles only, and are kept small (one 32-column
 // piece of code) so that they do not push the loop over its other tiles out of the
