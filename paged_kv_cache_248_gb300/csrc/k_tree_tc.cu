@@ -11,7 +11,8 @@
 // nodes x GP heads (GP = G rounded up to a power of two).  A unit is (request, kv head, one
 // row tile, or two) and goes over all of the request's key tiles of 128 keys.
 //
-// Cut.  All units' key tiles, one after the other, are cut into equal runs, so that one long
+// Cut.  All units' key tiles, one after the other (and a few places more for each unit, whose
+// beginning and end take time too), are cut into equal runs, so that one long
 // request and a thousand short ones keep every SM equally busy; a CTA derives its runs from
 // the lengths by itself, without a planning launch.  A unit that lies within one run is
 // finished there; of one that is cut, each run leaves its rows' unnormalised accumulator,
@@ -63,7 +64,7 @@ struct alignas(16) Item {
 };
 
 struct Run {
-  int64_t begin, end, base;  // key tiles; the first tile of the request it begins in
+  int64_t begin, end, base;  // places; the first place of the request it begins in
   int64_t seq;
 };
 
@@ -80,6 +81,7 @@ struct Ctl {
   int64_t warp_sum[kThreads / 32];
   uint32_t tmem_base;
   uint32_t q_loads[2];
+  uint32_t number[2][8];  // numbers in the rings of a run's latest tiles
   int abort_flag;
 };
 
@@ -106,7 +108,7 @@ struct Params {
   Cut* cuts;       // [runs]
   int64_t num_blocks, num_tokens;
   int32_t num_seqs, max_blocks, max_q, mask_words;
-  int32_t hkv, hq, group, gp, gp_log2, rows_q, unit_q, rows_cap, min_run, out_v8;
+  int32_t hkv, hq, group, gp, gp_log2, rows_q, unit_q, unit_q_log2, unit_cost, rows_cap, min_run, out_v8;
   int32_t row0[2];  // the MMA tile's row that holds a stream's first row (see launch_tree_tc)
   float scale_log2;
 };
@@ -119,13 +121,23 @@ __device__ __forceinline__ uint32_t sm_clock() {
   asm volatile("mov.u32 %0, %%clock;" : "=r"(t));
   return t;
 }
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   const uint32_t t0 = sm_clock();
-#pragma unroll 1
-  while (!mbar_try_wait(bar, parity))
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
     if ((abort_flag != nullptr && *abort_flag) || sm_clock() - t0 > 0x7fffffffu) return false;
-  return true;
+  }
+}
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return mbar_try_wait(bar, parity) || wait_long(smem_u32(bar), parity, abort_flag);
 }
 
 __device__ __forceinline__ void raise_abort(Ctl& c, uint32_t* err) {
@@ -138,35 +150,39 @@ struct Request {
   int32_t t0, q_len, len;
   bool wrong;            // rows to zero: lengths that do not fit
   int32_t tiles, units;  // key tiles of a unit; units of one kv head
-  int64_t cost;          // key tiles of all its units
+  int32_t cost;          // of all its units: a unit costs its key tiles and P.unit_cost
 };
 
 __device__ __forceinline__ Request make_request(const Params& P, int32_t q0, int32_t q1, int32_t len) {
   Request r;
   const int64_t n = static_cast<int64_t>(q1) - q0;
   const bool rows = n > 0 && q0 >= 0 && q1 <= P.num_tokens;
-  const bool fits = rows && len >= n && n <= P.max_q && (static_cast<int64_t>(len) + kBlock - 1) / kBlock <= P.max_blocks;
+  bool fits = rows && len >= n && n <= P.max_q && (static_cast<int64_t>(len) + kBlock - 1) / kBlock <= P.max_blocks;
   r.t0 = q0;
   r.q_len = rows ? static_cast<int32_t>(n) : 0;
   r.len = len;
+  r.tiles = static_cast<int>(static_cast<uint32_t>(len - 1) / kTileKeys) + 1;
+  r.units = (r.q_len + P.unit_q - 1) >> P.unit_q_log2;
+  // (2^31 places and more would be terabytes of K and V, read once a unit)
+  const int64_t cost = static_cast<int64_t>(P.hkv) * r.units * (r.tiles + P.unit_cost);
+  fits = fits && cost < (int64_t(1) << 31);
   r.wrong = rows && !fits;
-  r.tiles = fits ? (len - 1) / kTileKeys + 1 : 1;
-  r.units = fits ? (r.q_len + P.unit_q - 1) / P.unit_q : 0;
-  r.cost = static_cast<int64_t>(P.hkv) * r.units * r.tiles;
+  r.cost = fits ? static_cast<int32_t>(cost) : 0;
   return r;
 }
 
-__device__ __forceinline__ Request load_request(const Params& P, int i) {
+__device__ __noinline__ Request load_request(const Params& P, int i) {
   return make_request(P, __ldg(P.qsl + i), __ldg(P.qsl + i + 1), __ldg(P.seq_lens + i));
 }
 
-// This CTA's kRuns runs (all threads).  Rows of requests whose lengths do not fit are zeroed here.
+// This CTA's kRuns runs (all threads): run k * CTAs + CTA, so that few runs have an SM each.  Rows of requests whose lengths do not fit are zeroed here.
 template <int kRuns>
 __device__ void find_runs(const Params& P, Ctl& c) {
   const int per = (P.num_seqs + kThreads - 1) / kThreads;
   const int i0 = min(static_cast<int>(threadIdx.x) * per, P.num_seqs), i1 = min(i0 + per, P.num_seqs);
   int64_t mine = 0;
   bool wrong = false;
+#pragma unroll 1
   for (int i = i0; i < i1; ++i) {
     const Request r = load_request(P, i);
     mine += r.cost;
@@ -174,7 +190,7 @@ __device__ void find_runs(const Params& P, Ctl& c) {
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t incl = mine;
-#pragma unroll
+#pragma unroll 1
   for (int d = 1; d < 32; d <<= 1) {
     const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
     if (lane >= d) incl += y;
@@ -182,7 +198,7 @@ __device__ void find_runs(const Params& P, Ctl& c) {
   if (lane == 31) c.warp_sum[warp] = incl;
   const bool any_wrong = __syncthreads_or(wrong);
   int64_t before = incl - mine, total = 0;
-#pragma unroll
+#pragma unroll 1
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += c.warp_sum[w];
     total += c.warp_sum[w];
@@ -191,15 +207,16 @@ __device__ void find_runs(const Params& P, Ctl& c) {
   const int64_t even = (total + runs - 1) / runs;
   const int64_t len = even > P.min_run ? even : P.min_run;
   if (threadIdx.x == 0) c.run_len = len;
-#pragma unroll
+#pragma unroll 1
   for (int k = 0; k < kRuns; ++k) {
-    const int64_t begin = len * (static_cast<int64_t>(blockIdx.x) * kRuns + k);
+    const int64_t begin = len * (static_cast<int64_t>(k) * gridDim.x + blockIdx.x);
     if (threadIdx.x == 0) {
       c.run[k].begin = begin;
       c.run[k].end = begin + len < total ? begin + len : total;
     }
     if (begin >= before && begin < before + mine) {
       int64_t at = before;
+#pragma unroll 1
       for (int i = i0; i < i1; ++i) {
         const int64_t cost = load_request(P, i).cost;
         if (begin < at + cost) {
@@ -212,12 +229,14 @@ __device__ void find_runs(const Params& P, Ctl& c) {
     }
   }
   if (any_wrong) {
+#pragma unroll 1
     for (int i = blockIdx.x; i < P.num_seqs; i += gridDim.x) {
       const Request r = load_request(P, i);
       if (!r.wrong) continue;
       if (threadIdx.x == 0) flag_error(P.err, kErrLength);
       const int64_t vecs = static_cast<int64_t>(r.q_len) * P.hq * 16;
       uint4* dst = reinterpret_cast<uint4*>(P.out) + static_cast<int64_t>(r.t0) * P.hq * 16;
+#pragma unroll 1
       for (int64_t v = threadIdx.x; v < vecs; v += kThreads) dst[v] = make_uint4(0, 0, 0, 0);
     }
   }
@@ -255,10 +274,17 @@ __device__ __noinline__ Item next_item(const Params& P, Walk& k, int run, int64_
       if (++k.i >= P.num_seqs) k.pos = k.end;  // (lengths that changed meanwhile)
       continue;
     }
-    const int64_t off = k.pos - k.base;
-    const int unit = static_cast<int>(off / rq.tiles);
-    const int first = static_cast<int>(off - static_cast<int64_t>(unit) * rq.tiles);
-    const int64_t room = k.end - k.pos;
+    // a unit's first unit_cost places stand for its beginning and end, its tiles come after
+    const uint32_t off = static_cast<uint32_t>(k.pos - k.base);
+    const uint32_t places = rq.tiles + P.unit_cost;
+    const int unit = static_cast<int>(off / places);
+    const uint32_t at = off - unit * places;
+    const int64_t left = k.end - k.pos;  // this run's places of the unit: [at, stop)
+    const uint32_t stop = left < places - at ? at + static_cast<uint32_t>(left) : places;
+    const int first = max(0, static_cast<int>(at) - P.unit_cost);
+    const int nt = max(0, static_cast<int>(stop) - P.unit_cost) - first;
+    k.pos += stop - at;
+    if (nt == 0) continue;
     info.idx = 0;
     info.seq = k.i;
     info.t0 = rq.t0;
@@ -266,9 +292,9 @@ __device__ __noinline__ Item next_item(const Params& P, Walk& k, int run, int64_
     info.len = rq.len;
     info.ctx = rq.len - rq.q_len;
     info.kt0 = first;
-    info.nt = static_cast<int>(rq.tiles - first < room ? rq.tiles - first : room);
-    info.head = unit / rq.units;
-    const int j = (unit - info.head * rq.units) * P.unit_q;
+    info.nt = nt;
+    info.head = static_cast<int>(static_cast<uint32_t>(unit) / static_cast<uint32_t>(rq.units));
+    const int j = (unit - info.head * rq.units) << P.unit_q_log2;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       info.j0[w] = j + w * P.rows_q;
@@ -277,8 +303,8 @@ __device__ __noinline__ Item next_item(const Params& P, Walk& k, int run, int64_
     info.slot = info.nt == rq.tiles ? -1 : 2 * run + (first == 0 ? 1 : 0);
     if (info.slot >= 0 && first == 0 && (threadIdx.x & 31) == 0) {  // the unit goes on in the next runs
       Cut cut;
-      const int64_t last = (k.base + (static_cast<int64_t>(unit) + 1) * rq.tiles - 1) / run_len;
-      cut.parts = static_cast<int32_t>(last - run) + 1;
+      const uint32_t len = run_len < 0x7fffffff ? static_cast<uint32_t>(run_len) : 0x7fffffffu;
+      cut.parts = 1 + static_cast<int32_t>((places - stop + len - 1) / len);
       cut.head = info.head;
       cut.t0 = info.t0;
       cut.pad = 0;
@@ -289,7 +315,6 @@ __device__ __noinline__ Item next_item(const Params& P, Walk& k, int run, int64_
       }
       P.cuts[run] = cut;
     }
-    k.pos += info.nt;
     break;
   }
   return info;
@@ -310,9 +335,10 @@ __device__ __forceinline__ bool publish(Ctl& c, int k, uint32_t it, const Item& 
   return true;
 }
 
-// Q tile w: the item's rows from node j0 on.  n counts its loads.
-__device__ __forceinline__ bool load_q(const Params& P, const CUtensorMap* qmap, Ctl& c, uint8_t* qbuf, int w, uint32_t& n,
+// Q tile w: the item's rows from node j0 on.
+__device__ __forceinline__ bool load_q(const Params& P, const CUtensorMap* qmap, Ctl& c, uint8_t* qbuf, int w,
                                        const Item& info, int j0, volatile int* abort_flag) {
+  const uint32_t n = c.q_loads[w];
   if (!wait_for(&c.q_free[w], (n & 1) ^ 1, abort_flag)) return false;
   if ((threadIdx.x & 31) == 0) {
     uint8_t* q = qbuf + w * kTileBytes;
@@ -321,8 +347,8 @@ __device__ __forceinline__ bool load_q(const Params& P, const CUtensorMap* qmap,
     tma_load_3d(q, qmap, &c.q_full[w], 0, y, z, l2_policy_evict_first());
     tma_load_3d(q + kHalfBytes, qmap, &c.q_full[w], 64, y, z, l2_policy_evict_first());
   }
-  ++n;
-  if ((threadIdx.x & 31) == 0) c.q_loads[w] = n;
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) c.q_loads[w] = n + 1;
   __syncwarp();
   return true;
 }
@@ -334,142 +360,116 @@ __device__ __forceinline__ int tile_id(const Params& P, const Item& info, int ti
              ? __ldg(P.bt + static_cast<int64_t>(info.seq) * P.max_blocks + at) : 0;
 }
 
-// A key tile's K or V rows into a ring slot: 2 boxes of 16 rows per block.
-__device__ __forceinline__ bool load_tile(const Params& P, const CUtensorMap* map, uint64_t* full, uint64_t* empty,
-                                          uint8_t* buf, int stages, uint32_t n, const Item& info, int tile, int id,
-                                          volatile int* abort_flag) {
-  const int lane = threadIdx.x & 31;
-  const int s = n % stages;
-  const int nblk = min(kBlocksPerTile, (info.len - 1) / kBlock + 1 - tile * kBlocksPerTile);
-  const int32_t row = (id * P.hkv + info.head) * kBlock;
-  if (!wait_for(&empty[s], ((n / stages) & 1) ^ 1, abort_flag)) return false;
-  if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nblk) * 4096u);
-  __syncwarp();
-  if (lane < nblk) {
-    uint8_t* d = buf + s * kTileBytes + lane * 2048;
-    tma_load_2d(d, map, &full[s], 0, row, l2_policy_evict_first());
-    tma_load_2d(d + kHalfBytes, map, &full[s], 64, row, l2_policy_evict_first());
-  }
-  return true;
-}
-
-// Copies already issued land before the CTA's shared memory goes away.
-__device__ __forceinline__ void drain_ring(uint64_t* full, int stages, uint32_t n) {
-  for (uint32_t i = n > static_cast<uint32_t>(stages) ? n - stages : 0; i < n; ++i)
-    wait_for(&full[i % stages], (i / stages) & 1, nullptr);
-}
-
 // The producers walk the runs' tiles in the order in which the MMA thread takes them: a tile
-// of each run by turns (one run: its tiles).  The K producer finds the items and publishes
-// them, the V producer reads them like the other warps.
-// With two runs, a turn works on `a` and the two states change places after it, so that there
-// is one copy of the code.
-template <typename T>
-__device__ __forceinline__ void change_places(T& a, T& b) {
-  const T t = a;
-  a = b;
-  b = t;
-}
-
+// of each run by turns (one run: its tiles).  The K producer finds the items, publishes them
+// and loads Q too; the V producer reads the items like the other warps.  Both run this one
+// piece of code, and leave their runs' states in local memory, to keep it small.
 template <int kRuns>
-__device__ void k_producer_warp(const Params& P, const CUtensorMap* qmap, const CUtensorMap* kmap, Ctl& c, uint8_t* qbuf,
-                                uint8_t* kbuf) {
+__device__ void producer_warp(const Params& P, bool is_k, const CUtensorMap* qmap, const CUtensorMap* map, Ctl& c,
+                              uint8_t* qbuf, uint8_t* buf) {
   struct State {
-    Walk walk;
+    Walk walk;  // (K)
     Item item;
-    uint32_t it, qn;
+    uint32_t it, tiles;
     int j, id, live;
   };
   const int lane = threadIdx.x & 31;
   volatile int* abort_flag = &c.abort_flag;
-  uint32_t tk = 0, qn1 = 0;
-  State a{start_walk(c.run[0]), Item{}, 0, 0, 0, 0, 1};
-  State b{start_walk(c.run[kRuns - 1]), Item{}, 0, 0, 0, 0, kRuns == 2 ? 1 : 0};
-  if (lane < kRuns) P.cuts[static_cast<int64_t>(blockIdx.x) * kRuns + lane].parts = 0;
+  uint64_t* full = is_k ? c.kfull : c.vfull;
+  uint64_t* empty = is_k ? c.kempty : c.vempty;
+  const int stages = is_k ? kKStages : kVStages;
+  State st[kRuns];
+#pragma unroll 1
+  for (int k = 0; k < kRuns; ++k) {
+    st[k].walk = start_walk(c.run[k]);
+    st[k].item.nt = 0;
+    st[k].it = st[k].tiles = 0;
+    st[k].j = st[k].id = 0;
+    st[k].live = 1;
+  }
+  if (is_k && lane < kRuns) P.cuts[lane * gridDim.x + blockIdx.x].parts = 0;
   __syncwarp();
+  uint32_t n = 0;
+  int live = kRuns, s = 0, phase = 1;  // of the next slot
   bool ok = true;
 #pragma unroll 1
-  for (int k = 0; ok && (a.live | b.live); k ^= kRuns - 1) {
-    if (a.live && a.j == a.item.nt) {
-      a.item = next_item(P, a.walk, blockIdx.x * kRuns + k, c.run_len);
+  for (int k = 0; ok && live > 0; k ^= kRuns - 1) {
+    State& a = st[k];
+    if (!a.live) continue;
+    if (a.j == a.item.nt) {
+      const int slot = a.it % kRing;
+      if (is_k) {
+        a.item = next_item(P, a.walk, k * gridDim.x + blockIdx.x, c.run_len);
+        ok = publish(c, k, a.it, a.item, abort_flag);
+      } else {
+        ok = wait_for(&c.item_full[k][slot], (a.it / kRing) & 1, abort_flag);
+        if (ok) a.item = c.ring[k][slot];
+        __syncwarp();
+      }
+      ++a.it;
       a.j = 0;
-      ok = publish(c, k, a.it++, a.item, abort_flag);
-      a.live = a.item.idx >= 0;
-      if (ok && a.live) {
-        a.id = tile_id(P, a.item, a.item.kt0);
-        ok = load_q(P, qmap, c, qbuf, k, a.qn, a.item, a.item.j0[0] - (P.row0[k] >> P.gp_log2), abort_flag);
-        if (kRuns == 1 && ok && a.item.nq[1] > 0)
-          ok = load_q(P, qmap, c, qbuf, 1, qn1, a.item, a.item.j0[1], abort_flag);
+      if (!ok) break;
+      if (a.item.idx < 0) {
+        a.live = 0;
+        --live;
+        continue;
+      }
+      a.id = tile_id(P, a.item, a.item.kt0);
+      if (is_k) {
+#pragma unroll 1
+        for (int w = 0; w < 3 - kRuns && ok; ++w)  // the item's one row tile, or two
+          if (kRuns == 2 || a.item.nq[w] > 0)
+            ok = load_q(P, qmap, c, qbuf, kRuns == 2 ? k : w, a.item,
+                        (w ? a.item.j0[1] : a.item.j0[0]) - (P.row0[k] >> P.gp_log2), abort_flag);
+        if (!ok) break;
+      } else if (lane == 0) {
+        mbar_arrive(&c.item_empty[k][slot]);
       }
     }
-    if (ok && a.live) {
-      const int tile = a.item.kt0 + a.j;
-      int cur = a.id;
-      ++a.j;
-      if (a.j < a.item.nt) a.id = tile_id(P, a.item, tile + 1);  // loads while this tile waits for its slot
-      const bool wrong = cur < 0 || cur >= P.num_blocks;
+    const int tile = a.item.kt0 + a.j;
+    int cur = a.id;
+    ++a.j;
+    if (a.j < a.item.nt) a.id = tile_id(P, a.item, tile + 1);  // loads while this tile waits for its slot
+    const bool wrong = cur < 0 || cur >= P.num_blocks;
+    if (wrong) cur = 0;
+    if (is_k) {
       if (__any_sync(0xffffffffu, wrong)) {
         if (wrong) flag_error(P.err, kErrBlockId);
-        if (wrong) cur = 0;
         if (lane == 0) c.bad[k][(a.it - 1) % kRing] = 1;
         __syncwarp();
       }
-      ok = load_tile(P, kmap, c.kfull, c.kempty, kbuf, kKStages, tk, a.item, tile, cur, abort_flag);
-      if (ok) ++tk;
+      if (lane == 0) c.number[k][a.tiles % 8] = n;
+      ++a.tiles;
     }
-    if (kRuns == 2) change_places(a, b);
+    // K or V of the tile into its ring slot: 2 boxes of 16 rows per block
+    const int nblk = min(kBlocksPerTile, (a.item.len - 1) / kBlock + 1 - tile * kBlocksPerTile);
+    const int32_t row = (cur * P.hkv + a.item.head) * kBlock;
+    ok = wait_for(&empty[s], phase, abort_flag);
+    if (!ok) break;
+    if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nblk) * 4096u);
+    __syncwarp();
+    if (lane < nblk) {
+      uint8_t* d = buf + s * kTileBytes + lane * 2048;
+      tma_load_2d(d, map, &full[s], 0, row, l2_policy_evict_first());
+      tma_load_2d(d + kHalfBytes, map, &full[s], 64, row, l2_policy_evict_first());
+    }
+    ++n;
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1;
+    }
   }
   if (!ok && !*abort_flag && lane == 0) raise_abort(c, P.err);
-  if (*abort_flag) {
-    drain_ring(c.kfull, kKStages, tk);
-    const uint32_t q0 = c.q_loads[0], q1 = c.q_loads[1];
-    if (q0 > 0) wait_for(&c.q_full[0], (q0 - 1) & 1, nullptr);
-    if (q1 > 0) wait_for(&c.q_full[1], (q1 - 1) & 1, nullptr);
-  }
-}
-
-template <int kRuns>
-__device__ void v_producer_warp(const Params& P, const CUtensorMap* vmap, Ctl& c, uint8_t* vbuf) {
-  struct State {
-    Item item;
-    uint32_t it;
-    int j, id, live;
-  };
-  const int lane = threadIdx.x & 31;
-  volatile int* abort_flag = &c.abort_flag;
-  uint32_t tv = 0;
-  State a{Item{}, 0, 0, 0, 1};
-  State b{Item{}, 0, 0, 0, kRuns == 2 ? 1 : 0};
-  bool ok = true;
+  if (*abort_flag) {  // copies already issued land before the CTA's shared memory goes away
 #pragma unroll 1
-  for (int k = 0; ok && (a.live | b.live); k ^= kRuns - 1) {
-    if (a.live && a.j == a.item.nt) {
-      const int slot = a.it % kRing;
-      ok = wait_for(&c.item_full[k][slot], (a.it / kRing) & 1, abort_flag);
-      if (ok) {
-        a.item = c.ring[k][slot];
-        __syncwarp();
-        ++a.it;
-        a.j = 0;
-        a.live = a.item.idx >= 0;
-        if (a.live) {
-          if (lane == 0) mbar_arrive(&c.item_empty[k][slot]);
-          a.id = tile_id(P, a.item, a.item.kt0);
-        }
-      }
+    for (uint32_t i = n > static_cast<uint32_t>(stages) ? n - stages : 0; i < n; ++i)
+      wait_for(&full[i % stages], (i / stages) & 1, nullptr);
+#pragma unroll 1
+    for (int w = 0; w < 2 && is_k; ++w) {
+      const uint32_t q = c.q_loads[w];
+      if (q > 0) wait_for(&c.q_full[w], (q - 1) & 1, nullptr);
     }
-    if (ok && a.live) {
-      const int tile = a.item.kt0 + a.j;
-      const int cur = a.id >= 0 && a.id < P.num_blocks ? a.id : 0;  // (the K producer flags it)
-      ++a.j;
-      if (a.j < a.item.nt) a.id = tile_id(P, a.item, tile + 1);
-      ok = load_tile(P, vmap, c.vfull, c.vempty, vbuf, kVStages, tv, a.item, tile, cur, abort_flag);
-      if (ok) ++tv;
-    }
-    if (kRuns == 2) change_places(a, b);
   }
-  if (!ok && !*abort_flag && lane == 0) raise_abort(c, P.err);
-  if (*abort_flag) drain_ring(c.vfull, kVStages, tv);
 }
 
 // ------------------------------------------------------------------ MMA warp
@@ -484,6 +484,7 @@ struct Issuer {
   bool issued;
 
   // O_w += P_w V of the tile numbered n; `first` begins O_w anew, `last` reports it.
+  // (P being there means that V is: the softmax waits for it and looks through it.)
   __device__ __forceinline__ bool pv(int w, uint32_t n, bool first, bool last) {
     constexpr uint32_t idesc = umma_idesc_bf16(128, 128, false, true);
     const uint64_t b = umma_smem_desc(v + (n % kVStages) * kTileBytes, kHalfBytes, 1024, kLayout128B);
@@ -535,6 +536,14 @@ struct Issuer {
     return true;
   }
 };
+
+// With two runs, a turn works on `a` and the two states change places after it.
+template <typename T>
+__device__ __forceinline__ void change_places(T& a, T& b) {
+  const T t = a;
+  a = b;
+  b = t;
+}
 
 template <int kRuns>
 __device__ void mma_warp(const Params& P, Ctl& c, uint8_t* qbuf, uint8_t* kbuf, uint8_t* vbuf, uint32_t tmem) {
@@ -614,7 +623,7 @@ __device__ void mma_warp(const Params& P, Ctl& c, uint8_t* qbuf, uint8_t* kbuf, 
 // ------------------------------------------------------------------ softmax warps
 // Bits s .. s + 63 of what a row sees, counted from its first drafted key (s < 0: context,
 // seen whole), without those past the draft.
-__device__ __forceinline__ uint64_t seen_bits(const uint64_t* row, int words, int q_len, int s) {
+__device__ __noinline__ uint64_t seen_bits(const uint64_t* row, int words, int q_len, int s) {
   if (s <= -64) return ~uint64_t(0);
   if (s >= q_len) return 0;
   uint64_t b;
@@ -641,28 +650,24 @@ __device__ __forceinline__ uint32_t finite2(uint32_t x) {
   return x;
 }
 
-// Takes what is not finite out of row r of a V tile (whole rows past the context), so that a
+// Takes what is not finite out of row r of a V tile (all of a row past the context), so that a
 // weight of 0 can stand for a key that a row does not see.  Returns whether it took something
 // out that a row may see.
 __device__ __forceinline__ bool clean_v_row(uint8_t* vtile, int r, bool past) {
   // starting each lane at chunk r mod 8 spreads eight lanes over all banks
   uint8_t* row = vtile + r * 128;
   bool wrote = past, spoilt = false;
-#pragma unroll 1  // (called with a score row in registers)
-  for (int ch = 0; ch < 8; ++ch) {
-    const int off = ((ch + r) & 7) * 16;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint4* at = reinterpret_cast<uint4*>(row + half * kHalfBytes + off);
-      if (past) {
-        *at = make_uint4(0, 0, 0, 0);
-        continue;
-      }
-      const uint4 x = *at;
-      if (not_finite2(x.x) | not_finite2(x.y) | not_finite2(x.z) | not_finite2(x.w)) {
-        *at = make_uint4(finite2(x.x), finite2(x.y), finite2(x.z), finite2(x.w));
-        wrote = spoilt = true;
-      }
+#pragma unroll 1
+  for (int ch = 0; ch < 16; ++ch) {
+    uint4* at = reinterpret_cast<uint4*>(row + (ch >> 3) * kHalfBytes + ((ch + r) & 7) * 16);
+    if (past) {
+      *at = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    const uint4 x = *at;
+    if (not_finite2(x.x) | not_finite2(x.y) | not_finite2(x.z) | not_finite2(x.w)) {
+      *at = make_uint4(finite2(x.x), finite2(x.y), finite2(x.z), finite2(x.w));
+      wrote = spoilt = true;
     }
   }
   if (wrote) fence_proxy_async_smem();
@@ -707,12 +712,8 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
   const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
   const uint32_t srow = tmem + lane_off + 128u * w, orow = tmem + lane_off + kOCol + 128u * w;
   volatile int* abort_flag = &c.abort_flag;
-  // Tiles of this stream so far, and their numbers in the rings: with two runs the tiles
-  // alternate as long as both last.
-  const uint32_t other = kRuns == 2 ? static_cast<uint32_t>(max(int64_t(0), c.run[w ^ 1].end - c.run[w ^ 1].begin)) : 0;
-  uint32_t tiles = 0;
-  auto number = [&](uint32_t t) -> uint32_t { return kRuns == 2 ? t + min(t + w, other) : t; };
-  uint32_t it = 0, tc = 0, oc = 0;
+  uint32_t tiles = 0;  // of this stream's run
+  uint32_t it = 0, tc = 0, oc = 0, before = 0;
   bool ok = true;
   const int row = r - P.row0[w];  // the row within the item's row tile (below 0: none)
   const int rj = row >> P.gp_log2, rg = r & (P.gp - 1);
@@ -736,7 +737,7 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
       continue;
     }
     const int ctx = item.ctx, q_len = item.q_len, kt0 = item.kt0;
-    // this stream is the last one to read the item's tiles, and looks after their V rows
+    // this stream is the last one to read the item's tiles, and looks through their V rows
     const bool releases = kRuns == 2 || w == 1 || item.nq[1] == 0, cleans = kRuns == 2 || w == 0;
     const bool live = rj >= 0 && rj < nq && rg < P.group;  // a real (node, head) row
     const bool warp_live = __any_sync(0xffffffffu, live);
@@ -744,7 +745,6 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
     float m_ref = -INFINITY, l_sum = 0.f;
 
     for (int j = 0; j < nt; ++j) {
-      const uint32_t n = number(tiles + j);
       const int k0 = (kt0 + j) * kTileKeys;
       const bool drafted = k0 + kTileKeys > ctx;  // the tile holds keys that not every row sees
       const bool masked = drafted || sign < 0.f;  // (a negative scale wants the minimum)
@@ -765,12 +765,14 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
       tc_fence_after();
       // S of this tile is complete, and with it every MMA issued before: K has been read, and
       // V of the tile before
+      const uint32_t n = c.number[k][tiles++ % 8];  // the tile's number in the rings
       if (r == 0 && releases) {
         mbar_arrive(&c.kempty[n % kKStages]);
-        if (j > 0) mbar_arrive(&c.vempty[number(tiles + j - 1) % kVStages]);
+        if (j > 0) mbar_arrive(&c.vempty[before % kVStages]);
       }
-      bool v_ok = true;
+      before = n;
       // Before the first half of P is handed over, V of this key tile has landed and is clean.
+      bool v_ok = true;
       auto first_half = [&]() {
         if (warp_live) tmem_st_wait();
         v_ok = wait_for(&c.vfull[n % kVStages], (n / kVStages) & 1, abort_flag);
@@ -829,8 +831,7 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
       break;
     }
     tc_fence_after();
-    if (r == 0 && releases) mbar_arrive(&c.vempty[number(tiles + nt - 1) % kVStages]);
-    tiles += nt;
+    if (r == 0 && releases) mbar_arrive(&c.vempty[before % kVStages]);
     const bool bad = c.bad[k][slot] != 0;
     const int part = item.slot;
     // where the row goes: the output, or its partial
@@ -922,7 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       mbar_init(&c.q_free[w], 1);
       for (int s = 0; s < kRing; ++s) {
         mbar_init(&c.item_full[w][s], 1);
-        mbar_init(&c.item_empty[w][s], kPairs ? 10 : 6);  // the MMA thread, the V producer and the softmax warps
+        mbar_init(&c.item_empty[w][s], kPairs ? 10 : 6);  // MMA thread, V producer, softmax warps
       }
       c.run[w].seq = 0;
       c.run[w].base = 0;
@@ -943,9 +944,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   grid_dep_wait();
   grid_dep_launch();
   find_runs<kRuns>(P, c);
-  if (warp == 0) k_producer_warp<kRuns>(P, &qmap, &kmap, c, qbuf, kbuf);
+  if (warp == 0 || warp == 10) producer_warp<kRuns>(P, warp == 0, &qmap, warp == 0 ? &kmap : &vmap, c, qbuf, warp == 0 ? kbuf : vbuf);
   else if (warp == 1) mma_warp<kRuns>(P, c, qbuf, kbuf, vbuf, tmem);
-  else if (warp == 10) v_producer_warp<kRuns>(P, &vmap, c, vbuf);
+
   else softmax_warps<kRuns>(P, c, vbuf, tmem);
   tc_fence_before();
   __syncthreads();
@@ -1073,13 +1074,16 @@ int launch_tree_tc(const TreeArgs& t, void* workspace, int num_sms, uint32_t* er
   if (st) return st;
   const bool pairs = a.max_query_len > p.rows_q;
   p.unit_q = pairs ? 2 * p.rows_q : p.rows_q;
-  p.min_run = pairs ? 2 : 1;
+  p.unit_q_log2 = 7 - p.gp_log2 + (pairs ? 1 : 0);
   // CTAs: one per SM, fewer where the caller's bounds leave less to do
   const int runs_per_cta = pairs ? 1 : 2;
   const int64_t units = static_cast<int64_t>((a.max_query_len + p.unit_q - 1) / p.unit_q) * hkv;
   const int64_t tiles = units * ((static_cast<int64_t>(a.max_seq_len) + kTileKeys - 1) / kTileKeys);
   const int64_t most = tiles >= 2 * num_sms ? 2 * num_sms : tiles * a.num_seqs;
-  const int ctas = static_cast<int>(most < 2 * num_sms ? (most + 1) / 2 : num_sms);
+  const int min_tiles = pairs ? 2 : 1;
+  const int ctas = static_cast<int>(most < min_tiles * num_sms ? (most + min_tiles - 1) / min_tiles : num_sms);
+  p.unit_cost = most < 2 * num_sms ? 0 : 1;
+  p.min_run = min_tiles + p.unit_cost;
   const Layout l = layout_of(group, a.max_query_len, num_sms);
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.v_cache = static_cast<const __nv_bfloat16*>(a.v_cache);
