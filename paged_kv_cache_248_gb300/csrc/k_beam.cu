@@ -6,20 +6,20 @@
 // its running maximum and sum (the log-sum-exp) and its num_select best logits at once;
 // only their few candidates meet the log-sum-exp, and each other, afterwards.
 //
-// scan_kernel.  A CTA reads a piece of one row, in chunks of 32 values a thread that stay in
-// registers: each value is loaded once, feeds the thread's running sum of exponents
-// (fp32, relative to the thread's running maximum), and is compared with the block's
-// threshold, the num_select-th best value met so far.  Candidates carry a 64-bit key, the
-// value in an order-preserving form above the complement of its index, so that all keys
-// differ and equal values rank by their index.  The first threshold comes from the threads'
-// maxima of the first chunk (the num_select-th best of 256 of them: at least that many values
-// are as good, and only the threads with a maximum above it hold any better one), so that a
-// few hundred candidates at most are ever collected from ordinary logits; when the buffer
-// is full all the same (equal or rising values) it is cut down to its num_select best, the
-// threshold rises, and the rest of the chunk is looked at again.
+// scan_kernel.  A CTA reads a piece of one row in chunks of 32 values a thread, which stay in
+// registers while the next chunk's are on their way: each value is loaded once, feeds the
+// thread's running sum of exponents (fp32, relative to the thread's running maximum), and is
+// compared with a threshold.  The threshold comes from the threads' maxima of each chunk: if
+// every one of the 8 warps has ceil(num_select / 8) threads whose maximum reaches t, then t is
+// no better than the num_select-th best value, and nothing below it can be selected.  That
+// costs a few warp reductions and lets a few dozen candidates through.  A candidate's 64-bit key
+// is its value in an order-preserving form above the complement of its index, so that all keys
+// differ and equal values rank by their index.  When the buffer is full all the same (equal or
+// rising values) it is cut to its num_select best, the threshold becomes the last of them, and
+// the rest of the chunk is looked at again.
 //
-// select_kernel.  One CTA per request joins the pieces: the log-sum-exp of each beam in 64
-// bits, then the same collection over the pieces' candidates, ranked by their 64-bit score.
+// select_kernel.  One CTA per request joins the pieces: the log-sum-exp of each beam, joined in
+// 64 bits, then the same collection over the pieces' candidates, ranked by 64-bit scores.
 //
 // Bound: reading the logits once (HBM); for one request, two launches and their latency.
 #include "pkv_internal.cuh"
@@ -28,17 +28,16 @@
 namespace pkv {
 namespace {
 
-constexpr int kScanThreads = 256;
-constexpr int kChunkVals = 32;                          // values of a chunk per thread
-constexpr int kChunk = kScanThreads * kChunkVals;       // values of a chunk
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kChunkVals = 32;                    // values of a chunk per thread
+constexpr int kChunk = kThreads * kChunkVals;     // values of a chunk
 constexpr int kMaxSelect = 64;
 constexpr int kMaxBeams = 64;
-constexpr int kScanCap = 1536;                          // candidates collected between cuts
-constexpr int kPushMost = 4;                            // pushed per thread between barriers
-constexpr int kSelThreads = 512;
-constexpr int kSelCap = 2048;
+constexpr int kCap = 1536;                        // candidates collected between cuts
+constexpr int kPushMost = 4;                      // pushed per thread between barriers
 constexpr float kLog2e = 1.4426950408889634f;
-static_assert(kScanCap >= kScanThreads * kPushMost + kMaxSelect, "a cut buffer takes one round of pushes");
+static_assert(kCap >= kThreads * kPushMost + kMaxSelect, "a cut buffer takes one round of pushes");
 
 // Order-preserving 32-bit form of a float (no NaN; -0 first becomes +0), larger is larger.
 __device__ __forceinline__ uint32_t ordered_bits(float x) {
@@ -69,41 +68,155 @@ struct ScanParams {
   int32_t vocab, select, pieces, chunks_per_piece;
 };
 
-// Cuts the `n` collected keys to the `k` best, best first in place (n >= 1).  All threads
-// call it, with everything pushed; returns the new count.
-template <int kThreads, int kCap>
-__device__ int cut_keys(uint64_t* buf, int n, int k) {
-  constexpr int kPer = (kCap + kThreads - 1) / kThreads;
-  uint64_t mine[kPer];
+// A value that at least `need` threads of this warp reach (0: none), from their own.
+__device__ __forceinline__ uint32_t reached_by(uint32_t mine, int need) {
+  uint32_t top = 0;
+#pragma unroll 1
+  for (int i = 0; i < need; ++i) {
+    top = __reduce_max_sync(0xffffffffu, mine);
+    const uint32_t who = __ballot_sync(0xffffffffu, mine == top);
+    if ((threadIdx.x & 31) == __ffs(who) - 1) mine = 0;
+  }
+  return top;
+}
+
+// A collected candidate: rank first by `hi`, then by `lo` (both larger is better).
+struct Cand {
+  uint64_t hi;
+  uint32_t lo;
+};
+__device__ __forceinline__ bool better(const Cand& a, const Cand& b) {
+  return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo);
+}
+__device__ __forceinline__ bool better(uint64_t a, uint64_t b) { return a > b; }
+
+// Collected candidates in shared memory: 64-bit keys, or keys with a 32-bit tie-break.
+struct Keys {
+  uint64_t hi[kCap];
+  __device__ __forceinline__ uint64_t get(int i) const { return hi[i]; }
+  __device__ __forceinline__ void set(int i, uint64_t k) { hi[i] = k; }
+};
+struct Cands {
+  uint64_t hi[kCap];
+  uint32_t lo[kCap];
+  __device__ __forceinline__ Cand get(int i) const { return Cand{hi[i], lo[i]}; }
+  __device__ __forceinline__ void set(int i, const Cand& c) {
+    hi[i] = c.hi;
+    lo[i] = c.lo;
+  }
+};
+
+// Cuts the n collected candidates to the k best, best first (all threads, with everything
+// pushed); returns the new count.  Every candidate's rank is the number of better ones.
+template <typename T, typename Buf>
+__device__ int cut(Buf& buf, int n, int k) {
+  constexpr int kPer = kCap / kThreads;
+  T mine[kPer];
   int rank[kPer];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int i = threadIdx.x + j * kThreads;
-    mine[j] = i < n ? buf[i] : 0;
-    rank[j] = 0;
+    rank[j] = i < n ? 0 : kCap;
+    if (i < n) mine[j] = buf.get(i);
   }
-  for (int i = 0; i < n; ++i) {  // (a broadcast read)
-    const uint64_t o = buf[i];
+  if (n <= kThreads) {
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) rank[0] += better(buf.get(i), mine[0]) ? 1 : 0;
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const T o = buf.get(i);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) rank[j] += o > mine[j] ? 1 : 0;
+      for (int j = 0; j < kPer; ++j) rank[j] += better(o, mine[j]) ? 1 : 0;
+    }
   }
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int i = threadIdx.x + j * kThreads;
-    if (i < n && rank[j] < k) buf[rank[j]] = mine[j];
-  }
+  for (int j = 0; j < kPer; ++j)
+    if (rank[j] < k) buf.set(rank[j], mine[j]);
   __syncthreads();
   return min(n, k);
 }
 
+// A chunk's values of one thread, as they were loaded.
 template <typename T, bool kAligned>
-__global__ void __launch_bounds__(kScanThreads) scan_kernel(const ScanParams P) {
-  constexpr int kVec = 16 / static_cast<int>(sizeof(T));  // values of a 16-byte vector
-  constexpr int kVecs = kChunkVals / kVec;
-  __shared__ uint64_t buf[kScanCap];
+struct Chunk;
+template <bool kAligned>
+struct Chunk<float, kAligned> {
+  uint32_t w[kChunkVals];
+  __device__ __forceinline__ float value(int k) const { return __uint_as_float(w[k]); }
+};
+template <bool kAligned>
+struct Chunk<__nv_bfloat16, kAligned> {
+  uint32_t w[kChunkVals / 2];
+  __device__ __forceinline__ float value(int k) const {
+    return __uint_as_float(k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
+  }
+};
+
+// Index within the row of value k of the chunk that starts at `base`.
+template <typename T, bool kAligned>
+__device__ __forceinline__ int64_t index_of(int64_t base, int k) {
+  constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+  return kAligned ? base + (static_cast<int64_t>(k / kVec) * kThreads + threadIdx.x) * kVec + k % kVec
+                  : base + static_cast<int64_t>(k) * kThreads + threadIdx.x;
+}
+
+template <typename T, bool kAligned>
+__device__ __forceinline__ void load_chunk(Chunk<T, kAligned>& c, const T* x, int64_t base, int64_t end) {
+  constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+  constexpr int kWords = 4 / static_cast<int>(sizeof(T));  // values of a 32-bit word
+  constexpr uint32_t kNone = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;  // -inf
+  if (kAligned && base + kChunk <= end) {
+#pragma unroll
+    for (int v = 0; v < kChunkVals / kVec; ++v) {
+      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(x + index_of<T, kAligned>(base, v * kVec)));
+      c.w[4 * v] = w.x;
+      c.w[4 * v + 1] = w.y;
+      c.w[4 * v + 2] = w.z;
+      c.w[4 * v + 3] = w.w;
+    }
+  } else if (sizeof(T) == 4) {
+#pragma unroll
+    for (int k = 0; k < kChunkVals; ++k) {
+      const int64_t i = index_of<T, kAligned>(base, k);
+      c.w[k] = i < end ? __ldg(reinterpret_cast<const uint32_t*>(x) + i) : kNone;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kChunkVals; k += kWords) {
+      const int64_t i = index_of<T, kAligned>(base, k), j = index_of<T, kAligned>(base, k + 1);
+      const uint32_t lo = i < end ? __ldg(reinterpret_cast<const uint16_t*>(x) + i) : kNone & 0xffffu;
+      const uint32_t hi = j < end ? __ldg(reinterpret_cast<const uint16_t*>(x) + j) : kNone & 0xffffu;
+      c.w[k / kWords] = lo | hi << 16;
+    }
+  }
+}
+
+// The largest value (NaN does not count).
+template <typename T, bool kAligned>
+__device__ __forceinline__ float chunk_max(const Chunk<T, kAligned>& c) {
+  if (sizeof(T) == 4) {
+    float a = c.value(0), b = c.value(1);
+#pragma unroll
+    for (int k = 2; k < kChunkVals; k += 2) {
+      a = fmaxf(a, c.value(k));
+      b = fmaxf(b, c.value(k + 1));
+    }
+    return fmaxf(a, b);
+  }
+  __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&c.w[0]);
+#pragma unroll
+  for (int k = 1; k < kChunkVals / 2; ++k) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&c.w[k]));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+
+template <typename T, bool kAligned>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) scan_kernel(const ScanParams P) {
+  __shared__ Keys buf;
   __shared__ int s_count;
-  __shared__ float s_m[kScanThreads / 32], s_l[kScanThreads / 32];
+  __shared__ uint32_t s_reach[2][kWarps];
+  __shared__ float s_m[kWarps], s_l[kWarps];
   if (threadIdx.x == 0) s_count = 0;
   grid_dep_wait();
   grid_dep_launch();
@@ -111,39 +224,22 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(const ScanParams P) 
   const int piece = static_cast<int>(blockIdx.x % P.pieces);
   if (P.finished != nullptr && __ldg(P.finished + row) != 0) return;
   const T* x = static_cast<const T*>(P.logits) + row * P.row_stride;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int need = (P.select + kWarps - 1) / kWarps;
+  const int64_t end = P.vocab;
+  int64_t base = static_cast<int64_t>(piece) * P.chunks_per_piece * kChunk;
+  const int64_t stop = min(end, base + static_cast<int64_t>(P.chunks_per_piece) * kChunk);
   float m = -INFINITY, l = 0.f;
   uint64_t floor_key = 0;  // keys up to this one are out
-  // index within the row of value k of the chunk that starts at `base`
-  auto index_of = [&](int64_t base, int k) -> int64_t {
-    return kAligned ? base + (static_cast<int64_t>(k / kVec) * kScanThreads + threadIdx.x) * kVec + k % kVec
-                    : base + static_cast<int64_t>(k) * kScanThreads + threadIdx.x;
-  };
-  __syncthreads();
-  for (int ch = 0; ch < P.chunks_per_piece; ++ch) {
-    const int64_t base = (static_cast<int64_t>(piece) * P.chunks_per_piece + ch) * kChunk;
-    if (base >= P.vocab) break;
-    float val[kChunkVals];
-#pragma unroll
-    for (int v = 0; v < kVecs; ++v) {
-      const int64_t e0 = index_of(base, v * kVec);
-      if (kAligned && e0 + kVec <= P.vocab) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(x + e0));
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int e = 0; e < kVec; ++e)
-          val[v * kVec + e] = sizeof(T) == 4 ? __uint_as_float(u[e * 4 / kVec])
-                                             : __uint_as_float(e & 1 ? u[e * 4 / kVec] & 0xffff0000u : u[e * 4 / kVec] << 16);
-      } else {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          const int64_t i = index_of(base, v * kVec + e);
-          val[v * kVec + e] = i < P.vocab ? Elem<T>::to_f32(x[i]) : -INFINITY;
-        }
-      }
-    }
-    float top = val[0];
-#pragma unroll
-    for (int k = 1; k < kChunkVals; ++k) top = fmaxf(top, val[k]);
+  Chunk<T, kAligned> cur, next;
+  load_chunk<T, kAligned>(next, x, base, end);
+#pragma unroll 1
+  for (int turn = 0; base < stop; base += kChunk, turn ^= 1) {
+    cur = next;
+    if (base + kChunk < stop) load_chunk<T, kAligned>(next, x, base + kChunk, end);
+    const float top = chunk_max<T, kAligned>(cur);
+    const uint32_t reach = reached_by(top > -INFINITY ? ordered_bits(top) : 0, need);
+    if (lane == 0) s_reach[turn][warp] = reach;
     const float m_new = fmaxf(m, top);
     if (m_new != -INFINITY) {
       // x - m first: exact for values near the maximum, and whole for the type's lowest
@@ -151,97 +247,89 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(const ScanParams P) 
       float a0 = 0.f, a1 = 0.f;
 #pragma unroll
       for (int k = 0; k < kChunkVals; k += 2) {
-        a0 += ex2_approx((val[k] - m_new) * kLog2e);
-        a1 += ex2_approx((val[k + 1] - m_new) * kLog2e);
+        a0 += ex2_approx((cur.value(k) - m_new) * kLog2e);
+        a1 += ex2_approx((cur.value(k + 1) - m_new) * kLog2e);
       }
       l = l * ex2_approx((m - m_new) * kLog2e) + (a0 + a1);
       m = m_new;
     } else {
 #pragma unroll
-      for (int k = 0; k < kChunkVals; ++k) l += isnan(val[k]) ? val[k] : 0.f;
+      for (int k = 0; k < kChunkVals; ++k) l += isnan(cur.value(k)) ? cur.value(k) : 0.f;
+    }
+    __syncthreads();
+    // Values that 8 * need >= num_select threads reach: what is lower is out (keys with the
+    // value itself stay in).  A key of 0 is no threshold: not every warp has enough values.
+    uint32_t least = s_reach[turn][0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) least = min(least, s_reach[turn][w]);
+    if (least > 0) {
+      const uint64_t f = (static_cast<uint64_t>(least) << 32) - 1;
+      floor_key = f > floor_key ? f : floor_key;
     }
     auto key_of = [&](int k) -> uint64_t {
-      return (static_cast<uint64_t>(ordered_bits(val[k])) << 32) | (0xffffffffu - static_cast<uint32_t>(index_of(base, k)));
+      return (static_cast<uint64_t>(ordered_bits(cur.value(k))) << 32) |
+             (0xffffffffu - static_cast<uint32_t>(index_of<T, kAligned>(base, k)));
     };
-    if (floor_key == 0) {
-      // a threshold from the threads' maxima, ranked behind what is collected already (a
-      // cut leaves room for them); the values it lets pass are collected below
-      uint64_t best = 0;
-#pragma unroll
-      for (int k = 0; k < kChunkVals; ++k) {
-        const uint64_t key = val[k] > -INFINITY ? key_of(k) : 0;
-        best = key > best ? key : best;
-      }
-      const int had = s_count;
-      __syncthreads();
-      if (best != 0) buf[atomicAdd(&s_count, 1)] = best;
-      __syncthreads();
-      const int n = s_count - had;
-      __syncthreads();
-      if (threadIdx.x == 0) s_count = had;
-      if (n >= P.select) {
-        cut_keys<kScanThreads, kScanThreads>(buf + had, n, P.select);
-        floor_key = buf[had + P.select - 1] - 1;
-      }
-      __syncthreads();
-    }
-    // collect everything better than the threshold
     uint32_t pending = 0;
-    if (ordered_bits(top) >= static_cast<uint32_t>(floor_key >> 32) && top > -INFINITY) {
+    if (top > -INFINITY && ordered_bits(top) >= static_cast<uint32_t>(floor_key >> 32)) {
+      const float at_least = floor_key ? from_ordered_bits(static_cast<uint32_t>(floor_key >> 32)) : -INFINITY;
 #pragma unroll
       for (int k = 0; k < kChunkVals; ++k)
-        if (val[k] > -INFINITY && key_of(k) > floor_key) pending |= 1u << k;
+        if (cur.value(k) >= at_least && cur.value(k) > -INFINITY) pending |= 1u << k;
     }
     while (true) {
       int pushed = 0;
+      if (pending != 0) {
 #pragma unroll
-      for (int k = 0; k < kChunkVals; ++k) {
-        if ((pending >> k & 1u) && pushed < kPushMost) {
-          const uint64_t key = key_of(k);
-          if (key > floor_key) {
-            buf[atomicAdd(&s_count, 1)] = key;
-            ++pushed;
+        for (int k = 0; k < kChunkVals; ++k) {
+          if ((pending >> k & 1u) && pushed < kPushMost) {
+            const uint64_t key = key_of(k);
+            if (key > floor_key) {
+              buf.set(atomicAdd(&s_count, 1), key);
+              ++pushed;
+            }
+            pending &= ~(1u << k);
           }
-          pending &= ~(1u << k);
         }
       }
       const int more = __syncthreads_or(pending != 0);
       const int n = s_count;
-      __syncthreads();
-      if (n + kScanThreads * kPushMost > kScanCap) {
-        const int left = cut_keys<kScanThreads, kScanCap>(buf, n, P.select);
-        if (left == P.select) floor_key = buf[P.select - 1];
+      if (n + kThreads * kPushMost > kCap) {
+        __syncthreads();
+        const int left = cut<uint64_t>(buf, n, P.select);
+        if (left == P.select) floor_key = max(floor_key, buf.get(P.select - 1));
         if (threadIdx.x == 0) s_count = left;
         __syncthreads();
+      } else if (more) {
+        __syncthreads();  // (everyone has read the count)
       }
       if (!more) break;
     }
   }
   // the piece's candidates, best first
   const int n = s_count;
-  __syncthreads();
-  const int left = n > 0 ? cut_keys<kScanThreads, kScanCap>(buf, n, P.select) : 0;
+  const int left = n > 0 ? cut<uint64_t>(buf, n, P.select) : 0;
   uint64_t* out = P.keys + (row * P.pieces + piece) * P.select;
-  for (int k = threadIdx.x; k < P.select; k += kScanThreads) out[k] = k < left ? buf[k] : 0;
+  for (int k = threadIdx.x; k < P.select; k += kThreads) out[k] = k < left ? buf.get(k) : 0;
   // its maximum and sum
   float wm = m;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, d));
-  if ((threadIdx.x & 31) == 0) s_m[threadIdx.x >> 5] = wm;
+  if (lane == 0) s_m[warp] = wm;
   __syncthreads();
   float bm = s_m[0];
 #pragma unroll
-  for (int w = 1; w < kScanThreads / 32; ++w) bm = fmaxf(bm, s_m[w]);
+  for (int w = 1; w < kWarps; ++w) bm = fmaxf(bm, s_m[w]);
   // (a thread without values has l = 0, or NaN where it met nothing but that)
   float part = m == -INFINITY ? l : l * exp2f((m - bm) * kLog2e);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
-  if ((threadIdx.x & 31) == 0) s_l[threadIdx.x >> 5] = part;
+  if (lane == 0) s_l[warp] = part;
   __syncthreads();
   if (threadIdx.x == 0) {
     float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kScanThreads / 32; ++w) sum += s_l[w];
+    for (int w = 0; w < kWarps; ++w) sum += s_l[w];
     P.ml[(row * P.pieces + piece) * 2] = bm;
     P.ml[(row * P.pieces + piece) * 2 + 1] = sum;
   }
@@ -258,116 +346,108 @@ struct SelParams {
   int32_t beams, vocab, select, pieces, eos;
 };
 
-// A scored candidate: the score in its order-preserving form, then the complement of
-// beam * vocab + token.
-struct Cand {
-  uint64_t score;
-  uint32_t tie;
-};
-__device__ __forceinline__ bool better(const Cand& a, const Cand& b) {
-  return a.score > b.score || (a.score == b.score && a.tie > b.tie);
-}
-
-// Like cut_keys, for scored candidates.
-__device__ int cut_cands(uint64_t* score, uint32_t* tie, int n, int k) {
-  constexpr int kPer = (kSelCap + kSelThreads - 1) / kSelThreads;
-  Cand mine[kPer];
-  int rank[kPer];
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int i = threadIdx.x + j * kSelThreads;
-    mine[j] = i < n ? Cand{score[i], tie[i]} : Cand{~uint64_t(0), ~0u};
-    rank[j] = 0;
-  }
-  for (int i = 0; i < n; ++i) {
-    const Cand o{score[i], tie[i]};
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) rank[j] += better(o, mine[j]) ? 1 : 0;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int i = threadIdx.x + j * kSelThreads;
-    if (i < n && rank[j] < k) {
-      score[rank[j]] = mine[j].score;
-      tie[rank[j]] = mine[j].tie;
-    }
-  }
-  __syncthreads();
-  return min(n, k);
-}
-
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelParams P) {
+__global__ void __launch_bounds__(kThreads) select_kernel(const SelParams P) {
   __shared__ double s_lse[kMaxBeams], s_cum[kMaxBeams];
-  __shared__ uint64_t s_score[kSelCap];
-  __shared__ uint32_t s_tie[kSelCap];
+  __shared__ uint8_t s_done[kMaxBeams];
+  __shared__ Cands buf;
+  __shared__ uint32_t s_reach[kWarps];
   __shared__ int s_count;
+  const int64_t n = blockIdx.x;
+  const int W = P.beams, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) s_count = 0;
   grid_dep_wait();
   grid_dep_launch();
-  const int64_t n = blockIdx.x;
-  const int W = P.beams;
-  if (threadIdx.x == 0) s_count = 0;
-  if (threadIdx.x < W) {
-    const int64_t row = n * W + threadIdx.x;
-    const double cum = __ldg(P.cum + row);
-    s_cum[threadIdx.x] = cum;
-    if (P.finished == nullptr || __ldg(P.finished + row) == 0) {
-      const float* ml = P.ml + row * P.pieces * 2;
-      float m = -INFINITY;
-      for (int p = 0; p < P.pieces; ++p) m = fmaxf(m, __ldcg(ml + 2 * p));
-      double sum = 0.0;
-      for (int p = 0; p < P.pieces; ++p) {
+  // a warp per beam joins its pieces
+  for (int w = warp; w < W; w += kWarps) {
+    const int64_t row = n * W + w;
+    const bool done = P.finished != nullptr && __ldg(P.finished + row) != 0;
+    const float* ml = P.ml + row * P.pieces * 2;
+    float m = -INFINITY;
+    double sum = 0.0;
+    if (!done) {
+      for (int p = lane; p < P.pieces; p += 32) m = fmaxf(m, __ldcg(ml + 2 * p));
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      for (int p = lane; p < P.pieces; p += 32) {
         const float pm = __ldcg(ml + 2 * p), pl = __ldcg(ml + 2 * p + 1);
         // (a piece without values adds 0, or NaN where it met nothing but that)
-        sum += pm == -INFINITY ? static_cast<double>(pl) : pl * exp(static_cast<double>(pm) - m);
+        sum += pm == -INFINITY ? pl : pl * exp2f((pm - m) * kLog2e);
       }
-      s_lse[threadIdx.x] = m + log(sum);  // not finite: the beam has no candidates
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    }
+    if (lane == 0) {
+      s_cum[w] = __ldg(P.cum + row);
+      s_done[w] = done ? 1 : 0;
+      if (!done) s_lse[w] = m + log(sum);  // not finite: the beam has no candidates
     }
   }
   __syncthreads();
   const int per_beam = P.pieces * P.select;
   const int total = W * per_beam;
-  Cand floor_c{0, 0};  // ordered forms of finite scores are above 0
-  for (int base = 0; base < total; base += kSelThreads) {
-    const int i = base + threadIdx.x;
+  // Candidate i, or {0, 0} (ordered forms of finite scores are above 0).
+  auto cand = [&](int i) -> Cand {
     Cand c{0, 0};
-    if (i < total) {
-      const int w = i / per_beam;
-      if (P.finished != nullptr && __ldg(P.finished + n * W + w) != 0) {
-        if (i == w * per_beam && isfinite(s_cum[w]))
-          c = Cand{ordered_bits(s_cum[w]), 0xffffffffu - (static_cast<uint32_t>(w) * P.vocab + P.eos)};
-      } else {
-        const uint64_t key = __ldcg(P.keys + n * total + i);
-        const double lse = s_lse[w];
-        const double score = s_cum[w] + (static_cast<double>(from_ordered_bits(static_cast<uint32_t>(key >> 32))) - lse);
-        if (key != 0 && isfinite(lse) && isfinite(score))
-          c = Cand{ordered_bits(score),
-                   0xffffffffu - (static_cast<uint32_t>(w) * P.vocab + (0xffffffffu - static_cast<uint32_t>(key)))};
-      }
+    const int w = i / per_beam;
+    if (s_done[w]) {
+      if (i == w * per_beam && isfinite(s_cum[w]))
+        c = Cand{ordered_bits(s_cum[w]), 0xffffffffu - (static_cast<uint32_t>(w) * P.vocab + P.eos)};
+      return c;
     }
-    if (better(c, floor_c)) {
-      const int at = atomicAdd(&s_count, 1);
-      s_score[at] = c.score;
-      s_tie[at] = c.tie;
+    const uint64_t key = __ldcg(P.keys + n * total + i);
+    const double lse = s_lse[w];
+    const double score = s_cum[w] + (static_cast<double>(from_ordered_bits(static_cast<uint32_t>(key >> 32))) - lse);
+    if (key != 0 && isfinite(lse) && isfinite(score))
+      c = Cand{ordered_bits(score), 0xffffffffu - (static_cast<uint32_t>(w) * P.vocab + (0xffffffffu - static_cast<uint32_t>(key)))};
+    return c;
+  };
+  // a threshold on the upper half of the scores, as in the scan
+  uint32_t best = 0;
+  constexpr int kKeep = 4;  // candidates that a thread keeps in registers
+  Cand kept[kKeep];
+#pragma unroll
+  for (int j = 0; j < kKeep; ++j) {
+    const int i = threadIdx.x + j * kThreads;
+    kept[j] = i < total ? cand(i) : Cand{0, 0};
+    best = max(best, static_cast<uint32_t>(kept[j].hi >> 32));
+  }
+  for (int i = threadIdx.x + kKeep * kThreads; i < total; i += kThreads)
+    best = max(best, static_cast<uint32_t>(cand(i).hi >> 32));
+  const uint32_t reach = reached_by(best, (P.select + kWarps - 1) / kWarps);
+  if (lane == 0) s_reach[warp] = reach;
+  __syncthreads();
+  uint32_t least = s_reach[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) least = min(least, s_reach[w]);
+  Cand floor_c{least > 0 ? (static_cast<uint64_t>(least) << 32) - 1 : 0, 0xffffffffu};
+  for (int base = 0; base < total; base += kKeep * kThreads) {
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j) {
+      const int i = base + threadIdx.x + j * kThreads;
+      const Cand c = base == 0 ? kept[j] : (i < total ? cand(i) : Cand{0, 0});
+      if (better(c, floor_c)) buf.set(atomicAdd(&s_count, 1), c);
     }
     __syncthreads();
     const int cnt = s_count;
-    __syncthreads();
-    if (cnt + kSelThreads > kSelCap && base + kSelThreads < total) {
-      const int left = cut_cands(s_score, s_tie, cnt, P.select);
-      if (left == P.select) floor_c = Cand{s_score[left - 1], s_tie[left - 1]};
-      if (threadIdx.x == 0) s_count = left;
+    if (cnt + kKeep * kThreads > kCap && base + kKeep * kThreads < total) {
       __syncthreads();
+      const int left = cut<Cand>(buf, cnt, P.select);
+      if (left == P.select) {
+        const Cand last = buf.get(left - 1);
+        if (better(last, floor_c)) floor_c = last;
+      }
+      if (threadIdx.x == 0) s_count = left;
     }
+    __syncthreads();
   }
   const int cnt = s_count;
-  __syncthreads();
-  const int left = cnt > 0 ? cut_cands(s_score, s_tie, cnt, P.select) : 0;
-  for (int k = threadIdx.x; k < P.select; k += kSelThreads) {
+  const int left = cnt > 0 ? cut<Cand>(buf, cnt, P.select) : 0;
+  for (int k = threadIdx.x; k < P.select; k += kThreads) {
     const int64_t o = n * P.select + k;
     if (k < left) {
-      const uint32_t flat = 0xffffffffu - s_tie[k];
-      P.out_scores[o] = static_cast<float>(from_ordered_bits(s_score[k]));
+      const Cand c = buf.get(k);
+      const uint32_t flat = 0xffffffffu - c.lo;
+      P.out_scores[o] = static_cast<float>(from_ordered_bits(c.hi));
       P.out_parents[o] = static_cast<int32_t>(flat / static_cast<uint32_t>(P.vocab));
       P.out_tokens[o] = static_cast<int32_t>(flat % static_cast<uint32_t>(P.vocab));
     } else {
@@ -422,15 +502,15 @@ int launch_beam_select(const BeamArgs& a, void* workspace, int num_sms, cudaStre
   const bool aligned = (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0 && a.row_stride * elem % 16 == 0;
   cudaError_t e;
   if (a.dtype == PKV_F32)
-    e = aligned ? launch_k(scan_kernel<float, true>, grid, dim3(kScanThreads), 0, s, p)
-                : launch_k(scan_kernel<float, false>, grid, dim3(kScanThreads), 0, s, p);
+    e = aligned ? launch_k(scan_kernel<float, true>, grid, dim3(kThreads), 0, s, p)
+                : launch_k(scan_kernel<float, false>, grid, dim3(kThreads), 0, s, p);
   else
-    e = aligned ? launch_k(scan_kernel<__nv_bfloat16, true>, grid, dim3(kScanThreads), 0, s, p)
-                : launch_k(scan_kernel<__nv_bfloat16, false>, grid, dim3(kScanThreads), 0, s, p);
+    e = aligned ? launch_k(scan_kernel<__nv_bfloat16, true>, grid, dim3(kThreads), 0, s, p)
+                : launch_k(scan_kernel<__nv_bfloat16, false>, grid, dim3(kThreads), 0, s, p);
   if (e != cudaSuccess) return PKV_ERR_CUDA;
   SelParams q{p.keys, p.ml, a.cum, a.finished, a.out_scores, a.out_parents, a.out_tokens,
               a.beams, a.vocab, a.select, b.pieces, a.eos};
-  return cuda_status(launch_k(select_kernel, dim3(a.num_seqs), dim3(kSelThreads), 0, s, q));
+  return cuda_status(launch_k(select_kernel, dim3(a.num_seqs), dim3(kThreads), 0, s, q));
 }
 
 }  // namespace pkv
