@@ -35,9 +35,7 @@ constexpr int kChunk = kThreads * kChunkVals;     // values of a chunk
 constexpr int kMaxSelect = 64;
 constexpr int kMaxBeams = 64;
 constexpr int kCap = 1536;                        // candidates collected between cuts
-constexpr int kPushMost = 4;                      // pushed per thread between barriers
 constexpr float kLog2e = 1.4426950408889634f;
-static_assert(kCap >= kThreads * kPushMost + kMaxSelect, "a cut buffer takes one round of pushes");
 
 // Order-preserving 32-bit form of a float (no NaN; -0 first becomes +0), larger is larger.
 __device__ __forceinline__ uint32_t ordered_bits(float x) {
@@ -67,6 +65,31 @@ struct ScanParams {
   int64_t row_stride;
   int32_t vocab, select, pieces, chunks_per_piece;
 };
+
+constexpr uint32_t kOrderedNegInf = 0x007fffffu;  // ordered_bits(-inf)
+constexpr float kLowest = -3.402823466e38f;      // what a candidate has at least
+
+// (ya, yb) = ((xa, xb) + s) * log2(e) and (a0, a1) += (b0, b1), packed in fp32x2 instructions.
+__device__ __forceinline__ void scaled_diff2(float& ya, float& yb, float xa, float xb, float s) {
+  asm("{\n\t.reg .b64 x, t, c;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 t, {%4, %4};\n\t"
+      "mov.b64 c, {%5, %5};\n\t"
+      "add.rn.f32x2 x, x, t;\n\t"
+      "mul.rn.f32x2 x, x, c;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(ya), "=f"(yb)
+      : "f"(xa), "f"(xb), "f"(s), "f"(kLog2e));
+}
+__device__ __forceinline__ void fadd2(float& a0, float& a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%0, %1};\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "add.rn.f32x2 a, a, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
 
 // A value that at least `need` threads of this warp reach (0: none), from their own.
 __device__ __forceinline__ uint32_t reached_by(uint32_t mine, int need) {
@@ -212,10 +235,10 @@ __device__ __forceinline__ float chunk_max(const Chunk<T, kAligned>& c) {
 }
 
 template <typename T, bool kAligned>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) scan_kernel(const ScanParams P) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3) scan_kernel(const ScanParams P) {
   __shared__ Keys buf;
   __shared__ int s_count;
-  __shared__ uint32_t s_reach[2][kWarps];
+  __shared__ uint32_t s_reach[kWarps];
   __shared__ float s_m[kWarps], s_l[kWarps];
   if (threadIdx.x == 0) s_count = 0;
   grid_dep_wait();
@@ -231,15 +254,18 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) scan_kernel(
   const int64_t stop = min(end, base + static_cast<int64_t>(P.chunks_per_piece) * kChunk);
   float m = -INFINITY, l = 0.f;
   uint64_t floor_key = 0;  // keys up to this one are out
+  bool exact = false;      // it is the num_select-th best key of a cut
   Chunk<T, kAligned> cur, next;
   load_chunk<T, kAligned>(next, x, base, end);
 #pragma unroll 1
-  for (int turn = 0; base < stop; base += kChunk, turn ^= 1) {
+  for (; base < stop; base += kChunk) {
     cur = next;
     if (base + kChunk < stop) load_chunk<T, kAligned>(next, x, base + kChunk, end);
     const float top = chunk_max<T, kAligned>(cur);
-    const uint32_t reach = reached_by(top > -INFINITY ? ordered_bits(top) : 0, need);
-    if (lane == 0) s_reach[turn][warp] = reach;
+    if (floor_key == 0) {
+      const uint32_t reach = reached_by(top > -INFINITY ? ordered_bits(top) : 0, need);
+      if (lane == 0) s_reach[warp] = reach;
+    }
     const float m_new = fmaxf(m, top);
     if (m_new != -INFINITY) {
       // x - m first: exact for values near the maximum, and whole for the type's lowest
@@ -247,8 +273,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) scan_kernel(
       float a0 = 0.f, a1 = 0.f;
 #pragma unroll
       for (int k = 0; k < kChunkVals; k += 2) {
-        a0 += ex2_approx((cur.value(k) - m_new) * kLog2e);
-        a1 += ex2_approx((cur.value(k + 1) - m_new) * kLog2e);
+        float ya, yb;
+        scaled_diff2(ya, yb, cur.value(k), cur.value(k + 1), -m_new);
+        fadd2(a0, a1, ex2_approx(ya), ex2_approx(yb));
       }
       l = l * ex2_approx((m - m_new) * kLog2e) + (a0 + a1);
       m = m_new;
@@ -256,54 +283,53 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) scan_kernel(
 #pragma unroll
       for (int k = 0; k < kChunkVals; ++k) l += isnan(cur.value(k)) ? cur.value(k) : 0.f;
     }
-    __syncthreads();
-    // Values that 8 * need >= num_select threads reach: what is lower is out (keys with the
-    // value itself stay in).  A key of 0 is no threshold: not every warp has enough values.
-    uint32_t least = s_reach[turn][0];
+    if (floor_key == 0) {
+      __syncthreads();
+      // A value that 8 * need >= num_select threads reach: what is lower is out (keys with the
+      // value itself stay in).  0 is no threshold: not every warp has enough values.
+      uint32_t least = s_reach[0];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) least = min(least, s_reach[turn][w]);
-    if (least > 0) {
-      const uint64_t f = (static_cast<uint64_t>(least) << 32) - 1;
-      floor_key = f > floor_key ? f : floor_key;
+      for (int w = 1; w < kWarps; ++w) least = min(least, s_reach[w]);
+      if (least > 0) floor_key = (static_cast<uint64_t>(least) << 32) - 1;
+      exact = false;
     }
-    auto key_of = [&](int k) -> uint64_t {
-      return (static_cast<uint64_t>(ordered_bits(cur.value(k))) << 32) |
-             (0xffffffffu - static_cast<uint32_t>(index_of<T, kAligned>(base, k)));
-    };
-    uint32_t pending = 0;
+    uint32_t todo = 0;
     if (top > -INFINITY && ordered_bits(top) >= static_cast<uint32_t>(floor_key >> 32)) {
-      const float at_least = floor_key ? from_ordered_bits(static_cast<uint32_t>(floor_key >> 32)) : -INFINITY;
+      const float at_least =
+          floor_key >> 32 > kOrderedNegInf ? from_ordered_bits(static_cast<uint32_t>(floor_key >> 32)) : kLowest;
 #pragma unroll
-      for (int k = 0; k < kChunkVals; ++k)
-        if (cur.value(k) >= at_least && cur.value(k) > -INFINITY) pending |= 1u << k;
+      for (int k = 0; k < kChunkVals; ++k) todo |= cur.value(k) >= at_least ? 1u << k : 0u;
     }
     while (true) {
-      int pushed = 0;
-      if (pending != 0) {
-#pragma unroll
-        for (int k = 0; k < kChunkVals; ++k) {
-          if ((pending >> k & 1u) && pushed < kPushMost) {
-            const uint64_t key = key_of(k);
-            if (key > floor_key) {
-              buf.set(atomicAdd(&s_count, 1), key);
-              ++pushed;
-            }
-            pending &= ~(1u << k);
-          }
+      uint32_t again = 0;  // values that found no room
+      while (todo != 0) {  // few: each is read once more, so that no register is indexed
+        const int k = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int64_t i = index_of<T, kAligned>(base, k);
+        const uint64_t key = (static_cast<uint64_t>(ordered_bits(Elem<T>::to_f32(x[i]))) << 32) |
+                             (0xffffffffu - static_cast<uint32_t>(i));
+        if (key > floor_key) {
+          const int at = atomicAdd(&s_count, 1);
+          if (at < kCap) buf.set(at, key);
+          else again |= 1u << k;
         }
       }
-      const int more = __syncthreads_or(pending != 0);
-      const int n = s_count;
-      if (n + kThreads * kPushMost > kCap) {
+      const int more = __syncthreads_or(again != 0);
+      const int n = min(s_count, kCap);
+      // The first chunk's exact threshold is worth a cut (later chunks pass few values then),
+      // and so is a buffer that fills.
+      if (more || n >= (exact ? 512 : P.select)) {
         __syncthreads();
         const int left = cut<uint64_t>(buf, n, P.select);
-        if (left == P.select) floor_key = max(floor_key, buf.get(P.select - 1));
+        if (left == P.select) {
+          floor_key = max(floor_key, buf.get(P.select - 1));
+          exact = true;
+        }
         if (threadIdx.x == 0) s_count = left;
         __syncthreads();
-      } else if (more) {
-        __syncthreads();  // (everyone has read the count)
       }
       if (!more) break;
+      todo = again;
     }
   }
   // the piece's candidates, best first
@@ -350,7 +376,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelParams P) {
   __shared__ double s_lse[kMaxBeams], s_cum[kMaxBeams];
   __shared__ uint8_t s_done[kMaxBeams];
   __shared__ Cands buf;
-  __shared__ uint32_t s_reach[kWarps];
+  __shared__ __align__(16) uint32_t s_best[kThreads];
+  __shared__ uint32_t s_floor;
   __shared__ int s_count;
   const int64_t n = blockIdx.x;
   const int W = P.beams, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -383,25 +410,27 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelParams P) {
     }
   }
   __syncthreads();
-  const int per_beam = P.pieces * P.select;
-  const int total = W * per_beam;
-  // Candidate i, or {0, 0} (ordered forms of finite scores are above 0).
+  const int lists = W * P.pieces;
+  const int total = lists * P.select;
+  // Candidate i: entry i / lists of list i % lists, so that consecutive threads hold the best
+  // entries of all lists.  {0, 0}: none (ordered forms of finite scores are above 0).
   auto cand = [&](int i) -> Cand {
     Cand c{0, 0};
-    const int w = i / per_beam;
+    const int entry = i / lists, list = i - entry * lists, w = list / P.pieces;
     if (s_done[w]) {
-      if (i == w * per_beam && isfinite(s_cum[w]))
+      if (entry == 0 && list == w * P.pieces && isfinite(s_cum[w]))
         c = Cand{ordered_bits(s_cum[w]), 0xffffffffu - (static_cast<uint32_t>(w) * P.vocab + P.eos)};
       return c;
     }
-    const uint64_t key = __ldcg(P.keys + n * total + i);
+    const uint64_t key = __ldcg(P.keys + (n * lists + list) * P.select + entry);
     const double lse = s_lse[w];
     const double score = s_cum[w] + (static_cast<double>(from_ordered_bits(static_cast<uint32_t>(key >> 32))) - lse);
     if (key != 0 && isfinite(lse) && isfinite(score))
       c = Cand{ordered_bits(score), 0xffffffffu - (static_cast<uint32_t>(w) * P.vocab + (0xffffffffu - static_cast<uint32_t>(key)))};
     return c;
   };
-  // a threshold on the upper half of the scores, as in the scan
+  // A threshold on the upper half of the scores: the num_select-th largest of the threads'
+  // maxima (the threads take the lists' best entries first, see cand).
   uint32_t best = 0;
   constexpr int kKeep = 4;  // candidates that a thread keeps in registers
   Cand kept[kKeep];
@@ -411,15 +440,24 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelParams P) {
     kept[j] = i < total ? cand(i) : Cand{0, 0};
     best = max(best, static_cast<uint32_t>(kept[j].hi >> 32));
   }
-  for (int i = threadIdx.x + kKeep * kThreads; i < total; i += kThreads)
-    best = max(best, static_cast<uint32_t>(cand(i).hi >> 32));
-  const uint32_t reach = reached_by(best, (P.select + kWarps - 1) / kWarps);
-  if (lane == 0) s_reach[warp] = reach;
-  __syncthreads();
-  uint32_t least = s_reach[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) least = min(least, s_reach[w]);
-  Cand floor_c{least > 0 ? (static_cast<uint64_t>(least) << 32) - 1 : 0, 0xffffffffu};
+  Cand floor_c{0, 0xffffffffu};
+  if (total > kThreads) {
+    for (int i = threadIdx.x + kKeep * kThreads; i < total; i += kThreads)
+      best = max(best, static_cast<uint32_t>(cand(i).hi >> 32));
+    s_best[threadIdx.x] = best;
+    if (threadIdx.x == 0) s_floor = 0;
+    __syncthreads();
+    int rank = 0;  // threads with a larger maximum, or the same and a lower index
+#pragma unroll 4
+    for (int t = 0; t < kThreads; t += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(s_best + t);
+      rank += (o.x > best || (o.x == best && t < threadIdx.x)) + (o.y > best || (o.y == best && t + 1 < threadIdx.x)) +
+              (o.z > best || (o.z == best && t + 2 < threadIdx.x)) + (o.w > best || (o.w == best && t + 3 < threadIdx.x));
+    }
+    if (rank == P.select - 1) s_floor = best;
+    __syncthreads();
+    if (s_floor > 0) floor_c.hi = (static_cast<uint64_t>(s_floor) << 32) - 1;
+  }
   for (int base = 0; base < total; base += kKeep * kThreads) {
 #pragma unroll
     for (int j = 0; j < kKeep; ++j) {
