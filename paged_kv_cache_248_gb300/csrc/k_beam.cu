@@ -32,7 +32,6 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kChunkVals = 32;                    // values of a chunk per thread
 constexpr int kChunk = kThreads * kChunkVals;     // values of a chunk
-constexpr int kMaxSelect = 64;
 constexpr int kMaxBeams = 64;
 constexpr int kCap = 1536;                        // candidates collected between cuts
 constexpr float kLog2e = 1.4426950408889634f;
@@ -130,9 +129,29 @@ struct Cands {
 };
 
 // Cuts the n collected candidates to the k best, best first (all threads, with everything
-// pushed); returns the new count.  Every candidate's rank is the number of better ones.
+// pushed); returns the new count.  Every candidate's rank is the number of better ones; few
+// candidates are each ranked by several threads, which share the comparisons.
 template <typename T, typename Buf>
-__device__ int cut(Buf& buf, int n, int k) {
+__device__ int cut(Buf& buf, int* ranks, int n, int k) {
+  if (n <= kThreads / 2) {
+    int width = 32;
+    while (width < n) width *= 2;
+    const int i = threadIdx.x & (width - 1), step = kThreads / width;
+    ranks[threadIdx.x] = 0;
+    __syncthreads();
+    T mine{};
+    if (i < n) {
+      mine = buf.get(i);
+      int rank = 0;
+#pragma unroll 4
+      for (int j = threadIdx.x / width; j < n; j += step) rank += better(buf.get(j), mine) ? 1 : 0;
+      if (rank > 0) atomicAdd(ranks + i, rank);
+    }
+    __syncthreads();
+    if (threadIdx.x < n && ranks[threadIdx.x] < k) buf.set(ranks[threadIdx.x], mine);  // (i = threadIdx.x)
+    __syncthreads();
+    return min(n, k);
+  }
   constexpr int kPer = kCap / kThreads;
   T mine[kPer];
   int rank[kPer];
@@ -142,16 +161,11 @@ __device__ int cut(Buf& buf, int n, int k) {
     rank[j] = i < n ? 0 : kCap;
     if (i < n) mine[j] = buf.get(i);
   }
-  if (n <= kThreads) {
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) rank[0] += better(buf.get(i), mine[0]) ? 1 : 0;
-  } else {
 #pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-      const T o = buf.get(i);
+  for (int i = 0; i < n; ++i) {
+    const T o = buf.get(i);
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) rank[j] += better(o, mine[j]) ? 1 : 0;
-    }
+    for (int j = 0; j < kPer; ++j) rank[j] += better(o, mine[j]) ? 1 : 0;
   }
   __syncthreads();
 #pragma unroll
@@ -237,7 +251,7 @@ __device__ __forceinline__ float chunk_max(const Chunk<T, kAligned>& c) {
 template <typename T, bool kAligned>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3) scan_kernel(const ScanParams P) {
   __shared__ Keys buf;
-  __shared__ int s_count;
+  __shared__ int s_count, s_rank[kThreads];
   __shared__ uint32_t s_reach[kWarps];
   __shared__ float s_m[kWarps], s_l[kWarps];
   if (threadIdx.x == 0) s_count = 0;
@@ -320,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3) scan_kernel(
       // and so is a buffer that fills.
       if (more || n >= (exact ? 512 : P.select)) {
         __syncthreads();
-        const int left = cut<uint64_t>(buf, n, P.select);
+        const int left = cut<uint64_t>(buf, s_rank, n, P.select);
         if (left == P.select) {
           floor_key = max(floor_key, buf.get(P.select - 1));
           exact = true;
@@ -334,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3) scan_kernel(
   }
   // the piece's candidates, best first
   const int n = s_count;
-  const int left = n > 0 ? cut<uint64_t>(buf, n, P.select) : 0;
+  const int left = n > 0 ? cut<uint64_t>(buf, s_rank, n, P.select) : 0;
   uint64_t* out = P.keys + (row * P.pieces + piece) * P.select;
   for (int k = threadIdx.x; k < P.select; k += kThreads) out[k] = k < left ? buf.get(k) : 0;
   // its maximum and sum
@@ -378,7 +392,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelParams P) {
   __shared__ Cands buf;
   __shared__ __align__(16) uint32_t s_best[kThreads];
   __shared__ uint32_t s_floor;
-  __shared__ int s_count;
+  __shared__ int s_count, s_rank[kThreads];
   const int64_t n = blockIdx.x;
   const int W = P.beams, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) s_count = 0;
@@ -457,6 +471,15 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelParams P) {
     if (rank == P.select - 1) s_floor = best;
     __syncthreads();
     if (s_floor > 0) floor_c.hi = (static_cast<uint64_t>(s_floor) << 32) - 1;
+  } else if (P.select <= 32) {
+    // few candidates: the num_select-th largest of any warp's will do, and the first warps,
+    // which hold the lists' best entries, come close
+    if (threadIdx.x == 0) s_floor = 0;
+    __syncthreads();
+    const uint32_t reach = reached_by(best, P.select);
+    if (lane == 0 && reach > 0) atomicMax(&s_floor, reach);
+    __syncthreads();
+    if (s_floor > 0) floor_c.hi = (static_cast<uint64_t>(s_floor) << 32) - 1;
   }
   for (int base = 0; base < total; base += kKeep * kThreads) {
 #pragma unroll
@@ -469,7 +492,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelParams P) {
     const int cnt = s_count;
     if (cnt + kKeep * kThreads > kCap && base + kKeep * kThreads < total) {
       __syncthreads();
-      const int left = cut<Cand>(buf, cnt, P.select);
+      const int left = cut<Cand>(buf, s_rank, cnt, P.select);
       if (left == P.select) {
         const Cand last = buf.get(left - 1);
         if (better(last, floor_c)) floor_c = last;
@@ -479,7 +502,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelParams P) {
     __syncthreads();
   }
   const int cnt = s_count;
-  const int left = cnt > 0 ? cut<Cand>(buf, cnt, P.select) : 0;
+  const int left = cnt > 0 ? cut<Cand>(buf, s_rank, cnt, P.select) : 0;
   for (int k = threadIdx.x; k < P.select; k += kThreads) {
     const int64_t o = n * P.select + k;
     if (k < left) {
