@@ -6,10 +6,10 @@
 // its running maximum and sum (the log-sum-exp) and its num_select best logits at once;
 // only their few candidates meet the log-sum-exp, and each other, afterwards.
 //
-// scan_kernel.  A CTA reads a piece of one row in chunks of 32 values a thread, which stay in
-// registers while the next chunk's are on their way: each value is loaded once, feeds the
-// thread's running sum of exponents (fp32, relative to the thread's running maximum), and is
-// compared with a threshold.  The threshold comes from the threads' maxima of each chunk: if
+// scan_kernel.  A CTA reads a run of the rows in chunks of 64 bytes a thread, which stay in
+// registers while the next chunk's are on their way: each value is loaded once, feeds its
+// warp's sum of exponents (fp32, relative to the warp's maximum of the chunk), and is compared
+// with a threshold.  The threshold comes from the threads' maxima of each chunk: if
 // every one of the 8 warps has ceil(num_select / 8) threads whose maximum reaches t, then t is
 // no better than the num_select-th best value, and nothing below it can be selected.  That
 // costs a few warp reductions and lets a few dozen candidates through.  A candidate's 64-bit key
@@ -24,14 +24,15 @@
 // Bound: reading the logits once (HBM); for one request, two launches and their latency.
 #include "pkv_internal.cuh"
 #include "ptx.cuh"
+#include "softmax_row.cuh"
 
 namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kChunkVals = 32;                    // values of a chunk per thread
-constexpr int kChunk = kThreads * kChunkVals;     // values of a chunk
+constexpr int kVals = 32;                         // values of a chunk per thread
+constexpr int kChunk = kThreads * kVals;          // values of a chunk
 constexpr int kMaxBeams = 64;
 constexpr int kCap = 1536;                        // candidates collected between cuts
 constexpr float kLog2e = 1.4426950408889634f;
@@ -60,35 +61,15 @@ struct ScanParams {
   const void* logits;
   const uint8_t* finished;
   uint64_t* keys;    // [rows][pieces][select], best first, 0: none
-  float* ml;         // [rows][pieces][2]: maximum, sum of exp(x - maximum)
+  float* ml;         // [rows][row_chunks][kWarps][2]: maximum, sum of exp(x - maximum) of a warp's values
   int64_t row_stride;
-  int32_t vocab, select, pieces, chunks_per_piece;
+  int32_t vocab, select, pieces;
+  int32_t row_chunks, run;  // chunks of a row; chunks of a CTA's run (the last run may be shorter)
+  int64_t chunks;           // of all rows
 };
 
 constexpr uint32_t kOrderedNegInf = 0x007fffffu;  // ordered_bits(-inf)
 constexpr float kLowest = -3.402823466e38f;      // what a candidate has at least
-
-// (ya, yb) = ((xa, xb) + s) * log2(e) and (a0, a1) += (b0, b1), packed in fp32x2 instructions.
-__device__ __forceinline__ void scaled_diff2(float& ya, float& yb, float xa, float xb, float s) {
-  asm("{\n\t.reg .b64 x, t, c;\n\t"
-      "mov.b64 x, {%2, %3};\n\t"
-      "mov.b64 t, {%4, %4};\n\t"
-      "mov.b64 c, {%5, %5};\n\t"
-      "add.rn.f32x2 x, x, t;\n\t"
-      "mul.rn.f32x2 x, x, c;\n\t"
-      "mov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(ya), "=f"(yb)
-      : "f"(xa), "f"(xb), "f"(s), "f"(kLog2e));
-}
-__device__ __forceinline__ void fadd2(float& a0, float& a1, float b0, float b1) {
-  asm("{\n\t.reg .b64 a, b;\n\t"
-      "mov.b64 a, {%0, %1};\n\t"
-      "mov.b64 b, {%2, %3};\n\t"
-      "add.rn.f32x2 a, a, b;\n\t"
-      "mov.b64 {%0, %1}, a;\n\t}"
-      : "+f"(a0), "+f"(a1)
-      : "f"(b0), "f"(b1));
-}
 
 // A value that at least `need` threads of this warp reach (0: none), from their own.
 __device__ __forceinline__ uint32_t reached_by(uint32_t mine, int need) {
@@ -180,12 +161,12 @@ template <typename T, bool kAligned>
 struct Chunk;
 template <bool kAligned>
 struct Chunk<float, kAligned> {
-  uint32_t w[kChunkVals];
+  uint32_t w[kVals];
   __device__ __forceinline__ float value(int k) const { return __uint_as_float(w[k]); }
 };
 template <bool kAligned>
 struct Chunk<__nv_bfloat16, kAligned> {
-  uint32_t w[kChunkVals / 2];
+  uint32_t w[kVals / 2];
   __device__ __forceinline__ float value(int k) const {
     return __uint_as_float(k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
   }
@@ -206,8 +187,8 @@ __device__ __forceinline__ void load_chunk(Chunk<T, kAligned>& c, const T* x, in
   constexpr uint32_t kNone = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;  // -inf
   if (kAligned && base + kChunk <= end) {
 #pragma unroll
-    for (int v = 0; v < kChunkVals / kVec; ++v) {
-      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(x + index_of<T, kAligned>(base, v * kVec)));
+    for (int v = 0; v < kVals / kVec; ++v) {
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(x + index_of<T, kAligned>(base, v * kVec)));
       c.w[4 * v] = w.x;
       c.w[4 * v + 1] = w.y;
       c.w[4 * v + 2] = w.z;
@@ -215,13 +196,13 @@ __device__ __forceinline__ void load_chunk(Chunk<T, kAligned>& c, const T* x, in
     }
   } else if (sizeof(T) == 4) {
 #pragma unroll
-    for (int k = 0; k < kChunkVals; ++k) {
+    for (int k = 0; k < kVals; ++k) {
       const int64_t i = index_of<T, kAligned>(base, k);
       c.w[k] = i < end ? __ldg(reinterpret_cast<const uint32_t*>(x) + i) : kNone;
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < kChunkVals; k += kWords) {
+    for (int k = 0; k < kVals; k += kWords) {
       const int64_t i = index_of<T, kAligned>(base, k), j = index_of<T, kAligned>(base, k + 1);
       const uint32_t lo = i < end ? __ldg(reinterpret_cast<const uint16_t*>(x) + i) : kNone & 0xffffu;
       const uint32_t hi = j < end ? __ldg(reinterpret_cast<const uint16_t*>(x) + j) : kNone & 0xffffu;
@@ -230,73 +211,113 @@ __device__ __forceinline__ void load_chunk(Chunk<T, kAligned>& c, const T* x, in
   }
 }
 
-// The largest value (NaN does not count).
+// The largest value, and that of each quarter (NaN does not count).
 template <typename T, bool kAligned>
-__device__ __forceinline__ float chunk_max(const Chunk<T, kAligned>& c) {
-  if (sizeof(T) == 4) {
-    float a = c.value(0), b = c.value(1);
+__device__ __forceinline__ float chunk_max(const Chunk<T, kAligned>& c, float (&tops)[4]) {
 #pragma unroll
-    for (int k = 2; k < kChunkVals; k += 2) {
-      a = fmaxf(a, c.value(k));
-      b = fmaxf(b, c.value(k + 1));
+  for (int g = 0; g < 4; ++g) {
+    if (sizeof(T) == 4) {
+      float a = c.value(8 * g), b = c.value(8 * g + 1);
+#pragma unroll
+      for (int k = 2; k < 8; k += 2) {
+        a = fmaxf(a, c.value(8 * g + k));
+        b = fmaxf(b, c.value(8 * g + k + 1));
+      }
+      tops[g] = fmaxf(a, b);
+    } else {
+      auto pair = [&](int k) { return *reinterpret_cast<const __nv_bfloat162*>(&c.w[4 * g + k]); };
+      const __nv_bfloat162 m = __hmax2(__hmax2(pair(0), pair(1)), __hmax2(pair(2), pair(3)));
+      tops[g] = fmaxf(__low2float(m), __high2float(m));
     }
-    return fmaxf(a, b);
   }
-  __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&c.w[0]);
-#pragma unroll
-  for (int k = 1; k < kChunkVals / 2; ++k) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&c.w[k]));
-  return fmaxf(__low2float(m), __high2float(m));
+  return fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
 }
 
 template <typename T, bool kAligned>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3) scan_kernel(const ScanParams P) {
+__global__ void __launch_bounds__(kThreads, 3) scan_kernel(const ScanParams P) {
   __shared__ Keys buf;
   __shared__ int s_count, s_rank[kThreads];
   __shared__ uint32_t s_reach[kWarps];
-  __shared__ float s_m[kWarps], s_l[kWarps];
-  if (threadIdx.x == 0) s_count = 0;
   grid_dep_wait();
   grid_dep_launch();
-  const int64_t row = blockIdx.x / P.pieces;
-  const int piece = static_cast<int>(blockIdx.x % P.pieces);
-  if (P.finished != nullptr && __ldg(P.finished + row) != 0) return;
-  const T* x = static_cast<const T*>(P.logits) + row * P.row_stride;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int need = (P.select + kWarps - 1) / kWarps;
   const int64_t end = P.vocab;
-  int64_t base = static_cast<int64_t>(piece) * P.chunks_per_piece * kChunk;
-  const int64_t stop = min(end, base + static_cast<int64_t>(P.chunks_per_piece) * kChunk);
-  float m = -INFINITY, l = 0.f;
+  int64_t at_chunk = static_cast<int64_t>(blockIdx.x) * P.run;
+  const int64_t last_chunk = min(at_chunk + P.run, P.chunks);
+  // the run's part of one row after the other
+#pragma unroll 1
+  while (at_chunk < last_chunk) {
+  const int64_t row = at_chunk / P.row_chunks;
+  const int first = static_cast<int>(at_chunk - row * P.row_chunks);
+  const int count = static_cast<int>(min(static_cast<int64_t>(P.row_chunks - first), last_chunk - at_chunk));
+  at_chunk += count;
+  // this part's number among the row's parts; the row's last part marks the numbers after it
+  const int piece = static_cast<int>(blockIdx.x - row * P.row_chunks / P.run);
+  const int pieces_here = first + count == P.row_chunks ? P.pieces - piece : 1;
+  if (P.finished != nullptr && __ldg(P.finished + row) != 0) continue;
+  const T* x = static_cast<const T*>(P.logits) + row * P.row_stride;
+  int64_t base = static_cast<int64_t>(first) * kChunk;
+  const int64_t stop = min(end, base + static_cast<int64_t>(count) * kChunk);
+  if (threadIdx.x == 0) s_count = 0;
+  __syncthreads();
+  float2* ml = reinterpret_cast<float2*>(P.ml) + (row * P.row_chunks + first) * kWarps + warp;
   uint64_t floor_key = 0;  // keys up to this one are out
   bool exact = false;      // it is the num_select-th best key of a cut
+  // (a 32-bit chunk takes as many registers as two 16-bit ones: it is not loaded ahead)
+  constexpr bool kAhead = sizeof(T) == 2;
   Chunk<T, kAligned> cur, next;
-  load_chunk<T, kAligned>(next, x, base, end);
+  if (kAhead) load_chunk<T, kAligned>(next, x, base, end);
 #pragma unroll 1
   for (; base < stop; base += kChunk) {
-    cur = next;
-    if (base + kChunk < stop) load_chunk<T, kAligned>(next, x, base + kChunk, end);
-    const float top = chunk_max<T, kAligned>(cur);
+    if (kAhead) {
+      cur = next;
+      if (base + kChunk < stop) load_chunk<T, kAligned>(next, x, base + kChunk, end);
+    } else {
+      load_chunk<T, kAligned>(cur, x, base, end);
+    }
+    float tops[4];  // of the chunk's four vectors (quarters)
+    const float top = chunk_max<T, kAligned>(cur, tops);
     if (floor_key == 0) {
       const uint32_t reach = reached_by(top > -INFINITY ? ordered_bits(top) : 0, need);
       if (lane == 0) s_reach[warp] = reach;
     }
-    const float m_new = fmaxf(m, top);
-    if (m_new != -INFINITY) {
-      // x - m first: exact for values near the maximum, and whole for the type's lowest
-      // value, which times log2(e) would not be (a NaN is no maximum, but makes the sum NaN)
-      float a0 = 0.f, a1 = 0.f;
+    // The warp's maximum and sum, each chunk's and warp's for itself: rows are cut at different
+    // places, and equal rows are to have equal sums all the same, so that their ties stay ties.
+    // 2^(x c - r) with r = m c rounded; what the rounding left, m c - r, is put right in the sum,
+    // and values near the maximum have exponents near 0, where they are exact.  (A NaN is no
+    // maximum, but makes the sum NaN.)
+    const uint32_t warp_top = __reduce_max_sync(0xffffffffu, top > -INFINITY ? ordered_bits(top) : 0);
+    const float m = warp_top ? from_ordered_bits(warp_top) : -INFINITY;
+    float a0 = 0.f, a1 = 0.f;
+    if (fabsf(m) < 1e30f) {
+      const float r = m * kLog2e;
 #pragma unroll
-      for (int k = 0; k < kChunkVals; k += 2) {
+      for (int k = 0; k < kVals; k += 2) {
         float ya, yb;
-        scaled_diff2(ya, yb, cur.value(k), cur.value(k + 1), -m_new);
+        ffma2(ya, yb, cur.value(k), cur.value(k + 1), kLog2e, -r);
         fadd2(a0, a1, ex2_approx(ya), ex2_approx(yb));
       }
-      l = l * ex2_approx((m - m_new) * kLog2e) + (a0 + a1);
-      m = m_new;
+      a0 *= exp2f(fmaf(-m, kLog2e, r));
+      a1 *= exp2f(fmaf(-m, kLog2e, r));
+    } else if (warp_top) {  // values that times log2(e) may not be finite (a type's lowest value)
+#pragma unroll 1
+      for (int k = 0; k < kVals; k += 8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int64_t i = index_of<T, kAligned>(base, k + e);
+          if (i < end) a0 += ex2_approx((Elem<T>::to_f32(x[i]) - m) * kLog2e);
+        }
+      }
     } else {
 #pragma unroll
-      for (int k = 0; k < kChunkVals; ++k) l += isnan(cur.value(k)) ? cur.value(k) : 0.f;
+      for (int k = 0; k < kVals; ++k) a0 += isnan(cur.value(k)) ? cur.value(k) : 0.f;
     }
+    float l = a0 + a1;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    if (lane == 0) *ml = make_float2(m, l);
+    ml += kWarps;
     if (floor_key == 0) {
       __syncthreads();
       // A value that 8 * need >= num_select threads reach: what is lower is out (keys with the
@@ -312,7 +333,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3) scan_kernel(
       const float at_least =
           floor_key >> 32 > kOrderedNegInf ? from_ordered_bits(static_cast<uint32_t>(floor_key >> 32)) : kLowest;
 #pragma unroll
-      for (int k = 0; k < kChunkVals; ++k) todo |= cur.value(k) >= at_least ? 1u << k : 0u;
+      for (int g = 0; g < 4; ++g) {
+        if (tops[g] >= at_least) {
+#pragma unroll
+          for (int k = 8 * g; k < 8 * g + 8; ++k) todo |= cur.value(k) >= at_least ? 1u << k : 0u;
+        }
+      }
     }
     while (true) {
       uint32_t again = 0;  // values that found no room
@@ -346,32 +372,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3) scan_kernel(
       todo = again;
     }
   }
-  // the piece's candidates, best first
+  // the part's candidates, best first
   const int n = s_count;
   const int left = n > 0 ? cut<uint64_t>(buf, s_rank, n, P.select) : 0;
   uint64_t* out = P.keys + (row * P.pieces + piece) * P.select;
-  for (int k = threadIdx.x; k < P.select; k += kThreads) out[k] = k < left ? buf.get(k) : 0;
-  // its maximum and sum
-  float wm = m;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, d));
-  if (lane == 0) s_m[warp] = wm;
-  __syncthreads();
-  float bm = s_m[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) bm = fmaxf(bm, s_m[w]);
-  // (a thread without values has l = 0, or NaN where it met nothing but that)
-  float part = m == -INFINITY ? l : l * exp2f((m - bm) * kLog2e);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
-  if (lane == 0) s_l[warp] = part;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += s_l[w];
-    P.ml[(row * P.pieces + piece) * 2] = bm;
-    P.ml[(row * P.pieces + piece) * 2 + 1] = sum;
+  for (int k = threadIdx.x; k < P.select * pieces_here; k += kThreads) out[k] = k < left ? buf.get(k) : 0;
   }
 }
 
@@ -383,7 +388,7 @@ struct SelParams {
   float* out_scores;
   int32_t* out_parents;
   int32_t* out_tokens;
-  int32_t beams, vocab, select, pieces, eos;
+  int32_t beams, vocab, select, pieces, sums, eos;  // sums: maxima and sums of a row
 };
 
 __global__ void __launch_bounds__(kThreads) select_kernel(const SelParams P) {
@@ -398,21 +403,21 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelParams P) {
   if (threadIdx.x == 0) s_count = 0;
   grid_dep_wait();
   grid_dep_launch();
-  // a warp per beam joins its pieces
+  // a warp per beam joins its sums
   for (int w = warp; w < W; w += kWarps) {
     const int64_t row = n * W + w;
     const bool done = P.finished != nullptr && __ldg(P.finished + row) != 0;
-    const float* ml = P.ml + row * P.pieces * 2;
+    const float2* ml = reinterpret_cast<const float2*>(P.ml) + row * P.sums;
     float m = -INFINITY;
     double sum = 0.0;
     if (!done) {
-      for (int p = lane; p < P.pieces; p += 32) m = fmaxf(m, __ldcg(ml + 2 * p));
+      for (int p = lane; p < P.sums; p += 32) m = fmaxf(m, __ldcg(ml + p).x);
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-      for (int p = lane; p < P.pieces; p += 32) {
-        const float pm = __ldcg(ml + 2 * p), pl = __ldcg(ml + 2 * p + 1);
-        // (a piece without values adds 0, or NaN where it met nothing but that)
-        sum += pm == -INFINITY ? pl : pl * exp2f((pm - m) * kLog2e);
+      for (int p = lane; p < P.sums; p += 32) {
+        const float2 pml = __ldcg(ml + p);
+        // (values of -inf alone add 0, or NaN where NaN was among them)
+        sum += pml.x == -INFINITY ? pml.y : pml.y * exp2f((pml.x - m) * kLog2e);
       }
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -520,23 +525,26 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelParams P) {
 }
 
 struct BeamPlan {
-  int pieces, chunks_per_piece;
+  int row_chunks, run, pieces, ctas;
+  int64_t chunks;
   size_t key_bytes, bytes;
 };
 
-// Rows are cut into pieces until every SM has a few CTAs: a piece is at least one chunk.
+// All rows' chunks, one after the other, are cut into equal runs for as many CTAs as the GPU holds at
+// once (kResident per SM); a row that lies in several runs has a part in each.
+constexpr int kResident = 3;
 BeamPlan beam_plan(int32_t num_seqs, int32_t beams, int32_t vocab, int32_t select, int num_sms) {
-  const int64_t rows = static_cast<int64_t>(num_seqs) * beams;
-  const int64_t chunks = (static_cast<int64_t>(vocab) + kChunk - 1) / kChunk;
-  int64_t pieces = (4LL * num_sms + rows - 1) / rows;
-  pieces = pieces < chunks ? (pieces < 1 ? 1 : pieces) : chunks;
-  const int64_t per = (chunks + pieces - 1) / pieces;
-  pieces = (chunks + per - 1) / per;
   BeamPlan b;
-  b.pieces = static_cast<int>(pieces);
-  b.chunks_per_piece = static_cast<int>(per);
-  b.key_bytes = (static_cast<size_t>(rows) * pieces * select * sizeof(uint64_t) + 255) & ~static_cast<size_t>(255);
-  b.bytes = b.key_bytes + ((static_cast<size_t>(rows) * pieces * 2 * sizeof(float) + 255) & ~static_cast<size_t>(255));
+  const int64_t rows = static_cast<int64_t>(num_seqs) * beams;
+  b.row_chunks = static_cast<int>((static_cast<int64_t>(vocab) + kChunk - 1) / kChunk);
+  b.chunks = rows * b.row_chunks;
+  const int64_t ctas = static_cast<int64_t>(kResident) * num_sms;
+  b.run = static_cast<int>((b.chunks + ctas - 1) / ctas);
+  b.ctas = static_cast<int>((b.chunks + b.run - 1) / b.run);
+  b.pieces = (b.row_chunks + b.run - 2) / b.run + 1;  // runs that row_chunks chunks in a row can touch
+  b.key_bytes = (static_cast<size_t>(rows) * b.pieces * select * sizeof(uint64_t) + 255) & ~static_cast<size_t>(255);
+  b.bytes = b.key_bytes +
+            ((static_cast<size_t>(b.chunks) * kWarps * 2 * sizeof(float) + 255) & ~static_cast<size_t>(255));
   return b;
 }
 
@@ -557,8 +565,10 @@ int launch_beam_select(const BeamArgs& a, void* workspace, int num_sms, cudaStre
   p.vocab = a.vocab;
   p.select = a.select;
   p.pieces = b.pieces;
-  p.chunks_per_piece = b.chunks_per_piece;
-  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.num_seqs) * a.beams * b.pieces));
+  p.row_chunks = b.row_chunks;
+  p.run = b.run;
+  p.chunks = b.chunks;
+  const dim3 grid(static_cast<unsigned>(b.ctas));
   const int64_t elem = a.dtype == PKV_F32 ? 4 : 2;
   const bool aligned = (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0 && a.row_stride * elem % 16 == 0;
   cudaError_t e;
@@ -570,7 +580,7 @@ int launch_beam_select(const BeamArgs& a, void* workspace, int num_sms, cudaStre
                 : launch_k(scan_kernel<__nv_bfloat16, false>, grid, dim3(kThreads), 0, s, p);
   if (e != cudaSuccess) return PKV_ERR_CUDA;
   SelParams q{p.keys, p.ml, a.cum, a.finished, a.out_scores, a.out_parents, a.out_tokens,
-              a.beams, a.vocab, a.select, b.pieces, a.eos};
+              a.beams, a.vocab, a.select, b.pieces, b.row_chunks * kWarps, a.eos};
   return cuda_status(launch_k(select_kernel, dim3(a.num_seqs), dim3(kThreads), 0, s, q));
 }
 
