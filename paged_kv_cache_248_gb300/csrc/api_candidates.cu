@@ -28,9 +28,9 @@ int check_beams(int32_t num_seqs, int32_t num_beams, int32_t vocab, int32_t num_
   if (num_seqs < 0 || num_beams < 1 || vocab < 1 || num_select < 1) return PKV_ERR_INVALID_ARG;
   if (num_beams > kMaxBeams || num_select > kMaxSelect) return PKV_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(num_beams) * vocab >= (int64_t(1) << 31)) return PKV_ERR_UNSUPPORTED;
-  // CTAs of the scan: at most one per 8192 logits and one per row
+  // blocks of 1024 logits are numbered in 32 bits
   const int64_t rows = static_cast<int64_t>(num_seqs) * num_beams;
-  return rows * (vocab / 8192 + 1) >= (int64_t(1) << 31) ? PKV_ERR_UNSUPPORTED : PKV_OK;
+  return rows * (vocab / 1024 + 1) >= (int64_t(1) << 31) ? PKV_ERR_UNSUPPORTED : PKV_OK;
 }
 
 int check_tree(const pkv_cache_desc* cache, int32_t num_q_heads, int32_t max_query_len) {
