@@ -28,6 +28,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kVals = 32;                 // values of a block per lane
 constexpr int kBlockVals = 32 * kVals;
+constexpr int kSelThreads = 512;          // of the selection
+constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMaxBeams = 64;
 constexpr int kCap = 1536;                // candidates collected between cuts
 constexpr int kResident = 5;              // CTAs of the scan on an SM
@@ -69,15 +71,67 @@ struct Cands {
   }
 };
 
+// The largest t that at least `need` of the threads' counts-above reach: with count(t) how many
+// of a thread's values are t or more, the largest t whose counts sum to `need` or more (0: none).
+// One bit of t at a time; it ends early where the sum is `need` exactly.
+template <typename F>
+__device__ uint32_t reached_by(int* s_sum, int need, F&& count) {
+  uint32_t t = 0;
+  if (threadIdx.x < 2) s_sum[threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll 1
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t u = t | 1u << bit;
+    const int mine = __reduce_add_sync(0xffffffffu, count(u));
+    int* sum = s_sum + (bit & 1);
+    if ((threadIdx.x & 31) == 0 && mine > 0) atomicAdd(sum, mine);
+    __syncthreads();
+    const int all = *sum;
+    if (threadIdx.x == 0) s_sum[(bit & 1) ^ 1] = 0;  // the next round's
+    __syncthreads();
+    if (all >= need) {
+      t = u;
+      if (all == need) break;
+    }
+  }
+  return t;
+}
+
 // Cuts the n collected candidates to the k best, best first (all threads, with everything
 // pushed); returns the new count.  Every candidate's rank is the number of better ones; few
-// candidates are each ranked by several threads, which share the comparisons.
+// candidates are each ranked by several threads, which share the comparisons, and of many the
+// worse ones are left out by their upper halves first.
 __device__ int cut(Cands& buf, int* ranks, int n, int k) {
-  if (n <= kThreads / 2) {
+  constexpr int kPer = kCap / kSelThreads;
+  if (n > 128) {
+    Cand mine[kPer];
+    uint32_t top[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = threadIdx.x + j * kSelThreads;
+      mine[j] = i < n ? buf.get(i) : Cand{0, 0};
+      top[j] = static_cast<uint32_t>(mine[j].hi >> 32);
+    }
+    const uint32_t least = reached_by(ranks, k, [&](uint32_t t) {
+      int c = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) c += top[j] >= t ? 1 : 0;
+      return c;
+    });
+    if (threadIdx.x == 0) ranks[0] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (threadIdx.x + j * kSelThreads < n && top[j] >= least) buf.set(atomicAdd(ranks, 1), mine[j]);
+    __syncthreads();
+    n = ranks[0];
+    __syncthreads();
+  }
+  if (n <= 128) {
     int width = 32;
     while (width < n) width *= 2;
-    const int i = threadIdx.x & (width - 1), step = kThreads / width;
-    ranks[threadIdx.x] = 0;
+    const int i = threadIdx.x & (width - 1), step = kSelThreads / width;
+    if (threadIdx.x < 128) ranks[threadIdx.x] = 0;
     __syncthreads();
     Cand mine{0, 0};
     if (i < n) {
@@ -92,14 +146,13 @@ __device__ int cut(Cands& buf, int* ranks, int n, int k) {
     __syncthreads();
     return min(n, k);
   }
-  constexpr int kPer = kCap / kThreads;
-  Cand mine[kPer];
+  Cand mine[kPer];  // (many with the same upper half)
   int rank[kPer];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    const int i = threadIdx.x + j * kThreads;
+    const int i = threadIdx.x + j * kSelThreads;
     rank[j] = i < n ? 0 : kCap;
-    if (i < n) mine[j] = buf.get(i);
+    mine[j] = i < n ? buf.get(i) : Cand{0, 0};
   }
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
@@ -258,46 +311,32 @@ struct SelParams {
 // nothing) into buf, best first; returns how many there are.  What scores below the
 // num_select-th largest of the threads' maxima is left out from the start.
 template <typename F>
-__device__ int best_of(Cands& buf, int* s_rank, int* s_count, uint32_t* s_best, uint32_t* s_floor, int total, int select,
-                       F&& cand) {
-  constexpr int kKeep = 4;  // candidates that a thread keeps in registers
+__device__ int best_of(Cands& buf, int* s_rank, int* s_count, int total, int select, F&& cand) {
+  constexpr int kKeep = 2;  // candidates that a thread keeps in registers
   Cand kept[kKeep];
   uint32_t best = 0;
 #pragma unroll
   for (int j = 0; j < kKeep; ++j) {
-    const int i = threadIdx.x + j * kThreads;
+    const int i = threadIdx.x + j * kSelThreads;
     kept[j] = i < total ? cand(i) : Cand{0, 0};
     best = max(best, static_cast<uint32_t>(kept[j].hi >> 32));
   }
-  for (int i = threadIdx.x + kKeep * kThreads; i < total; i += kThreads)
+  for (int i = threadIdx.x + kKeep * kSelThreads; i < total; i += kSelThreads)
     best = max(best, static_cast<uint32_t>(cand(i).hi >> 32));
-  s_best[threadIdx.x] = best;
-  if (threadIdx.x == 0) {
-    *s_floor = 0;
-    *s_count = 0;
-  }
-  __syncthreads();
-  int rank = 0;  // threads with a larger maximum, or the same and a lower index
-#pragma unroll 4
-  for (int t = 0; t < kThreads; t += 4) {
-    const uint4 o = *reinterpret_cast<const uint4*>(s_best + t);
-    rank += (o.x > best || (o.x == best && t < threadIdx.x)) + (o.y > best || (o.y == best && t + 1 < threadIdx.x)) +
-            (o.z > best || (o.z == best && t + 2 < threadIdx.x)) + (o.w > best || (o.w == best && t + 3 < threadIdx.x));
-  }
-  if (rank == select - 1) *s_floor = best;
-  __syncthreads();
-  Cand floor_c{*s_floor > 0 ? (static_cast<uint64_t>(*s_floor) << 32) - 1 : 0, 0xffffffffu};
+  if (threadIdx.x == 0) *s_count = 0;
+  const uint32_t least = reached_by(s_rank, select, [&](uint32_t t) { return best >= t ? 1 : 0; });
+  Cand floor_c{least > 0 ? (static_cast<uint64_t>(least) << 32) - 1 : 0, 0xffffffffu};
 #pragma unroll 1
-  for (int base = 0; base < total; base += kKeep * kThreads) {
+  for (int base = 0; base < total; base += kKeep * kSelThreads) {
 #pragma unroll
     for (int j = 0; j < kKeep; ++j) {
-      const int i = base + threadIdx.x + j * kThreads;
+      const int i = base + threadIdx.x + j * kSelThreads;
       const Cand c = base == 0 ? kept[j] : (i < total ? cand(i) : Cand{0, 0});
       if (better(c, floor_c)) buf.set(atomicAdd(s_count, 1), c);  // (room for all: kCap - 512 a turn)
     }
     __syncthreads();
     const int cnt = *s_count;
-    if (cnt + kKeep * kThreads > kCap && base + kKeep * kThreads < total) {
+    if (cnt + kKeep * kSelThreads > kCap && base + kKeep * kSelThreads < total) {
       __syncthreads();
       const int left = cut(buf, s_rank, cnt, select);
       if (left == select && better(buf.get(left - 1), floor_c)) floor_c = buf.get(left - 1);
@@ -310,20 +349,19 @@ __device__ int best_of(Cands& buf, int* s_rank, int* s_count, uint32_t* s_best, 
 }
 
 template <typename T, bool kAligned>
-__global__ void __launch_bounds__(kThreads) select_kernel(const SelParams P) {
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelParams P) {
   __shared__ double s_lse[kMaxBeams], s_cum[kMaxBeams];
   __shared__ uint8_t s_done[kMaxBeams];
   __shared__ Cands buf;
-  __shared__ __align__(16) uint32_t s_best[kThreads];
-  __shared__ uint32_t s_floor, s_blocks[64];
-  __shared__ int s_count, s_rank[kThreads];
+  __shared__ uint32_t s_blocks[64];
+  __shared__ int s_count, s_rank[128];
   const int64_t n = blockIdx.x;
   const int W = P.beams, V = P.scan.vocab, per_row = P.scan.row_blocks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
   grid_dep_launch();
   // a warp per beam joins its sums
-  for (int w = warp; w < W; w += kWarps) {
+  for (int w = warp; w < W; w += kSelWarps) {
     const int64_t row = n * W + w;
     const bool done = P.scan.finished != nullptr && __ldg(P.scan.finished + row) != 0;
     const float2* sums = P.scan.sums + row * per_row;
@@ -356,7 +394,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelParams P) {
     return isfinite(lse) && isfinite(score) ? ordered_bits(score) : 0;
   };
   // the best blocks: a finished beam is one of one candidate, its first
-  const int blocks = best_of(buf, s_rank, &s_count, s_best, &s_floor, W * per_row, P.select, [&](int i) -> Cand {
+  const int blocks = best_of(buf, s_rank, &s_count, W * per_row, P.select, [&](int i) -> Cand {
     const int w = i / per_row;
     uint64_t hi;
     if (s_done[w]) hi = i == w * per_row && isfinite(s_cum[w]) ? ordered_bits(s_cum[w]) : 0;
@@ -371,7 +409,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelParams P) {
   if (threadIdx.x == 0) s_count = 0;
   __syncthreads();
 #pragma unroll 1
-  for (int b0 = 0; b0 < blocks; b0 += kWarps) {
+  for (int b0 = 0; b0 < blocks; b0 += kSelWarps) {
     uint32_t todo = 0;
     int w = 0, at = 0;
     const T* x = nullptr;
@@ -425,7 +463,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelParams P) {
   }
   const int cnt = s_count;
   const int left = cnt > 0 ? cut(buf, s_rank, cnt, P.select) : 0;
-  for (int k = threadIdx.x; k < P.select; k += kThreads) {
+  for (int k = threadIdx.x; k < P.select; k += kSelThreads) {
     const int64_t o = n * P.select + k;
     if (k < left) {
       const Cand c = buf.get(k);
@@ -447,7 +485,7 @@ int launch_typed(const SelParams& q, int32_t num_seqs, int num_sms, cudaStream_t
   const int st = cuda_status(launch_k(scan_kernel<T, kAligned>, dim3(static_cast<unsigned>(want < most ? want : most)),
                                       dim3(kThreads), 0, s, q.scan));
   if (st) return st;
-  return cuda_status(launch_k(select_kernel<T, kAligned>, dim3(num_seqs), dim3(kThreads), 0, s, q));
+  return cuda_status(launch_k(select_kernel<T, kAligned>, dim3(num_seqs), dim3(kSelThreads), 0, s, q));
 }
 
 int64_t row_blocks(int32_t vocab) { return (static_cast<int64_t>(vocab) + kBlockVals - 1) / kBlockVals; }
