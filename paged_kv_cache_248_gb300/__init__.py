@@ -272,84 +272,25 @@ def paged_attention_step(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
 
 
 # ----------------------------------------------------------------------------- candidate continuations
-# These calls are short on the GPU, so what the binding does between two of them counts: it
-# checks a tensor with attribute reads alone, passes pointers as integers and asks torch for
-# the raw stream.
-_I32, _I64, _F32, _U8, _BF16 = torch.int32, torch.int64, torch.float32, torch.uint8, torch.bfloat16
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-_descs: dict = {}    # (shape, dtype) of a cache -> (descriptor, pointer to it, layers)
-_ws_bytes: dict = {}  # sizes of a call -> bytes of its workspace
+# These calls are short on the GPU, so what the binding does between two of them counts: but for
+# pkv_tree_mask they go through the CPython module _native (csrc/binding.c), which checks the
+# tensors, makes results and scratch (torch.empty, for every call its own) and calls libpkv.
+_nat = None
 
 
-def _ptr(t: torch.Tensor, name: str, dtype, dev: int) -> int:
-    """Pointer of a contiguous tensor of this type on the current device."""
-    if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
-        _refuse(t, name, dtype, dev)
-    return t.data_ptr()
-
-
-def _refuse(t, name, dtype, dev):
-    if not t.is_cuda or t.get_device() != dev:
-        raise ValueError(f"{name} must be a tensor on the current CUDA device (cuda:{dev})")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _shaped(t: torch.Tensor, name: str, shape) -> None:
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-
-
-def _caches(k_cache: torch.Tensor, v_cache: torch.Tensor):
-    """(descriptor, pointer to it, layers) of one cache [blocks, Hkv, 16, d] or of a model's,
-    [layers, ...]."""
-    key = (k_cache.shape, k_cache.dtype)
-    got = _descs.get(key)
-    if got is None or v_cache.shape != key[0] or v_cache.dtype is not key[1]:
-        if k_cache.dim() == 5 and k_cache.shape == v_cache.shape and k_cache.shape[0] > 0:
-            desc, layers = _cache_desc(k_cache[0], v_cache[0]), k_cache.shape[0]
-        else:
-            desc, layers = _cache_desc(k_cache, v_cache), 1
-        if len(_descs) > 256:
-            _descs.clear()
-        got = _descs[key] = (desc, ctypes.byref(desc), layers)
-    return got
-
-
-def _scratch(name: str, sizes: tuple, args: tuple, dev: int, stream, more: tuple = ()) -> torch.Tensor:
-    """Scratch of one call, from torch's allocator: its own for every call and every captured
-    graph.  A tensor made here belongs to the current stream; one used on ``stream`` stays
-    alive until that stream is done with it."""
-    key = (name, dev, sizes, more)
-    n = _ws_bytes.get(key)
-    if n is None:
-        size = ctypes.c_int64(0)
-        _check(getattr(lib(), name)(*args, *sizes, ctypes.byref(size)), name)
-        if len(_ws_bytes) > 4096:
-            _ws_bytes.clear()
-        n = _ws_bytes[key] = max(256, size.value)
-    ws = torch.empty(n, dtype=_U8, device=dev)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws
-
-
-def _made(shape, dtype, dev: int, stream) -> torch.Tensor:
-    out = torch.empty(shape, dtype=dtype, device=dev)
-    if stream is not None:
-        out.record_stream(stream)
-    return out
-
-
-def _requests(block_tables, seq_lens, query_start_loc):
-    """(number of requests, columns of their tables)."""
-    n = seq_lens.shape[0]
-    shape = block_tables.shape
-    if len(shape) != 2 or shape[0] != n or query_start_loc.shape[0] != n + 1:
-        raise ValueError("block_tables, seq_lens and query_start_loc disagree on the number of requests")
-    return n, shape[1]
+def _calls():
+    global _nat
+    if _nat is None:
+        lib()
+        try:
+            from . import _native as m
+        except ImportError as e:
+            raise ImportError("_native.so not built; run `python -m paged_kv_cache_248_gb300._build`") from e
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        m.setup(LIB_PATH, torch, PkvError, torch.cuda.current_device, raw)
+        _nat = m
+    return _nat
 
 
 def pkv_tree_mask(parents: torch.Tensor, query_start_loc: torch.Tensor, max_query_len: int,
@@ -358,22 +299,19 @@ def pkv_tree_mask(parents: torch.Tensor, query_start_loc: torch.Tensor, max_quer
     iff node u of t's request is t itself or one of its ancestors.  ``parents`` int32 [T]: the
     node that each token continues (smaller than its own index), -1 for the context.
     ``depths``, if given, receives the number of ancestors (int32 [T])."""
-    n = parents.shape[0]
-    words = (int(max_query_len) + 63) // 64
-    if out is not None and (out.dim() != 2 or out.shape[0] != n):
-        raise ValueError("out must be int64 [num_tokens, words]")
-    if depths is not None:
-        _shaped(depths, "depths", (n,))
-    dev = torch.cuda.current_device()
+    n, words = parents.shape[0], (int(max_query_len) + 63) // 64
+    for t, name in ((out, "out"), (depths, "depths")):
+        if t is not None and (t.dim() != (2 if name == "out" else 1) or t.shape[0] != n):
+            raise ValueError(f"{name} must have a row for every token")
     if out is None:
-        out = _made((n, max(words, 1)), _I64, dev, stream)
-    st = (_lib or lib()).pkv_tree_mask(
-        _ptr(parents, "parents", _I32, dev), _ptr(query_start_loc, "query_start_loc", _I32, dev),
-        query_start_loc.shape[0] - 1, n, _ptr(out, "out", _I64, dev), out.shape[1],
-        None if depths is None else _ptr(depths, "depths", _I32, dev),
-        _raw_stream(dev) if stream is None else stream.cuda_stream)
-    if st:
-        raise PkvError(st, "pkv_tree_mask")
+        out = torch.empty((n, max(words, 1)), dtype=torch.int64, device=parents.device)
+        if stream is not None:
+            out.record_stream(stream)
+    _check(lib().pkv_tree_mask(_dev(parents, "parents", torch.int32),
+                               _dev(query_start_loc, "query_start_loc", torch.int32), query_start_loc.shape[0] - 1, n,
+                               _dev(out, "out", torch.int64), out.shape[1],
+                               _dev(depths, "depths", torch.int32) if depths is not None else None,
+                               _stream(stream)), "pkv_tree_mask")
     return out
 
 
@@ -386,36 +324,8 @@ def paged_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     ``tree_mask`` (int64 [T, words], as pkv_tree_mask makes it) has.  A row that sees nothing
     is zero.  ``workspace``: scratch of a caller that keeps its own (uint8; calls that may
     overlap take one each)."""
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache and v_cache must both be [num_blocks, num_kv_heads, 16, head_dim]")
-    desc, pdesc, _ = _caches(k_cache, v_cache)
-    T, hq, d = q.shape
-    if d != desc.head_dim:
-        raise ValueError("q must be [num_tokens, num_q_heads, head_dim]")
-    mshape = tree_mask.shape
-    if len(mshape) != 2 or mshape[0] != T:
-        raise ValueError("tree_mask must be int64 [num_tokens, words]")
-    n, cols = _requests(block_tables, seq_lens, query_start_loc)
-    if out is not None:
-        _shaped(out, "out", q.shape)
-    dev = torch.cuda.current_device()
-    dt = k_cache.dtype
-    args = (_ptr(q, "q", dt, dev), _ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev), pdesc,
-            _ptr(block_tables, "block_tables", _I32, dev), cols, _ptr(seq_lens, "seq_lens", _I32, dev),
-            _ptr(query_start_loc, "query_start_loc", _I32, dev), _ptr(tree_mask, "tree_mask", _I64, dev), mshape[1], n,
-            hq, T, max_query_len, max_seq_len, scale)
-    if out is None:
-        out = _made(q.shape, dt, dev, stream)
-    if T == 0:
-        return out
-    if workspace is None:
-        workspace = _scratch("pkv_tree_workspace", (hq, max_query_len), (pdesc,), dev, stream,
-                             (desc.num_kv_heads, d, dt))
-    st = (_lib or lib()).paged_attention_tree(*args, _ptr(out, "out", dt, dev), _ptr(workspace, "workspace", _U8, dev),
-                                              workspace.numel(), _raw_stream(dev) if stream is None else stream.cuda_stream)
-    if st:
-        raise PkvError(st, "paged_attention_tree")
-    return out
+    return (_nat or _calls()).tree(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, tree_mask, scale,
+                                    max_query_len, max_seq_len, out, workspace, stream)
 
 
 def pkv_compact_path(path: torch.Tensor, path_lens: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
@@ -424,26 +334,8 @@ def pkv_compact_path(path: torch.Tensor, path_lens: torch.Tensor, block_tables: 
     """Moves the accepted path of each request's drafted tree together, in place and in every
     layer (caches [blocks, Hkv, 16, d] or [layers, blocks, Hkv, 16, d]): node path[i][a] goes
     to position c_i + a, c_i = seq_lens[i] - q_i.  Returns the new lengths c_i + path_lens[i]."""
-    _, pdesc, layers = _caches(k_cache, v_cache)
-    n, cols = _requests(block_tables, seq_lens, query_start_loc)
-    pshape = path.shape
-    if len(pshape) != 2 or pshape[0] != n or path_lens.shape != (n,):
-        raise ValueError("path must be [num_seqs, max_path], path_lens [num_seqs]")
-    if new_seq_lens is not None:
-        _shaped(new_seq_lens, "new_seq_lens", (n,))
-    dev = torch.cuda.current_device()
-    dt = k_cache.dtype
-    args = (_ptr(path, "path", _I32, dev), pshape[1], _ptr(path_lens, "path_lens", _I32, dev),
-            _ptr(block_tables, "block_tables", _I32, dev), cols, _ptr(seq_lens, "seq_lens", _I32, dev),
-            _ptr(query_start_loc, "query_start_loc", _I32, dev), n, _ptr(k_cache, "k_cache", dt, dev),
-            _ptr(v_cache, "v_cache", dt, dev), pdesc, layers)
-    if new_seq_lens is None:
-        new_seq_lens = _made(n, _I32, dev, stream)
-    st = (_lib or lib()).pkv_compact_path(*args, _ptr(new_seq_lens, "new_seq_lens", _I32, dev),
-                                          _raw_stream(dev) if stream is None else stream.cuda_stream)
-    if st:
-        raise PkvError(st, "pkv_compact_path")
-    return new_seq_lens
+    return (_nat or _calls()).compact(path, path_lens, block_tables, seq_lens, query_start_loc, k_cache, v_cache,
+                                       new_seq_lens, stream)
 
 
 def pkv_beam_select(logits: torch.Tensor, cum_scores: torch.Tensor, num_select: int,
@@ -456,46 +348,7 @@ def pkv_beam_select(logits: torch.Tensor, cum_scores: torch.Tensor, num_select: 
     will do); ``cum_scores`` fp32 [N, W].  A beam with ``finished`` (bool or uint8 [N, W])
     stands for itself, as token ``eos_token``.  Equal scores go by beam, then token; where
     candidates run out, score is -inf and parent and token are -1."""
-    shape = logits.shape
-    if len(shape) != 3:
-        raise ValueError("logits must be [num_seqs, num_beams, vocab]")
-    N, W, V = shape
-    dtype = logits.dtype
-    if dtype is not _F32 and dtype is not _BF16:
-        raise ValueError(f"logits must be float32 or bfloat16, got {dtype}")
-    step = V
-    if not logits.is_contiguous() and N * W * V > 0:
-        s0, s1, s2 = logits.stride()
-        step = s1 if W > 1 else (s0 if N > 1 else V)
-        if (V > 1 and s2 != 1) or (N > 1 and s0 != W * step) or step < V:
-            raise ValueError("logits must have contiguous rows, evenly spaced")
-    _shaped(cum_scores, "cum_scores", (N, W))
-    if finished is not None:
-        _shaped(finished, "finished", (N, W))
-        if finished.dtype is torch.bool:
-            finished = finished.view(_U8)
-    K = int(num_select)
-    dev = torch.cuda.current_device()
-    if logits.get_device() != dev:
-        _refuse(logits, "logits", dtype, dev)
-    if out is None:
-        shape = (N, max(K, 0))
-        out = _made(shape, _F32, dev, stream), _made(shape, _I32, dev, stream), _made(shape, _I32, dev, stream)
-    else:
-        for t, name in zip(out, ("scores", "parents", "tokens")):
-            _shaped(t, name, (N, K))
-    scores, parents, tokens = out
-    if workspace is None:
-        workspace = _scratch("pkv_beam_workspace", (N, W, V, K), (), dev, stream)
-    st = (_lib or lib()).pkv_beam_select(
-        logits.data_ptr(), PKV_F32 if dtype is _F32 else PKV_BF16, step, _ptr(cum_scores, "cum_scores", _F32, dev),
-        None if finished is None else _ptr(finished, "finished", _U8, dev), eos_token, N, W, V, K,
-        _ptr(scores, "scores", _F32, dev), _ptr(parents, "parents", _I32, dev), _ptr(tokens, "tokens", _I32, dev),
-        _ptr(workspace, "workspace", _U8, dev), workspace.numel(),
-        _raw_stream(dev) if stream is None else stream.cuda_stream)
-    if st:
-        raise PkvError(st, "pkv_beam_select")
-    return scores, parents, tokens
+    return (_nat or _calls()).beam(logits, cum_scores, num_select, finished, eos_token, out, workspace, stream)
 
 
 def pkv_fork_tables(block_tables: torch.Tensor, seq_lens: torch.Tensor, parents: torch.Tensor,
@@ -510,41 +363,8 @@ def pkv_fork_tables(block_tables: torch.Tensor, seq_lens: torch.Tensor, parents:
     place; a block without users is free.  Too few free blocks change nothing and show as
     PKV_ERR_NO_MEMORY in pkv_get_last_error.  Without caches (None, None) only the tables
     and counts change."""
-    shape = block_tables.shape
-    if len(shape) != 2:
-        raise ValueError("block_tables must be [num_rows, max_blocks_per_seq]")
-    B, M = shape
-    if k_cache is None or v_cache is None:
-        if k_cache is not None or v_cache is not None:
-            raise ValueError("k_cache and v_cache must be given together")
-        desc = _CacheDesc(ref_counts.shape[0], BLOCK_SIZE, 1, 128, PKV_BF16)
-        pdesc, layers = ctypes.byref(desc), 1
-    else:
-        desc, pdesc, layers = _caches(k_cache, v_cache)
-    if ref_counts.shape != (desc.num_blocks,):
-        raise ValueError("ref_counts must be [num_blocks] of the cache")
-    _shaped(seq_lens, "seq_lens", (B,))
-    _shaped(parents, "parents", (B,))
-    if out is not None:
-        _shaped(out[0], "new tables", (B, M))
-        _shaped(out[1], "new lengths", (B,))
-    dev = torch.cuda.current_device()
-    kp = vp = None
-    if k_cache is not None:
-        dt = k_cache.dtype
-        kp, vp = _ptr(k_cache, "k_cache", dt, dev), _ptr(v_cache, "v_cache", dt, dev)
-    tables, lens = out if out is not None else (_made(shape, _I32, dev, stream), _made(B, _I32, dev, stream))
-    if workspace is None:
-        workspace = _scratch("pkv_fork_workspace", (B,), (), dev, stream)
-    st = (_lib or lib()).pkv_fork_tables(
-        _ptr(block_tables, "block_tables", _I32, dev), _ptr(seq_lens, "seq_lens", _I32, dev), B, M,
-        _ptr(parents, "parents", _I32, dev), new_tokens, _ptr(ref_counts, "ref_counts", _I32, dev),
-        _ptr(tables, "new tables", _I32, dev), _ptr(lens, "new lengths", _I32, dev), kp, vp, pdesc, layers,
-        _ptr(workspace, "workspace", _U8, dev), workspace.numel(),
-        _raw_stream(dev) if stream is None else stream.cuda_stream)
-    if st:
-        raise PkvError(st, "pkv_fork_tables")
-    return tables, lens
+    return (_nat or _calls()).fork(block_tables, seq_lens, parents, ref_counts, k_cache, v_cache, new_tokens, out,
+                                    workspace, stream)
 
 
 def pkv_get_last_error(stream=None) -> int:

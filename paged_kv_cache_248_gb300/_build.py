@@ -2,7 +2,8 @@
 
 Each translation unit compiles in parallel to an object file under
 ``paged_kv_cache_248_gb300/_build/``; the objects link into
-``paged_kv_cache_248_gb300/libpkv.so``.  No cmake, no torch extension machinery.
+``paged_kv_cache_248_gb300/libpkv.so``; ``binding.c`` becomes the CPython module ``_native.so``.
+No cmake, no torch extension machinery.
 Run ``python -m paged_kv_cache_248_gb300._build`` or call :func:`build`.
 """
 from __future__ import annotations
@@ -12,12 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpkv.so")
+NATIVE = os.path.join(PKG, "_native.so")  # CPython module over libpkv (binding.c)
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -78,6 +81,15 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         if r.returncode != 0:
             raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    src = os.path.join(CSRC, "binding.c")
+    if force or not os.path.exists(NATIVE) or os.path.getmtime(NATIVE) < max(os.path.getmtime(src), hdr):
+        tmp = NATIVE + f".tmp{os.getpid()}"
+        cmd = [shutil.which("gcc") or "gcc", "-O2", "-shared", "-fPIC", f"-I{INCLUDE}",
+               f"-I{sysconfig.get_paths()['include']}", src, "-o", tmp, "-ldl"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"gcc failed for binding.c:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, NATIVE)
     return LIB
 
 
