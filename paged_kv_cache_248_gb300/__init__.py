@@ -274,7 +274,7 @@ def paged_attention_step(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
 # ----------------------------------------------------------------------------- candidate continuations
 # These calls are short on the GPU, so what the binding does between two of them counts: but for
 # pkv_tree_mask they go through the CPython module _native (csrc/binding.c), which checks the
-# tensors, makes results and scratch (torch.empty, for every call its own) and calls libpkv.
+# tensors, makes results and scratch and calls libpkv.
 _nat = None
 
 
@@ -288,7 +288,7 @@ def _calls():
             raise ImportError("_native.so not built; run `python -m paged_kv_cache_248_gb300._build`") from e
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-        m.setup(LIB_PATH, torch, PkvError, torch.cuda.current_device, raw)
+        m.setup(LIB_PATH, torch, PkvError, torch.cuda.current_device, raw, torch.cuda.is_current_stream_capturing)
         _nat = m
     return _nat
 

@@ -3,9 +3,15 @@
  * These calls take a few microseconds on the GPU, less than what a Python function spends on
  * checking ten tensors and converting twenty arguments.  This module does the same in C: it
  * reads a tensor's type, shape, device and pointer through its Python attributes (no libtorch),
- * checks them, makes results and scratch with torch.empty and calls libpkv.  Scratch comes from
- * torch's allocator for every call: calls on two streams and captured graphs never share it.
- * Every entry holds the GIL for its whole call, which only enqueues work.
+ * checks them, makes results and scratch and calls libpkv.
+ *
+ * torch.empty takes as long as such a call (5 us beside a launch on a Grace core), so small
+ * results are made 32 at a time, as parts of one tensor, and handed out once each; and scratch
+ * is kept per device, stream and call.  Work on one stream runs in order, and every entry holds
+ * the GIL for its whole call, which only enqueues work, so two calls never use one scratch at
+ * the same time.  Where neither is safe -- while the stream is captured into a graph, whose
+ * replays need memory of their own, or on a stream that the caller names -- both come from
+ * torch.empty for that call alone.
  *
  * setup(path, torch, PkvError) opens libpkv and keeps what is needed of torch.
  */
@@ -19,10 +25,11 @@
 typedef int64_t i64;
 
 static struct {
-  PyObject *empty, *error, *get_device, *raw_stream, *current_device;
+  PyObject *empty, *error, *raw_stream, *current_device, *capturing;
+  PyObject *results, *scratch; /* see take_result, take_scratch */
   PyObject *i32, *i64, *f32, *bf16, *u8, *boolean;
   PyObject *s_dtype, *s_shape, *s_data_ptr, *s_is_contiguous, *s_get_device, *s_stride, *s_cuda_stream, *s_record_stream,
-      *s_view, *kw_empty;
+      *s_view, *s_unbind, *kw_empty;
   __typeof__(&paged_attention_tree) tree;
   __typeof__(&pkv_tree_workspace) tree_ws;
   __typeof__(&pkv_compact_path) compact;
@@ -116,24 +123,36 @@ static int shaped(const Arg* a, int dim, i64 n0, i64 n1) {
   return 0;
 }
 
-/* The current device, and the stream to launch on. */
-static int place(PyObject* stream, i64* dev, void** s) {
+/* Where a call runs: its device, its stream, and whether results and scratch may be kept ready. */
+typedef struct {
+  i64 dev;
+  void* stream;
+  PyObject* given; /* the caller's stream, or None */
+  int keep;
+} Place;
+
+static int place(PyObject* stream, Place* w) {
   PyObject* d = PyObject_CallNoArgs(T.current_device);
   if (!d) return 0;
-  *dev = PyLong_AsLongLong(d);
+  w->dev = PyLong_AsLongLong(d);
+  w->given = stream;
   PyObject* h = stream == Py_None ? PyObject_CallOneArg(T.raw_stream, d) : PyObject_GetAttr(stream, T.s_cuda_stream);
   Py_DECREF(d);
   if (!h) return 0;
-  *s = PyLong_AsVoidPtr(h);
+  w->stream = PyLong_AsVoidPtr(h);
   Py_DECREF(h);
+  PyObject* c = PyObject_CallNoArgs(T.capturing);
+  if (!c) return 0;
+  w->keep = stream == Py_None && c == Py_False;
+  Py_DECREF(c);
   return !PyErr_Occurred();
 }
 
 /* torch.empty(shape, dtype=dtype, device=dev); one that a given stream uses stays alive until
  * that stream is done with it. */
-static PyObject* made(int dim, const i64* n, PyObject* dtype, i64 dev, PyObject* stream) {
+static PyObject* made(int dim, const i64* n, PyObject* dtype, const Place* w) {
   PyObject* shape = PyTuple_New(dim);
-  PyObject* d = PyLong_FromLongLong(dev);
+  PyObject* d = PyLong_FromLongLong(w->dev);
   PyObject* r = NULL;
   if (shape && d) {
     for (int i = 0; i < dim; ++i) PyTuple_SET_ITEM(shape, i, PyLong_FromLongLong(n[i]));
@@ -142,17 +161,84 @@ static PyObject* made(int dim, const i64* n, PyObject* dtype, i64 dev, PyObject*
   }
   Py_XDECREF(shape);
   Py_XDECREF(d);
-  if (r && stream != Py_None) {
-    PyObject* x = PyObject_CallMethodOneArg(r, T.s_record_stream, stream);
+  if (r && w->given != Py_None) {
+    PyObject* x = PyObject_CallMethodOneArg(r, T.s_record_stream, w->given);
     if (!x) Py_CLEAR(r);
     Py_XDECREF(x);
   }
   return r;
 }
 
+/* A new tensor of four bytes a value or two, small ones from a store of ready parts. */
+static PyObject* take_result(int dim, const i64* n, PyObject* dtype, const Place* w) {
+  enum { kParts = 32, kMostBytes = 2048 };
+  i64 values = 1;
+  for (int i = 0; i < dim; ++i) values *= n[i];
+  if (!w->keep || dim > 2 || values * 4 > kMostBytes || values == 0) return made(dim, n, dtype, w);
+  struct {
+    PyObject* dtype;
+    void* stream;
+    i64 dev, n[2];
+  } key = {dtype, w->stream, w->dev, {n[0], dim > 1 ? n[1] : -1}};
+  PyObject* k = PyBytes_FromStringAndSize((const char*)&key, sizeof key);
+  if (!k) return NULL;
+  PyObject* r = NULL;
+  PyObject* ready = PyDict_GetItemWithError(T.results, k); /* a list, borrowed */
+  if (!ready && !PyErr_Occurred()) {
+    if (PyDict_GET_SIZE(T.results) >= 512) PyDict_Clear(T.results);
+    ready = PyList_New(0);
+    if (ready && PyDict_SetItem(T.results, k, ready)) Py_CLEAR(ready);
+    Py_XDECREF(ready); /* the store holds it */
+  }
+  if (ready && PyList_GET_SIZE(ready) == 0) {
+    const i64 whole[3] = {kParts, n[0], dim > 1 ? n[1] : 0};
+    PyObject* t = made(dim + 1, whole, dtype, w);
+    PyObject* parts = t ? PyObject_CallMethodNoArgs(t, T.s_unbind) : NULL;
+    if (!parts || PyList_SetSlice(ready, 0, 0, parts)) ready = NULL;
+    Py_XDECREF(parts);
+    Py_XDECREF(t);
+  }
+  if (ready) {
+    const Py_ssize_t last = PyList_GET_SIZE(ready) - 1;
+    r = Py_NewRef(PyList_GET_ITEM(ready, last));
+    if (PyList_SetSlice(ready, last, last + 1, NULL)) Py_CLEAR(r);
+  }
+  Py_DECREF(k);
+  return r;
+}
+
+/* Scratch of at least `bytes` for call number `call`. */
+static PyObject* take_scratch(i64 bytes, int call, const Place* w) {
+  if (bytes < 256) bytes = 256;
+  if (!w->keep) return made(1, &bytes, T.u8, w);
+  struct {
+    void* stream;
+    i64 dev, call;
+  } key = {w->stream, w->dev, call};
+  PyObject* k = PyBytes_FromStringAndSize((const char*)&key, sizeof key);
+  if (!k) return NULL;
+  PyObject* r = PyDict_GetItemWithError(T.scratch, k); /* (bytes, tensor), borrowed */
+  if (r && PyLong_AsLongLong(PyTuple_GET_ITEM(r, 0)) >= bytes) {
+    r = Py_NewRef(PyTuple_GET_ITEM(r, 1));
+  } else if (PyErr_Occurred()) {
+    r = NULL;
+  } else {
+    if (PyDict_GET_SIZE(T.scratch) >= 256) PyDict_Clear(T.scratch);
+    r = made(1, &bytes, T.u8, w);
+    PyObject* entry = r ? Py_BuildValue("(LO)", (long long)bytes, r) : NULL;
+    if (!entry || PyDict_SetItem(T.scratch, k, entry)) Py_CLEAR(r);
+    Py_XDECREF(entry);
+  }
+  Py_DECREF(k);
+  return r;
+}
+
 /* A given tensor (new reference), or a new one. */
-static PyObject* given_or_made(PyObject* given, int dim, const i64* n, PyObject* dtype, i64 dev, PyObject* stream) {
-  return given == Py_None ? made(dim, n, dtype, dev, stream) : Py_NewRef(given);
+static PyObject* given_or_made(PyObject* given, int dim, const i64* n, PyObject* dtype, const Place* w) {
+  return given == Py_None ? take_result(dim, n, dtype, w) : Py_NewRef(given);
+}
+static PyObject* given_or_scratch(PyObject* given, i64 bytes, int call, const Place* w) {
+  return given == Py_None ? take_scratch(bytes, call, w) : Py_NewRef(given);
 }
 
 static PyObject* failed(int status, const char* what) {
@@ -210,9 +296,9 @@ static int as_int32(PyObject* o, int32_t* v) {
 static PyObject* py_tree(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   Arg q, k, v, bt, lens, qsl, mask, o, w;
   pkv_cache_desc desc;
-  PyObject *dt, *out = NULL, *ws = NULL, *res = NULL, *stream = a[12];
-  i64 layers, dev, bytes = 0;
-  void* s;
+  PyObject *dt, *out = NULL, *ws = NULL, *res = NULL;
+  i64 layers, bytes = 0;
+  Place at;
   int32_t max_q, max_len;
   if (!want(n, 13)) return NULL;
   if (!shape_of(&k, a[1], "k_cache") || !shape_of(&v, a[2], "v_cache") || !caches(&k, &v, 0, &desc, &layers, &dt)) return NULL;
@@ -230,12 +316,12 @@ static PyObject* py_tree(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   const double scale = PyFloat_AsDouble(a[7]);
   if (scale == -1.0 && PyErr_Occurred()) return NULL;
   if (!as_int32(a[8], &max_q) || !as_int32(a[9], &max_len)) return NULL;
-  if (!place(stream, &dev, &s)) return NULL;
-  if (!check(&q, dt, dev) || !check(&k, dt, dev) || !check(&v, dt, dev) || !check(&bt, T.i32, dev) || !check(&lens, T.i32, dev) ||
-      !check(&qsl, T.i32, dev) || !check(&mask, T.i64, dev))
+  if (!place(a[12], &at)) return NULL;
+  if (!check(&q, dt, at.dev) || !check(&k, dt, at.dev) || !check(&v, dt, at.dev) || !check(&bt, T.i32, at.dev) || !check(&lens, T.i32, at.dev) ||
+      !check(&qsl, T.i32, at.dev) || !check(&mask, T.i64, at.dev))
     return NULL;
-  out = given_or_made(a[10], 3, q.n, dt, dev, stream);
-  if (!out || !shape_of(&o, out, "out") || !check(&o, dt, dev)) goto end;
+  out = given_or_made(a[10], 3, q.n, dt, &at);
+  if (!out || !shape_of(&o, out, "out") || !check(&o, dt, at.dev)) goto end;
   if (q.n[0] == 0) {
     res = Py_NewRef(out);
     goto end;
@@ -247,10 +333,10 @@ static PyObject* py_tree(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       goto end;
     }
   }
-  ws = given_or_made(a[11], 1, &bytes, T.u8, dev, stream);
-  if (!ws || !shape_of(&w, ws, "workspace") || !check(&w, T.u8, dev)) goto end;
+  ws = given_or_scratch(a[11], bytes, 0, &at);
+  if (!ws || !shape_of(&w, ws, "workspace") || !check(&w, T.u8, at.dev)) goto end;
   const int st = T.tree(q.ptr, k.ptr, v.ptr, &desc, bt.ptr, (int32_t)bt.n[1], lens.ptr, qsl.ptr, mask.ptr, (int32_t)mask.n[1],
-                        (int32_t)lens.n[0], (int32_t)q.n[1], q.n[0], max_q, max_len, (float)scale, o.ptr, w.ptr, w.n[0], s);
+                        (int32_t)lens.n[0], (int32_t)q.n[1], q.n[0], max_q, max_len, (float)scale, o.ptr, w.ptr, w.n[0], at.stream);
   res = st ? failed(st, "paged_attention_tree") : Py_NewRef(out);
 end:
   Py_XDECREF(out);
@@ -262,9 +348,9 @@ end:
 static PyObject* py_compact(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   Arg path, plens, bt, lens, qsl, k, v, o;
   pkv_cache_desc desc;
-  PyObject *dt, *out = NULL, *res = NULL, *stream = a[8];
-  i64 layers, dev;
-  void* s;
+  PyObject *dt, *out = NULL, *res = NULL;
+  i64 layers;
+  Place at;
   if (!want(n, 9)) return NULL;
   if (!shape_of(&k, a[5], "k_cache") || !shape_of(&v, a[6], "v_cache") || !caches(&k, &v, 1, &desc, &layers, &dt)) return NULL;
   if (!shape_of(&bt, a[2], "block_tables") || !shape_of(&lens, a[3], "seq_lens") || !shape_of(&qsl, a[4], "query_start_loc") ||
@@ -274,14 +360,14 @@ static PyObject* py_compact(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (path.dim != 2 || path.n[0] != lens.n[0] || plens.dim != 1 || plens.n[0] != lens.n[0])
     return refuse("path must be [num_seqs, max_path], path_lens [num_seqs]"), NULL;
   if (a[7] != Py_None && (!shape_of(&o, a[7], "new_seq_lens") || !shaped(&o, 1, lens.n[0], 0))) return NULL;
-  if (!place(stream, &dev, &s)) return NULL;
-  if (!check(&path, T.i32, dev) || !check(&plens, T.i32, dev) || !check(&bt, T.i32, dev) || !check(&lens, T.i32, dev) ||
-      !check(&qsl, T.i32, dev) || !check(&k, dt, dev) || !check(&v, dt, dev))
+  if (!place(a[8], &at)) return NULL;
+  if (!check(&path, T.i32, at.dev) || !check(&plens, T.i32, at.dev) || !check(&bt, T.i32, at.dev) || !check(&lens, T.i32, at.dev) ||
+      !check(&qsl, T.i32, at.dev) || !check(&k, dt, at.dev) || !check(&v, dt, at.dev))
     return NULL;
-  out = given_or_made(a[7], 1, lens.n, T.i32, dev, stream);
-  if (!out || !shape_of(&o, out, "new_seq_lens") || !check(&o, T.i32, dev)) goto end;
+  out = given_or_made(a[7], 1, lens.n, T.i32, &at);
+  if (!out || !shape_of(&o, out, "new_seq_lens") || !check(&o, T.i32, at.dev)) goto end;
   const int st = T.compact(path.ptr, (int32_t)path.n[1], plens.ptr, bt.ptr, (int32_t)bt.n[1], lens.ptr, qsl.ptr,
-                           (int32_t)lens.n[0], k.ptr, v.ptr, &desc, (int32_t)layers, o.ptr, s);
+                           (int32_t)lens.n[0], k.ptr, v.ptr, &desc, (int32_t)layers, o.ptr, at.stream);
   res = st ? failed(st, "pkv_compact_path") : Py_NewRef(out);
 end:
   Py_XDECREF(out);
@@ -291,11 +377,11 @@ end:
 /* (logits, cum_scores, num_select, finished, eos_token, out, workspace, stream) */
 static PyObject* py_beam(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   Arg x, cum, fin, r[3], w;
-  PyObject *out[3] = {NULL, NULL, NULL}, *ws = NULL, *res = NULL, *done = NULL, *stream = a[7];
+  PyObject *out[3] = {NULL, NULL, NULL}, *ws = NULL, *res = NULL, *done = NULL;
   PyObject* const types[3] = {T.f32, T.i32, T.i32};
   static const char* const names[3] = {"scores", "parents", "tokens"};
-  i64 dev, bytes = 0;
-  void* s;
+  i64 bytes = 0;
+  Place at;
   int32_t K, eos;
   if (!want(n, 8)) return NULL;
   if (!shape_of(&x, a[0], "logits")) return NULL;
@@ -328,23 +414,23 @@ static PyObject* py_beam(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     for (int i = 0; i < 3; ++i)
       if (!shape_of(&r[i], PyTuple_GET_ITEM(a[5], i), names[i]) || !shaped(&r[i], 2, N, K)) return NULL;
   }
-  if (!place(stream, &dev, &s)) return NULL;
-  if (call_long(x.t, T.s_get_device) != dev) {
-    if (!PyErr_Occurred()) PyErr_Format(PyExc_ValueError, "logits must be a tensor on the current CUDA device (cuda:%lld)", (long long)dev);
+  if (!place(a[7], &at)) return NULL;
+  if (call_long(x.t, T.s_get_device) != at.dev) {
+    if (!PyErr_Occurred()) PyErr_Format(PyExc_ValueError, "logits must be a tensor on the current CUDA device (cuda:%lld)", (long long)at.dev);
     return NULL;
   }
   PyObject* p = PyObject_CallMethodNoArgs(x.t, T.s_data_ptr);
   if (!p) return NULL;
   x.ptr = PyLong_AsVoidPtr(p);
   Py_DECREF(p);
-  if (!check(&cum, T.f32, dev)) return NULL;
+  if (!check(&cum, T.f32, at.dev)) return NULL;
   fin.ptr = NULL;
   if (a[3] != Py_None) {
     const int b = is_dtype(a[3], T.boolean);
     if (b < 0) return NULL;
     done = b ? PyObject_CallMethodOneArg(a[3], T.s_view, T.u8) : Py_NewRef(a[3]);
     fin.t = done;
-    if (!done || !check(&fin, T.u8, dev)) goto end;
+    if (!done || !check(&fin, T.u8, at.dev)) goto end;
   }
   if (a[6] == Py_None) {
     const int st = T.beam_ws((int32_t)N, (int32_t)W, (int32_t)V, K, &bytes);
@@ -352,18 +438,17 @@ static PyObject* py_beam(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       failed(st, "pkv_beam_select");
       goto end;
     }
-    if (bytes < 256) bytes = 256;
   }
   for (int i = 0; i < 3; ++i) {
-    out[i] = given_or_made(a[5] == Py_None ? Py_None : PyTuple_GET_ITEM(a[5], i), 2, shape, types[i], dev, stream);
+    out[i] = given_or_made(a[5] == Py_None ? Py_None : PyTuple_GET_ITEM(a[5], i), 2, shape, types[i], &at);
     r[i].name = names[i];
     r[i].t = out[i];
-    if (!out[i] || !check(&r[i], types[i], dev)) goto end;
+    if (!out[i] || !check(&r[i], types[i], at.dev)) goto end;
   }
-  ws = given_or_made(a[6], 1, &bytes, T.u8, dev, stream);
-  if (!ws || !shape_of(&w, ws, "workspace") || !check(&w, T.u8, dev)) goto end;
+  ws = given_or_scratch(a[6], bytes, 1, &at);
+  if (!ws || !shape_of(&w, ws, "workspace") || !check(&w, T.u8, at.dev)) goto end;
   const int st = T.beam(x.ptr, f32 ? PKV_F32 : PKV_BF16, step, cum.ptr, fin.ptr, eos, (int32_t)N, (int32_t)W, (int32_t)V, K,
-                        r[0].ptr, r[1].ptr, r[2].ptr, w.ptr, w.n[0], s);
+                        r[0].ptr, r[1].ptr, r[2].ptr, w.ptr, w.n[0], at.stream);
   res = st ? failed(st, "pkv_beam_select") : PyTuple_Pack(3, out[0], out[1], out[2]);
 end:
   for (int i = 0; i < 3; ++i) Py_XDECREF(out[i]);
@@ -376,9 +461,9 @@ end:
 static PyObject* py_fork(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   Arg bt, lens, par, refs, k, v, obt, olens, w;
   pkv_cache_desc desc = {0, PKV_BLOCK_SIZE, 1, 128, PKV_BF16};
-  PyObject *dt = NULL, *tables = NULL, *nlens = NULL, *ws = NULL, *res = NULL, *stream = a[9];
-  i64 layers = 1, dev, bytes = 0;
-  void* s;
+  PyObject *dt = NULL, *tables = NULL, *nlens = NULL, *ws = NULL, *res = NULL;
+  i64 layers = 1, bytes = 0;
+  Place at;
   int32_t num_new;
   if (!want(n, 10)) return NULL;
   if (!shape_of(&bt, a[0], "block_tables")) return NULL;
@@ -401,13 +486,13 @@ static PyObject* py_fork(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       return NULL;
   }
   if (!as_int32(a[6], &num_new)) return NULL;
-  if (!place(stream, &dev, &s)) return NULL;
-  if (!check(&bt, T.i32, dev) || !check(&lens, T.i32, dev) || !check(&par, T.i32, dev) || !check(&refs, T.i32, dev)) return NULL;
-  if (data && (!check(&k, dt, dev) || !check(&v, dt, dev))) return NULL;
-  tables = given_or_made(a[7] == Py_None ? Py_None : PyTuple_GET_ITEM(a[7], 0), 2, bt.n, T.i32, dev, stream);
-  nlens = given_or_made(a[7] == Py_None ? Py_None : PyTuple_GET_ITEM(a[7], 1), 1, bt.n, T.i32, dev, stream);
-  if (!tables || !nlens || !shape_of(&obt, tables, "new tables") || !check(&obt, T.i32, dev) ||
-      !shape_of(&olens, nlens, "new lengths") || !check(&olens, T.i32, dev))
+  if (!place(a[9], &at)) return NULL;
+  if (!check(&bt, T.i32, at.dev) || !check(&lens, T.i32, at.dev) || !check(&par, T.i32, at.dev) || !check(&refs, T.i32, at.dev)) return NULL;
+  if (data && (!check(&k, dt, at.dev) || !check(&v, dt, at.dev))) return NULL;
+  tables = given_or_made(a[7] == Py_None ? Py_None : PyTuple_GET_ITEM(a[7], 0), 2, bt.n, T.i32, &at);
+  nlens = given_or_made(a[7] == Py_None ? Py_None : PyTuple_GET_ITEM(a[7], 1), 1, bt.n, T.i32, &at);
+  if (!tables || !nlens || !shape_of(&obt, tables, "new tables") || !check(&obt, T.i32, at.dev) ||
+      !shape_of(&olens, nlens, "new lengths") || !check(&olens, T.i32, at.dev))
     goto end;
   if (a[8] == Py_None) {
     const int st = T.fork_ws((int32_t)bt.n[0], &bytes);
@@ -415,12 +500,11 @@ static PyObject* py_fork(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       failed(st, "pkv_fork_tables");
       goto end;
     }
-    if (bytes < 256) bytes = 256;
   }
-  ws = given_or_made(a[8], 1, &bytes, T.u8, dev, stream);
-  if (!ws || !shape_of(&w, ws, "workspace") || !check(&w, T.u8, dev)) goto end;
+  ws = given_or_scratch(a[8], bytes, 2, &at);
+  if (!ws || !shape_of(&w, ws, "workspace") || !check(&w, T.u8, at.dev)) goto end;
   const int st = T.fork_(bt.ptr, lens.ptr, (int32_t)bt.n[0], (int32_t)bt.n[1], par.ptr, num_new, refs.ptr, obt.ptr, olens.ptr,
-                         data ? k.ptr : NULL, data ? v.ptr : NULL, &desc, (int32_t)layers, w.ptr, w.n[0], s);
+                         data ? k.ptr : NULL, data ? v.ptr : NULL, &desc, (int32_t)layers, w.ptr, w.n[0], at.stream);
   res = st ? failed(st, "pkv_fork_tables") : PyTuple_Pack(2, tables, nlens);
 end:
   Py_XDECREF(tables);
@@ -429,11 +513,12 @@ end:
   return res;
 }
 
-/* (path of libpkv, torch, PkvError, torch.cuda.current_device, function from a device to its raw stream) */
+/* (path of libpkv, torch, PkvError, torch.cuda.current_device, a function from a device to its raw stream, one that tells
+ * whether the current stream is captured) */
 static PyObject* py_setup(PyObject* self, PyObject* args) {
   const char* path;
   PyObject* torch;
-  if (!PyArg_ParseTuple(args, "sOOOO", &path, &torch, &T.error, &T.current_device, &T.raw_stream)) return NULL;
+  if (!PyArg_ParseTuple(args, "sOOOOO", &path, &torch, &T.error, &T.current_device, &T.raw_stream, &T.capturing)) return NULL;
   void* h = dlopen(path, RTLD_NOW | RTLD_LOCAL);
   if (!h) {
     PyErr_SetString(PyExc_ImportError, dlerror());
@@ -455,6 +540,8 @@ static PyObject* py_setup(PyObject* self, PyObject* args) {
   Py_INCREF(T.error);
   Py_INCREF(T.current_device);
   Py_INCREF(T.raw_stream);
+  Py_INCREF(T.capturing);
+  if (!(T.results = PyDict_New()) || !(T.scratch = PyDict_New())) return NULL;
   if (!(T.empty = PyObject_GetAttrString(torch, "empty")) || !(T.i32 = PyObject_GetAttrString(torch, "int32")) ||
       !(T.i64 = PyObject_GetAttrString(torch, "int64")) || !(T.f32 = PyObject_GetAttrString(torch, "float32")) ||
       !(T.bf16 = PyObject_GetAttrString(torch, "bfloat16")) || !(T.u8 = PyObject_GetAttrString(torch, "uint8")) ||
@@ -469,6 +556,7 @@ static PyObject* py_setup(PyObject* self, PyObject* args) {
   T.s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
   T.s_record_stream = PyUnicode_InternFromString("record_stream");
   T.s_view = PyUnicode_InternFromString("view");
+  T.s_unbind = PyUnicode_InternFromString("unbind");
   T.kw_empty = Py_BuildValue("(ss)", "dtype", "device");
   Py_RETURN_NONE;
 }

@@ -691,3 +691,59 @@ def test_beam_search_over_the_paged_cache(pkv):
     # every block is held by as many rows as name it
     t = tg.cpu().numpy()
     assert np.array_equal(np.bincount(t[t >= 0], minlength=pool), rg.cpu().numpy())
+
+
+def test_results_are_handed_out_once_and_scratch_is_per_stream(pkv):
+    """Small results come from a store of ready parts and scratch is kept per stream: results of many
+    calls stay distinct, and calls on several streams at once do not disturb one another."""
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    xs = [torch.randn((2, 3, 5000), generator=gen, device="cuda") for _ in range(4)]
+    cum = torch.randn((2, 3), generator=gen, device="cuda")
+    want = [pkv.pkv_beam_select(x, cum, 6) for x in xs]
+    flat = [t for w in want for t in w]
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in flat)
+    assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+    many = [pkv.pkv_beam_select(xs[i % 4], cum, 6) for i in range(100)]
+    assert len({t.data_ptr() for m in many for t in m}) == 300
+    for i, m in enumerate(many):
+        assert all(torch.equal(a, b) for a, b in zip(m, want[i % 4]))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [[] for _ in xs]
+    for _ in range(50):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(pkv.pkv_beam_select(xs[i], cum, 6))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(a, b) for m in g for a, b in zip(m, w))
+    # a graph keeps its own memory: replays after other calls, and the other way round
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        held = pkv.pkv_beam_select(xs[0], cum, 6)
+    for _ in range(3):
+        others = [pkv.pkv_beam_select(xs[1], cum, 6) for _ in range(40)]
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, want[0]))
+        assert all(torch.equal(a, b) for m in others for a, b in zip(m, want[1]))
+
+
+def test_calls_from_several_threads(pkv):
+    import threading
+    x = torch.randn(2, 3, 5000, device="cuda")
+    cum = torch.randn(2, 3, device="cuda")
+    want = pkv.pkv_beam_select(x, cum, 6)
+    bad = []
+
+    def work():
+        for _ in range(200):  # all on one stream
+            got = pkv.pkv_beam_select(x, cum, 6)
+            if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                bad.append(1)
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
