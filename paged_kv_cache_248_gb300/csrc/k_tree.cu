@@ -6,6 +6,7 @@
 // over those keys alone, with the softmax's running maximum and sum in fp32.  Keys that are
 // not seen are never multiplied with anything, so whatever they hold stays out.
 #include "pkv_internal.cuh"
+#include "ptx.cuh"
 
 namespace pkv {
 namespace {
@@ -58,133 +59,427 @@ __global__ void __launch_bounds__(128) tree_mask_kernel(const int32_t* __restric
 }
 
 // ------------------------------------------------------------------ CUDA-core attention
-// One CTA per (drafted token, kv head, chunk of up to 8 of its query heads); each warp takes
-// every fourth seen key and keeps its own online-softmax state, and the four are merged at
-// the end.  Lane l owns head_dim / 32 consecutive elements.
-constexpr int kTreeThreads = 128;
-constexpr int kTreeWarps = kTreeThreads / 32;
-constexpr int kHeadChunk = 8;
+// The G query heads of a kv head and the nodes of a request are rows (node * G + head), 32 to a
+// unit; a unit goes over the request's key tiles of 64 keys, K and V of which are staged in
+// shared memory once for all its rows.  A thread owns 4 rows with 4 keys of the scores, and the
+// same 4 rows with D / 16 columns of the result, so that the 16 threads of a row keep its
+// maximum, sum and result in registers from tile to tile.  All units' key tiles, one after the
+// other, are cut into equal runs, one per CTA; a unit that is cut leaves partials (accumulator,
+// maximum, sum) that the merge kernel joins in the order of the keys.
+//
+// Bound: latency for few requests, fp32 FMAs for many.
+constexpr int kRows = 32;      // rows of a unit
+constexpr int kKeys = 64;      // keys of a tile
+constexpr int kThreads = 128;
+constexpr int kCtasPerSm = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kTreeThreads) tree_attention_kernel(const TreeArgs A, int64_t num_blocks, int hkv,
-                                                                      float scale_log2, uint32_t* err) {
-  constexpr int E = D / 32;
-  __shared__ int bad;
-  __shared__ float sm_m[kTreeWarps][kHeadChunk], sm_l[kTreeWarps][kHeadChunk];
-  __shared__ float sm_o[kTreeWarps][kHeadChunk][D];
-  grid_dep_wait();
-  grid_dep_launch();
-  const T* q = static_cast<const T*>(A.a.q);
-  const T* kc = static_cast<const T*>(A.a.k_cache);
-  const T* vc = static_cast<const T*>(A.a.v_cache);
-  T* out = static_cast<T*>(A.a.out);
-  const int hq = A.a.num_q_heads, group = hq / hkv;
-  const int nchunks = (group + kHeadChunk - 1) / kHeadChunk;
-  int64_t bid = blockIdx.x;
-  const int chunk = static_cast<int>(bid % nchunks);
-  bid /= nchunks;
-  const int g = static_cast<int>(bid % hkv);
-  const int64_t t = bid / hkv;
-  const int h0 = g * group + chunk * kHeadChunk;
-  const int nh = min(kHeadChunk, group - chunk * kHeadChunk);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int i = find_seq(A.a.qsl, A.a.num_seqs, t);
-  const int64_t q0 = __ldg(A.a.qsl + i), q1 = __ldg(A.a.qsl + i + 1);
-  const int64_t L = __ldg(A.a.seq_lens + i);
-  const int64_t ctx = L - (q1 - q0);
-  const bool len_ok = t >= q0 && t < q1 && ctx >= 0 && (L + kBlock - 1) / kBlock <= A.a.max_blocks &&
-                      q1 - q0 <= A.a.max_query_len;
-  if (threadIdx.x == 0) {
-    bad = len_ok ? 0 : 1;
-    if (!len_ok) flag_error(err, kErrLength);
-  }
-  __syncthreads();
-  float qr[kHeadChunk][E], m[kHeadChunk], l[kHeadChunk], o[kHeadChunk][E];
-#pragma unroll
-  for (int hh = 0; hh < kHeadChunk; ++hh) {
-    m[hh] = -INFINITY;
-    l[hh] = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      o[hh][e] = 0.f;
-      qr[hh][e] = hh < nh ? Elem<T>::to_f32(q[(t * hq + h0 + hh) * D + lane * E + e]) : 0.f;
+struct Cut32 {
+  int32_t parts;  // runs that hold a part of the unit, 0: none
+  int32_t t0, row0, rows, head;
+  int32_t pad[3];
+};
+
+struct Params32 {
+  TreeArgs a;
+  uint32_t* err;
+  float* part_o;   // [2 * runs][kRows][D]
+  float* part_ml;  // [2 * runs][kRows][2]
+  Cut32* cuts;     // [runs]
+  int32_t hkv, group;
+  float scale_log2;
+};
+
+struct Request32 {
+  int32_t t0, q_len, len, tiles, units, cost;
+  bool wrong;
+};
+
+__device__ __forceinline__ Request32 request_of(const Params32& P, int i) {
+  const AttnArgs& A = P.a.a;
+  Request32 r;
+  const int32_t q0 = __ldg(A.qsl + i), q1 = __ldg(A.qsl + i + 1), len = __ldg(A.seq_lens + i);
+  const int64_t n = static_cast<int64_t>(q1) - q0;
+  const bool rows = n > 0 && q0 >= 0 && q1 <= A.num_tokens;
+  bool fits = rows && len >= n && n <= A.max_query_len && (static_cast<int64_t>(len) + kBlock - 1) / kBlock <= A.max_blocks;
+  r.t0 = q0;
+  r.q_len = rows ? static_cast<int32_t>(n) : 0;
+  r.len = len;
+  r.tiles = static_cast<int>(static_cast<uint32_t>(len - 1) / kKeys) + 1;
+  const int64_t units = (static_cast<int64_t>(r.q_len) * P.group + kRows - 1) / kRows;
+  const int64_t cost = units * P.hkv * r.tiles;
+  fits = fits && cost < (int64_t(1) << 31);  // (more would be terabytes of K and V, read once a unit)
+  r.units = static_cast<int32_t>(units);
+  r.cost = fits ? static_cast<int32_t>(cost) : 0;
+  r.wrong = rows && !fits;
+  return r;
+}
+
+// One tile's rows (K or V) into shared memory, rows past the context as zeros.
+template <int D>
+__device__ __forceinline__ void stage_tile(float* dst, const float* src, const int32_t* ids, int k0, int len, int head, int hkv) {
+  constexpr int kVecs = D / 4;
+  for (int v = threadIdx.x; v < kKeys * kVecs; v += kThreads) {
+    const int key = v / kVecs, c = v % kVecs;
+    float* to = dst + key * (D + 4) + 4 * c;
+    if (k0 + key < len) {
+      const float* from = src + ((static_cast<int64_t>(ids[key / kBlock]) * hkv + head) * kBlock + key % kBlock) * D + 4 * c;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+    } else {
+      *reinterpret_cast<float4*>(to) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
-  const int32_t* row = A.a.block_tables + static_cast<int64_t>(i) * A.a.max_blocks;
-  const uint64_t* mrow = A.mask + t * A.mask_words;
-  for (int64_t u = warp; u < (len_ok ? L : 0); u += kTreeWarps) {
-    const int32_t b = __ldg(row + u / kBlock);
-    if (b < 0 || b >= num_blocks) {
-      if (lane == 0) {
-        flag_error(err, kErrBlockId);
-        bad = 1;
+  cp_async_commit();
+}
+
+// The result's 4 rows += P V over a tile; kDrafted: keys of weight 0 are left out, whatever V holds.
+template <int D, bool kDrafted>
+__device__ __forceinline__ void add_pv(float (&o)[4][D / 16], const float* sp, const float* sv, int rg, int cg) {
+  constexpr int C = D / 16;
+#pragma unroll 2
+  for (int u = 0; u < kKeys; u += 4) {
+    float4 p[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) p[r] = *reinterpret_cast<const float4*>(sp + (4 * rg + r) * (kKeys + 4) + u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float v[C];
+#pragma unroll
+      for (int c = 0; c < C; c += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(sv + (u + e) * (D + 4) + 64 * (c / 4) + 4 * cg);
+        v[c] = x.x;
+        v[c + 1] = x.y;
+        v[c + 2] = x.z;
+        v[c + 3] = x.w;
       }
-      break;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float w = e == 0 ? p[r].x : e == 1 ? p[r].y : e == 2 ? p[r].z : p[r].w;
+        if (!kDrafted || !(w == 0.f)) {
+#pragma unroll
+          for (int c = 0; c < C; ++c) o[r][c] = fmaf(w, v[c], o[r][c]);
+        }
+      }
     }
-    if (u >= ctx && !(__ldg(mrow + (u - ctx) / 64) >> ((u - ctx) % 64) & 1)) continue;
-    const int64_t off = ((static_cast<int64_t>(b) * hkv + g) * kBlock + u % kBlock) * D + lane * E;
-    float kf[E], vf[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      kf[e] = Elem<T>::to_f32(kc[off + e]);
-      vf[e] = Elem<T>::to_f32(vc[off + e]);
-    }
-#pragma unroll
-    for (int hh = 0; hh < kHeadChunk; ++hh) {
-      if (hh >= nh) break;
-      float dot = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) dot = fmaf(qr[hh][e], kf[e], dot);
-#pragma unroll
-      for (int sh = 16; sh > 0; sh >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, sh);
-      const float s = dot * scale_log2;
-      const float m_new = fmaxf(m[hh], s);
-      const float m_use = m_new == -INFINITY ? 0.f : m_new;  // nothing but -inf so far: weight 0
-      const float alpha = exp2f(m[hh] - m_use);
-      const float pr = exp2f(s - m_use);
-      l[hh] = l[hh] * alpha + pr;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[hh][e] = fmaf(o[hh][e], alpha, pr * vf[e]);
-      m[hh] = m_new;
-    }
-  }
-#pragma unroll
-  for (int hh = 0; hh < kHeadChunk; ++hh) {
-    if (lane == 0) {
-      sm_m[warp][hh] = m[hh];
-      sm_l[warp][hh] = l[hh];
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) sm_o[warp][hh][lane * E + e] = o[hh][e];
-  }
-  __syncthreads();
-  const bool zero = bad != 0;
-  for (int idx = threadIdx.x; idx < nh * D; idx += kTreeThreads) {
-    const int hh = idx / D, c = idx % D;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kTreeWarps; ++w) M = fmaxf(M, sm_m[w][hh]);
-    const float m_use = M == -INFINITY ? 0.f : M;
-    float den = 0.f, num = 0.f;
-#pragma unroll
-    for (int w = 0; w < kTreeWarps; ++w) {
-      const float f = exp2f(sm_m[w][hh] - m_use);
-      den = fmaf(sm_l[w][hh], f, den);
-      num = fmaf(sm_o[w][hh][c], f, num);
-    }
-    out[(t * hq + h0 + hh) * D + c] = Elem<T>::from_f32(zero || den == 0.f ? 0.f : num / den);
   }
 }
 
-template <typename T, int D>
-int launch_typed(const TreeArgs& t, uint32_t* err, cudaStream_t s) {
-  const int hkv = t.a.cache.num_kv_heads;
-  const int nchunks = (t.a.num_q_heads / hkv + kHeadChunk - 1) / kHeadChunk;
-  const int64_t blocks = t.a.num_tokens * hkv * nchunks;
-  if (blocks > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
-  return cuda_status(launch_k(tree_attention_kernel<T, D>, dim3(static_cast<unsigned>(blocks)), dim3(kTreeThreads), 0,
-                              s, t, t.a.cache.num_blocks, hkv, t.a.scale * kLog2e, err));
+template <int D>
+constexpr int kSmem32 = (kRows * (D + 4) + 2 * kKeys * (D + 4) + kRows * (kKeys + 4)) * static_cast<int>(sizeof(float));
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_f32_kernel(const Params32 P) {
+  constexpr int C = D / 16;  // result columns of a thread
+  extern __shared__ __align__(16) float smem[];
+  float* sq = smem;
+  float* sk = sq + kRows * (D + 4);
+  float* sv = sk + kKeys * (D + 4);
+  float* sp = sv + kKeys * (D + 4);
+  __shared__ int64_t s_sum[kThreads / 32], s_base;
+  __shared__ int32_t s_seq, s_ids[2][kKeys / kBlock], s_bad;
+  const AttnArgs& A = P.a.a;
+  const float* q = static_cast<const float*>(A.q);
+  const float* kc = static_cast<const float*>(A.k_cache);
+  const float* vc = static_cast<const float*>(A.v_cache);
+  float* out = static_cast<float*>(A.out);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cg = tid & 15, rg = tid >> 4;
+  grid_dep_wait();
+  grid_dep_launch();
+  // this CTA's run of key tiles
+  const int per = (A.num_seqs + kThreads - 1) / kThreads;
+  const int i0 = min(tid * per, A.num_seqs), i1 = min(i0 + per, A.num_seqs);
+  int64_t mine = 0;
+  bool wrong = false;
+  for (int i = i0; i < i1; ++i) {
+    const Request32 r = request_of(P, i);
+    mine += r.cost;
+    wrong |= r.wrong;
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += y;
+  }
+  if (lane == 31) s_sum[warp] = incl;
+  if (tid == 0) s_seq = 0;
+  const bool any_wrong = __syncthreads_or(wrong);
+  int64_t before = incl - mine, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
+  }
+  const int64_t run = (total + gridDim.x - 1) / gridDim.x;
+  int64_t pos = run * blockIdx.x;
+  const int64_t end = min(total, pos + run);
+  if (pos >= before && pos < before + mine) {
+    int64_t at = before;
+    for (int i = i0; i < i1; ++i) {
+      const int cost = request_of(P, i).cost;
+      if (pos < at + cost) {
+        s_seq = i;
+        s_base = at;
+        break;
+      }
+      at += cost;
+    }
+  }
+  if (any_wrong) {  // rows of requests whose lengths do not fit are zero
+    for (int i = blockIdx.x; i < A.num_seqs; i += gridDim.x) {
+      const Request32 r = request_of(P, i);
+      if (!r.wrong) continue;
+      if (tid == 0) flag_error(P.err, kErrLength);
+      const int64_t n = static_cast<int64_t>(r.q_len) * A.num_q_heads * D;
+      for (int64_t e = tid; e < n; e += kThreads) out[static_cast<int64_t>(r.t0) * A.num_q_heads * D + e] = 0.f;
+    }
+  }
+  if (tid == 0) P.cuts[blockIdx.x].parts = 0;
+  __syncthreads();
+  int seq = s_seq;
+  int64_t base = pos < end ? s_base : 0;
+  while (pos < end) {
+    const Request32 rq = request_of(P, seq);
+    if (pos >= base + rq.cost) {
+      base += rq.cost;
+      if (++seq >= A.num_seqs) break;  // (lengths that changed meanwhile)
+      continue;
+    }
+    const uint32_t off = static_cast<uint32_t>(pos - base);
+    const int unit = static_cast<int>(off / rq.tiles), first = static_cast<int>(off - unit * rq.tiles);
+    const int nt = static_cast<int>(min(static_cast<int64_t>(rq.tiles - first), end - pos));
+    pos += nt;
+    const int head = unit / rq.units, row0 = (unit - head * rq.units) * kRows;
+    const int rows = min(kRows, rq.q_len * P.group - row0), ctx = rq.len - rq.q_len;
+    const int slot = nt == rq.tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (first == 0 ? 1 : 0);
+    if (slot >= 0 && first == 0 && tid == 0) {
+      const int rest = rq.tiles - nt, len = static_cast<int>(min(run, int64_t(0x7fffffff)));
+      P.cuts[blockIdx.x] = Cut32{1 + (rest + len - 1) / len, rq.t0, row0, rows, head, {0, 0, 0}};
+    }
+    const int32_t* btrow = A.block_tables + static_cast<int64_t>(seq) * A.max_blocks;
+    // ids of the first tile; Q rows
+    auto load_ids = [&](int tile, int slot2) {
+      if (tid < kKeys / kBlock) {
+        const int blk = tile * (kKeys / kBlock) + tid;
+        int id = 0;
+        if (blk * kBlock < rq.len) {
+          id = __ldg(btrow + blk);
+          if (id < 0 || id >= A.cache.num_blocks) {
+            flag_error(P.err, kErrBlockId);
+            s_bad = 1;
+            id = 0;
+          }
+        }
+        s_ids[slot2][tid] = id;
+      }
+    };
+    if (tid == 0) s_bad = 0;
+    __syncthreads();
+    load_ids(first, 0);
+    for (int v = tid; v < kRows * D / 4; v += kThreads) {
+      const int r = v / (D / 4), c = v % (D / 4), row = row0 + r;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < rows)
+        x = __ldg(reinterpret_cast<const float4*>(
+                      q + ((static_cast<int64_t>(rq.t0) + row / P.group) * A.num_q_heads + head * P.group + row % P.group) * D) + c);
+      *reinterpret_cast<float4*>(sq + r * (D + 4) + 4 * c) = x;
+    }
+    __syncthreads();
+    stage_tile<D>(sk, kc, s_ids[0], first * kKeys, rq.len, head, P.hkv);
+    stage_tile<D>(sv, vc, s_ids[0], first * kKeys, rq.len, head, P.hkv);
+    float m[4], l[4], o[4][C];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) o[r][c] = 0.f;
+    }
+    for (int j = 0; j < nt; ++j) {
+      const int k0 = (first + j) * kKeys;
+      const bool drafted = k0 + kKeys > ctx;
+      if (j + 1 < nt) load_ids(first + j + 1, (j + 1) & 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");  // K has landed
+      __syncthreads();
+      // scores of 4 rows and keys cg, cg + 16, cg + 32, cg + 48
+      float s[4][4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[r][e] = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < D; d += 4) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) a[r] = *reinterpret_cast<const float4*>(sq + (4 * rg + r) * (D + 4) + d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[e] = *reinterpret_cast<const float4*>(sk + (cg + 16 * e) * (D + 4) + d);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[r][e] = fmaf(a[r].w, b[e].w, fmaf(a[r].z, b[e].z, fmaf(a[r].y, b[e].y, fmaf(a[r].x, b[e].x, s[r][e]))));
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint64_t* mrow = P.a.mask + (static_cast<int64_t>(rq.t0) + (row0 + min(4 * rg + r, rows - 1)) / P.group) * P.a.mask_words;
+        float top = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int u = k0 + cg + 16 * e - ctx;  // below 0: context
+          const bool seen = !drafted || u < 0 || (u < rq.q_len && (__ldg(mrow + u / 64) >> (u % 64) & 1));
+          s[r][e] = seen ? s[r][e] * P.scale_log2 : -INFINITY;
+          top = fmaxf(top, s[r][e]);
+        }
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float m_new = fmaxf(m[r], top);
+        const float m_use = m_new == -INFINITY ? 0.f : m_new;  // a row that has seen nothing yet: weights 0
+        const float alpha = exp2f(m[r] - m_use);
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p = exp2f(s[r][e] - m_use);
+          sum += p;
+          sp[(4 * rg + r) * (kKeys + 4) + cg + 16 * e] = p;
+        }
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        l[r] = l[r] * alpha + sum;
+        m[r] = m_new;
+#pragma unroll
+        for (int c = 0; c < C; ++c) o[r][c] *= alpha;
+      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");  // V has landed
+      __syncthreads();
+      if (j + 1 < nt) stage_tile<D>(sk, kc, s_ids[(j + 1) & 1], k0 + kKeys, rq.len, head, P.hkv);
+      if (drafted) add_pv<D, true>(o, sp, sv, rg, cg);
+      else add_pv<D, false>(o, sp, sv, rg, cg);
+      __syncthreads();
+      if (j + 1 < nt) stage_tile<D>(sv, vc, s_ids[(j + 1) & 1], k0 + kKeys, rq.len, head, P.hkv);
+    }
+    const bool bad = s_bad != 0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 4 * rg + r;
+      if (row >= rows) continue;
+      float* dst;
+      float f = 1.f;
+      if (slot < 0) {
+        const int at = row0 + row;
+        dst = out + ((static_cast<int64_t>(rq.t0) + at / P.group) * A.num_q_heads + head * P.group + at % P.group) * D;
+        f = l[r] == 0.f ? 0.f : 1.f / l[r];
+      } else {
+        const int64_t prow = static_cast<int64_t>(slot) * kRows + row;
+        dst = P.part_o + prow * D;
+        if (cg == 0) {
+          P.part_ml[2 * prow] = m[r];
+          P.part_ml[2 * prow + 1] = bad ? -1.f : l[r];
+        }
+      }
+      const bool zero = slot < 0 && (bad || l[r] == 0.f);
+#pragma unroll
+      for (int c = 0; c < C; c += 4)
+        *reinterpret_cast<float4*>(dst + 64 * (c / 4) + 4 * cg) =
+            zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[r][c] * f, o[r][c + 1] * f, o[r][c + 2] * f, o[r][c + 3] * f);
+    }
+    __syncthreads();
+  }
+}
+
+// One warp per row of a cut unit: the parts' weights 2^(m - M), then the weighted sum of their
+// accumulators in the order of the keys.
+template <int D>
+__global__ void __launch_bounds__(256) tree_f32_merge_kernel(const Params32 P) {
+  constexpr int E = D / 32;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int4* rec = reinterpret_cast<const int4*>(P.cuts + blockIdx.x);
+  int4 c = __ldcg(rec);  // parts, t0, row0, rows
+  c.x = min(c.x, static_cast<int>(gridDim.x - blockIdx.x));
+  const int head = __ldcg(rec + 1).x;
+  const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (c.x < 2 || row >= c.w) return;
+  auto part_row = [&](int p) -> int64_t {
+    return (p == 0 ? 2 * static_cast<int64_t>(blockIdx.x) + 1 : 2 * (static_cast<int64_t>(blockIdx.x) + p)) * kRows + row;
+  };
+  float M = -INFINITY;
+  bool bad = false, nan = false;
+  for (int p = lane; p < c.x; p += 32) {
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(P.part_ml) + part_row(p));
+    nan |= isnan(ml.x);
+    bad |= ml.y == -1.f;
+    M = fmaxf(M, ml.x);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  bad = __any_sync(0xffffffffu, bad);
+  if (__any_sync(0xffffffffu, nan)) M = __int_as_float(0x7fffffff);
+  float den = 0.f, acc[E] = {};
+  for (int p = 0; p < c.x; ++p) {
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(P.part_ml) + part_row(p));
+    // (a part without a maximum saw nothing, or nothing but NaN, which its sum says)
+    const float w = ml.x == -INFINITY ? ml.y * 0.f : exp2f(ml.x - M);
+    const float* o = P.part_o + part_row(p) * D + lane * E;
+    float x[E];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 y = __ldcg(reinterpret_cast<const float2*>(o + e));
+      x[e] = y.x;
+      x[e + 1] = y.y;
+    }
+    if (!(w == 0.f)) {
+      den = fmaf(ml.y, w, den);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(x[e], w, acc[e]);
+    }
+  }
+  const bool zero = bad || den == 0.f;
+  const float inv = zero ? 0.f : 1.f / den;
+  const int at = c.z + row;
+  float* dst = static_cast<float*>(P.a.a.out) +
+               ((static_cast<int64_t>(c.y) + at / P.group) * P.a.a.num_q_heads + head * P.group + at % P.group) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) dst[e] = zero ? 0.f : acc[e] * inv;
+}
+
+struct Layout32 {
+  size_t o_bytes, ml_bytes, bytes;
+};
+Layout32 layout32(int d, int num_sms) {
+  const size_t runs = static_cast<size_t>(kCtasPerSm) * num_sms, rows = 2 * runs * kRows;
+  Layout32 l;
+  l.o_bytes = rows * d * sizeof(float);
+  l.ml_bytes = (rows * 2 * sizeof(float) + 255) & ~static_cast<size_t>(255);
+  l.bytes = l.o_bytes + l.ml_bytes + runs * sizeof(Cut32);
+  return l;
+}
+
+template <int D>
+int launch_f32(const TreeArgs& t, void* workspace, int num_sms, uint32_t* err, cudaStream_t s) {
+  const AttnArgs& a = t.a;
+  const Layout32 l = layout32(D, num_sms);
+  Params32 p{};
+  p.a = t;
+  p.err = err;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + l.o_bytes);
+  p.cuts = reinterpret_cast<Cut32*>(static_cast<uint8_t*>(workspace) + l.o_bytes + l.ml_bytes);
+  p.hkv = a.cache.num_kv_heads;
+  p.group = a.num_q_heads / p.hkv;
+  p.scale_log2 = a.scale * kLog2e;
+  // CTAs: kCtasPerSm per SM, fewer where the caller's bounds leave less to do
+  const int64_t most = static_cast<int64_t>(kCtasPerSm) * num_sms;
+  const int64_t units = (static_cast<int64_t>(a.max_query_len) * p.group + kRows - 1) / kRows * p.hkv;
+  const int64_t tiles = units * ((static_cast<int64_t>(a.max_seq_len) + kKeys - 1) / kKeys);
+  const int64_t want = tiles >= most ? most : tiles * a.num_seqs;
+  const int ctas = static_cast<int>(want < 1 ? 1 : want < most ? want : most);
+  static uint64_t smem_set = 0;
+  int st = set_smem_once(reinterpret_cast<const void*>(tree_f32_kernel<D>), kSmem32<D>, &smem_set);
+  if (st) return st;
+  st = cuda_status(launch_k(tree_f32_kernel<D>, dim3(ctas), dim3(kThreads), kSmem32<D>, s, p));
+  if (st) return st;
+  return cuda_status(launch_k(tree_f32_merge_kernel<D>, dim3(ctas, kRows / 8), dim3(256), 0, s, p));
 }
 
 }  // namespace
@@ -198,12 +493,14 @@ int launch_tree_mask(const int32_t* parents, const int32_t* qsl, int32_t num_seq
 }
 
 size_t tree_workspace(const pkv_cache_desc& c, int32_t num_q_heads, int32_t max_query_len, int num_sms) {
-  return c.dtype == PKV_BF16 ? tree_tc_workspace(num_q_heads / c.num_kv_heads, max_query_len, num_sms) : 256;
+  return c.dtype == PKV_BF16 ? tree_tc_workspace(num_q_heads / c.num_kv_heads, max_query_len, num_sms)
+                             : layout32(c.head_dim, num_sms).bytes;
 }
 
 int launch_tree_attention(const TreeArgs& t, void* workspace, int num_sms, uint32_t* err, cudaStream_t s) {
   if (t.a.cache.dtype == PKV_BF16) return launch_tree_tc(t, workspace, num_sms, err, s);
-  return t.a.cache.head_dim == 64 ? launch_typed<float, 64>(t, err, s) : launch_typed<float, 128>(t, err, s);
+  return t.a.cache.head_dim == 64 ? launch_f32<64>(t, workspace, num_sms, err, s)
+                                  : launch_f32<128>(t, workspace, num_sms, err, s);
 }
 
 }  // namespace pkv
