@@ -51,6 +51,18 @@ __device__ __forceinline__ double from_ordered_bits(uint64_t o) {
   return __longlong_as_double(static_cast<long long>((o >> 63) ? o & ~(uint64_t(1) << 63) : ~o));
 }
 
+// sum + lost += x, where lost gathers what the rounding of sum leaves out.
+__device__ __forceinline__ void two_sum(float& sum, float& lost, float x) {
+  const float s = __fadd_rn(sum, x), back = __fsub_rn(s, sum);
+  lost += __fadd_rn(__fsub_rn(sum, __fsub_rn(s, back)), __fsub_rn(x, back));
+  sum = s;
+}
+// The largest of the warp's values (NaN does not count).
+__device__ __forceinline__ float max_over_warp(float x) {
+  const uint32_t top = __reduce_max_sync(0xffffffffu, x > -INFINITY ? ordered_bits(x) : 0);
+  return top ? from_ordered_bits(top) : -INFINITY;
+}
+
 // A collected candidate: its score in the order-preserving form, then the complement of its
 // index (both larger is better; no two candidates are equal).
 struct Cand {
@@ -71,29 +83,49 @@ struct Cands {
   }
 };
 
-// The largest t that at least `need` of the threads' counts-above reach: with count(t) how many
-// of a thread's values are t or more, the largest t whose counts sum to `need` or more (0: none).
-// One bit of t at a time; it ends early where the sum is `need` exactly.
-template <typename F>
-__device__ uint32_t reached_by(int* s_sum, int need, F&& count) {
+// The largest t that `need` or more of the threads' values reach (0: none).  Four bits of t at
+// a time: a value counts for as many of the 15 thresholds above t as it reaches, in bytes of four
+// words.  It ends early where the count is `need` exactly.  s_sum: 48 counters, of which a turn
+// uses a third and clears the next one's.
+template <int kValues>
+__device__ uint32_t reached_by(int* s_sum, int need, const uint32_t (&v)[kValues]) {
+  static_assert(kValues < 8, "a warp's counts fit into bytes");
+  const int lane = threadIdx.x & 31;
   uint32_t t = 0;
-  if (threadIdx.x < 2) s_sum[threadIdx.x] = 0;
+  if (threadIdx.x < 16) s_sum[threadIdx.x] = 0;
   __syncthreads();
+  int* now = s_sum;
 #pragma unroll 1
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t u = t | 1u << bit;
-    const int mine = __reduce_add_sync(0xffffffffu, count(u));
-    int* sum = s_sum + (bit & 1);
-    if ((threadIdx.x & 31) == 0 && mine > 0) atomicAdd(sum, mine);
-    __syncthreads();
-    const int all = *sum;
-    if (threadIdx.x == 0) s_sum[(bit & 1) ^ 1] = 0;  // the next round's
-    __syncthreads();
-    if (all >= need) {
-      t = u;
-      if (all == need) break;
+  for (int shift = 28; shift >= 0; shift -= 4) {
+    int* next = now == s_sum + 32 ? s_sum : now + 16;
+    if (threadIdx.x < 16) next[threadIdx.x] = 0;
+    uint32_t words[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < kValues; ++j) {
+      const uint32_t a = v[j] >> shift, b = t >> shift;
+      const int d = a > b ? static_cast<int>(min(a - b, 15u)) : 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)  // min(max(d - 4 k, 0), 4) bytes of 1
+        words[k] += __funnelshift_rc(0x01010101u, 0, 8 * max(0, 4 - max(d - 4 * k, 0)));
     }
+    uint32_t mine = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t all = __reduce_add_sync(0xffffffffu, words[k]);
+      if (lane >> 2 == k) mine = all >> (8 * (lane & 3)) & 255;
+    }
+    if (lane < 15 && mine > 0) atomicAdd(now + lane, static_cast<int>(mine));  // values that reach t + (lane + 1) 2^shift
+    __syncthreads();
+    const int all = lane < 15 ? now[lane] : 0;
+    const uint32_t reach = __ballot_sync(0xffffffffu, all >= need);
+    if (reach) {
+      const int digit = 32 - __clz(reach);
+      t += static_cast<uint32_t>(digit) << shift;
+      if (__shfl_sync(0xffffffffu, all, digit - 1) == need) break;
+    }
+    now = next;
   }
+  __syncthreads();
   return t;
 }
 
@@ -112,12 +144,7 @@ __device__ int cut(Cands& buf, int* ranks, int n, int k) {
       mine[j] = i < n ? buf.get(i) : Cand{0, 0};
       top[j] = static_cast<uint32_t>(mine[j].hi >> 32);
     }
-    const uint32_t least = reached_by(ranks, k, [&](uint32_t t) {
-      int c = 0;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) c += top[j] >= t ? 1 : 0;
-      return c;
-    });
+    const uint32_t least = reached_by(ranks, k, top);
     if (threadIdx.x == 0) ranks[0] = 0;
     __syncthreads();
 #pragma unroll
@@ -267,8 +294,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : kResident) scan
     const T* x = static_cast<const T*>(P.logits) + row * P.row_stride + at;
     load_values<T, kAligned>(c, x, P.vocab - at);
     const float top = max_of(c);
-    const uint32_t warp_top = __reduce_max_sync(0xffffffffu, top > -INFINITY ? ordered_bits(top) : 0);
-    const float m = warp_top ? from_ordered_bits(warp_top) : -INFINITY;
+    const float m = max_over_warp(top);
     float a0 = 0.f, a1 = 0.f;
     if (fabsf(m) < 1e30f) {
       // 2^(x c - r) with r = m c rounded; what the rounding left, m c - r, is put right in the
@@ -282,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : kResident) scan
         fadd2(a0, a1, ex2_approx(ya), ex2_approx(yb));
       }
       a0 = (a0 + a1) * exp2f(fmaf(-m, kLog2e, r));
-    } else if (warp_top) {  // values that times log2(e) may not be finite (a type's lowest value)
+    } else if (m > -INFINITY) {  // values that times log2(e) may not be finite (a type's lowest value)
 #pragma unroll 1
       for (int k = 0; k < kVals; ++k) {
         const int i = index_of<T, kAligned>(k);
@@ -314,17 +340,17 @@ template <typename F>
 __device__ int best_of(Cands& buf, int* s_rank, int* s_count, int total, int select, F&& cand) {
   constexpr int kKeep = 2;  // candidates that a thread keeps in registers
   Cand kept[kKeep];
-  uint32_t best = 0;
+  uint32_t best[1] = {0};
 #pragma unroll
   for (int j = 0; j < kKeep; ++j) {
     const int i = threadIdx.x + j * kSelThreads;
     kept[j] = i < total ? cand(i) : Cand{0, 0};
-    best = max(best, static_cast<uint32_t>(kept[j].hi >> 32));
+    best[0] = max(best[0], static_cast<uint32_t>(kept[j].hi >> 32));
   }
   for (int i = threadIdx.x + kKeep * kSelThreads; i < total; i += kSelThreads)
-    best = max(best, static_cast<uint32_t>(cand(i).hi >> 32));
+    best[0] = max(best[0], static_cast<uint32_t>(cand(i).hi >> 32));
   if (threadIdx.x == 0) *s_count = 0;
-  const uint32_t least = reached_by(s_rank, select, [&](uint32_t t) { return best >= t ? 1 : 0; });
+  const uint32_t least = reached_by(s_rank, select, best);
   Cand floor_c{least > 0 ? (static_cast<uint64_t>(least) << 32) - 1 : 0, 0xffffffffu};
 #pragma unroll 1
   for (int base = 0; base < total; base += kKeep * kSelThreads) {
@@ -350,7 +376,9 @@ __device__ int best_of(Cands& buf, int* s_rank, int* s_count, int total, int sel
 
 template <typename T, bool kAligned>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelParams P) {
-  __shared__ double s_lse[kMaxBeams], s_cum[kMaxBeams];
+  __shared__ double s_off[kMaxBeams];  // what a row's values score besides themselves; not finite: it has no candidates
+  __shared__ float s_top[kMaxBeams], s_log[kMaxBeams], s_least[kMaxBeams];
+  __shared__ int s_exp[kMaxBeams];
   __shared__ uint8_t s_done[kMaxBeams];
   __shared__ Cands buf;
   __shared__ uint32_t s_blocks[64];
@@ -360,51 +388,71 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelParams P) 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
   grid_dep_launch();
-  // a warp per beam joins its sums
+  // A warp per beam joins its sums, each with what its rounding lost beside it.
   for (int w = warp; w < W; w += kSelWarps) {
     const int64_t row = n * W + w;
     const bool done = P.scan.finished != nullptr && __ldg(P.scan.finished + row) != 0;
     const float2* sums = P.scan.sums + row * per_row;
-    float m = -INFINITY;
-    double sum = 0.0;
+    float m = -INFINITY, sum = 0.f, lost = 0.f;
     if (!done) {
-      for (int p = lane; p < per_row; p += 32) m = fmaxf(m, __ldcg(sums + p).x);
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      for (int p = lane; p < per_row; p += 32) m = fmaxf(m, sums[p].x);
+      m = max_over_warp(m);
       for (int p = lane; p < per_row; p += 32) {
-        const float2 s = __ldcg(sums + p);
+        const float2 s = sums[p];
         // (values of -inf alone add 0, or NaN where NaN was among them)
-        sum += s.x == -INFINITY ? s.y : s.y * exp2f((s.x - m) * kLog2e);
+        two_sum(sum, lost, s.x == -INFINITY ? s.y : s.y * exp2f((s.x - m) * kLog2e));
       }
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      for (int d = 16; d > 0; d >>= 1) {
+        lost += __shfl_xor_sync(0xffffffffu, lost, d);
+        two_sum(sum, lost, __shfl_xor_sync(0xffffffffu, sum, d));
+      }
     }
     if (lane == 0) {
-      s_cum[w] = __ldg(P.cum + row);
+      // log(sum) = e ln 2 + log1p(f - 1) with f in [0.75, 1.5): the second part, below 0.41, is
+      // off by 2^-25 of 1 or so in fp32, and the first is left to 64 bits
+      const int e = (static_cast<int>(__float_as_uint(sum)) - 0x3f400000) >> 23;
+      const bool usual = sum > 0.f && sum < INFINITY;
+      const float down = __int_as_float((127 - e) << 23);
       s_done[w] = done ? 1 : 0;
-      s_lse[w] = done ? 0.0 : m + log(sum);  // not finite: the beam has no candidates
+      s_top[w] = m;
+      s_exp[w] = e;
+      s_log[w] = usual ? log1pf(fmaf(sum, down, -1.f) + lost * down) : NAN;
     }
+  }
+  __syncthreads();
+  if (threadIdx.x < W) {
+    const int w = threadIdx.x;
+    const double cum = __ldg(P.cum + n * W + w);
+    s_off[w] = s_done[w] ? cum : cum - (s_top[w] + (s_exp[w] * 0.6931471805599453 + s_log[w]));
   }
   __syncthreads();
   // A value's score in its order-preserving form, 0 where it is no candidate (those of finite
   // scores are above 0).
   auto score_of = [&](int w, float x) -> uint64_t {
-    const double lse = s_lse[w];
-    const double score = s_cum[w] + (static_cast<double>(x) - lse);
-    return isfinite(lse) && isfinite(score) ? ordered_bits(score) : 0;
+    const double score = s_off[w] + static_cast<double>(x);
+    return isfinite(score) ? ordered_bits(score) : 0;
   };
   // the best blocks: a finished beam is one of one candidate, its first
   const int blocks = best_of(buf, s_rank, &s_count, W * per_row, P.select, [&](int i) -> Cand {
     const int w = i / per_row;
     uint64_t hi;
-    if (s_done[w]) hi = i == w * per_row && isfinite(s_cum[w]) ? ordered_bits(s_cum[w]) : 0;
-    else hi = score_of(w, __ldcg(P.scan.sums + n * W * per_row + i).x);
+    if (s_done[w]) hi = i == w * per_row ? score_of(w, 0.f) : 0;
+    else hi = score_of(w, P.scan.sums[n * W * per_row + i].x);
     return hi ? Cand{hi, ~static_cast<uint32_t>(i)} : Cand{0, 0};
   });
   // what they hold, as far as it scores as the last of their maxima
   Cand floor_c{0, 0xffffffffu};
   if (blocks == P.select) floor_c.hi = buf.get(blocks - 1).hi - 1;
   if (threadIdx.x < blocks) s_blocks[threadIdx.x] = ~buf.get(threadIdx.x).lo;
+  if (threadIdx.x < W) {  // a little below the value that has the floor's score
+    float least = -3.402823466e38f;
+    if (floor_c.hi) {
+      const double at = from_ordered_bits(floor_c.hi), t = at - s_off[threadIdx.x];
+      least = fmaxf(least, static_cast<float>(t - (1e-5 * fabs(t) + 1e-15 * (fabs(at) + fabs(s_off[threadIdx.x])) + 1e-30)));
+    }
+    s_least[threadIdx.x] = least;
+  }
   __syncthreads();
   if (threadIdx.x == 0) s_count = 0;
   __syncthreads();
@@ -423,13 +471,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelParams P) 
         x = static_cast<const T*>(P.scan.logits) + (n * W + w) * P.scan.row_stride + at;
         Values<T> c;
         load_values<T, kAligned>(c, x, V - at);
-        // a little below the value that has the floor's score
-        float least = -3.402823466e38f;
-        if (floor_c.hi) {
-          const double t = from_ordered_bits(floor_c.hi) - s_cum[w] + s_lse[w];
-          const double off = 1e-5 * fabs(t) + 1e-15 * (fabs(s_cum[w]) + fabs(s_lse[w])) + 1e-30;
-          least = fmaxf(least, static_cast<float>(t - off));
-        }
+        const float least = s_least[w];
 #pragma unroll
         for (int k = 0; k < kVals; ++k) todo |= c.get(k) >= least ? 1u << k : 0u;
       }
@@ -440,7 +482,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelParams P) 
         const int k = __ffs(todo) - 1;
         todo &= todo - 1;
         const int i = index_of<T, kAligned>(k);
-        const Cand c = s_done[w] ? Cand{ordered_bits(s_cum[w]), ~(static_cast<uint32_t>(w) * V + P.eos)}
+        const Cand c = s_done[w] ? Cand{score_of(w, 0.f), ~(static_cast<uint32_t>(w) * V + P.eos)}
                                  : Cand{score_of(w, Elem<T>::to_f32(x[i])), ~(static_cast<uint32_t>(w) * V + at + i)};
         if (c.hi && better(c, floor_c)) {
           const int to = atomicAdd(&s_count, 1);
