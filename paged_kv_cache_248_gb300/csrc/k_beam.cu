@@ -30,6 +30,7 @@ constexpr int kVals = 32;                 // values of a block per lane
 constexpr int kBlockVals = 32 * kVals;
 constexpr int kSelThreads = 512;          // of the selection
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kGroups = kSelThreads / 4;   // groups of threads in a threshold
 constexpr int kMaxBeams = 64;
 constexpr int kCap = 1536;                // candidates collected between cuts
 constexpr int kResident = 5;              // CTAs of the scan on an SM
@@ -83,82 +84,71 @@ struct Cands {
   }
 };
 
-// The largest t that `need` or more of the threads' values reach (0: none).  Four bits of t at
-// a time: a value counts for as many of the 15 thresholds above t as it reaches, in bytes of four
-// words.  It ends early where the count is `need` exactly.  s_sum: 48 counters, of which a turn
-// uses a third and clears the next one's.
-template <int kValues>
-__device__ uint32_t reached_by(int* s_sum, int need, const uint32_t (&v)[kValues]) {
-  static_assert(kValues < 8, "a warp's counts fit into bytes");
-  const int lane = threadIdx.x & 31;
-  uint32_t t = 0;
-  if (threadIdx.x < 16) s_sum[threadIdx.x] = 0;
+// What a selection needs in shared memory besides the candidates.
+struct Scratch {
+  uint32_t top[kGroups];
+  int rank[kGroups];
+  uint32_t least;
+  int count;
+};
+
+// A threshold that `need` or more of the threads' values reach, and few more than `need` do (0:
+// there are not as many): the need-th largest of the maxima of groups of four threads.
+__device__ uint32_t reached_by(Scratch& s, int need, uint32_t value) {
+  value = max(value, __shfl_xor_sync(0xffffffffu, value, 1));
+  value = max(value, __shfl_xor_sync(0xffffffffu, value, 2));
+  if ((threadIdx.x & 3) == 0) s.top[threadIdx.x >> 2] = value;
+  if (threadIdx.x < kGroups) s.rank[threadIdx.x] = 0;
+  if (threadIdx.x == 0) s.least = 0;
   __syncthreads();
-  int* now = s_sum;
-#pragma unroll 1
-  for (int shift = 28; shift >= 0; shift -= 4) {
-    int* next = now == s_sum + 32 ? s_sum : now + 16;
-    if (threadIdx.x < 16) next[threadIdx.x] = 0;
-    uint32_t words[4] = {0, 0, 0, 0};
+  const int i = threadIdx.x % kGroups;
+  const uint32_t mine = s.top[i];
+  const uint4* other = reinterpret_cast<const uint4*>(s.top) + threadIdx.x / kGroups * (kGroups / 16);
+  int reach = 0;  // of a quarter of the groups
 #pragma unroll
-    for (int j = 0; j < kValues; ++j) {
-      const uint32_t a = v[j] >> shift, b = t >> shift;
-      const int d = a > b ? static_cast<int>(min(a - b, 15u)) : 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)  // min(max(d - 4 k, 0), 4) bytes of 1
-        words[k] += __funnelshift_rc(0x01010101u, 0, 8 * max(0, 4 - max(d - 4 * k, 0)));
-    }
-    uint32_t mine = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t all = __reduce_add_sync(0xffffffffu, words[k]);
-      if (lane >> 2 == k) mine = all >> (8 * (lane & 3)) & 255;
-    }
-    if (lane < 15 && mine > 0) atomicAdd(now + lane, static_cast<int>(mine));  // values that reach t + (lane + 1) 2^shift
-    __syncthreads();
-    const int all = lane < 15 ? now[lane] : 0;
-    const uint32_t reach = __ballot_sync(0xffffffffu, all >= need);
-    if (reach) {
-      const int digit = 32 - __clz(reach);
-      t += static_cast<uint32_t>(digit) << shift;
-      if (__shfl_sync(0xffffffffu, all, digit - 1) == need) break;
-    }
-    now = next;
+  for (int j = 0; j < kGroups / 16; ++j) {
+    const uint4 o = other[j];
+    reach += (o.x >= mine) + (o.y >= mine) + (o.z >= mine) + (o.w >= mine);
   }
+  atomicAdd(s.rank + i, reach);
   __syncthreads();
-  return t;
+  if (threadIdx.x < kGroups && s.rank[i] >= need) atomicMax(&s.least, mine);
+  __syncthreads();
+  return s.least;
 }
 
 // Cuts the n collected candidates to the k best, best first (all threads, with everything
 // pushed); returns the new count.  Every candidate's rank is the number of better ones; few
 // candidates are each ranked by several threads, which share the comparisons, and of many the
 // worse ones are left out by their upper halves first.
-__device__ int cut(Cands& buf, int* ranks, int n, int k) {
+__device__ int cut(Cands& buf, Scratch& s, int n, int k) {
   constexpr int kPer = kCap / kSelThreads;
-  if (n > 128) {
+  for (int before = kCap + 1; n > kGroups && n < before;) {
+    before = n;
+    __syncthreads();  // (the count has been read)
     Cand mine[kPer];
-    uint32_t top[kPer];
+    uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int i = threadIdx.x + j * kSelThreads;
       mine[j] = i < n ? buf.get(i) : Cand{0, 0};
-      top[j] = static_cast<uint32_t>(mine[j].hi >> 32);
+      top = max(top, static_cast<uint32_t>(mine[j].hi >> 32));
     }
-    const uint32_t least = reached_by(ranks, k, top);
-    if (threadIdx.x == 0) ranks[0] = 0;
-    __syncthreads();
+    if (threadIdx.x == 0) s.count = 0;
+    const uint32_t least = reached_by(s, k, top);
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
-      if (threadIdx.x + j * kSelThreads < n && top[j] >= least) buf.set(atomicAdd(ranks, 1), mine[j]);
+      if (threadIdx.x + j * kSelThreads < n && static_cast<uint32_t>(mine[j].hi >> 32) >= least)
+        buf.set(atomicAdd(&s.count, 1), mine[j]);
     __syncthreads();
-    n = ranks[0];
+    n = s.count;
     __syncthreads();
   }
-  if (n <= 128) {
+  if (n <= kGroups) {
     int width = 32;
     while (width < n) width *= 2;
     const int i = threadIdx.x & (width - 1), step = kSelThreads / width;
-    if (threadIdx.x < 128) ranks[threadIdx.x] = 0;
+    if (threadIdx.x < kGroups) s.rank[threadIdx.x] = 0;
     __syncthreads();
     Cand mine{0, 0};
     if (i < n) {
@@ -166,10 +156,10 @@ __device__ int cut(Cands& buf, int* ranks, int n, int k) {
       int rank = 0;
 #pragma unroll 4
       for (int j = threadIdx.x / width; j < n; j += step) rank += better(buf.get(j), mine) ? 1 : 0;
-      if (rank > 0) atomicAdd(ranks + i, rank);
+      if (rank > 0) atomicAdd(s.rank + i, rank);
     }
     __syncthreads();
-    if (threadIdx.x < n && ranks[threadIdx.x] < k) buf.set(ranks[threadIdx.x], mine);  // (i = threadIdx.x)
+    if (threadIdx.x < n && s.rank[i] < k) buf.set(s.rank[i], mine);  // (i = threadIdx.x)
     __syncthreads();
     return min(n, k);
   }
@@ -337,20 +327,20 @@ struct SelParams {
 // nothing) into buf, best first; returns how many there are.  What scores below the
 // num_select-th largest of the threads' maxima is left out from the start.
 template <typename F>
-__device__ int best_of(Cands& buf, int* s_rank, int* s_count, int total, int select, F&& cand) {
+__device__ int best_of(Cands& buf, Scratch& s, int total, int select, F&& cand) {
   constexpr int kKeep = 2;  // candidates that a thread keeps in registers
   Cand kept[kKeep];
-  uint32_t best[1] = {0};
+  uint32_t best = 0;
 #pragma unroll
   for (int j = 0; j < kKeep; ++j) {
     const int i = threadIdx.x + j * kSelThreads;
     kept[j] = i < total ? cand(i) : Cand{0, 0};
-    best[0] = max(best[0], static_cast<uint32_t>(kept[j].hi >> 32));
+    best = max(best, static_cast<uint32_t>(kept[j].hi >> 32));
   }
   for (int i = threadIdx.x + kKeep * kSelThreads; i < total; i += kSelThreads)
-    best[0] = max(best[0], static_cast<uint32_t>(cand(i).hi >> 32));
-  if (threadIdx.x == 0) *s_count = 0;
-  const uint32_t least = reached_by(s_rank, select, best);
+    best = max(best, static_cast<uint32_t>(cand(i).hi >> 32));
+  if (threadIdx.x == 0) s.count = 0;
+  const uint32_t least = reached_by(s, select, best);
   Cand floor_c{least > 0 ? (static_cast<uint64_t>(least) << 32) - 1 : 0, 0xffffffffu};
 #pragma unroll 1
   for (int base = 0; base < total; base += kKeep * kSelThreads) {
@@ -358,20 +348,20 @@ __device__ int best_of(Cands& buf, int* s_rank, int* s_count, int total, int sel
     for (int j = 0; j < kKeep; ++j) {
       const int i = base + threadIdx.x + j * kSelThreads;
       const Cand c = base == 0 ? kept[j] : (i < total ? cand(i) : Cand{0, 0});
-      if (better(c, floor_c)) buf.set(atomicAdd(s_count, 1), c);  // (room for all: kCap - 512 a turn)
+      if (better(c, floor_c)) buf.set(atomicAdd(&s.count, 1), c);  // (room for all: kCap - 512 a turn)
     }
     __syncthreads();
-    const int cnt = *s_count;
+    const int cnt = s.count;
     if (cnt + kKeep * kSelThreads > kCap && base + kKeep * kSelThreads < total) {
       __syncthreads();
-      const int left = cut(buf, s_rank, cnt, select);
+      const int left = cut(buf, s, cnt, select);
       if (left == select && better(buf.get(left - 1), floor_c)) floor_c = buf.get(left - 1);
-      if (threadIdx.x == 0) *s_count = left;
+      if (threadIdx.x == 0) s.count = left;
     }
     __syncthreads();
   }
-  const int cnt = *s_count;
-  return cnt > 0 ? cut(buf, s_rank, cnt, select) : 0;
+  const int cnt = s.count;
+  return cnt > 0 ? cut(buf, s, cnt, select) : 0;
 }
 
 template <typename T, bool kAligned>
@@ -382,12 +372,13 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelParams P) 
   __shared__ uint8_t s_done[kMaxBeams];
   __shared__ Cands buf;
   __shared__ uint32_t s_blocks[64];
-  __shared__ int s_count, s_rank[128];
+  __shared__ __align__(16) Scratch s;
   const int64_t n = blockIdx.x;
   const int W = P.beams, V = P.scan.vocab, per_row = P.scan.row_blocks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
   grid_dep_launch();
+  const double cum = threadIdx.x < W ? __ldg(P.cum + n * W + threadIdx.x) : 0.f;
   // A warp per beam joins its sums, each with what its rounding lost beside it.
   for (int w = warp; w < W; w += kSelWarps) {
     const int64_t row = n * W + w;
@@ -398,9 +389,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelParams P) 
       for (int p = lane; p < per_row; p += 32) m = fmaxf(m, sums[p].x);
       m = max_over_warp(m);
       for (int p = lane; p < per_row; p += 32) {
-        const float2 s = sums[p];
+        const float2 part = sums[p];
         // (values of -inf alone add 0, or NaN where NaN was among them)
-        two_sum(sum, lost, s.x == -INFINITY ? s.y : s.y * exp2f((s.x - m) * kLog2e));
+        two_sum(sum, lost, part.x == -INFINITY ? part.y : part.y * exp2f((part.x - m) * kLog2e));
       }
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) {
@@ -423,7 +414,6 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelParams P) 
   __syncthreads();
   if (threadIdx.x < W) {
     const int w = threadIdx.x;
-    const double cum = __ldg(P.cum + n * W + w);
     s_off[w] = s_done[w] ? cum : cum - (s_top[w] + (s_exp[w] * 0.6931471805599453 + s_log[w]));
   }
   __syncthreads();
@@ -434,7 +424,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelParams P) 
     return isfinite(score) ? ordered_bits(score) : 0;
   };
   // the best blocks: a finished beam is one of one candidate, its first
-  const int blocks = best_of(buf, s_rank, &s_count, W * per_row, P.select, [&](int i) -> Cand {
+  const int blocks = best_of(buf, s, W * per_row, P.select, [&](int i) -> Cand {
     const int w = i / per_row;
     uint64_t hi;
     if (s_done[w]) hi = i == w * per_row ? score_of(w, 0.f) : 0;
@@ -454,7 +444,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelParams P) 
     s_least[threadIdx.x] = least;
   }
   __syncthreads();
-  if (threadIdx.x == 0) s_count = 0;
+  if (threadIdx.x == 0) s.count = 0;
   __syncthreads();
 #pragma unroll 1
   for (int b0 = 0; b0 < blocks; b0 += kSelWarps) {
@@ -485,26 +475,26 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelParams P) 
         const Cand c = s_done[w] ? Cand{score_of(w, 0.f), ~(static_cast<uint32_t>(w) * V + P.eos)}
                                  : Cand{score_of(w, Elem<T>::to_f32(x[i])), ~(static_cast<uint32_t>(w) * V + at + i)};
         if (c.hi && better(c, floor_c)) {
-          const int to = atomicAdd(&s_count, 1);
+          const int to = atomicAdd(&s.count, 1);
           if (to < kCap) buf.set(to, c);
           else again |= 1u << k;
         }
       }
       const int more = __syncthreads_or(again != 0);
-      const int cnt = min(s_count, kCap);
+      const int cnt = min(s.count, kCap);
       __syncthreads();
       if (more) {
-        const int left = cut(buf, s_rank, cnt, P.select);
+        const int left = cut(buf, s, cnt, P.select);
         if (left == P.select && better(buf.get(left - 1), floor_c)) floor_c = buf.get(left - 1);
-        if (threadIdx.x == 0) s_count = left;
+        if (threadIdx.x == 0) s.count = left;
         __syncthreads();
       }
       if (!more) break;
       todo = again;
     }
   }
-  const int cnt = s_count;
-  const int left = cnt > 0 ? cut(buf, s_rank, cnt, P.select) : 0;
+  const int cnt = s.count;
+  const int left = cnt > 0 ? cut(buf, s, cnt, P.select) : 0;
   for (int k = threadIdx.x; k < P.select; k += kSelThreads) {
     const int64_t o = n * P.select + k;
     if (k < left) {
