@@ -493,7 +493,8 @@ def run_fork(pkv, tables, lens, parents, refs, new, layers=1, hkv=2, d=128, dtyp
 
 @pytest.mark.parametrize("rows,prompt,new,layers,hkv,d,dtype", [
     (1, 5, 1, 1, 2, 128, BF), (4, 64, 1, 1, 8, 128, BF), (5, 100, 1, 3, 2, 64, F32), (33, 40, 20, 2, 1, 128, BF),
-    (8, 0, 1, 1, 2, 128, F32), (700, 32, 1, 1, 1, 128, BF), (12, 16, 0, 1, 2, 128, BF)])
+    (8, 0, 1, 1, 2, 128, F32), (700, 32, 1, 1, 1, 128, BF), (12, 16, 0, 1, 2, 128, BF),
+    (32, 300, 3, 1, 1, 128, BF), (6, 2200, 2, 1, 1, 128, BF), (2300, 4, 1, 1, 1, 64, F32)])
 def test_fork(pkv, rows, prompt, new, layers, hkv, d, dtype):
     rng, tables, lens, refs = fork_case(rows, rows, prompt, [3, 16, 21, 0, 32, 15, 1], slack=rows * 5 + 20)
     for parents in (np.arange(rows), rng.integers(0, rows, rows), np.zeros(rows, int),
@@ -526,19 +527,21 @@ def test_fork_a_large_pool_and_tables_alone(pkv):
     assert np.array_equal(t.cpu().numpy(), want[0]) and np.array_equal(rg.cpu().numpy(), want[2])
 
 
-def test_fork_errors_change_nothing(pkv):
-    rng, tables, lens, refs = fork_case(5, 6, 40, [5, 9, 30], slack=3)
+@pytest.mark.parametrize("rows", [6, 40])
+def test_fork_errors_change_nothing(pkv, rows):
+    rng, tables, lens, refs = fork_case(5, rows, 40, [5, 9, 30], slack=3)
     bad_table, bad_len, long_len = tables.copy(), lens.copy(), lens.copy()
     bad_table[2, 1] = -1
     big_table = tables.copy()
     big_table[4, 0] = len(refs)
     bad_len[1] = -1
     long_len[0] = tables.shape[1] * 16 + 1
-    ok = np.array([0, 0, 1, 3, 3, 5])
+    rest = list(range(6, rows))
+    ok = np.array([0, 0, 1, 3, 3, 5] + rest)
     for what, (tb, ln, par, new, status) in {
             "pool": (tables, lens, ok, 40, pkv.PKV_ERR_NO_MEMORY),
-            "parent": (tables, lens, np.array([0, 0, 6, 3, 3, 5]), 1, pkv.PKV_ERR_INDEX),
-            "parent below": (tables, lens, np.array([0, -2, 1, 3, 3, 5]), 1, pkv.PKV_ERR_INDEX),
+            "parent": (tables, lens, np.array([0, 0, rows, 3, 3, 5] + rest), 1, pkv.PKV_ERR_INDEX),
+            "parent below": (tables, lens, np.array([0, -2, 1, 3, 3, 5] + rest), 1, pkv.PKV_ERR_INDEX),
             "hole": (bad_table, lens, ok, 1, pkv.PKV_ERR_INDEX), "id": (big_table, lens, ok, 1, pkv.PKV_ERR_INDEX),
             "length": (tables, bad_len, ok, 1, pkv.PKV_ERR_INDEX), "too long": (tables, long_len, ok, 1, pkv.PKV_ERR_INDEX),
             "no room in the row": (tables, lens, ok, 1000, pkv.PKV_ERR_INDEX)}.items():
