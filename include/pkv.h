@@ -347,7 +347,7 @@ PKV_API int pkv_tree_workspace(const pkv_cache_desc* cache, int32_t num_q_heads,
  * k_cache, v_cache  [num_layers] pools of `cache`'s shape, one after the other
  * path            device int32 [num_seqs][max_path], entries past path_lens[i] not read
  * path_lens       device int32 [num_seqs]
- * new_seq_lens    device int32 [num_seqs], written; not the same array as seq_lens
+ * new_seq_lens    device int32 [num_seqs], written; shares no memory with the inputs
  * Caller contract: the blocks that hold the draft belong to the request alone.
  * Device errors: q_i or seq_lens[i] that do not fit (as in paged_attention), path_lens[i]
  * outside [0, min(max_path, q_i)], a path that does not ascend within [0, q_i), or a bad
@@ -369,7 +369,7 @@ PKV_API int pkv_compact_path(const int32_t* path, int32_t max_path, const int32_
  * returned, best first; equal scores are taken in order of w * vocab + v.  A score that
  * is not finite (a NaN or infinite beam, a logit of -inf) is no candidate, and where the
  * candidates run out, the score is -inf and beam and token are -1.  Scores are ranked in
- * 64 bits; sums over the vocabulary run in 32 and are joined in 64.
+ * 64 bits; sums over the vocabulary run in 32, and what their joins round off is kept.
  * logits          device [num_seqs * num_beams] rows of vocab values of `dtype` (pkv_dtype),
  *                 row_stride elements apart (>= vocab), aligned to their type
  * cum_scores      device fp32 [num_seqs][num_beams]

@@ -288,9 +288,18 @@ def _calls():
             raise ImportError("_native.so not built; run `python -m paged_kv_cache_248_gb300._build`") from e
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-        m.setup(LIB_PATH, torch, PkvError, torch.cuda.current_device, raw, torch.cuda.is_current_stream_capturing)
+        m.setup(LIB_PATH, torch, PkvError, torch.cuda.current_device, raw, torch.cuda.is_current_stream_capturing,
+                _ready_results)
         _nat = m
     return _nat
+
+
+def _ready_results(n, shape, dtype, device):
+    """``n`` small tensors in one piece of memory, for _native to hand out.  ``.data`` gives each a version
+    of its own, so that a change in place of one is none of another, and outside of inference mode they
+    may be handed to calls in it and out of it."""
+    with torch.inference_mode(False):
+        return [t.data for t in torch.empty((n, *shape), dtype=dtype, device=device).unbind()]
 
 
 def pkv_tree_mask(parents: torch.Tensor, query_start_loc: torch.Tensor, max_query_len: int,

@@ -110,7 +110,8 @@ int pkv_compact_path(const int32_t* path, int32_t max_path, const int32_t* path_
     return PKV_ERR_INVALID_ARG;
   if (!aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_INVALID_ARG;
   const int64_t len_bytes = static_cast<int64_t>(num_seqs) * 4;
-  if (overlap(new_seq_lens, len_bytes, seq_lens, len_bytes) || overlap(new_seq_lens, len_bytes, path_lens, len_bytes))
+  if (overlap(new_seq_lens, len_bytes, seq_lens, len_bytes) || overlap(new_seq_lens, len_bytes, path_lens, len_bytes) ||
+      overlap(new_seq_lens, len_bytes, query_start_loc, len_bytes + 4))
     return PKV_ERR_INVALID_ARG;
   DeviceCtx* ctx = device_ctx(&st);
   if (!ctx) return st;

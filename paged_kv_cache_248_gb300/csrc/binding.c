@@ -6,10 +6,10 @@
  * checks them, makes results and scratch and calls libpkv.
  *
  * torch.empty takes as long as such a call (5 us beside a launch on a Grace core), so small
- * results are made 32 at a time, as parts of one tensor, and handed out once each; and scratch
- * is kept per device, stream and call.  Work on one stream runs in order, and every entry holds
- * the GIL for its whole call, which only enqueues work, so two calls never use one scratch at
- * the same time.  Where neither is safe -- while the stream is captured into a graph, whose
+ * results are made 32 at a time, in one piece of memory (tensors of their own otherwise, see
+ * _ready_results in the package), and handed out once each; and scratch is kept per device,
+ * stream and call.  Work on one stream runs in order, and the GIL is held while libpkv enqueues a
+ * call's kernels, so two calls never use one scratch at the same time.  Where neither is safe -- while the stream is captured into a graph, whose
  * replays need memory of their own, or on a stream that the caller names -- both come from
  * torch.empty for that call alone.
  *
@@ -25,11 +25,11 @@
 typedef int64_t i64;
 
 static struct {
-  PyObject *empty, *error, *raw_stream, *current_device, *capturing;
+  PyObject *empty, *error, *raw_stream, *current_device, *capturing, *ready;
   PyObject *results, *scratch; /* see take_result, take_scratch */
   PyObject *i32, *i64, *f32, *bf16, *u8, *boolean;
   PyObject *s_dtype, *s_shape, *s_data_ptr, *s_is_contiguous, *s_get_device, *s_stride, *s_cuda_stream, *s_record_stream,
-      *s_view, *s_unbind, *kw_empty;
+      *s_view, *kw_empty;
   __typeof__(&paged_attention_tree) tree;
   __typeof__(&pkv_tree_workspace) tree_ws;
   __typeof__(&pkv_compact_path) compact;
@@ -183,26 +183,24 @@ static PyObject* take_result(int dim, const i64* n, PyObject* dtype, const Place
   PyObject* k = PyBytes_FromStringAndSize((const char*)&key, sizeof key);
   if (!k) return NULL;
   PyObject* r = NULL;
-  PyObject* ready = PyDict_GetItemWithError(T.results, k); /* a list, borrowed */
+  PyObject* ready = Py_XNewRef(PyDict_GetItemWithError(T.results, k)); /* a list; torch may let other threads run */
   if (!ready && !PyErr_Occurred()) {
     if (PyDict_GET_SIZE(T.results) >= 512) PyDict_Clear(T.results);
     ready = PyList_New(0);
     if (ready && PyDict_SetItem(T.results, k, ready)) Py_CLEAR(ready);
-    Py_XDECREF(ready); /* the store holds it */
   }
   if (ready && PyList_GET_SIZE(ready) == 0) {
-    const i64 whole[3] = {kParts, n[0], dim > 1 ? n[1] : 0};
-    PyObject* t = made(dim + 1, whole, dtype, w);
-    PyObject* parts = t ? PyObject_CallMethodNoArgs(t, T.s_unbind) : NULL;
-    if (!parts || PyList_SetSlice(ready, 0, 0, parts)) ready = NULL;
+    PyObject* parts = dim == 1 ? PyObject_CallFunction(T.ready, "i(L)OL", kParts, (long long)n[0], dtype, (long long)w->dev)
+                               : PyObject_CallFunction(T.ready, "i(LL)OL", kParts, (long long)n[0], (long long)n[1], dtype, (long long)w->dev);
+    if (!parts || PyList_SetSlice(ready, 0, 0, parts)) Py_CLEAR(ready);
     Py_XDECREF(parts);
-    Py_XDECREF(t);
   }
   if (ready) {
     const Py_ssize_t last = PyList_GET_SIZE(ready) - 1;
     r = Py_NewRef(PyList_GET_ITEM(ready, last));
     if (PyList_SetSlice(ready, last, last + 1, NULL)) Py_CLEAR(r);
   }
+  Py_XDECREF(ready);
   Py_DECREF(k);
   return r;
 }
@@ -250,6 +248,11 @@ static PyObject* failed(int status, const char* what) {
   return NULL;
 }
 
+/* Whether sizes fit the C entries' 32 bits. */
+static int fit(i64 a, i64 b, i64 c) {
+  return a <= INT32_MAX && b <= INT32_MAX && c <= INT32_MAX ? 1 : refuse("a size does not fit 32 bits");
+}
+
 /* The descriptor of one cache [blocks, Hkv, 16, d], or of a model's, [layers, ...]. */
 static int caches(Arg* k, Arg* v, int models, pkv_cache_desc* desc, i64* layers, PyObject** dtype) {
   int same = k->dim == v->dim;
@@ -261,6 +264,7 @@ static int caches(Arg* k, Arg* v, int models, pkv_cache_desc* desc, i64* layers,
   if (f32 < 0 || bf16 < 0) return 0;
   if (!f32 && !bf16) return refuse("unsupported cache dtype");
   *dtype = f32 ? T.f32 : T.bf16;
+  if (!fit(k->n[at + 1], k->n[at + 2], k->n[at + 3])) return 0;
   *layers = at == 1 ? k->n[0] : 1;
   desc->num_blocks = k->n[at];
   desc->num_kv_heads = (int32_t)k->n[at + 1];
@@ -313,6 +317,7 @@ static PyObject* py_tree(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     if (!shape_of(&o, a[10], "out")) return NULL;
     if (o.dim != 3 || o.n[0] != q.n[0] || o.n[1] != q.n[1] || o.n[2] != q.n[2]) return refuse("out must have the shape of q"), NULL;
   }
+  if (!fit(q.n[1], bt.n[1], mask.n[1]) || !fit(lens.n[0], 0, 0)) return NULL;
   const double scale = PyFloat_AsDouble(a[7]);
   if (scale == -1.0 && PyErr_Occurred()) return NULL;
   if (!as_int32(a[8], &max_q) || !as_int32(a[9], &max_len)) return NULL;
@@ -359,6 +364,7 @@ static PyObject* py_compact(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (!shape_of(&path, a[0], "path") || !shape_of(&plens, a[1], "path_lens")) return NULL;
   if (path.dim != 2 || path.n[0] != lens.n[0] || plens.dim != 1 || plens.n[0] != lens.n[0])
     return refuse("path must be [num_seqs, max_path], path_lens [num_seqs]"), NULL;
+  if (!fit(path.n[1], bt.n[1], lens.n[0]) || !fit(layers, 0, 0)) return NULL;
   if (a[7] != Py_None && (!shape_of(&o, a[7], "new_seq_lens") || !shaped(&o, 1, lens.n[0], 0))) return NULL;
   if (!place(a[8], &at)) return NULL;
   if (!check(&path, T.i32, at.dev) || !check(&plens, T.i32, at.dev) || !check(&bt, T.i32, at.dev) || !check(&lens, T.i32, at.dev) ||
@@ -387,6 +393,7 @@ static PyObject* py_beam(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (!shape_of(&x, a[0], "logits")) return NULL;
   if (x.dim != 3) return refuse("logits must be [num_seqs, num_beams, vocab]"), NULL;
   const i64 N = x.n[0], W = x.n[1], V = x.n[2];
+  if (!fit(N, W, V)) return NULL;
   const int f32 = is_dtype(x.t, T.f32), bf16 = f32 ? 0 : is_dtype(x.t, T.bf16);
   if (f32 < 0 || bf16 < 0) return NULL;
   if (!f32 && !bf16) return refuse("logits must be float32 or bfloat16"), NULL;
@@ -468,6 +475,7 @@ static PyObject* py_fork(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (!want(n, 10)) return NULL;
   if (!shape_of(&bt, a[0], "block_tables")) return NULL;
   if (bt.dim != 2) return refuse("block_tables must be [num_rows, max_blocks_per_seq]"), NULL;
+  if (!fit(bt.n[0], bt.n[1], 0)) return NULL;
   const int data = a[4] != Py_None;
   if (data != (a[5] != Py_None)) return refuse("k_cache and v_cache must be given together"), NULL;
   if (!shape_of(&refs, a[3], "ref_counts")) return NULL;
@@ -476,6 +484,7 @@ static PyObject* py_fork(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   } else if (refs.dim == 1) {
     desc.num_blocks = refs.n[0];
   }
+  if (!fit(layers, 0, 0)) return NULL;
   if (refs.dim != 1 || refs.n[0] != desc.num_blocks) return refuse("ref_counts must be [num_blocks] of the cache"), NULL;
   if (!shape_of(&lens, a[1], "seq_lens") || !shaped(&lens, 1, bt.n[0], 0)) return NULL;
   if (!shape_of(&par, a[2], "parents") || !shaped(&par, 1, bt.n[0], 0)) return NULL;
@@ -514,11 +523,11 @@ end:
 }
 
 /* (path of libpkv, torch, PkvError, torch.cuda.current_device, a function from a device to its raw stream, one that tells
- * whether the current stream is captured) */
+ * whether the current stream is captured, one that makes results: (shapes, type, device) -> list) */
 static PyObject* py_setup(PyObject* self, PyObject* args) {
   const char* path;
   PyObject* torch;
-  if (!PyArg_ParseTuple(args, "sOOOOO", &path, &torch, &T.error, &T.current_device, &T.raw_stream, &T.capturing)) return NULL;
+  if (!PyArg_ParseTuple(args, "sOOOOOO", &path, &torch, &T.error, &T.current_device, &T.raw_stream, &T.capturing, &T.ready)) return NULL;
   void* h = dlopen(path, RTLD_NOW | RTLD_LOCAL);
   if (!h) {
     PyErr_SetString(PyExc_ImportError, dlerror());
@@ -541,6 +550,7 @@ static PyObject* py_setup(PyObject* self, PyObject* args) {
   Py_INCREF(T.current_device);
   Py_INCREF(T.raw_stream);
   Py_INCREF(T.capturing);
+  Py_INCREF(T.ready);
   if (!(T.results = PyDict_New()) || !(T.scratch = PyDict_New())) return NULL;
   if (!(T.empty = PyObject_GetAttrString(torch, "empty")) || !(T.i32 = PyObject_GetAttrString(torch, "int32")) ||
       !(T.i64 = PyObject_GetAttrString(torch, "int64")) || !(T.f32 = PyObject_GetAttrString(torch, "float32")) ||
@@ -556,7 +566,6 @@ static PyObject* py_setup(PyObject* self, PyObject* args) {
   T.s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
   T.s_record_stream = PyUnicode_InternFromString("record_stream");
   T.s_view = PyUnicode_InternFromString("view");
-  T.s_unbind = PyUnicode_InternFromString("unbind");
   T.kw_empty = Py_BuildValue("(ss)", "dtype", "device");
   Py_RETURN_NONE;
 }

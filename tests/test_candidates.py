@@ -110,7 +110,8 @@ def test_compact_refusals(pkv):
 
     for kw in (dict(path=None), dict(max_path=-1), dict(path_lens=None), dict(bt=None), dict(max_blocks=0), dict(lens=None),
                dict(qsl=None), dict(seqs=-1), dict(k=None), dict(v=None), dict(k=P(0x1008)), dict(layers=0), dict(new=None),
-               dict(new=F), dict(new=P(0x1004)), dict(layers=65536)):
+               dict(new=F), dict(new=P(0x1004)), dict(layers=65536),
+               dict(lens=P(0x500000), path_lens=P(0x600000), new=F)):
         assert call(**kw) == pkv.PKV_ERR_INVALID_ARG, kw
     assert call(cache=B(_desc(pkv, d=64))) == pkv.PKV_ERR_UNSUPPORTED
     assert call(seqs=0) == pkv.PKV_OK
@@ -189,6 +190,16 @@ def test_binding_refuses_shapes_before_any_cuda_call(pkv):
         pkv.pkv_beam_select(x[:, :, ::2], z(2, 4), 8)
     with pytest.raises(ValueError, match="contiguous rows"):
         pkv.pkv_beam_select(x[:, :1].expand(2, 4, 100), z(2, 4), 8)
+    for big in ((1, 1, 1 << 31), (1, 1 << 31, 4), (1 << 31, 1, 4)):  # a size must not wrap round to a small one
+        with pytest.raises(ValueError, match="32 bits"):
+            pkv.pkv_beam_select(z(1).expand(big), z(1, 1), 1)
+    wide = torch.zeros(1, 1, dtype=torch.int32).expand(1, (1 << 32) + 4)
+    with pytest.raises(ValueError, match="32 bits"):
+        pkv.pkv_fork_tables(wide, i32(1), i32(1), i32(4), k, k)
+    with pytest.raises(ValueError, match="32 bits"):
+        pkv.pkv_compact_path(wide, i32(1), i32(1, 4), i32(1), i32(2), k, k)
+    with pytest.raises(ValueError, match="32 bits"):
+        pkv.paged_attention_tree(q, k, k, wide, i32(1), i32(2), mask, 1.0, 3, 8)
     with pytest.raises(ValueError, match="cum_scores"):
         pkv.pkv_beam_select(x, z(2, 3), 8)
     with pytest.raises(ValueError, match="finished"):

@@ -732,6 +732,26 @@ def test_results_are_handed_out_once_and_scratch_is_per_stream(pkv):
         assert all(torch.equal(a, b) for m in others for a, b in zip(m, want[1]))
 
 
+def test_small_results_are_tensors_of_their_own(pkv):
+    """Results share memory 32 at a time, but neither versions (a change in place of one must not spoil what
+    another was saved for) nor inference mode."""
+    x, cum = torch.randn(2, 3, 500, device="cuda"), torch.zeros(2, 3, device="cuda")
+    with torch.inference_mode():
+        pkv.pkv_beam_select(x, cum, 5)
+    w = torch.ones(2, 5, device="cuda", requires_grad=True)
+    a = pkv.pkv_beam_select(x, cum, 5)
+    b = pkv.pkv_beam_select(x, cum, 5)
+    assert not a[0].is_inference()
+    loss = (a[0] * w).sum() + torch.gather(w, 1, (a[2] % 5).long()).sum()
+    want = a[0].clone()
+    for t in b:
+        t.add_(1)
+    loss.backward()
+    assert torch.equal(w.grad, want + torch.zeros_like(w).scatter_add_(1, (a[2] % 5).long(), torch.ones_like(w)))
+    a[0].add_(w)  # and may be changed like any other
+    assert a[0].requires_grad
+
+
 def test_calls_from_several_threads(pkv):
     import threading
     x = torch.randn(2, 3, 5000, device="cuda")
