@@ -286,20 +286,20 @@ def _calls():
             from . import _native as m
         except ImportError as e:
             raise ImportError("_native.so not built; run `python -m paged_kv_cache_248_gb300._build`") from e
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-        m.setup(LIB_PATH, torch, PkvError, torch.cuda.current_device, raw, torch.cuda.is_current_stream_capturing,
-                _ready_results)
+        builtin = lambda name, other: getattr(torch._C, name, None) or other  # noqa: E731  (these cost 0.1 us less)
+        m.setup(LIB_PATH, torch, PkvError, builtin("_cuda_getDevice", torch.cuda.current_device),
+                builtin("_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream),
+                builtin("_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing), _ready_results)
         _nat = m
     return _nat
 
 
 def _ready_results(n, shape, dtype, device):
-    """``n`` small tensors in one piece of memory, for _native to hand out.  ``.data`` gives each a version
-    of its own, so that a change in place of one is none of another, and outside of inference mode they
-    may be handed to calls in it and out of it."""
+    """``n`` tensors for _native to hand out, made outside of inference mode so that calls in it and out
+    of it may have them."""
     with torch.inference_mode(False):
-        return [t.data for t in torch.empty((n, *shape), dtype=dtype, device=device).unbind()]
+        first = torch.empty(shape, dtype=dtype, device=device)
+        return [first] + [torch.empty_like(first) for _ in range(n - 1)]
 
 
 def pkv_tree_mask(parents: torch.Tensor, query_start_loc: torch.Tensor, max_query_len: int,

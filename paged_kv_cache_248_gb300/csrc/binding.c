@@ -6,14 +6,14 @@
  * checks them, makes results and scratch and calls libpkv.
  *
  * torch.empty takes as long as such a call (5 us beside a launch on a Grace core), so small
- * results are made 32 at a time, in one piece of memory (tensors of their own otherwise, see
- * _ready_results in the package), and handed out once each; and scratch is kept per device,
- * stream and call.  Work on one stream runs in order, and the GIL is held while libpkv enqueues a
- * call's kernels, so two calls never use one scratch at the same time.  Where neither is safe -- while the stream is captured into a graph, whose
+ * results are made 32 at a time, away from the launches (1.4 us each), and handed out once each;
+ * and scratch is kept per device, stream and call.  Work on one stream runs in order, and the GIL
+ * is held while libpkv enqueues a call's kernels, so two calls never use one scratch at the same
+ * time.  Where neither is safe -- while the stream is captured into a graph, whose
  * replays need memory of their own, or on a stream that the caller names -- both come from
  * torch.empty for that call alone.
  *
- * setup(path, torch, PkvError) opens libpkv and keeps what is needed of torch.
+ * setup(path, torch, PkvError, ...) opens libpkv and keeps what is needed of torch.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -83,6 +83,14 @@ static i64 call_long(PyObject* t, PyObject* name) {
   return v;
 }
 
+static int pointer(Arg* a) {
+  PyObject* p = PyObject_CallMethodNoArgs(a->t, T.s_data_ptr);
+  if (!p) return 0;
+  a->ptr = PyLong_AsVoidPtr(p);
+  Py_DECREF(p);
+  return !PyErr_Occurred();
+}
+
 /* The pointer of a contiguous tensor of this type on device dev. */
 static int check(Arg* a, PyObject* dtype, i64 dev) {
   if (call_long(a->t, T.s_get_device) != dev) {
@@ -104,11 +112,7 @@ static int check(Arg* a, PyObject* dtype, i64 dev) {
     PyErr_Format(PyExc_ValueError, "%s must be contiguous", a->name);
     return 0;
   }
-  PyObject* p = PyObject_CallMethodNoArgs(a->t, T.s_data_ptr);
-  if (!p) return 0;
-  a->ptr = PyLong_AsVoidPtr(p);
-  Py_DECREF(p);
-  return !PyErr_Occurred();
+  return pointer(a);
 }
 
 static int refuse(const char* what) {
@@ -169,7 +173,7 @@ static PyObject* made(int dim, const i64* n, PyObject* dtype, const Place* w) {
   return r;
 }
 
-/* A new tensor of four bytes a value or two, small ones from a store of ready parts. */
+/* A new tensor of four bytes a value or two, small ones from a store of ready ones. */
 static PyObject* take_result(int dim, const i64* n, PyObject* dtype, const Place* w) {
   enum { kParts = 32, kMostBytes = 2048 };
   i64 values = 1;
@@ -207,7 +211,7 @@ static PyObject* take_result(int dim, const i64* n, PyObject* dtype, const Place
 
 /* Scratch of at least `bytes` for call number `call`. */
 static PyObject* take_scratch(i64 bytes, int call, const Place* w) {
-  if (bytes < 256) bytes = 256;
+  if (bytes < 256) bytes = 256; /* (none is empty) */
   if (!w->keep) return made(1, &bytes, T.u8, w);
   struct {
     void* stream;
@@ -231,12 +235,24 @@ static PyObject* take_scratch(i64 bytes, int call, const Place* w) {
   return r;
 }
 
-/* A given tensor (new reference), or a new one. */
-static PyObject* given_or_made(PyObject* given, int dim, const i64* n, PyObject* dtype, const Place* w) {
-  return given == Py_None ? take_result(dim, n, dtype, w) : Py_NewRef(given);
+/* A result with its pointer: a given tensor of the right shape, checked, or a new one (a new
+ * reference, also where the check fails; NULL: none could be made). */
+static PyObject* result(Arg* a, PyObject* given, const char* name, int dim, const i64* n, PyObject* dtype, const Place* w, int* ok) {
+  a->name = name;
+  a->t = given == Py_None ? take_result(dim, n, dtype, w) : Py_NewRef(given);
+  *ok = a->t && (given == Py_None ? pointer(a) : check(a, dtype, w->dev));
+  return a->t;
 }
-static PyObject* given_or_scratch(PyObject* given, i64 bytes, int call, const Place* w) {
-  return given == Py_None ? take_scratch(bytes, call, w) : Py_NewRef(given);
+/* The same for scratch, whose bytes a->n[0] tells. */
+static PyObject* scratch(Arg* a, PyObject* given, i64 bytes, int call, const Place* w, int* ok) {
+  if (given != Py_None) {
+    *ok = shape_of(a, given, "workspace") && check(a, T.u8, w->dev);
+    return Py_NewRef(given);
+  }
+  a->t = take_scratch(bytes, call, w);
+  a->n[0] = bytes;
+  *ok = a->t && pointer(a);
+  return a->t;
 }
 
 static PyObject* failed(int status, const char* what) {
@@ -304,6 +320,7 @@ static PyObject* py_tree(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   i64 layers, bytes = 0;
   Place at;
   int32_t max_q, max_len;
+  int ok;
   if (!want(n, 13)) return NULL;
   if (!shape_of(&k, a[1], "k_cache") || !shape_of(&v, a[2], "v_cache") || !caches(&k, &v, 0, &desc, &layers, &dt)) return NULL;
   if (!shape_of(&q, a[0], "q")) return NULL;
@@ -325,8 +342,8 @@ static PyObject* py_tree(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (!check(&q, dt, at.dev) || !check(&k, dt, at.dev) || !check(&v, dt, at.dev) || !check(&bt, T.i32, at.dev) || !check(&lens, T.i32, at.dev) ||
       !check(&qsl, T.i32, at.dev) || !check(&mask, T.i64, at.dev))
     return NULL;
-  out = given_or_made(a[10], 3, q.n, dt, &at);
-  if (!out || !shape_of(&o, out, "out") || !check(&o, dt, at.dev)) goto end;
+  out = result(&o, a[10], "out", 3, q.n, dt, &at, &ok);
+  if (!ok) goto end;
   if (q.n[0] == 0) {
     res = Py_NewRef(out);
     goto end;
@@ -338,8 +355,8 @@ static PyObject* py_tree(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       goto end;
     }
   }
-  ws = given_or_scratch(a[11], bytes, 0, &at);
-  if (!ws || !shape_of(&w, ws, "workspace") || !check(&w, T.u8, at.dev)) goto end;
+  ws = scratch(&w, a[11], bytes, 0, &at, &ok);
+  if (!ok) goto end;
   const int st = T.tree(q.ptr, k.ptr, v.ptr, &desc, bt.ptr, (int32_t)bt.n[1], lens.ptr, qsl.ptr, mask.ptr, (int32_t)mask.n[1],
                         (int32_t)lens.n[0], (int32_t)q.n[1], q.n[0], max_q, max_len, (float)scale, o.ptr, w.ptr, w.n[0], at.stream);
   res = st ? failed(st, "paged_attention_tree") : Py_NewRef(out);
@@ -356,6 +373,7 @@ static PyObject* py_compact(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   PyObject *dt, *out = NULL, *res = NULL;
   i64 layers;
   Place at;
+  int ok;
   if (!want(n, 9)) return NULL;
   if (!shape_of(&k, a[5], "k_cache") || !shape_of(&v, a[6], "v_cache") || !caches(&k, &v, 1, &desc, &layers, &dt)) return NULL;
   if (!shape_of(&bt, a[2], "block_tables") || !shape_of(&lens, a[3], "seq_lens") || !shape_of(&qsl, a[4], "query_start_loc") ||
@@ -370,8 +388,8 @@ static PyObject* py_compact(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (!check(&path, T.i32, at.dev) || !check(&plens, T.i32, at.dev) || !check(&bt, T.i32, at.dev) || !check(&lens, T.i32, at.dev) ||
       !check(&qsl, T.i32, at.dev) || !check(&k, dt, at.dev) || !check(&v, dt, at.dev))
     return NULL;
-  out = given_or_made(a[7], 1, lens.n, T.i32, &at);
-  if (!out || !shape_of(&o, out, "new_seq_lens") || !check(&o, T.i32, at.dev)) goto end;
+  out = result(&o, a[7], "new_seq_lens", 1, lens.n, T.i32, &at, &ok);
+  if (!ok) goto end;
   const int st = T.compact(path.ptr, (int32_t)path.n[1], plens.ptr, bt.ptr, (int32_t)bt.n[1], lens.ptr, qsl.ptr,
                            (int32_t)lens.n[0], k.ptr, v.ptr, &desc, (int32_t)layers, o.ptr, at.stream);
   res = st ? failed(st, "pkv_compact_path") : Py_NewRef(out);
@@ -389,6 +407,7 @@ static PyObject* py_beam(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   i64 bytes = 0;
   Place at;
   int32_t K, eos;
+  int ok;
   if (!want(n, 8)) return NULL;
   if (!shape_of(&x, a[0], "logits")) return NULL;
   if (x.dim != 3) return refuse("logits must be [num_seqs, num_beams, vocab]"), NULL;
@@ -447,13 +466,11 @@ static PyObject* py_beam(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     }
   }
   for (int i = 0; i < 3; ++i) {
-    out[i] = given_or_made(a[5] == Py_None ? Py_None : PyTuple_GET_ITEM(a[5], i), 2, shape, types[i], &at);
-    r[i].name = names[i];
-    r[i].t = out[i];
-    if (!out[i] || !check(&r[i], types[i], at.dev)) goto end;
+    out[i] = result(&r[i], a[5] == Py_None ? Py_None : PyTuple_GET_ITEM(a[5], i), names[i], 2, shape, types[i], &at, &ok);
+    if (!ok) goto end;
   }
-  ws = given_or_scratch(a[6], bytes, 1, &at);
-  if (!ws || !shape_of(&w, ws, "workspace") || !check(&w, T.u8, at.dev)) goto end;
+  ws = scratch(&w, a[6], bytes, 1, &at, &ok);
+  if (!ok) goto end;
   const int st = T.beam(x.ptr, f32 ? PKV_F32 : PKV_BF16, step, cum.ptr, fin.ptr, eos, (int32_t)N, (int32_t)W, (int32_t)V, K,
                         r[0].ptr, r[1].ptr, r[2].ptr, w.ptr, w.n[0], at.stream);
   res = st ? failed(st, "pkv_beam_select") : PyTuple_Pack(3, out[0], out[1], out[2]);
@@ -472,6 +489,7 @@ static PyObject* py_fork(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   i64 layers = 1, bytes = 0;
   Place at;
   int32_t num_new;
+  int ok;
   if (!want(n, 10)) return NULL;
   if (!shape_of(&bt, a[0], "block_tables")) return NULL;
   if (bt.dim != 2) return refuse("block_tables must be [num_rows, max_blocks_per_seq]"), NULL;
@@ -498,11 +516,10 @@ static PyObject* py_fork(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (!place(a[9], &at)) return NULL;
   if (!check(&bt, T.i32, at.dev) || !check(&lens, T.i32, at.dev) || !check(&par, T.i32, at.dev) || !check(&refs, T.i32, at.dev)) return NULL;
   if (data && (!check(&k, dt, at.dev) || !check(&v, dt, at.dev))) return NULL;
-  tables = given_or_made(a[7] == Py_None ? Py_None : PyTuple_GET_ITEM(a[7], 0), 2, bt.n, T.i32, &at);
-  nlens = given_or_made(a[7] == Py_None ? Py_None : PyTuple_GET_ITEM(a[7], 1), 1, bt.n, T.i32, &at);
-  if (!tables || !nlens || !shape_of(&obt, tables, "new tables") || !check(&obt, T.i32, at.dev) ||
-      !shape_of(&olens, nlens, "new lengths") || !check(&olens, T.i32, at.dev))
-    goto end;
+  tables = result(&obt, a[7] == Py_None ? Py_None : PyTuple_GET_ITEM(a[7], 0), "new tables", 2, bt.n, T.i32, &at, &ok);
+  if (!ok) goto end;
+  nlens = result(&olens, a[7] == Py_None ? Py_None : PyTuple_GET_ITEM(a[7], 1), "new lengths", 1, bt.n, T.i32, &at, &ok);
+  if (!ok) goto end;
   if (a[8] == Py_None) {
     const int st = T.fork_ws((int32_t)bt.n[0], &bytes);
     if (st) {
@@ -510,8 +527,8 @@ static PyObject* py_fork(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       goto end;
     }
   }
-  ws = given_or_scratch(a[8], bytes, 2, &at);
-  if (!ws || !shape_of(&w, ws, "workspace") || !check(&w, T.u8, at.dev)) goto end;
+  ws = scratch(&w, a[8], bytes, 2, &at, &ok);
+  if (!ok) goto end;
   const int st = T.fork_(bt.ptr, lens.ptr, (int32_t)bt.n[0], (int32_t)bt.n[1], par.ptr, num_new, refs.ptr, obt.ptr, olens.ptr,
                          data ? k.ptr : NULL, data ? v.ptr : NULL, &desc, (int32_t)layers, w.ptr, w.n[0], at.stream);
   res = st ? failed(st, "pkv_fork_tables") : PyTuple_Pack(2, tables, nlens);

@@ -28,7 +28,7 @@
 //     and every key tile is loaded once for both.
 //
 // Per CTA (352 threads): warp 0 finds the runs' units and loads Q and K, warp 10 loads V (TMA
-// boxes of the blocks' 16-token rows, 128-byte swizzle; 2 K and 3 V tiles in flight), one
+// boxes of the blocks' 16-token rows, 128-byte swizzle; 2 K and 2 V tiles in flight), one
 // thread of warp 1 issues the MMAs, warps 2-5 and 6-9 are the streams' softmax.  The tiles
 // that hold drafted keys (the last one or two of a request) take their visibility from the
 // mask row's bits, the others see every key.  Their V rows are looked through for values that
@@ -45,7 +45,7 @@ namespace {
 
 constexpr int kThreads = 352;
 constexpr int kKStages = 2;
-constexpr int kVStages = 3;
+constexpr int kVStages = 2;
 constexpr int kHalfBytes = 16384;
 constexpr int kTileBytes = 2 * kHalfBytes;  // 128 x 128 bf16 in two 64-column halves
 constexpr int kRing = 4;                    // items published ahead, per ring
@@ -958,71 +958,73 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 }
 
 // ------------------------------------------------------------------ merge
-// One warp per row of a cut unit: the parts' weights 2^(m - M), then the weighted sum of their
-// accumulators in the order of the keys.
+// One warp per row of a cut unit: the weighted sum of its parts' accumulators, in the order of the
+// keys, with a running maximum; all loads of four parts at once, since latency is what it costs.
 constexpr int kMergeThreads = 256;
 constexpr int kMergeRows = kMergeThreads / 32;
+constexpr int kMergeParts = 4;
+constexpr int kMergeY = 8;  // CTAs per cut; each takes every 8th group of rows
 
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const Params P) {
-  grid_dep_wait();
-  grid_dep_launch();
   const int run = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4* rec = reinterpret_cast<const int4*>(P.cuts + run);
+  grid_dep_wait();
+  grid_dep_launch();
   const int4 c0 = __ldcg(rec), c1 = __ldcg(rec + 1);  // parts, head, t0; j0[2], nq[2]
-  const int parts = c0.x;
+  const int parts = min(c0.x, static_cast<int>(gridDim.x) - run);
   if (parts < 2) return;
-  const int row = blockIdx.y * kMergeRows + warp;
-  const int w = row >> 7, r = row & 127;
-  const int rj = r >> P.gp_log2, rg = r & (P.gp - 1);
-  if (rj >= (w ? c1.w : c1.z) || rg >= P.group) return;
-  auto slot_row = [&](int p) -> int64_t {
-    return static_cast<int64_t>(p == 0 ? 2 * run + 1 : 2 * (run + p)) * P.rows_cap + row;
-  };
-  float M = -INFINITY;
-  bool bad = false, nan = false;
-  for (int p = lane; p < parts; p += 32) {
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(P.part_ml) + slot_row(p));
-    nan |= isnan(ml.x);
-    M = fmaxf(M, ml.x);
-    bad |= ml.y == -1.f;
-  }
+#pragma unroll 1
+  for (int row = blockIdx.y * kMergeRows + warp; row < P.rows_cap; row += gridDim.y * kMergeRows) {
+    const int w = row >> 7, r = row & 127;
+    const int rj = r >> P.gp_log2, rg = r & (P.gp - 1);
+    if (rj >= (w ? c1.w : c1.z) || rg >= P.group) continue;
+    bool bad = false;
+    float M = -INFINITY, den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int p0 = 0; p0 < parts; p0 += kMergeParts) {
+      float2 ml[kMergeParts];
+      float4 o[kMergeParts];
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  bad = __any_sync(0xffffffffu, bad);
-  if (__any_sync(0xffffffffu, nan)) M = __int_as_float(0x7fffffff);
-  float den = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p0 = 0; p0 < parts; p0 += 32) {
-    float weight = 0.f, l = 0.f;
-    if (p0 + lane < parts) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(P.part_ml) + slot_row(p0 + lane));
-      // (a part without a maximum saw nothing, or nothing but NaN, which its sum says)
-      weight = ml.x == -INFINITY ? ml.y * 0.f : exp2f(ml.x - M);
-      l = ml.y;
-    }
-    const int n = min(32, parts - p0);
-#pragma unroll 4
-    for (int p = 0; p < n; ++p) {
-      const float a = __shfl_sync(0xffffffffu, weight, p);
-      const float lp = __shfl_sync(0xffffffffu, l, p);
-      const float4 o = __ldcg(reinterpret_cast<const float4*>(P.part_o + slot_row(p0 + p) * 128) + lane);
-      if (a != 0.f) {
-        den = fmaf(lp, a, den);
-        acc.x = fmaf(o.x, a, acc.x);
-        acc.y = fmaf(o.y, a, acc.y);
-        acc.z = fmaf(o.z, a, acc.z);
-        acc.w = fmaf(o.w, a, acc.w);
+      for (int k = 0; k < kMergeParts; ++k) {
+        const int p = p0 + k;
+        ml[k] = make_float2(-INFINITY, 0.f);
+        if (p < parts) {  // a run's second slot holds the unit that it begins, its first the one it goes on with
+          const int64_t at = static_cast<int64_t>(2 * (run + p) + (p == 0 ? 1 : 0)) * P.rows_cap + row;
+          ml[k] = __ldcg(reinterpret_cast<const float2*>(P.part_ml) + at);
+          o[k] = __ldcg(reinterpret_cast<const float4*>(P.part_o + at * 128) + lane);
+        }
+      }
+      float top = M;
+#pragma unroll
+      for (int k = 0; k < kMergeParts; ++k) top = fmaxf(top, ml[k].x);
+      const float f = M == top ? 1.f : exp2f(M - top);
+      M = top;
+      den *= f;
+      acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+      for (int k = 0; k < kMergeParts; ++k) {
+        bad |= ml[k].y == -1.f;
+        // (a part without a maximum saw nothing, or nothing but NaN, which its sum says)
+        const float a = ml[k].x == -INFINITY ? ml[k].y * 0.f : exp2f(ml[k].x - M);
+        if (a != 0.f && p0 + k < parts) {
+          den = fmaf(ml[k].y, a, den);
+          acc.x = fmaf(o[k].x, a, acc.x);
+          acc.y = fmaf(o[k].y, a, acc.y);
+          acc.z = fmaf(o[k].z, a, acc.z);
+          acc.w = fmaf(o[k].w, a, acc.w);
+        }
       }
     }
+    const bool zero = bad || den == 0.f;
+    const float inv = 1.f / den;
+    __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    uint2 packed = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+    if (zero) packed = make_uint2(0, 0);
+    const int64_t t = static_cast<int64_t>(c0.z) + (w ? c1.y : c1.x) + rj;
+    reinterpret_cast<uint2*>(P.out + (t * P.hq + static_cast<int64_t>(c0.y) * P.group + rg) * 128)[lane] = packed;
   }
-  const bool zero = bad || den == 0.f;
-  const float inv = zero ? 0.f : 1.f / den;
-  __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-  uint2 packed = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
-  if (zero) packed = make_uint2(0, 0);
-  const int64_t t = static_cast<int64_t>(c0.z) + (w ? c1.y : c1.x) + rj;
-  reinterpret_cast<uint2*>(P.out + (t * P.hq + static_cast<int64_t>(c0.y) * P.group + rg) * 128)[lane] = packed;
 }
 
 int gp_log2_of(int group) {
@@ -1122,7 +1124,7 @@ int launch_tree_tc(const TreeArgs& t, void* workspace, int num_sms, uint32_t* er
   if (st) return st;
   st = cuda_status(launch_k(kernel, dim3(ctas), dim3(kThreads), kSmemBytes, s, qm, km, vm, p));
   if (st) return st;
-  const int row_blocks = (l.rows_cap + kMergeRows - 1) / kMergeRows;
+  const int row_blocks = min((l.rows_cap + kMergeRows - 1) / kMergeRows, kMergeY);
   return cuda_status(launch_k(tree_merge_kernel, dim3(ctas * runs_per_cta, row_blocks), dim3(kMergeThreads), 0, s, p));
 }
 

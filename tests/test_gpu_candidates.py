@@ -733,8 +733,8 @@ def test_results_are_handed_out_once_and_scratch_is_per_stream(pkv):
 
 
 def test_small_results_are_tensors_of_their_own(pkv):
-    """Results share memory 32 at a time, but neither versions (a change in place of one must not spoil what
-    another was saved for) nor inference mode."""
+    """Results are made 32 at a time, but share neither memory nor versions (a change in place of one must not
+    spoil what another was saved for) nor inference mode."""
     x, cum = torch.randn(2, 3, 500, device="cuda"), torch.zeros(2, 3, device="cuda")
     with torch.inference_mode():
         pkv.pkv_beam_select(x, cum, 5)
