@@ -175,7 +175,27 @@ __device__ __noinline__ Request load_request(const Params& P, int i) {
   return make_request(P, __ldg(P.qsl + i), __ldg(P.qsl + i + 1), __ldg(P.seq_lens + i));
 }
 
-// This CTA's kRuns runs (all threads): run k * CTAs + CTA, so that few runs have an SM each.  Rows of requests whose lengths do not fit are zeroed here.
+// Rows of requests whose lengths do not fit are zeroed (by `step` threads, this is number `first`).
+__device__ __noinline__ void zero_wrong(const Params& P, int first, int step) {
+#pragma unroll 1
+  for (int i = blockIdx.x; i < P.num_seqs; i += gridDim.x) {
+    const Request r = load_request(P, i);
+    if (!r.wrong) continue;
+    if (first == 0) flag_error(P.err, kErrLength);
+    const int64_t vecs = static_cast<int64_t>(r.q_len) * P.hq * 16;
+    uint4* dst = reinterpret_cast<uint4*>(P.out) + static_cast<int64_t>(r.t0) * P.hq * 16;
+#pragma unroll 1
+    for (int64_t v = first; v < vecs; v += step) dst[v] = make_uint4(0, 0, 0, 0);
+  }
+}
+
+// Places of a run, of `total` places in all.
+__device__ __forceinline__ int64_t run_length(const Params& P, int64_t total, uint32_t runs) {
+  const int64_t even = total < 0x7fffffff ? (static_cast<uint32_t>(total) + runs - 1) / runs : (total + runs - 1) / runs;
+  return even > P.min_run ? even : P.min_run;
+}
+
+// This CTA's kRuns runs: run k * CTAs + CTA, so that few runs have an SM each (all threads).
 template <int kRuns>
 __device__ void find_runs(const Params& P, Ctl& c) {
   const int per = (P.num_seqs + kThreads - 1) / kThreads;
@@ -203,9 +223,7 @@ __device__ void find_runs(const Params& P, Ctl& c) {
     if (w < warp) before += c.warp_sum[w];
     total += c.warp_sum[w];
   }
-  const int64_t runs = static_cast<int64_t>(gridDim.x) * kRuns;
-  const int64_t even = (total + runs - 1) / runs;
-  const int64_t len = even > P.min_run ? even : P.min_run;
+  const int64_t len = run_length(P, total, gridDim.x * kRuns);
   if (threadIdx.x == 0) c.run_len = len;
 #pragma unroll 1
   for (int k = 0; k < kRuns; ++k) {
@@ -228,19 +246,67 @@ __device__ void find_runs(const Params& P, Ctl& c) {
       }
     }
   }
-  if (any_wrong) {
-#pragma unroll 1
-    for (int i = blockIdx.x; i < P.num_seqs; i += gridDim.x) {
-      const Request r = load_request(P, i);
-      if (!r.wrong) continue;
-      if (threadIdx.x == 0) flag_error(P.err, kErrLength);
-      const int64_t vecs = static_cast<int64_t>(r.q_len) * P.hq * 16;
-      uint4* dst = reinterpret_cast<uint4*>(P.out) + static_cast<int64_t>(r.t0) * P.hq * 16;
-#pragma unroll 1
-      for (int64_t v = threadIdx.x; v < vecs; v += kThreads) dst[v] = make_uint4(0, 0, 0, 0);
+  if (any_wrong) zero_wrong(P, threadIdx.x, kThreads);
+  __syncthreads();
+}
+
+// The same for up to kFewSeqs requests by warp 0 alone, which is the one that walks the runs: no
+// barriers, and the requests' loads are all on their way at once.
+constexpr int kFewSeqs = 128;
+template <int kRuns>
+__device__ void find_runs_few(const Params& P, Ctl& c) {
+  constexpr int kSets = kFewSeqs / 32;
+  const int lane = threadIdx.x & 31;
+  int32_t q0[kSets], q1[kSets], len[kSets];
+#pragma unroll
+  for (int s = 0; s < kSets; ++s) {
+    const int i = 32 * s + lane;
+    q0[s] = q1[s] = len[s] = 0;
+    if (i < P.num_seqs) {
+      q0[s] = __ldg(P.qsl + i);
+      q1[s] = __ldg(P.qsl + i + 1);
+      len[s] = __ldg(P.seq_lens + i);
     }
   }
-  __syncthreads();
+  int64_t total = 0, before[kSets];
+  int32_t cost[kSets];
+  bool wrong = false;
+#pragma unroll
+  for (int s = 0; s < kSets; ++s) {
+    before[s] = cost[s] = 0;
+    if (32 * s < P.num_seqs) {
+      const Request r = make_request(P, q0[s], q1[s], len[s]);
+      wrong |= r.wrong;
+      cost[s] = r.cost;
+      int64_t incl = r.cost;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += y;
+      }
+      before[s] = total + incl - r.cost;
+      total += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  const int64_t places = run_length(P, total, gridDim.x * kRuns);
+  if (lane == 0) c.run_len = places;
+#pragma unroll
+  for (int k = 0; k < kRuns; ++k) {
+    const int64_t begin = places * (static_cast<int64_t>(k) * gridDim.x + blockIdx.x);
+    if (lane == 0) {
+      c.run[k].begin = begin;
+      c.run[k].end = begin + places < total ? begin + places : total;
+    }
+#pragma unroll
+    for (int s = 0; s < kSets; ++s) {
+      if (begin >= before[s] && begin < before[s] + cost[s]) {
+        c.run[k].seq = 32 * s + lane;
+        c.run[k].base = before[s];
+      }
+    }
+  }
+  if (__any_sync(0xffffffffu, wrong)) zero_wrong(P, lane, 32);
+  __syncwarp();
 }
 
 // Walks the items of a run; the whole warp holds it, lane l the lengths of request rb + l.
@@ -353,111 +419,119 @@ __device__ __forceinline__ bool load_q(const Params& P, const CUtensorMap* qmap,
   return true;
 }
 
-// This lane's block id of key tile `tile` of a request (lanes 0-7).
-__device__ __forceinline__ int tile_id(const Params& P, const Item& info, int tile) {
-  const int at = tile * kBlocksPerTile + static_cast<int>(threadIdx.x & 31);
-  return (threadIdx.x & 31) < kBlocksPerTile && at <= (info.len - 1) / kBlock
-             ? __ldg(P.bt + static_cast<int64_t>(info.seq) * P.max_blocks + at) : 0;
+// A run's item as a producer goes through it, and this lane's block id of its next tile (lanes 0-7).
+struct Tiles {
+  int32_t seq, head, len;
+  int32_t tile, end;  // the next tile and the item's end
+  int32_t id;
+  uint32_t it, tiles;  // items and tiles of the run so far
+  int32_t live;
+
+  __device__ __forceinline__ void load_id(const Params& P) {
+    const int lane = threadIdx.x & 31, at = tile * kBlocksPerTile + lane;
+    id = lane < kBlocksPerTile && at <= (len - 1) / kBlock ? __ldg(P.bt + static_cast<int64_t>(seq) * P.max_blocks + at) : 0;
+  }
+};
+
+// With two runs, a turn works on `a` and the two states change places after it.
+template <typename T>
+__device__ __forceinline__ void change_places(T& a, T& b) {
+  const T t = a;
+  a = b;
+  b = t;
 }
 
 // The producers walk the runs' tiles in the order in which the MMA thread takes them: a tile
 // of each run by turns (one run: its tiles).  The K producer finds the items, publishes them
 // and loads Q too; the V producer reads the items like the other warps.  Both run this one
-// piece of code, and leave their runs' states in local memory, to keep it small.
+// piece of code, to keep it small.
 template <int kRuns>
 __device__ void producer_warp(const Params& P, bool is_k, const CUtensorMap* qmap, const CUtensorMap* map, Ctl& c,
                               uint8_t* qbuf, uint8_t* buf) {
-  struct State {
-    Walk walk;  // (K)
-    Item item;
-    uint32_t it, tiles;
-    int j, id, live;
-  };
   const int lane = threadIdx.x & 31;
   volatile int* abort_flag = &c.abort_flag;
   uint64_t* full = is_k ? c.kfull : c.vfull;
   uint64_t* empty = is_k ? c.kempty : c.vempty;
   const int stages = is_k ? kKStages : kVStages;
-  State st[kRuns];
+  Walk walk[kRuns];  // (K)
+  if (is_k) {
 #pragma unroll 1
-  for (int k = 0; k < kRuns; ++k) {
-    st[k].walk = start_walk(c.run[k]);
-    st[k].item.nt = 0;
-    st[k].it = st[k].tiles = 0;
-    st[k].j = st[k].id = 0;
-    st[k].live = 1;
+    for (int k = 0; k < kRuns; ++k) walk[k] = start_walk(c.run[k]);
+    if (lane < kRuns) P.cuts[lane * gridDim.x + blockIdx.x].parts = 0;
+    __syncwarp();
   }
-  if (is_k && lane < kRuns) P.cuts[lane * gridDim.x + blockIdx.x].parts = 0;
-  __syncwarp();
+  Tiles a{0, 0, 1, 0, 0, 0, 0, 0, 1}, b = a;
   uint32_t n = 0;
   int live = kRuns, s = 0, phase = 1;  // of the next slot
   bool ok = true;
 #pragma unroll 1
   for (int k = 0; ok && live > 0; k ^= kRuns - 1) {
-    State& a = st[k];
-    if (!a.live) continue;
-    if (a.j == a.item.nt) {
+    if (a.live && a.tile == a.end) {
       const int slot = a.it % kRing;
+      Item item;
       if (is_k) {
-        a.item = next_item(P, a.walk, k * gridDim.x + blockIdx.x, c.run_len);
-        ok = publish(c, k, a.it, a.item, abort_flag);
+        item = next_item(P, walk[k], k * gridDim.x + blockIdx.x, c.run_len);
       } else {
         ok = wait_for(&c.item_full[k][slot], (a.it / kRing) & 1, abort_flag);
-        if (ok) a.item = c.ring[k][slot];
+        if (!ok) break;
+        item = c.ring[k][slot];
         __syncwarp();
       }
-      ++a.it;
-      a.j = 0;
-      if (!ok) break;
-      if (a.item.idx < 0) {
-        a.live = 0;
-        --live;
-        continue;
-      }
-      a.id = tile_id(P, a.item, a.item.kt0);
+      a.live = item.idx >= 0;
+      a.seq = item.seq;
+      a.head = item.head;
+      a.len = item.len;
+      a.tile = item.kt0;
+      a.end = item.kt0 + item.nt;
+      if (a.live) a.load_id(P);
+      else --live;
       if (is_k) {
+        ok = publish(c, k, a.it, item, abort_flag);
 #pragma unroll 1
-        for (int w = 0; w < 3 - kRuns && ok; ++w)  // the item's one row tile, or two
-          if (kRuns == 2 || a.item.nq[w] > 0)
-            ok = load_q(P, qmap, c, qbuf, kRuns == 2 ? k : w, a.item,
-                        (w ? a.item.j0[1] : a.item.j0[0]) - (P.row0[k] >> P.gp_log2), abort_flag);
+        for (int w = 0; w < 3 - kRuns && ok && a.live; ++w)  // the item's one row tile, or two
+          if (kRuns == 2 || item.nq[w] > 0)
+            ok = load_q(P, qmap, c, qbuf, kRuns == 2 ? k : w, item, (w ? item.j0[1] : item.j0[0]) - (P.row0[k] >> P.gp_log2),
+                        abort_flag);
         if (!ok) break;
-      } else if (lane == 0) {
+      } else if (a.live && lane == 0) {
         mbar_arrive(&c.item_empty[k][slot]);
       }
+      ++a.it;
     }
-    const int tile = a.item.kt0 + a.j;
-    int cur = a.id;
-    ++a.j;
-    if (a.j < a.item.nt) a.id = tile_id(P, a.item, tile + 1);  // loads while this tile waits for its slot
-    const bool wrong = cur < 0 || cur >= P.num_blocks;
-    if (wrong) cur = 0;
-    if (is_k) {
-      if (__any_sync(0xffffffffu, wrong)) {
-        if (wrong) flag_error(P.err, kErrBlockId);
-        if (lane == 0) c.bad[k][(a.it - 1) % kRing] = 1;
-        __syncwarp();
+    if (a.live) {
+      const int tile = a.tile;
+      int cur = a.id;
+      if (++a.tile < a.end) a.load_id(P);  // loads while this tile waits for its slot
+      const bool wrong = cur < 0 || cur >= P.num_blocks;
+      if (wrong) cur = 0;
+      if (is_k) {
+        if (__any_sync(0xffffffffu, wrong)) {
+          if (wrong) flag_error(P.err, kErrBlockId);
+          if (lane == 0) c.bad[k][(a.it - 1) % kRing] = 1;
+          __syncwarp();
+        }
+        if (lane == 0) c.number[k][a.tiles % 8] = n;
+        ++a.tiles;
       }
-      if (lane == 0) c.number[k][a.tiles % 8] = n;
-      ++a.tiles;
+      // K or V of the tile into its ring slot: 2 boxes of 16 rows per block
+      const int nblk = min(kBlocksPerTile, (a.len - 1) / kBlock + 1 - tile * kBlocksPerTile);
+      const int32_t row = (cur * P.hkv + a.head) * kBlock;
+      ok = wait_for(&empty[s], phase, abort_flag);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nblk) * 4096u);
+      __syncwarp();
+      if (lane < nblk) {
+        uint8_t* d = buf + s * kTileBytes + lane * 2048;
+        tma_load_2d(d, map, &full[s], 0, row, l2_policy_evict_first());
+        tma_load_2d(d + kHalfBytes, map, &full[s], 64, row, l2_policy_evict_first());
+      }
+      ++n;
+      if (++s == stages) {
+        s = 0;
+        phase ^= 1;
+      }
     }
-    // K or V of the tile into its ring slot: 2 boxes of 16 rows per block
-    const int nblk = min(kBlocksPerTile, (a.item.len - 1) / kBlock + 1 - tile * kBlocksPerTile);
-    const int32_t row = (cur * P.hkv + a.item.head) * kBlock;
-    ok = wait_for(&empty[s], phase, abort_flag);
-    if (!ok) break;
-    if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nblk) * 4096u);
-    __syncwarp();
-    if (lane < nblk) {
-      uint8_t* d = buf + s * kTileBytes + lane * 2048;
-      tma_load_2d(d, map, &full[s], 0, row, l2_policy_evict_first());
-      tma_load_2d(d + kHalfBytes, map, &full[s], 64, row, l2_policy_evict_first());
-    }
-    ++n;
-    if (++s == stages) {
-      s = 0;
-      phase ^= 1;
-    }
+    if (kRuns == 2) change_places(a, b);
   }
   if (!ok && !*abort_flag && lane == 0) raise_abort(c, P.err);
   if (*abort_flag) {  // copies already issued land before the CTA's shared memory goes away
@@ -556,14 +630,6 @@ struct Issuer {
     return true;
   }
 };
-
-// With two runs, a turn works on `a` and the two states change places after it.
-template <typename T>
-__device__ __forceinline__ void change_places(T& a, T& b) {
-  const T t = a;
-  a = b;
-  b = t;
-}
 
 template <int kRuns>
 __device__ void mma_warp(const Params& P, Ctl& c, uint8_t* qbuf, uint8_t* kbuf, uint8_t* vbuf, uint32_t tmem_base) {
@@ -963,11 +1029,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   const uint32_t tmem = c.tmem_base;
   grid_dep_wait();
   grid_dep_launch();
-  find_runs<kRuns>(P, c);
-  if (warp == 0 || warp == 10) producer_warp<kRuns>(P, warp == 0, &qmap, warp == 0 ? &kmap : &vmap, c, qbuf, warp == 0 ? kbuf : vbuf);
-  else if (warp == 1) mma_warp<kRuns>(P, c, qbuf, kbuf, vbuf, tmem);
-
-  else softmax_warps<kRuns>(P, c, vbuf, tmem);
+  if (P.num_seqs > kFewSeqs) find_runs<kRuns>(P, c);
+  else if (warp == 0) find_runs_few<kRuns>(P, c);
+  if (warp == 0 || warp == 10)
+    producer_warp<kRuns>(P, warp == 0, &qmap, warp == 0 ? &kmap : &vmap, c, qbuf, warp == 0 ? kbuf : vbuf);
+  else if (warp == 1)
+    mma_warp<kRuns>(P, c, qbuf, kbuf, vbuf, tmem);
+  else
+    softmax_warps<kRuns>(P, c, vbuf, tmem);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
