@@ -549,7 +549,7 @@ __device__ void producer_warp(const Params& P, bool is_k, const CUtensorMap* qma
 // ------------------------------------------------------------------ MMA warp
 // One elected thread issues every MMA, but the whole warp walks through the tiles, with values
 // that the compiler can tell to be the same in all of its lanes: the operands of an MMA live in
-// uniform registers, and values of one thread have to be moved there before each (8 requests of 32768 keys: 470 -> 428 us).
+// uniform registers, and values of one thread have to be moved there before each (8 requests of 32768 keys: 470 -> 390 us).
 // A stream's step is P V of its tile before, then S of its next tile: MMAs of one thread complete in
 // order, so S cannot overwrite the P that this P V reads, and S being complete tells the softmax
 // that O holds every tile before.
@@ -568,26 +568,28 @@ struct Issuer {
   uint32_t tmem, q, k, v;  // shared-memory addresses of the Q tiles and the rings
   volatile int* abort_flag;
   uint32_t p_phase, o_phase, q_phase;  // bit w: the phase to wait for next
-  bool issued;
+  bool issued, failed;
 
-  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait_for(bar, parity, abort_flag));
-  }
+  // A wait that is given up may be given up by some lanes only, and elect.sync wants them all: so the
+  // turn goes on, on whatever is there, and the warp votes at its end (well-defined, if useless: the
+  // operands are this CTA's memory, and the call reports the timeout).
+  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) { failed |= !wait_for(bar, parity, abort_flag); }
+  __device__ __forceinline__ bool ok() { return !__any_sync(0xffffffffu, failed); }
 
   // O_w += P_w V of the tile in V slot `slot`; `first` begins O_w anew, `last` reports it.
   // (P being there means that V is: the softmax waits for it and looks through it.)
-  __device__ __forceinline__ bool pv(int w, uint32_t slot, bool first, bool last) {
+  __device__ __forceinline__ void pv(int w, uint32_t slot, bool first, bool last) {
     constexpr uint32_t idesc = umma_idesc_bf16(128, 128, false, true);
     const uint64_t b = umma_smem_desc(v + slot * kTileBytes, kHalfBytes, 1024, kLayout128B);
     const uint32_t s_col = tmem + 128 * w;
-    if (!wait(&c.p_full[w][0], p_phase >> w & 1)) return false;
+    wait(&c.p_full[w][0], p_phase >> w & 1);
     if (first) {
-      if (!wait(&c.o_free[w], (o_phase >> w & 1) ^ 1)) return false;
+      wait(&c.o_free[w], (o_phase >> w & 1) ^ 1);
       o_phase ^= 1u << w;
     }
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-      if (hf && !wait(&c.p_full[w][1], p_phase >> w & 1)) return false;
+      if (hf) wait(&c.p_full[w][1], p_phase >> w & 1);
       tc_fence_after();
       if (elected()) {
 #pragma unroll
@@ -598,13 +600,12 @@ struct Issuer {
       }
     }
     p_phase ^= 1u << w;
-    return true;
   }
 
   // S_w = Q_w K^T of the tile in K slot `slot`, whose turn's parity is given; `last`: Q_w has been read.
-  __device__ __forceinline__ bool s(int w, uint32_t slot, uint32_t parity, bool last) {
+  __device__ __forceinline__ void s(int w, uint32_t slot, uint32_t parity, bool last) {
     constexpr uint32_t idesc = umma_idesc_bf16(128, 128, false, false);
-    if (!wait(&c.kfull[slot], parity)) return false;
+    wait(&c.kfull[slot], parity);
     tc_fence_after();
     const uint64_t a = umma_smem_desc(q + w * kTileBytes, 16, 1024, kLayout128B);
     const uint64_t b = umma_smem_desc(k + slot * kTileBytes, 16, 1024, kLayout128B);
@@ -621,21 +622,19 @@ struct Issuer {
       if (last) umma_commit(&c.q_free[w]);
     }
     issued = true;
-    return true;
   }
 
-  __device__ __forceinline__ bool q_ready(int w) {
-    if (!wait(&c.q_full[w], q_phase >> w & 1)) return false;
+  __device__ __forceinline__ void q_ready(int w) {
+    wait(&c.q_full[w], q_phase >> w & 1);
     q_phase ^= 1u << w;
-    return true;
   }
 };
 
 template <int kRuns>
-__device__ void mma_warp(const Params& P, Ctl& c, uint8_t* qbuf, uint8_t* kbuf, uint8_t* vbuf, uint32_t tmem_base) {
+__device__ void mma_warp(const Params& P, Ctl& c, uint8_t* qbuf, uint8_t* kbuf, uint8_t* vbuf, uint32_t tmem) {
   static_assert(kKStages == 2 && kVStages == 2, "a tile's slots are its number's lowest bit");
   volatile int* abort_flag = &c.abort_flag;
-  Issuer x{c, same(tmem_base), smem_u32(qbuf), smem_u32(kbuf), smem_u32(vbuf), abort_flag, 0, 0, 0, false};
+  Issuer x{c, tmem, smem_u32(qbuf), smem_u32(kbuf), smem_u32(vbuf), abort_flag, 0, 0, 0, false, false};
   uint32_t n = 0;  // tiles
   bool ok = true;
   if (kRuns == 2) {
@@ -646,11 +645,12 @@ __device__ void mma_warp(const Params& P, Ctl& c, uint8_t* qbuf, uint8_t* kbuf, 
     State a{0, 0, 0, 0, 1, 0}, b{0, 0, 0, 0, 1, 0};
 #pragma unroll 1
     for (int w = 0; ok && (a.live | b.live); w ^= 1) {
-      if (a.pending) ok = x.pv(w, a.before, a.j == 1, a.j == a.nt);
+      if (a.pending) x.pv(w, a.before, a.j == 1, a.j == a.nt);
       a.pending = 0;
-      if (ok && a.live && a.j == a.nt) {
+      if (a.live && a.j == a.nt) {
         const int slot = a.it % kRing;
-        ok = x.wait(&c.item_full[w][slot], (a.it / kRing) & 1);
+        x.wait(&c.item_full[w][slot], (a.it / kRing) & 1);
+        ok = x.ok();
         if (ok) {
           a.nt = same(c.ring[w][slot].nt);
           a.live = same(c.ring[w][slot].idx) >= 0;
@@ -658,15 +658,16 @@ __device__ void mma_warp(const Params& P, Ctl& c, uint8_t* qbuf, uint8_t* kbuf, 
           a.j = 0;
           if (a.live) {
             if (elected()) mbar_arrive(&c.item_empty[w][slot]);
-            ok = x.q_ready(w);
+            x.q_ready(w);
           }
         }
       }
       if (ok && a.live) {
         ++a.j;
-        ok = x.s(w, n & 1, n >> 1 & 1, a.j == a.nt);
+        x.s(w, n & 1, n >> 1 & 1, a.j == a.nt);
         a.before = n++ & 1;
         a.pending = 1;
+        ok = x.ok();
       }
       change_places(a, b);
     }
@@ -674,20 +675,23 @@ __device__ void mma_warp(const Params& P, Ctl& c, uint8_t* qbuf, uint8_t* kbuf, 
     uint32_t it = 0;
     while (ok) {
       const int slot = it % kRing;
-      ok = x.wait(&c.item_full[0][slot], (it / kRing) & 1);
+      x.wait(&c.item_full[0][slot], (it / kRing) & 1);
+      ok = x.ok();
       if (!ok) break;
       const int nt = same(c.ring[0][slot].nt), rows = same(c.ring[0][slot].nq[1]) > 0 ? 2 : 1;
       const bool over = same(c.ring[0][slot].idx) < 0;
       ++it;
       if (over) break;
       if (elected()) mbar_arrive(&c.item_empty[0][slot]);
-      ok = x.q_ready(0) && (rows == 1 || x.q_ready(1));
+      x.q_ready(0);
+      if (rows == 2) x.q_ready(1);
       // turns of the row tiles: 0, 1, 0, 1, ... (one row tile: 0, 0, ...)
       int w = 0;
 #pragma unroll 1
       for (int j = 0; j <= nt && ok;) {
-        if (j > 0) ok = x.pv(w, (n + j - 1) & 1, j == 1, j == nt);
-        if (ok && j < nt) ok = x.s(w, (n + j) & 1, (n + j) >> 1 & 1, j == nt - 1);
+        if (j > 0) x.pv(w, (n + j - 1) & 1, j == 1, j == nt);
+        if (j < nt) x.s(w, (n + j) & 1, (n + j) >> 1 & 1, j == nt - 1);
+        ok = x.ok();
         if (++w == rows) {
           w = 0;
           ++j;
@@ -975,6 +979,12 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
   if (!ok && !*abort_flag && lane == 0) raise_abort(c, P.err);
 }
 
+// The kernel cannot run as it is laid out: the call reports a failure, and nothing is merged.
+__device__ __noinline__ void refuse_to_run(const Params& P, int runs) {
+  if (threadIdx.x == 0) flag_error(P.err, kErrTimeout);
+  if (threadIdx.x < runs) P.cuts[threadIdx.x * gridDim.x + blockIdx.x].parts = 0;
+}
+
 template <bool kPairs>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ CUtensorMap qmap,
                                                            const __grid_constant__ CUtensorMap kmap,
@@ -982,7 +992,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   constexpr int kRuns = kPairs ? 1 : 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if (smem_u32(smem_raw) & 1023u) {  // the swizzled tiles need it, and no room is left to round up in
-    flag_error(P.err, kErrTimeout);
+    grid_dep_wait();
+    refuse_to_run(P, kRuns);
     return;
   }
   uint8_t* qbuf = smem_raw;
@@ -1026,9 +1037,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = c.tmem_base;
+  constexpr uint32_t tmem = 0;  // all of it, which begins at the first column: constants need no registers
   grid_dep_wait();
   grid_dep_launch();
+  if (c.tmem_base != tmem) {
+    refuse_to_run(P, kRuns);
+    if (warp == 1) {
+      tmem_dealloc(c.tmem_base, kTmemCols);
+      tmem_relinquish();
+    }
+    return;
+  }
   if (P.num_seqs > kFewSeqs) find_runs<kRuns>(P, c);
   else if (warp == 0) find_runs_few<kRuns>(P, c);
   if (warp == 0 || warp == 10)
@@ -1173,7 +1192,7 @@ int launch_tree_tc(const TreeArgs& t, void* workspace, int num_sms, uint32_t* er
   const int64_t most = tiles >= 2 * num_sms ? 2 * num_sms : tiles * a.num_seqs;
   const int min_tiles = pairs ? 2 : 1;
   const int ctas = static_cast<int>(most < min_tiles * num_sms ? (most + min_tiles - 1) / min_tiles : num_sms);
-  p.unit_cost = most < 2 * num_sms ? 0 : 1;
+  p.unit_cost = most < 2 * num_sms ? 0 : 2;
   p.min_run = min_tiles + p.unit_cost;
   const Layout l = layout_of(group, a.max_query_len, num_sms);
   p.out = static_cast<__nv_bfloat16*>(a.out);
