@@ -11,13 +11,16 @@
 // nodes x GP heads (GP = G rounded up to a power of two).  A unit is (request, kv head, one
 // row tile, or two) and goes over all of the request's key tiles of 128 keys.
 //
-// Cut.  All units' key tiles, one after the other (and a few places more for each unit, whose
-// beginning and end take time too), are cut into equal runs, so that one long
-// request and a thousand short ones keep every SM equally busy; a CTA derives its runs from
-// the lengths by itself, without a planning launch.  A unit that lies within one run is
-// finished there; of one that is cut, each run leaves its rows' unnormalised accumulator,
+// Cut.  All units' key tiles, one after the other (and two places more for each unit, whose
+// beginning and end take time too: 64 requests 131, 124, 122 us with 0, 1, 3 of them), are cut into
+// equal runs, so that one long request and a thousand short ones keep every SM equally busy; a CTA
+// derives its runs from the lengths by itself, without a planning launch.  A unit that lies within
+// one run is finished there; of one that is cut, each run leaves its rows' unnormalised accumulator,
 // maximum and sum, and the merge kernel joins them in order.  A run leaves at most two such
-// partials.
+// partials.  Where every kv head of every request has the same number of units, above one, as many
+// runs at a time go through the same keys, each for one of the units, so that K and V come from
+// HBM once and not once a unit (8 requests of 32768 keys with 512 rows: 2.17 GB read and 415 us
+// one unit after the other, 1.09 GB and 391 us side by side).
 //
 // Streams.  Two S/P/O accumulator sets live in TMEM, each with a softmax warpgroup of its own, so
 // that one softmax runs while the tensor core works for the other.
@@ -65,7 +68,8 @@ struct alignas(16) Item {
 
 struct Run {
   int64_t begin, end, base;  // places; the first place of the request it begins in
-  int64_t seq;
+  int32_t seq;
+  int32_t unit;  // of each kv head, -1: all units, one after the other (see "Cut")
 };
 
 struct Ctl {
@@ -145,12 +149,22 @@ __device__ __forceinline__ void raise_abort(Ctl& c, uint32_t* err) {
   flag_error(err, kErrTimeout);
 }
 
+template <typename T>
+__device__ __forceinline__ T same(T x) {  // lane 0's value
+  return __shfl_sync(0xffffffffu, x, 0);
+}
+
 // ------------------------------------------------------------------ units
 struct Request {
   int32_t t0, q_len, len;
   bool wrong;            // rows to zero: lengths that do not fit
   int32_t tiles, units;  // key tiles of a unit; units of one kv head
   int32_t cost;          // of all its units: a unit costs its key tiles and P.unit_cost
+
+  // Its places where one unit of each kv head counts, or all.
+  __device__ __forceinline__ int32_t places(const Params& P, bool one) const {
+    return one && cost > 0 ? P.hkv * (tiles + P.unit_cost) : cost;
+  }
 };
 
 __device__ __forceinline__ Request make_request(const Params& P, int32_t q0, int32_t q1, int32_t len) {
@@ -189,10 +203,26 @@ __device__ __noinline__ void zero_wrong(const Params& P, int first, int step) {
   }
 }
 
-// Places of a run, of `total` places in all.
-__device__ __forceinline__ int64_t run_length(const Params& P, int64_t total, uint32_t runs) {
+// Run number k of this CTA: `total` places of one unit of each kv head (units > 0) or of all (0) cut
+// into equal runs.
+template <int kRuns>
+__device__ __forceinline__ Run cut_run(const Params& P, int k, int64_t total, uint32_t units, int64_t* len) {
+  uint32_t runs = gridDim.x * kRuns, number = k * gridDim.x + blockIdx.x, unit = 0;
+  if (units > 0) {
+    runs /= units;
+    unit = number / runs;
+    number -= unit * runs;
+  }
   const int64_t even = total < 0x7fffffff ? (static_cast<uint32_t>(total) + runs - 1) / runs : (total + runs - 1) / runs;
-  return even > P.min_run ? even : P.min_run;
+  *len = even > P.min_run ? even : P.min_run;
+  Run r;
+  r.begin = *len * number;
+  r.end = r.begin + *len < total ? r.begin + *len : total;
+  if (units > 0 && unit >= units) r.end = r.begin;  // (a CTA too many)
+  r.base = 0;
+  r.seq = 0;
+  r.unit = units > 0 ? static_cast<int32_t>(unit) : -1;
+  return r;
 }
 
 // This CTA's kRuns runs: run k * CTAs + CTA, so that few runs have an SM each (all threads).
@@ -200,14 +230,19 @@ template <int kRuns>
 __device__ void find_runs(const Params& P, Ctl& c) {
   const int per = (P.num_seqs + kThreads - 1) / kThreads;
   const int i0 = min(static_cast<int>(threadIdx.x) * per, P.num_seqs), i1 = min(i0 + per, P.num_seqs);
+  const Request first = load_request(P, 0);
   int64_t mine = 0;
-  bool wrong = false;
+  bool wrong = false, differ = false;
 #pragma unroll 1
   for (int i = i0; i < i1; ++i) {
     const Request r = load_request(P, i);
     mine += r.cost;
     wrong |= r.wrong;
+    differ |= r.cost > 0 && r.units != first.units;
   }
+  const bool any_differ = __syncthreads_or(differ);
+  const bool one = kRuns == 1 && !any_differ && first.units > 1 && first.units <= gridDim.x;
+  if (one) mine /= first.units;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t incl = mine;
 #pragma unroll 1
@@ -223,26 +258,29 @@ __device__ void find_runs(const Params& P, Ctl& c) {
     if (w < warp) before += c.warp_sum[w];
     total += c.warp_sum[w];
   }
-  const int64_t len = run_length(P, total, gridDim.x * kRuns);
-  if (threadIdx.x == 0) c.run_len = len;
-#pragma unroll 1
+  Run run[kRuns];
+  int64_t len;
+#pragma unroll
   for (int k = 0; k < kRuns; ++k) {
-    const int64_t begin = len * (static_cast<int64_t>(k) * gridDim.x + blockIdx.x);
-    if (threadIdx.x == 0) {
-      c.run[k].begin = begin;
-      c.run[k].end = begin + len < total ? begin + len : total;
-    }
+    run[k] = cut_run<kRuns>(P, k, total, one ? first.units : 0, &len);
+    if (threadIdx.x == 0) c.run[k] = run[k];
+  }
+  if (threadIdx.x == 0) c.run_len = len;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kRuns; ++k) {
+    const int64_t begin = run[k].begin;
     if (begin >= before && begin < before + mine) {
       int64_t at = before;
 #pragma unroll 1
       for (int i = i0; i < i1; ++i) {
-        const int64_t cost = load_request(P, i).cost;
-        if (begin < at + cost) {
+        const int64_t places = load_request(P, i).places(P, one);
+        if (begin < at + places) {
           c.run[k].seq = i;
           c.run[k].base = at;
           break;
         }
-        at += cost;
+        at += places;
       }
     }
   }
@@ -270,36 +308,46 @@ __device__ void find_runs_few(const Params& P, Ctl& c) {
   }
   int64_t total = 0, before[kSets];
   int32_t cost[kSets];
-  bool wrong = false;
+  bool wrong = false, differ = false;
+  const int32_t units = make_request(P, same(q0[0]), same(q1[0]), same(len[0])).units;
+  Request r[kSets];
+#pragma unroll
+  for (int s = 0; s < kSets; ++s) {
+    r[s].cost = 0;
+    if (32 * s < P.num_seqs) {
+      r[s] = make_request(P, q0[s], q1[s], len[s]);
+      wrong |= r[s].wrong;
+      differ |= r[s].cost > 0 && r[s].units != units;
+    }
+  }
+  const bool one = kRuns == 1 && units > 1 && units <= gridDim.x && !__any_sync(0xffffffffu, differ);
 #pragma unroll
   for (int s = 0; s < kSets; ++s) {
     before[s] = cost[s] = 0;
     if (32 * s < P.num_seqs) {
-      const Request r = make_request(P, q0[s], q1[s], len[s]);
-      wrong |= r.wrong;
-      cost[s] = r.cost;
-      int64_t incl = r.cost;
+      cost[s] = r[s].places(P, one);
+      int64_t incl = cost[s];
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
         if (lane >= d) incl += y;
       }
-      before[s] = total + incl - r.cost;
+      before[s] = total + incl - cost[s];
       total += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
-  const int64_t places = run_length(P, total, gridDim.x * kRuns);
-  if (lane == 0) c.run_len = places;
 #pragma unroll
   for (int k = 0; k < kRuns; ++k) {
-    const int64_t begin = places * (static_cast<int64_t>(k) * gridDim.x + blockIdx.x);
+    int64_t places;
+    const Run run = cut_run<kRuns>(P, k, total, one ? units : 0, &places);
     if (lane == 0) {
-      c.run[k].begin = begin;
-      c.run[k].end = begin + places < total ? begin + places : total;
+      c.run[k] = run;
+      c.run_len = places;
     }
+    __syncwarp();
 #pragma unroll
     for (int s = 0; s < kSets; ++s) {
-      if (begin >= before[s] && begin < before[s] + cost[s]) {
+      if (run.begin >= before[s] && run.begin < before[s] + cost[s]) {
         c.run[k].seq = 32 * s + lane;
         c.run[k].base = before[s];
       }
@@ -312,12 +360,12 @@ __device__ void find_runs_few(const Params& P, Ctl& c) {
 // Walks the items of a run; the whole warp holds it, lane l the lengths of request rb + l.
 struct Walk {
   int64_t pos, end, base;
-  int i, rb;
+  int i, unit, rb;
   int32_t q0, q1, len;
 };
 
 __device__ __forceinline__ Walk start_walk(const Run& r) {
-  return Walk{r.begin, r.end, r.base, static_cast<int>(r.seq), -64, 0, 0, 0};
+  return Walk{r.begin, r.end, r.base, r.seq, r.unit, -64, 0, 0, 0};
 }
 
 // The next item of run number `run` (idx -1: none is left).
@@ -335,16 +383,18 @@ __device__ __noinline__ Item next_item(const Params& P, Walk& k, int run, int64_
     const int src = k.i - k.rb;
     const Request rq = make_request(P, __shfl_sync(0xffffffffu, k.q0, src), __shfl_sync(0xffffffffu, k.q1, src),
                                     __shfl_sync(0xffffffffu, k.len, src));
-    if (k.pos >= k.base + rq.cost) {  // (cost 0 among them)
-      k.base += rq.cost;
+    const int32_t all = rq.places(P, k.unit >= 0);
+    if (k.pos >= k.base + all) {  // (0 among them)
+      k.base += all;
       if (++k.i >= P.num_seqs) k.pos = k.end;  // (lengths that changed meanwhile)
       continue;
     }
     // a unit's first unit_cost places stand for its beginning and end, its tiles come after
     const uint32_t off = static_cast<uint32_t>(k.pos - k.base);
     const uint32_t places = rq.tiles + P.unit_cost;
-    const int unit = static_cast<int>(off / places);
+    int unit = static_cast<int>(off / places);
     const uint32_t at = off - unit * places;
+    if (k.unit >= 0) unit = unit * rq.units + k.unit;
     const int64_t left = k.end - k.pos;  // this run's places of the unit: [at, stop)
     const uint32_t stop = left < places - at ? at + static_cast<uint32_t>(left) : places;
     const int first = max(0, static_cast<int>(at) - P.unit_cost);
@@ -558,11 +608,6 @@ __device__ __forceinline__ bool elected() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
 }
-template <typename T>
-__device__ __forceinline__ T same(T x) {  // lane 0's value
-  return __shfl_sync(0xffffffffu, x, 0);
-}
-
 struct Issuer {
   Ctl& c;
   uint32_t tmem, q, k, v;  // shared-memory addresses of the Q tiles and the rings

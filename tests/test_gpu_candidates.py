@@ -90,6 +90,17 @@ def test_tree_lengths(pkv, ctx, nodes):
     check(b.run(pkv), *b.expected())
 
 
+@pytest.mark.parametrize("seqs,nodes,hq,hkv,top", [(3, 64, 16, 1, 9000), (2, 33, 32, 2, 3000), (150, 33, 8, 1, 90),
+                                                   (130, 17, 16, 1, 500), (1, 600, 16, 1, 700)])
+def test_tree_units_side_by_side(pkv, seqs, nodes, hq, hkv, top):
+    """Requests whose kv heads have equally many row tiles, above two: their units go through the keys together."""
+    ctx = [(top * (i + 1) // seqs) for i in range(seqs)]
+    b = Tree(seqs + nodes, ctx, [nodes] * seqs, hq, hkv)
+    check(b.run(pkv), *b.expected())
+    mixed = Tree(seqs, ctx + [50], [nodes] * seqs + [1], hq, hkv)  # one that has fewer: one after the other again
+    check(mixed.run(pkv), *mixed.expected())
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("hq,hkv", [(8, 2), (3, 3), (16, 1), (11, 1)])
 def test_tree_fp32(pkv, d, hq, hkv):
