@@ -387,60 +387,69 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_f32_kernel(const Pa
   }
 }
 
-// One warp per row of a cut unit: the parts' weights 2^(m - M), then the weighted sum of their
-// accumulators in the order of the keys.
+// One warp per row of a cut unit: the weighted sum of its parts' accumulators, in the order of the
+// keys, with a running maximum; all loads of four parts at once, since latency is what it costs.
 template <int D>
 __global__ void __launch_bounds__(256) tree_f32_merge_kernel(const Params32 P) {
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, kParts = 4;
+  const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int4* rec = reinterpret_cast<const int4*>(P.cuts + blockIdx.x);
   grid_dep_wait();
   grid_dep_launch();
-  const int4* rec = reinterpret_cast<const int4*>(P.cuts + blockIdx.x);
-  int4 c = __ldcg(rec);  // parts, t0, row0, rows
-  c.x = min(c.x, static_cast<int>(gridDim.x - blockIdx.x));
+  const int4 c = __ldcg(rec);  // parts, t0, row0, rows
   const int head = __ldcg(rec + 1).x;
-  const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (c.x < 2 || row >= c.w) return;
-  auto part_row = [&](int p) -> int64_t {
-    return (p == 0 ? 2 * static_cast<int64_t>(blockIdx.x) + 1 : 2 * (static_cast<int64_t>(blockIdx.x) + p)) * kRows + row;
-  };
-  float M = -INFINITY;
-  bool bad = false, nan = false;
-  for (int p = lane; p < c.x; p += 32) {
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(P.part_ml) + part_row(p));
-    nan |= isnan(ml.x);
-    bad |= ml.y == -1.f;
-    M = fmaxf(M, ml.x);
-  }
+  const int parts = min(c.x, static_cast<int>(gridDim.x - blockIdx.x));
+  if (parts < 2 || row >= c.w) return;
+  bool bad = false;
+  float M = -INFINITY, den = 0.f, acc[E] = {};
+#pragma unroll 1
+  for (int p0 = 0; p0 < parts; p0 += kParts) {
+    float2 ml[kParts];
+    float o[kParts][E];
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  bad = __any_sync(0xffffffffu, bad);
-  if (__any_sync(0xffffffffu, nan)) M = __int_as_float(0x7fffffff);
-  float den = 0.f, acc[E] = {};
-  for (int p = 0; p < c.x; ++p) {
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(P.part_ml) + part_row(p));
-    // (a part without a maximum saw nothing, or nothing but NaN, which its sum says)
-    const float w = ml.x == -INFINITY ? ml.y * 0.f : exp2f(ml.x - M);
-    const float* o = P.part_o + part_row(p) * D + lane * E;
-    float x[E];
+    for (int k = 0; k < kParts; ++k) {
+      const int p = p0 + k;
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (p < parts) {  // a run's second slot holds the unit that it begins, its first the one it goes on with
+        const int64_t at = (2 * (static_cast<int64_t>(blockIdx.x) + p) + (p == 0 ? 1 : 0)) * kRows + row;
+        ml[k] = __ldcg(reinterpret_cast<const float2*>(P.part_ml) + at);
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 y = __ldcg(reinterpret_cast<const float2*>(o + e));
-      x[e] = y.x;
-      x[e + 1] = y.y;
+        for (int e = 0; e < E; e += 2) {
+          const float2 y = __ldcg(reinterpret_cast<const float2*>(P.part_o + at * D + lane * E + e));
+          o[k][e] = y.x;
+          o[k][e + 1] = y.y;
+        }
+      }
     }
-    if (!(w == 0.f)) {
-      den = fmaf(ml.y, w, den);
+    float top = M;
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(x[e], w, acc[e]);
+    for (int k = 0; k < kParts; ++k) top = fmaxf(top, ml[k].x);
+    const float f = M == top ? 1.f : exp2f(M - top);
+    M = top;
+    den *= f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= f;
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+      bad |= ml[k].y == -1.f;
+      // (a part without a maximum saw nothing, or nothing but NaN, which its sum says)
+      const float w = ml[k].x == -INFINITY ? ml[k].y * 0.f : exp2f(ml[k].x - M);
+      if (w != 0.f && p0 + k < parts) {
+        den = fmaf(ml[k].y, w, den);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(o[k][e], w, acc[e]);
+      }
     }
   }
   const bool zero = bad || den == 0.f;
-  const float inv = zero ? 0.f : 1.f / den;
+  const float inv = 1.f / den;
   const int at = c.z + row;
   float* dst = static_cast<float*>(P.a.a.out) +
                ((static_cast<int64_t>(c.y) + at / P.group) * P.a.a.num_q_heads + head * P.group + at % P.group) * D + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) dst[e] = zero ? 0.f : acc[e] * inv;
+  for (int e = 0; e < E; e += 2) {
+    *reinterpret_cast<float2*>(dst + e) = zero ? make_float2(0.f, 0.f) : make_float2(acc[e] * inv, acc[e + 1] * inv);
+  }
 }
 
 struct Layout32 {
