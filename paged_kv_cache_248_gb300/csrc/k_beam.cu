@@ -435,14 +435,13 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelParams P) 
   Cand floor_c{0, 0xffffffffu};
   if (blocks == P.select) floor_c.hi = buf.get(blocks - 1).hi - 1;
   if (threadIdx.x < blocks) s_blocks[threadIdx.x] = ~buf.get(threadIdx.x).lo;
-  if (threadIdx.x < W) {  // a little below the value that has the floor's score
-    float least = -3.402823466e38f;
-    if (floor_c.hi) {
-      const double at = from_ordered_bits(floor_c.hi), t = at - s_off[threadIdx.x];
-      least = fmaxf(least, static_cast<float>(t - (1e-5 * fabs(t) + 1e-15 * (fabs(at) + fabs(s_off[threadIdx.x])) + 1e-30)));
-    }
-    s_least[threadIdx.x] = least;
-  }
+  // a little below beam w's value that has the floor's score
+  auto least_value = [&](int w) -> float {
+    if (!floor_c.hi) return -3.402823466e38f;
+    const double at = from_ordered_bits(floor_c.hi), t = at - s_off[w];
+    return fmaxf(-3.402823466e38f, static_cast<float>(t - (1e-5 * fabs(t) + 1e-15 * (fabs(at) + fabs(s_off[w])) + 1e-30)));
+  };
+  if (threadIdx.x < W) s_least[threadIdx.x] = least_value(threadIdx.x);
   __syncthreads();
   if (threadIdx.x == 0) s.count = 0;
   __syncthreads();
@@ -451,16 +450,30 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelParams P) 
     uint32_t todo = 0;
     int w = 0, at = 0;
     const T* x = nullptr;
-    if (b0 + warp < blocks) {
+    const bool have = b0 + warp < blocks;
+    Values<T> c;
+    if (have) {
       const int i = static_cast<int>(s_blocks[b0 + warp]);
       w = i / per_row;
       at = (i - w * per_row) * kBlockVals;
+      x = static_cast<const T*>(P.scan.logits) + (n * W + w) * P.scan.row_stride + at;
+      if (!s_done[w]) load_values<T, kAligned>(c, x, V - at);
+    }
+    if (b0 == 0 && !floor_c.hi) {  // fewer blocks than asked for: the lanes' best values give a floor
+      uint64_t top = 0;
+      if (have && s_done[w]) top = lane == 0 ? score_of(w, 0.f) : 0;
+      else if (have) top = score_of(w, max_of(c));
+      const uint32_t least = reached_by(s, P.select, static_cast<uint32_t>(top >> 32));
+      if (least > 0) {
+        floor_c.hi = (static_cast<uint64_t>(least) << 32) - 1;
+        if (threadIdx.x < W) s_least[threadIdx.x] = least_value(threadIdx.x);
+        __syncthreads();
+      }
+    }
+    if (have) {
       if (s_done[w]) {
         todo = lane == 0 ? 1 : 0;
       } else {
-        x = static_cast<const T*>(P.scan.logits) + (n * W + w) * P.scan.row_stride + at;
-        Values<T> c;
-        load_values<T, kAligned>(c, x, V - at);
         const float least = s_least[w];
 #pragma unroll
         for (int k = 0; k < kVals; ++k) todo |= c.get(k) >= least ? 1u << k : 0u;
