@@ -17,7 +17,9 @@ namespace {
 // V rows (one kv head, one piece of a row) and moves them node by node: path[a] >= a
 // because the path ascends, so position c + a is never a source of a later move and a
 // thread may overwrite it once it has loaded the sources up to a.  Columns are
-// independent, so the threads need no order among them.
+// independent, so the threads need no order among them.  8 rows at a time hide the loads' latency:
+// 33 requests in one layer take 2.8 us, 64 in 32 layers (12 of 64 nodes, 92 MB of reads and
+// writes) 14.5 us (13.6 at a copy's rate).
 constexpr int kMoveThreads = 256;
 constexpr int kMoveBatch = 8;     // rows a thread holds in registers between loads and stores
 constexpr int kMoveChunk = 256;   // path entries staged in shared memory at a time
@@ -112,6 +114,8 @@ __global__ void __launch_bounds__(kMoveThreads) compact_path_kernel(const MovePa
 // the free blocks in order of their ids, found by a scan of the counts that stops as soon
 // as every row has its blocks.  fork_finish_kernel (a CTA per row, layer and slice): the
 // copies and the counts of copied and fresh blocks; after an error, everything back.
+// 64 requests of 8 beams and 16 layers copy 503 MB: 74 us, a copy's rate (the first two launches hide
+// behind the copies of the call before).  One request of 5 beams takes 6.5 us, all of it latency.
 //
 // Up to 32 rows of up to kFewBlocks blocks: the assigning CTA gathers by itself, a warp per row,
 // which saves a launch: 6.7 us instead of 7.2 for 5 rows of 20 blocks, 9.4 / 9.9 for 32 of 32,

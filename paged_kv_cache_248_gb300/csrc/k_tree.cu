@@ -67,7 +67,9 @@ __global__ void __launch_bounds__(128) tree_mask_kernel(const int32_t* __restric
 // other, are cut into equal runs, one per CTA; a unit that is cut leaves partials (accumulator,
 // maximum, sum) that the merge kernel joins in the order of the keys.
 //
-// Bound: latency for few requests, fp32 FMAs for many.
+// Bound: latency for few requests, fp32 FMAs and the shared-memory loads that feed them for many.
+// 5 requests of 100 to 700 keys with 3 to 13 nodes, 8 / 2 heads of 64: 12.2 us, of which the
+// joining kernel is 3 (one CTA per node and kv head, keys in turn, took 132).
 constexpr int kRows = 32;      // rows of a unit
 constexpr int kKeys = 64;      // keys of a tile
 constexpr int kThreads = 128;

@@ -12,7 +12,7 @@
 // row tile, or two) and goes over all of the request's key tiles of 128 keys.
 //
 // Cut.  All units' key tiles, one after the other (and two places more for each unit, whose
-// beginning and end take time too: 64 requests 131, 124, 122 us with 0, 1, 3 of them), are cut into
+// beginning and end take time too: 64 requests 123, 112, 110 us with 0, 1, 2 of them), are cut into
 // equal runs, so that one long request and a thousand short ones keep every SM equally busy; a CTA
 // derives its runs from the lengths by itself, without a planning launch.  A unit that lies within
 // one run is finished there; of one that is cut, each run leaves its rows' unnormalised accumulator,
@@ -31,12 +31,22 @@
 //     and every key tile is loaded once for both.
 //
 // Per CTA (352 threads): warp 0 finds the runs' units and loads Q and K, warp 10 loads V (TMA
-// boxes of the blocks' 16-token rows, 128-byte swizzle; 2 K and 2 V tiles in flight), one
-// thread of warp 1 issues the MMAs, warps 2-5 and 6-9 are the streams' softmax.  The tiles
+// boxes of the blocks' 16-token rows, 128-byte swizzle; 2 K and 2 V tiles in flight: a third V tile
+// takes the shared memory that the L1 then lacks, 113 us instead of 108 for the 64 requests; L2 is
+// told to drop what it passed on first, 115 us instead of 123), warp 1 issues the MMAs, warps 2-5
+// and 6-9 are the streams' softmax.  The tiles
 // that hold drafted keys (the last one or two of a request) take their visibility from the
 // mask row's bits, the others see every key.  Their V rows are looked through for values that
 // are not finite: a zero weight times those would reach rows that do not see them, so they
 // are taken out of the tile and given back, at the end, to the rows that do.
+//
+// Bound, 32 / 8 heads: 64 requests of 128..4096 keys with 16 nodes read 558 MB: 102 us, of which the
+// merge is 7 (82 us at a copy's rate; DRAM 72 % busy).  8 requests of 32768 keys with 64 nodes,
+// 64 / 8 heads, are 550 GFLOP: 391 us (290 us at the rate of a large matrix product, 320 us at the one
+// that the power limit sustains); softmax and MMAs of the two streams alternate, about 1900 cycles a
+// turn each, and the tensor pipe is busy for 64 % of the time.  One request of 500 keys: 10.5 us,
+// nearly all latency: 1.3 us until its run is known, 2.5 until its first tile is on its way, 0.6 until
+// that is there, 3 for the products and the softmax, 2 for the merge.
 //
 // All waits are bounded (ptx.cuh).
 #include "ptx.cuh"
@@ -289,7 +299,8 @@ __device__ void find_runs(const Params& P, Ctl& c) {
 }
 
 // The same for up to kFewSeqs requests by warp 0 alone, which is the one that walks the runs: no
-// barriers, and the requests' loads are all on their way at once.
+// barriers, and the requests' loads are all on their way at once (one request 10.7 instead of 11.4
+// us, 64 requests 100.7 instead of 101.9).
 constexpr int kFewSeqs = 128;
 template <int kRuns>
 __device__ void find_runs_few(const Params& P, Ctl& c) {
@@ -835,7 +846,7 @@ __device__ __noinline__ void give_back(const Params& P, const Item& item, const 
 
 // (Code size: the streams, the MMA thread and the producers run different code by turns.  With every
 // loop below unrolled, two thirds of the instruction fetches missed the SM's cache and all of its
-// warps waited for instructions: 64 requests of 128..4096 keys took 169 us instead of MEASURED.)
+// warps waited for instructions: 64 requests of 128..4096 keys took 169 us instead of 124.)
 template <int kRuns>
 __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t tmem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1227,6 +1238,10 @@ int launch_tree_tc(const TreeArgs& t, void* workspace, int num_sms, uint32_t* er
   const uint32_t qbox[3] = {64, static_cast<uint32_t>(p.gp), static_cast<uint32_t>(p.rows_q)};
   st = encode_tensor_map_3d(&qm, a.q, qdims, qstrides, qbox);
   if (st) return st;
+  // Requests with more rows than a tile share K and V between two of them (33 requests of up to 61
+  // nodes, 12 / 4 heads: 34 us, and 40 with single row tiles).  The others have streams that work for
+  // themselves (64 requests of 16 nodes: 101 us, and 107 in pairs, whose second stream would rest;
+  // one request: 10.7 and 12.1).
   const bool pairs = a.max_query_len > p.rows_q;
   p.unit_q = pairs ? 2 * p.rows_q : p.rows_q;
   p.unit_q_log2 = 7 - p.gp_log2 + (pairs ? 1 : 0);
@@ -1262,14 +1277,9 @@ int launch_tree_tc(const TreeArgs& t, void* workspace, int num_sms, uint32_t* er
   p.rows_cap = l.rows_cap;
   p.out_v8 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 ? 1 : 0;
   // Few rows: a warp takes as long for one live row as for 32, so the streams' live rows go to
-  // different SM sub-partitions (a warp's TMEM quarter is its sub-partition), away from the MMA
-  // thread's and the K producer's (1 and 0) where one warp is enough for each.
-  if (!pairs && l.rows_cap <= 32) {
-    p.row0[0] = 64;
-    p.row0[1] = 96;
-  } else if (!pairs && l.rows_cap <= 64) {
-    p.row0[1] = 64;
-  }
+  // different SM sub-partitions (a warp's TMEM quarter is its sub-partition): 100.7 instead of 101.6
+  // us for 64 requests of 16 nodes.
+  if (!pairs && l.rows_cap <= 64) p.row0[1] = 64;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   auto* kernel = pairs ? tree_kernel<true> : tree_kernel<false>;
   static uint64_t smem_set[2] = {0, 0};
