@@ -103,7 +103,8 @@ __device__ __forceinline__ Request32 request_of(const Params32& P, int i) {
   const int32_t q0 = __ldg(A.qsl + i), q1 = __ldg(A.qsl + i + 1), len = __ldg(A.seq_lens + i);
   const int64_t n = static_cast<int64_t>(q1) - q0;
   const bool rows = n > 0 && q0 >= 0 && q1 <= A.num_tokens;
-  bool fits = rows && len >= n && n <= A.max_query_len && (static_cast<int64_t>(len) + kBlock - 1) / kBlock <= A.max_blocks;
+  bool fits = rows && len >= n && len <= kMaxLen && n <= A.max_query_len &&
+              (static_cast<int64_t>(len) + kBlock - 1) / kBlock <= A.max_blocks;
   r.t0 = q0;
   r.q_len = rows ? static_cast<int32_t>(n) : 0;
   r.len = len;

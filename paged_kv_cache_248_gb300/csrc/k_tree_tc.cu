@@ -181,7 +181,8 @@ __device__ __forceinline__ Request make_request(const Params& P, int32_t q0, int
   Request r;
   const int64_t n = static_cast<int64_t>(q1) - q0;
   const bool rows = n > 0 && q0 >= 0 && q1 <= P.num_tokens;
-  bool fits = rows && len >= n && n <= P.max_q && (static_cast<int64_t>(len) + kBlock - 1) / kBlock <= P.max_blocks;
+  bool fits = rows && len >= n && len <= kMaxLen && n <= P.max_q &&
+              (static_cast<int64_t>(len) + kBlock - 1) / kBlock <= P.max_blocks;
   r.t0 = q0;
   r.q_len = rows ? static_cast<int32_t>(n) : 0;
   r.len = len;
@@ -1205,7 +1206,7 @@ Layout layout_of(int32_t group, int32_t max_query_len, int num_sms) {
   Layout l;
   const int64_t rows = static_cast<int64_t>(max_query_len) << gp_log2_of(group);
   l.rows_cap = static_cast<int>(rows < 256 ? rows : 256);
-  const size_t runs = 2 * static_cast<size_t>(num_sms);  // at most two a CTA
+  const size_t runs = (rows > kTileKeys ? 1 : 2) * static_cast<size_t>(num_sms);  // of each CTA one, or two
   const size_t slots = 2 * runs * l.rows_cap;
   l.o_bytes = slots * 128 * sizeof(float);
   l.ml_bytes = (slots * 2 * sizeof(float) + 255) & ~static_cast<size_t>(255);

@@ -324,6 +324,7 @@ int encode_tensor_map_2d(CUtensorMap* map, const void* base, uint64_t inner, uin
                          uint32_t box_inner, uint32_t box_outer);
 
 // Candidate continuations: drafted trees (k_tree*.cu), pages (k_pages.cu), beams (k_beam.cu).
+constexpr int32_t kMaxLen = 0x7fffffff - 1023;  // of a request with a drafted tree: its tiles' ends fit 32 bits
 struct TreeArgs {
   AttnArgs a;
   const uint64_t* mask;  // [num_tokens][mask_words]

@@ -198,13 +198,14 @@ def test_tree_shared_blocks_and_empty_requests(pkv):
     check(b.run(pkv), *b.expected())
 
 
-def test_tree_bad_data_is_flagged_and_zeroed(pkv):
-    b = Tree(11, [100, 40, 30, 64], [3, 4, 5, 2], 8, 2)
+@pytest.mark.parametrize("dtype,d,more", [(BF, 128, 0), (BF, 128, 130), (F32, 64, 0)])
+def test_tree_bad_data_is_flagged_and_zeroed(pkv, dtype, d, more):
+    b = Tree(11, [100, 40, 30, 64] + [20] * more, [3, 4, 5, 2] + [2] * more, 8, 2, dtype=dtype, d=d)
     want, tol = b.expected()
     tables, lens = b.tables.copy(), b.lens.copy()
     b.tables[0, 2], b.tables[3, 1] = -1, 10**6    # ids outside of the pool
     b.lens[1] = 2                                 # shorter than its draft
-    got = b.run(pkv, out=torch.full(b.q.shape, float("nan"), dtype=BF, device="cuda"))
+    got = b.run(pkv, out=torch.full(b.q.shape, float("nan"), dtype=dtype, device="cuda"))
     assert pkv.pkv_peek_error_bits() == 0b101
     assert pkv.pkv_get_last_error() == pkv.PKV_ERR_INDEX
     sl = [slice(b.qsl[i], b.qsl[i + 1]) for i in range(4)]
@@ -212,10 +213,11 @@ def test_tree_bad_data_is_flagged_and_zeroed(pkv):
         assert (got[sl[i]] == 0).all(), i
     check(got[sl[2]], want[sl[2]], tol[sl[2]])
     b.tables, b.lens = tables, lens
-    b.lens[2] = 16 * b.tables.shape[1] + 1        # more keys than the table has room for
-    got = b.run(pkv)
-    assert pkv.pkv_get_last_error() == pkv.PKV_ERR_INDEX
-    assert (got[sl[2]] == 0).all()
+    for wrong in (16 * b.tables.shape[1] + 1, 2**31 - 5):  # more keys than the table has room for
+        b.lens[2] = wrong
+        got = b.run(pkv)
+        assert pkv.pkv_get_last_error() == pkv.PKV_ERR_INDEX
+        assert (got[sl[2]] == 0).all()
     b.lens[2] = lens[2]
     got = b.run(pkv, max_q=4)                     # a draft past the caller's bound
     assert pkv.pkv_get_last_error() == pkv.PKV_ERR_INDEX
