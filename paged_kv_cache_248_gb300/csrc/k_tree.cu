@@ -70,10 +70,13 @@ __global__ void __launch_bounds__(128) tree_mask_kernel(const int32_t* __restric
 // Bound: latency for few requests, fp32 FMAs and the shared-memory loads that feed them for many.
 // 5 requests of 100 to 700 keys with 3 to 13 nodes, 8 / 2 heads of 64: 12.2 us, of which the
 // joining kernel is 3 (one CTA per node and kv head, keys in turn, took 132).
+// 4 requests of 4000 keys with 24 nodes, 32 / 8 heads of 64 (3.1 GFLOP): 104 us, 40 % of the FMA
+// rate, with four CTAs an SM (two: 129); heads of 128 leave room for two.
 constexpr int kRows = 32;      // rows of a unit
 constexpr int kKeys = 64;      // keys of a tile
 constexpr int kThreads = 128;
-constexpr int kCtasPerSm = 2;
+template <int D>
+constexpr int kCtasPerSm = D == 64 ? 4 : 2;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Cut32 {
@@ -118,6 +121,15 @@ __device__ __forceinline__ Request32 request_of(const Params32& P, int i) {
   return r;
 }
 
+// d += a * b, two values at a time: half the instructions of single ones, which leaves issue slots
+// for the shared-memory loads.
+__device__ __forceinline__ void fma_pair(float2& d, const float2& a, const float2& b) {
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%0, %1};\n\t"
+      "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "+f"(d.x), "+f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+}
+
 // One tile's rows (K or V) into shared memory, rows past the context as zeros.
 template <int D>
 __device__ __forceinline__ void stage_tile(float* dst, const float* src, const int32_t* ids, int k0, int len, int head, int hkv) {
@@ -137,8 +149,8 @@ __device__ __forceinline__ void stage_tile(float* dst, const float* src, const i
 
 // The result's 4 rows += P V over a tile; kDrafted: keys of weight 0 are left out, whatever V holds.
 template <int D, bool kDrafted>
-__device__ __forceinline__ void add_pv(float (&o)[4][D / 16], const float* sp, const float* sv, int rg, int cg) {
-  constexpr int C = D / 16;
+__device__ __forceinline__ void add_pv(float2 (&o)[4][D / 32], const float* sp, const float* sv, int rg, int cg) {
+  constexpr int C = D / 32;  // pairs of result columns
 #pragma unroll 2
   for (int u = 0; u < kKeys; u += 4) {
     float4 p[4];
@@ -146,21 +158,19 @@ __device__ __forceinline__ void add_pv(float (&o)[4][D / 16], const float* sp, c
     for (int r = 0; r < 4; ++r) p[r] = *reinterpret_cast<const float4*>(sp + (4 * rg + r) * (kKeys + 4) + u);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      float v[C];
+      float2 v[C];
 #pragma unroll
-      for (int c = 0; c < C; c += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(sv + (u + e) * (D + 4) + 64 * (c / 4) + 4 * cg);
-        v[c] = x.x;
-        v[c + 1] = x.y;
-        v[c + 2] = x.z;
-        v[c + 3] = x.w;
+      for (int c = 0; c < C; c += 2) {
+        const float4 x = *reinterpret_cast<const float4*>(sv + (u + e) * (D + 4) + 64 * (c / 2) + 4 * cg);
+        v[c] = make_float2(x.x, x.y);
+        v[c + 1] = make_float2(x.z, x.w);
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float w = e == 0 ? p[r].x : e == 1 ? p[r].y : e == 2 ? p[r].z : p[r].w;
         if (!kDrafted || !(w == 0.f)) {
 #pragma unroll
-          for (int c = 0; c < C; ++c) o[r][c] = fmaf(w, v[c], o[r][c]);
+          for (int c = 0; c < C; ++c) fma_pair(o[r][c], make_float2(w, w), v[c]);
         }
       }
     }
@@ -171,8 +181,8 @@ template <int D>
 constexpr int kSmem32 = (kRows * (D + 4) + 2 * kKeys * (D + 4) + kRows * (kKeys + 4)) * static_cast<int>(sizeof(float));
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_f32_kernel(const Params32 P) {
-  constexpr int C = D / 16;  // result columns of a thread
+__global__ void __launch_bounds__(kThreads, kCtasPerSm<D>) tree_f32_kernel(const Params32 P) {
+  constexpr int C = D / 32;  // pairs of result columns of a thread
   extern __shared__ __align__(16) float smem[];
   float* sq = smem;
   float* sk = sq + kRows * (D + 4);
@@ -290,13 +300,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_f32_kernel(const Pa
     __syncthreads();
     stage_tile<D>(sk, kc, s_ids[0], first * kKeys, rq.len, head, P.hkv);
     stage_tile<D>(sv, vc, s_ids[0], first * kKeys, rq.len, head, P.hkv);
-    float m[4], l[4], o[4][C];
+    float m[4], l[4];
+    float2 o[4][C];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       m[r] = -INFINITY;
       l[r] = 0.f;
 #pragma unroll
-      for (int c = 0; c < C; ++c) o[r][c] = 0.f;
+      for (int c = 0; c < C; ++c) o[r][c] = make_float2(0.f, 0.f);
     }
     for (int j = 0; j < nt; ++j) {
       const int k0 = (first + j) * kKeys;
@@ -305,11 +316,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_f32_kernel(const Pa
       asm volatile("cp.async.wait_group 1;" ::: "memory");  // K has landed
       __syncthreads();
       // scores of 4 rows and keys cg, cg + 16, cg + 32, cg + 48
-      float s[4][4];
+      // (sums of the even and of the odd columns)
+      float2 s2[4][4];
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[r][e] = 0.f;
+        for (int e = 0; e < 4; ++e) s2[r][e] = make_float2(0.f, 0.f);
 #pragma unroll 4
       for (int d = 0; d < D; d += 4) {
         float4 a[4], b[4];
@@ -320,19 +332,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_f32_kernel(const Pa
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            s[r][e] = fmaf(a[r].w, b[e].w, fmaf(a[r].z, b[e].z, fmaf(a[r].y, b[e].y, fmaf(a[r].x, b[e].x, s[r][e]))));
+          for (int e = 0; e < 4; ++e) {
+            fma_pair(s2[r][e], make_float2(a[r].x, a[r].y), make_float2(b[e].x, b[e].y));
+            fma_pair(s2[r][e], make_float2(a[r].z, a[r].w), make_float2(b[e].z, b[e].w));
+          }
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const uint64_t* mrow = P.a.mask + (static_cast<int64_t>(rq.t0) + (row0 + min(4 * rg + r, rows - 1)) / P.group) * P.a.mask_words;
-        float top = -INFINITY;
+        float s[4], top = -INFINITY;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int u = k0 + cg + 16 * e - ctx;  // below 0: context
           const bool seen = !drafted || u < 0 || (u < rq.q_len && (__ldg(mrow + u / 64) >> (u % 64) & 1));
-          s[r][e] = seen ? s[r][e] * P.scale_log2 : -INFINITY;
-          top = fmaxf(top, s[r][e]);
+          s[e] = seen ? (s2[r][e].x + s2[r][e].y) * P.scale_log2 : -INFINITY;
+          top = fmaxf(top, s[e]);
         }
 #pragma unroll
         for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -342,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_f32_kernel(const Pa
         float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float p = exp2f(s[r][e] - m_use);
+          const float p = exp2f(s[e] - m_use);
           sum += p;
           sp[(4 * rg + r) * (kKeys + 4) + cg + 16 * e] = p;
         }
@@ -351,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_f32_kernel(const Pa
         l[r] = l[r] * alpha + sum;
         m[r] = m_new;
 #pragma unroll
-        for (int c = 0; c < C; ++c) o[r][c] *= alpha;
+        for (int c = 0; c < C; ++c) o[r][c] = make_float2(o[r][c].x * alpha, o[r][c].y * alpha);
       }
       asm volatile("cp.async.wait_group 0;" ::: "memory");  // V has landed
       __syncthreads();
@@ -382,9 +396,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_f32_kernel(const Pa
       }
       const bool zero = slot < 0 && (bad || l[r] == 0.f);
 #pragma unroll
-      for (int c = 0; c < C; c += 4)
-        *reinterpret_cast<float4*>(dst + 64 * (c / 4) + 4 * cg) =
-            zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[r][c] * f, o[r][c + 1] * f, o[r][c + 2] * f, o[r][c + 3] * f);
+      for (int c = 0; c < C; c += 2)
+        *reinterpret_cast<float4*>(dst + 64 * (c / 2) + 4 * cg) =
+            zero ? make_float4(0.f, 0.f, 0.f, 0.f)
+                 : make_float4(o[r][c].x * f, o[r][c].y * f, o[r][c + 1].x * f, o[r][c + 1].y * f);
     }
     __syncthreads();
   }
@@ -459,7 +474,7 @@ struct Layout32 {
   size_t o_bytes, ml_bytes, bytes;
 };
 Layout32 layout32(int d, int num_sms) {
-  const size_t runs = static_cast<size_t>(kCtasPerSm) * num_sms, rows = 2 * runs * kRows;
+  const size_t runs = static_cast<size_t>(d == 64 ? kCtasPerSm<64> : kCtasPerSm<128>) * num_sms, rows = 2 * runs * kRows;
   Layout32 l;
   l.o_bytes = rows * d * sizeof(float);
   l.ml_bytes = (rows * 2 * sizeof(float) + 255) & ~static_cast<size_t>(255);
@@ -480,8 +495,8 @@ int launch_f32(const TreeArgs& t, void* workspace, int num_sms, uint32_t* err, c
   p.hkv = a.cache.num_kv_heads;
   p.group = a.num_q_heads / p.hkv;
   p.scale_log2 = a.scale * kLog2e;
-  // CTAs: kCtasPerSm per SM, fewer where the caller's bounds leave less to do
-  const int64_t most = static_cast<int64_t>(kCtasPerSm) * num_sms;
+  // CTAs: as many as fit, fewer where the caller's bounds leave less to do
+  const int64_t most = static_cast<int64_t>(kCtasPerSm<D>) * num_sms;
   const int64_t units = (static_cast<int64_t>(a.max_query_len) * p.group + kRows - 1) / kRows * p.hkv;
   const int64_t tiles = units * ((static_cast<int64_t>(a.max_seq_len) + kKeys - 1) / kKeys);
   const int64_t want = tiles >= most ? most : tiles * a.num_seqs;
