@@ -26,7 +26,7 @@
 // that one softmax runs while the tensor core works for the other.
 //   tree_kernel<false>: a stream has a run of its own, of units of one row tile; the streams
 //     take turns at the tensor core and at the rings, a tile each, and one's last rows are
-//     stored while the other goes on.
+//     stored while the other goes on (requests of few rows, or few keys).
 //   tree_kernel<true>: a CTA has one run, of units of two row tiles; a stream is a row tile,
 //     and every key tile is loaded once for both.
 //
@@ -65,6 +65,7 @@ constexpr int kRing = 4;                    // items published ahead, per ring
 constexpr uint32_t kTmemCols = 512;         // S_0, S_1 (P over their first 64 columns), O_0, O_1
 constexpr uint32_t kOCol = 256;
 constexpr int kBlocksPerTile = kTileKeys / kBlock;
+constexpr int kShortKeys = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled when a row's maximum grows by > 2^8
 
 // A part of a unit: what one run does of it.
@@ -1202,11 +1203,11 @@ struct Layout {
   int rows_cap;
   size_t o_bytes, ml_bytes, bytes;
 };
-Layout layout_of(int32_t group, int32_t max_query_len, int num_sms) {
+Layout layout_of(int32_t group, int32_t max_query_len, int num_sms, bool pairs) {
   Layout l;
-  const int64_t rows = static_cast<int64_t>(max_query_len) << gp_log2_of(group);
-  l.rows_cap = static_cast<int>(rows < 256 ? rows : 256);
-  const size_t runs = (rows > kTileKeys ? 1 : 2) * static_cast<size_t>(num_sms);  // of each CTA one, or two
+  const int64_t rows = static_cast<int64_t>(max_query_len) << gp_log2_of(group), most = pairs ? 256 : 128;
+  l.rows_cap = static_cast<int>(rows < most ? rows : most);
+  const size_t runs = (pairs ? 1 : 2) * static_cast<size_t>(num_sms);
   const size_t slots = 2 * runs * l.rows_cap;
   l.o_bytes = slots * 128 * sizeof(float);
   l.ml_bytes = (slots * 2 * sizeof(float) + 255) & ~static_cast<size_t>(255);
@@ -1217,7 +1218,7 @@ Layout layout_of(int32_t group, int32_t max_query_len, int num_sms) {
 }  // namespace
 
 size_t tree_tc_workspace(int32_t group, int32_t max_query_len, int num_sms) {
-  return layout_of(group, max_query_len, num_sms).bytes;
+  return layout_of(group, max_query_len, num_sms, false).bytes;  // (the other is never larger)
 }
 
 int launch_tree_tc(const TreeArgs& t, void* workspace, int num_sms, uint32_t* err, cudaStream_t s) {
@@ -1239,11 +1240,13 @@ int launch_tree_tc(const TreeArgs& t, void* workspace, int num_sms, uint32_t* er
   const uint32_t qbox[3] = {64, static_cast<uint32_t>(p.gp), static_cast<uint32_t>(p.rows_q)};
   st = encode_tensor_map_3d(&qm, a.q, qdims, qstrides, qbox);
   if (st) return st;
-  // Requests with more rows than a tile share K and V between two of them (33 requests of up to 61
-  // nodes, 12 / 4 heads: 34 us, and 40 with single row tiles).  The others have streams that work for
-  // themselves (64 requests of 16 nodes: 101 us, and 107 in pairs, whose second stream would rest;
-  // one request: 10.7 and 12.1).
-  const bool pairs = a.max_query_len > p.rows_q;
+  // Requests with more rows than a tile share K and V between two of them, if they are long: 68 requests
+  // with 12 / 4 heads and 61 nodes each take 56, 79 us with 1500, 3000 keys, and 70, 110 in single row
+  // tiles.  For short ones a unit's beginning and end count more, which streams that work for
+  // themselves have twice as fast: 6 requests of 40, 200, 400 keys take 11.4, 15.4, 15.9 us (17.4,
+  // 20.8, 20.9 in pairs), 68 of 400 with 2 to 61 nodes 32.5 (34.1).  Where no request has more rows
+  // than a tile, the second stream of a pair would rest: 64 requests of 16 nodes 101 us (107 in pairs).
+  const bool pairs = a.max_query_len > p.rows_q && a.max_seq_len > kShortKeys;
   p.unit_q = pairs ? 2 * p.rows_q : p.rows_q;
   p.unit_q_log2 = 7 - p.gp_log2 + (pairs ? 1 : 0);
   // CTAs: one per SM, fewer where the caller's bounds leave less to do
@@ -1255,7 +1258,7 @@ int launch_tree_tc(const TreeArgs& t, void* workspace, int num_sms, uint32_t* er
   const int ctas = static_cast<int>(most < min_tiles * num_sms ? (most + min_tiles - 1) / min_tiles : num_sms);
   p.unit_cost = most < 2 * num_sms ? 0 : 2;
   p.min_run = min_tiles + p.unit_cost;
-  const Layout l = layout_of(group, a.max_query_len, num_sms);
+  const Layout l = layout_of(group, a.max_query_len, num_sms, pairs);
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.v_cache = static_cast<const __nv_bfloat16*>(a.v_cache);
   p.bt = a.block_tables;

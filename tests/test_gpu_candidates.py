@@ -125,13 +125,13 @@ def test_tree_chain_matches_chunked_prefill(pkv):
     check(plain, *b.expected())
 
 
-@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
-def test_tree_any_mask_and_rows_that_see_nothing(pkv, dtype, d):
+@pytest.mark.parametrize("dtype,d,far", [(BF, 128, 0), (BF, 128, 600), (F32, 64, 0)])
+def test_tree_any_mask_and_rows_that_see_nothing(pkv, dtype, d, far):
     def mask(rng, b, words):  # any bits at all, bits past the draft among them, and empty rows
         m = rng.integers(0, 1 << 63, (int(b.qsl[-1]), words), dtype=np.uint64)
         m[rng.random(len(m)) < 0.3] = 0
         return m
-    b = Tree(5, [0, 0, 33, 130, 0], [40, 1, 70, 20, 100], 8, 2, mask=mask, words=3, dtype=dtype, d=d)
+    b = Tree(5, [0, 0, 33, 130 + far, 0], [40, 1, 70, 20, 100], 8, 2, mask=mask, words=3, dtype=dtype, d=d)
     want, tol = b.expected()
     assert (want == 0).flatten(1).all(1).sum() > 5
     check(b.run(pkv), want, tol)
