@@ -382,7 +382,7 @@ __device__ __forceinline__ Walk start_walk(const Run& r) {
 }
 
 // The next item of run number `run` (idx -1: none is left).
-__device__ __noinline__ Item next_item(const Params& P, Walk& k, int run, int64_t run_len) {
+__device__ __forceinline__ Item next_item(const Params& P, Walk& k, int run, int64_t run_len) {
   Item info{};
   info.idx = -1;
   while (k.pos < k.end) {
@@ -786,10 +786,8 @@ __device__ __noinline__ uint64_t seen_bits(const uint64_t* row, int words, int q
   return left < 64 ? b & ((uint64_t(1) << left) - 1) : b;
 }
 
-// Whether some bf16 of the pair is an infinity or NaN.
-__device__ __forceinline__ bool not_finite2(uint32_t x) {
-  return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
-}
+// Bits 15 and 31 tell whether a bf16 of the pair is an infinity or NaN (its exponent all ones).
+__device__ __forceinline__ uint32_t not_finite2(uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; }
 
 // The pair with a zero in the place of each infinity or NaN.
 __device__ __forceinline__ uint32_t finite2(uint32_t x) {
@@ -801,24 +799,35 @@ __device__ __forceinline__ uint32_t finite2(uint32_t x) {
 // Takes what is not finite out of row r of a V tile (all of a row past the context), so that a
 // weight of 0 can stand for a key that a row does not see.  Returns whether it took something
 // out that a row may see.
-__device__ __forceinline__ bool clean_v_row(uint8_t* vtile, int r, bool past) {
+__device__ __noinline__ bool clean_v_row(uint8_t* vtile, int r, bool past) {
   // starting each lane at chunk r mod 8 spreads eight lanes over all banks
   uint8_t* row = vtile + r * 128;
-  bool wrote = past, spoilt = false;
+  bool spoilt = false;
 #pragma unroll 1
-  for (int ch = 0; ch < 16; ++ch) {
-    uint4* at = reinterpret_cast<uint4*>(row + (ch >> 3) * kHalfBytes + ((ch + r) & 7) * 16);
+  for (int half = 0; half < 2; ++half, row += kHalfBytes) {
     if (past) {
-      *at = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int ch = 0; ch < 8; ++ch) *reinterpret_cast<uint4*>(row + ((ch + r) & 7) * 16) = make_uint4(0, 0, 0, 0);
       continue;
     }
-    const uint4 x = *at;
-    if (not_finite2(x.x) | not_finite2(x.y) | not_finite2(x.z) | not_finite2(x.w)) {
-      *at = make_uint4(finite2(x.x), finite2(x.y), finite2(x.z), finite2(x.w));
-      wrote = spoilt = true;
+    uint4 x[8];
+    uint32_t any = 0;
+#pragma unroll
+    for (int ch = 0; ch < 8; ++ch) x[ch] = *reinterpret_cast<uint4*>(row + ((ch + r) & 7) * 16);
+#pragma unroll
+    for (int ch = 0; ch < 8; ++ch)
+      any |= not_finite2(x[ch].x) | not_finite2(x[ch].y) | not_finite2(x[ch].z) | not_finite2(x[ch].w);
+    if (any & 0x80008000u) {
+      spoilt = true;
+#pragma unroll 1
+      for (int ch = 0; ch < 8; ++ch) {
+        uint4* at = reinterpret_cast<uint4*>(row + ((ch + r) & 7) * 16);
+        const uint4 y = *at;
+        *at = make_uint4(finite2(y.x), finite2(y.y), finite2(y.z), finite2(y.w));
+      }
     }
   }
-  if (wrote) fence_proxy_async_smem();
+  if (past || spoilt) fence_proxy_async_smem();
   return spoilt;
 }
 
