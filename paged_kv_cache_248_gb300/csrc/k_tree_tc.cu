@@ -40,13 +40,13 @@
 // are not finite: a zero weight times those would reach rows that do not see them, so they
 // are taken out of the tile and given back, at the end, to the rows that do.
 //
-// Bound, 32 / 8 heads: 64 requests of 128..4096 keys with 16 nodes read 558 MB: 102 us, of which the
+// Bound, 32 / 8 heads: 64 requests of 128..4096 keys with 16 nodes read 558 MB: 101 us, of which the
 // merge is 7 (82 us at a copy's rate; DRAM 72 % busy).  8 requests of 32768 keys with 64 nodes,
-// 64 / 8 heads, are 550 GFLOP: 391 us (290 us at the rate of a large matrix product, 320 us at the one
-// that the power limit sustains); softmax and MMAs of the two streams alternate, about 1900 cycles a
-// turn each, and the tensor pipe is busy for 64 % of the time.  One request of 500 keys: 10.5 us,
-// nearly all latency: 1.3 us until its run is known, 2.5 until its first tile is on its way, 0.6 until
-// that is there, 3 for the products and the softmax, 2 for the merge.
+// 64 / 8 heads, are 550 GFLOP: 375 to 420 us as the power limit has it (290 us at the rate of a large
+// matrix product, 320 us at the one that the limit sustains); softmax and MMAs of the two streams
+// alternate, about 1900 cycles a turn each, and the tensor pipe is busy for 64 % of the time.  One
+// request of 500 keys: 9.6 us, nearly all latency: 1.3 us until its run is known, 2 until its first tile
+// is on its way, 0.6 until that is there, 3 for the products and the softmax, 2 for the merge.
 //
 // All waits are bounded (ptx.cuh).
 #include "ptx.cuh"
@@ -1000,34 +1000,40 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
       dst = reinterpret_cast<uint8_t*>(P.part_o + (static_cast<int64_t>(part) * P.rows_cap + 128 * tile + row) * 128);
     const bool zero = bad || l_sum == 0.f;
     const float inv = 1.f / l_sum;
-#pragma unroll 1  // a quarter of the row at a time keeps the code and the registers small
-    for (int h = 0; h < 4; ++h) {
-      uint32_t v[32];
-      tmem_ld32_issue(orow + 32 * h, v);
-      tmem_ld32_wait(v);
-      if (live && part >= 0) {
+#pragma unroll 1  // half of the row at a time keeps the code and the registers small
+    for (int g = 0; g < 2; ++g) {
+      uint32_t v[2][32];
+      tmem_ld32_issue(orow + 64 * g, v[0]);
+      tmem_ld32_issue(orow + 64 * g + 32, v[1]);
+      tmem_ld32_wait(v[0]);
+      tmem_ld32_wait(v[1]);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          st_global_v8(dst + 128 * h + 32 * q, *reinterpret_cast<const uint32_t(*)[8]>(v + 8 * q));
-      } else if (live) {
+      for (int h = 0; h < 2; ++h) {
+        if (live && part >= 0) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t wv[8];
+          for (int q = 0; q < 4; ++q)
+            st_global_v8(dst + 256 * g + 128 * h + 32 * q, *reinterpret_cast<const uint32_t(*)[8]>(v[h] + 8 * q));
+        } else if (live) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(v[16 * q + 2 * e]) * inv,
-                                                            __uint_as_float(v[16 * q + 2 * e + 1]) * inv);
-            wv[e] = zero ? 0u : *reinterpret_cast<const uint32_t*>(&h2);
-          }
-          if (P.out_v8) {
-            st_global_v8(dst + 64 * h + 32 * q, wv);
-          } else {
-            reinterpret_cast<uint4*>(dst + 64 * h + 32 * q)[0] = make_uint4(wv[0], wv[1], wv[2], wv[3]);
-            reinterpret_cast<uint4*>(dst + 64 * h + 32 * q)[1] = make_uint4(wv[4], wv[5], wv[6], wv[7]);
+          for (int q = 0; q < 2; ++q) {
+            uint32_t wv[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(v[h][16 * q + 2 * e]) * inv,
+                                                              __uint_as_float(v[h][16 * q + 2 * e + 1]) * inv);
+              wv[e] = zero ? 0u : *reinterpret_cast<const uint32_t*>(&h2);
+            }
+            uint8_t* to = dst + 128 * g + 64 * h + 32 * q;
+            if (P.out_v8) {
+              st_global_v8(to, wv);
+            } else {
+              reinterpret_cast<uint4*>(to)[0] = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+              reinterpret_cast<uint4*>(to)[1] = make_uint4(wv[4], wv[5], wv[6], wv[7]);
+            }
           }
         }
+        __syncwarp();
       }
-      __syncwarp();
     }
     if (live && part >= 0) {  // maximum and sum (a sum of -1: a bad block id)
       float* ml = P.part_ml + (static_cast<int64_t>(part) * P.rows_cap + 128 * tile + row) * 2;
