@@ -6,7 +6,7 @@
  * checks them, makes results and scratch and calls libpkv.
  *
  * torch.empty takes as long as such a call (5 us beside a launch on a Grace core), so small
- * results are made 32 at a time, away from the launches (1.4 us each), and handed out once each;
+ * results are made many at a time, away from the launches (1.4 us each), and handed out once each;
  * and scratch is kept per device, stream and call.  Work on one stream runs in order, and the GIL
  * is held while libpkv enqueues a call's kernels, so two calls never use one scratch at the same
  * time.  Where neither is safe -- while the stream is captured into a graph, whose
@@ -173,39 +173,57 @@ static PyObject* made(int dim, const i64* n, PyObject* dtype, const Place* w) {
   return r;
 }
 
-/* A new tensor of four bytes a value or two, small ones from a store of ready ones. */
+/* A new tensor, those of up to 64 KB from a store of ready ones: per type, shape and stream a list of
+ * how many to make next and those that are left.  The first call of a shape makes one, later ones
+ * 8 and then 32, up to 256 KB: shapes that come once cost no more than torch.empty. */
 static PyObject* take_result(int dim, const i64* n, PyObject* dtype, const Place* w) {
-  enum { kParts = 32, kMostBytes = 2048 };
-  i64 values = 1;
-  for (int i = 0; i < dim; ++i) values *= n[i];
-  if (!w->keep || dim > 2 || values * 4 > kMostBytes || values == 0) return made(dim, n, dtype, w);
+  enum { kMostReady = 32, kMostBytes = 65536, kMostKept = 262144 };
+  i64 bytes = dtype == T.bf16 ? 2 : 4;
+  for (int i = 0; i < dim; ++i) bytes = n[i] > kMostBytes ? kMostBytes + 1 : bytes * n[i];
+  if (!w->keep || dim > 3 || bytes > kMostBytes || bytes <= 0) return made(dim, n, dtype, w);
   struct {
     PyObject* dtype;
     void* stream;
-    i64 dev, n[2];
-  } key = {dtype, w->stream, w->dev, {n[0], dim > 1 ? n[1] : -1}};
+    i64 dev, n[3];
+  } key = {dtype, w->stream, w->dev, {n[0], dim > 1 ? n[1] : -1, dim > 2 ? n[2] : -1}};
   PyObject* k = PyBytes_FromStringAndSize((const char*)&key, sizeof key);
   if (!k) return NULL;
   PyObject* r = NULL;
-  PyObject* ready = Py_XNewRef(PyDict_GetItemWithError(T.results, k)); /* a list; torch may let other threads run */
+  PyObject* ready = Py_XNewRef(PyDict_GetItemWithError(T.results, k)); /* (torch may let other threads run) */
   if (!ready && !PyErr_Occurred()) {
     if (PyDict_GET_SIZE(T.results) >= 512) PyDict_Clear(T.results);
-    ready = PyList_New(0);
+    ready = Py_BuildValue("[i]", 1);
     if (ready && PyDict_SetItem(T.results, k, ready)) Py_CLEAR(ready);
   }
-  if (ready && PyList_GET_SIZE(ready) == 0) {
-    PyObject* parts = dim == 1 ? PyObject_CallFunction(T.ready, "i(L)OL", kParts, (long long)n[0], dtype, (long long)w->dev)
-                               : PyObject_CallFunction(T.ready, "i(LL)OL", kParts, (long long)n[0], (long long)n[1], dtype, (long long)w->dev);
-    if (!parts || PyList_SetSlice(ready, 0, 0, parts)) Py_CLEAR(ready);
-    Py_XDECREF(parts);
-  }
-  if (ready) {
+  Py_DECREF(k);
+  if (!ready) return NULL;
+  if (PyList_GET_SIZE(ready) == 1) {
+    const long count = PyLong_AsLong(PyList_GET_ITEM(ready, 0));
+    long next = count * 8 < kMostReady ? count * 8 : kMostReady;
+    if (next * bytes > kMostKept) next = kMostKept / bytes;
+    if (count == 1) {
+      r = made(dim, n, dtype, w);
+    } else {
+      PyObject* shape = dim == 1   ? Py_BuildValue("(L)", (long long)n[0])
+                        : dim == 2 ? Py_BuildValue("(LL)", (long long)n[0], (long long)n[1])
+                                   : Py_BuildValue("(LLL)", (long long)n[0], (long long)n[1], (long long)n[2]);
+      PyObject* more = shape ? PyObject_CallFunction(T.ready, "lOOL", count, shape, dtype, (long long)w->dev) : NULL;
+      if (more && PyList_GET_SIZE(more) > 0 && !PyList_SetSlice(ready, 1, 1, more)) {
+        const Py_ssize_t last = PyList_GET_SIZE(ready) - 1;
+        r = Py_NewRef(PyList_GET_ITEM(ready, last));
+        if (PyList_SetSlice(ready, last, last + 1, NULL)) Py_CLEAR(r);
+      }
+      Py_XDECREF(more);
+      Py_XDECREF(shape);
+    }
+    PyObject* number = PyLong_FromLong(next);
+    if (!number || PyList_SetItem(ready, 0, number)) Py_CLEAR(r);
+  } else {
     const Py_ssize_t last = PyList_GET_SIZE(ready) - 1;
     r = Py_NewRef(PyList_GET_ITEM(ready, last));
     if (PyList_SetSlice(ready, last, last + 1, NULL)) Py_CLEAR(r);
   }
-  Py_XDECREF(ready);
-  Py_DECREF(k);
+  Py_DECREF(ready);
   return r;
 }
 

@@ -746,7 +746,7 @@ def test_results_are_handed_out_once_and_scratch_is_per_stream(pkv):
 
 
 def test_small_results_are_tensors_of_their_own(pkv):
-    """Results are made 32 at a time, but share neither memory nor versions (a change in place of one must not
+    """Results are made many at a time, but share neither memory nor versions (a change in place of one must not
     spoil what another was saved for) nor inference mode."""
     x, cum = torch.randn(2, 3, 500, device="cuda"), torch.zeros(2, 3, device="cuda")
     with torch.inference_mode():
