@@ -7,6 +7,7 @@
 // not seen are never multiplied with anything, so whatever they hold stays out.
 #include "pkv_internal.cuh"
 #include "ptx.cuh"
+#include "tree_merge.cuh"
 
 namespace pkv {
 namespace {
@@ -79,18 +80,12 @@ template <int D>
 constexpr int kCtasPerSm = D == 64 ? 4 : 2;
 constexpr float kLog2e = 1.4426950408889634f;
 
-struct Cut32 {
-  int32_t parts;  // runs that hold a part of the unit, 0: none
-  int32_t t0, row0, rows, head;
-  int32_t pad[3];
-};
-
 struct Params32 {
   TreeArgs a;
   uint32_t* err;
   float* part_o;   // [2 * runs][kRows][D]
   float* part_ml;  // [2 * runs][kRows][2]
-  Cut32* cuts;     // [runs]
+  Cut* cuts;       // [2 * runs]
   int32_t hkv, group;
   float scale_log2;
 };
@@ -247,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>) tree_f32_kernel(const
       for (int64_t e = tid; e < n; e += kThreads) out[static_cast<int64_t>(r.t0) * A.num_q_heads * D + e] = 0.f;
     }
   }
-  if (tid == 0) P.cuts[blockIdx.x].parts = 0;
+  if (tid < 2) P.cuts[2 * blockIdx.x + tid].parts = 0;
   __syncthreads();
   int seq = s_seq;
   int64_t base = pos < end ? s_base : 0;
@@ -265,9 +260,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>) tree_f32_kernel(const
     const int head = unit / rq.units, row0 = (unit - head * rq.units) * kRows;
     const int rows = min(kRows, rq.q_len * P.group - row0), ctx = rq.len - rq.q_len;
     const int slot = nt == rq.tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (first == 0 ? 1 : 0);
-    if (slot >= 0 && first == 0 && tid == 0) {
-      const int rest = rq.tiles - nt, len = static_cast<int>(min(run, int64_t(0x7fffffff)));
-      P.cuts[blockIdx.x] = Cut32{1 + (rest + len - 1) / len, rq.t0, row0, rows, head, {0, 0, 0}};
+    if (slot >= 0 && tid == 0) {  // the runs before that have a part of the unit, and after
+      const int len = static_cast<int>(min(run, int64_t(0x3fffffff)));
+      const int before = (first + len - 1) / len, after = (rq.tiles - first - nt + len - 1) / len;
+      P.cuts[slot] = Cut{before + 1 + after, before, rq.t0, head, {row0, 0}, {rows, 0}};
     }
     const int32_t* btrow = A.block_tables + static_cast<int64_t>(seq) * A.max_blocks;
     // ids of the first tile; Q rows
@@ -405,69 +401,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>) tree_f32_kernel(const
   }
 }
 
-// One warp per row of a cut unit: the weighted sum of its parts' accumulators, in the order of the
-// keys, with a running maximum; all loads of four parts at once, since latency is what it costs.
 template <int D>
-__global__ void __launch_bounds__(256) tree_f32_merge_kernel(const Params32 P) {
-  constexpr int E = D / 32, kParts = 4;
-  const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int4* rec = reinterpret_cast<const int4*>(P.cuts + blockIdx.x);
+__global__ void __launch_bounds__(kMergeThreads) tree_f32_merge_kernel(const Params32 P) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
   grid_dep_wait();
   grid_dep_launch();
-  const int4 c = __ldcg(rec);  // parts, t0, row0, rows
-  const int head = __ldcg(rec + 1).x;
-  const int parts = min(c.x, static_cast<int>(gridDim.x - blockIdx.x));
-  if (parts < 2 || row >= c.w) return;
-  bool bad = false;
-  float M = -INFINITY, den = 0.f, acc[E] = {};
-#pragma unroll 1
-  for (int p0 = 0; p0 < parts; p0 += kParts) {
-    float2 ml[kParts];
-    float o[kParts][E];
+  join_rows<E>(
+      P.cuts, P.part_o, P.part_ml, kRows, [&](const Cut& cut, int row) { return row < cut.rows[0]; },
+      [&](const Cut& cut, int row, const Joined<E>& j) {
+        const bool zero = j.bad || j.l == 0.f;
+        const float inv = 1.f / j.l;
+        const int at = cut.first[0] + row;
+        float* dst = static_cast<float*>(P.a.a.out) +
+                     ((static_cast<int64_t>(cut.t0) + at / P.group) * P.a.a.num_q_heads + cut.head * P.group + at % P.group) * D;
 #pragma unroll
-    for (int k = 0; k < kParts; ++k) {
-      const int p = p0 + k;
-      ml[k] = make_float2(-INFINITY, 0.f);
-      if (p < parts) {  // a run's second slot holds the unit that it begins, its first the one it goes on with
-        const int64_t at = (2 * (static_cast<int64_t>(blockIdx.x) + p) + (p == 0 ? 1 : 0)) * kRows + row;
-        ml[k] = __ldcg(reinterpret_cast<const float2*>(P.part_ml) + at);
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float2 y = __ldcg(reinterpret_cast<const float2*>(P.part_o + at * D + lane * E + e));
-          o[k][e] = y.x;
-          o[k][e + 1] = y.y;
-        }
-      }
-    }
-    float top = M;
-#pragma unroll
-    for (int k = 0; k < kParts; ++k) top = fmaxf(top, ml[k].x);
-    const float f = M == top ? 1.f : exp2f(M - top);
-    M = top;
-    den *= f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= f;
-#pragma unroll
-    for (int k = 0; k < kParts; ++k) {
-      bad |= ml[k].y == -1.f;
-      // (a part without a maximum saw nothing, or nothing but NaN, which its sum says)
-      const float w = ml[k].x == -INFINITY ? ml[k].y * 0.f : exp2f(ml[k].x - M);
-      if (w != 0.f && p0 + k < parts) {
-        den = fmaf(ml[k].y, w, den);
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(o[k][e], w, acc[e]);
-      }
-    }
-  }
-  const bool zero = bad || den == 0.f;
-  const float inv = 1.f / den;
-  const int at = c.z + row;
-  float* dst = static_cast<float*>(P.a.a.out) +
-               ((static_cast<int64_t>(c.y) + at / P.group) * P.a.a.num_q_heads + head * P.group + at % P.group) * D + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; e += 2) {
-    *reinterpret_cast<float2*>(dst + e) = zero ? make_float2(0.f, 0.f) : make_float2(acc[e] * inv, acc[e + 1] * inv);
-  }
+        for (int e = 0; e < E; e += 2)
+          reinterpret_cast<float2*>(dst)[(lane * E + e) / 2] =
+              zero ? make_float2(0.f, 0.f) : make_float2(j.o[e] * inv, j.o[e + 1] * inv);
+      });
 }
 
 struct Layout32 {
@@ -478,7 +430,7 @@ Layout32 layout32(int d, int num_sms) {
   Layout32 l;
   l.o_bytes = rows * d * sizeof(float);
   l.ml_bytes = (rows * 2 * sizeof(float) + 255) & ~static_cast<size_t>(255);
-  l.bytes = l.o_bytes + l.ml_bytes + runs * sizeof(Cut32);
+  l.bytes = l.o_bytes + l.ml_bytes + 2 * runs * sizeof(Cut);
   return l;
 }
 
@@ -491,7 +443,7 @@ int launch_f32(const TreeArgs& t, void* workspace, int num_sms, uint32_t* err, c
   p.err = err;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + l.o_bytes);
-  p.cuts = reinterpret_cast<Cut32*>(static_cast<uint8_t*>(workspace) + l.o_bytes + l.ml_bytes);
+  p.cuts = reinterpret_cast<Cut*>(static_cast<uint8_t*>(workspace) + l.o_bytes + l.ml_bytes);
   p.hkv = a.cache.num_kv_heads;
   p.group = a.num_q_heads / p.hkv;
   p.scale_log2 = a.scale * kLog2e;
@@ -506,7 +458,7 @@ int launch_f32(const TreeArgs& t, void* workspace, int num_sms, uint32_t* err, c
   if (st) return st;
   st = cuda_status(launch_k(tree_f32_kernel<D>, dim3(ctas), dim3(kThreads), kSmem32<D>, s, p));
   if (st) return st;
-  return cuda_status(launch_k(tree_f32_merge_kernel<D>, dim3(ctas, kRows / 8), dim3(256), 0, s, p));
+  return cuda_status(launch_k(tree_f32_merge_kernel<D>, dim3(2 * ctas, 2), dim3(kMergeThreads), 0, s, p));
 }
 
 }  // namespace

@@ -52,6 +52,7 @@
 #include "ptx.cuh"
 #include "pkv_internal.cuh"
 #include "softmax_row.cuh"
+#include "tree_merge.cuh"
 
 namespace pkv {
 namespace {
@@ -103,13 +104,6 @@ struct Ctl {
 constexpr int kSmemBytes = (2 + kKStages + kVStages) * kTileBytes + static_cast<int>(sizeof(Ctl));
 static_assert(kSmemBytes <= 232448, "tree attention shared memory");
 
-// What the merge kernel needs of a unit that a run begins and does not finish.
-struct alignas(16) Cut {
-  int32_t parts;  // runs that hold a part of it, 0: none
-  int32_t head, t0, pad;
-  int32_t j0[2], nq[2];
-};
-
 struct Params {
   __nv_bfloat16* out;
   const __nv_bfloat16* v_cache;
@@ -120,7 +114,7 @@ struct Params {
   uint32_t* err;
   float* part_o;   // [2 * runs][rows_cap][128]
   float* part_ml;  // [2 * runs][rows_cap][2]
-  Cut* cuts;       // [runs]
+  Cut* cuts;       // [2 * runs]
   int64_t num_blocks, num_tokens;
   int32_t num_seqs, max_blocks, max_q, mask_words;
   int32_t hkv, hq, group, gp, gp_log2, rows_q, unit_q, unit_q_log2, unit_cost, rows_cap, min_run, out_v8;
@@ -430,19 +424,11 @@ __device__ __forceinline__ Item next_item(const Params& P, Walk& k, int run, int
       info.nq[w] = max(0, min(P.rows_q, min(rq.q_len, j + P.unit_q) - info.j0[w]));
     }
     info.slot = info.nt == rq.tiles ? -1 : 2 * run + (first == 0 ? 1 : 0);
-    if (info.slot >= 0 && first == 0 && (threadIdx.x & 31) == 0) {  // the unit goes on in the next runs
-      Cut cut;
+    if (info.slot >= 0 && (threadIdx.x & 31) == 0) {  // the runs before that have a part of the unit, and after
       const uint32_t len = run_len < 0x7fffffff ? static_cast<uint32_t>(run_len) : 0x7fffffffu;
-      cut.parts = 1 + static_cast<int32_t>((places - stop + len - 1) / len);
-      cut.head = info.head;
-      cut.t0 = info.t0;
-      cut.pad = 0;
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        cut.j0[w] = info.j0[w];
-        cut.nq[w] = info.nq[w];
-      }
-      P.cuts[run] = cut;
+      const uint32_t before = (static_cast<uint32_t>(first) + len - 1) / len, after = (places - stop + len - 1) / len;
+      P.cuts[info.slot] = Cut{static_cast<int32_t>(before + 1 + after), static_cast<int32_t>(before), info.t0, info.head,
+                              {info.j0[0], info.j0[1]}, {info.nq[0], info.nq[1]}};
     }
     break;
   }
@@ -520,7 +506,7 @@ __device__ void producer_warp(const Params& P, bool is_k, const CUtensorMap* qma
   if (is_k) {
 #pragma unroll 1
     for (int k = 0; k < kRuns; ++k) walk[k] = start_walk(c.run[k]);
-    if (lane < kRuns) P.cuts[lane * gridDim.x + blockIdx.x].parts = 0;
+    if (lane < 2 * kRuns) P.cuts[2 * ((lane >> 1) * gridDim.x + blockIdx.x) + (lane & 1)].parts = 0;
     __syncwarp();
   }
   Tiles a{0, 0, 1, 0, 0, 0, 0, 0, 1}, b = a;
@@ -1055,7 +1041,7 @@ __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t t
 // The kernel cannot run as it is laid out: the call reports a failure, and nothing is merged.
 __device__ __noinline__ void refuse_to_run(const Params& P, int runs) {
   if (threadIdx.x == 0) flag_error(P.err, kErrTimeout);
-  if (threadIdx.x < runs) P.cuts[threadIdx.x * gridDim.x + blockIdx.x].parts = 0;
+  if (threadIdx.x < 2 * runs) P.cuts[2 * ((threadIdx.x >> 1) * gridDim.x + blockIdx.x) + (threadIdx.x & 1)].parts = 0;
 }
 
 template <bool kPairs>
@@ -1139,73 +1125,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 }
 
 // ------------------------------------------------------------------ merge
-// One warp per row of a cut unit: the weighted sum of its parts' accumulators, in the order of the
-// keys, with a running maximum; all loads of four parts at once, since latency is what it costs.
-constexpr int kMergeThreads = 256;
-constexpr int kMergeRows = kMergeThreads / 32;
-constexpr int kMergeParts = 4;
-constexpr int kMergeY = 8;  // CTAs per cut; each takes every 8th group of rows
-
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const Params P) {
-  const int run = blockIdx.x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int4* rec = reinterpret_cast<const int4*>(P.cuts + run);
+  const int lane = threadIdx.x & 31;
   grid_dep_wait();
   grid_dep_launch();
-  const int4 c0 = __ldcg(rec), c1 = __ldcg(rec + 1);  // parts, head, t0; j0[2], nq[2]
-  const int parts = min(c0.x, static_cast<int>(gridDim.x) - run);
-  if (parts < 2) return;
-#pragma unroll 1
-  for (int row = blockIdx.y * kMergeRows + warp; row < P.rows_cap; row += gridDim.y * kMergeRows) {
-    const int w = row >> 7, r = row & 127;
-    const int rj = r >> P.gp_log2, rg = r & (P.gp - 1);
-    if (rj >= (w ? c1.w : c1.z) || rg >= P.group) continue;
-    bool bad = false;
-    float M = -INFINITY, den = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-    for (int p0 = 0; p0 < parts; p0 += kMergeParts) {
-      float2 ml[kMergeParts];
-      float4 o[kMergeParts];
-#pragma unroll
-      for (int k = 0; k < kMergeParts; ++k) {
-        const int p = p0 + k;
-        ml[k] = make_float2(-INFINITY, 0.f);
-        if (p < parts) {  // a run's second slot holds the unit that it begins, its first the one it goes on with
-          const int64_t at = static_cast<int64_t>(2 * (run + p) + (p == 0 ? 1 : 0)) * P.rows_cap + row;
-          ml[k] = __ldcg(reinterpret_cast<const float2*>(P.part_ml) + at);
-          o[k] = __ldcg(reinterpret_cast<const float4*>(P.part_o + at * 128) + lane);
-        }
-      }
-      float top = M;
-#pragma unroll
-      for (int k = 0; k < kMergeParts; ++k) top = fmaxf(top, ml[k].x);
-      const float f = M == top ? 1.f : exp2f(M - top);
-      M = top;
-      den *= f;
-      acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-#pragma unroll
-      for (int k = 0; k < kMergeParts; ++k) {
-        bad |= ml[k].y == -1.f;
-        // (a part without a maximum saw nothing, or nothing but NaN, which its sum says)
-        const float a = ml[k].x == -INFINITY ? ml[k].y * 0.f : exp2f(ml[k].x - M);
-        if (a != 0.f && p0 + k < parts) {
-          den = fmaf(ml[k].y, a, den);
-          acc.x = fmaf(o[k].x, a, acc.x);
-          acc.y = fmaf(o[k].y, a, acc.y);
-          acc.z = fmaf(o[k].z, a, acc.z);
-          acc.w = fmaf(o[k].w, a, acc.w);
-        }
-      }
-    }
-    const bool zero = bad || den == 0.f;
-    const float inv = 1.f / den;
-    __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-    uint2 packed = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
-    if (zero) packed = make_uint2(0, 0);
-    const int64_t t = static_cast<int64_t>(c0.z) + (w ? c1.y : c1.x) + rj;
-    reinterpret_cast<uint2*>(P.out + (t * P.hq + static_cast<int64_t>(c0.y) * P.group + rg) * 128)[lane] = packed;
-  }
+  join_rows<4>(
+      P.cuts, P.part_o, P.part_ml, P.rows_cap,
+      [&](const Cut& cut, int row) {
+        return ((row & 127) >> P.gp_log2) < (row >> 7 ? cut.rows[1] : cut.rows[0]) && (row & (P.gp - 1)) < P.group;
+      },
+      [&](const Cut& cut, int row, const Joined<4>& j) {
+        const bool zero = j.bad || j.l == 0.f;
+        const float inv = 1.f / j.l;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(j.o[0] * inv, j.o[1] * inv);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(j.o[2] * inv, j.o[3] * inv);
+        const uint2 packed = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        const int64_t t = static_cast<int64_t>(cut.t0) + (row >> 7 ? cut.first[1] : cut.first[0]) + ((row & 127) >> P.gp_log2);
+        const int64_t at = (t * P.hq + static_cast<int64_t>(cut.head) * P.group + (row & (P.gp - 1))) * 128;
+        reinterpret_cast<uint2*>(P.out + at)[lane] = zero ? make_uint2(0, 0) : packed;
+      });
 }
 
 int gp_log2_of(int group) {
@@ -1226,7 +1164,7 @@ Layout layout_of(int32_t group, int32_t max_query_len, int num_sms, bool pairs) 
   const size_t slots = 2 * runs * l.rows_cap;
   l.o_bytes = slots * 128 * sizeof(float);
   l.ml_bytes = (slots * 2 * sizeof(float) + 255) & ~static_cast<size_t>(255);
-  l.bytes = l.o_bytes + l.ml_bytes + runs * sizeof(Cut);
+  l.bytes = l.o_bytes + l.ml_bytes + 2 * runs * sizeof(Cut);
   return l;
 }
 
@@ -1306,8 +1244,7 @@ int launch_tree_tc(const TreeArgs& t, void* workspace, int num_sms, uint32_t* er
   if (st) return st;
   st = cuda_status(launch_k(kernel, dim3(ctas), dim3(kThreads), kSmemBytes, s, qm, km, vm, p));
   if (st) return st;
-  const int row_blocks = min((l.rows_cap + kMergeRows - 1) / kMergeRows, kMergeY);
-  return cuda_status(launch_k(tree_merge_kernel, dim3(ctas * runs_per_cta, row_blocks), dim3(kMergeThreads), 0, s, p));
+  return cuda_status(launch_k(tree_merge_kernel, dim3(2 * ctas * runs_per_cta, merge_ctas(l.rows_cap)), dim3(kMergeThreads), 0, s, p));
 }
 
 }  // namespace pkv
