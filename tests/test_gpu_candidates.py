@@ -186,9 +186,18 @@ def test_tree_many_requests_of_all_lengths(pkv):
     check(b.run(pkv), *b.expected())
 
 
-def test_tree_split_over_a_long_axis(pkv):
-    b = Tree(9, [20000, 3, 9000], [4, 2, 2], 4, 1)
-    check(b.run(pkv), *b.expected())
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64), (F32, 128)])
+def test_tree_split_over_a_long_axis(pkv, dtype, d):
+    b = Tree(9, [20000, 3, 9000], [4, 2, 2], 4, 1, dtype=dtype, d=d)
+    want, tol = b.expected()
+    check(b.run(pkv), want, tol)
+    # one part of many: a bad block id makes the request's rows zero, a NaN its rows NaN
+    b.tables[2, 300] = -1
+    b.k[b.tables[0, 700], :, 5] = float("nan")
+    got = b.run(pkv)
+    assert pkv.pkv_get_last_error() == pkv.PKV_ERR_INDEX
+    assert torch.isnan(got[:4]).all() and (got[6:] == 0).all()
+    check(got[4:6], want[4:6], tol[4:6])
 
 
 def test_tree_shared_blocks_and_empty_requests(pkv):
