@@ -45,7 +45,7 @@
 // 64 / 8 heads, are 550 GFLOP: 375 to 420 us as the power limit has it (290 us at the rate of a large
 // matrix product, 320 us at the one that the limit sustains); softmax and MMAs of the two streams
 // alternate, about 1900 cycles a turn each, and the tensor pipe is busy for 64 % of the time.  One
-// request of 500 keys: 9.6 us, nearly all latency: 1.3 us until its run is known, 2 until its first tile
+// request of 500 keys: 9.7 us, nearly all latency: 1.3 us until its run is known, 2 until its first tile
 // is on its way, 0.6 until that is there, 3 for the products and the softmax, 2 for the merge.
 //
 // All waits are bounded (ptx.cuh).
