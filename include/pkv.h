@@ -323,7 +323,7 @@ PKV_API int pkv_tree_mask(const int32_t* parents, const int32_t* query_start_loc
  *                 its rows zeroed
  * max_seq_len     host bound on seq_lens, used only to plan the launch
  * workspace       device memory of at least pkv_tree_workspace() bytes, 256-byte aligned
- * seq_lens        up to 2^31 - 1024 (more is flagged)
+ * seq_lens        up to 2^31 - 1024 (more is flagged); num_seqs below 2^30, num_tokens below 2^31
  * Everything else, the types and the errors: as paged_attention().  Work is cut along the
  * keys by the batch's sizes, so rounding (not the result) may depend on the batch.
  */

@@ -86,7 +86,7 @@ int paged_attention_tree(const void* q, const void* k_cache, const void* v_cache
     return PKV_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned(tree_mask, 8))
     return PKV_ERR_INVALID_ARG;
-  if (num_tokens >= (int64_t(1) << 31)) return PKV_ERR_UNSUPPORTED;
+  if (num_tokens >= (int64_t(1) << 31) || num_seqs >= (1 << 30)) return PKV_ERR_UNSUPPORTED;
   DeviceCtx* ctx = device_ctx(&st);
   if (!ctx) return st;
   st = check_workspace(workspace, workspace_bytes, tree_workspace(*cache, num_q_heads, max_query_len, ctx->num_sms));

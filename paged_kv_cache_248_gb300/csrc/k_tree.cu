@@ -450,7 +450,7 @@ int launch_f32(const TreeArgs& t, void* workspace, int num_sms, uint32_t* err, c
   // CTAs: as many as fit, fewer where the caller's bounds leave less to do
   const int64_t most = static_cast<int64_t>(kCtasPerSm<D>) * num_sms;
   const int64_t units = (static_cast<int64_t>(a.max_query_len) * p.group + kRows - 1) / kRows * p.hkv;
-  const int64_t tiles = units * ((static_cast<int64_t>(a.max_seq_len) + kKeys - 1) / kKeys);
+  const int64_t tiles = units >= most ? units : units * ((static_cast<int64_t>(a.max_seq_len) + kKeys - 1) / kKeys);
   const int64_t want = tiles >= most ? most : tiles * a.num_seqs;
   const int ctas = static_cast<int>(want < 1 ? 1 : want < most ? want : most);
   static uint64_t smem_set = 0;

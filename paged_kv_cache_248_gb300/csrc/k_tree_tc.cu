@@ -1204,8 +1204,9 @@ int launch_tree_tc(const TreeArgs& t, void* workspace, int num_sms, uint32_t* er
   p.unit_q_log2 = 7 - p.gp_log2 + (pairs ? 1 : 0);
   // CTAs: one per SM, fewer where the caller's bounds leave less to do
   const int runs_per_cta = pairs ? 1 : 2;
-  const int64_t units = static_cast<int64_t>((a.max_query_len + p.unit_q - 1) / p.unit_q) * hkv;
-  const int64_t tiles = units * ((static_cast<int64_t>(a.max_seq_len) + kTileKeys - 1) / kTileKeys);
+  const int64_t units = (static_cast<int64_t>(a.max_query_len) + p.unit_q - 1) / p.unit_q * hkv;
+  const int64_t key_tiles = (static_cast<int64_t>(a.max_seq_len) + kTileKeys - 1) / kTileKeys;
+  const int64_t tiles = units >= 2 * num_sms ? units : units * key_tiles;  // (enough to know)
   const int64_t most = tiles >= 2 * num_sms ? 2 * num_sms : tiles * a.num_seqs;
   const int min_tiles = pairs ? 2 : 1;
   const int ctas = static_cast<int>(most < min_tiles * num_sms ? (most + min_tiles - 1) / min_tiles : num_sms);

@@ -94,7 +94,8 @@ def test_tree_attention_refusals(pkv):
                dict(seqs=-1), dict(hq=0), dict(hq=3), dict(tokens=-1), dict(max_q=0), dict(max_len=0),
                dict(scale=float("nan")), dict(scale=float("inf")), dict(cache=None), dict(cache=B(_desc(pkv, bs=8)))):
         assert call(**kw) == pkv.PKV_ERR_INVALID_ARG, kw
-    for kw in (dict(cache=B(_desc(pkv, d=64))), dict(cache=B(_desc(pkv, d=96, dt=0))), dict(hq=34), dict(tokens=1 << 31)):
+    for kw in (dict(cache=B(_desc(pkv, d=64))), dict(cache=B(_desc(pkv, d=96, dt=0))), dict(hq=34), dict(tokens=1 << 31),
+               dict(seqs=1 << 30)):
         assert call(**kw) == pkv.PKV_ERR_UNSUPPORTED, kw
     assert call(tokens=0) == pkv.PKV_OK
 

@@ -200,6 +200,18 @@ def test_tree_split_over_a_long_axis(pkv, dtype, d):
     check(got[4:6], want[4:6], tol[4:6])
 
 
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+def test_tree_bounds_far_above_the_batch(pkv, dtype, d):
+    b = Tree(21, [0, 40, 300], [1, 20, 3], 8, 2, dtype=dtype, d=d)
+    wide = np.zeros((len(b.mask), 1 << 14), np.uint64)  # room for 2^20 nodes
+    wide[:, :b.mask.shape[1]] = b.mask
+    for longest in (300, 2**31 - 1):
+        got = pkv.paged_attention_tree(b.q.cuda(), b.k.cuda(), b.v.cuda(), dev(b.tables), dev(b.lens), dev(b.qsl),
+                                       dev(wide.view(np.int64)), b.scale, 1 << 20, longest)
+        check(got, *b.expected())
+    assert pkv.pkv_get_last_error() == 0
+
+
 def test_tree_shared_blocks_and_empty_requests(pkv):
     b = Tree(10, [100, 64, 64, 0], [3, 2, 0, 0], 8, 2)
     b.tables[2] = b.tables[1]                    # a request that brings nothing, on another's blocks
