@@ -7,6 +7,10 @@ the current CUDA stream, and turns a non-zero status into :class:`PkvError`.
 Every computation runs in the library's CUDA kernels; there is no CPU path.
 If the library has not been built, importing a function raises immediately.
 
+A call runs on the current stream, or on ``stream`` where that is given.  A result that it makes for a given stream
+lies in that stream's memory and may be used on the stream that was current, once that has waited for the other;
+a third one needs Tensor.record_stream, as for any tensor.
+
 Functions carry the C names:
   pkv_slot_mapping, pkv_write, pkv_copy_blocks, paged_attention, paged_attention_cascade,
   paged_attention_step,
@@ -122,6 +126,19 @@ def _stream(stream=None) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream=None, shared=True) -> torch.Tensor:
+    """torch.empty for a call on ``stream``, in that stream's own memory: what the allocator hands out may have a
+    last user that still runs on the stream it was made on, and only this one waits for it.  ``shared``: the caller's
+    stream uses the tensor too, so its memory does not go to the next one before that use is over either."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if shared:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _dev(t: torch.Tensor, name: str, dtype=None):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -149,7 +166,7 @@ def pkv_slot_mapping(block_tables: torch.Tensor, seq_lens: torch.Tensor, query_s
                      num_tokens: int, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """int64 physical slot of every new token (block_tables[i][p // 16] * 16 + p % 16)."""
     if out is None:
-        out = torch.empty(num_tokens, dtype=torch.int64, device=block_tables.device)
+        out = _empty(num_tokens, torch.int64, block_tables.device, stream)
     num_seqs = seq_lens.shape[0]
     _check(lib().pkv_slot_mapping(_dev(block_tables, "block_tables", torch.int32), block_tables.shape[1],
                                   _dev(seq_lens, "seq_lens", torch.int32),
@@ -183,7 +200,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     """Attention of one mixed batch of chunked prefills and decodes over the paged cache."""
     desc = _cache_desc(k_cache, v_cache)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     T, hq, d = q.shape
     _check(lib().paged_attention(_dev(q, "q", k_cache.dtype), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
                                  ctypes.byref(desc), _dev(block_tables, "block_tables", torch.int32),
@@ -204,7 +221,7 @@ def paged_attention_cascade(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     requests member_seqs[member_start[g]:member_start[g + 1]].  Same result."""
     desc = _cache_desc(k_cache, v_cache)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     T, hq, d = q.shape
     groups = _groups((prefix_block_tables, prefix_num_blocks, member_start, member_seqs))
     _check(lib().paged_attention_cascade(_dev(q, "q", k_cache.dtype), _dev(k_cache, "k_cache"),
@@ -246,7 +263,7 @@ def paged_attention_step(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
     paged_attention_step_cow)."""
     desc = _cache_desc(k_cache, v_cache)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     T, hq, d = q.shape
     if k_new.shape != (T, k_cache.shape[1], d) or v_new.shape != k_new.shape:
         raise ValueError("k_new and v_new must be [num_tokens, num_kv_heads, head_dim]")
@@ -289,7 +306,7 @@ def _calls():
         builtin = lambda name, other: getattr(torch._C, name, None) or other  # noqa: E731  (these cost 0.1 us less)
         m.setup(LIB_PATH, torch, PkvError, builtin("_cuda_getDevice", torch.cuda.current_device),
                 builtin("_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream),
-                builtin("_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing), _ready_results)
+                builtin("_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing), _ready_results, _empty)
         _nat = m
     return _nat
 
@@ -313,9 +330,7 @@ def pkv_tree_mask(parents: torch.Tensor, query_start_loc: torch.Tensor, max_quer
         if t is not None and (t.dim() != (2 if name == "out" else 1) or t.shape[0] != n):
             raise ValueError(f"{name} must have a row for every token")
     if out is None:
-        out = torch.empty((n, max(words, 1)), dtype=torch.int64, device=parents.device)
-        if stream is not None:
-            out.record_stream(stream)
+        out = _empty((n, max(words, 1)), torch.int64, parents.device, stream)
     _check(lib().pkv_tree_mask(_dev(parents, "parents", torch.int32),
                                _dev(query_start_loc, "query_start_loc", torch.int32), query_start_loc.shape[0] - 1, n,
                                _dev(out, "out", torch.int64), out.shape[1],

@@ -11,7 +11,8 @@
  * is held while libpkv enqueues a call's kernels, so two calls never use one scratch at the same
  * time.  Where neither is safe -- while the stream is captured into a graph, whose
  * replays need memory of their own, or on a stream that the caller names -- both come from
- * torch.empty for that call alone.
+ * torch.empty for that call alone, and for a named stream from that stream's memory: a block that
+ * the allocator makes for the current stream may have a last user that still runs there.
  *
  * setup(path, torch, PkvError, ...) opens libpkv and keeps what is needed of torch.
  */
@@ -25,10 +26,10 @@
 typedef int64_t i64;
 
 static struct {
-  PyObject *empty, *error, *raw_stream, *current_device, *capturing, *ready;
+  PyObject *empty, *error, *raw_stream, *current_device, *capturing, *ready, *empty_on;
   PyObject *results, *scratch; /* see take_result, take_scratch */
   PyObject *i32, *i64, *f32, *bf16, *u8, *boolean;
-  PyObject *s_dtype, *s_shape, *s_data_ptr, *s_is_contiguous, *s_get_device, *s_stride, *s_cuda_stream, *s_record_stream,
+  PyObject *s_dtype, *s_shape, *s_data_ptr, *s_is_contiguous, *s_get_device, *s_stride, *s_cuda_stream,
       *s_view, *kw_empty;
   __typeof__(&paged_attention_tree) tree;
   __typeof__(&pkv_tree_workspace) tree_ws;
@@ -152,24 +153,19 @@ static int place(PyObject* stream, Place* w) {
   return !PyErr_Occurred();
 }
 
-/* torch.empty(shape, dtype=dtype, device=dev); one that a given stream uses stays alive until
- * that stream is done with it. */
-static PyObject* made(int dim, const i64* n, PyObject* dtype, const Place* w) {
+/* torch.empty(shape, dtype=dtype, device=dev), for a given stream in that stream's memory; `shared`:
+ * the current stream uses it too. */
+static PyObject* made(int dim, const i64* n, PyObject* dtype, const Place* w, int shared) {
   PyObject* shape = PyTuple_New(dim);
   PyObject* d = PyLong_FromLongLong(w->dev);
   PyObject* r = NULL;
   if (shape && d) {
     for (int i = 0; i < dim; ++i) PyTuple_SET_ITEM(shape, i, PyLong_FromLongLong(n[i]));
-    PyObject* args[3] = {shape, dtype, d};
-    r = PyObject_Vectorcall(T.empty, args, 1, T.kw_empty);
+    PyObject* args[5] = {shape, dtype, d, w->given, shared ? Py_True : Py_False};
+    r = w->given == Py_None ? PyObject_Vectorcall(T.empty, args, 1, T.kw_empty) : PyObject_Vectorcall(T.empty_on, args, 5, NULL);
   }
   Py_XDECREF(shape);
   Py_XDECREF(d);
-  if (r && w->given != Py_None) {
-    PyObject* x = PyObject_CallMethodOneArg(r, T.s_record_stream, w->given);
-    if (!x) Py_CLEAR(r);
-    Py_XDECREF(x);
-  }
   return r;
 }
 
@@ -180,7 +176,7 @@ static PyObject* take_result(int dim, const i64* n, PyObject* dtype, const Place
   enum { kMostReady = 32, kMostBytes = 65536, kMostKept = 262144 };
   i64 bytes = dtype == T.bf16 ? 2 : 4;
   for (int i = 0; i < dim; ++i) bytes = n[i] > kMostBytes ? kMostBytes + 1 : bytes * n[i];
-  if (!w->keep || dim > 3 || bytes > kMostBytes || bytes <= 0) return made(dim, n, dtype, w);
+  if (!w->keep || dim > 3 || bytes > kMostBytes || bytes <= 0) return made(dim, n, dtype, w, 1);
   struct {
     PyObject* dtype;
     void* stream;
@@ -202,7 +198,7 @@ static PyObject* take_result(int dim, const i64* n, PyObject* dtype, const Place
     long next = count * 8 < kMostReady ? count * 8 : kMostReady;
     if (next * bytes > kMostKept) next = kMostKept / bytes;
     if (count == 1) {
-      r = made(dim, n, dtype, w);
+      r = made(dim, n, dtype, w, 1);
     } else {
       PyObject* shape = dim == 1   ? Py_BuildValue("(L)", (long long)n[0])
                         : dim == 2 ? Py_BuildValue("(LL)", (long long)n[0], (long long)n[1])
@@ -230,7 +226,7 @@ static PyObject* take_result(int dim, const i64* n, PyObject* dtype, const Place
 /* Scratch of at least `bytes` for call number `call`. */
 static PyObject* take_scratch(i64 bytes, int call, const Place* w) {
   if (bytes < 256) bytes = 256; /* (none is empty) */
-  if (!w->keep) return made(1, &bytes, T.u8, w);
+  if (!w->keep) return made(1, &bytes, T.u8, w, 0);
   struct {
     void* stream;
     i64 dev, call;
@@ -244,7 +240,7 @@ static PyObject* take_scratch(i64 bytes, int call, const Place* w) {
     r = NULL;
   } else {
     if (PyDict_GET_SIZE(T.scratch) >= 256) PyDict_Clear(T.scratch);
-    r = made(1, &bytes, T.u8, w);
+    r = made(1, &bytes, T.u8, w, 0);
     PyObject* entry = r ? Py_BuildValue("(LO)", (long long)bytes, r) : NULL;
     if (!entry || PyDict_SetItem(T.scratch, k, entry)) Py_CLEAR(r);
     Py_XDECREF(entry);
@@ -558,11 +554,13 @@ end:
 }
 
 /* (path of libpkv, torch, PkvError, torch.cuda.current_device, a function from a device to its raw stream, one that tells
- * whether the current stream is captured, one that makes results: (shapes, type, device) -> list) */
+ * whether the current stream is captured, one that makes results: (number, shape, type, device) -> list, one that makes a
+ * tensor for a named stream: (shape, type, device, stream, shared)) */
 static PyObject* py_setup(PyObject* self, PyObject* args) {
   const char* path;
   PyObject* torch;
-  if (!PyArg_ParseTuple(args, "sOOOOOO", &path, &torch, &T.error, &T.current_device, &T.raw_stream, &T.capturing, &T.ready)) return NULL;
+  if (!PyArg_ParseTuple(args, "sOOOOOOO", &path, &torch, &T.error, &T.current_device, &T.raw_stream, &T.capturing, &T.ready, &T.empty_on))
+    return NULL;
   void* h = dlopen(path, RTLD_NOW | RTLD_LOCAL);
   if (!h) {
     PyErr_SetString(PyExc_ImportError, dlerror());
@@ -586,6 +584,7 @@ static PyObject* py_setup(PyObject* self, PyObject* args) {
   Py_INCREF(T.raw_stream);
   Py_INCREF(T.capturing);
   Py_INCREF(T.ready);
+  Py_INCREF(T.empty_on);
   if (!(T.results = PyDict_New()) || !(T.scratch = PyDict_New())) return NULL;
   if (!(T.empty = PyObject_GetAttrString(torch, "empty")) || !(T.i32 = PyObject_GetAttrString(torch, "int32")) ||
       !(T.i64 = PyObject_GetAttrString(torch, "int64")) || !(T.f32 = PyObject_GetAttrString(torch, "float32")) ||
@@ -599,7 +598,6 @@ static PyObject* py_setup(PyObject* self, PyObject* args) {
   T.s_get_device = PyUnicode_InternFromString("get_device");
   T.s_stride = PyUnicode_InternFromString("stride");
   T.s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
-  T.s_record_stream = PyUnicode_InternFromString("record_stream");
   T.s_view = PyUnicode_InternFromString("view");
   T.kw_empty = Py_BuildValue("(ss)", "dtype", "device");
   Py_RETURN_NONE;

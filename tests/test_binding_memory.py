@@ -1,0 +1,102 @@
+"""Where the binding takes results and scratch from, and what it does with the tensors it is given.  No GPU: torch's
+device, streams and allocator are stood in for, and every call is one that libpkv has nothing to do for."""
+import contextlib
+import types
+
+import pytest
+import torch
+
+HOST = -1  # what a CPU tensor's get_device() says, and so the "current device" here
+
+
+class Kept(torch.Tensor):
+    """A CPU tensor that notes who records a use of it."""
+
+    def record_stream(self, stream):
+        LOG.append(("record", stream))
+
+
+LOG = []
+
+
+@pytest.fixture
+def pkv(monkeypatch):
+    from paged_kv_cache_248_gb300 import _build
+    _build.build()
+    import paged_kv_cache_248_gb300 as m
+    m.lib()
+    LOG.clear()
+    main = types.SimpleNamespace(cuda_stream=0, name="main")
+    here = [main]
+    real = torch.empty
+
+    def empty(shape, dtype=None, device=None):
+        LOG.append(("empty", here[-1]))
+        return real(shape, dtype=dtype).as_subclass(Kept)
+
+    @contextlib.contextmanager
+    def on(stream):
+        here.append(stream)
+        yield
+        here.pop()
+
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: here[-1])
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: HOST, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: here[-1].cuda_stream, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: False, raising=False)
+    monkeypatch.setattr(m, "_dev", lambda t, name, dtype=None: None)
+    monkeypatch.setattr(m, "_nat", None)  # set up anew with the stand-ins, and again with torch's own after the test
+    m.main_stream = main
+    yield m
+    m._nat = None
+
+
+def i32(*s):
+    return torch.zeros(s, dtype=torch.int32)
+
+
+K = torch.zeros(4, 2, 16, 128, dtype=torch.bfloat16)
+Q = torch.zeros(0, 4, 128, dtype=torch.bfloat16)
+def _refused(m, call, *args, **kw):
+    """A call without tokens that is refused, after it has asked for its result."""
+    with pytest.raises(m.PkvError):
+        call(*args, **kw)
+
+
+CALLS = {  # nothing to do: no tokens, no requests, no rows
+    "tree": lambda m, **kw: m.paged_attention_tree(Q, K, K, i32(1, 4), i32(1), i32(2), torch.zeros(0, 1, dtype=torch.int64),
+                                                   1.0, 1, 8, **kw),
+    "tree_mask": lambda m, **kw: m.pkv_tree_mask(i32(0), i32(2), 8, **kw),
+    "compact": lambda m, **kw: m.pkv_compact_path(i32(0, 3), i32(0), i32(0, 4), i32(0), i32(1), K, K, **kw),
+    "beam": lambda m, **kw: m.pkv_beam_select(torch.zeros(0, 4, 100), torch.zeros(0, 4), 8, **kw),
+    "fork": lambda m, **kw: m.pkv_fork_tables(i32(0, 4), i32(0), i32(0), i32(4), K, K, **kw),
+    "slots": lambda m, **kw: m.pkv_slot_mapping(i32(1, 4), i32(1), i32(2), 0, **kw),
+    "attention": lambda m, **kw: m.paged_attention(Q, K, K, i32(1, 4), i32(1), i32(2), 1.0, 1, 8, **kw),
+    "cascade": lambda m, **kw: m.paged_attention_cascade(Q, K, K, i32(1, 4), i32(1), i32(2), 1.0, 1, 8, i32(0, 1), i32(0),
+                                                         i32(1), i32(0), **kw),
+    "step": lambda m, **kw: _refused(m, m.paged_attention_step, Q, Q[:, :2], Q[:, :2], K, K, i32(1, 4), i32(1), i32(2), 1.0,
+                                     1, 8, **kw),
+}
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_a_named_stream_works_in_memory_of_its_own(pkv, call):
+    """The allocator may hand out memory whose last user still runs on the stream that it is asked on.  So whatever a call
+    on a named stream writes is asked for on that stream; and what it returns, which the caller's stream reads later, is
+    recorded there."""
+    side = types.SimpleNamespace(cuda_stream=7, name="side")
+    got = CALLS[call](pkv, stream=side)
+    results = got if isinstance(got, tuple) else (got,)
+    asked = [s for what, s in LOG if what == "empty"]
+    assert len(asked) >= len(results) and all(s is side for s in asked), [s.name for s in asked]
+    recorded = [s for what, s in LOG if what == "record"]
+    assert len(recorded) >= len(results) and all(s is pkv.main_stream for s in recorded), [s.name for s in recorded]
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_the_current_stream_needs_no_record(pkv, call):
+    CALLS[call](pkv)
+    assert [s for what, s in LOG if what == "record"] == []
+    assert all(s is pkv.main_stream for what, s in LOG if what == "empty")
