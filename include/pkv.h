@@ -321,6 +321,8 @@ PKV_API int pkv_tree_mask(const int32_t* parents, const int32_t* query_start_loc
  * mask_words      64 * mask_words >= max_query_len
  * max_query_len   host bound on q_i: a request with more is flagged (PKV_ERR_INDEX) and
  *                 its rows zeroed
+ * query_start_loc rows outside of [0, num_tokens), or a request that ends before it begins, are flagged
+ *                 too (PKV_ERR_INDEX); what exists of the request's rows is zeroed
  * max_seq_len     host bound on seq_lens, used only to plan the launch
  * workspace       device memory of at least pkv_tree_workspace() bytes, 256-byte aligned
  * seq_lens        up to 2^31 - 1024 (more is flagged); num_seqs below 2^30, num_tokens below 2^31

@@ -100,11 +100,12 @@ __device__ __forceinline__ Request32 request_of(const Params32& P, int i) {
   Request32 r;
   const int32_t q0 = __ldg(A.qsl + i), q1 = __ldg(A.qsl + i + 1), len = __ldg(A.seq_lens + i);
   const int64_t n = static_cast<int64_t>(q1) - q0;
-  const bool rows = n > 0 && q0 >= 0 && q1 <= A.num_tokens;
+  const bool real = n >= 0 && q0 >= 0 && q1 <= A.num_tokens, rows = real && n > 0;
   bool fits = rows && len >= n && len <= kMaxLen && n <= A.max_query_len &&
               (static_cast<int64_t>(len) + kBlock - 1) / kBlock <= A.max_blocks;
-  r.t0 = q0;
-  r.q_len = rows ? static_cast<int32_t>(n) : 0;
+  // (of rows that are not real, those that exist)
+  r.t0 = max(q0, 0);
+  r.q_len = static_cast<int32_t>(max(int64_t(0), min(static_cast<int64_t>(q1), A.num_tokens) - r.t0));
   r.len = len;
   r.tiles = static_cast<int>(static_cast<uint32_t>(len - 1) / kKeys) + 1;
   const int64_t units = (static_cast<int64_t>(r.q_len) * P.group + kRows - 1) / kRows;
@@ -112,7 +113,7 @@ __device__ __forceinline__ Request32 request_of(const Params32& P, int i) {
   fits = fits && cost < (int64_t(1) << 31);  // (more would be terabytes of K and V, read once a unit)
   r.units = static_cast<int32_t>(units);
   r.cost = fits ? static_cast<int32_t>(cost) : 0;
-  r.wrong = rows && !fits;
+  r.wrong = !real || (rows && !fits);
   return r;
 }
 
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>) tree_f32_kernel(const
       at += cost;
     }
   }
-  if (any_wrong) {  // rows of requests whose lengths do not fit are zero
+  if (any_wrong) {  // lengths that do not fit, rows that do not exist: reported, and zero as far as they do
     for (int i = blockIdx.x; i < A.num_seqs; i += gridDim.x) {
       const Request32 r = request_of(P, i);
       if (!r.wrong) continue;

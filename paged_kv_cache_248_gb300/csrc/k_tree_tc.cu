@@ -162,7 +162,7 @@ __device__ __forceinline__ T same(T x) {  // lane 0's value
 // ------------------------------------------------------------------ units
 struct Request {
   int32_t t0, q_len, len;
-  bool wrong;            // rows to zero: lengths that do not fit
+  bool wrong;            // to be reported, its rows to zero: lengths that do not fit, rows that do not exist
   int32_t tiles, units;  // key tiles of a unit; units of one kv head
   int32_t cost;          // of all its units: a unit costs its key tiles and P.unit_cost
 
@@ -175,18 +175,19 @@ struct Request {
 __device__ __forceinline__ Request make_request(const Params& P, int32_t q0, int32_t q1, int32_t len) {
   Request r;
   const int64_t n = static_cast<int64_t>(q1) - q0;
-  const bool rows = n > 0 && q0 >= 0 && q1 <= P.num_tokens;
+  const bool real = n >= 0 && q0 >= 0 && q1 <= P.num_tokens, rows = real && n > 0;
   bool fits = rows && len >= n && len <= kMaxLen && n <= P.max_q &&
               (static_cast<int64_t>(len) + kBlock - 1) / kBlock <= P.max_blocks;
-  r.t0 = q0;
-  r.q_len = rows ? static_cast<int32_t>(n) : 0;
+  // (of rows that are not real, those that exist)
+  r.t0 = max(q0, 0);
+  r.q_len = static_cast<int32_t>(max(int64_t(0), min(static_cast<int64_t>(q1), P.num_tokens) - r.t0));
   r.len = len;
   r.tiles = static_cast<int>(static_cast<uint32_t>(len - 1) / kTileKeys) + 1;
   r.units = (r.q_len + P.unit_q - 1) >> P.unit_q_log2;
   // (2^31 places and more would be terabytes of K and V, read once a unit)
   const int64_t cost = static_cast<int64_t>(P.hkv) * r.units * (r.tiles + P.unit_cost);
   fits = fits && cost < (int64_t(1) << 31);
-  r.wrong = rows && !fits;
+  r.wrong = !real || (rows && !fits);
   r.cost = fits ? static_cast<int32_t>(cost) : 0;
   return r;
 }
@@ -195,7 +196,7 @@ __device__ __noinline__ Request load_request(const Params& P, int i) {
   return make_request(P, __ldg(P.qsl + i), __ldg(P.qsl + i + 1), __ldg(P.seq_lens + i));
 }
 
-// Rows of requests whose lengths do not fit are zeroed (by `step` threads, this is number `first`).
+// Wrong requests are reported and their rows zeroed (by `step` threads, this is number `first`).
 __device__ __noinline__ void zero_wrong(const Params& P, int first, int step) {
 #pragma unroll 1
   for (int i = blockIdx.x; i < P.num_seqs; i += gridDim.x) {
