@@ -257,10 +257,11 @@ static PyObject* result(Arg* a, PyObject* given, const char* name, int dim, cons
   *ok = a->t && (given == Py_None ? pointer(a) : check(a, dtype, w->dev));
   return a->t;
 }
-/* The same for scratch, whose bytes a->n[0] tells. */
+/* The same for scratch, whose bytes a->n[0] tells afterwards. */
 static PyObject* scratch(Arg* a, PyObject* given, i64 bytes, int call, const Place* w, int* ok) {
   if (given != Py_None) {
-    *ok = shape_of(a, given, "workspace") && check(a, T.u8, w->dev);
+    *ok = shape_of(a, given, "workspace") && (a->dim < 1 || a->dim > 5 ? refuse("workspace must be a vector") : check(a, T.u8, w->dev));
+    for (int i = 1; *ok && i < a->dim; ++i) a->n[0] *= a->n[i];
     return Py_NewRef(given);
   }
   a->t = take_scratch(bytes, call, w);

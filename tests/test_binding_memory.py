@@ -100,3 +100,14 @@ def test_the_current_stream_needs_no_record(pkv, call):
     CALLS[call](pkv)
     assert [s for what, s in LOG if what == "record"] == []
     assert all(s is pkv.main_stream for what, s in LOG if what == "empty")
+
+
+@pytest.mark.parametrize("call", ["beam", "fork"])
+def test_a_workspace_has_a_length(pkv, call):
+    """The bytes that a call may use are its workspace's, whatever its shape; a tensor of no dimension has none to tell."""
+    with pytest.raises(ValueError, match="workspace"):
+        CALLS[call](pkv, workspace=torch.zeros((), dtype=torch.uint8))
+    for shape in ((1 << 20,), (4, 1 << 18), (1 << 20, 1), (0,), (0, 4), (1,) * 5):
+        CALLS[call](pkv, workspace=torch.zeros(shape, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="workspace"):
+        CALLS[call](pkv, workspace=torch.zeros((1,) * 6, dtype=torch.uint8))
