@@ -64,7 +64,7 @@ static int shape_of(Arg* a, PyObject* t, const char* name) {
   a->dim = d > 5 ? 6 : (int)d;
   for (Py_ssize_t i = 0; i < d && i < 5; ++i) a->n[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(s, i));
   Py_DECREF(s);
-  return 1;
+  return !PyErr_Occurred();
 }
 
 static int is_dtype(PyObject* t, PyObject* dtype) {
@@ -442,6 +442,7 @@ static PyObject* py_beam(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     i64 d[3] = {0, 0, 0};
     for (int i = 0; i < 3 && PyTuple_Check(st) && i < PyTuple_GET_SIZE(st); ++i) d[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(st, i));
     Py_DECREF(st);
+    if (PyErr_Occurred()) return NULL;
     step = W > 1 ? d[1] : N > 1 ? d[0] : V;
     if ((V > 1 && d[2] != 1) || (N > 1 && d[0] != W * step) || step < V)
       return refuse("logits must have contiguous rows, evenly spaced"), NULL;

@@ -111,3 +111,18 @@ def test_a_workspace_has_a_length(pkv, call):
         CALLS[call](pkv, workspace=torch.zeros(shape, dtype=torch.uint8))
     with pytest.raises(ValueError, match="workspace"):
         CALLS[call](pkv, workspace=torch.zeros((1,) * 6, dtype=torch.uint8))
+
+
+def test_a_shape_that_is_none_is_an_error_of_its_own(pkv):
+    """Numbers that a tensor-like object gives for its shape or strides are looked at when they are read."""
+    odd = types.SimpleNamespace(shape=("x", 4, 100))
+    with pytest.raises(TypeError):
+        pkv.pkv_beam_select(odd, torch.zeros(0, 4), 8)
+    with pytest.raises(TypeError):
+        pkv.pkv_beam_select(torch.zeros(0, 4, 100), types.SimpleNamespace(shape=(0, None)), 8)
+    with pytest.raises(OverflowError):
+        pkv.pkv_beam_select(types.SimpleNamespace(shape=(1 << 70, 4, 100)), torch.zeros(0, 4), 8)
+    strided = types.SimpleNamespace(shape=(2, 4, 100), dtype=torch.float32, is_contiguous=lambda: False,
+                                    stride=lambda: (400, "x", 1))
+    with pytest.raises(TypeError):
+        pkv.pkv_beam_select(strided, torch.zeros(2, 4), 8)
