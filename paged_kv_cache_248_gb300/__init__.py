@@ -421,6 +421,10 @@ def pkv_trace_read() -> dict:
 
 
 def pkv_shutdown() -> None:
+    """Gives back what the library allocated, and the results and scratch that the binding keeps ready for the calls
+    for candidate continuations (as much as 40 MB a stream for drafted trees).  Both are made anew when needed."""
+    if _nat is not None:
+        _nat.release()
     lib().pkv_shutdown()
 
 

@@ -605,7 +605,16 @@ static PyObject* py_setup(PyObject* self, PyObject* args) {
   Py_RETURN_NONE;
 }
 
+/* Lets go of the ready results and of the scratch.  (Torch hands their memory out again in the order of the streams
+ * that use it, so calls that still run keep theirs.) */
+static PyObject* py_release(PyObject* self, PyObject* none) {
+  if (T.results) PyDict_Clear(T.results);
+  if (T.scratch) PyDict_Clear(T.scratch);
+  Py_RETURN_NONE;
+}
+
 static PyMethodDef methods[] = {{"setup", py_setup, METH_VARARGS, NULL},
+                                {"release", py_release, METH_NOARGS, NULL},
                                 {"tree", (PyCFunction)(void*)py_tree, METH_FASTCALL, NULL},
                                 {"compact", (PyCFunction)(void*)py_compact, METH_FASTCALL, NULL},
                                 {"beam", (PyCFunction)(void*)py_beam, METH_FASTCALL, NULL},

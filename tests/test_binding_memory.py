@@ -2,6 +2,7 @@
 device, streams and allocator are stood in for, and every call is one that libpkv has nothing to do for."""
 import contextlib
 import types
+import weakref
 
 import pytest
 import torch
@@ -17,6 +18,7 @@ class Kept(torch.Tensor):
 
 
 LOG = []
+MADE = []
 
 
 @pytest.fixture
@@ -26,13 +28,16 @@ def pkv(monkeypatch):
     import paged_kv_cache_248_gb300 as m
     m.lib()
     LOG.clear()
+    MADE.clear()
     main = types.SimpleNamespace(cuda_stream=0, name="main")
     here = [main]
     real = torch.empty
 
     def empty(shape, dtype=None, device=None):
         LOG.append(("empty", here[-1]))
-        return real(shape, dtype=dtype).as_subclass(Kept)
+        t = real(shape, dtype=dtype).as_subclass(Kept)
+        MADE.append(weakref.ref(t))
+        return t
 
     @contextlib.contextmanager
     def on(stream):
@@ -126,3 +131,19 @@ def test_a_shape_that_is_none_is_an_error_of_its_own(pkv):
                                     stride=lambda: (400, "x", 1))
     with pytest.raises(TypeError):
         pkv.pkv_beam_select(strided, torch.zeros(2, 4), 8)
+
+
+def test_shutdown_gives_back_what_the_binding_keeps(pkv):
+    """Scratch stays for the next call on its stream, and ready results for the next of their shape, until pkv_shutdown."""
+    for _ in range(3):
+        CALLS["beam"](pkv)
+        CALLS["fork"](pkv)
+        pkv.pkv_fork_tables(i32(0, 4), i32(0), i32(0), i32(4), None, None)
+    assert any(t() is not None for t in MADE)
+    pkv.pkv_shutdown()
+    assert all(t() is None for t in MADE)
+    CALLS["beam"](pkv)  # and calls go on as before
+    assert any(t() is not None for t in MADE)
+    pkv.pkv_shutdown()
+    pkv.pkv_shutdown()
+    assert all(t() is None for t in MADE)
