@@ -302,7 +302,7 @@ def _calls():
         try:
             from . import _native as m
         except ImportError as e:
-            raise ImportError("_native.so not built; run `python -m paged_kv_cache_248_gb300._build`") from e
+            raise ImportError("_native is not built for this Python; run `python -m paged_kv_cache_248_gb300._build`") from e
         builtin = lambda name, other: getattr(torch._C, name, None) or other  # noqa: E731  (these cost 0.1 us less)
         m.setup(LIB_PATH, torch, PkvError, builtin("_cuda_getDevice", torch.cuda.current_device),
                 builtin("_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream),

@@ -2,7 +2,7 @@
 
 Each translation unit compiles in parallel to an object file under
 ``paged_kv_cache_248_gb300/_build/``; the objects link into
-``paged_kv_cache_248_gb300/libpkv.so``; ``binding.c`` becomes the CPython module ``_native.so``.
+``paged_kv_cache_248_gb300/libpkv.so``; ``binding.c`` becomes the CPython module ``_native`` of this Python's ABI.
 No cmake, no torch extension machinery.
 Run ``python -m paged_kv_cache_248_gb300._build`` or call :func:`build`.
 """
@@ -20,7 +20,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpkv.so")
-NATIVE = os.path.join(PKG, "_native.so")  # CPython module over libpkv (binding.c)
+NATIVE = os.path.join(PKG, "_native" + sysconfig.get_config_var("EXT_SUFFIX"))  # CPython module over libpkv (binding.c)
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -82,14 +82,22 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
     src = os.path.join(CSRC, "binding.c")
-    if force or not os.path.exists(NATIVE) or os.path.getmtime(NATIVE) < max(os.path.getmtime(src), hdr):
+    cmd = [shutil.which("gcc") or "gcc", "-O2", "-shared", "-fPIC", f"-I{INCLUDE}",
+           f"-I{sysconfig.get_paths()['include']}", src, "-ldl"]
+    record = os.path.join(OUT_DIR, "_native.cmd")  # the command that made the module: another Python's differs
+    made_by = open(record).read() if os.path.exists(record) else ""
+    if (force or made_by != " ".join(cmd) or not os.path.exists(NATIVE)
+            or os.path.getmtime(NATIVE) < max(os.path.getmtime(src), hdr)):
         tmp = NATIVE + f".tmp{os.getpid()}"
-        cmd = [shutil.which("gcc") or "gcc", "-O2", "-shared", "-fPIC", f"-I{INCLUDE}",
-               f"-I{sysconfig.get_paths()['include']}", src, "-o", tmp, "-ldl"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
+        r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"gcc failed for binding.c:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, NATIVE)
+        with open(record, "w") as f:
+            f.write(" ".join(cmd))
+    untagged = os.path.join(PKG, "_native.so")  # of a build before the module carried its ABI: any Python would load it
+    if os.path.exists(untagged):
+        os.remove(untagged)
     return LIB
 
 
