@@ -326,6 +326,9 @@ def pkv_tree_mask(parents: torch.Tensor, query_start_loc: torch.Tensor, max_quer
     node that each token continues (smaller than its own index), -1 for the context.
     ``depths``, if given, receives the number of ancestors (int32 [T])."""
     n, words = parents.shape[0], (int(max_query_len) + 63) // 64
+    for t, name in ((parents, "parents"), (query_start_loc, "query_start_loc"), (out, "out"), (depths, "depths")):
+        if t is not None and t.is_cuda and t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"{name} must be a tensor on the current CUDA device (cuda:{torch.cuda.current_device()})")
     for t, name in ((out, "out"), (depths, "depths")):
         if t is not None and (t.dim() != (2 if name == "out" else 1) or t.shape[0] != n):
             raise ValueError(f"{name} must have a row for every token")

@@ -147,3 +147,30 @@ def test_shutdown_gives_back_what_the_binding_keeps(pkv):
     pkv.pkv_shutdown()
     pkv.pkv_shutdown()
     assert all(t() is None for t in MADE)
+
+
+class Elsewhere(torch.Tensor):
+    """A CPU tensor that says it lies on another CUDA device than the current one."""
+    is_cuda = True
+
+    def get_device(self):
+        return 1
+
+
+@pytest.mark.parametrize("which", ["parents", "query_start_loc", "out", "depths"])
+def test_tree_masks_are_refused_on_another_device(pkv, monkeypatch, which):
+    """The kernel runs on the current device, and what lies on another cannot be read there."""
+    monkeypatch.undo()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: types.SimpleNamespace(cuda_stream=0))
+
+    class Here(Elsewhere):
+        def get_device(self):
+            return 0
+
+    given = {"parents": i32(0), "query_start_loc": i32(2), "out": torch.zeros(0, 1, dtype=torch.int64), "depths": i32(0)}
+    given = {n: t.as_subclass(Elsewhere if n == which else Here) for n, t in given.items()}
+    with pytest.raises(ValueError, match=f"{which} must be a tensor on the current CUDA device"):
+        pkv.pkv_tree_mask(given["parents"], given["query_start_loc"], 8, out=given["out"], depths=given["depths"])
+    given[which] = given[which].as_subclass(Here)
+    pkv.pkv_tree_mask(given["parents"], given["query_start_loc"], 8, out=given["out"], depths=given["depths"])
