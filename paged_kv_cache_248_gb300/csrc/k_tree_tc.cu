@@ -17,10 +17,10 @@
 // derives its runs from the lengths by itself, without a planning launch.  A unit that lies within
 // one run is finished there; of one that is cut, each run leaves its rows' unnormalised accumulator,
 // maximum and sum, and the merge kernel joins them in order.  A run leaves at most two such
-// partials.  Where every kv head of every request has the same number of units, above one, as many
-// runs at a time go through the same keys, each for one of the units, so that K and V come from
-// HBM once and not once a unit (8 requests of 32768 keys with 512 rows: 2.17 GB read and 415 us
-// one unit after the other, 1.09 GB and 391 us side by side).
+// partials.  Where every kv head of every request that has rows has the same number of units, above
+// one, as many runs at a time go through the same keys, each for one of the units, so that K and V come
+// from HBM once and not once a unit (8 requests of 32768 keys with 512 rows: 2.17 GB read and 415 us
+// one unit after the other, 1.09 GB and 391 us side by side); see side_by_side for what it costs.
 //
 // Streams.  Two S/P/O accumulator sets live in TMEM, each with a softmax warpgroup of its own, so
 // that one softmax runs while the tensor core works for the other.
@@ -95,6 +95,7 @@ struct Ctl {
   Run run[2];
   int64_t run_len;
   int64_t warp_sum[kThreads / 32];
+  int32_t warp_most[kThreads / 32], warp_least[kThreads / 32];
   uint32_t tmem_base;
   uint32_t q_loads[2];
   uint32_t number[2][8];  // numbers in the rings of a run's latest tiles
@@ -232,25 +233,48 @@ __device__ __forceinline__ Run cut_run(const Params& P, int k, int64_t total, ui
   return r;
 }
 
+// Whether so many units of each kv head go side by side.  Every unit gets equally many runs, and the CTAs
+// that are left over rest; where those are more than a sixth the units come one after the other.  One
+// request of 8000 keys on 152 SMs, side by side / one after the other: 38 units 48.4 / 54.5 us, 70 (12 SMs
+// rest) 86.7 / 85.9, 128 (24) 150.0 / 149.2, 60 (32) 82.5 / 73.9, 51 (50) 79.4 / 64.6, 80 (72) 131.9 / 95.7;
+// of 2000 keys 128 units 78.9 / 88.9, 60 units 49.1 / 46.3.
+__device__ __forceinline__ bool side_by_side(uint32_t units) {
+  return units > 1 && 6 * (gridDim.x / units * units) >= 5 * gridDim.x;
+}
+
 // This CTA's kRuns runs: run k * CTAs + CTA, so that few runs have an SM each (all threads).
 template <int kRuns>
 __device__ void find_runs(const Params& P, Ctl& c) {
   const int per = (P.num_seqs + kThreads - 1) / kThreads;
   const int i0 = min(static_cast<int>(threadIdx.x) * per, P.num_seqs), i1 = min(i0 + per, P.num_seqs);
-  const Request first = load_request(P, 0);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t mine = 0;
-  bool wrong = false, differ = false;
+  int32_t most = 0, least = 0x7fffffff;  // units of a kv head, of requests that have any
+  bool wrong = false;
 #pragma unroll 1
   for (int i = i0; i < i1; ++i) {
     const Request r = load_request(P, i);
     mine += r.cost;
     wrong |= r.wrong;
-    differ |= r.cost > 0 && r.units != first.units;
+    if (r.cost > 0) {
+      most = max(most, r.units);
+      least = min(least, r.units);
+    }
   }
-  const bool any_differ = __syncthreads_or(differ);
-  const bool one = kRuns == 1 && !any_differ && first.units > 1 && first.units <= gridDim.x;
-  if (one) mine /= first.units;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  most = __reduce_max_sync(0xffffffffu, most);
+  least = __reduce_min_sync(0xffffffffu, least);
+  if (lane == 0) {
+    c.warp_most[warp] = most;
+    c.warp_least[warp] = least;
+  }
+  const bool any_wrong = __syncthreads_or(wrong);
+#pragma unroll 1
+  for (int w = 0; w < kThreads / 32; ++w) {
+    most = max(most, c.warp_most[w]);
+    least = min(least, c.warp_least[w]);
+  }
+  const bool one = kRuns == 1 && most == least && side_by_side(most);
+  if (one) mine /= most;
   int64_t incl = mine;
 #pragma unroll 1
   for (int d = 1; d < 32; d <<= 1) {
@@ -258,7 +282,7 @@ __device__ void find_runs(const Params& P, Ctl& c) {
     if (lane >= d) incl += y;
   }
   if (lane == 31) c.warp_sum[warp] = incl;
-  const bool any_wrong = __syncthreads_or(wrong);
+  __syncthreads();
   int64_t before = incl - mine, total = 0;
 #pragma unroll 1
   for (int w = 0; w < kThreads / 32; ++w) {
@@ -269,7 +293,7 @@ __device__ void find_runs(const Params& P, Ctl& c) {
   int64_t len;
 #pragma unroll
   for (int k = 0; k < kRuns; ++k) {
-    run[k] = cut_run<kRuns>(P, k, total, one ? first.units : 0, &len);
+    run[k] = cut_run<kRuns>(P, k, total, one ? most : 0, &len);
     if (threadIdx.x == 0) c.run[k] = run[k];
   }
   if (threadIdx.x == 0) c.run_len = len;
@@ -316,8 +340,8 @@ __device__ void find_runs_few(const Params& P, Ctl& c) {
   }
   int64_t total = 0, before[kSets];
   int32_t cost[kSets];
-  bool wrong = false, differ = false;
-  const int32_t units = make_request(P, same(q0[0]), same(q1[0]), same(len[0])).units;
+  bool wrong = false;
+  int32_t most = 0, least = 0x7fffffff;  // units of a kv head, of requests that have any
   Request r[kSets];
 #pragma unroll
   for (int s = 0; s < kSets; ++s) {
@@ -325,10 +349,14 @@ __device__ void find_runs_few(const Params& P, Ctl& c) {
     if (32 * s < P.num_seqs) {
       r[s] = make_request(P, q0[s], q1[s], len[s]);
       wrong |= r[s].wrong;
-      differ |= r[s].cost > 0 && r[s].units != units;
+      if (r[s].cost > 0) {
+        most = max(most, r[s].units);
+        least = min(least, r[s].units);
+      }
     }
   }
-  const bool one = kRuns == 1 && units > 1 && units <= gridDim.x && !__any_sync(0xffffffffu, differ);
+  const int32_t units = kRuns == 1 ? __reduce_max_sync(0xffffffffu, most) : 0;
+  const bool one = kRuns == 1 && units == __reduce_min_sync(0xffffffffu, least) && side_by_side(units);
 #pragma unroll
   for (int s = 0; s < kSets; ++s) {
     before[s] = cost[s] = 0;
