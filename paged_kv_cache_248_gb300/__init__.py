@@ -139,9 +139,12 @@ def _empty(shape, dtype, device, stream=None, shared=True) -> torch.Tensor:
     return t
 
 
-def _dev(t: torch.Tensor, name: str, dtype=None):
+def _dev(t: torch.Tensor, name: str, dtype=None, here: int | None = None):
+    """The pointer of a contiguous CUDA tensor, of this type and on device ``here`` where they are given."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if here is not None and t.get_device() != here:
+        raise ValueError(f"{name} must be a tensor on the current CUDA device (cuda:{here})")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
@@ -326,18 +329,16 @@ def pkv_tree_mask(parents: torch.Tensor, query_start_loc: torch.Tensor, max_quer
     node that each token continues (smaller than its own index), -1 for the context.
     ``depths``, if given, receives the number of ancestors (int32 [T])."""
     n, words = parents.shape[0], (int(max_query_len) + 63) // 64
-    for t, name in ((parents, "parents"), (query_start_loc, "query_start_loc"), (out, "out"), (depths, "depths")):
-        if t is not None and t.is_cuda and t.get_device() != torch.cuda.current_device():
-            raise ValueError(f"{name} must be a tensor on the current CUDA device (cuda:{torch.cuda.current_device()})")
     for t, name in ((out, "out"), (depths, "depths")):
         if t is not None and (t.dim() != (2 if name == "out" else 1) or t.shape[0] != n):
             raise ValueError(f"{name} must have a row for every token")
     if out is None:
         out = _empty((n, max(words, 1)), torch.int64, parents.device, stream)
-    _check(lib().pkv_tree_mask(_dev(parents, "parents", torch.int32),
-                               _dev(query_start_loc, "query_start_loc", torch.int32), query_start_loc.shape[0] - 1, n,
-                               _dev(out, "out", torch.int64), out.shape[1],
-                               _dev(depths, "depths", torch.int32) if depths is not None else None,
+    here = torch.cuda.current_device() if getattr(parents, "is_cuda", False) else None
+    _check(lib().pkv_tree_mask(_dev(parents, "parents", torch.int32, here),
+                               _dev(query_start_loc, "query_start_loc", torch.int32, here), query_start_loc.shape[0] - 1,
+                               n, _dev(out, "out", torch.int64, here), out.shape[1],
+                               _dev(depths, "depths", torch.int32, here) if depths is not None else None,
                                _stream(stream)), "pkv_tree_mask")
     return out
 

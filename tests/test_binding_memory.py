@@ -51,7 +51,8 @@ def pkv(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: HOST, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: here[-1].cuda_stream, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: False, raising=False)
-    monkeypatch.setattr(m, "_dev", lambda t, name, dtype=None: None)
+    monkeypatch.setattr(m, "_dev", lambda t, name, dtype=None, here=None: None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: HOST)
     monkeypatch.setattr(m, "_nat", None)  # set up anew with the stand-ins, and again with torch's own after the test
     m.main_stream = main
     yield m
