@@ -132,6 +132,8 @@ def _empty(shape, dtype, device, stream=None, shared=True) -> torch.Tensor:
     stream uses the tensor too, so its memory does not go to the next one before that use is over either."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):  # (another library's: its handle will do)
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
     if shared:

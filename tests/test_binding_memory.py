@@ -17,6 +17,11 @@ class Kept(torch.Tensor):
         LOG.append(("record", stream))
 
 
+class Stream:
+    def __init__(self, cuda_stream, name):
+        self.cuda_stream, self.name = cuda_stream, name
+
+
 LOG = []
 MADE = []
 
@@ -29,7 +34,7 @@ def pkv(monkeypatch):
     m.lib()
     LOG.clear()
     MADE.clear()
-    main = types.SimpleNamespace(cuda_stream=0, name="main")
+    main = Stream(0, "main")
     here = [main]
     real = torch.empty
 
@@ -47,6 +52,8 @@ def pkv(monkeypatch):
 
     monkeypatch.setattr(torch, "empty", empty)
     monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: Stream(handle, "foreign"))
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: here[-1])
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: HOST, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: here[-1].cuda_stream, raising=False)
@@ -92,13 +99,20 @@ def test_a_named_stream_works_in_memory_of_its_own(pkv, call):
     """The allocator may hand out memory whose last user still runs on the stream that it is asked on.  So whatever a call
     on a named stream writes is asked for on that stream; and what it returns, which the caller's stream reads later, is
     recorded there."""
-    side = types.SimpleNamespace(cuda_stream=7, name="side")
+    side = Stream(7, "side")
     got = CALLS[call](pkv, stream=side)
     results = got if isinstance(got, tuple) else (got,)
     asked = [s for what, s in LOG if what == "empty"]
     assert len(asked) >= len(results) and all(s is side for s in asked), [s.name for s in asked]
     recorded = [s for what, s in LOG if what == "record"]
     assert len(recorded) >= len(results) and all(s is pkv.main_stream for s in recorded), [s.name for s in recorded]
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_a_stream_that_is_not_torchs_needs_its_handle_only(pkv, call):
+    CALLS[call](pkv, stream=types.SimpleNamespace(cuda_stream=9))
+    asked = [(s.cuda_stream, s.name) for what, s in LOG if what == "empty"]
+    assert asked and all(s == (9, "foreign") for s in asked)
 
 
 @pytest.mark.parametrize("call", CALLS)

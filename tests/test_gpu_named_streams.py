@@ -96,3 +96,18 @@ def test_results_of_a_named_stream_outlive_their_use_on_the_current_one(pkv):
         del other
     torch.cuda.synchronize()
     assert torch.equal(total, want)
+
+
+def test_streams_of_another_library(pkv):
+    """Anything that tells a stream's handle names it."""
+    import types
+    side = torch.cuda.Stream()
+    for name, (call, _) in calls(pkv).items():
+        want = call()
+        torch.cuda.synchronize()
+        extra = {"refs": torch.cat([torch.ones(4096), torch.zeros(512)]).int().cuda()} if name == "fork" else {}
+        torch.cuda.synchronize()
+        got = call(stream=types.SimpleNamespace(cuda_stream=side.cuda_stream), **extra)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+    assert pkv.pkv_get_last_error() == 0
