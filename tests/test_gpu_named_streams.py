@@ -41,6 +41,7 @@ def calls(pkv):
     ftd, fld, fpd, r0 = dev(ft), dev(fl), dev(fp), dev(refs0)
 
     def fork(stream=None, refs=None):
+        assert stream is None or refs is not None  # (a count made here would be the current stream's)
         return pkv.pkv_fork_tables(ftd, fld, fpd, refs if refs is not None else r0.clone(), None, None, stream=stream)
 
     n = ctypes.c_int64(0)
@@ -110,4 +111,34 @@ def test_streams_of_another_library(pkv):
         got = call(stream=types.SimpleNamespace(cuda_stream=side.cuda_stream), **extra)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+    assert pkv.pkv_get_last_error() == 0
+
+
+@pytest.mark.parametrize("name", ["tree", "mask", "beam", "fork"])
+def test_named_streams_within_a_captured_graph(pkv, name):
+    """A captured call on a side stream keeps memory of the graph's: replays after other work give the same again."""
+    call, _ = calls(pkv)[name]
+    want = call()
+    refs = torch.cat([torch.ones(4096), torch.zeros(512)]).int().cuda()
+    first = refs.clone()
+    extra = {"refs": refs} if name == "fork" else {}
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        refs.copy_(first)
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(stream=side, **extra)
+        other = torch.full((1 << 24,), 5.0, device="cuda") * 2  # work of the capturing stream meanwhile
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        junk = [torch.full((1 << 22,), 9.0, device="cuda") for _ in range(4)]
+        own = {"refs": first.clone()} if name == "fork" else {}
+        side.wait_stream(torch.cuda.current_stream())
+        g.replay()
+        again = call(stream=side, **own)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and (other == 10).all()
+        assert all(torch.equal(a, b) for a, b in zip(again, want))
+        del junk
     assert pkv.pkv_get_last_error() == 0
