@@ -13,8 +13,8 @@
 // maximum, the exponents relative to it and their sum in fp32.  No block shares anything with
 // another, and equal rows have equal sums, so that their ties stay ties.  Bound: reading the
 // logits (64 x 4 rows of 128256 bf16, 66 MB: 14.4 us, 67 % of a copy's rate; five CTAs an SM keep
-// 80 KB of loads under way, and loading the next block ahead as well was slower, 20 instead of 17.6
-// us for the call, because fewer warps fit).
+// 80 KB of loads under way, and loading the next block ahead in registers as well was slower,
+// because fewer warps fit).
 //
 // select_kernel.  One CTA per request joins the sums, ranks the blocks' maxima, collects what its
 // best blocks hold, and ranks that, all by 64-bit scores.  Bound: the latency of its steps, 10
@@ -25,9 +25,10 @@
 // 3500.  A threshold that leaves few candidates comes from ranking 128 maxima against one another
 // (600 cycles; a search bit by bit, with a barrier a bit, took 4000).
 //
-// Whole calls: 7.8 us for one request of 4 beams and 32000 logits, 17.6 us for the batch above (HBM
-// needs 9.7), 15.7 us for 9 requests of 16 beams and 50257 fp32 logits, 32 selected, a quarter of the
-// beams finished (3.1).
+// Whole calls, on logits that are not in L2: 21.0 us for the batch above (HBM needs 9.7), 18.1 us for 9
+// requests of 16 beams and 50257 fp32 logits, 32 selected, three in ten beams finished (3.1); on logits
+// that are, as a model's last product leaves small ones, 17.6 and 15.4 us, and 7.7 us for one request of
+// 4 beams and 32000 logits.
 #include "pkv_internal.cuh"
 #include "ptx.cuh"
 #include "softmax_row.cuh"

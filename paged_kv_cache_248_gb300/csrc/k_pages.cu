@@ -5,8 +5,8 @@
 // Technical Details: samples share blocks until they diverge, and a block without users
 // is free again).
 //
-// Both move bytes and count; neither computes.  They are bound by launch and memory
-// latency at one layer and by HBM over the layers of a model.
+// Both move bytes and count; neither computes.  They are bound by launch and memory latency at one
+// layer; over the layers of a model forking is bound by HBM, moving a path still by latency.
 #include "pkv_internal.cuh"
 
 namespace pkv {
@@ -17,9 +17,10 @@ namespace {
 // V rows (one kv head, one piece of a row) and moves them node by node: path[a] >= a
 // because the path ascends, so position c + a is never a source of a later move and a
 // thread may overwrite it once it has loaded the sources up to a.  Columns are
-// independent, so the threads need no order among them.  8 rows at a time hide the loads' latency:
-// 33 requests in one layer take 2.8 us, 64 in 32 layers (12 of 64 nodes, 92 MB of reads and
-// writes) 14.5 us (13.6 at a copy's rate).
+// independent, so the threads need no order among them.  8 rows at a time hide part of the loads'
+// latency, which is the bound: before its first row a CTA loads lengths, path and table, each by the
+// one before.  33 requests in one layer take 2.7 us, 64 in 32 layers (12 of 64 nodes, 92 MB of reads
+// and writes, 13.6 us at a copy's rate) 19.2 us, and 14.5 where L2 holds the rows; DRAM is 31 % busy.
 constexpr int kMoveThreads = 256;
 constexpr int kMoveBatch = 8;     // rows a thread holds in registers between loads and stores
 constexpr int kMoveChunk = 256;   // path entries staged in shared memory at a time
@@ -115,11 +116,11 @@ __global__ void __launch_bounds__(kMoveThreads) compact_path_kernel(const MovePa
 // as every row has its blocks.  fork_finish_kernel (a CTA per row, layer and slice): the
 // copies and the counts of copied and fresh blocks; after an error, everything back.
 // 64 requests of 8 beams and 16 layers copy 503 MB: 74 us, a copy's rate (the first two launches hide
-// behind the copies of the call before).  One request of 5 beams takes 6.5 us, all of it latency.
+// behind the copies of the call before).  One request of 5 beams takes 6.3 to 7.2 us, all of it latency.
 //
 // Up to 32 rows of up to kFewBlocks blocks: the assigning CTA gathers by itself, a warp per row,
-// which saves a launch: 6.7 us instead of 7.2 for 5 rows of 20 blocks, 9.4 / 9.9 for 32 of 32,
-// 12.1 / 12.0 for 32 of 128, 16.1 / 13.2 for 32 of 512, and 2 us on the host.
+// which saves a launch: 0.5 us less for 5 rows of 20 blocks and for 32 of 32, as long for 32 of 128,
+// 3 us more for 32 of 512; and 2 us less on the host.
 constexpr int kForkThreads = 256;
 constexpr int kAssignThreads = 1024;
 constexpr int kForkMaxRows = 4096;

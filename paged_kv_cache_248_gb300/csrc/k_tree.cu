@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(128) tree_mask_kernel(const int32_t* __restric
 // 5 requests of 100 to 700 keys with 3 to 13 nodes, 8 / 2 heads of 64: 12.7 us, of which the
 // joining kernel is 3 (one CTA per node and kv head, keys in turn, took 132).
 // 4 requests of 4000 keys with 24 nodes, 32 / 8 heads of 64 (3.1 GFLOP): 105 us, 40 % of the FMA
-// rate, with four CTAs an SM (two: 129); heads of 128 leave room for two.
+// rate, with four CTAs an SM (two: 121); heads of 128 leave room for two.
 constexpr int kRows = 32;      // rows of a unit
 constexpr int kKeys = 64;      // keys of a tile
 constexpr int kThreads = 128;

@@ -12,15 +12,15 @@
 // row tile, or two) and goes over all of the request's key tiles of 128 keys.
 //
 // Cut.  All units' key tiles, one after the other (and two places more for each unit, whose
-// beginning and end take time too: 64 requests 123, 112, 110 us with 0, 1, 2 of them), are cut into
-// equal runs, so that one long request and a thousand short ones keep every SM equally busy; a CTA
+// beginning and end take time too: 33 requests of 0..1500 keys 36.2, 31.4, 30.2 us with 0, 1, 2 of
+// them), are cut into equal runs, so that one long request and a thousand short ones keep every SM equally busy; a CTA
 // derives its runs from the lengths by itself, without a planning launch.  A unit that lies within
 // one run is finished there; of one that is cut, each run leaves its rows' unnormalised accumulator,
 // maximum and sum, and the merge kernel joins them in order.  A run leaves at most two such
 // partials.  Where every kv head of every request that has rows has the same number of units, above
 // one, as many runs at a time go through the same keys, each for one of the units, so that K and V come
-// from HBM once and not once a unit (8 requests of 32768 keys with 512 rows: 2.17 GB read and 415 us
-// one unit after the other, 1.09 GB and 391 us side by side); see side_by_side for what it costs.
+// from HBM once and not once a unit (8 requests of 32768 keys with 512 rows: 2.17 GB read and 398 us
+// one unit after the other, 1.09 GB and 373 us side by side); see side_by_side for what it costs.
 //
 // Streams.  Two S/P/O accumulator sets live in TMEM, each with a softmax warpgroup of its own, so
 // that one softmax runs while the tensor core works for the other.
@@ -32,20 +32,20 @@
 //
 // Per CTA (352 threads): warp 0 finds the runs' units and loads Q and K, warp 10 loads V (TMA
 // boxes of the blocks' 16-token rows, 128-byte swizzle; 2 K and 2 V tiles in flight: a third V tile
-// takes the shared memory that the L1 then lacks, 113 us instead of 108 for the 64 requests; L2 is
-// told to drop what it passed on first, 115 us instead of 123), warp 1 issues the MMAs, warps 2-5
-// and 6-9 are the streams' softmax.  The tiles
+// takes the shared memory that the L1 then lacks, and 5 % more time for the 64 requests below; L2 is
+// told to drop what it passed on first, 101.5 us instead of 111 for them), warp 1 issues the MMAs,
+// warps 2-5 and 6-9 are the streams' softmax.  The tiles
 // that hold drafted keys (the last one or two of a request) take their visibility from the
 // mask row's bits, the others see every key.  Their V rows are looked through for values that
 // are not finite: a zero weight times those would reach rows that do not see them, so they
 // are taken out of the tile and given back, at the end, to the rows that do.
 //
-// Bound, 32 / 8 heads: 64 requests of 128..4096 keys with 16 nodes read 558 MB: 101 us, of which the
-// merge is 7 (82 us at a copy's rate; DRAM 72 % busy).  8 requests of 32768 keys with 64 nodes,
-// 64 / 8 heads, are 550 GFLOP: 375 to 420 us as the power limit has it (290 us at the rate of a large
+// Bound, 32 / 8 heads: 64 requests of 128..4096 keys with 16 nodes read 558 MB: 103 us, of which the
+// merge is 7 (82 us at a copy's rate; DRAM 73 % busy).  8 requests of 32768 keys with 64 nodes,
+// 64 / 8 heads, are 550 GFLOP: 375 to 425 us as the power limit has it (290 us at the rate of a large
 // matrix product, 320 us at the one that the limit sustains); softmax and MMAs of the two streams
 // alternate, about 1900 cycles a turn each, and the tensor pipe is busy for 64 % of the time.  One
-// request of 500 keys: 9.7 us, nearly all latency: 1.3 us until its run is known, 2 until its first tile
+// request of 500 keys: 10 us, nearly all latency: 1.3 us until its run is known, 2 until its first tile
 // is on its way, 0.6 until that is there, 3 for the products and the softmax, 2 for the merge.
 //
 // All waits are bounded (ptx.cuh).
@@ -320,8 +320,8 @@ __device__ void find_runs(const Params& P, Ctl& c) {
 }
 
 // The same for up to kFewSeqs requests by warp 0 alone, which is the one that walks the runs: no
-// barriers, and the requests' loads are all on their way at once (one request 10.7 instead of 11.4
-// us, 64 requests 100.7 instead of 101.9).
+// barriers, and the requests' loads are all on their way at once (one request 9.8 instead of 10.9
+// us, 33 requests 30.2 instead of 31.4, 64 requests 101.5 instead of 102.3).
 constexpr int kFewSeqs = 128;
 template <int kRuns>
 __device__ void find_runs_few(const Params& P, Ctl& c) {
@@ -627,7 +627,8 @@ __device__ void producer_warp(const Params& P, bool is_k, const CUtensorMap* qma
 // ------------------------------------------------------------------ MMA warp
 // One elected thread issues every MMA, but the whole warp walks through the tiles, with values
 // that the compiler can tell to be the same in all of its lanes: the operands of an MMA live in
-// uniform registers, and values of one thread have to be moved there before each (8 requests of 32768 keys: 470 -> 390 us).
+// uniform registers, and values of one thread have to be moved there before each (a tenth
+// more time for 8 requests of 32768 keys).
 // A stream's step is P V of its tile before, then S of its next tile: MMAs of one thread complete in
 // order, so S cannot overwrite the P that this P V reads, and S being complete tells the softmax
 // that O holds every tile before.
@@ -872,7 +873,7 @@ __device__ __noinline__ void give_back(const Params& P, const Item& item, const 
 
 // (Code size: the streams, the MMA thread and the producers run different code by turns.  With every
 // loop below unrolled, two thirds of the instruction fetches missed the SM's cache and all of its
-// warps waited for instructions: 64 requests of 128..4096 keys took 169 us instead of 124.)
+// warps waited for instructions: 64 requests of 128..4096 keys took a third longer.)
 template <int kRuns>
 __device__ void softmax_warps(const Params& P, Ctl& c, uint8_t* vbuf, uint32_t tmem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1223,11 +1224,12 @@ int launch_tree_tc(const TreeArgs& t, void* workspace, int num_sms, uint32_t* er
   st = encode_tensor_map_3d(&qm, a.q, qdims, qstrides, qbox);
   if (st) return st;
   // Requests with more rows than a tile share K and V between two of them, if they are long: 68 requests
-  // with 12 / 4 heads and 61 nodes each take 56, 79 us with 1500, 3000 keys, and 70, 110 in single row
+  // with 12 / 4 heads and 61 nodes each take 68, 100 us with 1500, 3000 keys, and 92, 153 in single row
   // tiles.  For short ones a unit's beginning and end count more, which streams that work for
-  // themselves have twice as fast: 6 requests of 40, 200, 400 keys take 11.4, 15.4, 15.9 us (17.4,
-  // 20.8, 20.9 in pairs), 68 of 400 with 2 to 61 nodes 32.5 (34.1).  Where no request has more rows
-  // than a tile, the second stream of a pair would rest: 64 requests of 16 nodes 101 us (107 in pairs).
+  // themselves have twice as fast: 6 such requests of 40, 200, 400 keys take 9.9, 14.8, 16.5 us (14.6,
+  // 19.5, 18.1 in pairs), 68 of 400 with 2 to 61 nodes 32.5 (33.1).  Where no request has more rows than
+  // a tile, the second stream of a pair would rest: one request of 7 nodes 9.7 us (12.3 in pairs), 64 of
+  // 20..300 keys and 16 nodes 28.6 (31.5); what reads enough is bound by that (64 of 128..4096: 101.5 both).
   const bool pairs = a.max_query_len > p.rows_q && a.max_seq_len > kShortKeys;
   p.unit_q = pairs ? 2 * p.rows_q : p.rows_q;
   p.unit_q_log2 = 7 - p.gp_log2 + (pairs ? 1 : 0);
@@ -1264,7 +1266,7 @@ int launch_tree_tc(const TreeArgs& t, void* workspace, int num_sms, uint32_t* er
   p.rows_cap = l.rows_cap;
   p.out_v8 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 ? 1 : 0;
   // Few rows: a warp takes as long for one live row as for 32, so the streams' live rows go to
-  // different SM sub-partitions (a warp's TMEM quarter is its sub-partition): 100.7 instead of 101.6
+  // different SM sub-partitions (a warp's TMEM quarter is its sub-partition): 101.5 instead of 101.8
   // us for 64 requests of 16 nodes.
   if (!pairs && l.rows_cap <= 64) p.row0[1] = 64;
   p.scale_log2 = a.scale * 1.4426950408889634f;

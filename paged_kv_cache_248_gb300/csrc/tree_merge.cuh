@@ -5,8 +5,8 @@
 // added up in the order of the keys.  The rows of a unit are shared out among the CTAs of its
 // parts.  Up to 16 parts a warp joins a row's; of more, the CTA's warps join an eighth each, and one
 // of them the eighths, in order.  Loads of four parts are under way at once, since latency is what
-// this costs (2 requests of 8000 and 15000 keys, 2 kv heads, up to 100 parts: 15.7 us a call, and 22 with
-// a warp for all of a row's parts).
+// this costs (2 requests of 8000 and 15000 keys, 8 nodes, 8 / 2 heads, up to 100 parts: 18.5 us a call,
+// and 20.8 with a warp for all of a row's parts).
 #pragma once
 #include "pkv_internal.cuh"
 
@@ -16,7 +16,7 @@ constexpr int kMergeThreads = 256;
 constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kManyParts = 16;
 // CTAs per part.  (A unit has two parts or more, so that this makes for one turn of its rows, or two; twice
-// as many CTAs take longer to start than they save: 102.4 instead of 100.1 us for 64 requests of 16 nodes.)
+// as many CTAs take longer to start than they save: 102.1 instead of 101.5 us for 64 requests of 16 nodes.)
 inline unsigned merge_ctas(int rows_cap) { return static_cast<unsigned>(rows_cap > 128 ? 4 : (rows_cap + 31) / 32); }
 
 // What a part of a unit that is cut leaves besides its rows, at the slot of its partials.
