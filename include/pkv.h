@@ -28,6 +28,13 @@
  *   pkv_fork_tables        block tables after the beams they continue: reference
  *                          counts, freed and fresh blocks, copy-on-write
  *
+ * and a decoding step over a cache that may be held in 8 bits:
+ *
+ *   pkv_rope_append        new queries and keys rotated by their positions, keys and values
+ *                          put into the cache (of any type, 8 bits among them)
+ *   paged_attention_q8     paged_attention over a cache in 8 bits
+ *   pkv_sample             tokens drawn from logits: temperature, top-k, min-p, top-p
+ *
  * Conventions for every call
  *  - Pointers named as device pointers must point to device memory of the current
  *    CUDA device; `stream` is a cudaStream_t (NULL = legacy default stream).  All
@@ -50,7 +57,9 @@
  * Cache layout (a reading where the pages are silent): k_cache and v_cache are
  * each [num_blocks][num_kv_heads][16][head_dim], row-major, so that one
  * (block, kv head) is a contiguous 16 x head_dim tile.
- * Supported element types: fp32 with head_dim 64 or 128; bf16 with head_dim 128.
+ * Supported element types: fp32 with head_dim 64 or 128; bf16 with head_dim 128.  A cache
+ * in 8 bits (PKV_E4M3, head_dim 128) is served by pkv_rope_append and paged_attention_q8; any
+ * other call refuses it.
  */
 #ifndef PKV_H_
 #define PKV_H_
@@ -77,7 +86,11 @@ typedef enum {
   PKV_ERR_TIMEOUT = 6      /* a kernel gave up a bounded wait (internal error) */
 } pkv_status;
 
-typedef enum { PKV_F32 = 0, PKV_BF16 = 1 } pkv_dtype;
+typedef enum {
+  PKV_F32 = 0,
+  PKV_BF16 = 1,
+  PKV_E4M3 = 2 /* 8 bits: sign, 4 of exponent, 3 of mantissa; a value is its code times a scale */
+} pkv_dtype;
 
 #define PKV_BLOCK_SIZE 16
 
@@ -423,13 +436,104 @@ PKV_API int pkv_fork_tables(const int32_t* block_tables, const int32_t* seq_lens
                             int64_t workspace_bytes, void* stream);
 PKV_API int pkv_fork_workspace(int32_t num_rows, int64_t* bytes);
 
+/*
+ * pkv_rope_append -- the new tokens' keys and values into the paged cache, keys (and queries)
+ * rotated by their positions on the way: what pkv_slot_mapping and pkv_write do, from a
+ * projection's raw output ("vLLM's PagedAttention" teardown, section "PagedAttention": new
+ * tokens go to the slots that their block table names).
+ * Token j of request i sits at position p = seq_lens[i] - q_i + j, in slot block_tables[i][p / 16] *
+ * 16 + p % 16.  Its queries and keys turn by row a = positions[t] (NULL: p) of cos_sin: with half =
+ * rot_dim / 2, pair m of a head's first rot_dim elements, (x, y) = elements (m, m + half), or (2m,
+ * 2m + 1) where interleaved is not 0, becomes
+ *     (x cos_sin[a][m] - y cos_sin[a][half + m],  y cos_sin[a][m] + x cos_sin[a][half + m]).
+ * Elements past rot_dim and values stay as they are.  Results are computed in fp32 and rounded once,
+ * to the type of q_out and of the cache.
+ * An 8-bit cache (PKV_E4M3) holds codes; the value in slot s of block b is code * scales[b][h][0] for K and
+ * scales[b][h][1] for V.  Where the call's tokens begin a block (its first position is among them, or the
+ * request has none before), its scales are made anew, otherwise they can only grow: to the
+ * least power of two s, at least 2^-80, with |x| <= 448 s for all finite new values x of the block and
+ * head.  What the block held of the request is then put in the new units (each code rounded again, which
+ * changes only those that leave e4m3's normal range where scales are powers of two).  Infinities
+ * become +-448 s, NaN stays NaN.
+ * q               device [num_tokens][num_q_heads][head_dim], tokens q_stride elements apart; NULL: none
+ * k, v            device [num_tokens][num_kv_heads][head_dim], tokens k_stride and v_stride elements apart
+ *                 (slices of one projection's output will do); strides of at least a token's elements, 16-byte
+ *                 aligned as all of its rows
+ * dtype           of q, k, v and q_out: the cache's, PKV_BF16 for an 8-bit cache
+ * cos_sin         device fp32 [num_angles][rot_dim], 16-byte aligned; rot_dim a multiple of 16, 0 to head_dim (0:
+ *                 nothing turns, cos_sin is not read)
+ * positions       optional device int32 [num_tokens]: rows of cos_sin (a drafted tree's tokens turn by
+ *                 their depth, not by their slot)
+ * scales          device fp32 [num_blocks][num_kv_heads][2] of an 8-bit cache, updated; NULL for others
+ * max_query_len   host bound on q_i: a request with more is flagged, its tokens not written
+ * q_out           device, as q, tokens q_out_stride apart; written.  May be q itself (same stride); any other
+ *                 overlap with q, k or v is refused
+ * Rows of tokens behind the last request stay as they are.
+ * Device errors: a request whose lengths do not fit or a row outside of [0, num_angles) flag PKV_ERR_INDEX, its
+ * tokens are not written and their q_out rows are zero; so is a bad block id, whose q_out row stays valid.
+ */
+PKV_API int pkv_rope_append(const void* q, const void* k, const void* v, int32_t dtype, int64_t q_stride,
+                            int64_t k_stride, int64_t v_stride, int32_t num_q_heads, const float* cos_sin,
+                            int32_t rot_dim, int32_t interleaved, int64_t num_angles, const int32_t* positions,
+                            void* k_cache, void* v_cache, float* scales, const pkv_cache_desc* cache,
+                            const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                            const int32_t* query_start_loc, int32_t num_seqs, int64_t num_tokens,
+                            int32_t max_query_len, void* q_out, int64_t q_out_stride, void* stream);
+
+/*
+ * paged_attention_q8 -- paged_attention() over a cache in 8 bits (cache->dtype PKV_E4M3, head_dim 128, up to 16
+ * query heads a kv head): the same sum over K_u = code * scales[b][g][0] and V_u = code * scales[b][g][1] of
+ * block b = block_tables[i][u / 16].  q and out are bf16.  Chunks and single tokens mix freely.
+ * scales          device fp32 [num_blocks][num_kv_heads][2]; positive.  V's are taken as at least 2^-80 and at
+ *                 most 2^110
+ * max_query_len   host bound on q_i: a request with more is flagged (PKV_ERR_INDEX) and its rows zeroed
+ * query_start_loc rows outside of [0, num_tokens) are flagged too; rows that no request has stay as they are
+ * workspace       device memory of at least pkv_q8_workspace() bytes, 256-byte aligned
+ * What a row does not see (later tokens of its chunk, slots behind the context) has no part in it, whatever its
+ * codes are, NaN among them.  A NaN that a row sees makes the row's elements NaN.
+ * Everything else and the errors: as paged_attention().  Work is cut along the keys by the batch's
+ * sizes, so rounding (not the result) may depend on the batch.
+ */
+PKV_API int paged_attention_q8(const void* q, const void* k_cache, const void* v_cache, const float* scales,
+                               const pkv_cache_desc* cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                               const int32_t* seq_lens, const int32_t* query_start_loc, int32_t num_seqs,
+                               int32_t num_q_heads, int64_t num_tokens, int32_t max_query_len, int32_t max_seq_len,
+                               float scale, void* out, void* workspace, int64_t workspace_bytes, void* stream);
+/* Bytes of workspace that paged_attention_q8 needs for these sizes (*bytes). */
+PKV_API int pkv_q8_workspace(const pkv_cache_desc* cache, int32_t num_q_heads, int32_t max_query_len,
+                             int64_t* bytes);
+
+/*
+ * pkv_sample -- one token for each row of logits, drawn with a given random number.  Row n's candidates are its
+ * finite logits x, in order: larger ones first, of equal ones the lower index; a candidate's weight is
+ * exp((x - max) / temperature[n]).  Kept are, one after the other,
+ *     the first top_k[n] of them (0 or less: all),
+ *     of these the ones whose weight is at least min_p[n] (that of the first is 1; 0 or less: all),
+ *     of these the shortest beginning whose weights are at least top_p[n] of the sum (1 or more: all; one at least).
+ * The token is the first of the kept ones whose cumulative weight exceeds uniform[n] times their sum.
+ * temperature[n] == 0 takes the first candidate.  Weights are right to 2^-40 and their sums exact, so
+ * that two tokens are told apart as 64-bit arithmetic does, and a call repeats bit by bit.
+ * logits          device [num_seqs] rows of vocab values of `dtype` (pkv_dtype: fp32 or bf16), row_stride elements
+ *                 apart (>= vocab), aligned to their type; vocab up to 2^20
+ * temperature, top_k, top_p, min_p  optional device fp32, int32, fp32, fp32 [num_seqs] (NULL: 1, all, 1, 0)
+ * uniform         device fp32 [num_seqs], in [0, 1)
+ * out_tokens      device int32 [num_seqs]
+ * out_logprobs    optional device fp32 [num_seqs]: log of the token's share of the kept weights
+ * A row without a candidate gives token -1 and -inf; so does a setting outside of its range (a temperature that is
+ * negative or not finite, uniform outside of [0, 1), top_p below 0, min_p above 1, a NaN), which flags bit 5
+ * (PKV_ERR_INDEX).
+ */
+PKV_API int pkv_sample(const void* logits, int32_t dtype, int64_t row_stride, const float* temperature,
+                       const int32_t* top_k, const float* top_p, const float* min_p, const float* uniform,
+                       int32_t num_seqs, int32_t vocab, int32_t* out_tokens, float* out_logprobs, void* stream);
+
 /* Synchronises `stream`, returns the device error word of the current device as a
  * pkv_status (PKV_OK, PKV_ERR_INDEX, PKV_ERR_TIMEOUT, or PKV_ERR_NO_MEMORY where a fork
  * that found too few free blocks is all there is) and clears it. */
 PKV_API int pkv_get_last_error(void* stream);
 
 /* Raw device error bits of the current device (bit 0 bad block id, bit 1 bad slot,
- * bit 2 bad length, bit 3 wait timeout, bit 4 no free block left); synchronises `stream`; does not clear. */
+ * bit 2 bad length, bit 3 wait timeout, bit 4 no free block left, bit 5 a sampling setting out of range); synchronises `stream`; does not clear. */
 PKV_API int pkv_peek_error_bits(void* stream, uint32_t* bits);
 
 /* Human-readable name of a pkv_status value (static string). */
@@ -448,8 +552,8 @@ PKV_API void pkv_shutdown(void);
  * returns, per kernel kind, the launch count and the summed device time in ms,
  * then resets the counters.  Kinds: 0 slot mapping, 1 write, 2 copy, 3 plan,
  * 4 decode, 5 prefill, 6 generic attention, 7 split merge, 8 shared-prefix (cascade)
- * pass.  Arrays hold PKV_TRACE_KINDS entries.  (The calls for candidate continuations,
- * pkv_tree_mask to pkv_fork_tables, are not traced.)
+ * pass.  Arrays hold PKV_TRACE_KINDS entries.  (The calls for candidate continuations
+ * and those of a step over a cache in 8 bits, pkv_tree_mask to pkv_sample, are not traced.)
  */
 #define PKV_TRACE_KINDS 9
 PKV_API int pkv_trace_enable(int on);
@@ -468,11 +572,14 @@ PKV_API const char* pkv_trace_kind_name(int kind);
  * [128 rows][a_bytes / 512] 32-bit columns, two bf16 each, stored to the rows' lanes
  * after the N accumulator columns, and a_off[k] is k step k's first column (a multiple
  * of 8) within them.
+ * pkv_umma8_selftest is the same for e4m3 operands (kind::f8f6f4, 32 along K to an MMA),
+ * both from shared memory.
  * pkv_tma_selftest loads rows [row0, row0+16) of a bf16 [rows][128] matrix with two
  * 16 x 64 boxes in the 128-byte swizzle and copies the 4 KiB of shared memory they
  * land in to dump.
  */
 PKV_API int pkv_umma_selftest(const int32_t* params, const void* a_img, const void* b_img, float* d_out, void* stream);
+PKV_API int pkv_umma8_selftest(const int32_t* params, const void* a_img, const void* b_img, float* d_out, void* stream);
 PKV_API int pkv_tma_selftest(const void* src, int64_t rows, int32_t row0, void* dump, void* stream);
 /*
  * pkv_wait_selftest launches one CTA that waits on an mbarrier nothing arrives on.

@@ -15,6 +15,7 @@ Functions carry the C names:
   pkv_slot_mapping, pkv_write, pkv_copy_blocks, paged_attention, paged_attention_cascade,
   paged_attention_step,
   pkv_tree_mask, paged_attention_tree, pkv_compact_path, pkv_beam_select, pkv_fork_tables,
+  pkv_rope_append, paged_attention_q8, pkv_sample,
   pkv_get_last_error, pkv_peek_error_bits, pkv_trace_enable, pkv_trace_read,
   pkv_num_workers, pkv_shutdown, pkv_umma_selftest, pkv_tma_selftest, pkv_wait_selftest.
 """
@@ -31,7 +32,7 @@ LIB_PATH = os.path.join(_HERE, "libpkv.so")
 
 PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_INDEX = 0, 1, 2, 3
 PKV_ERR_CUDA, PKV_ERR_NO_MEMORY, PKV_ERR_TIMEOUT = 4, 5, 6
-PKV_F32, PKV_BF16 = 0, 1
+PKV_F32, PKV_BF16, PKV_E4M3 = 0, 1, 2
 BLOCK_SIZE = 16
 TRACE_KINDS = 9
 
@@ -86,12 +87,18 @@ def lib():
                 "pkv_beam_select": [P, i32, i64, P, P, i32, i32, i32, i32, i32, P, P, P, P, i64, P],
                 "pkv_fork_workspace": [i32, ctypes.POINTER(i64)],
                 "pkv_fork_tables": [P, P, i32, i32, P, i32, P, P, P, P, P, D, i32, P, i64, P],
+                "pkv_rope_append": [P, P, P, i32, i64, i64, i64, i32, P, i32, i32, i64, P, P, P, P, D, P, i32, P, P, i32, i64,
+                                    i32, P, i64, P],
+                "pkv_q8_workspace": [D, i32, i32, ctypes.POINTER(i64)],
+                "paged_attention_q8": [P, P, P, P, D, P, i32, P, P, i32, i32, i64, i32, i32, f32, P, P, i64, P],
+                "pkv_sample": [P, i32, i64, P, P, P, P, P, i32, i32, P, P, P],
                 "pkv_get_last_error": [P],
                 "pkv_peek_error_bits": [P, ctypes.POINTER(ctypes.c_uint32)],
                 "pkv_num_workers": [ctypes.POINTER(ctypes.c_int32)],
                 "pkv_trace_enable": [ctypes.c_int],
                 "pkv_trace_read": [ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_double)],
                 "pkv_umma_selftest": [P, P, P, P, P],
+                "pkv_umma8_selftest": [P, P, P, P, P],
                 "pkv_tma_selftest": [P, i64, i32, P, P],
                 "pkv_wait_selftest": [P],
             }
@@ -397,6 +404,47 @@ def pkv_fork_tables(block_tables: torch.Tensor, seq_lens: torch.Tensor, parents:
                                     workspace, stream)
 
 
+# ----------------------------------------------------------------------------- a step over a cache in 8 bits
+# (through _native too)
+def pkv_rope_append(k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor | None, k_cache: torch.Tensor,
+                    v_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                    query_start_loc: torch.Tensor, max_query_len: int, q: torch.Tensor | None = None,
+                    scales: torch.Tensor | None = None, positions: torch.Tensor | None = None, interleaved: bool = False,
+                    q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """New tokens' keys, rotated by their positions, and values into the paged cache; returns the queries ``q``
+    rotated likewise (None without any).  ``k``, ``v`` [T, Hkv, d] and ``q`` [T, Hq, d] may be slices of one
+    projection's output.  ``cos_sin`` fp32 [positions, rot_dim]: cosines, then sines, of each position's rot_dim / 2
+    angles, for the first rot_dim elements of a head, in halves or (``interleaved``) in neighbours; None: nothing turns.
+    ``positions`` int32 [T]: rows of it other than the tokens' places in the context.  A cache of the
+    inputs' type, or one in 8 bits (uint8 or float8_e4m3fn, bf16 inputs) with ``scales`` fp32
+    [blocks, Hkv, 2], which grow as a block fills.  ``q_out`` may be ``q``."""
+    return (_nat or _calls()).append(k, v, cos_sin, k_cache, v_cache, block_tables, seq_lens, query_start_loc,
+                                      max_query_len, q, scales, positions, interleaved, q_out, stream)
+
+
+def paged_attention_q8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Tensor,
+                       block_tables: torch.Tensor, seq_lens: torch.Tensor, query_start_loc: torch.Tensor, scale: float,
+                       max_query_len: int, max_seq_len: int, out: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """paged_attention over a cache in 8 bits: e4m3 codes (uint8 or float8_e4m3fn) [blocks, Hkv, 16, 128] and a scale for
+    each block, head and of K and V, ``scales`` fp32 [blocks, Hkv, 2].  bf16 queries; chunks and single
+    tokens mix freely.  ``workspace``: scratch of a caller that keeps its own (uint8; calls that may overlap take one
+    each)."""
+    return (_nat or _calls()).q8(q, k_cache, v_cache, scales, block_tables, seq_lens, query_start_loc, scale, max_query_len,
+                                  max_seq_len, out, workspace, stream)
+
+
+def pkv_sample(logits: torch.Tensor, uniform: torch.Tensor, temperature: torch.Tensor | None = None,
+               top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None, min_p: torch.Tensor | None = None,
+               out: tuple[torch.Tensor, torch.Tensor] | None = None, stream=None):
+    """One token for each row of ``logits`` [N, V] (fp32 or bf16, rows contiguous), drawn with ``uniform`` fp32 [N] in
+    [0, 1): (tokens int32 [N], logprobs fp32 [N], each the log of its token's share of what was kept).  ``temperature``
+    (0: the largest logit), ``top_k`` int32 (0: all), ``min_p`` and ``top_p`` fp32, [N] each, filter in this order;
+    candidates go by logit, of equal ones by index, and the token is the first whose cumulative weight
+    exceeds ``uniform`` of the whole.  -1 and -inf where no logit is finite or a setting is out of its range."""
+    return (_nat or _calls()).sample(logits, uniform, temperature, top_k, top_p, min_p, out, stream)
+
+
 def pkv_get_last_error(stream=None) -> int:
     """Sync the stream; return (and clear) the device error status."""
     return int(lib().pkv_get_last_error(_stream(stream)))
@@ -438,6 +486,12 @@ def pkv_umma_selftest(params, a_img: torch.Tensor, b_img: torch.Tensor, d_out: t
     arr = (ctypes.c_int32 * 29)(*[int(x) for x in params])
     _check(lib().pkv_umma_selftest(arr, _dev(a_img, "a_img"), _dev(b_img, "b_img"),
                                    _dev(d_out, "d_out", torch.float32), _stream(stream)), "pkv_umma_selftest")
+
+
+def pkv_umma8_selftest(params, a_img: torch.Tensor, b_img: torch.Tensor, d_out: torch.Tensor, stream=None) -> None:
+    arr = (ctypes.c_int32 * 29)(*[int(x) for x in params])
+    _check(lib().pkv_umma8_selftest(arr, _dev(a_img, "a_img"), _dev(b_img, "b_img"),
+                                    _dev(d_out, "d_out", torch.float32), _stream(stream)), "pkv_umma8_selftest")
 
 
 def pkv_wait_selftest(stream=None) -> None:

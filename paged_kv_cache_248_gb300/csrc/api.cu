@@ -612,13 +612,22 @@ const char* pkv_trace_kind_name(int kind) {
   return kTraceNames[kind];
 }
 
-int pkv_umma_selftest(const int32_t* params, const void* a_img, const void* b_img, float* d_out, void* stream) {
+static int umma_selftest(const int32_t* params, const void* a_img, const void* b_img, float* d_out, bool eight_bit,
+                         void* stream) {
   if (!params || !a_img || !b_img || !d_out) return PKV_ERR_INVALID_ARG;
   if (!aligned16(a_img) || !aligned16(b_img)) return PKV_ERR_INVALID_ARG;
   int st = PKV_OK;
   DeviceCtx* ctx = device_ctx(&st);
   if (!ctx) return st;
-  return run_umma_selftest(params, a_img, b_img, d_out, ctx->err, as_stream(stream));
+  return run_umma_selftest(params, a_img, b_img, d_out, eight_bit, ctx->err, as_stream(stream));
+}
+
+int pkv_umma_selftest(const int32_t* params, const void* a_img, const void* b_img, float* d_out, void* stream) {
+  return umma_selftest(params, a_img, b_img, d_out, false, stream);
+}
+
+int pkv_umma8_selftest(const int32_t* params, const void* a_img, const void* b_img, float* d_out, void* stream) {
+  return umma_selftest(params, a_img, b_img, d_out, true, stream);
 }
 
 int pkv_tma_selftest(const void* src, int64_t rows, int32_t row0, void* dump, void* stream) {

@@ -1,4 +1,4 @@
-/* binding.c -- the calls for candidate continuations from Python, without the cost of ctypes.
+/* binding.c -- the calls for candidate continuations and of a step over a cache in 8 bits from Python, without the cost of ctypes.
  *
  * These calls take a few microseconds on the GPU, less than what a Python function spends on
  * checking ten tensors and converting twenty arguments.  This module does the same in C: it
@@ -28,7 +28,7 @@ typedef int64_t i64;
 static struct {
   PyObject *empty, *error, *raw_stream, *current_device, *capturing, *ready, *empty_on;
   PyObject *results, *scratch; /* see take_result, take_scratch */
-  PyObject *i32, *i64, *f32, *bf16, *u8, *boolean;
+  PyObject *i32, *i64, *f32, *bf16, *u8, *e4m3, *boolean;
   PyObject *s_dtype, *s_shape, *s_data_ptr, *s_is_contiguous, *s_get_device, *s_stride, *s_cuda_stream,
       *s_view, *kw_empty;
   __typeof__(&paged_attention_tree) tree;
@@ -38,6 +38,10 @@ static struct {
   __typeof__(&pkv_beam_workspace) beam_ws;
   __typeof__(&pkv_fork_tables) fork_;
   __typeof__(&pkv_fork_workspace) fork_ws;
+  __typeof__(&pkv_rope_append) append;
+  __typeof__(&paged_attention_q8) q8;
+  __typeof__(&pkv_q8_workspace) q8_ws;
+  __typeof__(&pkv_sample) sample;
 } T;
 
 /* A tensor argument: its shape, and (after check) its pointer. */
@@ -284,8 +288,8 @@ static int fit(i64 a, i64 b, i64 c) {
   return a <= INT32_MAX && b <= INT32_MAX && c <= INT32_MAX ? 1 : refuse("a size does not fit 32 bits");
 }
 
-/* The descriptor of one cache [blocks, Hkv, 16, d], or of a model's, [layers, ...]. */
-static int caches(Arg* k, Arg* v, int models, pkv_cache_desc* desc, i64* layers, PyObject** dtype) {
+/* The descriptor of one cache [blocks, Hkv, 16, d], or of a model's, [layers, ...]; `eight`: one in 8 bits will do. */
+static int any_caches(Arg* k, Arg* v, int models, int eight, pkv_cache_desc* desc, i64* layers, PyObject** dtype) {
   int same = k->dim == v->dim;
   for (int i = 0; same && i < k->dim; ++i) same = k->n[i] == v->n[i];
   const int at = k->dim - 4;
@@ -293,16 +297,21 @@ static int caches(Arg* k, Arg* v, int models, pkv_cache_desc* desc, i64* layers,
     return refuse("k_cache and v_cache must both be [num_blocks, num_kv_heads, 16, head_dim]");
   const int f32 = is_dtype(k->t, T.f32), bf16 = f32 ? 0 : is_dtype(k->t, T.bf16);
   if (f32 < 0 || bf16 < 0) return 0;
-  if (!f32 && !bf16) return refuse("unsupported cache dtype");
-  *dtype = f32 ? T.f32 : T.bf16;
+  const int u8 = f32 || bf16 || !eight ? 0 : is_dtype(k->t, T.u8), e4m3 = f32 || bf16 || u8 || !eight ? 0 : is_dtype(k->t, T.e4m3);
+  if (u8 < 0 || e4m3 < 0) return 0;
+  if (!f32 && !bf16 && !u8 && !e4m3) return refuse("unsupported cache dtype");
+  *dtype = f32 ? T.f32 : bf16 ? T.bf16 : u8 ? T.u8 : T.e4m3;
   if (!fit(k->n[at + 1], k->n[at + 2], k->n[at + 3])) return 0;
   *layers = at == 1 ? k->n[0] : 1;
   desc->num_blocks = k->n[at];
   desc->num_kv_heads = (int32_t)k->n[at + 1];
   desc->block_size = (int32_t)k->n[at + 2];
   desc->head_dim = (int32_t)k->n[at + 3];
-  desc->dtype = f32 ? PKV_F32 : PKV_BF16;
+  desc->dtype = f32 ? PKV_F32 : bf16 ? PKV_BF16 : PKV_E4M3;
   return 1;
+}
+static int caches(Arg* k, Arg* v, int models, pkv_cache_desc* desc, i64* layers, PyObject** dtype) {
+  return any_caches(k, v, models, 0, desc, layers, dtype);
 }
 
 static int requests(const Arg* bt, const Arg* lens, const Arg* qsl) {
@@ -555,6 +564,220 @@ end:
   return res;
 }
 
+/* The strides of a tensor that is not contiguous (up to three). */
+static int strides(PyObject* t, i64* d) {
+  PyObject* st = PyObject_CallMethodNoArgs(t, T.s_stride);
+  if (!st) return 0;
+  d[0] = d[1] = d[2] = 0;
+  for (int i = 0; i < 3 && PyTuple_Check(st) && i < PyTuple_GET_SIZE(st); ++i) d[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(st, i));
+  Py_DECREF(st);
+  return !PyErr_Occurred();
+}
+
+static int on_device(const Arg* a, i64 dev) {
+  if (call_long(a->t, T.s_get_device) == dev) return 1;
+  if (!PyErr_Occurred())
+    PyErr_Format(PyExc_ValueError, "%s must be a tensor on the current CUDA device (cuda:%lld)", a->name, (long long)dev);
+  return 0;
+}
+
+/* The pointer of a [tokens, heads, d] tensor whose tokens may lie apart, and how far (elements). */
+static int token_rows(Arg* a, PyObject* dtype, i64 dev, i64* step) {
+  i64 s[3];
+  if (!on_device(a, dev)) return 0;
+  const int same = is_dtype(a->t, dtype);
+  if (same < 0) return 0;
+  if (!same) {
+    PyErr_Format(PyExc_ValueError, "%s must be %S", a->name, dtype);
+    return 0;
+  }
+  if (!strides(a->t, s)) return 0;
+  const i64 width = a->n[1] * a->n[2];
+  *step = a->n[0] > 1 ? s[0] : width;
+  if ((a->n[2] > 1 && s[2] != 1) || (a->n[1] > 1 && s[1] != a->n[2]) || *step < width) {
+    PyErr_Format(PyExc_ValueError, "%s must have tokens of contiguous heads", a->name);
+    return 0;
+  }
+  return pointer(a);
+}
+
+/* (k, v, cos_sin, k_cache, v_cache, block_tables, seq_lens, query_start_loc, max_query_len, q, scales, positions, interleaved,
+ *  q_out, stream) */
+static PyObject* py_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  Arg k, v, angles, kc, vc, bt, lens, qsl, q, scales, pos, o;
+  pkv_cache_desc desc;
+  PyObject *dt, *out = NULL, *res = NULL;
+  i64 layers, k_step, v_step, q_step = 0, o_step = 0;
+  Place at;
+  int32_t max_q;
+  int ok;
+  if (!want(n, 15)) return NULL;
+  if (!shape_of(&kc, a[3], "k_cache") || !shape_of(&vc, a[4], "v_cache") || !any_caches(&kc, &vc, 0, 1, &desc, &layers, &dt)) return NULL;
+  const int eight = desc.dtype == PKV_E4M3;
+  PyObject* rows = eight ? T.bf16 : dt;
+  if (!shape_of(&k, a[0], "k") || !shape_of(&v, a[1], "v")) return NULL;
+  if (k.dim != 3 || k.n[1] != desc.num_kv_heads || k.n[2] != desc.head_dim || v.dim != 3 || v.n[0] != k.n[0] || v.n[1] != k.n[1] ||
+      v.n[2] != k.n[2])
+    return refuse("k and v must both be [num_tokens, num_kv_heads, head_dim]"), NULL;
+  const int has_q = a[9] != Py_None, turns = a[2] != Py_None;
+  if (has_q) {
+    if (!shape_of(&q, a[9], "q")) return NULL;
+    if (q.dim != 3 || q.n[0] != k.n[0] || q.n[2] != k.n[2]) return refuse("q must be [num_tokens, num_q_heads, head_dim]"), NULL;
+    if (!fit(q.n[1], 0, 0)) return NULL;
+  }
+  if (a[13] != Py_None) {
+    if (!has_q) return refuse("q_out without q"), NULL;
+    if (!shape_of(&o, a[13], "q_out")) return NULL;
+    if (o.dim != 3 || o.n[0] != q.n[0] || o.n[1] != q.n[1] || o.n[2] != q.n[2]) return refuse("q_out must have the shape of q"), NULL;
+  }
+  if (turns) {
+    if (!shape_of(&angles, a[2], "cos_sin")) return NULL;
+    if (angles.dim != 2) return refuse("cos_sin must be [num_angles, rot_dim]"), NULL;
+    if (!fit(angles.n[1], 0, 0)) return NULL;
+  }
+  if (eight != (a[10] != Py_None)) return refuse("scales belong to a cache in 8 bits"), NULL;
+  if (eight) {
+    if (!shape_of(&scales, a[10], "scales")) return NULL;
+    if (scales.dim != 3 || scales.n[0] != desc.num_blocks || scales.n[1] != desc.num_kv_heads || scales.n[2] != 2)
+      return refuse("scales must be [num_blocks, num_kv_heads, 2]"), NULL;
+  }
+  if (a[11] != Py_None && (!shape_of(&pos, a[11], "positions") || !shaped(&pos, 1, k.n[0], 0))) return NULL;
+  if (!shape_of(&bt, a[5], "block_tables") || !shape_of(&lens, a[6], "seq_lens") || !shape_of(&qsl, a[7], "query_start_loc") ||
+      !requests(&bt, &lens, &qsl))
+    return NULL;
+  if (!fit(bt.n[1], lens.n[0], 0) || !as_int32(a[8], &max_q)) return NULL;
+  const int interleaved = PyObject_IsTrue(a[12]);
+  if (interleaved < 0 || !place(a[14], &at)) return NULL;
+  if (!token_rows(&k, rows, at.dev, &k_step) || !token_rows(&v, rows, at.dev, &v_step) || !check(&kc, dt, at.dev) || !check(&vc, dt, at.dev) ||
+      !check(&bt, T.i32, at.dev) || !check(&lens, T.i32, at.dev) || !check(&qsl, T.i32, at.dev))
+    return NULL;
+  if (has_q && !token_rows(&q, rows, at.dev, &q_step)) return NULL;
+  if (turns && !check(&angles, T.f32, at.dev)) return NULL;
+  if (eight && !check(&scales, T.f32, at.dev)) return NULL;
+  if (a[11] != Py_None && !check(&pos, T.i32, at.dev)) return NULL;
+  if (!has_q) {
+    out = Py_NewRef(Py_None);
+  } else if (a[13] == Py_None) {
+    out = result(&o, Py_None, "q_out", 3, q.n, rows, &at, &ok);
+    if (!ok) goto end;
+    o_step = q.n[1] * q.n[2];
+  } else {
+    out = Py_NewRef(a[13]);
+    if (!token_rows(&o, rows, at.dev, &o_step)) goto end;
+  }
+  const int st = T.append(has_q ? q.ptr : NULL, k.ptr, v.ptr, rows == T.f32 ? PKV_F32 : PKV_BF16, q_step, k_step, v_step,
+                          has_q ? (int32_t)q.n[1] : 0, turns ? angles.ptr : NULL, turns ? (int32_t)angles.n[1] : 0, interleaved,
+                          turns ? angles.n[0] : 0, a[11] != Py_None ? pos.ptr : NULL, kc.ptr, vc.ptr, eight ? scales.ptr : NULL, &desc,
+                          bt.ptr, (int32_t)bt.n[1], lens.ptr, qsl.ptr, (int32_t)lens.n[0], k.n[0], max_q, has_q ? o.ptr : NULL, o_step,
+                          at.stream);
+  res = st ? failed(st, "pkv_rope_append") : Py_NewRef(out);
+end:
+  Py_XDECREF(out);
+  return res;
+}
+
+/* (q, k_cache, v_cache, scales, block_tables, seq_lens, query_start_loc, scale, max_query_len, max_seq_len, out, workspace, stream) */
+static PyObject* py_q8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  Arg q, k, v, scales, bt, lens, qsl, o, w;
+  pkv_cache_desc desc;
+  PyObject *dt, *out = NULL, *ws = NULL, *res = NULL;
+  i64 layers, bytes = 0;
+  Place at;
+  int32_t max_q, max_len;
+  int ok;
+  if (!want(n, 13)) return NULL;
+  if (!shape_of(&k, a[1], "k_cache") || !shape_of(&v, a[2], "v_cache") || !any_caches(&k, &v, 0, 1, &desc, &layers, &dt)) return NULL;
+  if (desc.dtype != PKV_E4M3) return refuse("the cache must be in 8 bits (uint8 or float8_e4m3fn)"), NULL;
+  if (!shape_of(&q, a[0], "q")) return NULL;
+  if (q.dim != 3 || q.n[2] != desc.head_dim) return refuse("q must be [num_tokens, num_q_heads, head_dim]"), NULL;
+  if (!shape_of(&scales, a[3], "scales")) return NULL;
+  if (scales.dim != 3 || scales.n[0] != desc.num_blocks || scales.n[1] != desc.num_kv_heads || scales.n[2] != 2)
+    return refuse("scales must be [num_blocks, num_kv_heads, 2]"), NULL;
+  if (!shape_of(&bt, a[4], "block_tables") || !shape_of(&lens, a[5], "seq_lens") || !shape_of(&qsl, a[6], "query_start_loc") ||
+      !requests(&bt, &lens, &qsl))
+    return NULL;
+  if (a[10] != Py_None) {
+    if (!shape_of(&o, a[10], "out")) return NULL;
+    if (o.dim != 3 || o.n[0] != q.n[0] || o.n[1] != q.n[1] || o.n[2] != q.n[2]) return refuse("out must have the shape of q"), NULL;
+  }
+  if (!fit(q.n[1], bt.n[1], lens.n[0])) return NULL;
+  const double scale = PyFloat_AsDouble(a[7]);
+  if (scale == -1.0 && PyErr_Occurred()) return NULL;
+  if (!as_int32(a[8], &max_q) || !as_int32(a[9], &max_len)) return NULL;
+  if (!place(a[12], &at)) return NULL;
+  if (!check(&q, T.bf16, at.dev) || !check(&k, dt, at.dev) || !check(&v, dt, at.dev) || !check(&scales, T.f32, at.dev) ||
+      !check(&bt, T.i32, at.dev) || !check(&lens, T.i32, at.dev) || !check(&qsl, T.i32, at.dev))
+    return NULL;
+  out = result(&o, a[10], "out", 3, q.n, T.bf16, &at, &ok);
+  if (!ok) goto end;
+  if (q.n[0] == 0) {
+    res = Py_NewRef(out);
+    goto end;
+  }
+  if (a[11] == Py_None) {
+    const int st = T.q8_ws(&desc, (int32_t)q.n[1], max_q, &bytes);
+    if (st) {
+      failed(st, "paged_attention_q8");
+      goto end;
+    }
+  }
+  ws = scratch(&w, a[11], bytes, 3, &at, &ok);
+  if (!ok) goto end;
+  const int st = T.q8(q.ptr, k.ptr, v.ptr, scales.ptr, &desc, bt.ptr, (int32_t)bt.n[1], lens.ptr, qsl.ptr, (int32_t)lens.n[0],
+                      (int32_t)q.n[1], q.n[0], max_q, max_len, (float)scale, o.ptr, w.ptr, w.n[0], at.stream);
+  res = st ? failed(st, "paged_attention_q8") : Py_NewRef(out);
+end:
+  Py_XDECREF(out);
+  Py_XDECREF(ws);
+  return res;
+}
+
+/* (logits, uniform, temperature, top_k, top_p, min_p, out, stream) */
+static PyObject* py_sample(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  Arg x, s[5], r[2]; /* s: uniform, temperature, top_k, top_p, min_p */
+  static const char* const settings[5] = {"uniform", "temperature", "top_k", "top_p", "min_p"};
+  static const char* const names[2] = {"tokens", "logprobs"};
+  PyObject* const types[2] = {T.i32, T.f32};
+  PyObject *out[2] = {NULL, NULL}, *res = NULL;
+  Place at;
+  int ok;
+  if (!want(n, 8)) return NULL;
+  if (!shape_of(&x, a[0], "logits")) return NULL;
+  if (x.dim != 2) return refuse("logits must be [num_seqs, vocab]"), NULL;
+  const i64 N = x.n[0], V = x.n[1];
+  if (!fit(N, V, 0)) return NULL;
+  const int f32 = is_dtype(x.t, T.f32), bf16 = f32 ? 0 : is_dtype(x.t, T.bf16);
+  if (f32 < 0 || bf16 < 0) return NULL;
+  if (!f32 && !bf16) return refuse("logits must be float32 or bfloat16"), NULL;
+  i64 d[3];
+  if (!strides(x.t, d)) return NULL;
+  const i64 step = N > 1 ? d[0] : V;
+  if ((V > 1 && d[1] != 1) || (N > 1 && step < V)) return refuse("logits must have contiguous rows, evenly spaced"), NULL;
+  for (int i = 0; i < 5; ++i) {
+    s[i].ptr = NULL;
+    if ((i == 0 || a[i + 1] != Py_None) && (!shape_of(&s[i], a[i + 1], settings[i]) || !shaped(&s[i], 1, N, 0))) return NULL;
+  }
+  if (a[6] != Py_None) {
+    if (!PyTuple_Check(a[6]) || PyTuple_GET_SIZE(a[6]) != 2) return refuse("out must be (tokens, logprobs)"), NULL;
+    for (int i = 0; i < 2; ++i)
+      if (!shape_of(&r[i], PyTuple_GET_ITEM(a[6], i), names[i]) || !shaped(&r[i], 1, N, 0)) return NULL;
+  }
+  if (!place(a[7], &at)) return NULL;
+  if (!on_device(&x, at.dev) || !pointer(&x)) return NULL;
+  for (int i = 0; i < 5; ++i)
+    if ((i == 0 || a[i + 1] != Py_None) && !check(&s[i], i == 2 ? T.i32 : T.f32, at.dev)) return NULL;
+  for (int i = 0; i < 2; ++i) {
+    out[i] = result(&r[i], a[6] == Py_None ? Py_None : PyTuple_GET_ITEM(a[6], i), names[i], 1, &N, types[i], &at, &ok);
+    if (!ok) goto end;
+  }
+  const int st = T.sample(x.ptr, f32 ? PKV_F32 : PKV_BF16, step, s[1].ptr, s[2].ptr, s[3].ptr, s[4].ptr, s[0].ptr, (int32_t)N,
+                          (int32_t)V, r[0].ptr, r[1].ptr, at.stream);
+  res = st ? failed(st, "pkv_sample") : PyTuple_Pack(2, out[0], out[1]);
+end:
+  for (int i = 0; i < 2; ++i) Py_XDECREF(out[i]);
+  return res;
+}
+
 /* (path of libpkv, torch, PkvError, torch.cuda.current_device, a function from a device to its raw stream, one that tells
  * whether the current stream is captured, one that makes results: (number, shape, type, device) -> list, one that makes a
  * tensor for a named stream: (shape, type, device, stream, shared)) */
@@ -580,6 +803,10 @@ static PyObject* py_setup(PyObject* self, PyObject* args) {
   SYMBOL(beam_ws, pkv_beam_workspace)
   SYMBOL(fork_, pkv_fork_tables)
   SYMBOL(fork_ws, pkv_fork_workspace)
+  SYMBOL(append, pkv_rope_append)
+  SYMBOL(q8, paged_attention_q8)
+  SYMBOL(q8_ws, pkv_q8_workspace)
+  SYMBOL(sample, pkv_sample)
 #undef SYMBOL
   Py_INCREF(T.error);
   Py_INCREF(T.current_device);
@@ -591,6 +818,7 @@ static PyObject* py_setup(PyObject* self, PyObject* args) {
   if (!(T.empty = PyObject_GetAttrString(torch, "empty")) || !(T.i32 = PyObject_GetAttrString(torch, "int32")) ||
       !(T.i64 = PyObject_GetAttrString(torch, "int64")) || !(T.f32 = PyObject_GetAttrString(torch, "float32")) ||
       !(T.bf16 = PyObject_GetAttrString(torch, "bfloat16")) || !(T.u8 = PyObject_GetAttrString(torch, "uint8")) ||
+      !(T.e4m3 = PyObject_GetAttrString(torch, "float8_e4m3fn")) ||
       !(T.boolean = PyObject_GetAttrString(torch, "bool")))
     return NULL;
   T.s_dtype = PyUnicode_InternFromString("dtype");
@@ -619,6 +847,9 @@ static PyMethodDef methods[] = {{"setup", py_setup, METH_VARARGS, NULL},
                                 {"compact", (PyCFunction)(void*)py_compact, METH_FASTCALL, NULL},
                                 {"beam", (PyCFunction)(void*)py_beam, METH_FASTCALL, NULL},
                                 {"fork", (PyCFunction)(void*)py_fork, METH_FASTCALL, NULL},
+                                {"append", (PyCFunction)(void*)py_append, METH_FASTCALL, NULL},
+                                {"q8", (PyCFunction)(void*)py_q8, METH_FASTCALL, NULL},
+                                {"sample", (PyCFunction)(void*)py_sample, METH_FASTCALL, NULL},
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", NULL, -1, methods, NULL, NULL, NULL, NULL};
 PyMODINIT_FUNC PyInit__native(void) { return PyModule_Create(&module); }

@@ -20,6 +20,7 @@ struct UmmaProbe {
 
 constexpr int kProbeSmem = 64 * 1024 * 2 + 2048;
 
+template <bool k8Bit>
 __global__ void __launch_bounds__(128) umma_probe_kernel(UmmaProbe P, const uint4* __restrict__ a_img,
                                                          const uint4* __restrict__ b_img, float* __restrict__ d,
                                                          uint32_t* err) {
@@ -66,7 +67,8 @@ __global__ void __launch_bounds__(128) umma_probe_kernel(UmmaProbe P, const uint
   __syncthreads();
   tc_fence_after();
   if (threadIdx.x == 0) {
-    const uint32_t idesc = umma_idesc_bf16(P.M, P.N, P.a_mn != 0, P.b_mn != 0);
+    const uint32_t idesc = k8Bit ? umma_idesc_e4m3(P.M, P.N, P.a_mn != 0, P.b_mn != 0)
+                                 : umma_idesc_bf16(P.M, P.N, P.a_mn != 0, P.b_mn != 0);
     const uint64_t b0 = umma_smem_desc(smem_u32(b_s), P.b_lbo, P.b_sbo, P.b_layout);
     if (a_tm) {
       for (int k = 0; k < P.k_steps; ++k)
@@ -74,8 +76,11 @@ __global__ void __launch_bounds__(128) umma_probe_kernel(UmmaProbe P, const uint
                     k > 0);
     } else {
       const uint64_t a0 = umma_smem_desc(smem_u32(a_s), P.a_lbo, P.a_sbo, P.a_layout);
-      for (int k = 0; k < P.k_steps; ++k)
-        umma_f16_ss(tmem, umma_desc_advance(a0, P.a_off[k]), umma_desc_advance(b0, P.b_off[k]), idesc, k > 0);
+      for (int k = 0; k < P.k_steps; ++k) {
+        const uint64_t a = umma_desc_advance(a0, P.a_off[k]), b = umma_desc_advance(b0, P.b_off[k]);
+        if (k8Bit) umma_f8_ss(tmem, a, b, idesc, k > 0);
+        else umma_f16_ss(tmem, a, b, idesc, k > 0);
+      }
     }
     umma_commit(&bar);
   }
@@ -142,14 +147,15 @@ int run_wait_selftest(uint32_t* err, cudaStream_t s) {
   return cuda_status(cudaGetLastError());
 }
 
-int run_umma_selftest(const int32_t* params, const void* a_img, const void* b_img, float* d_out, uint32_t* err,
-                      cudaStream_t s) {
+int run_umma_selftest(const int32_t* params, const void* a_img, const void* b_img, float* d_out, bool eight_bit,
+                      uint32_t* err, cudaStream_t s) {
   UmmaProbe P;
   static_assert(sizeof(UmmaProbe) == 29 * sizeof(int32_t), "probe params");
   std::memcpy(&P, params, sizeof P);
   if (!(P.M == 128) || P.N < 16 || P.N > 256 || P.N % 16 != 0) return PKV_ERR_INVALID_ARG;
   if (P.a_bytes <= 0 || P.a_bytes > 65536 || P.b_bytes <= 0 || P.b_bytes > 65536) return PKV_ERR_INVALID_ARG;
   if (P.a_bytes % 16 || P.b_bytes % 16 || P.k_steps < 1 || P.k_steps > 8) return PKV_ERR_INVALID_ARG;
+  if (eight_bit && P.a_layout < 0) return PKV_ERR_UNSUPPORTED;
   if (P.a_layout < 0) {  // A from TMEM: 128 rows of acols columns, each k step 8 columns in
     const int acols = P.a_bytes / (128 * 4);
     if (P.a_bytes != acols * 128 * 4 || acols % 16 || P.N + acols > 512 || P.a_mn) return PKV_ERR_INVALID_ARG;
@@ -160,10 +166,10 @@ int run_umma_selftest(const int32_t* params, const void* a_img, const void* b_im
     if ((P.a_layout >= 0 && (P.a_off[k] < 0 || P.a_off[k] >= P.a_bytes || P.a_off[k] % 16)) || P.b_off[k] < 0 ||
         P.b_off[k] >= P.b_bytes || P.b_off[k] % 16)
       return PKV_ERR_INVALID_ARG;
-  cudaError_t e = cudaFuncSetAttribute(umma_probe_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProbeSmem);
+  auto* kernel = eight_bit ? umma_probe_kernel<true> : umma_probe_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProbeSmem);
   if (e != cudaSuccess) return cuda_status(e);
-  umma_probe_kernel<<<1, 128, kProbeSmem, s>>>(P, static_cast<const uint4*>(a_img),
-                                               static_cast<const uint4*>(b_img), d_out, err);
+  kernel<<<1, 128, kProbeSmem, s>>>(P, static_cast<const uint4*>(a_img), static_cast<const uint4*>(b_img), d_out, err);
   return cuda_status(cudaGetLastError());
 }
 

@@ -18,6 +18,7 @@ enum : uint32_t {
   kErrLength = 1u << 2,    // seq_len < q_len, or more blocks than a table row holds
   kErrTimeout = 1u << 3,   // a bounded wait gave up
   kErrNoPages = 1u << 4,   // a fork found too few free blocks
+  kErrSetting = 1u << 5,   // a sampling setting outside of its range
 };
 
 constexpr int kTileKeys = 128;       // keys per tensor-core tile (8 blocks)
@@ -359,8 +360,44 @@ struct BeamArgs {
 size_t beam_workspace(int32_t num_seqs, int32_t beams, int32_t vocab, int32_t select, int num_sms);
 int launch_beam_select(const BeamArgs& a, void* workspace, int num_sms, cudaStream_t s);
 
-int run_umma_selftest(const int32_t* params, const void* a_img, const void* b_img, float* d_out, uint32_t* err,
-                      cudaStream_t s);
+// A step over a cache in 8 bits: appending with rotation (k_append.cu), attention (k_q8.cu), sampling (k_sample.cu).
+struct AppendArgs {
+  const void *q, *k, *v;  // q may be null
+  int64_t q_stride, k_stride, v_stride, out_stride;
+  int32_t num_q_heads;
+  const float* cos_sin;
+  int32_t rot_dim, interleaved;
+  int64_t num_angles;
+  const int32_t* positions;
+  void *k_cache, *v_cache;
+  float* scales;
+  pkv_cache_desc cache;
+  const int32_t* block_tables;
+  int32_t max_blocks;
+  const int32_t* seq_lens;
+  const int32_t* qsl;
+  int32_t num_seqs;
+  int64_t num_tokens;
+  int32_t max_query_len;
+  void* q_out;
+};
+int launch_append(const AppendArgs& a, uint32_t* err, cudaStream_t s);
+size_t q8_workspace(const pkv_cache_desc& c, int32_t num_q_heads, int32_t max_query_len, int num_sms);
+int launch_q8(const AttnArgs& a, const float* scales, void* workspace, int num_sms, uint32_t* err, cudaStream_t s);
+struct SampleArgs {
+  const void* logits;
+  int32_t dtype;
+  int64_t row_stride;
+  const float *temperature, *top_p, *min_p, *uniform;
+  const int32_t* top_k;
+  int32_t num_seqs, vocab;
+  int32_t* tokens;
+  float* logprobs;
+};
+int launch_sample(const SampleArgs& a, int num_sms, uint32_t* err, cudaStream_t s);
+
+int run_umma_selftest(const int32_t* params, const void* a_img, const void* b_img, float* d_out, bool eight_bit,
+                      uint32_t* err, cudaStream_t s);
 int run_tma_selftest(const void* src, int64_t rows, int32_t row0, void* dump, uint32_t* err, cudaStream_t s);
 int run_wait_selftest(uint32_t* err, cudaStream_t s);
 
