@@ -8,19 +8,22 @@
 // of w (weight.cuh), and sums of them exact, in any order.
 //
 // Work.  A row belongs to a cluster of CTAs, which go through it three times (twice from L2):
-//   1. its largest logit;
-//   2. how many candidates fall into each of 4096 bins of (max - x) / T, 1/128 of a power of two wide.  That bounds
-//      every mass to 0.6 %, and so tells for each border (the end of top-k and min-p, of top-p, the token) a few
-//      bins in which it must lie;
+//   1. its largest and its least logit;
+//   2. how many candidates fall into each of 2048 bins of (max - x) / T, 1/64 of a power of two wide or less, and the sum
+//      of their places within it.  That tells every mass to 1e-4 (the weight of the mean place, from below, is off by an
+//      eighth of the square of a bin's width), and so, for each border (the end of top-k and min-p, of top-p,
+//      the token), the one or two bins in which it must lie;
 //   3. the candidates of those bins are collected in the cluster's first CTA, and the others' exact weights summed
 //      up between them.
-// The first CTA sorts what was collected (hundreds, as a rule) and finds the borders exactly.  With top-k or min-p
+// The first CTA sorts what was collected (hundreds at most, as a rule) and finds the borders exactly.  With top-k or min-p
 // nothing behind their end is looked at closely, so that no weight but the collected ones' is ever computed.
-// Where more than 8192 candidates lie in the borders' bins (rows of equal logits), borders are found by bisection
+// Weights below 2^-20 of the largest need not be right to 2^-40 of themselves: they are rounded to fp32 first.  The larger
+// ones, few in most rows, wait in a queue of each thread's, so that a warp computes as many as it has lanes at a time.
+// Where more than 2048 candidates lie in the borders' bins (rows of equal logits), borders are found by bisection
 // of the keys instead, a pass over the row each.
 //
-// Bound: latency.  Three passes and five cluster barriers for one row; for many rows the exact weights of rows
-// without top-k or min-p (about 40 instructions a logit).
+// Bound: latency: three passes, three cluster barriers, and code that runs once, so that it has to be fetched (loops,
+// not unrolled copies).
 #include <cooperative_groups.h>
 
 #include "pkv_internal.cuh"
@@ -32,9 +35,11 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 4096, kPerThread = kBins / kThreads;
-constexpr float kBinsPerUnit = 128.f;
-constexpr int kCollect = 8192;
+constexpr int kBins = 2048, kPerThread = kBins / kThreads;
+constexpr float kBinsPerUnit = 64.f;
+constexpr float kTailUnits = 20.f;  // weights below 2^-20 of the largest are rounded to fp32
+constexpr int kCollect = 2048;
+constexpr int kQueue = 16;  // places of a thread's queue, eight of which a piece may fill
 constexpr int kGather = 255, kIgnore = 254;  // of a bin: its candidates are collected; lie behind everything
 
 struct Params {
@@ -48,34 +53,35 @@ struct Params {
   int32_t vocab, shift;
 };
 
-// What the first CTA finds out about the bins: up to three disjoint intervals of bins that are collected.
+// What the counts tell: up to three disjoint intervals of bins that are collected.
 struct Plan {
-  int32_t count;         // intervals
+  int32_t count;             // intervals
   int32_t begin[3], end[3];  // bins [begin, end]
-  int32_t last;          // bins behind it are ignored
-  int32_t rank[3];       // candidate number e of the list, in interval j, is number rank[j] + e of the row
+  int32_t last;              // bins behind it are ignored
+  int32_t rank[3];           // candidate number e of the list, in interval j, is number rank[j] + e of the row
 };
 
 struct Shared {
+  uint32_t bins[kBins], places[kBins];  // of this CTA: candidates, and their places in the bin in 1/2048
+  uint32_t all[kBins];                  // of the row: candidates, and the mean of their places
+  float mean[kBins];
+  uint64_t list[kCollect], weights[kCollect];  // (first CTA) keys, sorted
   union {
-    struct {
-      uint32_t bins[kBins];   // of this CTA
-      uint32_t total[kBins];  // of the row (first CTA)
-    };
-    uint64_t list[kCollect];  // keys (first CTA)
+    float queue[kQueue][kThreads];
+    uint64_t unsorted[kCollect];  // (first CTA, after the queues)
   };
   uint8_t kind[kBins];  // of a bin: kGather, kIgnore, or how many intervals come before it
   uint64_t table[256];
-  unsigned long long best[16], finite[16];  // of each CTA: its least key; its candidates
+  float largest[16], least[16];  // of each CTA's candidates
   unsigned long long segment[4];            // masses of what is not collected, between the intervals (first CTA)
-  unsigned long long warp_u64[kWarps + 1];
-  float warp_lo[kWarps], warp_hi[kWarps];
+  unsigned long long warp_u64[kWarps];
+  float warp_mass[kWarps], warp_low[kWarps];
   uint32_t warp_n[kWarps];
   int32_t found[8];
-  float bound[4];
-  uint32_t collected;  // (first CTA)
-  Plan plan;           // (first CTA)
-  unsigned long long sum[2], least, most;  // of a pass of the bisection
+  float bound[2];
+  uint32_t collected, best;  // (first CTA) of the list; the first of the largest logits
+  Plan plan;
+  unsigned long long sum[2], low, high;  // of a pass of the bisection
 };
 
 // Larger logits have smaller keys; the index in the lower half.
@@ -90,49 +96,46 @@ __device__ __forceinline__ float logit_of(uint64_t key) {
 }
 __device__ __forceinline__ bool candidate(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
-// Calls f(x, i) for this thread's logits of the row (those of 16-byte pieces `first`, first + step, ...), of which
-// several pieces are on their way at once.
-template <typename T, typename F>
-__device__ __forceinline__ void each(const Params& P, int64_t row, int first, int step, F&& f) {
-  constexpr int kVec = 16 / sizeof(T), kAtOnce = 4;
+// A piece of 16 bytes of a row; what does not belong to the row is NaN, no candidate.
+template <typename T>
+__device__ __forceinline__ uint4 load_piece(const T* p, int i0, int vocab) {
+  constexpr int kVec = 16 / sizeof(T);
+  if (i0 >= 0 && i0 + kVec <= vocab) return __ldg(reinterpret_cast<const uint4*>(p + i0));
+  uint32_t w[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) {
+    if (i0 + e < 0 || i0 + e >= vocab) continue;
+    const uint32_t x = __float_as_uint(Elem<T>::to_f32(p[i0 + e]));
+    if constexpr (sizeof(T) == 4) w[e] = x;
+    else w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | x : (w[e / 2] & 0xffff0000u) | x >> 16;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Calls f(x, i) for this thread's logits of the row (those of the 16-byte pieces `first`, first + step, ...), and
+// piece_done() after each piece, which all threads of a warp call equally often.  Three pieces are on their way while one
+// is worked on.
+template <typename T, typename F, typename Done>
+__device__ __forceinline__ void each(const Params& P, int64_t row, int first, int step, F&& f, Done&& piece_done) {
+  constexpr int kVec = 16 / sizeof(T);
   const T* p = static_cast<const T*>(P.logits) + row * P.stride;
   const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));  // piece 0 begins so much before
-  const int pieces = (skew + P.vocab + kVec - 1) / kVec;
-  const uint4* base = reinterpret_cast<const uint4*>(p - skew);
+  const int at_warp = first - static_cast<int>(threadIdx.x & 31);
+  const int end = skew + P.vocab;
+  int i0 = first * kVec - skew;
+  const int hop = step * kVec;
+  uint4 a = load_piece<T>(p, i0, P.vocab), b = load_piece<T>(p, i0 + hop, P.vocab), c = load_piece<T>(p, i0 + 2 * hop, P.vocab);
 #pragma unroll 1
-  for (int v0 = first; v0 < pieces; v0 += kAtOnce * step) {
-    uint4 raw[kAtOnce];
+  for (int v = at_warp; v * kVec < end; v += step, i0 += hop) {
+    const uint4 d = load_piece<T>(p, i0 + 3 * hop, P.vocab);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) {
-      const int v = v0 + k * step, i0 = v * kVec - skew;
-      raw[k] = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);  // NaN: no candidates
-      if (v >= pieces) continue;
-      if (i0 >= 0 && i0 + kVec <= P.vocab) {
-        raw[k] = __ldg(base + v);
-      } else {  // a piece that the row has a part of
-        uint32_t* w = reinterpret_cast<uint32_t*>(&raw[k]);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          if (i0 + e < 0 || i0 + e >= P.vocab) continue;
-          if constexpr (sizeof(T) == 4) {
-            w[e] = __float_as_uint(Elem<T>::to_f32(p[i0 + e]));
-          } else {
-            const uint32_t h = __float_as_uint(Elem<T>::to_f32(p[i0 + e])) >> 16;
-            w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | h << 16 : (w[e / 2] & 0xffff0000u) | h;
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) {
-      const int i0 = (v0 + k * step) * kVec - skew;
-      const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        const float x = __uint_as_float(sizeof(T) == 4 ? w[e % 4] : e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
-        f(x, i0 + e);
-      }
-    }
+    for (int e = 0; e < kVec; ++e)
+      f(__uint_as_float(sizeof(T) == 4 ? w[e % 4] : e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16), i0 + e);
+    piece_done();
+    a = b;
+    b = c;
+    c = d;
   }
 }
 
@@ -194,78 +197,77 @@ struct Row {
   int32_t top_k;
 };
 
-// The borders' bins, from the counts (the first CTA; candidates: all of the row).
-__device__ __forceinline__ void make_plan(Shared& s, const Row& r, uint32_t candidates) {
+// The borders' bins, from the row's counts (every CTA makes the same plan).  The last bin's candidates are not
+// counted: there are `rest` of their weights, 2^-32 each, at most.
+__device__ __forceinline__ void make_plan(Shared& s, const Row& r, float per_unit, float rest) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b0 = threadIdx.x * kPerThread;
-  // this thread's bins: candidates up to each, and bounds of their mass
-  uint32_t n[kPerThread];
-  float lo[kPerThread], hi[kPerThread];
-  uint32_t cn = 0;
-  float cl = 0.f, ch = 0.f;
+  static_assert(kPerThread == 4, "a thread's bins are a vector");
+  const uint4 x = *reinterpret_cast<const uint4*>(s.all + b0);
+  const float4 y = *reinterpret_cast<const float4*>(s.mean + b0);
+  uint32_t n[4] = {x.x, x.y, x.z, x.w};
+  const float mean[4] = {y.x, y.y, y.z, y.w};
+  // candidates of these bins and up to each, and the mass up to each
+  const uint32_t here[4] = {n[0], n[1], n[2], n[3]};
+  float mass[4];
+  uint32_t counted = 0;
+  float weighed = 0.f;
 #pragma unroll
-  for (int k = 0; k < kPerThread; ++k) {
-    const int b = b0 + k;
-    const uint32_t here = s.total[b];
-    // (a bin number is off by up to 2^-10, and the sums of bounds by 2^-13)
-    const float top = exp2f(static_cast<float>(-b) * (1.f / kBinsPerUnit));
-    cn += here;
-    ch += here * (top * (1.f + 1.f / 4096.f));
-    cl += b == kBins - 1 ? 0.f : here * (top * (0.99459944f * (1.f - 1.f / 4096.f)));  // 2^(-1/128)
-    n[k] = cn;
-    lo[k] = cl;
-    hi[k] = ch;
+  for (int k = 0; k < 4; ++k) {
+    weighed += here[k] * exp2f(-(static_cast<float>(b0 + k) + mean[k]) / per_unit);
+    counted += here[k];
+    n[k] = counted;
+    mass[k] = weighed;
   }
-  uint32_t in = cn;
-  float il = cl, ih = ch;
-#pragma unroll
+  uint32_t in = counted;
+  float im = weighed;
+#pragma unroll 1
   for (int d = 1; d < 32; d <<= 1) {
     const uint32_t y = __shfl_up_sync(0xffffffffu, in, d);
-    const float yl = __shfl_up_sync(0xffffffffu, il, d), yh = __shfl_up_sync(0xffffffffu, ih, d);
+    const float z = __shfl_up_sync(0xffffffffu, im, d);
     if (lane >= d) {
       in += y;
-      il += yl;
-      ih += yh;
+      im += z;
     }
   }
   if (lane == 31) {
     s.warp_n[warp] = in;
-    s.warp_lo[warp] = il;
-    s.warp_hi[warp] = ih;
+    s.warp_mass[warp] = im;
   }
   if (threadIdx.x < 8) s.found[threadIdx.x] = kBins - 1;
   __syncthreads();
-  uint32_t bn = in - cn;
-  float bl = il - cl, bh = ih - ch, all_lo = 0.f, all_hi = 0.f;
-#pragma unroll
+  uint32_t bn = in - counted;
+  float bm = im - weighed, all = 0.f;
+#pragma unroll 1
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) {
       bn += s.warp_n[w];
-      bl += s.warp_lo[w];
-      bh += s.warp_hi[w];
+      bm += s.warp_mass[w];
     }
-    all_lo += s.warp_lo[w];
-    all_hi += s.warp_hi[w];
+    all += s.warp_mass[w];
   }
 #pragma unroll
-  for (int k = 0; k < kPerThread; ++k) {
+  for (int k = 0; k < 4; ++k) {
     n[k] += bn;
-    // (the differences above may round to below what was; the margins cover it)
-    lo[k] += bl;
-    hi[k] += bh;
+    mass[k] += bm;
   }
-  // The first bin up to which more than `x` lies, by counts (0), by the lower (1) or the upper bounds (2): found[at].
-  const auto search = [&](int at, int what, float x, uint32_t count) {
-#pragma unroll
-    for (int k = kPerThread - 1; k >= 0; --k)
-      if (what == 0 ? n[k] >= count : (what == 1 ? lo[k] : hi[k]) > x) atomicMin(&s.found[at], b0 + k);
+  // the masses above are off by a part of 1e-4 at most, and by what lies behind the last bin
+  constexpr float kLow = 0.9999f, kHigh = 1.0001f;
+  const auto first_over = [&](int at, float x) {  // the first bin up to which more than x lies, by these masses
+    const int k = mass[0] > x ? 0 : mass[1] > x ? 1 : mass[2] > x ? 2 : 3;
+    const int mine = __reduce_min_sync(0xffffffffu, mass[3] > x ? b0 + k : kBins - 1);
+    if (lane == 0 && mine < kBins - 1) atomicMin(&s.found[at], mine);
   };
-  const bool cut_k = r.top_k > 0 && static_cast<uint32_t>(r.top_k) < candidates, cut_m = r.min_p > 0.f;
-  if (cut_k) search(0, 0, 0.f, static_cast<uint32_t>(r.top_k));
+  const bool cut_k = r.top_k > 0, cut_m = r.min_p > 0.f;  // (a top-k of all and more ends in the last bin)
+  if (cut_k) {
+    const uint32_t k = static_cast<uint32_t>(r.top_k);
+    const int at = n[0] >= k ? 0 : n[1] >= k ? 1 : n[2] >= k ? 2 : 3;
+    if (bn < k && n[3] >= k) s.found[0] = b0 + at;
+  }
   __syncthreads();
   int a1 = kBins, e1 = kBins - 1;  // the end of top-k and min-p
   if (cut_k) a1 = e1 = s.found[0];
   if (cut_m) {
-    const int at = static_cast<int>(fminf(-log2f(r.min_p) * kBinsPerUnit, kBins - 1.f));
+    const int at = static_cast<int>(fminf(-log2f(r.min_p) * per_unit, kBins - 1.f));
     a1 = min(a1, max(at - 1, 0));
     e1 = min(e1, min(at + 1, kBins - 1));
   }
@@ -273,91 +275,112 @@ __device__ __forceinline__ void make_plan(Shared& s, const Row& r, uint32_t cand
   // the mass up to there: bounds
   if (cut1) {
 #pragma unroll
-    for (int k = 0; k < kPerThread; ++k) {
-      if (b0 + k == a1 - 1) s.bound[0] = lo[k];
-      if (b0 + k == e1) s.bound[1] = hi[k];
+    for (int k = 0; k < 4; ++k) {
+      if (b0 + k == a1 - 1) s.bound[0] = mass[k];
+      if (b0 + k == e1) s.bound[1] = mass[k];
     }
     if (threadIdx.x == 0 && a1 == 0) s.bound[0] = 0.f;
     __syncthreads();
   }
-  float z_lo = cut1 ? s.bound[0] : all_lo, z_hi = cut1 ? s.bound[1] : all_hi;
-  z_lo *= 0.9999f;
-  z_hi *= 1.0001f;
+  float z_lo = (cut1 ? s.bound[0] : all) * kLow, z_hi = (cut1 ? s.bound[1] : all) * kHigh + rest;
   // the end of top-p
   int a2 = kBins, e2 = e1;
   const bool cut_p = r.top_p < 1.f;
   if (cut_p) {
-    search(1, 2, r.top_p * z_lo * 0.9999f, 0);
-    search(2, 1, r.top_p * z_hi * 1.0001f, 0);
+    first_over(1, r.top_p * z_lo * kLow - rest);
+    first_over(2, r.top_p * z_hi * kHigh);
     __syncthreads();
     a2 = min(s.found[1], e1);
     e2 = min(s.found[2], e1);
     z_lo *= r.top_p;
-    z_hi = fminf(z_hi, r.top_p * z_hi + 1.001f * exp2f(static_cast<float>(-a2) * (1.f / kBinsPerUnit)));
+    z_hi = fminf(z_hi, r.top_p * z_hi + kHigh * exp2f(-static_cast<float>(a2) / per_unit));
   }
-  search(3, 2, r.u * z_lo * 0.9999f, 0);
-  search(4, 1, r.u * z_hi * 1.0001f, 0);
+  first_over(3, r.u * z_lo * kLow - rest);
+  first_over(4, r.u * z_hi * kHigh);
   __syncthreads();
   if (threadIdx.x == 0) {
-    int begin[3] = {}, end[3] = {}, m = 0;
-    const auto add = [&](int a, int e) {  // (in order of their beginnings)
-      if (m > 0 && a <= end[m - 1] + 1) {
-        end[m - 1] = max(end[m - 1], e);
-        return;
-      }
-      begin[m] = a;
-      end[m++] = e;
-    };
     const int a3 = min(s.found[3], e2), e3 = min(s.found[4], e2);
-    // the token comes before the end of top-p, and that before the end of the others; their windows may overlap
-    int a[3] = {a3, a2, a1}, e[3] = {e3, e2, e1};
-    bool on[3] = {true, cut_p, cut1};
-    for (int i = 0; i < 3; ++i)
-      for (int k = i + 1; k < 3; ++k)
-        if (on[k] && (!on[i] || a[k] < a[i])) {
-          const int x = a[i], y = e[i];
-          const bool z = on[i];
-          a[i] = a[k], e[i] = e[k], on[i] = on[k];
-          a[k] = x, e[k] = y, on[k] = z;
-        }
-    for (int i = 0; i < 3; ++i)
-      if (on[i]) add(a[i], max(a[i], e[i]));
-    s.plan.count = m;
+    // three windows in order of their beginnings, joined where they meet
+    int a[3] = {a3, cut_p ? a2 : kBins, cut1 ? a1 : kBins}, e[3] = {max(a3, e3), max(a2, e2), max(a1, e1)};
+#pragma unroll
     for (int i = 0; i < 3; ++i) {
-      s.plan.begin[i] = i < m ? begin[i] : kBins;
-      s.plan.end[i] = i < m ? end[i] : kBins;
+      const int x = i == 1 ? 1 : 0;  // places 0 and 1, 1 and 2, 0 and 1
+      if (a[x + 1] < a[x]) {
+        const int y = a[x], z = e[x];
+        a[x] = a[x + 1], e[x] = e[x + 1];
+        a[x + 1] = y, e[x + 1] = z;
+      }
     }
+    int m = 0;
+#pragma unroll 1
+    for (int i = 0; i < 3; ++i) {
+      const int from = i == 0 ? a[0] : i == 1 ? a[1] : a[2], to = i == 0 ? e[0] : i == 1 ? e[1] : e[2];
+      if (from >= kBins) continue;
+      if (m > 0 && from <= s.plan.end[m - 1] + 1) {
+        s.plan.end[m - 1] = max(s.plan.end[m - 1], to);
+      } else {
+        s.plan.begin[m] = from;
+        s.plan.end[m++] = to;
+      }
+    }
+    s.plan.count = m;
+#pragma unroll 1
+    for (int i = m; i < 3; ++i) s.plan.begin[i] = s.plan.end[i] = kBins;
     s.plan.last = cut1 ? e1 : kBins - 1;
   }
   __syncthreads();
-  // candidates before an interval that are not collected
+  const Plan p = s.plan;
+  // candidates before an interval that are not collected; the bins' kinds
+  uint32_t kinds = 0;
 #pragma unroll
-  for (int k = 0; k < kPerThread; ++k)
+  for (int k = 0; k < 4; ++k) {
+    const int b = b0 + k;
+    uint32_t kind = 0;
+    bool in_one = false;
+#pragma unroll
     for (int j = 0; j < 3; ++j) {
-      if (s.plan.begin[j] == b0 + k) s.plan.rank[j] = static_cast<int32_t>(n[k] - s.total[b0 + k]);
-      if (s.plan.end[j] == b0 + k) s.found[5 + j] = static_cast<int32_t>(n[k]);
+      if (p.begin[j] == b) s.found[j] = static_cast<int32_t>(n[k] - here[k]);
+      if (p.end[j] == b) s.found[5 + j] = static_cast<int32_t>(n[k]);
+      in_one |= b >= p.begin[j] && b <= p.end[j];
+      kind += b > p.end[j];
     }
+    kinds |= (in_one ? kGather : b > p.last ? kIgnore : kind) << (8 * k);
+  }
+  reinterpret_cast<uint32_t*>(s.kind)[threadIdx.x] = kinds;
   __syncthreads();
   if (threadIdx.x == 0) {
     int collected = 0;
-    for (int j = 0; j < s.plan.count; ++j) {
-      const int before = s.plan.rank[j];
-      s.plan.rank[j] -= collected;
-      collected += s.found[5 + j] - before;
+#pragma unroll 1
+    for (int j = 0; j < p.count; ++j) {
+      s.plan.rank[j] = s.found[j] - collected;
+      collected += s.found[5 + j] - s.found[j];
     }
-    s.collected = 0;
-    for (int k = 0; k < 4; ++k) s.segment[k] = 0;
   }
+  __syncthreads();
 }
 
-// Sorts list[0, n) (the first CTA), n up to kCollect: bitonic, the part behind n filled up with the largest key.
+// Sorts the n keys of `unsorted` into `list` (the first CTA).
 __device__ __forceinline__ void sort_list(Shared& s, int n) {
-  int size = 64;
+  if (n <= kThreads) {  // each key's place is the number of smaller ones
+    if (static_cast<int>(threadIdx.x) < n) {
+      const uint64_t mine = s.unsorted[threadIdx.x];
+      int place = 0;
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) place += s.unsorted[i] < mine;
+      s.list[place] = mine;
+    }
+    __syncthreads();
+    return;
+  }
+  int size = kThreads;
   while (size < n) size <<= 1;
-  for (int i = n + threadIdx.x; i < size; i += kThreads) s.list[i] = ~uint64_t(0);
+  for (int i = threadIdx.x; i < size; i += kThreads) s.list[i] = i < n ? s.unsorted[i] : ~uint64_t(0);
   __syncthreads();
+#pragma unroll 1
   for (int k = 2; k <= size; k <<= 1) {
+#pragma unroll 1
     for (int j = k >> 1; j > 0; j >>= 1) {
+#pragma unroll 1
       for (int i = threadIdx.x; i < size / 2; i += kThreads) {
         const int a = 2 * i - (i & (j - 1)), b = a + j;  // bit j of a is 0
         const uint64_t x = s.list[a], y = s.list[b];
@@ -375,62 +398,63 @@ __device__ __forceinline__ void sort_list(Shared& s, int n) {
 }
 
 // The token out of the collected candidates (the first CTA).
-__device__ __forceinline__ void finish(const Params& P, Shared& s, const Row& r, const Weight& w, float per_bin, int64_t row,
-                                       uint32_t candidates) {
+__device__ __forceinline__ void finish(const Params& P, Shared& s, const Row& r, const Weight& w, float per_place, int64_t row) {
   const int n = static_cast<int>(s.collected);
   sort_list(s, n);
+  const Plan p = s.plan;
   const uint64_t least_w = r.min_p > 0.f ? w.part_up(r.min_p) : 0;
   const uint32_t most = r.top_k > 0 ? static_cast<uint32_t>(r.top_k) : 0xffffffffu;
   const int per = (n + kThreads - 1) / kThreads, e0 = threadIdx.x * per, e1 = min(e0 + per, n);
-  const uint64_t seg[4] = {s.segment[0], s.segment[1], s.segment[2], s.segment[3]};
+  // the mass before the intervals, of what is not collected
+  const uint64_t seg0 = s.segment[0], seg1 = seg0 + s.segment[1], seg2 = seg1 + s.segment[2], segs = seg2 + s.segment[3];
   // a candidate's interval, from its bin
-  const auto interval = [&](float x) {
-    const int b = min(static_cast<int>((w.top - x) * per_bin), kBins - 1);
-    return (s.plan.count > 1 && b >= s.plan.begin[1]) + (s.plan.count > 2 && b >= s.plan.begin[2]);
+  const auto interval = [&](int e) {
+    const float y = fminf((w.top - logit_of(s.list[e])) * per_place, (kBins - 1) * 2048.f);
+    const int b = __float_as_uint(__fadd_rd(y, 8388608.f)) >> 11 & (kBins - 1);
+    return (b >= p.begin[1]) + (b >= p.begin[2]);
   };
-  const auto before = [&](int j) { return seg[0] + (j > 0 ? seg[1] : 0) + (j > 1 ? seg[2] : 0); };
+  const auto rank_of = [&](int e, int j) { return static_cast<uint32_t>((j == 0 ? p.rank[0] : j == 1 ? p.rank[1] : p.rank[2]) + e); };
   uint64_t mine = 0, kept = 0, all;
+#pragma unroll 1
   for (int e = e0; e < e1; ++e) {
-    const float x = logit_of(s.list[e]);
-    const uint64_t m = w.of(x, s.table);
+    const uint64_t m = w.of(logit_of(s.list[e]), s.table);
+    s.weights[e] = m;
     mine += m;
-    if (m >= least_w && static_cast<uint32_t>(s.plan.rank[interval(x)] + e) < most) kept += m;
+    if (m >= least_w && rank_of(e, interval(e)) < most) kept += m;
   }
   const uint64_t first = block_scan(mine, s, &all) - mine;  // of this thread's part
-  const uint64_t z1 = block_sum(kept, s) + seg[0] + seg[1] + seg[2] + seg[3];
-  // p z1, in 128 bits
+  const uint64_t z1 = block_sum(kept, s) + segs;
+  // What is kept after top-p, and the token, of this thread's part.
   const uint64_t share = fraction64(r.top_p), p_hi = __umul64hi(z1, share), p_lo = z1 * share;
-  const auto is_kept = [&](int e, float x, uint64_t m, uint64_t upto) {
-    const uint32_t rank = static_cast<uint32_t>(s.plan.rank[interval(x)] + e);
-    return rank < most && m >= least_w && (r.top_p >= 1.f || rank == 0 || upto < p_hi || (upto == p_hi && p_lo != 0));
-  };
-  uint64_t z2 = z1;
-  if (r.top_p < 1.f) {
+  uint64_t z2 = z1, token = ~uint64_t(0), target = 0;
+#pragma unroll 1
+  for (int pass = r.top_p < 1.f ? 0 : 1; pass < 2; ++pass) {
+    if (pass == 1) target = part_of(z2, r.u);
     uint64_t at = first, top = 0;
+#pragma unroll 1
     for (int e = e0; e < e1; ++e) {
-      const float x = logit_of(s.list[e]);
-      const uint64_t m = w.of(x, s.table), upto = before(interval(x)) + at;
-      if (is_kept(e, x, m, upto)) top = upto + m;
+      const int j = interval(e);
+      const uint64_t m = s.weights[e], upto = (j == 0 ? seg0 : j == 1 ? seg1 : seg2) + at;
       at += m;
+      if (pass == 1) {
+        if (upto + m > target) {
+          token = e;
+          break;
+        }
+      } else {
+        const uint32_t rank = rank_of(e, j);
+        if (rank < most && m >= least_w && (rank == 0 || upto < p_hi || (upto == p_hi && p_lo != 0))) top = upto + m;
+      }
     }
-    z2 = ~block_min(~top, s);
+    const uint64_t least = block_min(pass == 1 ? token : ~top, s);
+    if (pass == 1) token = least;
+    else z2 = ~least;
   }
-  const uint64_t target = part_of(z2, r.u);
-  uint64_t at = first, token = ~uint64_t(0);
-  for (int e = e0; e < e1; ++e) {
-    const float x = logit_of(s.list[e]);
-    const uint64_t m = w.of(x, s.table);
-    at += m;
-    if (before(interval(x)) + at > target) {
-      token = e;
-      break;
-    }
-  }
-  token = block_min(token, s);
   if (threadIdx.x == 0) {
-    const uint64_t key = s.list[min(token, static_cast<uint64_t>(n - 1))];
+    const int e = static_cast<int>(min(token, static_cast<uint64_t>(n - 1)));
+    const uint64_t key = s.list[e];
     P.tokens[row] = static_cast<int32_t>(key & 0xffffffffu);
-    if (P.logprobs) P.logprobs[row] = w.log_share(logit_of(key), s.table, z2);
+    if (P.logprobs) P.logprobs[row] = w.log_share(s.weights[e], z2);
   }
 }
 
@@ -452,10 +476,10 @@ __device__ __noinline__ void look(const Params& P, Shared& s, const Weight& w, i
       lo = min(lo, key);
       hi = max(hi, key);
     }
-  });
+  }, [] {});
   if (threadIdx.x == 0) {
-    s.sum[0] = s.sum[1] = s.most = 0;
-    s.least = ~0ull;
+    s.sum[0] = s.sum[1] = s.high = 0;
+    s.low = ~0ull;
   }
   __syncthreads();
   n = warp_sum(n);
@@ -465,8 +489,8 @@ __device__ __noinline__ void look(const Params& P, Shared& s, const Weight& w, i
   if ((threadIdx.x & 31) == 0) {
     atomicAdd(&s.sum[0], static_cast<unsigned long long>(n));
     atomicAdd(&s.sum[1], static_cast<unsigned long long>(m));
-    atomicMin(&s.least, static_cast<unsigned long long>(lo));
-    atomicMax(&s.most, static_cast<unsigned long long>(hi));
+    atomicMin(&s.low, static_cast<unsigned long long>(lo));
+    atomicMax(&s.high, static_cast<unsigned long long>(hi));
   }
   cluster.sync();
   *count = *mass = *most = 0;
@@ -475,8 +499,8 @@ __device__ __noinline__ void look(const Params& P, Shared& s, const Weight& w, i
     const Shared* o = cluster.map_shared_rank(&s, c);
     *count += o->sum[0];
     *mass += o->sum[1];
-    *least = min(*least, static_cast<uint64_t>(o->least));
-    *most = max(*most, static_cast<uint64_t>(o->most));
+    *least = min(*least, static_cast<uint64_t>(o->low));
+    *most = max(*most, static_cast<uint64_t>(o->high));
   }
   cluster.sync();
 }
@@ -503,11 +527,11 @@ __device__ __forceinline__ uint64_t bisect(const Params& P, Shared& s, const Wei
 }
 
 template <typename T, int kCtas>
-__device__ __noinline__ void by_bisection(const Params& P, Shared& s, const Row& r, const Weight& w, int64_t row, int rank,
-                                          uint32_t candidates) {
+__device__ __noinline__ void by_bisection(const Params& P, Shared& s, const Row& r, const Weight& w, int64_t row, int rank) {
   const uint64_t all = ~uint64_t(0);
   uint64_t end = all, count, mass, x, y;
-  if (r.top_k > 0 && static_cast<uint32_t>(r.top_k) < candidates)
+  look<T, kCtas>(P, s, w, row, rank, all, all, &count, &mass, &x, &y);
+  if (r.top_k > 0 && static_cast<uint64_t>(r.top_k) < count)
     end = bisect<T, kCtas>(P, s, w, row, rank, all, [&](uint64_t n, uint64_t) { return n >= static_cast<uint64_t>(r.top_k); });
   if (r.min_p > 0.f) {
     // kept are the keys up to the last whose weight is enough: weights fall with the keys
@@ -532,7 +556,7 @@ __device__ __noinline__ void by_bisection(const Params& P, Shared& s, const Row&
   const uint64_t key = bisect<T, kCtas>(P, s, w, row, rank, end, [&](uint64_t, uint64_t m) { return m > target; });
   if (rank == 0 && threadIdx.x == 0) {
     P.tokens[row] = static_cast<int32_t>(key & 0xffffffffu);
-    if (P.logprobs) P.logprobs[row] = w.log_share(logit_of(key), s.table, mass);
+    if (P.logprobs) P.logprobs[row] = w.log_share(w.of(logit_of(key), s.table), mass);
   }
 }
 
@@ -546,7 +570,10 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) sample
   const int64_t row = blockIdx.x / kCtas;
   const int first = rank * kThreads + threadIdx.x, step = kCtas * kThreads;
   if (threadIdx.x < 256) s.table[threadIdx.x] = kPowers.v[threadIdx.x];
-  for (int b = threadIdx.x; b < kBins; b += kThreads) s.bins[b] = 0;
+  for (int b = threadIdx.x; b < kBins; b += kThreads) s.bins[b] = s.places[b] = 0;
+  if (threadIdx.x < 4) s.segment[threadIdx.x] = 0;
+  if (threadIdx.x == 4) s.collected = 0;
+  if (threadIdx.x == 5) s.best = 0x7fffffffu;
   grid_dep_wait();
   grid_dep_launch();
   Row r;
@@ -555,107 +582,147 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) sample
   r.min_p = P.min_p ? __ldg(P.min_p + row) : 0.f;
   r.top_k = P.top_k ? __ldg(P.top_k + row) : 0;
   r.u = __ldg(P.uniform + row);
-  // the largest logit
-  float top = -INFINITY;
-  int32_t at = 0;
-  uint32_t finite = 0;
-  each<T>(P, row, first, step, [&](float x, int i) {
-    if (!candidate(x)) return;
-    ++finite;
-    if (x > top) {
-      top = x;
-      at = i;
+  // the largest logit and the least
+  float top = -INFINITY, low = INFINITY;
+  each<T>(P, row, first, step, [&](float x, int) {
+    const bool is_one = candidate(x);
+    top = fmaxf(top, is_one ? x : -INFINITY);
+    low = fminf(low, is_one ? x : INFINITY);
+  }, [] {});
+  {
+    const uint32_t a = __reduce_min_sync(0xffffffffu, order_of(top)), b = __reduce_max_sync(0xffffffffu, order_of(low));
+    if ((threadIdx.x & 31) == 0) {
+      s.warp_mass[threadIdx.x >> 5] = logit_of(static_cast<uint64_t>(a) << 32);
+      s.warp_low[threadIdx.x >> 5] = logit_of(static_cast<uint64_t>(b) << 32);
     }
-  });
-  const uint64_t best = block_min(finite > 0 ? key_of(top, at) : ~uint64_t(0), s), here = block_sum(finite, s);
+  }
+  __syncthreads();
   if (threadIdx.x < kCtas) {
+    float x = -INFINITY, y = INFINITY;
+#pragma unroll
+    for (int v = 0; v < kWarps; ++v) {
+      x = fmaxf(x, s.warp_mass[v]);
+      y = fminf(y, s.warp_low[v]);
+    }
     Shared* o = cluster.map_shared_rank(&s, threadIdx.x);
-    o->best[rank] = best;
-    o->finite[rank] = here;
+    o->largest[rank] = x;
+    o->least[rank] = y;
   }
   cluster.sync();
-  uint64_t key = ~uint64_t(0);
-  uint32_t candidates = 0;
 #pragma unroll
   for (int c = 0; c < kCtas; ++c) {
-    key = min(key, static_cast<uint64_t>(s.best[c]));
-    candidates += static_cast<uint32_t>(s.finite[c]);
+    top = fmaxf(c == 0 ? -INFINITY : top, s.largest[c]);
+    low = fminf(c == 0 ? INFINITY : low, s.least[c]);
   }
   const bool wrong = !(r.temperature >= 0.f && r.temperature <= 3.4e38f) || !(r.u >= 0.f && r.u < 1.f) || !(r.top_p >= 0.f) ||
                      !(r.min_p <= 1.f);
-  if (wrong || candidates == 0 || r.temperature == 0.f) {
+  if (wrong || top == -INFINITY) {
     if (rank == 0 && threadIdx.x == 0) {
-      const bool none = wrong || candidates == 0;
       if (wrong) flag_error(P.err, kErrSetting);
-      P.tokens[row] = none ? -1 : static_cast<int32_t>(key & 0xffffffffu);
-      if (P.logprobs) P.logprobs[row] = none ? -INFINITY : 0.f;
+      P.tokens[row] = -1;
+      if (P.logprobs) P.logprobs[row] = -INFINITY;
     }
     return;
   }
-  const Weight w(logit_of(key), r.temperature, P.shift);
-  const float per_bin = fminf(w.ch * kBinsPerUnit, 3.0e38f);
-  // how many fall into each bin
-  each<T>(P, row, first, step, [&](float x, int) {
-    if (!candidate(x)) return;
-    const float y = (w.top - x) * per_bin;
-    if (y < kBins - 1.f) atomicAdd(&s.bins[static_cast<int>(y)], 1u);
-  });
-  cluster.sync();
   Shared* head = cluster.map_shared_rank(&s, 0);
+  if (r.temperature == 0.f) {  // the first of the largest
+    uint32_t at = 0x7fffffffu;
+    each<T>(P, row, first, step, [&](float x, int i) { at = x == top ? min(at, static_cast<uint32_t>(i)) : at; }, [] {});
+    at = __reduce_min_sync(0xffffffffu, at);
+    if ((threadIdx.x & 31) == 0) atomicMin(&head->best, at);
+    cluster.sync();
+    if (rank == 0 && threadIdx.x == 0) {
+      P.tokens[row] = static_cast<int32_t>(s.best);
+      if (P.logprobs) P.logprobs[row] = 0.f;
+    }
+    return;
+  }
+  const Weight w(top, r.temperature, P.shift);
+  // bins a power of two of the weights: 64, or as many as let the row's candidates have them all
+  const float range = fmaxf((top - low) * w.ch, 1e-6f);
+  const float per_unit = fmaxf(kBinsPerUnit, (kBins - 1.f) / range);
+  // A place in the bins in units of 1/2048, behind the binary point of 2^23: bin and place are its bits.
+  const float per_place = fminf(w.ch * per_unit, 1e30f) * 2048.f;
+  constexpr float kEnd = (kBins - 1) * 2048.f;
+  // how many fall into each bin, and where
+  each<T>(P, row, first, step, [&](float x, int) {
+    const float y = (top - x) * per_place;
+    if (!(y >= 0.f && y < kEnd)) return;  // (the last bin's, and what is no candidate)
+    const uint32_t at = __float_as_uint(__fadd_rd(y, 8388608.f));
+    atomicAdd(&s.bins[at >> 11 & (kBins - 1)], 1u);
+    atomicAdd(&s.places[at >> 11 & (kBins - 1)], at & 2047u);
+  }, [] {});
+  cluster.sync();
+  // summed up by shares, and given to all
   for (int b = rank * (kBins / kCtas) + threadIdx.x; b < (rank + 1) * (kBins / kCtas); b += kThreads) {
     uint32_t n = 0;
+    float place = 0.f;
 #pragma unroll
-    for (int c = 0; c < kCtas; ++c) n += cluster.map_shared_rank(&s, c)->bins[b];
-    head->total[b] = n;
-  }
-  cluster.sync();
-  if (rank == 0) {
-    // the rest are in the last bin
-    uint64_t counted = 0;
-    for (int b = threadIdx.x; b < kBins - 1; b += kThreads) counted += s.total[b];
-    counted = block_sum(counted, s);
-    if (threadIdx.x == 0) s.total[kBins - 1] = candidates - static_cast<uint32_t>(counted);
-    __syncthreads();
-    make_plan(s, r, candidates);
-  }
-  cluster.sync();
-  if (rank != 0 && threadIdx.x < sizeof(Plan) / 4)
-    reinterpret_cast<int32_t*>(&s.plan)[threadIdx.x] = reinterpret_cast<const int32_t*>(&head->plan)[threadIdx.x];
-  __syncthreads();
-  for (int b = threadIdx.x; b < kBins; b += kThreads) {
-    int kind = b > s.plan.last ? kIgnore : 0;
-    for (int j = 0; j < s.plan.count; ++j) {
-      if (b >= s.plan.begin[j] && b <= s.plan.end[j]) kind = kGather;
-      else if (kind < kIgnore && b > s.plan.end[j]) ++kind;
+    for (int c = 0; c < kCtas; ++c) {
+      const Shared* o = cluster.map_shared_rank(&s, c);
+      n += o->bins[b];
+      place += static_cast<float>(o->places[b]);
     }
-    s.kind[b] = static_cast<uint8_t>(kind);
+    place = n ? place / (2048.f * n) : 0.f;
+#pragma unroll
+    for (int c = 0; c < kCtas; ++c) {
+      Shared* o = cluster.map_shared_rank(&s, c);
+      o->all[b] = n;
+      o->mean[b] = place;
+    }
   }
-  __syncthreads();
+  cluster.sync();
+  make_plan(s, r, per_unit, P.vocab * 2.4e-10f);
   // candidates of the borders' bins are collected, the others' weights summed up
   uint64_t mass[4] = {0, 0, 0, 0};
+  const float tail = kTailUnits * per_unit * 2048.f, behind = (s.plan.last + 1) * 2048.f;
+  const bool all_bins = s.plan.last == kBins - 1;
+  int waiting = 0;
+  const auto add = [&](int kind, uint64_t m) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mass[k] += kind == k ? m : 0;
+  };
+  const auto kind_at = [&](float y) { return s.kind[__float_as_uint(__fadd_rd(fminf(y, kEnd), 8388608.f)) >> 11 & (kBins - 1)]; };
+  const auto work_off = [&]() {
+    while (__any_sync(0xffffffffu, waiting > 0)) {
+      if (waiting > 0) {
+        const float x = s.queue[--waiting][threadIdx.x];
+        add(kind_at((top - x) * per_place), w.of(x, s.table));
+      }
+    }
+  };
   each<T>(P, row, first, step, [&](float x, int i) {
-    if (!candidate(x)) return;
-    const int kind = s.kind[static_cast<int>(fminf((w.top - x) * per_bin, kBins - 1.f))];
-    if (kind == kIgnore) return;
+    const float y = (top - x) * per_place;
+    if (!(y >= 0.f) || (!all_bins && y >= behind) || !candidate(x)) return;
+    const int kind = kind_at(y);
     if (kind == kGather) {
       const uint32_t place = atomicAdd(&head->collected, 1u);
       if (place < kCollect) head->list[place] = key_of(x, i);
-      return;
+    } else if (y > tail) {
+      add(kind, w.small(x));
+    } else {
+      s.queue[waiting++][threadIdx.x] = x;
     }
-    const uint64_t m = w.of(x, s.table);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) mass[k] += kind == k ? m : 0;
+  }, [&] {
+    if (__any_sync(0xffffffffu, waiting > kQueue - 8)) work_off();
   });
+  work_off();
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
+    if (k > s.plan.count) break;
     const uint64_t m = warp_sum(mass[k]);
     if ((threadIdx.x & 31) == 0 && m) atomicAdd(&head->segment[k], static_cast<unsigned long long>(m));
   }
   cluster.sync();
-  const bool many = head->collected > kCollect;
+  const uint32_t collected = head->collected;
   cluster.sync();  // (the first CTA's memory has been read)
-  if (many) by_bisection<T, kCtas>(P, s, r, w, row, rank, candidates);
-  else if (rank == 0) finish(P, s, r, w, per_bin, row, candidates);
+  if (collected > kCollect) {
+    by_bisection<T, kCtas>(P, s, r, w, row, rank);
+  } else if (rank == 0) {
+    for (uint32_t i = threadIdx.x; i < collected; i += kThreads) s.unsorted[i] = s.list[i];
+    __syncthreads();
+    finish(P, s, r, w, per_place, row);
+  }
 }
 
 template <typename T, int kCtas>

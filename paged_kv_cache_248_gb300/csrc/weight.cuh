@@ -63,12 +63,13 @@ struct Weight {
   int shift;
 
   __device__ __forceinline__ Weight(float top_, float temperature, int shift_) : top(top_), shift(shift_) {
-    const double c = 1.4426950408889634074 / static_cast<double>(temperature);
-    ch = static_cast<float>(c);
-    cl = static_cast<float>(c - static_cast<double>(ch));
-    if (!(ch < 3.0e38f)) {  // (a temperature next to zero: only the largest logit has a weight)
-      ch = 3.0e38f;
+    constexpr float kHigh = 1.44269502162933349609375f, kLow = 1.925963033500e-8f;  // log2(e)
+    ch = kHigh / temperature;
+    if (!(ch < 1e30f)) {  // (a temperature next to zero: only the largest logit has a weight)
+      ch = 1e30f;
       cl = 0.f;
+    } else {  // (the remainder is exact)
+      cl = (fmaf(-ch, temperature, kHigh) + kLow) / temperature;
     }
   }
 
@@ -100,9 +101,24 @@ struct Weight {
     return share >= 1.f ? uint64_t(1) << (kWeightBits - shift) : part_of_up(uint64_t(1) << (kWeightBits - shift), share);
   }
 
+  // A weight below 2^-20 of the largest, right to 2^-21 of itself: fp32 to the end.
+  __device__ __forceinline__ uint64_t small(float x) const {
+    const float dh = x - top, minus = dh - x;
+    const float dl = (x - (dh - minus)) - (top + minus);
+    const float yh = dh * ch;
+    if (!(yh > -64.f)) return 0;
+    const float yl = fmaf(dl, ch, fmaf(dh, cl, fmaf(dh, ch, -yh)));
+    float w;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(yh));
+    w *= __int_as_float((127 + kWeightBits - shift) << 23);
+    // (46 - 20 bits at most: they fit 32)
+    return __float2uint_rn(fmaf(w * 0.6931472f, yl, w));
+  }
+
   // log(w / mass)
-  __device__ __forceinline__ float log_share(float x, const uint64_t* table, uint64_t mass) const {
-    return static_cast<float>(log(static_cast<double>(of(x, table)) / static_cast<double>(mass)));
+  __device__ __forceinline__ float log_share(uint64_t w, uint64_t mass) const {
+    const float all = __ull2float_rn(mass);
+    return w > mass - w ? log1pf(-(__ull2float_rn(mass - w) / all)) : logf(__ull2float_rn(w) / all);
   }
 };
 
