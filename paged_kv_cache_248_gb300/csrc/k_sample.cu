@@ -13,12 +13,15 @@
 //      of their places within it.  That tells every mass to 1e-4 (the weight of the mean place, from below, is off by an
 //      eighth of the square of a bin's width), and so, for each border (the end of top-k and min-p, of top-p,
 //      the token), the one or two bins in which it must lie;
-//   3. the candidates of those bins are collected in the cluster's first CTA, and the others' exact weights summed
-//      up between them.
-// The first CTA sorts what was collected (hundreds at most, as a rule) and finds the borders exactly.  With top-k or min-p
-// nothing behind their end is looked at closely, so that no weight but the collected ones' is ever computed.
-// Weights below 2^-20 of the largest need not be right to 2^-40 of themselves: they are rounded to fp32 first.  The larger
-// ones, few in most rows, wait in a queue of each thread's, so that a warp computes as many as it has lanes at a time.
+//   3. the candidates of those bins are collected in the cluster's first CTA, and the others' weights summed up
+//      between them: exact ones of 2^-12 of the largest and more, smaller ones in fp32.
+// The first CTA sorts what was collected (hundreds at most, as a rule), takes its exact weights and finds the borders.
+// Where one lies so close to a candidate's (2^-25 of the sums) that the fp32 weights could tell them wrong, the sums are
+// taken again, exact down to 2^-20 of the largest weight, and the borders found again: a few rows in a thousand flat
+// ones, hardly any other.  (The exponential unit's error is 2^-24 of a weight, rms, with a mean of -5.25e-8, measured, that
+// is given back; of thousands of weights below 2^-12 the sum is then right to 2^-29.)
+// Weights to be exact, few in most rows, wait in a queue of each thread's, so that a warp computes as many as it has lanes
+// at a time.  With top-k or min-p nothing behind their end is looked at closely.
 // Where more than 2048 candidates lie in the borders' bins (rows of equal logits), borders are found by bisection
 // of the keys instead, a pass over the row each.
 //
@@ -37,7 +40,7 @@ namespace {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2048, kPerThread = kBins / kThreads;
 constexpr float kBinsPerUnit = 64.f;
-constexpr float kTailUnits = 20.f;  // weights below 2^-20 of the largest are rounded to fp32
+constexpr float kExactFirst = 12.f, kExactAgain = 20.f;  // weights down to 2^-these are exact, at first and again
 constexpr int kCollect = 2048;
 constexpr int kQueue = 16;  // places of a thread's queue, eight of which a piece may fill
 constexpr int kGather = 255, kIgnore = 254;  // of a bin: its candidates are collected; lie behind everything
@@ -80,6 +83,7 @@ struct Shared {
   int32_t found[8];
   float bound[2];
   uint32_t collected, best;  // (first CTA) of the list; the first of the largest logits
+  int32_t unsure;            // (first CTA) the borders need exact sums
   Plan plan;
   unsigned long long sum[2], low, high;  // of a pass of the bisection
 };
@@ -397,10 +401,10 @@ __device__ __forceinline__ void sort_list(Shared& s, int n) {
   __syncthreads();
 }
 
-// The token out of the collected candidates (the first CTA).
-__device__ __forceinline__ void finish(const Params& P, Shared& s, const Row& r, const Weight& w, float per_place, int64_t row) {
-  const int n = static_cast<int>(s.collected);
-  sort_list(s, n);
+// The token out of the n collected candidates, which are sorted (the first CTA); false: with `exact` sums between them it
+// could be another.
+__device__ __forceinline__ bool finish(const Params& P, Shared& s, const Row& r, const Weight& w, float per_place, int64_t row, int n,
+                                    bool exact) {
   const Plan p = s.plan;
   const uint64_t least_w = r.min_p > 0.f ? w.part_up(r.min_p) : 0;
   const uint32_t most = r.top_k > 0 ? static_cast<uint32_t>(r.top_k) : 0xffffffffu;
@@ -424,6 +428,8 @@ __device__ __forceinline__ void finish(const Params& P, Shared& s, const Row& r,
   }
   const uint64_t first = block_scan(mine, s, &all) - mine;  // of this thread's part
   const uint64_t z1 = block_sum(kept, s) + segs;
+  const uint64_t off = exact ? 0 : segs >> 25;  // how far sums may be off
+  bool unsure = false;
   // What is kept after top-p, and the token, of this thread's part.
   const uint64_t share = fraction64(r.top_p), p_hi = __umul64hi(z1, share), p_lo = z1 * share;
   uint64_t z2 = z1, token = ~uint64_t(0), target = 0;
@@ -437,11 +443,10 @@ __device__ __forceinline__ void finish(const Params& P, Shared& s, const Row& r,
       const uint64_t m = s.weights[e], upto = (j == 0 ? seg0 : j == 1 ? seg1 : seg2) + at;
       at += m;
       if (pass == 1) {
-        if (upto + m > target) {
-          token = e;
-          break;
-        }
+        unsure |= upto + m <= target + off && upto + m + off >= target && off > 0;
+        if (upto + m > target) token = min(token, static_cast<uint64_t>(e));
       } else {
+        unsure |= upto <= p_hi + off && upto + off >= p_hi && off > 0;
         const uint32_t rank = rank_of(e, j);
         if (rank < most && m >= least_w && (rank == 0 || upto < p_hi || (upto == p_hi && p_lo != 0))) top = upto + m;
       }
@@ -450,12 +455,14 @@ __device__ __forceinline__ void finish(const Params& P, Shared& s, const Row& r,
     if (pass == 1) token = least;
     else z2 = ~least;
   }
+  if (__syncthreads_or(unsure)) return false;
   if (threadIdx.x == 0) {
     const int e = static_cast<int>(min(token, static_cast<uint64_t>(n - 1)));
     const uint64_t key = s.list[e];
     P.tokens[row] = static_cast<int32_t>(key & 0xffffffffu);
     if (P.logprobs) P.logprobs[row] = w.log_share(s.weights[e], z2);
   }
+  return true;
 }
 
 // ------------------------------------------------------------------ bisection
@@ -562,7 +569,7 @@ __device__ __noinline__ void by_bisection(const Params& P, Shared& s, const Row&
 
 // ------------------------------------------------------------------ kernel
 template <typename T, int kCtas>
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) sample_kernel(const Params P) {
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sample_kernel(const Params P) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Shared& s = *reinterpret_cast<Shared*>(smem_raw);
   cg::cluster_group cluster = cg::this_cluster();
@@ -673,55 +680,87 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) sample
   }
   cluster.sync();
   make_plan(s, r, per_unit, P.vocab * 2.4e-10f);
-  // candidates of the borders' bins are collected, the others' weights summed up
-  uint64_t mass[4] = {0, 0, 0, 0};
-  const float tail = kTailUnits * per_unit * 2048.f, behind = (s.plan.last + 1) * 2048.f;
-  const bool all_bins = s.plan.last == kBins - 1;
-  int waiting = 0;
-  const auto add = [&](int kind, uint64_t m) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) mass[k] += kind == k ? m : 0;
-  };
+  // candidates of the borders' bins are collected, the others' weights summed up: all, those behind the first interval, ...
+  const int intervals = s.plan.count;
+  const float behind = s.plan.last == kBins - 1 ? INFINITY : (s.plan.last + 1) * 2048.f;
   const auto kind_at = [&](float y) { return s.kind[__float_as_uint(__fadd_rd(fminf(y, kEnd), 8388608.f)) >> 11 & (kBins - 1)]; };
-  const auto work_off = [&]() {
-    while (__any_sync(0xffffffffu, waiting > 0)) {
-      if (waiting > 0) {
-        const float x = s.queue[--waiting][threadIdx.x];
-        add(kind_at((top - x) * per_place), w.of(x, s.table));
+  int waiting = 0;
+  uint32_t collected = 0;
+#pragma unroll 1
+  for (int round = 0; round < 2; ++round) {
+    const float limit = (round ? kExactAgain : kExactFirst) * per_unit * 2048.f;
+    uint64_t mass[4] = {0, 0, 0, 0}, light[4] = {0, 0, 0, 0};
+    float part[4] = {0.f, 0.f, 0.f, 0.f};  // of a piece
+    const auto work_off = [&]() {
+      while (__any_sync(0xffffffffu, waiting > 0)) {
+        if (waiting > 0) {
+          const float x = s.queue[--waiting][threadIdx.x];
+          const int kind = kind_at((top - x) * per_place);
+          const uint64_t m = w.of(x, s.table);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mass[k] += kind >= k ? m : 0;
+        }
+      }
+    };
+    each<T>(P, row, first, step, [&](float x, int i) {
+      const float y = (top - x) * per_place;
+      if (!(y >= 0.f && y < behind)) return;  // (what is no candidate among it)
+      const int kind = kind_at(y);
+      if (kind == kGather) {
+        if (round > 0) return;
+        const uint32_t place = atomicAdd(&head->collected, 1u);
+        if (place < kCollect) head->list[place] = key_of(x, i);
+      } else if (y < limit) {
+        s.queue[waiting++][threadIdx.x] = x;
+      } else {
+        const float m = w.rounded(x);
+        part[0] += m;
+        if (kind > 0) part[1] += m;
+        if (kind > 1) part[2] += m;
+        if (kind > 2) part[3] += m;
+      }
+    }, [&] {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k > intervals) break;
+        light[k] += __float2ull_rn(part[k]);
+        part[k] = 0.f;
+      }
+      if (__any_sync(0xffffffffu, waiting > kQueue - 8)) work_off();
+    });
+    work_off();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k > intervals) break;
+      // (5.25e-8 is 451 / 2^33)
+      uint64_t m = mass[k] + light[k] + (light[k] >> 20) * 451 / 8192;
+      if (k < 3) m -= mass[k + 1] + light[k + 1] + (light[k + 1] >> 20) * 451 / 8192;
+      m = warp_sum(m);
+      if ((threadIdx.x & 31) == 0 && m) atomicAdd(&head->segment[k], static_cast<unsigned long long>(m));
+    }
+    cluster.sync();
+    if (round == 0) {
+      collected = head->collected;
+      if (collected > kCollect) {
+        cluster.sync();  // (the first CTA's memory has been read)
+        by_bisection<T, kCtas>(P, s, r, w, row, rank);
+        return;
       }
     }
-  };
-  each<T>(P, row, first, step, [&](float x, int i) {
-    const float y = (top - x) * per_place;
-    if (!(y >= 0.f) || (!all_bins && y >= behind) || !candidate(x)) return;
-    const int kind = kind_at(y);
-    if (kind == kGather) {
-      const uint32_t place = atomicAdd(&head->collected, 1u);
-      if (place < kCollect) head->list[place] = key_of(x, i);
-    } else if (y > tail) {
-      add(kind, w.small(x));
-    } else {
-      s.queue[waiting++][threadIdx.x] = x;
+    if (rank == 0) {
+      if (round == 0) {
+        for (uint32_t i = threadIdx.x; i < collected; i += kThreads) s.unsorted[i] = s.list[i];
+        __syncthreads();
+        sort_list(s, static_cast<int>(collected));
+      }
+      const bool sure = finish(P, s, r, w, per_place, row, static_cast<int>(collected), round > 0);
+      if (threadIdx.x == 0) s.unsure = !sure;
+      if (!sure && threadIdx.x < 4) s.segment[threadIdx.x] = 0;
     }
-  }, [&] {
-    if (__any_sync(0xffffffffu, waiting > kQueue - 8)) work_off();
-  });
-  work_off();
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (k > s.plan.count) break;
-    const uint64_t m = warp_sum(mass[k]);
-    if ((threadIdx.x & 31) == 0 && m) atomicAdd(&head->segment[k], static_cast<unsigned long long>(m));
-  }
-  cluster.sync();
-  const uint32_t collected = head->collected;
-  cluster.sync();  // (the first CTA's memory has been read)
-  if (collected > kCollect) {
-    by_bisection<T, kCtas>(P, s, r, w, row, rank);
-  } else if (rank == 0) {
-    for (uint32_t i = threadIdx.x; i < collected; i += kThreads) s.unsorted[i] = s.list[i];
-    __syncthreads();
-    finish(P, s, r, w, per_place, row);
+    cluster.sync();
+    const bool again = head->unsure != 0;
+    cluster.sync();  // (the first CTA's memory has been read)
+    if (!again) return;
   }
 }
 

@@ -101,18 +101,14 @@ struct Weight {
     return share >= 1.f ? uint64_t(1) << (kWeightBits - shift) : part_of_up(uint64_t(1) << (kWeightBits - shift), share);
   }
 
-  // A weight below 2^-20 of the largest, right to 2^-21 of itself: fp32 to the end.
-  __device__ __forceinline__ uint64_t small(float x) const {
-    const float dh = x - top, minus = dh - x;
-    const float dl = (x - (dh - minus)) - (top + minus);
-    const float yh = dh * ch;
-    if (!(yh > -64.f)) return 0;
-    const float yl = fmaf(dl, ch, fmaf(dh, cl, fmaf(dh, ch, -yh)));
+  // The same in fp32, right to 2^-20 of itself.
+  __device__ __forceinline__ float rounded(float x) const {
+    const float d = x - top, yh = d * ch, yl = fmaf(d, cl, fmaf(d, ch, -yh));
     float w;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(yh));
     w *= __int_as_float((127 + kWeightBits - shift) << 23);
-    // (46 - 20 bits at most: they fit 32)
-    return __float2uint_rn(fmaf(w * 0.6931472f, yl, w));
+    const float full = fmaf(w * 0.6931472f, yl, w);
+    return yh > -64.f ? full : 0.f;  // (an infinite d among it)
   }
 
   // log(w / mass)
