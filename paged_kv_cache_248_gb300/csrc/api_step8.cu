@@ -82,7 +82,7 @@ int pkv_rope_append(const void* q, const void* k, const void* v, int32_t dtype, 
   const AppendArgs a{q,       k,       v,      q_stride, k_stride,     v_stride,           q_out_stride, num_q_heads,     cos_sin,
                      rot_dim, interleaved != 0, num_angles, positions, k_cache, v_cache, scales, *cache, block_tables,
                      max_blocks_per_seq, seq_lens, query_start_loc, num_seqs, num_tokens, max_query_len, q_out};
-  return launch_append(a, ctx->err, as_stream(stream));
+  return launch_append(a, ctx->num_sms, ctx->err, as_stream(stream));
 }
 
 int pkv_q8_workspace(const pkv_cache_desc* cache, int32_t num_q_heads, int32_t max_query_len, int64_t* bytes) {

@@ -11,7 +11,7 @@
 // without another rounding (but for codes that leave the normal range).
 //
 // Work.  A row (token, head) is read as 16-byte vectors, two for each of 8 (16) lanes: the two that
-// hold a vector's partners.  With 16- or 32-bit caches a CTA takes a token's rows.  With 8 bits a
+// hold a vector's partners.  With 16- or 32-bit caches a CTA, or a warp, takes a token's rows.  With 8 bits a
 // warp takes the new rows of one (request, block, kv head, K or V): up to 16 rows, 64 values a lane in
 // registers, so that the scale is known before anything is written and no one else writes it.
 // Request i touches at most ceil((q_i + 15) / 16) blocks, less than floor(qsl[i+1] / 16) -
@@ -39,6 +39,7 @@ struct Params {
   uint32_t* err;
   int64_t num_tokens, num_blocks, num_angles, cache_ctas;
   int32_t num_seqs, max_blocks, max_q, hq, hkv, rot, interleaved, d;
+  int32_t warp_a_token;  // else: a CTA
 };
 
 // The last request with start(i) <= x, 0 if there is none; start does not decrease.  (All lanes of a warp.)
@@ -70,8 +71,7 @@ struct Row {
 };
 
 template <typename T>
-__device__ __forceinline__ void load_vec(const T* p, float (&x)[16 / sizeof(T)]) {
-  const uint4 raw = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void unpack(const uint4& raw, float (&x)[16 / sizeof(T)]) {
   if constexpr (sizeof(T) == 4) {
     x[0] = __uint_as_float(raw.x);
     x[1] = __uint_as_float(raw.y);
@@ -85,6 +85,11 @@ __device__ __forceinline__ void load_vec(const T* p, float (&x)[16 / sizeof(T)])
       x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
+}
+
+template <typename T>
+__device__ __forceinline__ void load_vec(const T* p, float (&x)[16 / sizeof(T)]) {
+  unpack<T>(*reinterpret_cast<const uint4*>(p), x);
 }
 
 template <typename T>
@@ -191,32 +196,58 @@ __device__ __forceinline__ bool find_token(const Params& P, int64_t t, int& i, R
   return load_request(P, i, r);
 }
 
-// Rows first, first + step, ... of token t's queries.
+// Rows first, first + step, ... of token t's queries, four of them on their way at once.
 template <typename T>
 __device__ __forceinline__ void rotate_q(const Params& P, int64_t t, const Lane<T>& lane, const Turn<T>& turn, bool ok, int first,
                                          int step) {
+  constexpr int kAtOnce = 4;
   const T* src = static_cast<const T*>(P.q) + t * P.q_stride;
   T* dst = static_cast<T*>(P.q_out) + t * P.out_stride;
-  for (int h = first; h < P.hq; h += step) {
-    Row<T> x{};
-    if (ok) {
-      load_vec(src + h * P.d + lane.at, x.a);
-      load_vec(src + h * P.d + lane.other, x.b);
-      turn.apply(P, lane, x.a, x.b);
+#pragma unroll 1
+  for (int h0 = first; h0 < P.hq; h0 += kAtOnce * step) {
+    uint4 a[kAtOnce] = {}, b[kAtOnce] = {};
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int h = h0 + k * step;
+      if (!ok || h >= P.hq) continue;
+      a[k] = *reinterpret_cast<const uint4*>(src + h * P.d + lane.at);
+      b[k] = *reinterpret_cast<const uint4*>(src + h * P.d + lane.other);
     }
-    store_vec(dst + h * P.d + lane.at, x.a);
-    store_vec(dst + h * P.d + lane.other, x.b);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int h = h0 + k * step;
+      if (h >= P.hq) continue;
+      Row<T> x;
+      unpack<T>(a[k], x.a);
+      unpack<T>(b[k], x.b);
+      if (ok) turn.apply(P, lane, x.a, x.b);
+      store_vec(dst + h * P.d + lane.at, x.a);
+      store_vec(dst + h * P.d + lane.other, x.b);
+    }
   }
 }
 
-// A cache of the inputs' type: one CTA a token.
+// The token of this thread, and its place among the threads that share it (a CTA, or a warp where tokens are many: its
+// chain of dependent loads then costs a wave of CTAs instead of several).
+struct Sharer {
+  int64_t token;
+  int at, of;
+};
+__device__ __forceinline__ Sharer sharer(const Params& P, int64_t cta) {
+  return P.warp_a_token ? Sharer{cta * kWarps + (threadIdx.x >> 5), static_cast<int>(threadIdx.x & 31), 32}
+                        : Sharer{cta, static_cast<int>(threadIdx.x), kThreads};
+}
+
+// A cache of the inputs' type.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) append_kernel(const Params P) {
   grid_dep_wait();
   grid_dep_launch();
-  const int lanes = P.d / (2 * Row<T>::kVec), group = threadIdx.x / lanes, groups = kThreads / lanes;
-  const Lane<T> lane(P, threadIdx.x % lanes);
-  const int64_t t = blockIdx.x;
+  const Sharer me = sharer(P, blockIdx.x);
+  const int lanes = P.d / (2 * Row<T>::kVec), group = me.at / lanes, groups = me.of / lanes;
+  const Lane<T> lane(P, me.at % lanes);
+  const int64_t t = me.token;
+  if (t >= P.num_tokens) return;
   int i;
   Request r;
   bool ok = find_token(P, t, i, r);
@@ -225,12 +256,12 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Params P) {
   int64_t id = 0, angle = 0;
   if (!ok) {
     if (t < r.t0 || t >= r.t1) return;
-    if (threadIdx.x == 0) flag_error(P.err, kErrLength);
+    if (me.at == 0) flag_error(P.err, kErrLength);
   } else {
     id = __ldg(P.bt + static_cast<int64_t>(i) * P.max_blocks + p / kBlock);
     angle = angle_of(P, t, p);
-    if (threadIdx.x == 0 && angle < 0) flag_error(P.err, kErrLength);
-    if (threadIdx.x == 0 && (id < 0 || id >= P.num_blocks)) flag_error(P.err, kErrBlockId);
+    if (me.at == 0 && angle < 0) flag_error(P.err, kErrLength);
+    if (me.at == 0 && (id < 0 || id >= P.num_blocks)) flag_error(P.err, kErrBlockId);
     ok = angle >= 0;
   }
   Turn<T> turn;
@@ -281,16 +312,18 @@ __global__ void __launch_bounds__(kThreads) append8_kernel(const Params P, int u
   const int lane_id = threadIdx.x & 31;
   const Lane<T> lane(P, lane_id & 7);
   if (blockIdx.x >= P.cache_ctas) {
-    const int64_t t = blockIdx.x - P.cache_ctas;
+    const Sharer me = sharer(P, blockIdx.x - P.cache_ctas);
+    const int64_t t = me.token;
+    if (t >= P.num_tokens) return;
     int i;
     Request r;
     bool ok = find_token(P, t, i, r);
     if (t < r.t0 || t >= r.t1) return;
     const int64_t angle = ok ? angle_of(P, t, r.ctx + t - r.t0) : -1;
-    if (angle < 0 && threadIdx.x == 0) flag_error(P.err, kErrLength);
+    if (angle < 0 && me.at == 0) flag_error(P.err, kErrLength);
     Turn<T> turn;
     if (angle >= 0) turn.load(P, lane, angle);
-    rotate_q(P, t, lane, turn, angle >= 0, threadIdx.x / 8, kThreads / 8);
+    rotate_q(P, t, lane, turn, angle >= 0, me.at / 8, me.of / 8);
     return;
   }
   const int64_t x = blockIdx.x / units_per_block;
@@ -384,7 +417,7 @@ __global__ void __launch_bounds__(kThreads) append8_kernel(const Params P, int u
 
 }  // namespace
 
-int launch_append(const AppendArgs& a, uint32_t* err, cudaStream_t s) {
+int launch_append(const AppendArgs& a, int num_sms, uint32_t* err, cudaStream_t s) {
   Params p{};
   p.q = a.q;
   p.k = a.k;
@@ -414,17 +447,19 @@ int launch_append(const AppendArgs& a, uint32_t* err, cudaStream_t s) {
   p.rot = a.rot_dim;
   p.interleaved = a.interleaved;
   p.d = a.cache.head_dim;
+  // 16 CTAs of tokens an SM are under way at once; of more tokens a warp takes one
+  p.warp_a_token = a.num_tokens > 16 * static_cast<int64_t>(num_sms);
+  const int64_t token_ctas = p.warp_a_token ? (a.num_tokens + kWarps - 1) / kWarps : a.num_tokens;
   if (a.cache.dtype == PKV_E4M3) {
     const int units = (2 * p.hkv + kWarps - 1) / kWarps;
     const int64_t blocks = a.max_query_len == 1 ? a.num_seqs : a.num_tokens / kBlock + 2 * static_cast<int64_t>(a.num_seqs);
     p.cache_ctas = blocks * units;
-    const int64_t ctas = p.cache_ctas + (a.q ? a.num_tokens : 0);
+    const int64_t ctas = p.cache_ctas + (a.q ? token_ctas : 0);
     if (ctas > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
     return cuda_status(launch_k(append8_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, s, p, units));
   }
-  if (a.num_tokens > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
   auto* kernel = a.cache.dtype == PKV_F32 ? append_kernel<float> : append_kernel<__nv_bfloat16>;
-  return cuda_status(launch_k(kernel, dim3(static_cast<unsigned>(a.num_tokens)), dim3(kThreads), 0, s, p));
+  return cuda_status(launch_k(kernel, dim3(static_cast<unsigned>(token_ctas)), dim3(kThreads), 0, s, p));
 }
 
 }  // namespace pkv

@@ -381,7 +381,7 @@ struct AppendArgs {
   int32_t max_query_len;
   void* q_out;
 };
-int launch_append(const AppendArgs& a, uint32_t* err, cudaStream_t s);
+int launch_append(const AppendArgs& a, int num_sms, uint32_t* err, cudaStream_t s);
 size_t q8_workspace(const pkv_cache_desc& c, int32_t num_q_heads, int32_t max_query_len, int num_sms);
 int launch_q8(const AttnArgs& a, const float* scales, void* workspace, int num_sms, uint32_t* err, cudaStream_t s);
 struct SampleArgs {
