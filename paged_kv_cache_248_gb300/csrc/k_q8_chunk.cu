@@ -452,68 +452,67 @@ __device__ void softmax_warps(const Q8Params& P, Ctl& c, uint8_t* qbuf, uint32_t
   const float sign = P.scale_log2 < 0.f ? -1.f : 1.f;  // (a negative scale turns Q round)
   bool ok = true;
 
-  for (uint32_t it = 0; ok; ++it) {
-    const int slot = it % kItemRing;
-    ok = all(wait_for(&c.item_full[slot], (it / kItemRing) & 1, abort_flag));
-    if (!ok) break;
-    const Item item = c.ring[slot];
-    if (item.idx < 0) break;
-    const int nq = tokens_of(P, item.nq, w), j0 = item.j0 + w * (128 >> P.gp_log2);
-    if (nq == 0) {  // the unit has one row tile only
-      n += item.nt;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c.item_empty[slot]);
-      continue;
+  float next_factor = 0.f;  // of the unit whose Q is in place: |scale| log2(e) / c
+  // This row of Q times a power of two, in fp16.  (S of the unit before has been made: Q may be overwritten.)
+  const auto put_q = [&](const Item& item) {
+    const int j0 = item.j0 + w * (128 >> P.gp_log2);
+    const bool live = rj < tokens_of(P, item.nq, w) && rg < P.group;  // a real (token, head) row
+    const uint4* src = reinterpret_cast<const uint4*>(
+        P.q + ((static_cast<int64_t>(item.t0) + j0 + (live ? rj : 0)) * P.hq + static_cast<int64_t>(item.head) * P.group + (live ? rg : 0)) * 128);
+    uint4 raw[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) raw[i] = __ldg(src + i);
+    uint32_t top = 0;  // the largest finite size: bf16 bits compare as whole numbers
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t y[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t a = y[e] & 0x7fffu, b = y[e] >> 16 & 0x7fffu;
+        top = max(top, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
+      }
     }
+    // largest c in [1, 2)
+    const int e = min(max(static_cast<int>(top >> 7) - 127, -126), 126);
+    const float up = __int_as_float((127 - e) << 23) * sign;
+    next_factor = fabsf(P.scale_log2) * (e >= -100 ? __int_as_float((127 + e) << 23) : 0.f);
+    uint8_t* row = qbuf + w * kTileBytes + r * 128;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t y[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      uint32_t h[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        // (times 0 and added: an infinity makes its row NaN)
+        const float a = __uint_as_float(y[k] << 16), b = __uint_as_float(y[k] & 0xffff0000u);
+        const __half2 z = __floats2half2_rn(fmaf(a, up, a * 0.f), fmaf(b, up, b * 0.f));
+        h[k] = live ? *reinterpret_cast<const uint32_t*>(&z) : 0u;
+      }
+      *reinterpret_cast<uint4*>(row + (i >> 3) * kHalfBytes + (((i & 7) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&c.q_full[w]);
+  };
+
+  Item item{};
+  // (the first pass has no unit to work on: it only puts Q in place)
+  for (uint32_t next = 0; ok; ++next) {
+    const bool none = next == 0;
+    const int nq = none ? 0 : tokens_of(P, item.nq, w), j0 = item.j0 + w * (128 >> P.gp_log2);
+    const int slot = (next + kItemRing - 1) % kItemRing;  // of this unit
     // this row tile is the last one to read the unit's key tiles
     const bool releases = w == 1 || tokens_of(P, item.nq, 1) == 0;
     const bool live = rj < nq && rg < P.group;  // a real (token, head) row
     const bool warp_live = __any_sync(0xffffffffu, live);
-    // This row of Q times a power of two, in fp16.  (S of the unit before has been made: Q may be overwritten.)
-    float factor;
-    {
-      const uint4* src = reinterpret_cast<const uint4*>(
-          P.q + ((static_cast<int64_t>(item.t0) + j0 + (live ? rj : 0)) * P.hq + static_cast<int64_t>(item.head) * P.group + (live ? rg : 0)) * 128);
-      uint32_t top = 0;  // the largest finite size: bf16 bits compare as whole numbers
-#pragma unroll 4
-      for (int i = 0; i < 16; ++i) {
-        const uint4 x = __ldg(src + i);
-        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t a = y[e] & 0x7fffu, b = y[e] >> 16 & 0x7fffu;
-          top = max(top, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
-        }
-      }
-      // largest c in [1, 2)
-      const int e = min(max(static_cast<int>(top >> 7) - 127, -126), 126);
-      const float up = live ? __int_as_float((127 - e) << 23) * sign : 0.f;
-      factor = fabsf(P.scale_log2) * (e >= -100 ? __int_as_float((127 + e) << 23) : 0.f);
-      uint8_t* row = qbuf + w * kTileBytes + r * 128;
-#pragma unroll 4
-      for (int i = 0; i < 16; ++i) {
-        const uint4 x = __ldg(src + i);
-        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-        uint32_t h[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          // (times 0 and added: an infinity makes its row NaN)
-          float a = __uint_as_float(y[k] << 16), b = __uint_as_float(y[k] & 0xffff0000u);
-          const __half2 z = __floats2half2_rn(fmaf(a, up, a * 0.f), fmaf(b, up, b * 0.f));
-          h[k] = live ? *reinterpret_cast<const uint32_t*>(&z) : 0u;
-        }
-        *reinterpret_cast<uint4*>(row + (i >> 3) * kHalfBytes + (((i & 7) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c.q_full[w]);
-    }
+    const float factor = next_factor;
     float ref = -INFINITY, sum = 0.f;
 #pragma unroll 1
-    for (int j = 0; j < item.nt; ++j, ++n) {
+    for (int j = 0; j < item.nt && nq > 0; ++j, ++n) {
       const int k0 = (item.kt0 + j) * kTileKeys;
-      const bool edge = k0 + kTileKeys > item.ctx + item.j0 + 1;  // not every row of the unit sees all of the tile
       const int nvis = max(0, min(kTileKeys, item.ctx + j0 + rj + 1 - k0));
+      const bool edge = k0 + kTileKeys > item.ctx + item.j0 + 1;             // not every row of the unit sees all of the tile
+      const bool masked = edge && __any_sync(0xffffffffu, nvis < kTileKeys);  // nor of the warp
       ok = all(wait_for(&c.s_full[w], tc++ & 1, abort_flag));
       if (!ok) break;
       tc_fence_after();
@@ -530,7 +529,7 @@ __device__ void softmax_warps(const Q8Params& P, Ctl& c, uint8_t* qbuf, uint32_t
         if (lane == 0) mbar_arrive(&c.p_full[w][0]);
       };
       if (warp_live) {
-        const float top = edge ? row_largest<true>(srow, info, factor, nvis) : row_largest<false>(srow, info, factor, kTileKeys);
+        const float top = masked ? row_largest<true>(srow, info, factor, nvis) : row_largest<false>(srow, info, factor, kTileKeys);
         if (j == 0) {
           ref = top - kTop;
         } else {
@@ -553,7 +552,7 @@ __device__ void softmax_warps(const Q8Params& P, Ctl& c, uint8_t* qbuf, uint32_t
         }
         // a row that has seen nothing yet: all its weights are 0
         const float use = ref == -INFINITY ? 0.f : ref;
-        sum += edge ? row_weights<true>(srow, info, factor, use, nvis, first_half)
+        sum += masked ? row_weights<true>(srow, info, factor, use, nvis, first_half)
                     : row_weights<false>(srow, info, factor, use, kTileKeys, first_half);
         tmem_st_wait();
         if (edge) {
@@ -574,7 +573,21 @@ __device__ void softmax_warps(const Q8Params& P, Ctl& c, uint8_t* qbuf, uint32_t
       if (lane == 0) mbar_arrive(&c.p_full[w][1]);
       if (!ok) break;
     }
-    ok = ok && all(wait_for(&c.o_full[w], oc++ & 1, abort_flag));
+    if (!ok) break;
+    // the next unit's Q first: its S is made while this unit's rows are stored
+    ok = all(wait_for(&c.item_full[next % kItemRing], (next / kItemRing) & 1, abort_flag));
+    if (!ok) break;
+    const Item after = c.ring[next % kItemRing];
+    if (after.idx >= 0 && tokens_of(P, after.nq, w) > 0) put_q(after);
+    if (nq == 0) {  // no unit, or one without rows of this tile
+      n += item.nt;
+      __syncwarp();
+      if (!none && lane == 0) mbar_arrive(&c.item_empty[slot]);
+      if (after.idx < 0) break;
+      item = after;
+      continue;
+    }
+    ok = all(wait_for(&c.o_full[w], oc++ & 1, abort_flag));
     if (!ok) break;
     tc_fence_after();
     if (r == 0 && releases) mbar_arrive(&c.vempty[(n - 1) % kStages]);
@@ -628,6 +641,8 @@ __device__ void softmax_warps(const Q8Params& P, Ctl& c, uint8_t* qbuf, uint32_t
       mbar_arrive(&c.o_free[w]);
       mbar_arrive(&c.item_empty[slot]);
     }
+    if (after.idx < 0) break;
+    item = after;
   }
   if (!ok && !*abort_flag && lane == 0) raise_abort(c, P.err);
 }
