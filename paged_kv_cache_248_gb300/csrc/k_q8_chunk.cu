@@ -4,7 +4,7 @@
 // Mathematics.  out = sum_u softmax_u(scale q.K_u) V_u with K_u = ks code_u, V_u = vs code_u, over the keys up to a row's
 // own token, in one pass over the keys with a running maximum and sum per row.  Tiles of codes become fp16 in shared
 // memory, which is exact (e4m3 has 4 significant bits and exponents from -9 to 8); Q becomes fp16 times a
-// power of two for each row, exact but for what is 2^-24 of the row's largest element.  A block's scales
+// power of two for each 32 rows, exact down to 2^-24 of their largest element.  A block's scales
 // meet the scores: score * ks + log2 vs, so that a row's reference is the largest w vs of it, and its sum takes p / vs.
 // The weights are rounded to fp16 (2^-11 of each); they reach 2^7 when a reference is set and 2^15 at most, so that those of
 // 2^-21 of the largest and more keep all of their digits.
@@ -453,15 +453,19 @@ __device__ void softmax_warps(const Q8Params& P, Ctl& c, uint8_t* qbuf, uint32_t
   bool ok = true;
 
   float next_factor = 0.f;  // of the unit whose Q is in place: |scale| log2(e) / c
-  // This row of Q times a power of two, in fp16.  (S of the unit before has been made: Q may be overwritten.)
+  // The warp's rows of Q times a power of two, in fp16; half a warp loads a row.  (S of the unit before has been made: Q
+  // may be overwritten.)
   const auto put_q = [&](const Item& item) {
-    const int j0 = item.j0 + w * (128 >> P.gp_log2);
-    const bool live = rj < tokens_of(P, item.nq, w) && rg < P.group;  // a real (token, head) row
-    const uint4* src = reinterpret_cast<const uint4*>(
-        P.q + ((static_cast<int64_t>(item.t0) + j0 + (live ? rj : 0)) * P.hq + static_cast<int64_t>(item.head) * P.group + (live ? rg : 0)) * 128);
+    const int64_t token0 = static_cast<int64_t>(item.t0) + item.j0 + w * (128 >> P.gp_log2);
+    const int tokens = tokens_of(P, item.nq, w), chunk = lane & 15;
     uint4 raw[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) raw[i] = __ldg(src + i);
+    for (int i = 0; i < 16; ++i) {
+      const int row = wq * 32 + 2 * i + (lane >> 4), j = row >> P.gp_log2, g = row & ((1 << P.gp_log2) - 1);
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (j < tokens && g < P.group)
+        raw[i] = __ldg(reinterpret_cast<const uint4*>(P.q + ((token0 + j) * P.hq + static_cast<int64_t>(item.head) * P.group + g) * 128) + chunk);
+    }
     uint32_t top = 0;  // the largest finite size: bf16 bits compare as whole numbers
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -472,13 +476,14 @@ __device__ void softmax_warps(const Q8Params& P, Ctl& c, uint8_t* qbuf, uint32_t
         top = max(top, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
       }
     }
+    top = __reduce_max_sync(0xffffffffu, top);
     // largest c in [1, 2)
     const int e = min(max(static_cast<int>(top >> 7) - 127, -126), 126);
     const float up = __int_as_float((127 - e) << 23) * sign;
     next_factor = fabsf(P.scale_log2) * (e >= -100 ? __int_as_float((127 + e) << 23) : 0.f);
-    uint8_t* row = qbuf + w * kTileBytes + r * 128;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
+      const int row = wq * 32 + 2 * i + (lane >> 4);
       const uint32_t y[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
       uint32_t h[4];
 #pragma unroll
@@ -486,9 +491,10 @@ __device__ void softmax_warps(const Q8Params& P, Ctl& c, uint8_t* qbuf, uint32_t
         // (times 0 and added: an infinity makes its row NaN)
         const float a = __uint_as_float(y[k] << 16), b = __uint_as_float(y[k] & 0xffff0000u);
         const __half2 z = __floats2half2_rn(fmaf(a, up, a * 0.f), fmaf(b, up, b * 0.f));
-        h[k] = live ? *reinterpret_cast<const uint32_t*>(&z) : 0u;
+        h[k] = *reinterpret_cast<const uint32_t*>(&z);
       }
-      *reinterpret_cast<uint4*>(row + (i >> 3) * kHalfBytes + (((i & 7) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(qbuf + w * kTileBytes + (chunk >> 3) * kHalfBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) =
+          make_uint4(h[0], h[1], h[2], h[3]);
     }
     fence_proxy_async_smem();
     __syncwarp();
