@@ -645,7 +645,9 @@ int launch_q8(const AttnArgs& a, const float* scales, void* workspace, int num_s
   const int64_t tiles = units >= l.runs ? units : units * key_tiles;  // (enough to know)
   const int64_t most = tiles >= l.runs ? tiles : tiles * a.num_seqs;
   const int ctas = static_cast<int>(most < l.runs ? most : l.runs);
-  p.unit_cost = most < l.runs ? 0 : 2;
+  // (a unit's beginning and end as key tiles.  8 requests of 512 tokens: 146, 130, 125, 124, 129 us with 1, 2, 3, 4, 6; 33 of 1
+  // to 61: 39.9, 36.8, 36.8, 38.2, 39.2.  Single tokens: no difference)
+  p.unit_cost = most < l.runs ? 0 : single ? 2 : 3;
   p.min_run = 1 + p.unit_cost;
   p.q = static_cast<const __nv_bfloat16*>(a.q);
   p.k_cache = static_cast<const uint8_t*>(a.k_cache);

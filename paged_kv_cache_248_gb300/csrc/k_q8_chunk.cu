@@ -389,6 +389,7 @@ __device__ __forceinline__ float row_largest(uint32_t taddr, const TileInfo& inf
   uint32_t a[32];
 #pragma unroll 1
   for (int h = 0; h < 4; ++h) {
+    if (kMask && !__any_sync(0xffffffffu, nvis > 32 * h)) break;  // (no row of the warp sees more)
     tmem_ld32_issue(taddr + 32 * h, a);
     tmem_ld32_wait(a);
 #pragma unroll
@@ -410,6 +411,12 @@ __device__ __forceinline__ float row_weights(uint32_t taddr, const TileInfo& inf
   uint32_t a[32];
 #pragma unroll 1
   for (int h = 0; h < 4; ++h) {
+    if (kMask && !__any_sync(0xffffffffu, nvis > 32 * h)) {  // (no row of the warp sees more)
+      const uint32_t none[16] = {};
+      tmem_st16(taddr + 16 * h, none);
+      if (h == 2) half();
+      continue;
+    }
     tmem_ld32_issue(taddr + 32 * h, a);
     const float k0 = factor * info.ks[2 * h], k1 = factor * info.ks[2 * h + 1];
     const float m0 = info.lv[2 * h] - ref, m1 = info.lv[2 * h + 1] - ref;
@@ -466,17 +473,30 @@ __device__ void softmax_warps(const Q8Params& P, Ctl& c, uint8_t* qbuf, uint32_t
       if (j < tokens && g < P.group)
         raw[i] = __ldg(reinterpret_cast<const uint4*>(P.q + ((token0 + j) * P.hq + static_cast<int64_t>(item.head) * P.group + g) * 128) + chunk);
     }
-    uint32_t top = 0;  // the largest finite size: bf16 bits compare as whole numbers
+    // the largest size: bf16 bits without their signs compare as whole numbers, two at a time
+    uint32_t both_tops = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const uint32_t y[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t a = y[e] & 0x7fffu, b = y[e] >> 16 & 0x7fffu;
-        top = max(top, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
-      }
+      for (int e = 0; e < 4; ++e) both_tops = __vmaxu2(both_tops, y[e] & 0x7fff7fffu);
     }
-    top = __reduce_max_sync(0xffffffffu, top);
+    uint32_t top = __reduce_max_sync(0xffffffffu, max(both_tops & 0xffffu, both_tops >> 16));
+    if (top >= 0x7f80u) {  // (rare) the largest finite one; what is not finite becomes NaN, and its row with it
+      top = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        uint32_t* y = reinterpret_cast<uint32_t*>(&raw[i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t a = y[e] & 0x7fffu, b = y[e] >> 16 & 0x7fffu;
+          top = max(top, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
+          if (a >= 0x7f80u) y[e] |= 0x7fffu;
+          if (b >= 0x7f80u) y[e] |= 0x7fff0000u;
+        }
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+    }
     // largest c in [1, 2)
     const int e = min(max(static_cast<int>(top >> 7) - 127, -126), 126);
     const float up = __int_as_float((127 - e) << 23) * sign;
@@ -488,9 +508,7 @@ __device__ void softmax_warps(const Q8Params& P, Ctl& c, uint8_t* qbuf, uint32_t
       uint32_t h[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        // (times 0 and added: an infinity makes its row NaN)
-        const float a = __uint_as_float(y[k] << 16), b = __uint_as_float(y[k] & 0xffff0000u);
-        const __half2 z = __floats2half2_rn(fmaf(a, up, a * 0.f), fmaf(b, up, b * 0.f));
+        const __half2 z = __floats2half2_rn(__uint_as_float(y[k] << 16) * up, __uint_as_float(y[k] & 0xffff0000u) * up);
         h[k] = *reinterpret_cast<const uint32_t*>(&z);
       }
       *reinterpret_cast<uint4*>(qbuf + w * kTileBytes + (chunk >> 3) * kHalfBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) =
