@@ -401,9 +401,9 @@ __device__ __forceinline__ void sort_list(Shared& s, int n) {
   __syncthreads();
 }
 
-// The token out of the n collected candidates, which are sorted (the first CTA); false: with `exact` sums between them it
-// could be another.
-__device__ __forceinline__ bool finish(const Params& P, Shared& s, const Row& r, const Weight& w, float per_place, int64_t row, int n,
+// The token out of the n collected candidates, which are sorted (the first CTA): 0.  1: with `exact` sums between them it
+// could be another.  2: it is not among them.
+__device__ __forceinline__ int finish(const Params& P, Shared& s, const Row& r, const Weight& w, float per_place, int64_t row, int n,
                                     bool exact) {
   const Plan p = s.plan;
   const uint64_t least_w = r.min_p > 0.f ? w.part_up(r.min_p) : 0;
@@ -455,14 +455,15 @@ __device__ __forceinline__ bool finish(const Params& P, Shared& s, const Row& r,
     if (pass == 1) token = least;
     else z2 = ~least;
   }
-  if (__syncthreads_or(unsure)) return false;
+  if (__syncthreads_or(unsure)) return 1;
+  if (token == ~uint64_t(0)) return 2;
   if (threadIdx.x == 0) {
-    const int e = static_cast<int>(min(token, static_cast<uint64_t>(n - 1)));
+    const int e = static_cast<int>(token);
     const uint64_t key = s.list[e];
     P.tokens[row] = static_cast<int32_t>(key & 0xffffffffu);
     if (P.logprobs) P.logprobs[row] = w.log_share(s.weights[e], z2);
   }
-  return true;
+  return 0;
 }
 
 // ------------------------------------------------------------------ bisection
@@ -621,7 +622,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
     top = fmaxf(c == 0 ? -INFINITY : top, s.largest[c]);
     low = fminf(c == 0 ? INFINITY : low, s.least[c]);
   }
-  const bool wrong = !(r.temperature >= 0.f && r.temperature <= 3.4e38f) || !(r.u >= 0.f && r.u < 1.f) || !(r.top_p >= 0.f) ||
+  const bool wrong = !(r.temperature >= 0.f && r.temperature < INFINITY) || !(r.u >= 0.f && r.u < 1.f) || !(r.top_p >= 0.f) ||
                      !(r.min_p <= 1.f);
   if (wrong || top == -INFINITY) {
     if (rank == 0 && threadIdx.x == 0) {
@@ -645,9 +646,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
     return;
   }
   const Weight w(top, r.temperature, P.shift);
-  // bins a power of two of the weights: 64, or as many as let the row's candidates have them all
+  // bins a power of two of the weights: 64, or as many as let the row's candidates have all but the last one
   const float range = fmaxf((top - low) * w.ch, 1e-6f);
-  const float per_unit = fmaxf(kBinsPerUnit, (kBins - 1.f) / range);
+  const float per_unit = fmaxf(kBinsPerUnit, (kBins - 2.f) / range);
   // A place in the bins in units of 1/2048, behind the binary point of 2^23: bin and place are its bits.
   const float per_place = fminf(w.ch * per_unit, 1e30f) * 2048.f;
   constexpr float kEnd = (kBins - 1) * 2048.f;
@@ -743,8 +744,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
       collected = head->collected;
       if (collected > kCollect) {
         cluster.sync();  // (the first CTA's memory has been read)
-        by_bisection<T, kCtas>(P, s, r, w, row, rank);
-        return;
+        break;
       }
     }
     if (rank == 0) {
@@ -753,15 +753,17 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
         __syncthreads();
         sort_list(s, static_cast<int>(collected));
       }
-      const bool sure = finish(P, s, r, w, per_place, row, static_cast<int>(collected), round > 0);
-      if (threadIdx.x == 0) s.unsure = !sure;
-      if (!sure && threadIdx.x < 4) s.segment[threadIdx.x] = 0;
+      const int left = finish(P, s, r, w, per_place, row, static_cast<int>(collected), round > 0);
+      if (threadIdx.x == 0) s.unsure = left;
+      if (left && threadIdx.x < 4) s.segment[threadIdx.x] = 0;
     }
     cluster.sync();
-    const bool again = head->unsure != 0;
+    const int left = head->unsure;
     cluster.sync();  // (the first CTA's memory has been read)
-    if (!again) return;
+    if (left == 0) return;
+    if (left == 2) break;
   }
+  by_bisection<T, kCtas>(P, s, r, w, row, rank);
 }
 
 template <typename T, int kCtas>
