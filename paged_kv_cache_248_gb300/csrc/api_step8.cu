@@ -25,12 +25,20 @@ int check_heads(const pkv_cache_desc* cache, int32_t num_q_heads, int32_t max_qu
   return num_q_heads / cache->num_kv_heads > 16 ? PKV_ERR_UNSUPPORTED : PKV_OK;
 }
 
-// [rows] of `width` elements, `stride` apart: where they begin and end.
-struct Range {
-  uintptr_t begin, end;
-  Range(const void* p, int64_t rows, int64_t stride, int64_t width, int64_t size)
-      : begin(reinterpret_cast<uintptr_t>(p)), end(begin + static_cast<uintptr_t>(((rows - 1) * stride + width) * size)) {}
-  bool meets(const Range& o) const { return begin < o.end && o.begin < end; }
+// `rows` rows of `width` elements, `stride` apart, in bytes.
+struct Rows {
+  int64_t begin, end, stride, width;
+  Rows(const void* p, int64_t rows, int64_t stride_, int64_t width_, int64_t size)
+      : begin(static_cast<int64_t>(reinterpret_cast<uintptr_t>(p))), stride(stride_ * size), width(width_ * size) {
+    end = begin + (rows - 1) * stride + width;
+  }
+  // No byte in common: one lies behind the other, or they are different columns of rows of the same length.
+  bool apart(const Rows& o) const {
+    if (end <= o.begin || o.end <= begin) return true;
+    if (stride != o.stride) return false;
+    const int64_t at = ((o.begin - begin) % stride + stride) % stride;
+    return at >= width && at + o.width <= stride;
+  }
 };
 
 }  // namespace
@@ -70,11 +78,10 @@ int pkv_rope_append(const void* q, const void* k, const void* v, int32_t dtype, 
     if (q_stride < q_width || q_out_stride < q_width || q_stride * size % 16 || q_out_stride * size % 16 || !aligned16(q) ||
         !aligned16(q_out))
       return PKV_ERR_INVALID_ARG;
-    const Range out(q_out, num_tokens, q_out_stride, q_width, size);
+    const Rows out(q_out, num_tokens, q_out_stride, q_width, size);
     const bool in_place = q == q_out && q_stride == q_out_stride;
-    if (!in_place && (out.meets(Range(q, num_tokens, q_stride, q_width, size)) ||
-                      out.meets(Range(k, num_tokens, k_stride, kv_width, size)) ||
-                      out.meets(Range(v, num_tokens, v_stride, kv_width, size))))
+    if ((!in_place && !out.apart(Rows(q, num_tokens, q_stride, q_width, size))) ||
+        !out.apart(Rows(k, num_tokens, k_stride, kv_width, size)) || !out.apart(Rows(v, num_tokens, v_stride, kv_width, size)))
       return PKV_ERR_INVALID_ARG;
   }
   DeviceCtx* ctx = device_ctx(&st);

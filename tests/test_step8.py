@@ -82,6 +82,17 @@ def test_append_host_checks(pkv, over, status):
     assert _append(pkv, **over) == status
 
 
+@pytest.mark.parametrize("k,v,stride,status", [
+    (0x10000, 0x800000, 256, 1),            # k is q, which is written
+    (0x800000, 0x10000 + 512, 256, 1),      # v begins within q's first token
+    (0x10000 + 1024, 0x800000, 1024, 1),    # columns behind q's, of rows otherwise spaced
+    (0x10000 + 512, 0x10000 + 1536, 1024, 1),   # k's columns begin within q's
+    (0x10000 + 1024, 0x10000 - 256, 768, 1),    # v's columns end within the next token's q
+])
+def test_append_refuses_queries_in_place_over_keys_or_values(pkv, k, v, stride, status):
+    assert _append(pkv, qo=FAKE, qs=768, qos=768, k=P(k), v=P(v), ks=stride, vs=stride) == status
+
+
 def test_append_checks_the_cache(pkv):
     desc = pkv._CacheDesc
     assert _append(pkv, desc=desc(8, 16, 2, 64, pkv.PKV_E4M3)) == pkv.PKV_ERR_UNSUPPORTED
