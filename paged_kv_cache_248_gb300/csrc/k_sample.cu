@@ -40,7 +40,8 @@ namespace {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2048, kPerThread = kBins / kThreads;
 constexpr float kBinsPerUnit = 64.f;
-constexpr float kExactFirst = 12.f, kExactAgain = 20.f;  // weights down to 2^-these are exact, at first and again
+constexpr float kExactAgain = 20.f;  // weights down to 2^-20 of the largest are exact where sums are taken again
+constexpr float kRest = 1.f / 256.f;  // squares of the bins' masses that fp32 weights may leave, of the kept mass's
 constexpr int kCollect = 2048;
 constexpr int kQueue = 16;  // places of a thread's queue, eight of which a piece may fill
 constexpr int kGather = 255, kIgnore = 254;  // of a bin: its candidates are collected; lie behind everything
@@ -61,6 +62,7 @@ struct Plan {
   int32_t count;             // intervals
   int32_t begin[3], end[3];  // bins [begin, end]
   int32_t last;              // bins behind it are ignored
+  int32_t exact;             // weights of the bins before are exact
   int32_t rank[3];           // candidate number e of the list, in interval j, is number rank[j] + e of the row
 };
 
@@ -81,7 +83,7 @@ struct Shared {
   float warp_mass[kWarps], warp_low[kWarps];
   uint32_t warp_n[kWarps];
   int32_t found[8];
-  float bound[2];
+  float warp_sq[kWarps], bound[3];
   uint32_t collected, best;  // (first CTA) of the list; the first of the largest logits
   int32_t unsure;            // (first CTA) the borders need exact sums
   Plan plan;
@@ -212,53 +214,61 @@ __device__ __forceinline__ void make_plan(Shared& s, const Row& r, float per_uni
   const float mean[4] = {y.x, y.y, y.z, y.w};
   // candidates of these bins and up to each, and the mass up to each
   const uint32_t here[4] = {n[0], n[1], n[2], n[3]};
-  float mass[4];
+  float mass[4], sq[4];  // (and the squares of the bins' masses)
   uint32_t counted = 0;
-  float weighed = 0.f;
+  float weighed = 0.f, squares = 0.f;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    weighed += here[k] * exp2f(-(static_cast<float>(b0 + k) + mean[k]) / per_unit);
+    const float m = here[k] * exp2f(-(static_cast<float>(b0 + k) + mean[k]) / per_unit);
+    weighed += m;
+    squares = fmaf(m, m, squares);
     counted += here[k];
     n[k] = counted;
     mass[k] = weighed;
+    sq[k] = squares;
   }
   uint32_t in = counted;
-  float im = weighed;
+  float im = weighed, is = squares;
 #pragma unroll 1
   for (int d = 1; d < 32; d <<= 1) {
     const uint32_t y = __shfl_up_sync(0xffffffffu, in, d);
-    const float z = __shfl_up_sync(0xffffffffu, im, d);
+    const float z = __shfl_up_sync(0xffffffffu, im, d), x = __shfl_up_sync(0xffffffffu, is, d);
     if (lane >= d) {
       in += y;
       im += z;
+      is += x;
     }
   }
   if (lane == 31) {
     s.warp_n[warp] = in;
     s.warp_mass[warp] = im;
+    s.warp_sq[warp] = is;
   }
   if (threadIdx.x < 8) s.found[threadIdx.x] = kBins - 1;
   __syncthreads();
   uint32_t bn = in - counted;
-  float bm = im - weighed, all = 0.f;
+  float bm = im - weighed, bs = is - squares, all = 0.f, all_sq = 0.f;
 #pragma unroll 1
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) {
       bn += s.warp_n[w];
       bm += s.warp_mass[w];
+      bs += s.warp_sq[w];
     }
     all += s.warp_mass[w];
+    all_sq += s.warp_sq[w];
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     n[k] += bn;
     mass[k] += bm;
+    sq[k] += bs;
   }
   // the masses above are off by a part of 1e-4 at most, and by what lies behind the last bin
   constexpr float kLow = 0.9999f, kHigh = 1.0001f;
-  const auto first_over = [&](int at, float x) {  // the first bin up to which more than x lies, by these masses
-    const int k = mass[0] > x ? 0 : mass[1] > x ? 1 : mass[2] > x ? 2 : 3;
-    const int mine = __reduce_min_sync(0xffffffffu, mass[3] > x ? b0 + k : kBins - 1);
+  const auto first_over = [&](int at, const float (&of)[4], float x) {  // the first bin up to which more than x lies
+    const int k = of[0] > x ? 0 : of[1] > x ? 1 : of[2] > x ? 2 : 3;
+    const int mine = __reduce_min_sync(0xffffffffu, of[3] > x ? b0 + k : kBins - 1);
     if (lane == 0 && mine < kBins - 1) atomicMin(&s.found[at], mine);
   };
   const bool cut_k = r.top_k > 0, cut_m = r.min_p > 0.f;  // (a top-k of all and more ends in the last bin)
@@ -281,26 +291,31 @@ __device__ __forceinline__ void make_plan(Shared& s, const Row& r, float per_uni
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (b0 + k == a1 - 1) s.bound[0] = mass[k];
-      if (b0 + k == e1) s.bound[1] = mass[k];
+      if (b0 + k == e1) {
+        s.bound[1] = mass[k];
+        s.bound[2] = sq[k];
+      }
     }
     if (threadIdx.x == 0 && a1 == 0) s.bound[0] = 0.f;
     __syncthreads();
   }
   float z_lo = (cut1 ? s.bound[0] : all) * kLow, z_hi = (cut1 ? s.bound[1] : all) * kHigh + rest;
+  // the first bins, until the rest's squares are 2^-8 of the kept mass's at most
+  first_over(5, sq, (cut1 ? s.bound[2] : all_sq) - z_lo * z_lo * kRest);
   // the end of top-p
   int a2 = kBins, e2 = e1;
   const bool cut_p = r.top_p < 1.f;
   if (cut_p) {
-    first_over(1, r.top_p * z_lo * kLow - rest);
-    first_over(2, r.top_p * z_hi * kHigh);
+    first_over(1, mass, r.top_p * z_lo * kLow - rest);
+    first_over(2, mass, r.top_p * z_hi * kHigh);
     __syncthreads();
     a2 = min(s.found[1], e1);
     e2 = min(s.found[2], e1);
     z_lo *= r.top_p;
     z_hi = fminf(z_hi, r.top_p * z_hi + kHigh * exp2f(-static_cast<float>(a2) / per_unit));
   }
-  first_over(3, r.u * z_lo * kLow - rest);
-  first_over(4, r.u * z_hi * kHigh);
+  first_over(3, mass, r.u * z_lo * kLow - rest);
+  first_over(4, mass, r.u * z_hi * kHigh);
   __syncthreads();
   if (threadIdx.x == 0) {
     const int a3 = min(s.found[3], e2), e3 = min(s.found[4], e2);
@@ -331,6 +346,7 @@ __device__ __forceinline__ void make_plan(Shared& s, const Row& r, float per_uni
 #pragma unroll 1
     for (int i = m; i < 3; ++i) s.plan.begin[i] = s.plan.end[i] = kBins;
     s.plan.last = cut1 ? e1 : kBins - 1;
+    s.plan.exact = s.found[5] + 1;
   }
   __syncthreads();
   const Plan p = s.plan;
@@ -428,7 +444,7 @@ __device__ __forceinline__ int finish(const Params& P, Shared& s, const Row& r, 
   }
   const uint64_t first = block_scan(mine, s, &all) - mine;  // of this thread's part
   const uint64_t z1 = block_sum(kept, s) + segs;
-  const uint64_t off = exact ? 0 : segs >> 25;  // how far sums may be off
+  const uint64_t off = exact || segs == 0 ? 0 : z1 >> 25;  // how far sums may be off
   bool unsure = false;
   // What is kept after top-p, and the token, of this thread's part.
   const uint64_t share = fraction64(r.top_p), p_hi = __umul64hi(z1, share), p_lo = z1 * share;
@@ -689,7 +705,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
   uint32_t collected = 0;
 #pragma unroll 1
   for (int round = 0; round < 2; ++round) {
-    const float limit = (round ? kExactAgain : kExactFirst) * per_unit * 2048.f;
+    const float limit = fmaxf(s.plan.exact, round ? kExactAgain * per_unit : 0.f) * 2048.f;
     uint64_t mass[4] = {0, 0, 0, 0}, light[4] = {0, 0, 0, 0};
     float part[4] = {0.f, 0.f, 0.f, 0.f};  // of a piece
     const auto work_off = [&]() {
