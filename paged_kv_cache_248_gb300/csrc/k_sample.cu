@@ -44,7 +44,6 @@ constexpr float kExactAgain = 20.f;  // weights down to 2^-20 of the largest are
 constexpr float kRest = 1.f / 256.f;  // squares of the bins' masses that fp32 weights may leave, of the kept mass's
 constexpr int kCollect = 2048;
 constexpr int kQueue = 16;  // places of a thread's queue, eight of which a piece may fill
-constexpr int kGather = 255, kIgnore = 254;  // of a bin: its candidates are collected; lie behind everything
 
 struct Params {
   const void* logits;
@@ -67,24 +66,26 @@ struct Plan {
 };
 
 struct Shared {
-  uint32_t bins[kBins], places[kBins];  // of this CTA: candidates, and their places in the bin in 1/2048
+  uint32_t bins[kBins], places[kBins];  // of this CTA: candidates, and the sum of their places in the bin
   uint32_t all[kBins];                  // of the row: candidates, and the mean of their places
   float mean[kBins];
-  uint64_t list[kCollect], weights[kCollect];  // (first CTA) keys, sorted
+  uint64_t list[kCollect], weights[kCollect];  // (first CTA) keys, at last in order, and their weights
   union {
     float queue[kQueue][kThreads];
-    uint64_t unsorted[kCollect];  // (first CTA, after the queues)
+    struct {  // after the queues
+      uint64_t unsorted[kCollect], sorted[kCollect];  // (`sorted`: first CTA)
+    };
   };
-  uint8_t kind[kBins];  // of a bin: kGather, kIgnore, or how many intervals come before it
   uint64_t table[256];
   float largest[16], least[16];  // of each CTA's candidates
-  unsigned long long segment[4];            // masses of what is not collected, between the intervals (first CTA)
+  unsigned long long segment[3];  // masses of what is not collected: before the intervals, and behind the first ones
   unsigned long long warp_u64[kWarps];
   float warp_mass[kWarps], warp_low[kWarps];
   uint32_t warp_n[kWarps];
   int32_t found[8];
   float warp_sq[kWarps], bound[3];
   uint32_t collected, best;  // (first CTA) of the list; the first of the largest logits
+  uint32_t taken, place;     // candidates that this CTA collected (in `weights`), their place in the list
   int32_t unsure;            // (first CTA) the borders need exact sums
   Plan plan;
   unsigned long long sum[2], low, high;  // of a pass of the bisection
@@ -118,31 +119,48 @@ __device__ __forceinline__ uint4 load_piece(const T* p, int i0, int vocab) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Calls f(x, i) for this thread's logits of the row (those of the 16-byte pieces `first`, first + step, ...), and
-// piece_done() after each piece, which all threads of a warp call equally often.  Three pieces are on their way while one
-// is worked on.
-template <typename T, typename F, typename Done>
-__device__ __forceinline__ void each(const Params& P, int64_t row, int first, int step, F&& f, Done&& piece_done) {
+// Calls f(piece, i) with this thread's pieces of 16 bytes of the row (`first`, first + step, ...), whose logits begin at number
+// i; what the row does not have is NaN.  All threads of a CTA call it equally often.  Three pieces are on their way while
+// one is worked on.
+template <typename T, typename F>
+__device__ __forceinline__ void each_raw(const Params& P, int64_t row, int first, int step, F&& f) {
   constexpr int kVec = 16 / sizeof(T);
   const T* p = static_cast<const T*>(P.logits) + row * P.stride;
   const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));  // piece 0 begins so much before
-  const int at_warp = first - static_cast<int>(threadIdx.x & 31);
   const int end = skew + P.vocab;
   int i0 = first * kVec - skew;
   const int hop = step * kVec;
   uint4 a = load_piece<T>(p, i0, P.vocab), b = load_piece<T>(p, i0 + hop, P.vocab), c = load_piece<T>(p, i0 + 2 * hop, P.vocab);
 #pragma unroll 1
-  for (int v = at_warp; v * kVec < end; v += step, i0 += hop) {
+  for (int v = first - static_cast<int>(threadIdx.x); v * kVec < end; v += step, i0 += hop) {
     const uint4 d = load_piece<T>(p, i0 + 3 * hop, P.vocab);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int e = 0; e < kVec; ++e)
-      f(__uint_as_float(sizeof(T) == 4 ? w[e % 4] : e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16), i0 + e);
-    piece_done();
+    f(a, i0);
     a = b;
     b = c;
     c = d;
   }
+}
+// The same with their logits x[].
+template <typename T, typename F>
+__device__ __forceinline__ void each_piece(const Params& P, int64_t row, int first, int step, F&& f) {
+  constexpr int kVec = 16 / sizeof(T);
+  each_raw<T>(P, row, first, step, [&](const uint4& raw, int i0) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    float x[kVec];
+#pragma unroll
+    for (int e = 0; e < kVec; ++e)
+      x[e] = __uint_as_float(sizeof(T) == 4 ? w[e % 4] : e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+    f(x, i0);
+  });
+}
+// f(x, i) for each of them.
+template <typename T, typename F>
+__device__ __forceinline__ void each(const Params& P, int64_t row, int first, int step, F&& f) {
+  constexpr int kVec = 16 / sizeof(T);
+  each_piece<T>(P, row, first, step, [&](const float (&x)[kVec], int i0) {
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) f(x[e], i0 + e);
+  });
 }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
@@ -264,8 +282,8 @@ __device__ __forceinline__ void make_plan(Shared& s, const Row& r, float per_uni
     mass[k] += bm;
     sq[k] += bs;
   }
-  // the masses above are off by a part of 1e-4 at most, and by what lies behind the last bin
-  constexpr float kLow = 0.9999f, kHigh = 1.0001f;
+  // the masses above are off by a part of 2e-4 at most, and by what lies behind the last bin
+  constexpr float kLow = 0.9998f, kHigh = 1.0002f;
   const auto first_over = [&](int at, const float (&of)[4], float x) {  // the first bin up to which more than x lies
     const int k = of[0] > x ? 0 : of[1] > x ? 1 : of[2] > x ? 2 : 3;
     const int mine = __reduce_min_sync(0xffffffffu, of[3] > x ? b0 + k : kBins - 1);
@@ -350,23 +368,16 @@ __device__ __forceinline__ void make_plan(Shared& s, const Row& r, float per_uni
   }
   __syncthreads();
   const Plan p = s.plan;
-  // candidates before an interval that are not collected; the bins' kinds
-  uint32_t kinds = 0;
+  // candidates before an interval, and up to its end
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int b = b0 + k;
-    uint32_t kind = 0;
-    bool in_one = false;
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
       if (p.begin[j] == b) s.found[j] = static_cast<int32_t>(n[k] - here[k]);
       if (p.end[j] == b) s.found[5 + j] = static_cast<int32_t>(n[k]);
-      in_one |= b >= p.begin[j] && b <= p.end[j];
-      kind += b > p.end[j];
     }
-    kinds |= (in_one ? kGather : b > p.last ? kIgnore : kind) << (8 * k);
   }
-  reinterpret_cast<uint32_t*>(s.kind)[threadIdx.x] = kinds;
   __syncthreads();
   if (threadIdx.x == 0) {
     int collected = 0;
@@ -379,22 +390,35 @@ __device__ __forceinline__ void make_plan(Shared& s, const Row& r, float per_uni
   __syncthreads();
 }
 
-// Sorts the n keys of `unsorted` into `list` (the first CTA).
-__device__ __forceinline__ void sort_list(Shared& s, int n) {
-  if (n <= kThreads) {  // each key's place is the number of smaller ones
-    if (static_cast<int>(threadIdx.x) < n) {
-      const uint64_t mine = s.unsorted[threadIdx.x];
-      int place = 0;
+// Sorts the n keys of `unsorted` into the first CTA's `sorted`, with their weights: each key's place is the number of smaller
+// ones, which the lanes of a group count together.  Every CTA of the cluster takes a share of them.
+template <int kCtas>
+__device__ __forceinline__ void rank_share(Shared& s, Shared* head, const Weight& w, int n, int rank) {
+  const int e0 = n * rank / kCtas, e1 = n * (rank + 1) / kCtas;
+  int group = 1;
+  while (group < 32 && (e1 - e0) * group * 2 <= kThreads) group <<= 1;
+  const int at = threadIdx.x & (group - 1);
+#pragma unroll 1
+  for (int first = e0; first < e1; first += kThreads / group) {
+    const int e = first + static_cast<int>(threadIdx.x) / group;
+    const uint64_t mine = s.unsorted[min(e, e1 - 1)];
+    int place = 0;
 #pragma unroll 4
-      for (int i = 0; i < n; ++i) place += s.unsorted[i] < mine;
-      s.list[place] = mine;
+    for (int i = at; i < n; i += group) place += s.unsorted[i] < mine;
+#pragma unroll 1
+    for (int d = group >> 1; d; d >>= 1) place += __shfl_xor_sync(0xffffffffu, place, d);
+    if (e < e1 && at == 0) {
+      head->sorted[place] = mine;
+      head->weights[place] = w.of(logit_of(mine), s.table);
     }
-    __syncthreads();
-    return;
   }
+}
+
+// The same of many keys, by the first CTA.
+__device__ __forceinline__ void sort_many(Shared& s, const Weight& w, int n) {
   int size = kThreads;
   while (size < n) size <<= 1;
-  for (int i = threadIdx.x; i < size; i += kThreads) s.list[i] = i < n ? s.unsorted[i] : ~uint64_t(0);
+  for (int i = threadIdx.x; i < size; i += kThreads) s.sorted[i] = i < n ? s.unsorted[i] : ~uint64_t(0);
   __syncthreads();
 #pragma unroll 1
   for (int k = 2; k <= size; k <<= 1) {
@@ -403,10 +427,10 @@ __device__ __forceinline__ void sort_list(Shared& s, int n) {
 #pragma unroll 1
       for (int i = threadIdx.x; i < size / 2; i += kThreads) {
         const int a = 2 * i - (i & (j - 1)), b = a + j;  // bit j of a is 0
-        const uint64_t x = s.list[a], y = s.list[b];
+        const uint64_t x = s.sorted[a], y = s.sorted[b];
         if ((x > y) == ((a & k) == 0)) {
-          s.list[a] = y;
-          s.list[b] = x;
+          s.sorted[a] = y;
+          s.sorted[b] = x;
         }
       }
       // (pairs up to 32 apart stay within a warp's 64 places)
@@ -415,6 +439,8 @@ __device__ __forceinline__ void sort_list(Shared& s, int n) {
     }
   }
   __syncthreads();
+#pragma unroll 1
+  for (int i = threadIdx.x; i < n; i += kThreads) s.weights[i] = w.of(logit_of(s.sorted[i]), s.table);
 }
 
 // The token out of the n collected candidates, which are sorted (the first CTA): 0.  1: with `exact` sums between them it
@@ -426,7 +452,7 @@ __device__ __forceinline__ int finish(const Params& P, Shared& s, const Row& r, 
   const uint32_t most = r.top_k > 0 ? static_cast<uint32_t>(r.top_k) : 0xffffffffu;
   const int per = (n + kThreads - 1) / kThreads, e0 = threadIdx.x * per, e1 = min(e0 + per, n);
   // the mass before the intervals, of what is not collected
-  const uint64_t seg0 = s.segment[0], seg1 = seg0 + s.segment[1], seg2 = seg1 + s.segment[2], segs = seg2 + s.segment[3];
+  const uint64_t seg0 = s.segment[0], seg1 = seg0 + s.segment[1], segs = seg1 + s.segment[2], seg2 = segs;
   // a candidate's interval, from its bin
   const auto interval = [&](int e) {
     const float y = fminf((w.top - logit_of(s.list[e])) * per_place, (kBins - 1) * 2048.f);
@@ -437,8 +463,7 @@ __device__ __forceinline__ int finish(const Params& P, Shared& s, const Row& r, 
   uint64_t mine = 0, kept = 0, all;
 #pragma unroll 1
   for (int e = e0; e < e1; ++e) {
-    const uint64_t m = w.of(logit_of(s.list[e]), s.table);
-    s.weights[e] = m;
+    const uint64_t m = s.weights[e];
     mine += m;
     if (m >= least_w && rank_of(e, interval(e)) < most) kept += m;
   }
@@ -500,7 +525,7 @@ __device__ __noinline__ void look(const Params& P, Shared& s, const Weight& w, i
       lo = min(lo, key);
       hi = max(hi, key);
     }
-  }, [] {});
+  });
   if (threadIdx.x == 0) {
     s.sum[0] = s.sum[1] = s.high = 0;
     s.low = ~0ull;
@@ -595,8 +620,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
   const int first = rank * kThreads + threadIdx.x, step = kCtas * kThreads;
   if (threadIdx.x < 256) s.table[threadIdx.x] = kPowers.v[threadIdx.x];
   for (int b = threadIdx.x; b < kBins; b += kThreads) s.bins[b] = s.places[b] = 0;
-  if (threadIdx.x < 4) s.segment[threadIdx.x] = 0;
-  if (threadIdx.x == 4) s.collected = 0;
+  if (threadIdx.x < 3) s.segment[threadIdx.x] = 0;
+  if (threadIdx.x == 4) s.collected = s.taken = 0;
   if (threadIdx.x == 5) s.best = 0x7fffffffu;
   grid_dep_wait();
   grid_dep_launch();
@@ -606,37 +631,61 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
   r.min_p = P.min_p ? __ldg(P.min_p + row) : 0.f;
   r.top_k = P.top_k ? __ldg(P.top_k + row) : 0;
   r.u = __ldg(P.uniform + row);
-  // the largest logit and the least
-  float top = -INFINITY, low = INFINITY;
-  each<T>(P, row, first, step, [&](float x, int) {
-    const bool is_one = candidate(x);
-    top = fmaxf(top, is_one ? x : -INFINITY);
-    low = fminf(low, is_one ? x : INFINITY);
-  }, [] {});
-  {
+  // The largest logit and the least, which may be infinite: -inf makes the bins the coarsest, which they are for most rows;
+  // of a row with an infinity above its candidates the largest one is looked for again.
+  float top, low;
+#pragma unroll 1
+  for (int again = 0; again < 2; ++again) {
+    top = -INFINITY, low = INFINITY;
+    if (again) {
+      each<T>(P, row, first, step, [&](float x, int) {
+        const bool is_one = candidate(x);
+        top = fmaxf(top, is_one ? x : -INFINITY);
+        low = fminf(low, is_one ? x : INFINITY);
+      });
+    } else if constexpr (sizeof(T) == 4) {
+      each<T>(P, row, first, step, [&](float x, int) {  // (NaN is passed over)
+        top = fmaxf(top, x);
+        low = fminf(low, x);
+      });
+    } else {
+      __nv_bfloat162 hi = __float2bfloat162_rn(-INFINITY), lo = __float2bfloat162_rn(INFINITY);
+      each_raw<T>(P, row, first, step, [&](const uint4& raw, int) {
+        const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&raw);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          hi = __hmax2(hi, x[e]);
+          lo = __hmin2(lo, x[e]);
+        }
+      });
+      top = fmaxf(__low2float(hi), __high2float(hi));
+      low = fminf(__low2float(lo), __high2float(lo));
+    }
     const uint32_t a = __reduce_min_sync(0xffffffffu, order_of(top)), b = __reduce_max_sync(0xffffffffu, order_of(low));
     if ((threadIdx.x & 31) == 0) {
       s.warp_mass[threadIdx.x >> 5] = logit_of(static_cast<uint64_t>(a) << 32);
       s.warp_low[threadIdx.x >> 5] = logit_of(static_cast<uint64_t>(b) << 32);
     }
-  }
-  __syncthreads();
-  if (threadIdx.x < kCtas) {
-    float x = -INFINITY, y = INFINITY;
+    __syncthreads();
+    if (threadIdx.x < kCtas) {
+      float x = -INFINITY, y = INFINITY;
 #pragma unroll
-    for (int v = 0; v < kWarps; ++v) {
-      x = fmaxf(x, s.warp_mass[v]);
-      y = fminf(y, s.warp_low[v]);
+      for (int v = 0; v < kWarps; ++v) {
+        x = fmaxf(x, s.warp_mass[v]);
+        y = fminf(y, s.warp_low[v]);
+      }
+      Shared* o = cluster.map_shared_rank(&s, threadIdx.x);
+      o->largest[rank] = x;
+      o->least[rank] = y;
     }
-    Shared* o = cluster.map_shared_rank(&s, threadIdx.x);
-    o->largest[rank] = x;
-    o->least[rank] = y;
-  }
-  cluster.sync();
+    cluster.sync();
 #pragma unroll
-  for (int c = 0; c < kCtas; ++c) {
-    top = fmaxf(c == 0 ? -INFINITY : top, s.largest[c]);
-    low = fminf(c == 0 ? INFINITY : low, s.least[c]);
+    for (int c = 0; c < kCtas; ++c) {
+      top = fmaxf(c == 0 ? -INFINITY : top, s.largest[c]);
+      low = fminf(c == 0 ? INFINITY : low, s.least[c]);
+    }
+    if (top != INFINITY) break;
+    cluster.sync();
   }
   const bool wrong = !(r.temperature >= 0.f && r.temperature < INFINITY) || !(r.u >= 0.f && r.u < 1.f) || !(r.top_p >= 0.f) ||
                      !(r.min_p <= 1.f);
@@ -651,7 +700,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
   Shared* head = cluster.map_shared_rank(&s, 0);
   if (r.temperature == 0.f) {  // the first of the largest
     uint32_t at = 0x7fffffffu;
-    each<T>(P, row, first, step, [&](float x, int i) { at = x == top ? min(at, static_cast<uint32_t>(i)) : at; }, [] {});
+    each<T>(P, row, first, step, [&](float x, int i) { at = x == top ? min(at, static_cast<uint32_t>(i)) : at; });
     at = __reduce_min_sync(0xffffffffu, at);
     if ((threadIdx.x & 31) == 0) atomicMin(&head->best, at);
     cluster.sync();
@@ -668,14 +717,45 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
   // A place in the bins in units of 1/2048, behind the binary point of 2^23: bin and place are its bits.
   const float per_place = fminf(w.ch * per_unit, 1e30f) * 2048.f;
   constexpr float kEnd = (kBins - 1) * 2048.f;
-  // how many fall into each bin, and where
-  each<T>(P, row, first, step, [&](float x, int) {
-    const float y = (top - x) * per_place;
-    if (!(y >= 0.f && y < kEnd)) return;  // (the last bin's, and what is no candidate)
-    const uint32_t at = __float_as_uint(__fadd_rd(y, 8388608.f));
-    atomicAdd(&s.bins[at >> 11 & (kBins - 1)], 1u);
-    atomicAdd(&s.places[at >> 11 & (kBins - 1)], at & 2047u);
-  }, [] {});
+  // How many fall into each bin, and where, to 1/32 of it: both in one word while there are few (14 bits and 18), two arrays
+  // of them in turn; a thread keeps the sums of four bins.
+  {
+    static_assert(kPerThread == 4, "a thread's bins are a vector");
+    constexpr int kVec = 16 / sizeof(T), kPieces = 16 / kVec;
+    static_assert(16 * kThreads < (1 << 14) && 31 * 16 * kThreads < (1 << 18), "the fields of a word");
+    uint32_t* into = s.bins;
+    uint32_t n[4] = {0, 0, 0, 0}, place[4] = {0, 0, 0, 0};
+    int pieces = 0;
+    const auto take_over = [&](uint32_t* of) {
+      const uint4 x = reinterpret_cast<const uint4*>(of)[threadIdx.x];
+      const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+      reinterpret_cast<uint4*>(of)[threadIdx.x] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        n[k] += y[k] & 0x3fffu;
+        place[k] += y[k] >> 14;
+      }
+    };
+    each_piece<T>(P, row, first, step, [&](const float (&x)[kVec], int) {
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        const float y = (top - x[e]) * per_place;
+        if (!(fabsf(y) < kEnd)) continue;  // (the last bin's, and what is no candidate)
+        const uint32_t at = __float_as_uint(__fadd_rd(y, 8388608.f));
+        atomicAdd(&into[at >> 11 & (kBins - 1)], ((at & 0x7c0u) << 8) + 1u);
+      }
+      if (++pieces == kPieces) {
+        pieces = 0;
+        __syncthreads();
+        take_over(into);
+        into = into == s.bins ? s.places : s.bins;
+      }
+    });
+    __syncthreads();
+    take_over(into);
+    reinterpret_cast<uint4*>(s.bins)[threadIdx.x] = make_uint4(n[0], n[1], n[2], n[3]);
+    reinterpret_cast<uint4*>(s.places)[threadIdx.x] = make_uint4(place[0], place[1], place[2], place[3]);
+  }
   cluster.sync();
   // summed up by shares, and given to all
   for (int b = rank * (kBins / kCtas) + threadIdx.x; b < (rank + 1) * (kBins / kCtas); b += kThreads) {
@@ -687,7 +767,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
       n += o->bins[b];
       place += static_cast<float>(o->places[b]);
     }
-    place = n ? place / (2048.f * n) : 0.f;
+    place = n ? (place / n + 0.5f) * (1.f / 32.f) : 0.f;
 #pragma unroll
     for (int c = 0; c < kCtas; ++c) {
       Shared* o = cluster.map_shared_rank(&s, c);
@@ -697,81 +777,108 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
   }
   cluster.sync();
   make_plan(s, r, per_unit, P.vocab * 2.4e-10f);
-  // candidates of the borders' bins are collected, the others' weights summed up: all, those behind the first interval, ...
-  const int intervals = s.plan.count;
-  const float behind = s.plan.last == kBins - 1 ? INFINITY : (s.plan.last + 1) * 2048.f;
-  const auto kind_at = [&](float y) { return s.kind[__float_as_uint(__fadd_rd(fminf(y, kEnd), 8388608.f)) >> 11 & (kBins - 1)]; };
+  // Candidates of the borders' bins are collected, the others' weights summed up, for each segment between them.  (Behind the
+  // third interval nothing counts: that there are three takes a filter that ends all.)
+  const Plan& plan = s.plan;
+  const float behind = plan.last == kBins - 1 ? INFINITY : (plan.last + 1) * 2048.f;
+  float from[3], upto[3];  // the intervals' places
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    from[j] = plan.begin[j] >= kBins ? INFINITY : plan.begin[j] * 2048.f;  // (there are fewer than three)
+    upto[j] = plan.end[j] >= kBins - 1 ? INFINITY : (plan.end[j] + 1) * 2048.f;
+  }
   int waiting = 0;
   uint32_t collected = 0;
 #pragma unroll 1
   for (int round = 0; round < 2; ++round) {
-    const float limit = fmaxf(s.plan.exact, round ? kExactAgain * per_unit : 0.f) * 2048.f;
-    uint64_t mass[4] = {0, 0, 0, 0}, light[4] = {0, 0, 0, 0};
-    float part[4] = {0.f, 0.f, 0.f, 0.f};  // of a piece
+    constexpr int kVec = 16 / sizeof(T);
+    const float limit = fmaxf(plan.exact, round ? kExactAgain * per_unit : 0.f) * 2048.f;
+    // of the segments, the places whose weights are summed up in fp32
+    const float lo[3] = {limit, fmaxf(upto[0], limit), fmaxf(upto[1], limit)};
+    const float hi[3] = {fminf(from[0], behind), fminf(from[1], behind), fminf(from[2], behind)};
+    const bool third = lo[2] < hi[2];
+    uint64_t mass[3] = {0, 0, 0}, light[3] = {0, 0, 0};
     const auto work_off = [&]() {
       while (__any_sync(0xffffffffu, waiting > 0)) {
         if (waiting > 0) {
-          const float x = s.queue[--waiting][threadIdx.x];
-          const int kind = kind_at((top - x) * per_place);
+          const float x = s.queue[--waiting][threadIdx.x], y = (top - x) * per_place;
           const uint64_t m = w.of(x, s.table);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mass[k] += kind >= k ? m : 0;
+          mass[0] += y < upto[0] ? m : 0;
+          mass[1] += y >= upto[0] && y < upto[1] ? m : 0;
+          mass[2] += y >= upto[1] ? m : 0;
         }
       }
     };
-    each<T>(P, row, first, step, [&](float x, int i) {
-      const float y = (top - x) * per_place;
-      if (!(y >= 0.f && y < behind)) return;  // (what is no candidate among it)
-      const int kind = kind_at(y);
-      if (kind == kGather) {
-        if (round > 0) return;
-        const uint32_t place = atomicAdd(&head->collected, 1u);
-        if (place < kCollect) head->list[place] = key_of(x, i);
-      } else if (y < limit) {
-        s.queue[waiting++][threadIdx.x] = x;
-      } else {
-        const float m = w.rounded(x);
-        part[0] += m;
-        if (kind > 0) part[1] += m;
-        if (kind > 1) part[2] += m;
-        if (kind > 2) part[3] += m;
-      }
-    }, [&] {
+    each_piece<T>(P, row, first, step, [&](const float (&x)[kVec], int i0) {
+      float part[3] = {0.f, 0.f, 0.f};
+      uint32_t apart = 0;  // neither summed up here nor ignored
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (k > intervals) break;
-        light[k] += __float2ull_rn(part[k]);
-        part[k] = 0.f;
+      for (int e = 0; e < kVec; ++e) {
+        const float y = (top - x[e]) * per_place;
+        if (!(y < behind)) continue;  // (nor what is no candidate, but for an infinity)
+        const float m = w.rounded(x[e]);
+        const bool p0 = y >= lo[0] && y < hi[0], p1 = y >= lo[1] && y < hi[1], p2 = third && y >= lo[2] && y < hi[2];
+        if (p0) part[0] += m;
+        if (p1) part[1] += m;
+        if (p2) part[2] += m;
+        if (!(p0 || p1 || p2)) apart |= 1u << e;
       }
-      if (__any_sync(0xffffffffu, waiting > kQueue - 8)) work_off();
+      if (apart) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+          if (!(apart >> e & 1) || !candidate(x[e])) continue;
+          const float y = (top - x[e]) * per_place;
+          if ((y >= from[0] && y < upto[0]) || (y >= from[1] && y < upto[1]) || (y >= from[2] && y < upto[2])) {
+            if (round == 0) {
+              const uint32_t place = atomicAdd(&s.taken, 1u);
+              if (place < kCollect) s.weights[place] = key_of(x[e], i0 + e);
+            }
+          } else {
+            s.queue[waiting++][threadIdx.x] = x[e];
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 3; ++k) light[k] += __float2ull_rn(part[k] * w.unit);
+      if (__any_sync(0xffffffffu, waiting > kQueue - kVec)) work_off();
     });
     work_off();
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (k > intervals) break;
+    for (int k = 0; k < 3; ++k) {
       // (5.25e-8 is 451 / 2^33)
-      uint64_t m = mass[k] + light[k] + (light[k] >> 20) * 451 / 8192;
-      if (k < 3) m -= mass[k + 1] + light[k + 1] + (light[k + 1] >> 20) * 451 / 8192;
-      m = warp_sum(m);
+      const uint64_t m = warp_sum(mass[k] + light[k] + (light[k] >> 20) * 451 / 8192);
       if ((threadIdx.x & 31) == 0 && m) atomicAdd(&head->segment[k], static_cast<unsigned long long>(m));
+    }
+    if (round == 0) {  // what this CTA has collected goes to the first one
+      __syncthreads();
+      const uint32_t n = s.taken;
+      if (threadIdx.x == 0 && n > 0) s.place = atomicAdd(&head->collected, n);
+      __syncthreads();
+      for (uint32_t i = threadIdx.x; i < min(n, static_cast<uint32_t>(kCollect)); i += kThreads)
+        if (s.place + i < kCollect) head->list[s.place + i] = s.weights[i];
     }
     cluster.sync();
     if (round == 0) {
       collected = head->collected;
-      if (collected > kCollect) {
-        cluster.sync();  // (the first CTA's memory has been read)
-        break;
+      const int n = static_cast<int>(collected);
+      const bool many = n > kCollect, few = !many && n * n <= kThreads * kThreads * kCtas;
+      if (few || (rank == 0 && !many)) {
+        for (int i = threadIdx.x; i < n; i += kThreads) s.unsorted[i] = head->list[i];
+        __syncthreads();
       }
+      if (few) rank_share<kCtas>(s, head, w, n, rank);
+      else if (rank == 0 && !many) sort_many(s, w, n);
+      cluster.sync();  // (and the first CTA's memory has been read)
+      if (many) break;
     }
     if (rank == 0) {
       if (round == 0) {
-        for (uint32_t i = threadIdx.x; i < collected; i += kThreads) s.unsorted[i] = s.list[i];
+        for (uint32_t i = threadIdx.x; i < collected; i += kThreads) s.list[i] = s.sorted[i];
         __syncthreads();
-        sort_list(s, static_cast<int>(collected));
       }
       const int left = finish(P, s, r, w, per_place, row, static_cast<int>(collected), round > 0);
       if (threadIdx.x == 0) s.unsure = left;
-      if (left && threadIdx.x < 4) s.segment[threadIdx.x] = 0;
+      if (left && threadIdx.x < 3) s.segment[threadIdx.x] = 0;
     }
     cluster.sync();
     const int left = head->unsure;

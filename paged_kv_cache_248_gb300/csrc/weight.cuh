@@ -60,9 +60,11 @@ __device__ __forceinline__ uint64_t part_of_up(uint64_t mass, float share) {
 
 struct Weight {
   float top, ch, cl;  // the largest logit; log2(e) / T in two parts
+  float unit;         // a weight of 1 as a whole number
   int shift;
 
   __device__ __forceinline__ Weight(float top_, float temperature, int shift_) : top(top_), shift(shift_) {
+    unit = __int_as_float((127 + kWeightBits - shift) << 23);
     constexpr float kHigh = 1.44269502162933349609375f, kLow = 1.925963033500e-8f;  // log2(e)
     ch = kHigh / temperature;
     if (!(ch < 1e30f)) {  // (a temperature next to zero: only the largest logit has a weight)
@@ -101,14 +103,12 @@ struct Weight {
     return share >= 1.f ? uint64_t(1) << (kWeightBits - shift) : part_of_up(uint64_t(1) << (kWeightBits - shift), share);
   }
 
-  // The same in fp32, right to 2^-20 of itself.
+  // The weight in fp32, a part of 1 (of what is no candidate: anything).
   __device__ __forceinline__ float rounded(float x) const {
     const float d = x - top, yh = d * ch, yl = fmaf(d, cl, fmaf(d, ch, -yh));
     float w;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(yh));
-    w *= __int_as_float((127 + kWeightBits - shift) << 23);
-    const float full = fmaf(w * 0.6931472f, yl, w);
-    return yh > -64.f ? full : 0.f;  // (an infinite d among it)
+    return fmaf(w * 0.6931472f, yl, w);
   }
 
   // log(w / mass)
