@@ -58,8 +58,7 @@ struct Params {
 
 // What the counts tell: up to three disjoint intervals of bins that are collected.
 struct Plan {
-  int32_t count;             // intervals
-  int32_t begin[3], end[3];  // bins [begin, end]
+  int32_t begin[3], end[3];  // bins [begin, end], kBins where there are fewer
   int32_t last;              // bins behind it are ignored
   int32_t exact;             // weights of the bins before are exact
   int32_t rank[3];           // candidate number e of the list, in interval j, is number rank[j] + e of the row
@@ -68,7 +67,11 @@ struct Plan {
 struct Shared {
   uint32_t bins[kBins], places[kBins];  // of this CTA: candidates, and the sum of their places in the bin
   uint32_t all[kBins];                  // of the row: candidates, and the mean of their places
-  float mean[kBins];
+  union {
+    float mean[kBins];
+    int32_t base[kBins];  // (after the plan) where the list has a collected bin's candidates
+  };
+  uint32_t cursor[kBins];  // (first CTA) of a bin's candidates, those that have a place in the list
   uint64_t list[kCollect], weights[kCollect];  // (first CTA) keys, at last in order, and their weights
   union {
     float queue[kQueue][kThreads];
@@ -85,7 +88,7 @@ struct Shared {
   int32_t found[8];
   float warp_sq[kWarps], bound[3];
   uint32_t collected, best;  // (first CTA) of the list; the first of the largest logits
-  uint32_t taken, place;     // candidates that this CTA collected (in `weights`), their place in the list
+  uint32_t taken;            // candidates that this CTA collected (in `weights`)
   int32_t unsure;            // (first CTA) the borders need exact sums
   Plan plan;
   unsigned long long sum[2], low, high;  // of a pass of the bisection
@@ -140,16 +143,31 @@ __device__ __forceinline__ void each_raw(const Params& P, int64_t row, int first
     c = d;
   }
 }
+template <typename T>
+__device__ __forceinline__ void unpack_piece(const uint4& raw, float (&x)[16 / sizeof(T)]) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int e = 0; e < 16 / static_cast<int>(sizeof(T)); ++e)
+    x[e] = __uint_as_float(sizeof(T) == 4 ? w[e % 4] : e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+}
+// The largest logit of a piece (NaN is passed over).
+template <typename T>
+__device__ __forceinline__ float piece_largest(const uint4& raw) {
+  if constexpr (sizeof(T) == 4) {
+    return fmaxf(fmaxf(__uint_as_float(raw.x), __uint_as_float(raw.y)), fmaxf(__uint_as_float(raw.z), __uint_as_float(raw.w)));
+  } else {
+    const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&raw);
+    const __nv_bfloat162 y = __hmax2(__hmax2(x[0], x[1]), __hmax2(x[2], x[3]));
+    return fmaxf(__low2float(y), __high2float(y));
+  }
+}
 // The same with their logits x[].
 template <typename T, typename F>
 __device__ __forceinline__ void each_piece(const Params& P, int64_t row, int first, int step, F&& f) {
   constexpr int kVec = 16 / sizeof(T);
   each_raw<T>(P, row, first, step, [&](const uint4& raw, int i0) {
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     float x[kVec];
-#pragma unroll
-    for (int e = 0; e < kVec; ++e)
-      x[e] = __uint_as_float(sizeof(T) == 4 ? w[e % 4] : e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+    unpack_piece<T>(raw, x);
     f(x, i0);
   });
 }
@@ -161,6 +179,13 @@ __device__ __forceinline__ void each(const Params& P, int64_t row, int first, in
 #pragma unroll
     for (int e = 0; e < kVec; ++e) f(x[e], i0 + e);
   });
+}
+
+// Adds to a word of shared memory.
+__device__ __forceinline__ void add_if(bool really, uint32_t addr, uint32_t x) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p red.shared.add.u32 [%1], %2;\n\t}" ::"r"(really ? 1u : 0u),
+               "r"(addr), "r"(x)
+               : "memory");
 }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
@@ -335,65 +360,74 @@ __device__ __forceinline__ void make_plan(Shared& s, const Row& r, float per_uni
   first_over(3, mass, r.u * z_lo * kLow - rest);
   first_over(4, mass, r.u * z_hi * kHigh);
   __syncthreads();
-  if (threadIdx.x == 0) {
-    const int a3 = min(s.found[3], e2), e3 = min(s.found[4], e2);
-    // three windows in order of their beginnings, joined where they meet
-    int a[3] = {a3, cut_p ? a2 : kBins, cut1 ? a1 : kBins}, e[3] = {max(a3, e3), max(a2, e2), max(a1, e1)};
+  // three windows in order of their beginnings, joined where they meet (kBins: none)
+  const int a3 = min(s.found[3], e2), e3 = min(s.found[4], e2), exact = s.found[5] + 1;
+  int a[3] = {a3, cut_p ? a2 : kBins, cut1 ? a1 : kBins}, e[3] = {max(a3, e3), max(a2, e2), max(a1, e1)};
+  __syncthreads();  // (`found` has been read)
+  const auto swap = [&](int x, int y, bool really) {
+    const int u = really ? a[y] : a[x], v = really ? e[y] : e[x];
+    a[y] = really ? a[x] : a[y], e[y] = really ? e[x] : e[y];
+    a[x] = u, e[x] = v;
+  };
+  swap(0, 1, a[1] < a[0]);
+  swap(1, 2, a[2] < a[1]);
+  swap(0, 1, a[1] < a[0]);
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const int x = i == 1 ? 1 : 0;  // places 0 and 1, 1 and 2, 0 and 1
-      if (a[x + 1] < a[x]) {
-        const int y = a[x], z = e[x];
-        a[x] = a[x + 1], e[x] = e[x + 1];
-        a[x + 1] = y, e[x + 1] = z;
-      }
+  for (int i = 0; i < 2; ++i) {  // (what a window takes up is moved to the end)
+#pragma unroll
+    for (int k = 0; k < 2 - i; ++k) {
+      const bool meet = a[i + 1] < kBins && a[i + 1] <= e[i] + 1;
+      e[i] = meet ? max(e[i], e[i + 1]) : e[i];
+      a[i + 1] = meet ? kBins : a[i + 1];
+      if (i == 0) swap(1, 2, a[2] < a[1]);
     }
-    int m = 0;
-#pragma unroll 1
-    for (int i = 0; i < 3; ++i) {
-      const int from = i == 0 ? a[0] : i == 1 ? a[1] : a[2], to = i == 0 ? e[0] : i == 1 ? e[1] : e[2];
-      if (from >= kBins) continue;
-      if (m > 0 && from <= s.plan.end[m - 1] + 1) {
-        s.plan.end[m - 1] = max(s.plan.end[m - 1], to);
-      } else {
-        s.plan.begin[m] = from;
-        s.plan.end[m++] = to;
-      }
-    }
-    s.plan.count = m;
-#pragma unroll 1
-    for (int i = m; i < 3; ++i) s.plan.begin[i] = s.plan.end[i] = kBins;
-    s.plan.last = cut1 ? e1 : kBins - 1;
-    s.plan.exact = s.found[5] + 1;
   }
-  __syncthreads();
-  const Plan p = s.plan;
+#pragma unroll
+  for (int j = 0; j < 3; ++j) e[j] = a[j] < kBins ? e[j] : kBins;
   // candidates before an interval, and up to its end
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int b = b0 + k;
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
-      if (p.begin[j] == b) s.found[j] = static_cast<int32_t>(n[k] - here[k]);
-      if (p.end[j] == b) s.found[5 + j] = static_cast<int32_t>(n[k]);
+      if (a[j] == b0 + k) s.found[j] = static_cast<int32_t>(n[k] - here[k]);
+      if (e[j] == b0 + k) s.found[5 + j] = static_cast<int32_t>(n[k]);
     }
   }
   __syncthreads();
+  int rank[3], collected = 0;
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    rank[j] = s.found[j] - collected;
+    collected += a[j] < kBins ? s.found[5 + j] - s.found[j] : 0;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int b = b0 + k;
+    s.base[b] = static_cast<int32_t>(n[k] - here[k]) - (b >= a[2] ? rank[2] : b >= a[1] ? rank[1] : rank[0]);
+  }
   if (threadIdx.x == 0) {
-    int collected = 0;
-#pragma unroll 1
-    for (int j = 0; j < p.count; ++j) {
-      s.plan.rank[j] = s.found[j] - collected;
-      collected += s.found[5 + j] - s.found[j];
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      s.plan.begin[j] = a[j];
+      s.plan.end[j] = e[j];
+      s.plan.rank[j] = rank[j];
     }
+    s.plan.last = cut1 ? e1 : kBins - 1;
+    s.plan.exact = exact;
   }
   __syncthreads();
 }
 
-// Sorts the n keys of `unsorted` into the first CTA's `sorted`, with their weights: each key's place is the number of smaller
-// ones, which the lanes of a group count together.  Every CTA of the cluster takes a share of them.
+// The bin of a place.
+__device__ __forceinline__ int bin_of(float y) {
+  return __float_as_uint(__fadd_rd(fminf(y, (kBins - 1) * 2048.f), 8388608.f)) >> 11 & (kBins - 1);
+}
+
+// Sorts the n keys of `unsorted`, which are in order of their bins, into the first CTA's `sorted`, with their weights: each
+// key's place is the number of smaller ones of its bin behind the bin's first, which the lanes of a group count
+// together.  Every CTA of the cluster takes a share of them.
 template <int kCtas>
-__device__ __forceinline__ void rank_share(Shared& s, Shared* head, const Weight& w, int n, int rank) {
+__device__ __forceinline__ void rank_share(Shared& s, Shared* head, const Weight& w, float per_place, int n, int rank) {
   const int e0 = n * rank / kCtas, e1 = n * (rank + 1) / kCtas;
   int group = 1;
   while (group < 32 && (e1 - e0) * group * 2 <= kThreads) group <<= 1;
@@ -402,14 +436,18 @@ __device__ __forceinline__ void rank_share(Shared& s, Shared* head, const Weight
   for (int first = e0; first < e1; first += kThreads / group) {
     const int e = first + static_cast<int>(threadIdx.x) / group;
     const uint64_t mine = s.unsorted[min(e, e1 - 1)];
+    const float x = logit_of(mine);
+    const int bin = bin_of((w.top - x) * per_place), begin = s.base[bin];
+    const int end = bin == kBins - 1 ? n : begin + static_cast<int>(s.all[bin]);  // (the last bin's are not counted)
     int place = 0;
 #pragma unroll 4
-    for (int i = at; i < n; i += group) place += s.unsorted[i] < mine;
+    for (int i = begin + at; i < end; i += group) place += s.unsorted[i] < mine;
+    __syncwarp();
 #pragma unroll 1
     for (int d = group >> 1; d; d >>= 1) place += __shfl_xor_sync(0xffffffffu, place, d);
     if (e < e1 && at == 0) {
-      head->sorted[place] = mine;
-      head->weights[place] = w.of(logit_of(mine), s.table);
+      head->sorted[begin + place] = mine;
+      head->weights[begin + place] = w.of(x, s.table);
     }
   }
 }
@@ -455,8 +493,7 @@ __device__ __forceinline__ int finish(const Params& P, Shared& s, const Row& r, 
   const uint64_t seg0 = s.segment[0], seg1 = seg0 + s.segment[1], segs = seg1 + s.segment[2], seg2 = segs;
   // a candidate's interval, from its bin
   const auto interval = [&](int e) {
-    const float y = fminf((w.top - logit_of(s.list[e])) * per_place, (kBins - 1) * 2048.f);
-    const int b = __float_as_uint(__fadd_rd(y, 8388608.f)) >> 11 & (kBins - 1);
+    const int b = bin_of((w.top - logit_of(s.list[e])) * per_place);
     return (b >= p.begin[1]) + (b >= p.begin[2]);
   };
   const auto rank_of = [&](int e, int j) { return static_cast<uint32_t>((j == 0 ? p.rank[0] : j == 1 ? p.rank[1] : p.rank[2]) + e); };
@@ -619,7 +656,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
   const int64_t row = blockIdx.x / kCtas;
   const int first = rank * kThreads + threadIdx.x, step = kCtas * kThreads;
   if (threadIdx.x < 256) s.table[threadIdx.x] = kPowers.v[threadIdx.x];
-  for (int b = threadIdx.x; b < kBins; b += kThreads) s.bins[b] = s.places[b] = 0;
+  for (int b = threadIdx.x; b < kBins; b += kThreads) s.bins[b] = s.places[b] = s.cursor[b] = 0;
   if (threadIdx.x < 3) s.segment[threadIdx.x] = 0;
   if (threadIdx.x == 4) s.collected = s.taken = 0;
   if (threadIdx.x == 5) s.best = 0x7fffffffu;
@@ -717,42 +754,44 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
   // A place in the bins in units of 1/2048, behind the binary point of 2^23: bin and place are its bits.
   const float per_place = fminf(w.ch * per_unit, 1e30f) * 2048.f;
   constexpr float kEnd = (kBins - 1) * 2048.f;
-  // How many fall into each bin, and where, to 1/32 of it: both in one word while there are few (14 bits and 18), two arrays
-  // of them in turn; a thread keeps the sums of four bins.
+  // How many fall into each bin, and where, to 1/32 of it: both in one word while there are few (upper 14 bits and lower 18), two
+  // arrays of them in turn; a thread keeps the sums of four bins.
   {
     static_assert(kPerThread == 4, "a thread's bins are a vector");
     constexpr int kVec = 16 / sizeof(T), kPieces = 16 / kVec;
     static_assert(16 * kThreads < (1 << 14) && 31 * 16 * kThreads < (1 << 18), "the fields of a word");
-    uint32_t* into = s.bins;
+    uint32_t into = smem_u32(s.bins);
+    const float per_part = per_place * (1.f / 64.f);
     uint32_t n[4] = {0, 0, 0, 0}, place[4] = {0, 0, 0, 0};
     int pieces = 0;
-    const auto take_over = [&](uint32_t* of) {
+    const auto take_over = [&]() {
+      uint32_t* of = into == smem_u32(s.bins) ? s.bins : s.places;
       const uint4 x = reinterpret_cast<const uint4*>(of)[threadIdx.x];
       const uint32_t y[4] = {x.x, x.y, x.z, x.w};
       reinterpret_cast<uint4*>(of)[threadIdx.x] = make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        n[k] += y[k] & 0x3fffu;
-        place[k] += y[k] >> 14;
+        n[k] += y[k] >> 18;
+        place[k] += y[k] & 0x3ffffu;
       }
     };
     each_piece<T>(P, row, first, step, [&](const float (&x)[kVec], int) {
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
-        const float y = (top - x[e]) * per_place;
-        if (!(fabsf(y) < kEnd)) continue;  // (the last bin's, and what is no candidate)
+        const float y = (top - x[e]) * per_part;
         const uint32_t at = __float_as_uint(__fadd_rd(y, 8388608.f));
-        atomicAdd(&into[at >> 11 & (kBins - 1)], ((at & 0x7c0u) << 8) + 1u);
+        // (not the last bin's, nor what is no candidate)
+        add_if(fabsf(y) < kEnd / 64.f, into + (at >> 3 & 4 * (kBins - 1)), (at & 31u) | 0x40000u);
       }
       if (++pieces == kPieces) {
         pieces = 0;
         __syncthreads();
-        take_over(into);
-        into = into == s.bins ? s.places : s.bins;
+        take_over();
+        into ^= smem_u32(s.bins) ^ smem_u32(s.places);
       }
     });
     __syncthreads();
-    take_over(into);
+    take_over();
     reinterpret_cast<uint4*>(s.bins)[threadIdx.x] = make_uint4(n[0], n[1], n[2], n[3]);
     reinterpret_cast<uint4*>(s.places)[threadIdx.x] = make_uint4(place[0], place[1], place[2], place[3]);
   }
@@ -781,6 +820,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
   // third interval nothing counts: that there are three takes a filter that ends all.)
   const Plan& plan = s.plan;
   const float behind = plan.last == kBins - 1 ? INFINITY : (plan.last + 1) * 2048.f;
+  // the least logit that can count, and less (of bf16 pieces the largest logit tells whether one does)
+  const float least = fmaxf(top - behind / per_place * 1.00001f - fabsf(top) * 1e-6f, -3.4028235e38f);
   float from[3], upto[3];  // the intervals' places
 #pragma unroll
   for (int j = 0; j < 3; ++j) {
@@ -809,25 +850,31 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
         }
       }
     };
-    each_piece<T>(P, row, first, step, [&](const float (&x)[kVec], int i0) {
+    each_raw<T>(P, row, first, step, [&](const uint4& raw, int i0) {
+      if (!__any_sync(0xffffffffu, piece_largest<T>(raw) >= least)) return;
+      float x[kVec];
+      unpack_piece<T>(raw, x);
       float part[3] = {0.f, 0.f, 0.f};
-      uint32_t apart = 0;  // neither summed up here nor ignored
+      uint32_t apart = 0;  // not summed up here
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        const float y = (top - x[e]) * per_place;
-        if (!(y < behind)) continue;  // (nor what is no candidate, but for an infinity)
-        const float m = w.rounded(x[e]);
-        const bool p0 = y >= lo[0] && y < hi[0], p1 = y >= lo[1] && y < hi[1], p2 = third && y >= lo[2] && y < hi[2];
-        if (p0) part[0] += m;
-        if (p1) part[1] += m;
-        if (p2) part[2] += m;
-        if (!(p0 || p1 || p2)) apart |= 1u << e;
+      for (int e = 0; e < kVec; e += 2) {
+        const Two d = add2(two(x[e], x[e + 1]), two(-top));
+        const float2 y2 = both(mul2(d, two(-per_place))), m2 = both(w.rounded(d));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float y = h ? y2.y : y2.x, m = h ? m2.y : m2.x;
+          const bool p0 = y >= lo[0] && y < hi[0], p1 = y >= lo[1] && y < hi[1], p2 = third && y >= lo[2] && y < hi[2];
+          if (p0) part[0] += m;
+          if (p1) part[1] += m;
+          if (p2) part[2] += m;
+          if (!(p0 || p1 || p2)) apart |= 1u << (e + h);
+        }
       }
       if (apart) {
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
-          if (!(apart >> e & 1) || !candidate(x[e])) continue;
           const float y = (top - x[e]) * per_place;
+          if (!(apart >> e & 1) || !(y < behind) || !candidate(x[e])) continue;
           if ((y >= from[0] && y < upto[0]) || (y >= from[1] && y < upto[1]) || (y >= from[2] && y < upto[2])) {
             if (round == 0) {
               const uint32_t place = atomicAdd(&s.taken, 1u);
@@ -849,13 +896,16 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
       const uint64_t m = warp_sum(mass[k] + light[k] + (light[k] >> 20) * 451 / 8192);
       if ((threadIdx.x & 31) == 0 && m) atomicAdd(&head->segment[k], static_cast<unsigned long long>(m));
     }
-    if (round == 0) {  // what this CTA has collected goes to the first one
+    if (round == 0) {  // what this CTA has collected goes to the first one, in order of the bins
       __syncthreads();
       const uint32_t n = s.taken;
-      if (threadIdx.x == 0 && n > 0) s.place = atomicAdd(&head->collected, n);
-      __syncthreads();
-      for (uint32_t i = threadIdx.x; i < min(n, static_cast<uint32_t>(kCollect)); i += kThreads)
-        if (s.place + i < kCollect) head->list[s.place + i] = s.weights[i];
+      if (threadIdx.x == 0 && n > 0) atomicAdd(&head->collected, n);
+      for (uint32_t i = threadIdx.x; i < min(n, static_cast<uint32_t>(kCollect)); i += kThreads) {
+        const uint64_t key = s.weights[i];
+        const int bin = bin_of((top - logit_of(key)) * per_place);
+        const uint32_t place = s.base[bin] + atomicAdd(&head->cursor[bin], 1u);
+        if (place < kCollect) head->list[place] = key;
+      }
     }
     cluster.sync();
     if (round == 0) {
@@ -866,7 +916,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
         for (int i = threadIdx.x; i < n; i += kThreads) s.unsorted[i] = head->list[i];
         __syncthreads();
       }
-      if (few) rank_share<kCtas>(s, head, w, n, rank);
+      if (few) rank_share<kCtas>(s, head, w, per_place, n, rank);
       else if (rank == 0 && !many) sort_many(s, w, n);
       cluster.sync();  // (and the first CTA's memory has been read)
       if (many) break;

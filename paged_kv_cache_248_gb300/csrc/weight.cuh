@@ -8,6 +8,8 @@
 #pragma once
 #include <cstdint>
 
+#include "ptx.cuh"
+
 namespace pkv {
 
 constexpr int kWeightBits = 46;  // of the table
@@ -103,12 +105,12 @@ struct Weight {
     return share >= 1.f ? uint64_t(1) << (kWeightBits - shift) : part_of_up(uint64_t(1) << (kWeightBits - shift), share);
   }
 
-  // The weight in fp32, a part of 1 (of what is no candidate: anything).
-  __device__ __forceinline__ float rounded(float x) const {
-    const float d = x - top, yh = d * ch, yl = fmaf(d, cl, fmaf(d, ch, -yh));
-    float w;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(yh));
-    return fmaf(w * 0.6931472f, yl, w);
+  // Two weights in fp32, parts of 1, of d = x - max (of what is no candidate: anything).
+  __device__ __forceinline__ Two rounded(Two d) const {
+    const Two minus_yh = mul2(d, two(-ch)), yl = fma2(d, two(cl), fma2(d, two(ch), minus_yh));
+    const float2 y = both(minus_yh);
+    const Two m = two(ex2_approx(-y.x), ex2_approx(-y.y));
+    return fma2(mul2(m, two(0.6931472f)), yl, m);
   }
 
   // log(w / mass)
