@@ -112,6 +112,7 @@ __device__ __forceinline__ uint4 load_piece(const T* p, int i0, int vocab) {
   constexpr int kVec = 16 / sizeof(T);
   if (i0 >= 0 && i0 + kVec <= vocab) return __ldg(reinterpret_cast<const uint4*>(p + i0));
   uint32_t w[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+  if (i0 >= vocab) return make_uint4(w[0], w[1], w[2], w[3]);
 #pragma unroll
   for (int e = 0; e < kVec; ++e) {
     if (i0 + e < 0 || i0 + e >= vocab) continue;
