@@ -261,9 +261,10 @@ __device__ __forceinline__ void make_plan(Shared& s, const Row& r, float per_uni
   float mass[4], sq[4];  // (and the squares of the bins' masses)
   uint32_t counted = 0;
   float weighed = 0.f, squares = 0.f;
+  const float unit = 1.f / per_unit;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float m = here[k] * exp2f(-(static_cast<float>(b0 + k) + mean[k]) / per_unit);
+    const float m = here[k] * ex2_approx(-(static_cast<float>(b0 + k) + mean[k]) * unit);
     weighed += m;
     squares = fmaf(m, m, squares);
     counted += here[k];
@@ -290,18 +291,29 @@ __device__ __forceinline__ void make_plan(Shared& s, const Row& r, float per_uni
   }
   if (threadIdx.x < 8) s.found[threadIdx.x] = kBins - 1;
   __syncthreads();
-  uint32_t bn = in - counted;
-  float bm = im - weighed, bs = is - squares, all = 0.f, all_sq = 0.f;
-#pragma unroll 1
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) {
-      bn += s.warp_n[w];
-      bm += s.warp_mass[w];
-      bs += s.warp_sq[w];
+  // (the warps' sums: lane w has those up to warp w)
+  uint32_t wn = lane < kWarps ? s.warp_n[lane] : 0;
+  float wm = lane < kWarps ? s.warp_mass[lane] : 0.f, ws = lane < kWarps ? s.warp_sq[lane] : 0.f;
+#pragma unroll
+  for (int d = 1; d < kWarps; d <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, wn, d);
+    const float z = __shfl_up_sync(0xffffffffu, wm, d), x = __shfl_up_sync(0xffffffffu, ws, d);
+    if (lane >= d) {
+      wn += y;
+      wm += z;
+      ws += x;
     }
-    all += s.warp_mass[w];
-    all_sq += s.warp_sq[w];
   }
+  const float all = __shfl_sync(0xffffffffu, wm, kWarps - 1), all_sq = __shfl_sync(0xffffffffu, ws, kWarps - 1);
+  uint32_t bn = __shfl_sync(0xffffffffu, wn, max(warp - 1, 0));
+  float bm = __shfl_sync(0xffffffffu, wm, max(warp - 1, 0)), bs = __shfl_sync(0xffffffffu, ws, max(warp - 1, 0));
+  if (warp == 0) {
+    bn = 0;
+    bm = bs = 0.f;
+  }
+  bn += in - counted;
+  bm += im - weighed;
+  bs += is - squares;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     n[k] += bn;
@@ -356,7 +368,7 @@ __device__ __forceinline__ void make_plan(Shared& s, const Row& r, float per_uni
     a2 = min(s.found[1], e1);
     e2 = min(s.found[2], e1);
     z_lo *= r.top_p;
-    z_hi = fminf(z_hi, r.top_p * z_hi + kHigh * exp2f(-static_cast<float>(a2) / per_unit));
+    z_hi = fminf(z_hi, r.top_p * z_hi + kHigh * ex2_approx(-static_cast<float>(a2) * unit));
   }
   first_over(3, mass, r.u * z_lo * kLow - rest);
   first_over(4, mass, r.u * z_hi * kHigh);
@@ -438,8 +450,9 @@ __device__ __forceinline__ void rank_share(Shared& s, Shared* head, const Weight
     const int e = first + static_cast<int>(threadIdx.x) / group;
     const uint64_t mine = s.unsorted[min(e, e1 - 1)];
     const float x = logit_of(mine);
-    const int bin = bin_of((w.top - x) * per_place), begin = s.base[bin];
-    const int end = bin == kBins - 1 ? n : begin + static_cast<int>(s.all[bin]);  // (the last bin's are not counted)
+    // (the last bin's are not counted; bounds, so that logits which are written meanwhile cannot lead out of the list)
+    const int bin = bin_of((w.top - x) * per_place), begin = min(max(s.base[bin], 0), n - 1);
+    const int end = bin == kBins - 1 ? n : min(begin + static_cast<int>(min(s.all[bin], 1u << 20)), n);
     int place = 0;
 #pragma unroll 4
     for (int i = begin + at; i < end; i += group) place += s.unsorted[i] < mine;
@@ -447,8 +460,9 @@ __device__ __forceinline__ void rank_share(Shared& s, Shared* head, const Weight
 #pragma unroll 1
     for (int d = group >> 1; d; d >>= 1) place += __shfl_xor_sync(0xffffffffu, place, d);
     if (e < e1 && at == 0) {
-      head->sorted[begin + place] = mine;
-      head->weights[begin + place] = w.of(x, s.table);
+      const int to = min(begin + place, n - 1);
+      head->sorted[to] = mine;
+      head->weights[to] = w.of(x, s.table);
     }
   }
 }
