@@ -16,8 +16,8 @@
 // rounded up to a power of two).  A unit (q8_units.cuh) is (request, kv head, up to two row tiles), whose key tiles are
 // loaded and converted once.
 //
-// Per CTA (448 threads): warp 0 walks the run, warp 1 issues the MMAs, warps 2-5 and 6-9 are the softmax of a row tile each
-// (a thread a row; P stays in tensor memory, over S), warps 10-13 load codes from the cache, 16 bytes a lane and a tile
+// Per CTA (448 threads): warp 0 walks the run, warp 1 issues the MMAs,
+// warps 2-5 and 6-9 are the softmax of a row tile each (a thread a row; P stays in tensor memory, over S), warps 10-13 load codes from the cache, 16 bytes a lane and a tile
 // ahead in registers, convert them and put them into the K and V rings (two tiles each, 128-byte swizzle).
 // V rows behind the context are zero; in a tile that not every row sees whole, NaN codes of V are taken out and
 // told to the softmax, which makes the rows that see them NaN.  All waits are bounded.
@@ -44,7 +44,7 @@ struct TileInfo {
 
 struct Ctl {
   uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
-  uint64_t s_full[2], o_full[2], o_free[2], p_full[2][2], q_full[2];
+  uint64_t s_full[2], o_full[2], o_free[2], p_full[2], q_full[2];
   uint64_t item_full[kItemRing], item_empty[kItemRing];
   uint64_t drain;
   Item ring[kItemRing];
@@ -255,9 +255,10 @@ __device__ constexpr uint32_t idesc_f16(bool b_mn) {
   return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// One elected thread issues every MMA, but the whole warp walks through the tiles.  A row tile's step is P V of its key
-// tile before, then S of its next one: MMAs of one thread complete in order, so S cannot overwrite the P that this P V
-// reads, and S being complete tells the softmax that O holds every tile before.
+// One elected thread issues every MMA, but the whole warp walks through the tiles, the row tiles in turn: one's products are
+// made while the other's weights are.  A row tile's step is P V of its key tile before, then S of its next one: MMAs of
+// one thread complete in order, so S cannot overwrite the P that this P V reads, and S being complete tells the softmax that O
+// holds every tile before.
 struct Issuer {
   Ctl& c;
   uint32_t tmem, q, k, v;  // shared-memory addresses of the Q tiles and the rings
@@ -271,37 +272,34 @@ struct Issuer {
   __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) { failed |= !wait_for(bar, parity, abort_flag); }
   __device__ __forceinline__ bool ok() { return !__any_sync(0xffffffffu, failed); }
 
-  // O_w += P_w V of the tile in V slot `slot`; `first` begins O_w anew, `last` reports it.
-  __device__ __forceinline__ void pv(int w, uint32_t slot, uint32_t parity, bool first, bool last) {
+  // O_w += P_w V of tile number n; `first` begins O_w anew, `last` reports it, `frees`: V has been read.
+  __device__ __forceinline__ void pv(int w, uint32_t n, bool first, bool last, bool frees) {
+    const uint32_t slot = n & 1, s_col = tmem + 128 * w;
     const uint64_t b = umma_smem_desc(v + slot * kTileBytes, kHalfBytes, 1024, kLayout128B);
-    const uint32_t s_col = tmem + 128 * w;
-    wait(&c.vfull[slot], parity);
-    wait(&c.p_full[w][0], p_phase >> w & 1);
+    wait(&c.vfull[slot], n >> 1 & 1);
     if (first) {
       wait(&c.o_free[w], (o_phase >> w & 1) ^ 1);
       o_phase ^= 1u << w;
     }
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      if (hf) wait(&c.p_full[w][1], p_phase >> w & 1);
-      tc_fence_after();
-      if (elected()) {
-#pragma unroll
-        for (int k4 = 0; k4 < 4; ++k4)
-          umma_f16_ts(s_col + kOCol, s_col + 32 * hf + 8 * k4, umma_desc_advance(b, (4 * hf + k4) * 2048), idesc_f16(true),
-                      (!first || hf + k4 > 0) ? 1u : 0u);
-        if (hf && last) umma_commit(&c.o_full[w]);
-      }
-    }
+    wait(&c.p_full[w], p_phase >> w & 1);
     p_phase ^= 1u << w;
+    tc_fence_after();
+    if (elected()) {
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        umma_f16_ts(s_col + kOCol, s_col + 8 * kk, umma_desc_advance(b, kk * 2048), idesc_f16(true), (!first || kk > 0) ? 1u : 0u);
+      if (frees) umma_commit(&c.vempty[slot]);
+      if (last) umma_commit(&c.o_full[w]);
+    }
   }
 
-  // S_w = Q_w K^T of the tile in K slot `slot`, whose turn's parity is given.
-  __device__ __forceinline__ void s(int w, uint32_t slot, uint32_t parity) {
-    wait(&c.kfull[slot], parity);
-    tc_fence_after();
+  // S_w = Q_w K^T of tile number n; `frees`: K has been read.
+  __device__ __forceinline__ void s(int w, uint32_t n, bool frees) {
+    const uint32_t slot = n & 1;
     const uint64_t a = umma_smem_desc(q + w * kTileBytes, 16, 1024, kLayout128B);
     const uint64_t b = umma_smem_desc(k + slot * kTileBytes, 16, 1024, kLayout128B);
+    wait(&c.kfull[slot], n >> 1 & 1);
+    tc_fence_after();
     if (elected()) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -312,6 +310,7 @@ struct Issuer {
         }
       }
       umma_commit(&c.s_full[w]);
+      if (frees) umma_commit(&c.kempty[slot]);
     }
     issued = true;
   }
@@ -339,14 +338,13 @@ __device__ void mma_warp(const Q8Params& P, Ctl& c, uint8_t* qbuf, uint8_t* kbuf
     __syncwarp();
     if (over) break;
     if (elected()) mbar_arrive(&c.item_empty[slot]);
-    x.q_ready(0);
-    if (rows == 2) x.q_ready(1);
     // turns of the row tiles: 0, 1, 0, 1, ... (one row tile: 0, 0, ...)
     int w = 0;
 #pragma unroll 1
     for (int j = 0; j <= nt && ok;) {
-      if (j > 0) x.pv(w, (n + j - 1) & 1, (n + j - 1) >> 1 & 1, j == 1, j == nt);
-      if (j < nt) x.s(w, (n + j) & 1, (n + j) >> 1 & 1);
+      if (j == 0) x.q_ready(w);
+      if (j > 0) x.pv(w, n + j - 1, j == 1, j == nt, w == rows - 1);
+      if (j < nt) x.s(w, n + j, w == rows - 1);
       ok = x.ok();
       if (++w == rows) {
         w = 0;
@@ -403,25 +401,71 @@ __device__ __forceinline__ float row_largest(uint32_t taddr, const TileInfo& inf
   return top;
 }
 
-// The weights 2^(score * ks + log2 vs - reference) of a row as fp16 over its first 64 columns; returns their sum, each over
-// its vs.  half() hands the first half of them over.
-template <bool kMask, typename Half>
-__device__ __forceinline__ float row_weights(uint32_t taddr, const TileInfo& info, float factor, float ref, int nvis, Half&& half) {
-  float sum = 0.f;
-  uint32_t a[32];
+// Multiplies a row's O, or `pieces` of 32 fp16 weights, by alpha.
+__device__ __forceinline__ void scale_o(uint32_t taddr, float alpha) {
+#pragma unroll 1
+  for (int ch = 0; ch < 8; ++ch) {
+    uint32_t v[16];
+    tmem_ld16_sync(taddr + 16 * ch, v);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+    tmem_st16(taddr + 16 * ch, v);
+  }
+}
+__device__ __forceinline__ void scale_p(uint32_t taddr, int pieces, float alpha) {
+  const __half2 by = __float2half2_rn(alpha);
+#pragma unroll 1
+  for (int ch = 0; ch < pieces; ++ch) {
+    uint32_t v[16];
+    tmem_ld16_sync(taddr + 16 * ch, v);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&v[e]), by);
+      v[e] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+    tmem_st16(taddr + 16 * ch, v);
+  }
+}
+
+// The weights 2^(score * ks + log2 vs - ref) of a row as fp16 over its first 64 columns; `sum` gets them, each over its vs.
+// Where a weight would be more than 2^(kTop + kMost), the row's reference moves by a whole number and what has been
+// summed up, O (where there is one) among it, is rescaled.
+template <bool kMask>
+__device__ __forceinline__ void row_weights(uint32_t taddr, uint32_t orow, bool has_o, const TileInfo& info, float factor, float& ref,
+                                            float& sum, int nvis) {
 #pragma unroll 1
   for (int h = 0; h < 4; ++h) {
     if (kMask && !__any_sync(0xffffffffu, nvis > 32 * h)) {  // (no row of the warp sees more)
       const uint32_t none[16] = {};
       tmem_st16(taddr + 16 * h, none);
-      if (h == 2) half();
       continue;
     }
+    uint32_t a[32];
     tmem_ld32_issue(taddr + 32 * h, a);
     const float k0 = factor * info.ks[2 * h], k1 = factor * info.ks[2 * h + 1];
-    const float m0 = info.lv[2 * h] - ref, m1 = info.lv[2 * h + 1] - ref;
-    if (h == 2) half();
+    float m0 = info.lv[2 * h] - ref, m1 = info.lv[2 * h + 1] - ref;
     tmem_ld32_wait(a);
+    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      float ya, yb;
+      ffma2(ya, yb, __uint_as_float(a[2 * q]), __uint_as_float(a[2 * q + 1]), q < 8 ? k0 : k1, q < 8 ? m0 : m1);
+      if (kMask && 32 * h + 2 * q >= nvis) ya = -INFINITY;
+      if (kMask && 32 * h + 2 * q + 1 >= nvis) yb = -INFINITY;
+      a[2 * q] = __float_as_uint(ya);
+      a[2 * q + 1] = __float_as_uint(yb);
+      top[q & 3] = fmax3(top[q & 3], ya, yb);
+    }
+    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    if (__any_sync(0xffffffffu, most > kTop + kMost)) {  // (rare)
+      const float by = most > kTop + kMost ? ceilf(most - kTop) : 0.f, alpha = exp2f(-by);
+      if (has_o) scale_o(orow, alpha);
+      scale_p(taddr, h, alpha);
+      sum *= alpha;
+      ref += by;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) - by);
+    }
     uint32_t pw[16];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
@@ -429,10 +473,7 @@ __device__ __forceinline__ float row_weights(uint32_t taddr, const TileInfo& inf
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         const int k = 16 * b + 2 * q;
-        float ya, yb;
-        ffma2(ya, yb, __uint_as_float(a[k]), __uint_as_float(a[k + 1]), b ? k1 : k0, b ? m1 : m0);
-        const float pa = ex2_approx(!kMask || 32 * h + k < nvis ? ya : -INFINITY);
-        const float pb = ex2_approx(!kMask || 32 * h + k + 1 < nvis ? yb : -INFINITY);
+        const float pa = ex2_approx(__uint_as_float(a[k])), pb = ex2_approx(__uint_as_float(a[k + 1]));
         if (q & 1) fadd2(ls[2], ls[3], pa, pb);
         else fadd2(ls[0], ls[1], pa, pb);
         const __half2 h2 = __floats2half2_rn(pa, pb);
@@ -442,7 +483,6 @@ __device__ __forceinline__ float row_weights(uint32_t taddr, const TileInfo& inf
     }
     tmem_st16(taddr + 16 * h, pw);
   }
-  return sum;
 }
 
 __device__ void softmax_warps(const Q8Params& P, Ctl& c, uint8_t* qbuf, uint32_t tmem) {
@@ -525,8 +565,6 @@ __device__ void softmax_warps(const Q8Params& P, Ctl& c, uint8_t* qbuf, uint32_t
     const bool none = next == 0;
     const int nq = none ? 0 : tokens_of(P, item.nq, w), j0 = item.j0 + w * (128 >> P.gp_log2);
     const int slot = (next + kItemRing - 1) % kItemRing;  // of this unit
-    // this row tile is the last one to read the unit's key tiles
-    const bool releases = w == 1 || tokens_of(P, item.nq, 1) == 0;
     const bool live = rj < nq && rg < P.group;  // a real (token, head) row
     const bool warp_live = __any_sync(0xffffffffu, live);
     const float factor = next_factor;
@@ -540,44 +578,18 @@ __device__ void softmax_warps(const Q8Params& P, Ctl& c, uint8_t* qbuf, uint32_t
       ok = all(wait_for(&c.s_full[w], tc++ & 1, abort_flag));
       if (!ok) break;
       tc_fence_after();
-      // S of this tile is complete, and with it every MMA issued before: K has been read, and V of the tile before
-      if (r == 0 && releases) {
-        mbar_arrive(&c.kempty[n % kStages]);
-        if (j > 0) mbar_arrive(&c.vempty[(n - 1) % kStages]);
-      }
+      // (S of this tile is complete, and with it every MMA of the row tile that was issued before)
       const TileInfo& info = c.info[n & 3];
-      const auto first_half = [&]() {
-        if (warp_live) tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c.p_full[w][0]);
-      };
       if (warp_live) {
-        const float top = masked ? row_largest<true>(srow, info, factor, nvis) : row_largest<false>(srow, info, factor, kTileKeys);
-        if (j == 0) {
-          ref = top - kTop;
-        } else {
-          const bool need = top > ref + (kTop + kMost);
-          if (__any_sync(0xffffffffu, need)) {
-            const float now = need ? top - kTop : ref;
-            const float alpha = need ? exp2f(ref - now) : 1.f;
-#pragma unroll 1  // rare, and small in the instruction cache
-            for (int ch = 0; ch < 8; ++ch) {
-              uint32_t v[16];
-              tmem_ld16_sync(orow + 16 * ch, v);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-              tmem_st16(orow + 16 * ch, v);
-            }
-            tmem_st_wait();
-            sum *= alpha;
-            ref = now;
-          }
+        // a row's first reference; without one (it has seen nothing yet) all its weights are 0
+        if (__any_sync(0xffffffffu, ref == -INFINITY)) {
+          const float top = masked ? row_largest<true>(srow, info, factor, nvis) : row_largest<false>(srow, info, factor, kTileKeys);
+          if (ref == -INFINITY) ref = top - kTop;
         }
-        // a row that has seen nothing yet: all its weights are 0
-        const float use = ref == -INFINITY ? 0.f : ref;
-        sum += masked ? row_weights<true>(srow, info, factor, use, nvis, first_half)
-                    : row_weights<false>(srow, info, factor, use, kTileKeys, first_half);
+        float use = ref == -INFINITY ? 0.f : ref;
+        if (masked) row_weights<true>(srow, orow, j > 0, info, factor, use, sum, nvis);
+        else row_weights<false>(srow, orow, j > 0, info, factor, use, sum, kTileKeys);
+        if (ref != -INFINITY) ref = use;
         tmem_st_wait();
         if (edge) {
           ok = all(wait_for(&c.vfull[n % kStages], (n / kStages) & 1, abort_flag));
@@ -589,12 +601,10 @@ __device__ void softmax_warps(const Q8Params& P, Ctl& c, uint8_t* qbuf, uint32_t
           }
           if (seen) sum = __int_as_float(0x7fffffff);
         }
-      } else {
-        first_half();  // (no row of this warp is stored: its P may hold anything)
-      }
+      }  // (otherwise no row of this warp is stored: its P may hold anything)
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&c.p_full[w][1]);
+      if (lane == 0) mbar_arrive(&c.p_full[w]);
       if (!ok) break;
     }
     if (!ok) break;
@@ -614,7 +624,6 @@ __device__ void softmax_warps(const Q8Params& P, Ctl& c, uint8_t* qbuf, uint32_t
     ok = all(wait_for(&c.o_full[w], oc++ & 1, abort_flag));
     if (!ok) break;
     tc_fence_after();
-    if (r == 0 && releases) mbar_arrive(&c.vempty[(n - 1) % kStages]);
     const bool bad = *reinterpret_cast<volatile int*>(&c.bad[slot]) != 0;
     const int part = item.slot, row = 128 * w + r;
     // where the row goes: the output, or its partial
@@ -687,8 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_chunk_kernel(const Q8Params P)
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&c.s_full[w], 1);
-      mbar_init(&c.p_full[w][0], 4);
-      mbar_init(&c.p_full[w][1], 4);
+      mbar_init(&c.p_full[w], 4);
       mbar_init(&c.o_full[w], 1);
       mbar_init(&c.o_free[w], 4);
       mbar_init(&c.q_full[w], 4);
