@@ -16,9 +16,10 @@
 // rounded up to a power of two).  A unit (q8_units.cuh) is (request, kv head, up to two row tiles), whose key tiles are
 // loaded and converted once.
 //
-// Per CTA (448 threads): warp 0 walks the run, warp 1 issues the MMAs,
-// warps 2-5 and 6-9 are the softmax of a row tile each (a thread a row; P stays in tensor memory, over S), warps 10-13 load codes from the cache, 16 bytes a lane and a tile
-// ahead in registers, convert them and put them into the K and V rings (two tiles each, 128-byte swizzle).
+// Per CTA (448 threads): warp 0 walks the run, warp 1 issues the MMAs, warps 2-5 and 6-9 are the softmax of a row tile each
+// (a thread a row; P stays in tensor memory, over S), warps 10-13 load codes from the cache, 16 bytes a lane and a tile
+// ahead in registers, convert them and put them into the K and V rings (two tiles each, 128-byte swizzle).  The row tiles
+// take turns: one's products are made while the other's weights are.
 // V rows behind the context are zero; in a tile that not every row sees whole, NaN codes of V are taken out and
 // told to the softmax, which makes the rows that see them NaN.  All waits are bounded.
 #include "q8_units.cuh"

@@ -382,6 +382,58 @@ def test_attention_is_the_same_for_both_types_of_codes(pkv):
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("ctx,new", [([3000], [1]), ([700], [40]), ([0], [300]), ([130, 20], [3, 130])])
+def test_attention_scores_that_grow_with_the_context(pkv, ctx, new):
+    # every row's largest score lies near its end: references move again and again, within a tile too
+    def change(cache, scales, tables, lens, qsl):
+        for row, n in zip(tables, lens):
+            blocks = row[:(n + 15) // 16]
+            at = np.arange(len(blocks) * 16)
+            for s in range(len(at)):
+                cache[0, blocks[s // 16], :, s % 16, 0] = ref.encode8(np.full(1, 16.0))[0]
+            scales[blocks, :, 0] = np.float32(2.0 ** -10) * (1 + np.arange(len(blocks)))[:, None]
+    tables, lens, qsl, pool = ref.requests(ctx, new, 7)
+    cache, scales = ref.pool8(pool, 2, 7)
+    change(cache, scales, tables, lens, qsl)
+    for size in (3.0, 300.0):
+        q = bf16((int(qsl[-1]), 8, 128), 7, 0.1)
+        q[..., 0] = size
+        out = pkv.paged_attention_q8(q.cuda(), *gpu(cache[0], cache[1], scales, tables, lens, qsl), 0.5, max(new), int(lens.max()))
+        want, of = ref.attention(q.double().numpy(), cache[0], cache[1], scales, tables, lens, qsl, 0.5)
+        # a query's elements are held to 2^-22 of its largest one, half of that off at most: a score is off by g = 2^-23 max |q|
+        # sum |K| scale, a weight's share by e^(2 g) (here, with one element 300 times the others, that is more than all else)
+        grain = 2.0 ** -23 * size * 0.5 * (np.abs(ref.decode8(cache[0])).sum(-1).max(-1) * scales[..., 0]).max()
+        assert grain < 0.2
+        assert (np.abs(out.double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -9 + np.expm1(2 * grain)) * of).all()
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-30])
+@pytest.mark.parametrize("new", [[1, 1], [1, 40]])
+def test_attention_scales_of_the_scores(pkv, scale, new):
+    tables, lens, qsl, pool = ref.requests([200, 77], new, 3)
+    cache, scales = ref.pool8(pool, 2, 3)
+    q = bf16((int(qsl[-1]), 6, 128), 3)
+    out = pkv.paged_attention_q8(q.cuda(), *gpu(cache[0], cache[1], scales, tables, lens, qsl), scale, max(new), int(lens.max()))
+    want, of = ref.attention(q.double().numpy(), cache[0], cache[1], scales, tables, lens, qsl, scale)
+    assert (np.abs(out.double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -9 * of).all()
+
+
+def test_attention_units_of_256_tokens(pkv):
+    check_attention(pkv, [10, 0, 300], [700, 256, 257], 1, 1, seed=9)
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1], [1, 30, 5]])
+def test_attention_into_rows_that_are_16_byte_aligned(pkv, new):
+    tables, lens, qsl, pool = ref.requests([20, 0, 140], new, 5)
+    cache, scales = ref.pool8(pool, 2, 5)
+    q = bf16((int(qsl[-1]), 4, 128), 5).cuda()
+    args = gpu(cache[0], cache[1], scales, tables, lens, qsl)
+    want = pkv.paged_attention_q8(q, *args, 0.1, max(new), int(lens.max()))
+    out = torch.full((q.numel() + 16,), 3.0, device="cuda").bfloat16()
+    pkv.paged_attention_q8(q, *args, 0.1, max(new), int(lens.max()), out=out[8:-8].view(q.shape))
+    assert torch.equal(out[8:-8].view(q.shape), want) and (out[:8] == 3).all() and (out[-8:] == 3).all()
+
+
 # ----------------------------------------------------------------------------- sampling
 def check_sample(pkv, x, u, **settings):
     """x fp32 or bf16 [N, V] (CPU), settings as numpy arrays."""
@@ -494,6 +546,39 @@ def test_sample_padded_and_unaligned_rows(pkv, dtype):
     x = peaked(7, 1003, 4).to(dtype).cuda()
     for view in (x[:, :1000], x[:, 1:], x[:, 3:998], x[::2, 5:], x[:1, 1:2]):
         check_sample(pkv, view, np.linspace(0, 0.99, len(view)), top_p=np.full(len(view), 0.9, np.float32))
+
+
+@pytest.mark.parametrize("v,sigma", [(5000, 1.0), (5000, 2.5), (128256, 1.0)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("border", ["uniform", "top_p"])
+def test_sample_numbers_next_to_a_border(pkv, v, sigma, dtype, border):
+    # a share of the weights up to a token, rounded to fp32: 2^-25 from the border at most, and sums have to tell on which side
+    n, rng = 24, np.random.default_rng(v)
+    x = torch.from_numpy(rng.standard_normal((n, v)) * sigma).to(dtype)
+    share, kept = np.zeros(n, np.float32), np.zeros(n, bool)
+    for i, row in enumerate(x.double().numpy()):
+        w = np.cumsum(np.exp(np.sort(row)[::-1] - row.max()))
+        at = w[int(np.searchsorted(w, rng.random() * w[-1]))] / w[-1]
+        share[i] = min(at, 1 - 2.0 ** -20)
+        kept[i] = abs(float(share[i]) - at) > 2.0 ** -29  # (closer ones are 64-bit sums' own rounding)
+    x, share = x[torch.from_numpy(kept)], share[kept]
+    assert len(x) > n // 2
+    if border == "uniform":
+        check_sample(pkv, x, share)
+    else:
+        check_sample(pkv, x, np.full(len(x), 1 - 2.0 ** -24), top_p=share)
+
+
+@pytest.mark.parametrize("n,v", [(100, 30000), (320, 40000)])
+def test_sample_many_rows_of_a_large_vocabulary(pkv, n, v):
+    rng = np.random.default_rng(n)
+    u, p = rng.random(n, dtype=np.float32), np.full(n, 0.8, np.float32)
+    check_sample(pkv, peaked(n, v, n, sigma=1.0).bfloat16(), u, top_p=p)
+    x = torch.zeros((n, v))  # equal logits, two values, a few
+    x[::3, ::2] = 1.0
+    x[1::3] = torch.from_numpy(rng.integers(0, 5, (len(x[1::3]), v))).float()
+    check_sample(pkv, x, u)
+    check_sample(pkv, x.bfloat16(), u, top_p=p)
 
 
 def test_sample_largest_vocabulary(pkv):
