@@ -11,12 +11,15 @@
 // without another rounding (but for codes that leave the normal range).
 //
 // Work.  A row (token, head) is read as 16-byte vectors, two for each of 8 (16) lanes: the two that
-// hold a vector's partners.  With 16- or 32-bit caches a CTA, or a warp, takes a token's rows.  With 8 bits a
-// warp takes the new rows of one (request, block, kv head, K or V): up to 16 rows, 64 values a lane in
-// registers, so that the scale is known before anything is written and no one else writes it.
+// hold a vector's partners.  With 16- or 32-bit caches a CTA, or a warp, takes a token's rows.  With 8 bits the new rows of one
+// (request, block, kv head, K or V) belong to a warp, up to 16 rows, 64 values a lane in registers, or with
+// one token a request to eight lanes: so the scale is known before anything is written and no one else writes it.
 // Request i touches at most ceil((q_i + 15) / 16) blocks, less than floor(qsl[i+1] / 16) -
 // floor(qsl[i] / 16) + 2, so block number x of a launch belongs to the last request with
 // floor(qsl[i] / 16) + 2 i <= x: no plan and no prefix sum.
+//
+// Bound: for few tokens the launch and five loads that depend on one another (one token 2.7 us, 64 tokens 2.6 us, floor 0.2);
+// for many, HBM: 5300 tokens in 8 chunks, 122 MB, 27.4 us (18.2 at the copy's rate; a CTA a token instead of a warp: 33.8).
 #include <cuda_fp8.h>
 
 #include "pkv_internal.cuh"
@@ -26,7 +29,6 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr float kLeastScale = 8.271806125530277e-25f;  // 2^-80
 
 struct Params {
   const void *q, *k, *v;
@@ -302,41 +304,128 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t x, float ratio) {
   return e4m3x4(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
 }
 
-// A cache of e4m3 codes, d = 128, bf16 inputs: CTAs [0, cache_ctas) take four (block, kv head, K or V)
-// each, the others a token's queries.
+// The least power of two s, 2^-80 at least, with amax <= 448 s (448 = 1.75 * 2^8), of amax's bits.
+__device__ __forceinline__ float scale_of(uint32_t amax) {
+  const int e = max(static_cast<int>(amax >> 23) - 127 - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0), -80);
+  return __int_as_float((e + 127) << 23);
+}
+
+// Eight lanes' part of putting `held` rows of a block, from row `first` on in steps, into units `ratio` times as large.
+__device__ __forceinline__ void rescale_rows(uint8_t* block, int first, int held, int step, float ratio) {
+  for (int row = first; row < held; row += step) {
+    uint4* at = reinterpret_cast<uint4*>(block + row * 128) + (threadIdx.x & 7);
+    const uint4 y = *at;
+    *at = make_uint4(rescale4(y.x, ratio), rescale4(y.y, ratio), rescale4(y.z, ratio), rescale4(y.w, ratio));
+  }
+}
+
+__device__ __forceinline__ void store_codes(uint8_t* to, const Lane<__nv_bfloat16>& lane, float (&a)[8], float (&c)[8], float inv) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    a[k] *= inv;
+    c[k] *= inv;
+  }
+  *reinterpret_cast<uint2*>(to + lane.at) = make_uint2(e4m3x4(a[0], a[1], a[2], a[3]), e4m3x4(a[4], a[5], a[6], a[7]));
+  *reinterpret_cast<uint2*>(to + lane.other) = make_uint2(e4m3x4(c[0], c[1], c[2], c[3]), e4m3x4(c[4], c[5], c[6], c[7]));
+}
+
+// A token's queries, of CTA `cta` among those that take them.
+__device__ __forceinline__ void queries8(const Params& P, int64_t cta) {
+  using T = __nv_bfloat16;
+  const Sharer me = sharer(P, cta);
+  const int64_t t = me.token;
+  if (t >= P.num_tokens) return;
+  const Lane<T> lane(P, threadIdx.x & 7);
+  int i;
+  Request r;
+  const bool ok = find_token(P, t, i, r);
+  if (t < r.t0 || t >= r.t1) return;
+  const int64_t angle = ok ? angle_of(P, t, r.ctx + t - r.t0) : -1;
+  if (angle < 0 && me.at == 0) flag_error(P.err, kErrLength);
+  Turn<T> turn;
+  if (angle >= 0) turn.load(P, lane, angle);
+  rotate_q(P, t, lane, turn, angle >= 0, me.at / 8, me.of / 8);
+}
+
+// A cache of e4m3 codes, d = 128, bf16 inputs, requests of one token (or none) each: CTAs [0, cache_ctas) take 16 (kv head, K or V)
+// of a request's block each, eight lanes for one; the others a token's queries.  What it costs is the chain of loads (lengths,
+// table, scale, row) times the waves of CTAs: a warp for each, as below, takes 3.5, 10.6, 44 and 84 us for 64, 600, 2432 and 4800
+// tokens of 32 / 8 heads, this 3.2, 5.6, 14.7 and 25.8.
+__global__ void __launch_bounds__(kThreads) append8_one_kernel(const Params P, int ctas_per_block) {
+  using T = __nv_bfloat16;
+  grid_dep_wait();
+  grid_dep_launch();
+  if (blockIdx.x >= P.cache_ctas) {
+    queries8(P, blockIdx.x - P.cache_ctas);
+    return;
+  }
+  const int i = static_cast<int>(blockIdx.x / ctas_per_block);
+  const int unit = static_cast<int>(blockIdx.x - static_cast<unsigned>(i) * ctas_per_block) * (kThreads / 8) + static_cast<int>(threadIdx.x >> 3);
+  Request r;
+  if (!load_request(P, i, r)) {
+    if (threadIdx.x == 0) flag_error(P.err, kErrLength);
+    return;
+  }
+  if (r.t0 == r.t1) return;
+  const int64_t id = __ldg(P.bt + static_cast<int64_t>(i) * P.max_blocks + r.ctx / kBlock);
+  const int64_t angle = angle_of(P, r.t0, r.ctx);
+  if (id < 0 || id >= P.num_blocks || angle < 0) {
+    if (threadIdx.x == 0) flag_error(P.err, angle < 0 ? kErrLength : kErrBlockId);
+    return;
+  }
+  const Lane<T> lane(P, threadIdx.x & 7);
+  const bool real = unit < 2 * P.hkv, is_v = unit >= P.hkv;
+  const int h = !real ? 0 : is_v ? unit - P.hkv : unit, held = static_cast<int>(r.ctx % kBlock);
+  float* scale = P.scales + 2 * (id * P.hkv + h) + is_v;
+  const float old = real && held > 0 ? *scale : 0.f;
+  const T* src = (is_v ? static_cast<const T*>(P.v) + r.t0 * P.v_stride : static_cast<const T*>(P.k) + r.t0 * P.k_stride) + h * P.d;
+  float a[8] = {}, c[8] = {};
+  if (real) {
+    load_vec(src + lane.at, a);
+    load_vec(src + lane.other, c);
+  }
+  if (!is_v) {
+    Turn<T> turn;
+    turn.load(P, lane, angle);
+    turn.apply(P, lane, a, c);
+  }
+  uint32_t most = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) most = max(most, max(finite_size(a[e]), finite_size(c[e])));
+#pragma unroll
+  for (int d = 4; d; d >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+  __syncwarp();  // (all lanes have read the scale)
+  if (!real) return;
+  const float now = fmaxf(old, scale_of(most));
+  uint8_t* block = static_cast<uint8_t*>(is_v ? P.v_cache : P.k_cache) + (id * P.hkv + h) * kBlock * 128;
+  if (held > 0 && now != old) rescale_rows(block, 0, held, 1, old / now);
+  store_codes(block + held * 128, lane, a, c, 1.f / now);
+  if ((threadIdx.x & 7) == 0) *scale = now;
+}
+
+// The same for requests of any length: CTAs [0, cache_ctas) take four (block, kv head, K or V) each, a warp for one.
 __global__ void __launch_bounds__(kThreads) append8_kernel(const Params P, int units_per_block) {
   using T = __nv_bfloat16;
   constexpr int kVec = 8, kRows = 4;  // rows of a warp at a time
   grid_dep_wait();
   grid_dep_launch();
-  const int lane_id = threadIdx.x & 31;
-  const Lane<T> lane(P, lane_id & 7);
   if (blockIdx.x >= P.cache_ctas) {
-    const Sharer me = sharer(P, blockIdx.x - P.cache_ctas);
-    const int64_t t = me.token;
-    if (t >= P.num_tokens) return;
-    int i;
-    Request r;
-    bool ok = find_token(P, t, i, r);
-    if (t < r.t0 || t >= r.t1) return;
-    const int64_t angle = ok ? angle_of(P, t, r.ctx + t - r.t0) : -1;
-    if (angle < 0 && me.at == 0) flag_error(P.err, kErrLength);
-    Turn<T> turn;
-    if (angle >= 0) turn.load(P, lane, angle);
-    rotate_q(P, t, lane, turn, angle >= 0, me.at / 8, me.of / 8);
+    queries8(P, blockIdx.x - P.cache_ctas);
     return;
   }
+  const int lane_id = threadIdx.x & 31;
+  const Lane<T> lane(P, lane_id & 7);
   const int64_t x = blockIdx.x / units_per_block;
   const int unit = static_cast<int>(blockIdx.x - x * units_per_block) * kWarps + (threadIdx.x >> 5);
   if (unit >= 2 * P.hkv) return;
   const auto start = [&](int at) { return static_cast<int64_t>(__ldg(P.qsl + at)) / kBlock + 2 * static_cast<int64_t>(at); };
-  const int i = P.max_q == 1 ? static_cast<int>(x) : last_request(P.num_seqs, x, start);
+  const int i = last_request(P.num_seqs, x, start);
   Request r;
   if (!load_request(P, i, r)) {
     if (lane_id == 0) flag_error(P.err, kErrLength);
     return;
   }
-  const int64_t b = r.ctx / kBlock + (P.max_q == 1 ? 0 : x - start(i));  // of the request
+  const int64_t b = r.ctx / kBlock + x - start(i);  // of the request
   const int64_t n = r.t1 - r.t0, first = b * kBlock > r.ctx ? b * kBlock : r.ctx;
   const int64_t last = (b + 1) * kBlock < r.ctx + n ? (b + 1) * kBlock : r.ctx + n;  // positions [first, last)
   if (first >= last) return;
@@ -385,31 +474,12 @@ __global__ void __launch_bounds__(kThreads) append8_kernel(const Params P, int u
     }
   }
   most = __reduce_max_sync(0xffffffffu, most);
-  // the least power of two s with amax <= 448 s: 448 = 1.75 * 2^8
-  const int e = max(static_cast<int>(most >> 23) - 127 - 8 + ((most & 0x7fffffu) > 0x600000u ? 1 : 0), -80);
-  const float need = __int_as_float((e + 127) << 23), now = fmaxf(old, need);
-  if (held > 0 && now != old) {
-    const float ratio = old / now;
-    for (int row = sub; row < held; row += kRows) {
-      uint4* at = reinterpret_cast<uint4*>(dst + row * 128) + (lane_id & 7);
-      const uint4 y = *at;
-      *at = make_uint4(rescale4(y.x, ratio), rescale4(y.y, ratio), rescale4(y.z, ratio), rescale4(y.w, ratio));
-    }
-  }
+  const float now = fmaxf(old, scale_of(most));
+  if (held > 0 && now != old) rescale_rows(dst, sub, held, kRows, old / now);
   const float inv = 1.f / now;
 #pragma unroll
   for (int g = 0; g < kBlock / kRows; ++g) {
-    if (!there[g]) continue;
-    uint8_t* to = dst + (held + g * kRows + sub) * 128;
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) {
-      a[g][k] *= inv;
-      c[g][k] *= inv;
-    }
-    *reinterpret_cast<uint2*>(to + lane.at) =
-        make_uint2(e4m3x4(a[g][0], a[g][1], a[g][2], a[g][3]), e4m3x4(a[g][4], a[g][5], a[g][6], a[g][7]));
-    *reinterpret_cast<uint2*>(to + lane.other) =
-        make_uint2(e4m3x4(c[g][0], c[g][1], c[g][2], c[g][3]), e4m3x4(c[g][4], c[g][5], c[g][6], c[g][7]));
+    if (there[g]) store_codes(dst + (held + g * kRows + sub) * 128, lane, a[g], c[g], inv);
   }
   __syncwarp();
   if (lane_id == 0) *scale = now;
@@ -447,16 +517,20 @@ int launch_append(const AppendArgs& a, int num_sms, uint32_t* err, cudaStream_t 
   p.rot = a.rot_dim;
   p.interleaved = a.interleaved;
   p.d = a.cache.head_dim;
-  // 16 CTAs of tokens an SM are under way at once; of more tokens a warp takes one
-  p.warp_a_token = a.num_tokens > 16 * static_cast<int64_t>(num_sms);
+  // Up to 4 tokens an SM a CTA takes one, of more tokens a warp does.  CTA and warp, 32 / 8 heads of 128 in bf16 to 8 bits: 1200 tokens
+  // (4 requests of 300) 9.0 and 9.0 us, 2400 15.0 and 12.8, 5400 30.6 and 26.2; 8 / 2 heads of 64 in fp32: 64 tokens 3.6 and 3.7,
+  // 1200 5.8 and 4.0, 2400 7.9 and 6.0, 5400 16.6 and 10.0
+  p.warp_a_token = a.num_tokens > 4 * static_cast<int64_t>(num_sms);
   const int64_t token_ctas = p.warp_a_token ? (a.num_tokens + kWarps - 1) / kWarps : a.num_tokens;
   if (a.cache.dtype == PKV_E4M3) {
-    const int units = (2 * p.hkv + kWarps - 1) / kWarps;
-    const int64_t blocks = a.max_query_len == 1 ? a.num_seqs : a.num_tokens / kBlock + 2 * static_cast<int64_t>(a.num_seqs);
-    p.cache_ctas = blocks * units;
+    const bool one = a.max_query_len == 1;
+    const int per_cta = one ? kThreads / 8 : kWarps, ctas_per_block = (2 * p.hkv + per_cta - 1) / per_cta;
+    const int64_t blocks = one ? a.num_seqs : a.num_tokens / kBlock + 2 * static_cast<int64_t>(a.num_seqs);
+    p.cache_ctas = blocks * ctas_per_block;
     const int64_t ctas = p.cache_ctas + (a.q ? token_ctas : 0);
     if (ctas > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
-    return cuda_status(launch_k(append8_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, s, p, units));
+    return cuda_status(launch_k(one ? append8_one_kernel : append8_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, s, p,
+                                ctas_per_block));
   }
   auto* kernel = a.cache.dtype == PKV_F32 ? append_kernel<float> : append_kernel<__nv_bfloat16>;
   return cuda_status(launch_k(kernel, dim3(static_cast<unsigned>(token_ctas)), dim3(kThreads), 0, s, p));
