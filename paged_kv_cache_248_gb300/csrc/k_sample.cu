@@ -86,7 +86,7 @@ struct Shared {
   float warp_mass[kWarps], warp_low[kWarps];
   uint32_t warp_n[kWarps];
   int32_t found[8];
-  float warp_sq[kWarps], bound[3];
+  float warp_sq[kWarps], bound[4];
   uint32_t collected, best;  // (first CTA) of the list; the first of the largest logits
   uint32_t taken;            // candidates that this CTA collected (in `weights`)
   int32_t unsure;            // (first CTA) the borders need exact sums
@@ -258,13 +258,14 @@ __device__ __forceinline__ void make_plan(Shared& s, const Row& r, float per_uni
   const float mean[4] = {y.x, y.y, y.z, y.w};
   // candidates of these bins and up to each, and the mass up to each
   const uint32_t here[4] = {n[0], n[1], n[2], n[3]};
-  float mass[4], sq[4];  // (and the squares of the bins' masses)
+  float mass[4], sq[4], behind[4];  // (and the squares of the bins' masses; the mass behind each)
   uint32_t counted = 0;
   float weighed = 0.f, squares = 0.f;
   const float unit = 1.f / per_unit;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const float m = here[k] * ex2_approx(-(static_cast<float>(b0 + k) + mean[k]) * unit);
+    behind[k] = m;
     weighed += m;
     squares = fmaf(m, m, squares);
     counted += here[k];
@@ -272,17 +273,25 @@ __device__ __forceinline__ void make_plan(Shared& s, const Row& r, float per_uni
     mass[k] = weighed;
     sq[k] = squares;
   }
+  {
+    const float m3 = behind[3], m2 = behind[2], m1 = behind[1];
+    behind[3] = 0.f;
+    behind[2] = m3;
+    behind[1] = m2 + m3;
+    behind[0] = m1 + behind[1];
+  }
   uint32_t in = counted;
-  float im = weighed, is = squares;
+  float im = weighed, is = squares, ib = weighed;
 #pragma unroll 1
   for (int d = 1; d < 32; d <<= 1) {
     const uint32_t y = __shfl_up_sync(0xffffffffu, in, d);
-    const float z = __shfl_up_sync(0xffffffffu, im, d), x = __shfl_up_sync(0xffffffffu, is, d);
+    const float z = __shfl_up_sync(0xffffffffu, im, d), x = __shfl_up_sync(0xffffffffu, is, d), v = __shfl_down_sync(0xffffffffu, ib, d);
     if (lane >= d) {
       in += y;
       im += z;
       is += x;
     }
+    if (lane + d < 32) ib += v;
   }
   if (lane == 31) {
     s.warp_n[warp] = in;
@@ -293,20 +302,22 @@ __device__ __forceinline__ void make_plan(Shared& s, const Row& r, float per_uni
   __syncthreads();
   // (the warps' sums: lane w has those up to warp w)
   uint32_t wn = lane < kWarps ? s.warp_n[lane] : 0;
-  float wm = lane < kWarps ? s.warp_mass[lane] : 0.f, ws = lane < kWarps ? s.warp_sq[lane] : 0.f;
+  float wm = lane < kWarps ? s.warp_mass[lane] : 0.f, ws = lane < kWarps ? s.warp_sq[lane] : 0.f, wb = wm;
 #pragma unroll
   for (int d = 1; d < kWarps; d <<= 1) {
     const uint32_t y = __shfl_up_sync(0xffffffffu, wn, d);
-    const float z = __shfl_up_sync(0xffffffffu, wm, d), x = __shfl_up_sync(0xffffffffu, ws, d);
+    const float z = __shfl_up_sync(0xffffffffu, wm, d), x = __shfl_up_sync(0xffffffffu, ws, d), v = __shfl_down_sync(0xffffffffu, wb, d);
     if (lane >= d) {
       wn += y;
       wm += z;
       ws += x;
     }
+    if (lane + d < 32) wb += v;
   }
   const float all = __shfl_sync(0xffffffffu, wm, kWarps - 1), all_sq = __shfl_sync(0xffffffffu, ws, kWarps - 1);
   uint32_t bn = __shfl_sync(0xffffffffu, wn, max(warp - 1, 0));
   float bm = __shfl_sync(0xffffffffu, wm, max(warp - 1, 0)), bs = __shfl_sync(0xffffffffu, ws, max(warp - 1, 0));
+  float bb = __shfl_sync(0xffffffffu, wb, warp + 1);  // (nothing in lane kWarps)
   if (warp == 0) {
     bn = 0;
     bm = bs = 0.f;
@@ -314,17 +325,19 @@ __device__ __forceinline__ void make_plan(Shared& s, const Row& r, float per_uni
   bn += in - counted;
   bm += im - weighed;
   bs += is - squares;
+  const float next = __shfl_down_sync(0xffffffffu, ib, 1);
+  bb += lane < 31 ? next : 0.f;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     n[k] += bn;
     mass[k] += bm;
     sq[k] += bs;
+    behind[k] += bb;
   }
   // the masses above are off by a part of 2e-4 at most, and by what lies behind the last bin
   constexpr float kLow = 0.9998f, kHigh = 1.0002f;
-  const auto first_over = [&](int at, const float (&of)[4], float x) {  // the first bin up to which more than x lies
-    const int k = of[0] > x ? 0 : of[1] > x ? 1 : of[2] > x ? 2 : 3;
-    const int mine = __reduce_min_sync(0xffffffffu, of[3] > x ? b0 + k : kBins - 1);
+  const auto first_of = [&](int at, bool y0, bool y1, bool y2, bool y3) {  // the first bin of which it holds, and of all behind
+    const int mine = __reduce_min_sync(0xffffffffu, y3 ? b0 + (y0 ? 0 : y1 ? 1 : y2 ? 2 : 3) : kBins - 1);
     if (lane == 0 && mine < kBins - 1) atomicMin(&s.found[at], mine);
   };
   const bool cut_k = r.top_k > 0, cut_m = r.min_p > 0.f;  // (a top-k of all and more ends in the last bin)
@@ -346,32 +359,50 @@ __device__ __forceinline__ void make_plan(Shared& s, const Row& r, float per_uni
   if (cut1) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (b0 + k == a1 - 1) s.bound[0] = mass[k];
+      if (b0 + k == a1 - 1) {
+        s.bound[0] = mass[k];
+        s.bound[2] = behind[k];
+      }
       if (b0 + k == e1) {
-        s.bound[1] = mass[k];
-        s.bound[2] = sq[k];
+        s.bound[1] = sq[k];
+        s.bound[3] = behind[k];
       }
     }
-    if (threadIdx.x == 0 && a1 == 0) s.bound[0] = 0.f;
+    if (threadIdx.x == 0 && a1 == 0) s.bound[0] = 0.f, s.bound[2] = all;
     __syncthreads();
   }
-  float z_lo = (cut1 ? s.bound[0] : all) * kLow, z_hi = (cut1 ? s.bound[1] : all) * kHigh + rest;
-  // the first bins, until the rest's squares are 2^-8 of the kept mass's at most
-  first_over(5, sq, (cut1 ? s.bound[2] : all_sq) - z_lo * z_lo * kRest);
+  const float z_lo = (cut1 ? s.bound[0] : all) * kLow;
+  {  // the first bins, until the rest's squares are 2^-8 of the kept mass's
+    const float x = (cut1 ? s.bound[1] : all_sq) - z_lo * z_lo * kRest;
+    first_of(5, sq[0] > x, sq[1] > x, sq[2] > x, sq[3] > x);
+  }
+  // A share f of the kept mass is passed where f S < (1 - f) M, of the mass M up to a bin and S of the kept behind it: as tight
+  // near the end, where S is small and its bins are full, as at the beginning.  The first bin where that can be (f = lo), and
+  // where it must be (f = hi).
+  const float less = cut1 ? s.bound[2] * kHigh : 0.f, least = cut1 ? s.bound[3] * kLow : 0.f;
+  const auto borders = [&](int at, float lo, float hi) {
+    bool can[4], must[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      can[k] = lo * (behind[k] * kLow - less) < (1.f - lo) * (mass[k] * kHigh);
+      must[k] = hi * (behind[k] * kHigh - least + rest) < (1.f - hi) * (mass[k] * kLow);
+    }
+    first_of(at, can[0], can[1], can[2], can[3]);
+    first_of(at + 1, must[0], must[1], must[2], must[3]);
+  };
   // the end of top-p
   int a2 = kBins, e2 = e1;
   const bool cut_p = r.top_p < 1.f;
+  float kept_lo = 1.f, kept_hi = 1.f;  // top-p's share with what its last candidate adds
   if (cut_p) {
-    first_over(1, mass, r.top_p * z_lo * kLow - rest);
-    first_over(2, mass, r.top_p * z_hi * kHigh);
+    borders(1, r.top_p, r.top_p);
     __syncthreads();
     a2 = min(s.found[1], e1);
     e2 = min(s.found[2], e1);
-    z_lo *= r.top_p;
-    z_hi = fminf(z_hi, r.top_p * z_hi + kHigh * ex2_approx(-static_cast<float>(a2) * unit));
+    kept_lo = r.top_p * 0.9999998f;
+    kept_hi = fminf(1.f, r.top_p * 1.0000002f + kHigh * ex2_approx(-static_cast<float>(a2) * unit) / z_lo);
   }
-  first_over(3, mass, r.u * z_lo * kLow - rest);
-  first_over(4, mass, r.u * z_hi * kHigh);
+  borders(3, r.u * kept_lo, r.u * kept_hi);
   __syncthreads();
   // three windows in order of their beginnings, joined where they meet (kBins: none)
   const int a3 = min(s.found[3], e2), e3 = min(s.found[4], e2), exact = s.found[5] + 1;

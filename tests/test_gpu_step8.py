@@ -569,6 +569,15 @@ def test_sample_numbers_next_to_a_border(pkv, v, sigma, dtype, border):
         check_sample(pkv, x, np.full(len(x), 1 - 2.0 ** -24), top_p=share)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("p", [1.0, 0.999, 0.99999, 1e-4])
+def test_sample_numbers_next_to_0_and_1(pkv, dtype, p):
+    u = np.array([0, 1e-30, 1e-7, 1e-4, 0.01, 0.99, 0.999, 0.9999, 0.99999, 1 - 2.0 ** -20, 1 - 2.0 ** -24] * 2, np.float32)
+    x = torch.cat([peaked(11, 50257, 8), peaked(11, 50257, 9, sigma=1.0, spikes=0)]).to(dtype)
+    for kw in ({}, dict(top_k=np.full(22, 20000, np.int32)), dict(min_p=np.full(22, 1e-4, np.float32)), dict(temperature=np.full(22, 1.5, np.float32))):
+        check_sample(pkv, x, u, top_p=np.full(22, p, np.float32), **kw)
+
+
 @pytest.mark.parametrize("n,v", [(100, 30000), (320, 40000)])
 def test_sample_many_rows_of_a_large_vocabulary(pkv, n, v):
     rng = np.random.default_rng(n)
