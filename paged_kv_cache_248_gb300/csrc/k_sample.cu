@@ -106,58 +106,73 @@ __device__ __forceinline__ float logit_of(uint64_t key) {
 }
 __device__ __forceinline__ bool candidate(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
-// A piece of 16 bytes of a row; what does not belong to the row is NaN, no candidate.
+// A piece of a row: eight logits, 16 or 32 bytes.
+constexpr int kPiece = 8;
 template <typename T>
-__device__ __forceinline__ uint4 load_piece(const T* p, int i0, int vocab) {
-  constexpr int kVec = 16 / sizeof(T);
-  if (i0 >= 0 && i0 + kVec <= vocab) return __ldg(reinterpret_cast<const uint4*>(p + i0));
-  uint32_t w[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-  if (i0 >= vocab) return make_uint4(w[0], w[1], w[2], w[3]);
+struct Piece {
+  uint4 v[kPiece * sizeof(T) / 16];
+};
+
+// The piece that begins at logit i0; what does not belong to the row is NaN, no candidate.
+template <typename T>
+__device__ __forceinline__ Piece<T> load_piece(const T* p, int i0, int vocab) {
+  Piece<T> piece;
+  constexpr int kParts = sizeof(piece) / 16;
+  if (i0 >= 0 && i0 + kPiece <= vocab) {
 #pragma unroll
-  for (int e = 0; e < kVec; ++e) {
+    for (int k = 0; k < kParts; ++k) piece.v[k] = __ldg(reinterpret_cast<const uint4*>(p + i0) + k);
+    return piece;
+  }
+#pragma unroll
+  for (int k = 0; k < kParts; ++k) piece.v[k] = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
+  if (i0 >= vocab) return piece;
+  uint32_t* w = reinterpret_cast<uint32_t*>(piece.v);
+#pragma unroll
+  for (int e = 0; e < kPiece; ++e) {
     if (i0 + e < 0 || i0 + e >= vocab) continue;
     const uint32_t x = __float_as_uint(Elem<T>::to_f32(p[i0 + e]));
     if constexpr (sizeof(T) == 4) w[e] = x;
     else w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | x : (w[e / 2] & 0xffff0000u) | x >> 16;
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return piece;
 }
 
-// Calls f(piece, i) with this thread's pieces of 16 bytes of the row (`first`, first + step, ...), whose logits begin at number
-// i; what the row does not have is NaN.  All threads of a CTA call it equally often.  Three pieces are on their way while
-// one is worked on.
+// Calls f(piece, i) with this thread's pieces of the row (`first`, first + step, ...), whose logits begin at number i.  All threads of
+// a CTA call it equally often.  The next pieces, 48 (32) bytes of them, are on their way while one is worked on.
 template <typename T, typename F>
 __device__ __forceinline__ void each_raw(const Params& P, int64_t row, int first, int step, F&& f) {
-  constexpr int kVec = 16 / sizeof(T);
   const T* p = static_cast<const T*>(P.logits) + row * P.stride;
   const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));  // piece 0 begins so much before
   const int end = skew + P.vocab;
-  int i0 = first * kVec - skew;
-  const int hop = step * kVec;
-  uint4 a = load_piece<T>(p, i0, P.vocab), b = load_piece<T>(p, i0 + hop, P.vocab), c = load_piece<T>(p, i0 + 2 * hop, P.vocab);
+  int i0 = first * kPiece - skew;
+  const int hop = step * kPiece;
+  constexpr int kAhead = sizeof(T) == 4 ? 1 : 3;
+  Piece<T> ring[kAhead + 1];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) ring[k] = load_piece<T>(p, i0 + k * hop, P.vocab);
 #pragma unroll 1
-  for (int v = first - static_cast<int>(threadIdx.x); v * kVec < end; v += step, i0 += hop) {
-    const uint4 d = load_piece<T>(p, i0 + 3 * hop, P.vocab);
-    f(a, i0);
-    a = b;
-    b = c;
-    c = d;
+  for (int v = first - static_cast<int>(threadIdx.x); v * kPiece < end; v += step, i0 += hop) {
+    ring[kAhead] = load_piece<T>(p, i0 + kAhead * hop, P.vocab);
+    f(ring[0], i0);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) ring[k] = ring[k + 1];
   }
 }
 template <typename T>
-__device__ __forceinline__ void unpack_piece(const uint4& raw, float (&x)[16 / sizeof(T)]) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+__device__ __forceinline__ void unpack_piece(const Piece<T>& piece, float (&x)[kPiece]) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(piece.v);
 #pragma unroll
-  for (int e = 0; e < 16 / static_cast<int>(sizeof(T)); ++e)
-    x[e] = __uint_as_float(sizeof(T) == 4 ? w[e % 4] : e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+  for (int e = 0; e < kPiece; ++e)
+    x[e] = __uint_as_float(sizeof(T) == 4 ? w[e] : e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
 }
 // The largest logit of a piece (NaN is passed over).
 template <typename T>
-__device__ __forceinline__ float piece_largest(const uint4& raw) {
+__device__ __forceinline__ float piece_largest(const Piece<T>& piece) {
   if constexpr (sizeof(T) == 4) {
-    return fmaxf(fmaxf(__uint_as_float(raw.x), __uint_as_float(raw.y)), fmaxf(__uint_as_float(raw.z), __uint_as_float(raw.w)));
+    const float* x = reinterpret_cast<const float*>(piece.v);
+    return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
   } else {
-    const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&raw);
+    const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(piece.v);
     const __nv_bfloat162 y = __hmax2(__hmax2(x[0], x[1]), __hmax2(x[2], x[3]));
     return fmaxf(__low2float(y), __high2float(y));
   }
@@ -165,9 +180,8 @@ __device__ __forceinline__ float piece_largest(const uint4& raw) {
 // The same with their logits x[].
 template <typename T, typename F>
 __device__ __forceinline__ void each_piece(const Params& P, int64_t row, int first, int step, F&& f) {
-  constexpr int kVec = 16 / sizeof(T);
-  each_raw<T>(P, row, first, step, [&](const uint4& raw, int i0) {
-    float x[kVec];
+  each_raw<T>(P, row, first, step, [&](const Piece<T>& raw, int i0) {
+    float x[kPiece];
     unpack_piece<T>(raw, x);
     f(x, i0);
   });
@@ -175,10 +189,9 @@ __device__ __forceinline__ void each_piece(const Params& P, int64_t row, int fir
 // f(x, i) for each of them.
 template <typename T, typename F>
 __device__ __forceinline__ void each(const Params& P, int64_t row, int first, int step, F&& f) {
-  constexpr int kVec = 16 / sizeof(T);
-  each_piece<T>(P, row, first, step, [&](const float (&x)[kVec], int i0) {
+  each_piece<T>(P, row, first, step, [&](const float (&x)[kPiece], int i0) {
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) f(x[e], i0 + e);
+    for (int e = 0; e < kPiece; ++e) f(x[e], i0 + e);
   });
 }
 
@@ -733,8 +746,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
       });
     } else {
       __nv_bfloat162 hi = __float2bfloat162_rn(-INFINITY), lo = __float2bfloat162_rn(INFINITY);
-      each_raw<T>(P, row, first, step, [&](const uint4& raw, int) {
-        const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&raw);
+      each_raw<T>(P, row, first, step, [&](const Piece<T>& raw, int) {
+        const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(raw.v);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           hi = __hmax2(hi, x[e]);
@@ -804,8 +817,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
   // arrays of them in turn; a thread keeps the sums of four bins.
   {
     static_assert(kPerThread == 4, "a thread's bins are a vector");
-    constexpr int kVec = 16 / sizeof(T), kPieces = 16 / kVec;
-    static_assert(16 * kThreads < (1 << 14) && 31 * 16 * kThreads < (1 << 18), "the fields of a word");
+    constexpr int kPieces = 2;
+    static_assert(kPieces * kPiece * kThreads < (1 << 14) && 31 * kPieces * kPiece * kThreads < (1 << 18), "the fields of a word");
     uint32_t into = smem_u32(s.bins);
     const float per_part = per_place * (1.f / 64.f);
     uint32_t n[4] = {0, 0, 0, 0}, place[4] = {0, 0, 0, 0};
@@ -821,9 +834,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
         place[k] += y[k] & 0x3ffffu;
       }
     };
-    each_piece<T>(P, row, first, step, [&](const float (&x)[kVec], int) {
+    each_piece<T>(P, row, first, step, [&](const float (&x)[kPiece], int) {
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
+      for (int e = 0; e < kPiece; ++e) {
         const float y = (top - x[e]) * per_part;
         const uint32_t at = __float_as_uint(__fadd_rd(y, 8388608.f));
         // (not the last bin's, nor what is no candidate)
@@ -878,7 +891,6 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
   uint32_t collected = 0;
 #pragma unroll 1
   for (int round = 0; round < 2; ++round) {
-    constexpr int kVec = 16 / sizeof(T);
     const float limit = fmaxf(plan.exact, round ? kExactAgain * per_unit : 0.f) * 2048.f;
     // of the segments, the places whose weights are summed up in fp32
     const float lo[3] = {limit, fmaxf(upto[0], limit), fmaxf(upto[1], limit)};
@@ -896,14 +908,14 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
         }
       }
     };
-    each_raw<T>(P, row, first, step, [&](const uint4& raw, int i0) {
+    each_raw<T>(P, row, first, step, [&](const Piece<T>& raw, int i0) {
       if (!__any_sync(0xffffffffu, piece_largest<T>(raw) >= least)) return;
-      float x[kVec];
+      float x[kPiece];
       unpack_piece<T>(raw, x);
       float part[3] = {0.f, 0.f, 0.f};
       uint32_t apart = 0;  // not summed up here
 #pragma unroll
-      for (int e = 0; e < kVec; e += 2) {
+      for (int e = 0; e < kPiece; e += 2) {
         const Two d = add2(two(x[e], x[e + 1]), two(-top));
         const float2 y2 = both(mul2(d, two(-per_place))), m2 = both(w.rounded(d));
 #pragma unroll
@@ -918,7 +930,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
       }
       if (apart) {
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) {
+        for (int e = 0; e < kPiece; ++e) {
           const float y = (top - x[e]) * per_place;
           if (!(apart >> e & 1) || !(y < behind) || !candidate(x[e])) continue;
           if ((y >= from[0] && y < upto[0]) || (y >= from[1] && y < upto[1]) || (y >= from[2] && y < upto[2])) {
@@ -933,7 +945,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
       }
 #pragma unroll
       for (int k = 0; k < 3; ++k) light[k] += __float2ull_rn(part[k] * w.unit);
-      if (__any_sync(0xffffffffu, waiting > kQueue - kVec)) work_off();
+      if (__any_sync(0xffffffffu, waiting > kQueue - kPiece)) work_off();
     });
     work_off();
 #pragma unroll
