@@ -468,7 +468,7 @@ PKV_API int pkv_fork_workspace(int32_t num_rows, int64_t* bytes);
  * max_query_len   host bound on q_i: a request with more is flagged, its tokens not written
  * q_out           device, as q, tokens q_out_stride apart; written.  May be q itself (same stride); any other
  *                 overlap with q, k or v is refused
- * Rows of tokens behind the last request stay as they are.
+ * Rows of tokens behind the last request stay as they are.  A block that the call writes belongs to one request of it.
  * Device errors: a request whose lengths do not fit or a row outside of [0, num_angles) flag PKV_ERR_INDEX, its
  * tokens are not written and their q_out rows are zero; so is a bad block id, whose q_out row stays valid.
  */
@@ -485,12 +485,15 @@ PKV_API int pkv_rope_append(const void* q, const void* k, const void* v, int32_t
  * query heads a kv head): the same sum over K_u = code * scales[b][g][0] and V_u = code * scales[b][g][1] of
  * block b = block_tables[i][u / 16].  q and out are bf16.  Chunks and single tokens mix freely.
  * scales          device fp32 [num_blocks][num_kv_heads][2]; positive.  V's are taken as at least 2^-80 and at
- *                 most 2^110
+ *                 most 2^110; a key whose weight times V's scale is less than 2^-120 of the context's largest such product may
+ *                 be left out
  * max_query_len   host bound on q_i: a request with more is flagged (PKV_ERR_INDEX) and its rows zeroed
  * query_start_loc rows outside of [0, num_tokens) are flagged too; rows that no request has stay as they are
  * workspace       device memory of at least pkv_q8_workspace() bytes, 256-byte aligned
  * What a row does not see (later tokens of its chunk, slots behind the context) has no part in it, whatever its
- * codes are, NaN among them.  A NaN that a row sees makes the row's elements NaN.
+ * codes are, NaN among them.  A NaN that a row sees makes elements of the row NaN: those of its column at least, of a NaN in K
+ * or a query all.  An element of a query counts down to 2^-22 of the largest one among its unit's rows (the heads of a kv
+ * head; of a chunk 2^-24, 32 rows).
  * Everything else and the errors: as paged_attention().  Work is cut along the keys by the batch's
  * sizes, so rounding (not the result) may depend on the batch.
  */
@@ -511,8 +514,10 @@ PKV_API int pkv_q8_workspace(const pkv_cache_desc* cache, int32_t num_q_heads, i
  *     of these the ones whose weight is at least min_p[n] (that of the first is 1; 0 or less: all),
  *     of these the shortest beginning whose weights are at least top_p[n] of the sum (1 or more: all; one at least).
  * The token is the first of the kept ones whose cumulative weight exceeds uniform[n] times their sum.
- * temperature[n] == 0 takes the first candidate.  Weights are right to 2^-40 and their sums exact, so
- * that two tokens are told apart as 64-bit arithmetic does, and a call repeats bit by bit.
+ * temperature[n] == 0 takes the first candidate.  Near a border weights are right to 2^-40 (of the largest weight, 2^-44),
+ * and sums to 2^-28 of the kept ones, or, where a border lies within 2^-25 of a candidate's, exact down to weights of
+ * 2^-20 of the largest: tokens are told apart as 64-bit arithmetic does but for borders closer than that.  A call
+ * repeats bit by bit.
  * logits          device [num_seqs] rows of vocab values of `dtype` (pkv_dtype: fp32 or bf16), row_stride elements
  *                 apart (>= vocab), aligned to their type; vocab up to 2^20
  * temperature, top_k, top_p, min_p  optional device fp32, int32, fp32, fp32 [num_seqs] (NULL: 1, all, 1, 0)

@@ -20,6 +20,14 @@
 // (a thread a row; P stays in tensor memory, over S), warps 10-13 load codes from the cache, 16 bytes a lane and a tile
 // ahead in registers, convert them and put them into the K and V rings (two tiles each, 128-byte swizzle).  The row tiles
 // take turns: one's products are made while the other's weights are.
+// The reference of a row is set by its first tile and moves only when a weight would pass 2^15, which a vote of the warp tells
+// as the weights are made: one pass over S (with a pass for the maximum before it 122 us, so 117).
+//
+// Bound: the chain S (800 clocks with its latency) -> weights (1900) -> P V (500) of a row tile, two of which take turns: 3850 for a
+// key tile of 256 rows, where the tensor core is at work for 2100.  8 requests of 512 tokens, contexts of 0 to 2048, 32 / 8 heads:
+// 117 us, 735 TFLOP/s, 38 % of cuBLAS's burst; 105 of it here, 12 joining.  A unit's beginning and end cost 7000
+// clocks, most of them Q's way to shared memory and O's out of tensor memory.
+//
 // V rows behind the context are zero; in a tile that not every row sees whole, NaN codes of V are taken out and
 // told to the softmax, which makes the rows that see them NaN.  All waits are bounded.
 #include "q8_units.cuh"

@@ -4,29 +4,31 @@
 // weights w = exp((x - max) / T).  Every filter keeps a beginning of that order: the first k; those with
 // w >= min_p; the shortest with mass >= top_p of what is left.  The token is the first whose cumulative
 // weight exceeds u times the kept mass.  Whether a sum of a hundred thousand weights lies above or below
-// a border is decided by its last digits, so weights are whole numbers: w 2^S rounded, right to about 2^-40
+// a border is decided by its last digits, so weights near a border are whole numbers: w 2^S rounded, right to about 2^-40
 // of w (weight.cuh), and sums of them exact, in any order.
 //
 // Work.  A row belongs to a cluster of CTAs, which go through it three times (twice from L2):
 //   1. its largest and its least logit;
 //   2. how many candidates fall into each of 2048 bins of (max - x) / T, 1/64 of a power of two wide or less, and the sum
-//      of their places within it.  That tells every mass to 1e-4 (the weight of the mean place, from below, is off by an
-//      eighth of the square of a bin's width), and so, for each border (the end of top-k and min-p, of top-p,
-//      the token), the one or two bins in which it must lie;
-//   3. the candidates of those bins are collected in the cluster's first CTA, and the others' weights summed up
-//      between them: exact ones of 2^-12 of the largest and more, smaller ones in fp32.
-// The first CTA sorts what was collected (hundreds at most, as a rule), takes its exact weights and finds the borders.
-// Where one lies so close to a candidate's (2^-25 of the sums) that the fp32 weights could tell them wrong, the sums are
-// taken again, exact down to 2^-20 of the largest weight, and the borders found again: a few rows in a thousand flat
-// ones, hardly any other.  (The exponential unit's error is 2^-24 of a weight, rms, with a mean of -5.25e-8, measured, that
-// is given back; of thousands of weights below 2^-12 the sum is then right to 2^-29.)
-// Weights to be exact, few in most rows, wait in a queue of each thread's, so that a warp computes as many as it has lanes
-// at a time.  With top-k or min-p nothing behind their end is looked at closely.
+//      of their places within it, to 1/32 of it.  That tells the mass up to a bin and the mass behind it to 2e-4 of
+//      themselves (ln 2 / 64 / 64 for the places, an eighth of the square of a bin's width for taking the weight of their mean),
+//      and so, for each border (the end of top-k and min-p, of top-p, the token), the one or two bins in which it must lie;
+//   3. the candidates of those bins are collected, bin by bin, in the cluster's first CTA, and the others' weights summed up
+//      between them: exact ones of the first bins, the rest in fp32.
+// The first bins are those without which the squares of the others' masses would be more than 2^-8 of the square of the
+// kept mass: an fp32 weight is off by 2^-24 (the exponential unit's error, rms, with a mean of -5.25e-8, measured, that is
+// given back), so that sums are right to 2^-28 even where all weights of a bin are off the same way (equal logits).
+// What was collected (hundreds, as a rule) is put in order by all CTAs, with exact weights, and the first CTA finds the borders.
+// Where one lies so close to a candidate's (2^-25 of the sums, eight times their error) that the fp32 weights could tell them
+// wrong, the sums are taken again, exact down to 2^-20 of the largest weight, and the borders found again: a few rows in a
+// thousand flat ones, hardly any other.  Weights to be exact wait in a queue of each thread's, so that a warp computes as many
+// as it has lanes at a time.  With top-k or min-p nothing behind their end is looked at closely.
 // Where more than 2048 candidates lie in the borders' bins (rows of equal logits), borders are found by bisection
-// of the keys instead, a pass over the row each.
+// of the keys instead, a pass over the row each (1 ms for 128256 logits).
 //
-// Bound: latency: three passes, three cluster barriers, and code that runs once, so that it has to be fetched (loops,
-// not unrolled copies).
+// Bound: steps, not bytes.  64 rows of 128256 in bf16, four CTAs each, two on most SMs: 44 us (2.5 at the HBM copy's rate), in
+// clocks of the longest rows: first pass 6000, counts 15000, joining them and the plan 10000, sums 22000, order
+// 4000, borders 6000, where a pass issues 15 to 25 instructions a logit.  One row of 32000: 15 us.
 #include <cooperative_groups.h>
 
 #include "pkv_internal.cuh"
@@ -969,6 +971,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
     if (round == 0) {
       collected = head->collected;
       const int n = static_cast<int>(collected);
+      // Ranking takes the square of a CTA's share, sorting less of many (64 rows, 4 CTAs each: about 400, 800 and 1600 collected 48, 77
+      // and 90 us ranked, 61, 82 and 86 sorted; 300 rows, one each, 400 and 800: 143 and 277, 149 and 249)
       const bool many = n > kCollect, few = !many && n * n <= kThreads * kThreads * kCtas;
       if (few || (rank == 0 && !many)) {
         for (int i = threadIdx.x; i < n; i += kThreads) s.unsorted[i] = head->list[i];
@@ -1006,7 +1010,9 @@ int launch(const Params& p, int32_t rows, cudaStream_t s) {
 
 template <typename T>
 int launch_rows(const Params& p, int32_t rows, int num_sms, cudaStream_t s) {
-  // CTAs a row: as many as the SMs hold two of each, none with less than 1024 logits
+  // CTAs a row: as many as the SMs hold two of each, none with less than 1024 logits.  1, 2, 4 and 8 of them: one row of 32000 23.0,
+  // 18.4, 16.0, 15.3 us, of 4000 16.2, 15.9, 15.4, 15.9; 33 rows of 50257 in fp32 51, 35, 26, 27; 64 of 128256 101, 61, 48, 56; 152 of
+  // 32000 43, 39, 61, 100; 304 of 32000 54, 65, 105, 186
   const int64_t room = 2 * static_cast<int64_t>(num_sms) / rows;
   const int most = static_cast<int>(room < 1 ? 1 : room > 8 ? 8 : room);
   if (most >= 8 && p.vocab >= 8192) return launch<T, 8>(p, rows, s);
