@@ -197,11 +197,12 @@ __device__ __forceinline__ void each(const Params& P, int64_t row, int first, in
   });
 }
 
-// Adds to a word of shared memory.
-__device__ __forceinline__ void add_if(bool really, uint32_t addr, uint32_t x) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p red.shared.add.u32 [%1], %2;\n\t}" ::"r"(really ? 1u : 0u),
-               "r"(addr), "r"(x)
-               : "memory");
+// Adds to a word of shared memory where |y| < end.
+__device__ __forceinline__ void add_below(float y, float end, uint32_t addr, uint32_t x) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .f32 a;\n\tabs.f32 a, %0;\n\tsetp.lt.f32 p, a, %1;\n\t@p red.shared.add.u32 [%2], %3;\n\t}" ::"f"(y), "f"(end),
+      "r"(addr), "r"(x)
+      : "memory");
 }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
@@ -717,7 +718,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
   const int64_t row = blockIdx.x / kCtas;
   const int first = rank * kThreads + threadIdx.x, step = kCtas * kThreads;
   if (threadIdx.x < 256) s.table[threadIdx.x] = kPowers.v[threadIdx.x];
-  for (int b = threadIdx.x; b < kBins; b += kThreads) s.bins[b] = s.places[b] = s.cursor[b] = 0;
+  static_assert(kBins == 4 * kThreads, "a vector of bins a thread");
+  reinterpret_cast<uint4*>(s.bins)[threadIdx.x] = reinterpret_cast<uint4*>(s.places)[threadIdx.x] =
+      reinterpret_cast<uint4*>(s.cursor)[threadIdx.x] = make_uint4(0, 0, 0, 0);
   if (threadIdx.x < 3) s.segment[threadIdx.x] = 0;
   if (threadIdx.x == 4) s.collected = s.taken = 0;
   if (threadIdx.x == 5) s.best = 0x7fffffffu;
@@ -842,7 +845,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
         const float y = (top - x[e]) * per_part;
         const uint32_t at = __float_as_uint(__fadd_rd(y, 8388608.f));
         // (not the last bin's, nor what is no candidate)
-        add_if(fabsf(y) < kEnd / 64.f, into + (at >> 3 & 4 * (kBins - 1)), (at & 31u) | 0x40000u);
+        add_below(y, kEnd / 64.f, into + ((at & 32u * (kBins - 1)) >> 3), (at & 31u) | 0x40000u);
       }
       if (++pieces == kPieces) {
         pieces = 0;
