@@ -26,9 +26,10 @@
 // Where more than 2048 candidates lie in the borders' bins (rows of equal logits), borders are found by bisection
 // of the keys instead, a pass over the row each (1 ms for 128256 logits).
 //
-// Bound: steps, not bytes.  64 rows of 128256 in bf16, four CTAs each, two on most SMs: 44 us (2.5 at the HBM copy's rate), in
+// Bound: steps, not bytes.  64 rows of 128256 in bf16, four CTAs each, two on most SMs: 43.5 us (2.5 at the HBM copy's rate), in
 // clocks of the longest rows: first pass 6000, counts 15000, joining them and the plan 10000, sums 22000, order
-// 4000, borders 6000, where a pass issues 15 to 25 instructions a logit.  One row of 32000: 15 us.
+// 4000, borders 4000; a pass issues 15 to 25 instructions a logit.  One row of 32000: 13 us, of which the plan takes 2.5, the
+// three passes 1.3 each and six cluster barriers 0.6 each.
 #include <cooperative_groups.h>
 
 #include "pkv_internal.cuh"
@@ -45,6 +46,9 @@ constexpr float kBinsPerUnit = 64.f;
 constexpr float kExactAgain = 20.f;  // weights down to 2^-20 of the largest are exact where sums are taken again
 constexpr float kRest = 1.f / 256.f;  // squares of the bins' masses that fp32 weights may leave, of the kept mass's
 constexpr int kCollect = 2048;
+// Candidates whose borders a warp finds alone: of 32, 64, 128, 256 at most 64 rows of 128256 take 44.1, 43.8, 43.5, 44.2 us, 256 of 32000
+// 43.0, 42.1, 41.6, 41.9; one row, which has a few, 12.9, and 15.2 where the CTA always does.
+constexpr int kFew = 128;
 constexpr int kQueue = 16;  // places of a thread's queue, eight of which a piece may fill
 
 struct Params {
@@ -87,7 +91,7 @@ struct Shared {
   unsigned long long warp_u64[kWarps];
   float warp_mass[kWarps], warp_low[kWarps];
   uint32_t warp_n[kWarps];
-  int32_t found[8];
+  int32_t found[6], counts[6];  // (of the plan)
   float warp_sq[kWarps], bound[4];
   uint32_t collected, best;  // (first CTA) of the list; the first of the largest logits
   uint32_t taken;            // candidates that this CTA collected (in `weights`)
@@ -314,7 +318,7 @@ __device__ __forceinline__ void make_plan(Shared& s, const Row& r, float per_uni
     s.warp_mass[warp] = im;
     s.warp_sq[warp] = is;
   }
-  if (threadIdx.x < 8) s.found[threadIdx.x] = kBins - 1;
+  if (threadIdx.x < 6) s.found[threadIdx.x] = kBins - 1;
   __syncthreads();
   // (the warps' sums: lane w has those up to warp w)
   uint32_t wn = lane < kWarps ? s.warp_n[lane] : 0;
@@ -361,8 +365,8 @@ __device__ __forceinline__ void make_plan(Shared& s, const Row& r, float per_uni
     const uint32_t k = static_cast<uint32_t>(r.top_k);
     const int at = n[0] >= k ? 0 : n[1] >= k ? 1 : n[2] >= k ? 2 : 3;
     if (bn < k && n[3] >= k) s.found[0] = b0 + at;
+    __syncthreads();
   }
-  __syncthreads();
   int a1 = kBins, e1 = kBins - 1;  // the end of top-k and min-p
   if (cut_k) a1 = e1 = s.found[0];
   if (cut_m) {
@@ -423,7 +427,6 @@ __device__ __forceinline__ void make_plan(Shared& s, const Row& r, float per_uni
   // three windows in order of their beginnings, joined where they meet (kBins: none)
   const int a3 = min(s.found[3], e2), e3 = min(s.found[4], e2), exact = s.found[5] + 1;
   int a[3] = {a3, cut_p ? a2 : kBins, cut1 ? a1 : kBins}, e[3] = {max(a3, e3), max(a2, e2), max(a1, e1)};
-  __syncthreads();  // (`found` has been read)
   const auto swap = [&](int x, int y, bool really) {
     const int u = really ? a[y] : a[x], v = really ? e[y] : e[x];
     a[y] = really ? a[x] : a[y], e[y] = really ? e[x] : e[y];
@@ -449,16 +452,16 @@ __device__ __forceinline__ void make_plan(Shared& s, const Row& r, float per_uni
   for (int k = 0; k < 4; ++k) {
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
-      if (a[j] == b0 + k) s.found[j] = static_cast<int32_t>(n[k] - here[k]);
-      if (e[j] == b0 + k) s.found[5 + j] = static_cast<int32_t>(n[k]);
+      if (a[j] == b0 + k) s.counts[j] = static_cast<int32_t>(n[k] - here[k]);
+      if (e[j] == b0 + k) s.counts[3 + j] = static_cast<int32_t>(n[k]);
     }
   }
   __syncthreads();
   int rank[3], collected = 0;
 #pragma unroll
   for (int j = 0; j < 3; ++j) {
-    rank[j] = s.found[j] - collected;
-    collected += a[j] < kBins ? s.found[5 + j] - s.found[j] : 0;
+    rank[j] = s.counts[j] - collected;
+    collected += a[j] < kBins ? s.counts[3 + j] - s.counts[j] : 0;
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -543,14 +546,52 @@ __device__ __forceinline__ void sort_many(Shared& s, const Weight& w, int n) {
   for (int i = threadIdx.x; i < n; i += kThreads) s.weights[i] = w.of(logit_of(s.sorted[i]), s.table);
 }
 
-// The token out of the n collected candidates, which are sorted (the first CTA): 0.  1: with `exact` sums between them it
+// The same of at most 32 keys of `list`, in place, by a warp of the first CTA.
+__device__ __forceinline__ void rank_few(Shared& s, const Weight& w, int n) {
+  const int lane = threadIdx.x & 31;
+  const uint64_t mine = lane < n ? s.list[lane] : ~uint64_t(0);
+  int place = 0;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) place += __shfl_sync(0xffffffffu, mine, i) < mine;
+  __syncwarp();
+  if (lane < n) {
+    s.list[place] = mine;
+    s.weights[place] = w.of(logit_of(mine), s.table);
+  }
+  __syncwarp();
+}
+
+// Sums up to each thread and over all, a sum, a minimum, a vote: of a warp, or of all threads of the CTA.
+template <bool kWarp>
+struct Team {
+  Shared& s;
+  __device__ __forceinline__ uint64_t scan(uint64_t x, uint64_t* all) {
+    if constexpr (!kWarp) return block_scan(x, s, all);
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint64_t y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    *all = __shfl_sync(0xffffffffu, x, 31);
+    return x;
+  }
+  __device__ __forceinline__ uint64_t sum(uint64_t x) { return kWarp ? warp_sum(x) : block_sum(x, s); }
+  __device__ __forceinline__ uint64_t least(uint64_t x) { return kWarp ? warp_min(x) : block_min(x, s); }
+  __device__ __forceinline__ bool any(bool x) { return kWarp ? __any_sync(0xffffffffu, x) != 0 : __syncthreads_or(x) != 0; }
+};
+
+// The token out of the n collected candidates, which are sorted (the first CTA, or its first warp): 0.  1: with `exact` sums between them it
 // could be another.  2: it is not among them.
+template <bool kWarp>
 __device__ __forceinline__ int finish(const Params& P, Shared& s, const Row& r, const Weight& w, float per_place, int64_t row, int n,
                                     bool exact) {
   const Plan p = s.plan;
   const uint64_t least_w = r.min_p > 0.f ? w.part_up(r.min_p) : 0;
   const uint32_t most = r.top_k > 0 ? static_cast<uint32_t>(r.top_k) : 0xffffffffu;
-  const int per = (n + kThreads - 1) / kThreads, e0 = threadIdx.x * per, e1 = min(e0 + per, n);
+  constexpr int kTeam = kWarp ? 32 : kThreads;
+  Team<kWarp> team{s};
+  const int per = (n + kTeam - 1) / kTeam, e0 = threadIdx.x * per, e1 = min(e0 + per, n);
   // the mass before the intervals, of what is not collected
   const uint64_t seg0 = s.segment[0], seg1 = seg0 + s.segment[1], segs = seg1 + s.segment[2], seg2 = segs;
   // a candidate's interval, from its bin
@@ -566,8 +607,8 @@ __device__ __forceinline__ int finish(const Params& P, Shared& s, const Row& r, 
     mine += m;
     if (m >= least_w && rank_of(e, interval(e)) < most) kept += m;
   }
-  const uint64_t first = block_scan(mine, s, &all) - mine;  // of this thread's part
-  const uint64_t z1 = block_sum(kept, s) + segs;
+  const uint64_t first = team.scan(mine, &all) - mine;  // of this thread's part
+  const uint64_t z1 = team.sum(kept) + segs;
   const uint64_t off = exact || segs == 0 ? 0 : z1 >> 25;  // how far sums may be off
   bool unsure = false;
   // What is kept after top-p, and the token, of this thread's part.
@@ -591,11 +632,11 @@ __device__ __forceinline__ int finish(const Params& P, Shared& s, const Row& r, 
         if (rank < most && m >= least_w && (rank == 0 || upto < p_hi || (upto == p_hi && p_lo != 0))) top = upto + m;
       }
     }
-    const uint64_t least = block_min(pass == 1 ? token : ~top, s);
+    const uint64_t least = team.least(pass == 1 ? token : ~top);
     if (pass == 1) token = least;
     else z2 = ~least;
   }
-  if (__syncthreads_or(unsure)) return 1;
+  if (team.any(unsure)) return 1;
   if (token == ~uint64_t(0)) return 2;
   if (threadIdx.x == 0) {
     const int e = static_cast<int>(token);
@@ -977,21 +1018,29 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
       // Ranking takes the square of a CTA's share, sorting less of many (64 rows, 4 CTAs each: about 400, 800 and 1600 collected 48, 77
       // and 90 us ranked, 61, 82 and 86 sorted; 300 rows, one each, 400 and 800: 143 and 277, 149 and 249)
       const bool many = n > kCollect, few = !many && n * n <= kThreads * kThreads * kCtas;
-      if (few || (rank == 0 && !many)) {
-        for (int i = threadIdx.x; i < n; i += kThreads) s.unsorted[i] = head->list[i];
-        __syncthreads();
+      if (n <= 32) {
+        if (rank == 0 && threadIdx.x < 32) rank_few(s, w, n);
+      } else {
+        if (few || (rank == 0 && !many)) {
+          for (int i = threadIdx.x; i < n; i += kThreads) s.unsorted[i] = head->list[i];
+          __syncthreads();
+        }
+        if (few) rank_share<kCtas>(s, head, w, per_place, n, rank);
+        else if (rank == 0 && !many) sort_many(s, w, n);
+        cluster.sync();  // (and the first CTA's memory has been read)
+        if (many) break;
+        if (rank == 0) {
+          for (int i = threadIdx.x; i < n; i += kThreads) s.list[i] = s.sorted[i];
+          __syncthreads();
+        }
       }
-      if (few) rank_share<kCtas>(s, head, w, per_place, n, rank);
-      else if (rank == 0 && !many) sort_many(s, w, n);
-      cluster.sync();  // (and the first CTA's memory has been read)
-      if (many) break;
     }
     if (rank == 0) {
-      if (round == 0) {
-        for (uint32_t i = threadIdx.x; i < collected; i += kThreads) s.list[i] = s.sorted[i];
-        __syncthreads();
-      }
-      const int left = finish(P, s, r, w, per_place, row, static_cast<int>(collected), round > 0);
+      const int n = static_cast<int>(collected);
+      const bool exact = round > 0;
+      int left = 0;
+      if (n > kFew) left = finish<false>(P, s, r, w, per_place, row, n, exact);
+      else if (threadIdx.x < 32) left = finish<true>(P, s, r, w, per_place, row, n, exact);
       if (threadIdx.x == 0) s.unsure = left;
       if (left && threadIdx.x < 3) s.segment[threadIdx.x] = 0;
     }
