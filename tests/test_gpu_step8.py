@@ -108,6 +108,35 @@ def test_append_many_requests(pkv, kind):
     run_append(pkv, rng.integers(0, 60, n), np.ones(n, int), 2, 1, 128, 128, kind, seed=8)
 
 
+@pytest.mark.parametrize("hq,hkv,rot,inter", [(3, 3, 64, True), (8, 8, 128, False), (20, 20, 32, False), (40, 5, 0, False)])
+def test_append_single_tokens_of_any_number_of_heads(pkv, hq, hkv, rot, inter):
+    rng = np.random.default_rng(hkv)
+    run_append(pkv, rng.integers(0, 60, 70), np.ones(70, int), hq, hkv, 128, rot, "e4m3", inter=inter, seed=hkv)
+    run_append(pkv, rng.integers(0, 60, 9), rng.integers(0, 2, 9), hq, hkv, 128, rot, "e4m3", inter=inter, seed=hkv, in_place=True)
+
+
+def test_append_single_tokens_that_are_infinite_or_fit_nowhere(pkv):
+    tables, lens, qsl, pool, qkv, cs = append_case([20, 5, 40, 9, 30], [1] * 5, 4, 2, 128, 128, "e4m3", 3)
+    qkv[3, 4 * 128:4 * 128 + 4] = torch.tensor([float("inf"), -float("inf"), float("nan"), 3.0]).bfloat16()
+    tables[1, 0] = pool + 7              # a bad block
+    lens[2] = 16 * tables.shape[1] + 5   # past the table's row
+    cs = cs[:30]                         # request 4: its position (30) has no row
+    q, k, v = split(qkv, 4, 2, 128)
+    cache, scales = ref.pool8(pool, 2, 3)
+    want_c, want_s = cache.copy(), scales.copy()
+    good = [0, 3]
+    f = lambda x: x[good].float().numpy()  # noqa: E731
+    ref.append(None, f(k), f(v), cs, want_c[0], want_c[1], tables[good], lens[good], np.array([0, 1, 2]), want_s)
+    gc, gs = gpu(cache, scales)
+    out = pkv.pkv_rope_append(k.cuda(), v.cuda(), gpu(cs), gc[0], gc[1], *gpu(tables, lens, qsl), 1, q=q.cuda(), scales=gs).cpu()
+    assert pkv.pkv_peek_error_bits() == 1 + 4 and pkv.pkv_get_last_error() == pkv.PKV_ERR_INDEX
+    assert not out[2].any() and not out[4].any()
+    for t, p in ((0, 20), (1, 5), (3, 9)):
+        torch.testing.assert_close(out[t], torch.from_numpy(ref.rotated(q[t].float().numpy(), cs[p], False)).bfloat16(), rtol=0, atol=0)
+    np.testing.assert_array_equal(gs.cpu().numpy(), want_s)
+    np.testing.assert_array_equal(gc.cpu().numpy() & 127, want_c & 127)  # (a NaN has either sign)
+
+
 def test_append_grows_a_block_token_by_token(pkv):
     # one block filled token by token, sizes doubling: each token's codes come out as if written once in the last units,
     # since the codes stay in the normal range
