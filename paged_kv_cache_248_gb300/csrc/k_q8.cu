@@ -18,8 +18,8 @@
 // reference is the largest w vs of it, and out again of the row's sum, which takes p / vs.
 // Scores, maxima, sums and accumulators are fp32.
 //
-// This kernel serves steps in which every request brings one token: the G query heads of a kv head are the rows,
-// 8 or 16 of them.  (Requests with more tokens: k_q8_chunk.cu.)  A softmax thread is one key of the tile: its
+// This kernel serves requests of one token: the G query heads of a kv head are the rows, 8 or 16 of them.  (Requests with
+// more tokens, and a few single ones beside them: k_q8_chunk.cu.)  A softmax thread is one key of the tile: its
 // scales are its own, and its row sums stay in registers until the unit ends.  The reference of a row moves only
 // when a score of the tile exceeds it by 2^5, which a vote of the threads tells; only then is a maximum taken
 // across them and O rescaled.
@@ -32,6 +32,8 @@
 // Per CTA, two to an SM so that one's unit ends while the other streams (192 threads each): warp 0 walks its run
 // (q8_units.cuh) and loads K and V by TMA (16 rows of 128 bytes a block, 128-byte swizzle, three tiles in flight), warp 1
 // issues the MMAs, the others are softmax.  All waits are bounded.
+#include <algorithm>
+
 #include "q8_units.cuh"
 
 namespace pkv {
@@ -575,12 +577,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
 }
 
-__global__ void __launch_bounds__(kMergeThreads) q8_merge_kernel(const Q8Params P) {
+// The partials of one kernel, and of the other from slot `first` on.
+struct Partials {
+  const Cut* cuts;
+  const float *o, *ml;
+  int rows_cap;
+};
+__global__ void __launch_bounds__(kMergeThreads) q8_merge_kernel(const Q8Params P, const Partials one, const Partials other, int first) {
   const int lane = threadIdx.x & 31;
   grid_dep_wait();
   grid_dep_launch();
+  const int at_slot = static_cast<int>(blockIdx.x);
+  const bool is_other = at_slot >= first;
   join_rows<4>(
-      P.cuts, P.part_o, P.part_ml, P.rows_cap,
+      is_other ? other.cuts : one.cuts, is_other ? other.o : one.o, is_other ? other.ml : one.ml, is_other ? other.rows_cap : one.rows_cap,
       [&](const Cut& cut, int row) {
         return (row >> P.gp_log2) < cut.rows[0] && (row & ((1 << P.gp_log2) - 1)) < P.group;
       },
@@ -593,7 +603,8 @@ __global__ void __launch_bounds__(kMergeThreads) q8_merge_kernel(const Q8Params 
         const int64_t t = static_cast<int64_t>(cut.t0) + cut.first[0] + (row >> P.gp_log2);
         const int64_t at = (t * P.hq + static_cast<int64_t>(cut.head) * P.group + (row & ((1 << P.gp_log2) - 1))) * 128;
         reinterpret_cast<uint2*>(P.out + at)[lane] = zero ? make_uint2(0, 0) : packed;
-      });
+      },
+      is_other ? at_slot - first : at_slot, is_other ? static_cast<int>(gridDim.x) - first : first);
 }
 
 int gp_log2_of(int group) {
@@ -602,20 +613,20 @@ int gp_log2_of(int group) {
   return g;
 }
 
-// A step with one token a request takes the kernel of this file, any other the one of k_q8_chunk.cu.
+// The partials of a kernel: the one of this file (`single`), or that of k_q8_chunk.cu.
 struct Layout {
   int rows_cap, runs;
   size_t o_bytes, ml_bytes, bytes;
 };
-Layout layout_of(int32_t group, int32_t max_query_len, int num_sms) {
+Layout layout_of(bool single, int32_t group, int32_t max_query_len, int num_sms) {
   Layout l;
-  const int64_t rows = static_cast<int64_t>(max_query_len) << gp_log2_of(group);
+  const int64_t rows = static_cast<int64_t>(single ? 1 : max_query_len) << gp_log2_of(group);
   l.rows_cap = static_cast<int>(rows < 256 ? rows : 256);
-  l.runs = max_query_len == 1 ? num_sms * kCtasPerSm : num_sms;
+  l.runs = single ? num_sms * kCtasPerSm : num_sms;
   const size_t slots = 2 * static_cast<size_t>(l.runs) * l.rows_cap;
   l.o_bytes = slots * 128 * sizeof(float);
   l.ml_bytes = (slots * 2 * sizeof(float) + 255) & ~static_cast<size_t>(255);
-  l.bytes = l.o_bytes + l.ml_bytes + 2 * l.runs * sizeof(Cut);
+  l.bytes = (l.o_bytes + l.ml_bytes + 2 * l.runs * sizeof(Cut) + 255) & ~static_cast<size_t>(255);
   return l;
 }
 
@@ -632,28 +643,17 @@ int launch_single(const AttnArgs& a, const Q8Params& p, uint64_t rows, int ctas,
 }  // namespace
 
 size_t q8_workspace(const pkv_cache_desc& c, int32_t num_q_heads, int32_t max_query_len, int num_sms) {
-  return layout_of(num_q_heads / c.num_kv_heads, max_query_len, num_sms).bytes;
+  const int32_t group = num_q_heads / c.num_kv_heads;
+  return layout_of(true, group, max_query_len, num_sms).bytes +
+         (max_query_len > 1 ? layout_of(false, group, max_query_len, num_sms).bytes : 0);
 }
 
 int launch_q8(const AttnArgs& a, const float* scales, void* workspace, int num_sms, uint32_t* err, cudaStream_t s) {
   const int hkv = a.cache.num_kv_heads, group = a.num_q_heads / hkv;
   const uint64_t rows = static_cast<uint64_t>(a.cache.num_blocks) * hkv * kBlock;
   if (rows >= (1ull << 31)) return PKV_ERR_UNSUPPORTED;
-  const Layout l = layout_of(group, a.max_query_len, num_sms);
-  const bool single = a.max_query_len == 1;
   Q8Params p{};
   p.gp_log2 = gp_log2_of(group);
-  p.unit_q_log2 = single ? 0 : 8 - p.gp_log2;
-  // CTAs: all that fit, fewer where the caller's bounds leave less to do
-  const int64_t units = (((static_cast<int64_t>(a.max_query_len) - 1) >> p.unit_q_log2) + 1) * hkv;
-  const int64_t key_tiles = (static_cast<int64_t>(a.max_seq_len) + kTileKeys - 1) / kTileKeys;
-  const int64_t tiles = units >= l.runs ? units : units * key_tiles;  // (enough to know)
-  const int64_t most = tiles >= l.runs ? tiles : tiles * a.num_seqs;
-  const int ctas = static_cast<int>(most < l.runs ? most : l.runs);
-  // (a unit's beginning and end as key tiles.  8 requests of 512 tokens: 146, 130, 125, 124, 129 us with 1, 2, 3, 4, 6; 33 of 1
-  // to 61: 39.9, 36.8, 36.8, 38.2, 39.2.  Single tokens: no difference)
-  p.unit_cost = most < l.runs ? 0 : single ? 2 : 3;
-  p.min_run = 1 + p.unit_cost;
   p.q = static_cast<const __nv_bfloat16*>(a.q);
   p.k_cache = static_cast<const uint8_t*>(a.k_cache);
   p.v_cache = static_cast<const uint8_t*>(a.v_cache);
@@ -664,9 +664,6 @@ int launch_q8(const AttnArgs& a, const float* scales, void* workspace, int num_s
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.out_v8 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 ? 1 : 0;
   p.err = err;
-  p.part_o = static_cast<float*>(workspace);
-  p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + l.o_bytes);
-  p.cuts = reinterpret_cast<Cut*>(static_cast<uint8_t*>(workspace) + l.o_bytes + l.ml_bytes);
   p.num_blocks = a.cache.num_blocks;
   p.num_tokens = a.num_tokens;
   p.num_seqs = a.num_seqs;
@@ -675,13 +672,47 @@ int launch_q8(const AttnArgs& a, const float* scales, void* workspace, int num_s
   p.hkv = hkv;
   p.hq = a.num_q_heads;
   p.group = group;
-  p.rows_cap = l.rows_cap;
   p.scale_log2 = a.scale * 1.4426950408889634f;
-  const int st = !single     ? launch_q8_chunks(p, ctas, s)
-                 : group > 8 ? launch_single<2>(a, p, rows, ctas, s)
-                             : launch_single<1>(a, p, rows, ctas, s);
-  if (st) return st;
-  return cuda_status(launch_k(q8_merge_kernel, dim3(2 * ctas, merge_ctas(l.rows_cap)), dim3(kMergeThreads), 0, s, p));
+  // Steps of single tokens take the kernel of this file, others that of k_q8_chunk.cu, and where many requests must be, or are likely
+  // to be, of one token beside longer ones, each kernel takes its own.  One kernel and two: 256 requests of 500 to 3000 keys beside 2 chunks
+  // of 512 465 and 197 us, 100 beside 8 288 and 188, 16 beside one 52 and 49; 64 requests of 30 tokens 87 and 96, of 5 79 and 84,
+  // 8 of 16 24 and 29
+  const bool single = a.max_query_len == 1;
+  const bool both = !single && (a.num_tokens < 2 * static_cast<int64_t>(a.num_seqs) ||
+                                static_cast<int64_t>(a.max_query_len) * a.num_seqs >= 4 * a.num_tokens);
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  Partials parts[2] = {};
+  int ctas[2] = {0, 0};
+  for (int k = 0; k < 2; ++k) {  // single tokens, chunks
+    if (k == 0 ? !single && !both : single) continue;
+    const Layout l = layout_of(k == 0, group, a.max_query_len, num_sms);
+    Q8Params x = p;
+    x.unit_q_log2 = k == 0 ? 0 : 8 - p.gp_log2;
+    x.least_q = k == 1 && both ? 2 : 1;
+    x.most_q = k == 0 ? 1 : a.max_query_len;
+    x.reports = k == 0 || !both;
+    // CTAs: all that fit, fewer where the caller's bounds leave less to do
+    const int64_t units = (((static_cast<int64_t>(x.most_q) - 1) >> x.unit_q_log2) + 1) * hkv;
+    const int64_t key_tiles = (static_cast<int64_t>(a.max_seq_len) + kTileKeys - 1) / kTileKeys;
+    const int64_t tiles = units >= l.runs ? units : units * key_tiles;  // (enough to know)
+    const int64_t most = tiles >= l.runs ? tiles : tiles * a.num_seqs;
+    ctas[k] = static_cast<int>(most < l.runs ? most : l.runs);
+    // (a unit's beginning and end as key tiles.  8 requests of 512 tokens: 146, 130, 125, 124, 129 us with 1, 2, 3, 4, 6; 33 of 1
+    // to 61: 39.9, 36.8, 36.8, 38.2, 39.2.  Single tokens: no difference)
+    x.unit_cost = most < l.runs ? 0 : k == 0 ? 2 : 3;
+    x.min_run = 1 + x.unit_cost;
+    x.rows_cap = l.rows_cap;
+    x.part_o = reinterpret_cast<float*>(at);
+    x.part_ml = reinterpret_cast<float*>(at + l.o_bytes);
+    x.cuts = reinterpret_cast<Cut*>(at + l.o_bytes + l.ml_bytes);
+    parts[k] = Partials{x.cuts, x.part_o, x.part_ml, l.rows_cap};
+    at += l.bytes;
+    const int st = k == 1 ? launch_q8_chunks(x, ctas[k], s) : group > 8 ? launch_single<2>(a, x, rows, ctas[k], s) : launch_single<1>(a, x, rows, ctas[k], s);
+    if (st) return st;
+  }
+  const unsigned rows_ctas = std::max(merge_ctas(parts[0].rows_cap), merge_ctas(parts[1].rows_cap));
+  return cuda_status(launch_k(q8_merge_kernel, dim3(2 * (ctas[0] + ctas[1]), rows_ctas), dim3(kMergeThreads), 0, s, p, parts[0], parts[1],
+                              2 * ctas[0]));
 }
 
 }  // namespace pkv

@@ -32,6 +32,8 @@ struct Q8Params {
   Cut* cuts;       // [2 * runs]
   int64_t num_blocks, num_tokens;
   int32_t num_seqs, max_blocks, max_q, hkv, hq, group, gp_log2, unit_q_log2, unit_cost, rows_cap, min_run, out_v8;
+  int32_t least_q, most_q;  // tokens of the requests that the kernel takes
+  int32_t reports;          // it zeroes the rows of those that do not fit
   float scale_log2;
 };
 int launch_q8_chunks(const Q8Params& p, int ctas, cudaStream_t s);
@@ -123,8 +125,9 @@ __device__ __forceinline__ Request make_request(const Q8Params& P, int32_t q0, i
   r.q_len = static_cast<int32_t>(max(int64_t(0), min(static_cast<int64_t>(q1), P.num_tokens) - r.t0));
   r.len = len;
   r.wrong = !real || (rows && !fits);
-  r.units = fits ? ((r.q_len - 1) >> P.unit_q_log2) + 1 : 0;
-  r.head_cost = fits ? r.before(P, r.units - 1) + r.tiles(P, r.units - 1) + P.unit_cost : 0;
+  const bool takes = fits && n >= P.least_q && n <= P.most_q;
+  r.units = takes ? ((r.q_len - 1) >> P.unit_q_log2) + 1 : 0;
+  r.head_cost = takes ? r.before(P, r.units - 1) + r.tiles(P, r.units - 1) + P.unit_cost : 0;
   return r;
 }
 
@@ -197,7 +200,7 @@ __device__ __forceinline__ void find_run(const Q8Params& P, Run<kThreads>& c) {
       at += places;
     }
   }
-  if (any_wrong) zero_wrong(P);
+  if (any_wrong && P.reports) zero_wrong(P);
   __syncthreads();
 }
 

@@ -109,19 +109,20 @@ __device__ __forceinline__ Joined<E> join_parts(const float* part_o, const float
   return j;
 }
 
-// Joins this CTA's rows of the unit whose part the record at slot blockIdx.x is (all threads); calls
+// Joins this CTA's rows of the unit whose part the record at `slot` of `slots` is (all threads); calls
 // store(cut, row, joined) by whole warps, where live(cut, row) says that the row is one.
 template <int E, typename Live, typename Store>
 __device__ __forceinline__ void join_rows(const Cut* cuts, const float* part_o, const float* part_ml, int rows_cap, Live&& live,
-                                          Store&& store) {
+                                          Store&& store, int slot = static_cast<int>(blockIdx.x),
+                                          int slots = static_cast<int>(gridDim.x)) {
   __shared__ float s_m[kMergeWarps], s_l[kMergeWarps], s_o[kMergeWarps][32 * E];
   __shared__ int s_bad[kMergeWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int4* rec = reinterpret_cast<const int4*>(cuts + blockIdx.x);
+  const int4* rec = reinterpret_cast<const int4*>(cuts + slot);
   const int4 c0 = __ldcg(rec), c1 = __ldcg(rec + 1);
   const Cut cut{c0.x, c0.y, c0.z, c0.w, {c1.x, c1.y}, {c1.z, c1.w}};
-  const int begin = static_cast<int>(blockIdx.x >> 1) - cut.share;
-  if (cut.parts < 2 || begin < 0 || begin + cut.parts > static_cast<int>(gridDim.x >> 1)) return;
+  const int begin = (slot >> 1) - cut.share;
+  if (cut.parts < 2 || begin < 0 || begin + cut.parts > slots >> 1) return;
   const bool split = cut.parts > kManyParts;
   const int rows_at_once = split ? 1 : kMergeWarps, place = split ? 0 : warp;
   const int p0 = split ? cut.parts * warp / kMergeWarps : 0;

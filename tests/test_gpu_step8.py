@@ -261,6 +261,27 @@ def test_attention_many_requests(pkv):
     check_attention(pkv, rng.integers(0, 90, 200), rng.integers(0, 4, 200), 4, 1, seed=3)
 
 
+@pytest.mark.parametrize("hq,hkv", [(4, 1), (2, 2), (16, 1), (6, 2)])
+@pytest.mark.parametrize("ctx,new", [([500, 0, 127, 128, 40, 3000, 7, 16, 90, 15, 200, 33], [1, 1, 1, 1, 200, 1, 1, 0, 1, 1, 0, 1]),
+                                     ([0] * 20 + [70], [1] * 20 + [3]), ([9, 300, 2], [1, 2, 1]), ([10] * 9, [0] * 7 + [50, 1])])
+def test_attention_single_tokens_beside_chunks(pkv, hq, hkv, ctx, new):
+    check_attention(pkv, ctx, new, hq, hkv, seed=hq)
+
+
+def test_attention_single_tokens_beside_chunks_with_bad_pages_and_lengths(pkv):
+    ctx, new = [300, 40, 5, 77, 600, 9, 30, 20], [1, 1, 90, 1, 1, 1, 1, 1]
+
+    def change(cache, scales, tables, lens, qsl):
+        tables[0, 4] = len(scales) + 5       # a single token's page
+        lens[3] = 16 * tables.shape[1] + 1   # longer than its table
+        lens[5] = 0                          # less than its tokens
+    check_attention(pkv, ctx, new, 4, 2, seed=3, bad=(0, 3, 5), change=change)
+
+    def change_chunk(cache, scales, tables, lens, qsl):
+        tables[2, 1] = -1
+    check_attention(pkv, ctx, new, 4, 2, seed=3, bad=(2,), change=change_chunk)
+
+
 def test_attention_sharp_scores(pkv):
     check_attention(pkv, [700, 90], [1, 40], 8, 2, seed=4, q_scale=12.0)
 
