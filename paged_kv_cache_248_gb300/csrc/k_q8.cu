@@ -697,9 +697,9 @@ int launch_q8(const AttnArgs& a, const float* scales, void* workspace, int num_s
     const int64_t tiles = units >= l.runs ? units : units * key_tiles;  // (enough to know)
     const int64_t most = tiles >= l.runs ? tiles : tiles * a.num_seqs;
     ctas[k] = static_cast<int>(most < l.runs ? most : l.runs);
-    // (a unit's beginning and end as key tiles.  8 requests of 512 tokens: 146, 130, 125, 124, 129 us with 1, 2, 3, 4, 6; 33 of 1
-    // to 61: 39.9, 36.8, 36.8, 38.2, 39.2.  Single tokens: no difference)
-    x.unit_cost = most < l.runs ? 0 : k == 0 ? 2 : 3;
+    // (a unit's beginning and end as key tiles.  8 requests of 512 tokens: 118.9, 118.5, 118.9, 120.1 us with 2, 3, 4, 5; 33 of 1 to 61:
+    // 34.3, 35.5, 36.9, 38.3; 64 of 30: 88.5, 87.8, 86.3, 87.5.  Single tokens: no difference)
+    x.unit_cost = most < l.runs ? 0 : 2;
     x.min_run = 1 + x.unit_cost;
     x.rows_cap = l.rows_cap;
     x.part_o = reinterpret_cast<float*>(at);
