@@ -468,6 +468,8 @@ __device__ __forceinline__ void row_weights(uint32_t taddr, uint32_t orow, bool 
     const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
     if (__any_sync(0xffffffffu, most > kTop + kMost)) {  // (rare)
       const float by = most > kTop + kMost ? ceilf(most - kTop) : 0.f, alpha = exp2f(-by);
+      // (what is read again here may still be on its way: weights of the quarters before, O of a move before)
+      tmem_st_wait();
       if (has_o) scale_o(orow, alpha);
       scale_p(taddr, h, alpha);
       sum *= alpha;

@@ -457,6 +457,26 @@ def test_attention_scores_that_grow_with_the_context(pkv, ctx, new):
         assert (np.abs(out.double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -9 + np.expm1(2 * grain)) * of).all()
 
 
+@pytest.mark.parametrize("new", [3, 40])
+def test_attention_scores_that_grow_within_a_tile(pkv, new):
+    # each 32 keys of a tile 2^20 above those before: a reference moves in every quarter of the tile, over weights that
+    # have just been stored and sums that were rescaled a quarter before
+    scale = 128 ** -0.5
+    for ctx in (300, 450):
+        tables, lens, qsl, pool = ref.requests([ctx], [new], 11)
+        cache, scales = ref.pool8(pool, 2, 11)
+        cache[0] = 0  # (scores come from one element alone)
+        step = 20 * np.log(2.0)
+        for p in range(int(lens[0])):
+            cache[0, tables[0][p // 16], :, p % 16, 0] = ref.encode8(np.full(1, 2.0 * (p // 32)))[0]
+        scales[..., 0] = 1.0
+        q = torch.zeros((new, 4, 128)).bfloat16()
+        q[..., 0] = step / (2.0 * scale)
+        out = pkv.paged_attention_q8(q.cuda(), *gpu(cache[0], cache[1], scales, tables, lens, qsl), scale, new, int(lens[0]))
+        want, of = ref.attention(q.double().numpy(), cache[0], cache[1], scales, tables, lens, qsl, scale)
+        assert (np.abs(out.double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -9 * of).all()
+
+
 @pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-30])
 @pytest.mark.parametrize("new", [[1, 1], [1, 40]])
 def test_attention_scales_of_the_scores(pkv, scale, new):

@@ -1,5 +1,7 @@
 """A decoding step over a cache in 8 bits, without a GPU: the plain implementations, the host checks, the binding's refusals."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -55,6 +57,21 @@ def test_sampling_by_counting():
     assert ref.sample(x, [0.99], top_p=[0.6])[0][0] == 0
     assert ref.sample(x, [0.99], min_p=[0.9])[0][0] == 1
     assert ref.sample(np.full((1, 3), np.nan, np.float32), [0.5])[0][0] == -1
+
+
+def source(name):
+    """A kernel's source without its comments."""
+    import paged_kv_cache_248_gb300 as m
+    with open(os.path.join(os.path.dirname(m.__file__), "csrc", name)) as f:
+        return re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
+
+
+def test_weights_are_waited_for_before_they_are_read_again():
+    # stores to tensor memory are asynchronous, and a load waits for loads only: an order that no result shows
+    s = source("k_q8_chunk.cu")
+    body = s[s.index("void row_weights("):s.index("void softmax_warps(")]
+    move = body[body.index("most > kTop + kMost"):]
+    assert 0 < move.find("tmem_st_wait()") < min(move.index("scale_o("), move.index("scale_p("))
 
 
 P = ctypes.c_void_p
