@@ -765,6 +765,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
   if (threadIdx.x < 3) s.segment[threadIdx.x] = 0;
   if (threadIdx.x == 4) s.collected = s.taken = 0;
   if (threadIdx.x == 5) s.best = 0x7fffffffu;
+  if constexpr (kCtas > 1) cluster.barrier_arrive();
   grid_dep_wait();
   grid_dep_launch();
   Row r;
@@ -809,6 +810,10 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
       s.warp_low[threadIdx.x >> 5] = logit_of(static_cast<uint64_t>(b) << 32);
     }
     __syncthreads();
+    // (a CTA's shared memory is there once the CTA runs, which its arrival tells; one row of 32000, 8 CTAs: no difference)
+    if constexpr (kCtas > 1) {
+      if (!again) cluster.barrier_wait();
+    }
     if (threadIdx.x < kCtas) {
       float x = -INFINITY, y = INFINITY;
 #pragma unroll

@@ -660,6 +660,23 @@ def test_sample_many_rows_of_a_large_vocabulary(pkv, n, v):
     check_sample(pkv, x.bfloat16(), u, top_p=p)
 
 
+@pytest.mark.parametrize("n,v", [(70, 2048), (150, 2300), (40, 4096), (76, 5000), (3, 8192), (19, 9001)])
+def test_sample_short_rows_of_several_ctas(pkv, n, v):
+    # the shortest rows that 2, 4 and 8 CTAs share, beside a kernel that holds SMs, so that CTAs of a cluster begin apart
+    x = peaked(n, v, v).bfloat16().cuda()
+    u = np.random.default_rng(v).random(n, dtype=np.float32)
+    gu, busy, side = gpu(u), torch.randn((2048, 2048), device="cuda"), torch.cuda.Stream()
+    want, _ = ref.sample(x.float().cpu().numpy(), u)
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(30):
+        with torch.cuda.stream(side):
+            busy @ busy
+        got.append(pkv.pkv_sample(x, gu)[0])
+    for tokens in got:
+        np.testing.assert_array_equal(tokens.cpu().numpy(), want)
+
+
 def test_sample_largest_vocabulary(pkv):
     v = 1 << 20
     x = peaked(2, v, 5, sigma=1.0)

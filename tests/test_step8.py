@@ -74,6 +74,15 @@ def test_weights_are_waited_for_before_they_are_read_again():
     assert 0 < move.find("tmem_st_wait()") < min(move.index("scale_o("), move.index("scale_p("))
 
 
+def test_a_clusters_shared_memory_is_touched_once_all_of_it_runs():
+    # a CTA may begin long after its cluster's others, and has no shared memory before
+    s = source("k_sample.cu")
+    body = s[s.index("sample_kernel(const Params P)"):]
+    first = body.index("map_shared_rank(")
+    assert 0 < body.find("cluster.barrier_arrive()") < body.find("grid_dep_wait()")
+    assert 0 < body.find("cluster.barrier_wait()") < first < body.index("cluster.sync()")
+
+
 P = ctypes.c_void_p
 FAKE = P(0x10000)  # never dereferenced: every call below fails its host checks first
 
