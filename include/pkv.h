@@ -485,11 +485,13 @@ PKV_API int pkv_rope_append(const void* q, const void* k, const void* v, int32_t
  * query heads a kv head): the same sum over K_u = code * scales[b][g][0] and V_u = code * scales[b][g][1] of
  * block b = block_tables[i][u / 16].  q and out are bf16.  Chunks and single tokens mix freely.
  * scales          device fp32 [num_blocks][num_kv_heads][2]; positive.  V's are taken as at least 2^-80 and at
- *                 most 2^110; a key whose weight times V's scale is less than 2^-120 of the context's largest such product may
- *                 be left out
+ *                 most 2^110
  * max_query_len   host bound on q_i: a request with more is flagged (PKV_ERR_INDEX) and its rows zeroed
  * query_start_loc rows outside of [0, num_tokens) are flagged too; rows that no request has stay as they are
  * workspace       device memory of at least pkv_q8_workspace() bytes, 256-byte aligned
+ * A key counts by its weight times V's scale, next to the largest such product that the row sees: where max_query_len is 1, a
+ * product is held to 2^-11 of itself down to 2^-29 of the largest, and to 2^-40 of the largest below; otherwise to 2^-21 and
+ * 2^-32.  The sum of the weights takes fp32 ones; products below 2^-120 of the largest may be left out there too.
  * What a row does not see (later tokens of its chunk, slots behind the context) has no part in it, whatever its
  * codes are, NaN among them.  A NaN that a row sees makes elements of the row NaN: those of its column at least, of a NaN in K
  * or a query all.  An element of a query counts down to 2^-22 of the largest one among its unit's rows (the heads of a kv

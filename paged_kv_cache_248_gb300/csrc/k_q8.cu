@@ -11,9 +11,10 @@
 // The other operands, queries and weights, are split into e4m3 terms side by side in the columns:
 //   q = (hi + lo / 32) / c, c a power of two for a unit's rows: a bf16 has 8 significant bits, two terms of 4
 //     each give them exactly, down to 2^-22 of the unit's largest element;
-//   p = hi + mid / 32 + lo / 1024 of a weight p rounded to fp16 (2^-11): three terms hold it down to 2^-20,
-//     2^-23 of a row's largest weight at least, so that a hundred thousand small weights beside a large
-//     one keep their share, which two terms (2^-18) do not.
+//   p = hi + mid / 32 + lo / 1024 of a weight p rounded to fp16 (2^-11); of a small one, below 2^-9, the terms of 2^17 p,
+//     in three more columns.  So a weight is held to 2^-11 of itself down to 2^-26, which is 2^-29 of a row's largest weight
+//     at least, and smaller ones to 2^-37 (2^-40): a million small weights beside a large one keep their share
+//     even where the large one's V is 0.
 // Scales: ks multiplies a key's scores.  vs goes into the weight, as log2 vs added to the score, so that a row's
 // reference is the largest w vs of it, and out again of the row's sum, which takes p / vs.
 // Scores, maxima, sums and accumulators are fp32.
@@ -25,8 +26,8 @@
 // across them and O rescaled.
 //
 // Bound: HBM, once the cache is larger than a few MB.  32 requests of 32768 keys, 64 / 8 heads, 2.15 GB: 311 us, 103 % of the measured
-// copy rate (DRAM 87 % busy); 64 requests of 128 to 4096 keys, 279 MB: 51 us, 81 %, of which 4 are the start and 4 the
-// join.  One request of 500 keys: 8.7 us of latency, 3 of them the join's launch.  Bytes pass through shared memory twice (TMA in,
+// copy rate (DRAM 87 % busy); 64 requests of 128 to 4096 keys, 279 MB: 52 us, 80 %, of which 4 are the start and 4 the
+// join; with 128 / 8 heads, 282 MB, 55 us.  The columns of small weights cost none, 0.3 and 1.2 of these.  One request of 500 keys: 8.7 us of latency, 3 of them the join's launch.  Bytes pass through shared memory twice (TMA in,
 // the tensor core out); the tensor pipe is 7 % busy.
 //
 // Per CTA, two to an SM so that one's unit ends while the other streams (192 threads each): warp 0 walks its run
@@ -41,8 +42,9 @@ namespace {
 
 constexpr int kHalfTile = kTileKeys * 128;  // K or V of a tile, bytes
 constexpr int kStages = 3, kThreads = 192, kCtasPerSm = 2;
-constexpr uint32_t kTmemCols = 128;  // S of even and of odd tiles (32 columns each), O (48)
-constexpr uint32_t kSCols = 32, kOCol = 64;
+constexpr uint32_t kSCols = 32, kOCol = 64;  // tensor memory: S of even and of odd tiles, O
+constexpr int kTerms = 6;                    // of a weight: three, and three for small ones
+constexpr float kSmall = 1.f / 512.f, kUp = 131072.f, kDown = 1.f / 131072.f;  // 2^-9, 2^17, 2^-17
 constexpr float kTop = 3.f;   // log2 of a row's largest weight when its reference is set
 constexpr float kMost = 8.f;  // and the most that it may reach: the rest of a term is then at most 8 units
 
@@ -62,9 +64,13 @@ struct Ctl {
   int abort_flag;
 };
 
-constexpr int kQBytes = 2 * 16 * 128, kPBytes = 3 * 2048;
-constexpr int kSmemBytes = kStages * 2 * kHalfTile + kQBytes + kPBytes + static_cast<int>(sizeof(Ctl)) + 1024;
-static_assert(kSmemBytes <= 115712, "two CTAs an SM");
+template <int kOctets>
+struct Shape {
+  static constexpr uint32_t kOCols = 8 * kTerms * kOctets, kTmemCols = kOCol + kOCols <= 128 ? 128 : 256;
+  static constexpr int kQBytes = 16 * kOctets * 128, kPBytes = 128 * static_cast<int>(kOCols);
+  static constexpr int kSmemBytes = kStages * 2 * kHalfTile + kQBytes + kPBytes + static_cast<int>(sizeof(Ctl));
+  static_assert(kSmemBytes <= 115712 && kCtasPerSm * kTmemCols <= 512, "two CTAs an SM");
+};
 
 __device__ __forceinline__ void raise_abort(Ctl& c, uint32_t* err) {
   *reinterpret_cast<volatile int*>(&c.abort_flag) = 1;
@@ -147,7 +153,7 @@ __device__ void producer_warp(const Q8Params& P, const CUtensorMap* kmap, const 
 template <int kOctets>
 __device__ void mma_warp(const Q8Params& P, Ctl& c, uint32_t tiles, uint32_t qbuf, uint32_t pbuf, uint32_t tmem) {
   constexpr uint32_t s_idesc = umma_idesc_e4m3(128, 16 * kOctets, false, false);
-  constexpr uint32_t o_idesc = umma_idesc_e4m3(128, (24 * kOctets + 15) / 16 * 16, true, true);
+  constexpr uint32_t o_idesc = umma_idesc_e4m3(128, Shape<kOctets>::kOCols, true, true);
   volatile int* abort_flag = &c.abort_flag;
   uint32_t n = 0;  // tiles so far
   bool ok = true, issued = false;
@@ -414,8 +420,8 @@ __device__ __forceinline__ void softmax_warps(const Q8Params& P, Ctl& c, uint8_t
           }
           if (j > 0) {
 #pragma unroll 1
-            for (int k = 0; k < 3 * kOctets; ++k) {
-              const float4 f0 = c.factor[k / 3 * 2], f1 = c.factor[k / 3 * 2 + 1];
+            for (int k = 0; k < kTerms * kOctets; ++k) {
+              const float4 f0 = c.factor[k / kTerms * 2], f1 = c.factor[k / kTerms * 2 + 1];
               const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
               uint32_t o[8];
               tmem_ld8_sync(lanes + kOCol + 8 * k, o);
@@ -428,13 +434,15 @@ __device__ __forceinline__ void softmax_warps(const Q8Params& P, Ctl& c, uint8_t
         }
 #pragma unroll
         for (int g = 0; g < kOctets; ++g) {
-          uint32_t b[3][2] = {};
+          uint32_t b[3][2] = {}, small[2] = {};  // (all ones: of a small weight)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 z = both(x[4 * g + e]);
             const float p0 = ex2_approx(z.x), p1 = ex2_approx(z.y);
             l[4 * g + e] = fma2(two(p0, p1), two(iv), l[4 * g + e]);
-            const __half2 y = __floats2half2_rn(p0, p1);
+            const bool small0 = p0 < kSmall, small1 = p1 < kSmall;
+            small[e / 2] |= ((small0 ? 0xffu : 0u) | (small1 ? 0xff00u : 0u)) << (16 * (e & 1));
+            const __half2 y = __floats2half2_rn(p0 * (small0 ? kUp : 1.f), p1 * (small1 ? kUp : 1.f));
             const uint32_t hi = to_e4m3(y);
             const __half2 y1 = __hmul2(__hsub2(y, from_e4m3(hi)), __float2half2_rn(32.f));
             const uint32_t mid = to_e4m3(y1);
@@ -443,11 +451,12 @@ __device__ __forceinline__ void softmax_warps(const Q8Params& P, Ctl& c, uint8_t
             b[1][e / 2] |= mid << (16 * (e & 1));
             b[2][e / 2] |= to_e4m3(y2) << (16 * (e & 1));
           }
-#pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            const int o = 3 * g + k;  // its eight columns
-            *reinterpret_cast<uint2*>(p + (o >> 1) * 2048 + t * 16 + (o & 1) * 8) = make_uint2(b[k][0], b[k][1]);
-          }
+          // eight columns a term: those of weights that are not small, then of those that are
+          uint4* to = reinterpret_cast<uint4*>(p + kTerms / 2 * g * 2048 + t * 16);
+          const uint32_t s0 = small[0], s1 = small[1];
+          to[0] = make_uint4(b[0][0] & ~s0, b[0][1] & ~s1, b[1][0] & ~s0, b[1][1] & ~s1);
+          to[128] = make_uint4(b[2][0] & ~s0, b[2][1] & ~s1, b[0][0] & s0, b[0][1] & s1);
+          to[256] = make_uint4(b[1][0] & s0, b[1][1] & s1, b[2][0] & s0, b[2][1] & s1);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -489,16 +498,18 @@ __device__ __forceinline__ void softmax_warps(const Q8Params& P, Ctl& c, uint8_t
       __nv_bfloat16* out = P.out + (static_cast<int64_t>(item.t0) * P.hq + static_cast<int64_t>(item.head) * P.group) * 128 + t;
 #pragma unroll 1
       for (int g = 0; g < kOctets; ++g) {
-        uint32_t v[3][8];
+        uint32_t v[kTerms][8];
 #pragma unroll
-        for (int k = 0; k < 3; ++k) tmem_ld8_sync(lanes + kOCol + 24 * g + 8 * k, v[k]);
+        for (int k = 0; k < kTerms; ++k) tmem_ld8_sync(lanes + kOCol + 8 * (kTerms * g + k), v[k]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int r = 8 * g + e;
           const float4 y = c.across[r];
           const float sum = (y.x + y.y) + (y.z + y.w);
-          const float o =
-              fmaf(__uint_as_float(v[2][e]), 1.f / 1024.f, fmaf(__uint_as_float(v[1][e]), 1.f / 32.f, __uint_as_float(v[0][e])));
+          const auto sum_of = [&](int k) {
+            return fmaf(__uint_as_float(v[k + 2][e]), 1.f / 1024.f, fmaf(__uint_as_float(v[k + 1][e]), 1.f / 32.f, __uint_as_float(v[k][e])));
+          };
+          const float o = fmaf(sum_of(3), kDown, sum_of(0));
           if (r < P.group) {
             if (item.slot >= 0) {
               const int64_t row = static_cast<int64_t>(item.slot) * P.rows_cap + r;
@@ -528,12 +539,17 @@ __device__ __forceinline__ void softmax_warps(const Q8Params& P, Ctl& c, uint8_t
 template <int kOctets>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const Q8Params P) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* tiles = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  using S = Shape<kOctets>;
+  extern __shared__ __align__(1024) uint8_t tiles[];
   uint8_t* qbuf = tiles + kStages * 2 * kHalfTile;
-  uint8_t* pbuf = qbuf + kQBytes;
-  Ctl& c = *reinterpret_cast<Ctl*>(pbuf + kPBytes);
+  uint8_t* pbuf = qbuf + S::kQBytes;
+  Ctl& c = *reinterpret_cast<Ctl*>(pbuf + S::kPBytes);
   const int warp = threadIdx.x >> 5;
+  if ((smem_u32(tiles) & 1023u) != 0) {  // (there is no room to move up; swizzled tiles would not be where they are looked for)
+    grid_dep_wait();
+    if (threadIdx.x == 0) flag_error(P.err, kErrTimeout);
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&c.kfull[s], 1);
@@ -556,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     tma_prefetch_map(&vmap);
   }
   if (warp == 1) {
-    tmem_alloc(&c.tmem_base, kTmemCols);
+    tmem_alloc(&c.tmem_base, S::kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -573,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(tmem, S::kTmemCols);
   }
 }
 
@@ -636,8 +652,9 @@ int launch_single(const AttnArgs& a, const Q8Params& p, uint64_t rows, int ctas,
   int st = encode_tensor_map_2d(&km, a.k_cache, 64, rows, 128, 64, 16);
   if (!st) st = encode_tensor_map_2d(&vm, a.v_cache, 64, rows, 128, 64, 16);
   static uint64_t smem_set = 0;
-  if (!st) st = set_smem_once(reinterpret_cast<const void*>(q8_kernel<kOctets>), kSmemBytes, &smem_set);
-  return st ? st : cuda_status(launch_k(q8_kernel<kOctets>, dim3(ctas), dim3(kThreads), kSmemBytes, s, km, vm, p));
+  constexpr int kBytes = Shape<kOctets>::kSmemBytes;
+  if (!st) st = set_smem_once(reinterpret_cast<const void*>(q8_kernel<kOctets>), kBytes, &smem_set);
+  return st ? st : cuda_status(launch_k(q8_kernel<kOctets>, dim3(ctas), dim3(kThreads), kBytes, s, km, vm, p));
 }
 
 }  // namespace

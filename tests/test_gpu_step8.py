@@ -324,6 +324,32 @@ def test_attention_one_key_above_a_long_flat_rest(pkv, new):
         assert (np.abs(out.double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -9 * size).all()
 
 
+@pytest.mark.parametrize("new,hq", [(1, 4), (1, 16), (1, 11), (30, 4)])
+def test_attention_small_weights_beside_a_large_one(pkv, new, hq):
+    # so many requests that a CTA does all of one: its reference is the first key's weight, whose V is 0, and what comes
+    # out are the others' weights alone, 2^-14 to 2^-35 of it.  A single token's are held to 2^-11 of themselves down to 2^-29 of
+    # the largest, and to 2^-40 of it below; a chunk's to 2^-21 and 2^-32 (V is 2 at most).
+    n, requests, scale, least = 4000, 320 // new + 150, 128 ** -0.5, 2.0 ** (-40 if new == 1 else -32)
+    gaps = np.array([10.0, 13.0, 14.0, 15.0, 15.6, 16.0, 16.3, 17.0, 17.5, 18.0, 20.0, 22.0, 24.0])
+    tables, lens, qsl, pool = ref.requests([n], [new], 0)
+    cache, scales = np.zeros((2, pool, 1, 16, 128), np.uint8), np.ones((pool, 1, 2), np.float32)
+    cache[1] = ref.encode8(np.linspace(0.5, 2.0, 128))
+    first = tables[0][0]
+    cache[0, first, 0, 0, 0] = ref.encode8(np.full(1, 12.0))[0]
+    cache[1, first, 0, 0] = 0
+    q = torch.zeros((len(gaps), new, hq, 128)).bfloat16()
+    q[..., 0] = torch.from_numpy(gaps / (12.0 * scale))[:, None, None]
+    at = np.arange(requests) % len(gaps)
+    out = pkv.paged_attention_q8(q[at].flatten(0, 1).cuda(), *gpu(cache[0], cache[1], scales, tables.repeat(requests, 0), lens.repeat(requests),
+                                                                  (np.arange(requests + 1) * new).astype(np.int32)), scale, new, n + new)
+    one = q[:, :, :1].flatten(0, 1).double().numpy()  # (all heads are alike)
+    want, size = ref.attention(one, cache[0], cache[1], scales, tables.repeat(len(gaps), 0), lens.repeat(len(gaps)),
+                               np.arange(len(gaps) + 1) * new, scale)
+    pick = lambda x: x.reshape(len(gaps), new, 1, 128)[at]  # noqa: E731
+    off = np.abs(out.double().cpu().numpy().reshape(requests, new, hq, 128) - pick(want))
+    assert (off <= 2.0 ** -8 * np.abs(pick(want)) + 2.0 ** -9 * pick(size) + least * (n + new) * 2.0).all()
+
+
 def test_attention_outliers_of_a_query(pkv):
     # one element a thousand times the others: they keep their share of the scores
     tables, lens, qsl, pool = ref.requests([300], [1], 0)
