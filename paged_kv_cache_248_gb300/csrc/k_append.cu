@@ -14,9 +14,9 @@
 // hold a vector's partners.  With 16- or 32-bit caches a CTA, or a warp, takes a token's rows.  With 8 bits the new rows of one
 // (request, block, kv head, K or V) belong to a warp, up to 16 rows, 64 values a lane in registers, or with
 // one token a request to eight lanes: so the scale is known before anything is written and no one else writes it.
-// Request i touches at most ceil((q_i + 15) / 16) blocks, less than floor(qsl[i+1] / 16) -
-// floor(qsl[i] / 16) + 2, so block number x of a launch belongs to the last request with
-// floor(qsl[i] / 16) + 2 i <= x: no plan and no prefix sum.
+// Request i touches at most ceil((q_i + 15) / 16) blocks, at most floor(qsl[i+1] / 16) -
+// floor(qsl[i] / 16) + 2 (as many as that: two tokens in two blocks, neither number passing a multiple of 16), so block number x
+// of a launch belongs to the last request with floor(qsl[i] / 16) + 2 i <= x: no plan and no prefix sum.
 //
 // Bound: for few tokens the launch and five loads that depend on one another (one token 2.7 us, 64 tokens 2.6 us, floor 0.2);
 // for many, HBM: 5300 tokens in 8 chunks, 122 MB, 27.4 us (18.2 at the copy's rate; a CTA a token instead of a warp: 33.8).
@@ -58,13 +58,6 @@ __device__ __forceinline__ int last_request(int n, int64_t x, Start&& start) {
   }
   return lo;
 }
-
-// Where token t of request i goes.
-struct Place {
-  int64_t slot;   // -1: nowhere
-  int32_t angle;  // its row of the table
-  bool ok;
-};
 
 template <typename T>
 struct Row {

@@ -108,6 +108,11 @@ def test_append_many_requests(pkv, kind):
     run_append(pkv, rng.integers(0, 60, n), np.ones(n, int), 2, 1, 128, 128, kind, seed=8)
 
 
+@pytest.mark.parametrize("ctx,new", [([15], [2]), ([40, 31], [3, 2]), ([15, 15, 15], [2, 2, 2]), ([0, 14, 15], [13, 18, 17]), ([3, 15], [16, 18])])
+def test_append_requests_that_touch_as_many_blocks_as_they_can(pkv, ctx, new):
+    run_append(pkv, ctx, new, 4, 2, 128, 128, "e4m3", seed=sum(new))
+
+
 @pytest.mark.parametrize("hq,hkv,rot,inter", [(3, 3, 64, True), (8, 8, 128, False), (20, 20, 32, False), (40, 5, 0, False)])
 def test_append_single_tokens_of_any_number_of_heads(pkv, hq, hkv, rot, inter):
     rng = np.random.default_rng(hkv)
