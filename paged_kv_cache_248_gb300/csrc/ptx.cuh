@@ -208,8 +208,9 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-// 2^x by the MUFU instruction (PTX ex2.approx.ftz.f32): -inf gives +0, results below
-// 2^-126 flush to zero -- immaterial for softmax weights of at most 2^8.
+// 2^x by the MUFU instruction (PTX ex2.approx.ftz.f32): -inf gives +0, results below 2^-126 flush to zero.  That is
+// immaterial for softmax weights, of which a row's largest is 1 to 2^15 (the 8-bit attention of chunks), and for sampling's, at
+// most 1, of which nothing below 2^-64 counts.  1 / (V's scale) in the 8-bit attention is 2^-110 to 2^80.
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
