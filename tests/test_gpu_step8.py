@@ -628,6 +628,22 @@ def test_sample_temperatures_at_the_ends(pkv):
     check_sample(pkv, x, np.full(6, 0.9), temperature=np.array([1e-38, 1e-20, 1e-3, 100, 1e10, 3e38], np.float32))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("k", [20, 50, 1000, 9000, 10 ** 6])
+def test_sample_top_k_that_ends_far_below_the_largest(pkv, dtype, k):
+    # fewer than k logits within 2^-32 of the largest weight: which ones are kept matters to no sum
+    n, v = 12, 9000
+    x, u = peaked(n, v, k).to(dtype), np.random.default_rng(k).random(n, dtype=np.float32)
+    u[:3] = 0.0, 1 - 2.0 ** -24, 1e-30
+    s = dict(temperature=np.array([0.05, 0.1, 0.2, 0.3, 0.5, 1.0] * 2, np.float32), top_k=np.full(n, k, np.int32))
+    check_sample(pkv, x, u, **s)
+    check_sample(pkv, x, u, top_p=np.full(n, 0.95, np.float32), **s)
+    check_sample(pkv, x, u, min_p=np.full(n, 1e-12, np.float32), **s)
+    few = torch.full_like(x, torch.finfo(dtype).min)  # words that are not allowed have the type's lowest value
+    few[:, 100:130] = x[:, 100:130]
+    check_sample(pkv, few, u, **s)
+
+
 def test_sample_settings_out_of_range_are_flagged(pkv):
     nan = float("nan")
     x = peaked(6, 100, 3)
