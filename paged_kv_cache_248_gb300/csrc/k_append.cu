@@ -355,11 +355,12 @@ __global__ void __launch_bounds__(kThreads) append8_one_kernel(const Params P, i
   const int i = static_cast<int>(blockIdx.x / ctas_per_block);
   const int unit = static_cast<int>(blockIdx.x - static_cast<unsigned>(i) * ctas_per_block) * (kThreads / 8) + static_cast<int>(threadIdx.x >> 3);
   Request r;
-  if (!load_request(P, i, r)) {
+  const bool fits = load_request(P, i, r);
+  if (r.t0 == r.t1) return;  // (whatever its length is)
+  if (!fits) {
     if (threadIdx.x == 0) flag_error(P.err, kErrLength);
     return;
   }
-  if (r.t0 == r.t1) return;
   const int64_t id = __ldg(P.bt + static_cast<int64_t>(i) * P.max_blocks + r.ctx / kBlock);
   const int64_t angle = angle_of(P, r.t0, r.ctx);
   if (id < 0 || id >= P.num_blocks || angle < 0) {
@@ -414,7 +415,9 @@ __global__ void __launch_bounds__(kThreads) append8_kernel(const Params P, int u
   const auto start = [&](int at) { return static_cast<int64_t>(__ldg(P.qsl + at)) / kBlock + 2 * static_cast<int64_t>(at); };
   const int i = last_request(P.num_seqs, x, start);
   Request r;
-  if (!load_request(P, i, r)) {
+  const bool fits = load_request(P, i, r);
+  if (r.t0 == r.t1) return;  // (whatever its length is)
+  if (!fits) {
     if (lane_id == 0) flag_error(P.err, kErrLength);
     return;
   }

@@ -206,6 +206,25 @@ def test_append_bad_data_is_flagged_and_skipped(pkv, kind):
         assert torch.equal(gc[:, b], before[:, b]) == (b not in touched)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [[1, 1], [3, 20]])
+def test_append_the_lengths_of_empty_requests_are_not_looked_at(pkv, kind, new):
+    # a padded batch: places of requests that are not there, with lengths of any kind
+    tables, lens, qsl, pool, qkv, cs = append_case([4, 30], new, 4, 2, 128, 128, kind, 3)
+    q, k, v = split(qkv.cuda(), 4, 2, 128)
+    cache, scales = ref.pool8(pool, 2, 3)
+    got = []
+    for pad in (0, 5):
+        gc, gs = gpu(cache, scales) if kind == "e4m3" else (torch.zeros((2, pool, 2, 16, 128), dtype=torch.bfloat16, device="cuda"), None)
+        more = np.array([-7, 10 ** 6, 0, 2 ** 31 - 1, -2 ** 31])[:pad].astype(np.int32)
+        t = np.concatenate([tables, np.full((pad, tables.shape[1]), -1, np.int32)])
+        out = pkv.pkv_rope_append(k, v, gpu(cs), gc[0], gc[1], *gpu(t, np.concatenate([lens, more]), np.pad(qsl, (0, pad), mode="edge")),
+                                  max(new), q=q, scales=gs)
+        assert pkv.pkv_get_last_error() == 0
+        got.append((out, gc))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
 def test_append_leaves_rows_behind_the_last_request(pkv):
     for kind in ("bf16", "e4m3"):
         tables, lens, qsl, pool, qkv, cs = append_case([4, 9], [2, 1], 4, 2, 128, 128, kind, 3)
