@@ -526,6 +526,9 @@ PKV_API int pkv_q8_workspace(const pkv_cache_desc* cache, int32_t num_q_heads, i
  * uniform         device fp32 [num_seqs], in [0, 1)
  * out_tokens      device int32 [num_seqs]
  * out_logprobs    optional device fp32 [num_seqs]: log of the token's share of the kept weights
+ * Rows are a matter of tens of microseconds, but of a millisecond or two where a border lies among thousands of candidates
+ * that cannot be told apart in one look: equal logits, or the end of top_k more than 22 temperatures below the largest logit (a
+ * min_p of 1e-9 ends the row before that).
  * A row without a candidate gives token -1 and -inf; so does a setting outside of its range (a temperature that is
  * negative or not finite, uniform outside of [0, 1), top_p below 0, min_p above 1, a NaN), which flags bit 5
  * (PKV_ERR_INDEX).

@@ -19,7 +19,8 @@
 // of a launch belongs to the last request with floor(qsl[i] / 16) + 2 i <= x: no plan and no prefix sum.
 //
 // Bound: for few tokens the launch and five loads that depend on one another (one token 2.7 us, 64 tokens 2.6 us, floor 0.2);
-// for many, HBM: 5300 tokens in 8 chunks, 122 MB, 27.4 us (18.2 at the copy's rate; a CTA a token instead of a warp: 33.8).
+// for many, HBM: 5300 tokens in 8 chunks, 32 / 8 heads of 128, to 8 bits, 122 MB, 27.4 us (18.2 at the copy's rate; a CTA a token
+// instead of a warp: 33.8), to bf16 26.8 (133 MB, 19.8), to fp32 48.7 (263 MB, 39.3), of 8 / 2 heads of 64 9.6 (34 MB, 5.1).
 #include <cuda_fp8.h>
 
 #include "pkv_internal.cuh"

@@ -26,9 +26,9 @@
 // across them and O rescaled.
 //
 // Bound: HBM, once the cache is larger than a few MB.  32 requests of 32768 keys, 64 / 8 heads, 2.15 GB: 311 us, 103 % of the measured
-// copy rate (DRAM 87 % busy); 64 requests of 128 to 4096 keys, 279 MB: 52 us, 80 %, of which 4 are the start and 4 the
+// copy rate (DRAM 88 % busy); 64 requests of 128 to 4096 keys, 279 MB: 52 us, 80 %, of which 4 are the start and 4 the
 // join; with 128 / 8 heads, 282 MB, 55 us.  The columns of small weights cost none, 0.3 and 1.2 of these.  One request of 500 keys: 8.7 us of latency, 3 of them the join's launch.  Bytes pass through shared memory twice (TMA in,
-// the tensor core out); the tensor pipe is 7 % busy.
+// the tensor core out); the tensor pipe is 9 % busy.
 //
 // Per CTA, two to an SM so that one's unit ends while the other streams (192 threads each): warp 0 walks its run
 // (q8_units.cuh) and loads K and V by TMA (16 rows of 128 bytes a block, 128-byte swizzle, three tiles in flight), warp 1

@@ -18,13 +18,16 @@
 // The first bins are those without which the squares of the others' masses would be more than 2^-8 of the square of the
 // kept mass: an fp32 weight is off by 2^-24 (the exponential unit's error, rms, with a mean of -5.25e-8, measured, that is
 // given back), so that sums are right to 2^-28 even where all weights of a bin are off the same way (equal logits).
-// What was collected (hundreds, as a rule) is put in order by all CTAs, with exact weights, and the first CTA finds the borders.
+// What was collected (tens to hundreds, where the borders lie in counted bins) is put in order by all CTAs, with exact weights, and the first CTA finds the borders.
 // Where one lies so close to a candidate's (2^-25 of the sums, eight times their error) that the fp32 weights could tell them
 // wrong, the sums are taken again, exact down to 2^-20 of the largest weight, and the borders found again: a few rows in a
 // thousand flat ones, hardly any other.  Weights to be exact wait in a queue of each thread's, so that a warp computes as many
 // as it has lanes at a time.  With top-k or min-p nothing behind their end is looked at closely.
-// Where more than 2048 candidates lie in the borders' bins (rows of equal logits), borders are found by bisection
-// of the keys instead, a pass over the row each (1 ms for 128256 logits).
+// Where more than 2048 candidates lie in the borders' bins, borders are found by bisection of the keys instead, a pass over the
+// row each.  Rows of thousands of equal logits come to that (64 rows of 128256: 0.7 ms), and rows with a top-k and no
+// min-p whose k-th logit lies behind the counted bins, more than 32 powers of two, 22 temperatures, below the largest.
+// Ordinary settings reach that: 64 rows of 32000 (128256) with a top-k of 50 take 19 (29) us at a temperature of 1, 955
+// (1383) at 0.3 and 1087 (1834) at 0.2, with 1000 22 (39), 1321 (2326) and 1330 (2358).  A min-p of 2^-31 or more ends the plan before.
 //
 // Bound: steps, not bytes.  64 rows of 128256 in bf16, four CTAs each, two on most SMs: 43.5 us (2.5 at the HBM copy's rate), in
 // clocks of the longest rows: first pass 6000, counts 15000, joining them and the plan 10000, sums 22000, order
@@ -1020,8 +1023,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 2) sam
     if (round == 0) {
       collected = head->collected;
       const int n = static_cast<int>(collected);
-      // Ranking takes the square of a CTA's share, sorting less of many (64 rows, 4 CTAs each: about 400, 800 and 1600 collected 48, 77
-      // and 90 us ranked, 61, 82 and 86 sorted; 300 rows, one each, 400 and 800: 143 and 277, 149 and 249)
+      // Ranking takes the square of a CTA's share of a bin, sorting less of many.  Equal logits, all in one bin, where ranking is slowest:
+      // 64 rows of 128256, 4 CTAs each, 400, 800 and 1600 collected 43.6, 57.5 and 100 us ranked, 46.2, 52.7 and 72 sorted; 300 rows
+      // of 32000, one each, 55, 94 and 247, and 50, 57 and 74
       const bool many = n > kCollect, few = !many && n * n <= kThreads * kThreads * kCtas;
       if (n <= 32) {
         if (rank == 0 && threadIdx.x < 32) rank_few(s, w, n);
@@ -1067,9 +1071,9 @@ int launch(const Params& p, int32_t rows, cudaStream_t s) {
 
 template <typename T>
 int launch_rows(const Params& p, int32_t rows, int num_sms, cudaStream_t s) {
-  // CTAs a row: as many as the SMs hold two of each, none with less than 1024 logits.  1, 2, 4 and 8 of them: one row of 32000 23.0,
-  // 18.4, 16.0, 15.3 us, of 4000 16.2, 15.9, 15.4, 15.9; 33 rows of 50257 in fp32 51, 35, 26, 27; 64 of 128256 101, 61, 48, 56; 152 of
-  // 32000 43, 39, 61, 100; 304 of 32000 54, 65, 105, 186
+  // CTAs a row: as many as the SMs hold two of each, none with less than 1024 logits.  1, 2, 4 and 8 of them, all filters: one row of 32000 20.5,
+  // 16.0, 13.6, 13.0 us, of 4000 13.0, 12.6, 12.4, 12.9; 64 of 128256 56, 36, 31, 47; 152 of 32000 27, 25, 51, 86; 304 of them 35, 49, 88, 160.
+  // top-p alone: 33 rows of 50257 in fp32 44, 31, 24, 25; 64 of 128256 133, 77, 57, 65; 152 of 32000 37, 33, 56, 92; 304 of them 55, 63, 97, 174
   const int64_t room = 2 * static_cast<int64_t>(num_sms) / rows;
   const int most = static_cast<int>(room < 1 ? 1 : room > 8 ? 8 : room);
   if (most >= 8 && p.vocab >= 8192) return launch<T, 8>(p, rows, s);
