@@ -422,14 +422,18 @@ __device__ __forceinline__ void scale_o(uint32_t taddr, float alpha) {
   }
 }
 __device__ __forceinline__ void scale_p(uint32_t taddr, int pieces, float alpha) {
-  const __half2 by = __float2half2_rn(alpha);
+  // Two steps: alpha may be below fp16's least number, and its products with weights not.
+  const bool far = alpha < 0x1p-24f;
+  const __half2 by = __float2half2_rn(far ? 0x1p-15f : alpha), more = __float2half2_rn(far ? alpha * 0x1p15f : 1.f);
+  const bool any_far = __any_sync(0xffffffffu, far);
 #pragma unroll 1
   for (int ch = 0; ch < pieces; ++ch) {
     uint32_t v[16];
     tmem_ld16_sync(taddr + 16 * ch, v);
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&v[e]), by);
+      __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&v[e]), by);
+      if (any_far) y = __hmul2(y, more);
       v[e] = *reinterpret_cast<const uint32_t*>(&y);
     }
     tmem_st16(taddr + 16 * ch, v);

@@ -527,6 +527,32 @@ def test_attention_scores_that_grow_within_a_tile(pkv, new):
         assert (np.abs(out.double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -9 * of).all()
 
 
+@pytest.mark.parametrize("new", [1, 3, 40])
+@pytest.mark.parametrize("far", [20, 25, 26, 30, 33, 38, 40])
+def test_attention_a_key_far_above_others_of_its_tile(pkv, far, new):
+    # a tile of small weights sets the references; of the next one the first 32 keys weigh 2^7.5 times as much, and a later one 2^far as
+    # much, whose V is 0: what comes out are the 32, 2^(7.5 - far) of the largest, held to 2^-11 of themselves.  (So many requests, all
+    # alike, that a CTA does all of one.)
+    scale, ctx, requests = 128 ** -0.5, 256, 160
+    tables, lens, qsl, pool = ref.requests([ctx], [new], 3)
+    cache, scales = ref.pool8(pool, 2, 3)
+    cache[0] = 0
+    scales[:] = 1.0
+    for p in range(int(lens[0])):
+        at = cache[:, tables[0][p // 16], :, p % 16]
+        at[0, :, 0] = ref.encode8(np.array([0.0 if p < 128 or p >= 160 else 4.0]))[0]
+        at[0, :, 1] = ref.encode8(np.array([1.0 if p == 170 else 0.0]))[0]
+        if p == 170:
+            at[1] = 0
+    q = torch.zeros((new, 8, 128)).bfloat16()
+    q[..., 0], q[..., 1] = 7.5 * np.log(2.0) / (4.0 * scale), far * np.log(2.0) / scale
+    out = pkv.paged_attention_q8(q.repeat(requests, 1, 1).cuda(), *gpu(cache[0], cache[1], scales, tables.repeat(requests, 0), lens.repeat(requests),
+                                                                       (np.arange(requests + 1) * new).astype(np.int32)), scale, new, int(lens[0]))
+    want, of = ref.attention(q.double().numpy(), cache[0], cache[1], scales, tables, lens, qsl, scale)
+    off = np.abs(out.double().cpu().numpy().reshape(requests, *want.shape) - want)
+    assert (off <= 2.0 ** -8 * np.abs(want) + 2.0 ** -9 * of + 2.0 ** -32 * int(lens[0]) * 448.0).all()
+
+
 @pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-30])
 @pytest.mark.parametrize("new", [[1, 1], [1, 40]])
 def test_attention_scales_of_the_scores(pkv, scale, new):
