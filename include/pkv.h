@@ -516,16 +516,16 @@ PKV_API int pkv_q8_workspace(const pkv_cache_desc* cache, int32_t num_q_heads, i
  *     of these the ones whose weight is at least min_p[n] (that of the first is 1; 0 or less: all),
  *     of these the shortest beginning whose weights are at least top_p[n] of the sum (1 or more: all; one at least).
  * The token is the first of the kept ones whose cumulative weight exceeds uniform[n] times their sum.
- * temperature[n] == 0 takes the first candidate.  Near a border weights are right to 2^-40 (of the largest weight, 2^-44),
- * and sums to 2^-28 of the kept ones, or, where a border lies within 2^-25 of a candidate's, exact down to weights of
- * 2^-20 of the largest: tokens are told apart as 64-bit arithmetic does but for borders closer than that.  A call
- * repeats bit by bit.
+ * temperature[n] == 0 takes the first candidate.  Near a border weights are right to 2^-40 (of the largest weight, 2^-44, or
+ * vocab 2^-63 where that is more), and sums to 2^-28 of the kept ones (of the largest weight, vocab^2 2^-63 where that is more),
+ * or, where a border lies within 2^-25 of a candidate's, exact down to weights of 2^-20 of the largest: tokens are told apart as
+ * 64-bit arithmetic does but for borders closer than that.  A call repeats bit by bit.
  * logits          device [num_seqs] rows of vocab values of `dtype` (pkv_dtype: fp32 or bf16), row_stride elements
  *                 apart (>= vocab), aligned to their type; vocab up to 2^20
  * temperature, top_k, top_p, min_p  optional device fp32, int32, fp32, fp32 [num_seqs] (NULL: 1, all, 1, 0)
  * uniform         device fp32 [num_seqs], in [0, 1)
  * out_tokens      device int32 [num_seqs]
- * out_logprobs    optional device fp32 [num_seqs]: log of the token's share of the kept weights
+ * out_logprobs    optional device fp32 [num_seqs]: log of the token's share of the kept weights, to 2^-22 of itself and of 1
  * Rows are a matter of tens of microseconds, but of a millisecond or two where a border lies among thousands of candidates
  * that cannot be told apart in one look: equal logits, or the end of top_k more than 22 temperatures below the largest logit (a
  * min_p of 1e-9 ends the row before that).
