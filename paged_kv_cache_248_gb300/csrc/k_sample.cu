@@ -645,7 +645,7 @@ __device__ __forceinline__ int finish(const Params& P, Shared& s, const Row& r, 
     const int e = static_cast<int>(token);
     const uint64_t key = s.list[e];
     P.tokens[row] = static_cast<int32_t>(key & 0xffffffffu);
-    if (P.logprobs) P.logprobs[row] = w.log_share(s.weights[e], z2);
+    if (P.logprobs) P.logprobs[row] = w.log_share(logit_of(key), r.temperature, s.weights[e], z2);
   }
   return 0;
 }
@@ -748,7 +748,7 @@ __device__ __noinline__ void by_bisection(const Params& P, Shared& s, const Row&
   const uint64_t key = bisect<T, kCtas>(P, s, w, row, rank, end, [&](uint64_t, uint64_t m) { return m > target; });
   if (rank == 0 && threadIdx.x == 0) {
     P.tokens[row] = static_cast<int32_t>(key & 0xffffffffu);
-    if (P.logprobs) P.logprobs[row] = w.log_share(w.of(logit_of(key), s.table), mass);
+    if (P.logprobs) P.logprobs[row] = w.log_share(logit_of(key), r.temperature, w.of(logit_of(key), s.table), mass);
   }
 }
 

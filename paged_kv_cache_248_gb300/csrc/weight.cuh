@@ -113,9 +113,10 @@ struct Weight {
     return fma2(mul2(m, two(0.6931472f)), yl, m);
   }
 
-  // log(w / mass)
-  __device__ __forceinline__ float log_share(uint64_t w, uint64_t mass) const {
+  // log(w / mass) of logit x with weight w.  Few units of weight say little: then it is (x - max) / T - log(mass of the largest's weight).
+  __device__ __forceinline__ float log_share(float x, float temperature, uint64_t w, uint64_t mass) const {
     const float all = __ull2float_rn(mass);
+    if (w < (1u << 24)) return (x - top) / temperature - logf(all / unit);
     return w > mass - w ? log1pf(-(__ull2float_rn(mass - w) / all)) : logf(__ull2float_rn(w) / all);
   }
 };

@@ -769,6 +769,32 @@ def test_sample_short_rows_of_several_ctas(pkv, n, v):
         np.testing.assert_array_equal(tokens.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("v,low", [(5000, -22.0), (40000, -24.0), (128256, -26.0), (1 << 20, -27.0)])
+def test_sample_logprobs_of_words_far_down(pkv, v, low, dtype):
+    # numbers next to 1 fall to the tail, whose words weigh 2^-32 to 2^-39 of the largest each: closer than sums are told apart, so
+    # any word will do that is 2^-28 of the mass from the number's place, twice that with the number's own rounding of the target, and
+    # V^2 2^-63 of the largest weight (whole weights are V 2^-63 off at most)
+    n, rng = 8, np.random.default_rng(v)
+    x = torch.from_numpy(low + 0.3 * rng.standard_normal((n, v)))
+    x[:, 17] = 0.0
+    t = rng.uniform(0.9, 1.0, n).astype(np.float32)
+    x, u = x.to(dtype), 1 - 2.0 ** -23
+    tokens, logprobs = pkv.pkv_sample(x.cuda(), gpu(np.full(n, u, np.float32)), temperature=gpu(t))
+    near, far = 2.0 ** -27 + v * v * 2.0 ** -63, 0
+    for row, temp, token, logprob in zip(x.double().numpy(), t.astype(np.float64), tokens.tolist(), logprobs.tolist()):
+        order = np.argsort(-row, kind="stable")
+        w = np.exp((row[order] - row.max()) / temp)
+        upto = np.cumsum(w[::-1])[::-1]  # the mass from each word on: small ones first, so that 64 bits hold them
+        at = int(np.nonzero(order == token)[0][0])
+        want = np.log(w[at] / upto[0])
+        assert abs(logprob - want) <= 2.0 ** -22 * (1 + abs(want))
+        place = 1 - upto[at:at + 2] / upto[0]  # where the word begins, and the next one
+        assert place[0] <= u + near and place[-1] >= u - near
+        far += want < -20
+    assert far > 0
+
+
 def test_sample_largest_vocabulary(pkv):
     v = 1 << 20
     x = peaked(2, v, 5, sigma=1.0)
